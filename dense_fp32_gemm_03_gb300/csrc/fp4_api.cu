@@ -1,0 +1,281 @@
+// fp4_api.cu -- host side of the 4-bit operators' C ABI (include/fp4.h):
+// argument validation, scratch and launches.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "fp4.h"
+#include "fp4_internal.h"
+#include "sgemm_internal.h"
+
+namespace {
+
+using gb300::LibDevice;
+
+// Rows and columns: tile and piece counts stay within 32 bits.
+constexpr int64_t kMaxExtent = int64_t(1) << 30;
+
+int64_t block_of(int format) { return format == FP4_MXFP4 ? 32 : 16; }
+int64_t dtype_bytes(int dtype) { return dtype == FP4_F32 ? 4 : 2; }
+int64_t code_pitch(int64_t cols) { return (cols + 31) / 32 * 16; }
+int64_t scale_bytes(int format, int64_t rows, int64_t cols) {
+  return (rows + 127) / 128 * ((cols + 255) / 256) * (64 / block_of(format)) * 512;
+}
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+sgemm_status_t status_of(cudaError_t e) { return e == cudaSuccess ? SGEMM_OK : SGEMM_ERR_LAUNCH; }
+
+sgemm_status_t check_format(int format) {
+  return format == FP4_MXFP4 || format == FP4_NVFP4 ? SGEMM_OK : SGEMM_ERR_INVALID_VALUE;
+}
+
+sgemm_status_t check_extent(int64_t a, int64_t b) {
+  if (a < 0 || b < 0) return SGEMM_ERR_INVALID_VALUE;
+  return a > kMaxExtent || b > kMaxExtent ? SGEMM_ERR_UNSUPPORTED : SGEMM_OK;
+}
+
+sgemm_status_t check_quantized(const fp4_matrix_t* q) {
+  if (q == nullptr || check_format(q->format) != SGEMM_OK) return SGEMM_ERR_INVALID_VALUE;
+  const sgemm_status_t st = check_extent(q->rows, q->cols);
+  if (st != SGEMM_OK) return st;
+  if (q->rows == 0 || q->cols == 0) return SGEMM_OK;
+  if (q->codes == nullptr || q->scales == nullptr || !aligned(q->codes, 16) || !aligned(q->scales, 16) ||
+      q->ld < code_pitch(q->cols) || q->ld % 16 != 0 || !aligned(q->factor, 4))
+    return SGEMM_ERR_INVALID_VALUE;
+  return SGEMM_OK;
+}
+
+// An unquantised rows x cols matrix.
+sgemm_status_t check_dense(int dtype, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  if (dtype < FP4_F32 || dtype > FP4_F16) return SGEMM_ERR_INVALID_VALUE;
+  const sgemm_status_t st = check_extent(rows, cols);
+  if (st != SGEMM_OK) return st;
+  if (rows == 0 || cols == 0) return SGEMM_OK;
+  if (p == nullptr || ld < cols || !aligned(p, size_t(dtype_bytes(dtype)))) return SGEMM_ERR_INVALID_VALUE;
+  return SGEMM_OK;
+}
+
+struct Range {
+  uintptr_t lo, hi;
+};
+Range range(const void* p, int64_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, bytes > 0 ? a + uintptr_t(bytes) : a};
+}
+Range dense_range(int dtype, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  return range(p, rows && cols ? ((rows - 1) * ld + cols) * dtype_bytes(dtype) : 0);
+}
+Range code_range(const fp4_matrix_t* q) {
+  return range(q->codes, q->rows && q->cols ? (q->rows - 1) * q->ld + code_pitch(q->cols) : 0);
+}
+Range scale_range(const fp4_matrix_t* q) { return range(q->scales, scale_bytes(q->format, q->rows, q->cols)); }
+bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+
+}  // namespace
+
+extern "C" {
+
+sgemm_status_t fp4_layout(int format, int64_t rows, int64_t cols, int64_t* ld, int64_t* codes, int64_t* scales) {
+  sgemm_status_t st = check_format(format);
+  if (st == SGEMM_OK) st = check_extent(rows, cols);
+  if (st != SGEMM_OK) return st;
+  if (ld) *ld = code_pitch(cols);
+  if (codes) *codes = rows * code_pitch(cols);
+  if (scales) *scales = scale_bytes(format, rows, cols);
+  return SGEMM_OK;
+}
+
+sgemm_status_t fp4_quantize(int dtype, const void* x, int64_t ldx, const fp4_matrix_t* q, cudaStream_t stream) {
+  sgemm_status_t st = check_quantized(q);
+  if (st == SGEMM_OK) st = check_dense(dtype, x, q->rows, q->cols, ldx);
+  if (st != SGEMM_OK) return st;
+  const Range r = dense_range(dtype, x, q->rows, q->cols, ldx);
+  if (overlap(r, code_range(q)) || overlap(r, scale_range(q))) return SGEMM_ERR_INVALID_VALUE;
+  LibDevice d;
+  st = gb300::lib_device(&d);
+  if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
+  return status_of(gb300::launch_fp4_quantize(dtype, x, ldx, *q, stream));
+}
+
+sgemm_status_t fp4_pack(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales,
+                        const fp4_matrix_t* q, cudaStream_t stream) {
+  sgemm_status_t st = check_quantized(q);
+  if (st != SGEMM_OK) return st;
+  LibDevice d;
+  const int64_t blocks = (q->cols + block_of(q->format) - 1) / block_of(q->format);
+  if (q->rows != 0 && q->cols != 0) {
+    if (codes == nullptr || scales == nullptr || ld_codes < (q->cols + 1) / 2 || ld_scales < blocks)
+      return SGEMM_ERR_INVALID_VALUE;
+    const Range a = range(codes, (q->rows - 1) * ld_codes + (q->cols + 1) / 2);
+    const Range b = range(scales, (q->rows - 1) * ld_scales + blocks);
+    for (const Range& r : {code_range(q), scale_range(q)})
+      if (overlap(a, r) || overlap(b, r)) return SGEMM_ERR_INVALID_VALUE;
+  }
+  st = gb300::lib_device(&d);
+  if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
+  return status_of(gb300::launch_fp4_pack(codes, ld_codes, scales, ld_scales, *q, stream));
+}
+
+sgemm_status_t fp4_dequantize(const fp4_matrix_t* q, int dtype, void* y, int64_t ldy, cudaStream_t stream) {
+  sgemm_status_t st = check_quantized(q);
+  if (st == SGEMM_OK) st = check_dense(dtype, y, q->rows, q->cols, ldy);
+  if (st != SGEMM_OK) return st;
+  const Range r = dense_range(dtype, y, q->rows, q->cols, ldy);
+  if (overlap(r, code_range(q)) || overlap(r, scale_range(q))) return SGEMM_ERR_INVALID_VALUE;
+  LibDevice d;
+  st = gb300::lib_device(&d);
+  if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
+  return status_of(gb300::launch_fp4_dequantize(*q, dtype, y, ldy, stream));
+}
+
+sgemm_status_t fp4_gemm(const fp4_matrix_t* A, const fp4_matrix_t* B, int dtype, void* C, int64_t ldc,
+                        cudaStream_t stream) {
+  sgemm_status_t st = check_quantized(A);
+  if (st == SGEMM_OK) st = check_quantized(B);
+  if (st != SGEMM_OK) return st;
+  if (A->format != B->format || A->cols != B->cols) return SGEMM_ERR_INVALID_VALUE;
+  st = check_dense(dtype, C, A->rows, B->rows, ldc);
+  if (st != SGEMM_OK) return st;
+  const Range r = dense_range(dtype, C, A->rows, B->rows, ldc);
+  for (const fp4_matrix_t* q : {A, B})
+    if (overlap(r, code_range(q)) || overlap(r, scale_range(q))) return SGEMM_ERR_INVALID_VALUE;
+  LibDevice d;
+  st = gb300::lib_device(&d);
+  if (st != SGEMM_OK || A->rows == 0 || B->rows == 0) return st;
+  return status_of(gb300::launch_fp4_simple(*A, *B, dtype, C, ldc, stream));
+}
+
+sgemm_status_t fp4_linear(int dtype, const void* x, int64_t ldx, int64_t M, const float* x_factor,
+                          const fp4_matrix_t* W, void* y, int64_t ldy, cudaStream_t stream) {
+  sgemm_status_t st = check_quantized(W);
+  if (st == SGEMM_OK) st = check_dense(dtype, x, M, W->cols, ldx);
+  if (st == SGEMM_OK) st = check_dense(dtype, y, M, W->rows, ldy);
+  if (st != SGEMM_OK) return st;
+  if (!aligned(x_factor, 4)) return SGEMM_ERR_INVALID_VALUE;
+  const Range r = dense_range(dtype, y, M, W->rows, ldy);
+  if (overlap(r, code_range(W)) || overlap(r, scale_range(W)) ||
+      overlap(r, dense_range(dtype, x, M, W->cols, ldx)))
+    return SGEMM_ERR_INVALID_VALUE;
+  LibDevice d;
+  st = gb300::lib_device(&d);
+  if (st != SGEMM_OK || M == 0 || W->rows == 0) return st;
+  fp4_matrix_t q{};
+  q.format = W->format;
+  q.rows = M;
+  q.cols = W->cols;
+  q.ld = code_pitch(W->cols);
+  q.factor = x_factor;
+  const int64_t code_bytes = (M * q.ld + 255) / 256 * 256;
+  void* ws = nullptr;
+  st = gb300::lib_workspace(d.dev, stream,
+                            gb300::kWorkspaceCounterBytes + code_bytes + scale_bytes(W->format, M, W->cols), &ws);
+  if (st != SGEMM_OK) return st;
+  q.codes = static_cast<uint8_t*>(ws) + gb300::kWorkspaceCounterBytes;
+  q.scales = q.codes + code_bytes;
+  if (W->cols != 0 && gb300::launch_fp4_quantize(dtype, x, ldx, q, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+  return status_of(gb300::launch_fp4_simple(q, *W, dtype, y, ldy, stream));
+}
+
+sgemm_status_t fp4_experts_layout(int format, int64_t experts, int64_t d, int64_t f, int64_t* gate_up_bytes,
+                                  int64_t* down_bytes) {
+  sgemm_status_t st = check_format(format);
+  if (st == SGEMM_OK) st = check_extent(d, f);
+  if (st == SGEMM_OK) st = check_extent(experts, 0);
+  if (st != SGEMM_OK) return st;
+  if (experts > 1024) return SGEMM_ERR_UNSUPPORTED;
+  const int64_t chunk = gb300::fp4_expert_chunk_bytes(format);
+  if (gate_up_bytes) *gate_up_bytes = experts * ((f + 7) / 8) * ((d + 127) / 128) * chunk;
+  if (down_bytes) *down_bytes = experts * ((d + 15) / 16) * ((f + 127) / 128) * chunk;
+  return SGEMM_OK;
+}
+
+static sgemm_status_t check_experts(const fp4_experts_t* w) {
+  if (w == nullptr) return SGEMM_ERR_INVALID_VALUE;
+  int64_t up = 0, down = 0;
+  const sgemm_status_t st = fp4_experts_layout(w->format, w->experts, w->d, w->f, &up, &down);
+  if (st != SGEMM_OK) return st;
+  if ((up > 0 && (w->gate_up == nullptr || w->down == nullptr)) || !aligned(w->gate_up, 16) ||
+      !aligned(w->down, 16) || !aligned(w->gate_up_factor, 4) || !aligned(w->down_factor, 4))
+    return SGEMM_ERR_INVALID_VALUE;
+  return SGEMM_OK;
+}
+
+sgemm_status_t fp4_experts_pack(const fp4_matrix_t* gate_up, const fp4_matrix_t* down, const fp4_experts_t* w,
+                                cudaStream_t stream) {
+  sgemm_status_t st = check_quantized(gate_up);
+  if (st == SGEMM_OK) st = check_quantized(down);
+  if (st == SGEMM_OK) st = check_experts(w);
+  if (st != SGEMM_OK) return st;
+  if (gate_up->format != w->format || down->format != w->format || gate_up->cols != w->d || down->cols != w->f ||
+      gate_up->rows != w->experts * 2 * w->f || down->rows != w->experts * w->d)
+    return SGEMM_ERR_INVALID_VALUE;
+  LibDevice d;
+  st = gb300::lib_device(&d);
+  if (st != SGEMM_OK || w->experts == 0 || w->d == 0 || w->f == 0) return st;
+  return status_of(gb300::launch_fp4_experts_pack(*gate_up, *down, *w, stream));
+}
+
+sgemm_status_t fp4_moe(int dtype, const void* x, int64_t ldx, int64_t M, const float* router, int64_t ldr,
+                       const fp4_experts_t* w, int32_t top, int32_t renormalize, void* y, int64_t ldy, int32_t* ids,
+                       float* p, cudaStream_t stream) {
+  sgemm_status_t st = check_experts(w);
+  if (st == SGEMM_OK) st = check_dense(dtype, x, M, w->d, ldx);
+  if (st == SGEMM_OK) st = check_dense(FP4_F32, router, w->experts, w->d, ldr);
+  if (st == SGEMM_OK) st = check_dense(dtype, y, M, w->d, ldy);
+  if (st != SGEMM_OK) return st;
+  if (top < 1 || top > 32 || top > w->experts || !aligned(ids, 4) || !aligned(p, 4)) return SGEMM_ERR_INVALID_VALUE;
+  if (w->d == 0 || w->f == 0) return SGEMM_ERR_INVALID_VALUE;
+  const Range r = dense_range(dtype, y, M, w->d, ldy);
+  int64_t up_bytes = 0, down_bytes = 0;
+  fp4_experts_layout(w->format, w->experts, w->d, w->f, &up_bytes, &down_bytes);
+  if (overlap(r, dense_range(dtype, x, M, w->d, ldx)) ||
+      overlap(r, dense_range(FP4_F32, router, w->experts, w->d, ldr)) || overlap(r, range(w->gate_up, up_bytes)) ||
+      overlap(r, range(w->down, down_bytes)))
+    return SGEMM_ERR_INVALID_VALUE;
+  LibDevice d;
+  st = gb300::lib_device(&d);
+  if (st != SGEMM_OK || M == 0) return st;
+  const int64_t most = M < gb300::kMoeTokens ? M : gb300::kMoeTokens;
+  const gb300::MoeScratch s = gb300::fp4_moe_scratch(dtype, most, w->experts, w->d, w->f, top);
+  void* ws = nullptr;
+  st = gb300::lib_workspace(d.dev, stream, gb300::kWorkspaceCounterBytes + s.bytes, &ws);
+  if (st != SGEMM_OK) return st;
+  uint8_t* base = static_cast<uint8_t*>(ws) + gb300::kWorkspaceCounterBytes;
+  gb300::MoeArgs a{};
+  a.ldx = ldx;
+  a.router = router;
+  a.ldr = ldr;
+  a.gate_up = w->gate_up;
+  a.down = w->down;
+  a.gate_up_factor = w->format == FP4_NVFP4 ? w->gate_up_factor : nullptr;
+  a.down_factor = w->format == FP4_NVFP4 ? w->down_factor : nullptr;
+  a.ldy = ldy;
+  a.experts = int32_t(w->experts);
+  a.d = int32_t(w->d);
+  a.f = int32_t(w->f);
+  a.top = top;
+  a.renormalize = renormalize;
+  a.logits = reinterpret_cast<float*>(base + s.logits);
+  a.pick = reinterpret_cast<int32_t*>(base + s.pick);
+  a.weight = reinterpret_cast<float*>(base + s.weight);
+  a.x_scale = reinterpret_cast<float*>(base + s.x_scale);
+  a.h_max = reinterpret_cast<uint32_t*>(base + s.h_max);
+  a.x_frag = base + s.x_frag;
+  a.h = reinterpret_cast<float*>(base + s.h);
+  a.counters = static_cast<int32_t*>(ws);
+  a.status = d.status;
+  a.wait_limit_ns = d.wait_limit_ns;
+  const int64_t bytes = dtype_bytes(dtype);
+  for (int64_t t = 0; t < M; t += gb300::kMoeTokens) {
+    a.tokens = int32_t(M - t < gb300::kMoeTokens ? M - t : gb300::kMoeTokens);
+    a.x = static_cast<const uint8_t*>(x) + t * ldx * bytes;
+    a.y = static_cast<uint8_t*>(y) + t * ldy * bytes;
+    a.ids = ids ? ids + t * top : nullptr;
+    a.p = p ? p + t * top : nullptr;
+    if (gb300::launch_fp4_moe(dtype, w->format, a, d.sms, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+  }
+  return SGEMM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,117 @@
+// fp4_device.cuh -- device helpers of the microscaled 4-bit operators: the
+// formats' block sizes, code and scale conversions, and 32-bit reads and
+// writes of the unquantised types.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "fp4.h"
+
+namespace gb300 {
+namespace fp4 {
+
+template <int kFormat>
+struct Format {
+  static constexpr int kBlock = kFormat == FP4_MXFP4 ? 32 : 16;
+  static constexpr int kAtom = 4 * kBlock;                // columns whose scales make one 512-byte atom
+  static constexpr int kAtomsPerStage = 256 / kAtom;      // atoms of 256 columns
+};
+
+// Offset of the scale byte of block `k` of row `r` (fp4.h).
+__host__ __device__ __forceinline__ int64_t scale_offset(int64_t r, int64_t k, int64_t atoms) {
+  return (((r >> 7) * atoms + (k >> 2)) * 32 + (r & 31)) * 16 + ((r & 127) >> 5) * 4 + (k & 3);
+}
+
+// Two codes from two values (each rounded to nearest even, at most 6 in magnitude): lo in bits 0-3.
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+      "mov.b32 %0, {b, b, b, b};\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r & 0xffu;
+}
+
+// The two values of byte kByte of w, exact in 16-bit floats (low code in .x).
+template <int kByte>
+__device__ __forceinline__ __half2 decode2(uint32_t w) {
+  uint32_t h;
+  if constexpr (kByte == 0)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h) : "r"(w));
+  else if constexpr (kByte == 1)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(w));
+  else if constexpr (kByte == 2)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(h) : "r"(w));
+  else
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(h) : "r"(w));
+  return *reinterpret_cast<__half2*>(&h);
+}
+
+// 8-bit float scale (4 exponent bits, 3 fraction bits) of v >= 0: nearest even, at most 448.
+__device__ __forceinline__ uint32_t encode_e4m3(float v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(v));
+  return r & 0xffu;
+}
+
+__device__ __forceinline__ float decode_e4m3(uint32_t byte) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(byte)));
+  return __low2float(*reinterpret_cast<__half2*>(&h));
+}
+
+// 2^(byte - 127); 255: NaN.
+__device__ __forceinline__ float decode_e8m0(uint32_t byte) {
+  const uint32_t bits = byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23;
+  return __uint_as_float(bits);
+}
+
+// The unit of a block without the matrix's factor.
+template <int kFormat>
+__device__ __forceinline__ float decode_scale(uint32_t byte) {
+  return kFormat == FP4_MXFP4 ? decode_e8m0(byte) : decode_e4m3(byte);
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// Eight consecutive values from a 16-byte-aligned address.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const T* t = reinterpret_cast<const T*>(&a);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  uint4 a;
+  T* t = reinterpret_cast<T*>(&a);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = from_f32<T>(v[i]);
+  *reinterpret_cast<uint4*>(p) = a;
+}
+
+}  // namespace fp4
+}  // namespace gb300

@@ -693,6 +693,40 @@ sgemm_status_t run(int variant, int64_t M, int64_t N, int64_t K, float alpha, co
 
 }  // namespace
 
+namespace gb300 {
+
+sgemm_status_t lib_device(LibDevice* out) {
+  DeviceState* ds = nullptr;
+  const sgemm_status_t st = device_state(&ds, &out->dev);
+  if (st != SGEMM_OK) return st;
+  out->sms = ds->sms;
+  out->status = ds->status;
+  out->wait_limit_ns = kDefaultWaitLimitNs;
+  return SGEMM_OK;
+}
+
+static_assert(kWorkspaceCounterBytes == kCounterBytes, "one counter region for every entry point");
+
+sgemm_status_t lib_workspace(int dev, cudaStream_t stream, size_t need, void** out) {
+  return get_workspace_bytes(dev, stream, need, out);
+}
+
+sgemm_status_t lib_encode_bytes(const void* base, int64_t rows, int64_t row_bytes, int64_t pitch, int box_rows,
+                                CUtensorMap* map) {
+  std::memset(map, 0, sizeof(*map));
+  const cuuint32_t estr[2] = {1, 1};
+  const cuuint64_t dims[2] = {cuuint64_t(row_bytes), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(pitch)};
+  const cuuint32_t box[2] = {128, cuuint32_t(box_rows)};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? SGEMM_OK
+             : SGEMM_ERR_LAUNCH;
+}
+
+}  // namespace gb300
+
 extern "C" {
 
 sgemm_status_t sgemm(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda, const float* B,

@@ -9,6 +9,7 @@
 #include <cuda.h>
 #include <cuda_runtime_api.h>
 
+#include "sgemm.h"
 #include "sgemm_plan.h"
 
 namespace gb300 {
@@ -111,5 +112,23 @@ cudaError_t launch_status_take(uint32_t* status, cudaStream_t stream);
 
 // Frees sgemm_host()'s device staging, copy streams and events (every device).
 void host_staging_release();
+
+// The library's shared host state (sgemm_api.cu), for entry points in other
+// translation units: the current device, the per-(device, stream) workspace
+// cache and the tensor-map encoder.
+struct LibDevice {
+  int dev, sms;
+  uint32_t* status;  // device status word
+  uint64_t wait_limit_ns;
+};
+sgemm_status_t lib_device(LibDevice* out);
+// At least `need` bytes for this (device, stream); the first kWorkspaceCounterBytes are
+// arrival counters, zero on entry, which the caller's kernels leave zero.
+constexpr size_t kWorkspaceCounterBytes = 16384;
+sgemm_status_t lib_workspace(int dev, cudaStream_t stream, size_t need, void** out);
+// A 2-D tensor map of `rows` rows of `row_bytes` bytes (a multiple of 16), `pitch` bytes
+// apart, read in boxes of 128 bytes x box_rows with the 128-byte swizzle.
+sgemm_status_t lib_encode_bytes(const void* base, int64_t rows, int64_t row_bytes, int64_t pitch, int box_rows,
+                                CUtensorMap* map);
 
 }  // namespace gb300

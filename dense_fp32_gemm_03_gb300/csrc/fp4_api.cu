@@ -3,7 +3,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <cstring>
+#include <map>
+#include <mutex>
 
 #include "fp4.h"
 #include "fp4_internal.h"
@@ -71,6 +72,111 @@ Range code_range(const fp4_matrix_t* q) {
 }
 Range scale_range(const fp4_matrix_t* q) { return range(q->scales, scale_bytes(q->format, q->rows, q->cols)); }
 bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// ------------------------------------------------------------------- products
+std::mutex g_mu;
+std::map<int, int> g_pairs;  // CTA pairs that run at once, by device
+
+int tc_pairs(int dev) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  auto it = g_pairs.find(dev);
+  if (it == g_pairs.end()) it = g_pairs.emplace(dev, gb300::fp4_tc_prepare()).first;
+  return it->second;
+}
+
+struct Product {
+  gb300::Fp4TcShape shape;
+  gb300::Sched sc;
+  int grid;
+  size_t partial_bytes;
+};
+
+// Whole tiles fill complete waves of `units`; the tiles of the last, partial
+// wave are cut over K in shares of at least `least` slices if `split`.
+bool plan_tiles(int64_t rows, int64_t cols, int64_t K, gb300::Fp4TcShape shape, int units, int least, bool split,
+                Product* p) {
+  const gb300::Fp4TcTile t = gb300::fp4_tc_tile(shape);
+  const int64_t tm = (rows + t.rows - 1) / t.rows, tn = (cols + t.cols - 1) / t.cols, tiles = tm * tn;
+  if (tiles > 0x7fffffffLL) return false;
+  p->shape = shape;
+  p->sc = gb300::Sched{};
+  p->sc.tiles_m = int32_t(tm);
+  p->sc.tiles_n = int32_t(tn);
+  p->sc.group_m = gb300::kGroupM;
+  p->sc.iters_per_tile = int32_t((K + 255) / 256);
+  p->sc.dp_tiles = int32_t(tiles);
+  p->grid = int(tiles < units ? tiles : units);
+  p->partial_bytes = 0;
+  const int64_t rest = tiles % units, total = rest * p->sc.iters_per_tile;
+  int64_t shares = total / least < units ? total / least : units;
+  if (!split || shares <= rest) return true;
+  if (rest * t.ctas > int64_t(gb300::kWorkspaceCounterBytes / 4)) return true;
+  p->sc.dp_tiles = int32_t(tiles - rest);
+  p->sc.sk_tiles = int32_t(rest);
+  p->sc.sk_ctas = int32_t(shares);
+  p->sc.sk_base = int32_t(total / shares);
+  p->sc.sk_extra = int32_t(total % shares);
+  p->grid = p->sc.dp_tiles > 0 ? units : int(shares);
+  p->partial_bytes = size_t(rest + shares - 1) * t.rows * t.cols * 4;
+  return true;
+}
+
+// Few rows of A: B supplies the tile rows and A the columns, as few as hold
+// them.  Otherwise pairs of CTAs, or single ones where pairs would leave SMs idle.
+bool plan_product(int64_t M, int64_t N, int64_t K, int sms, int pairs, Product* p) {
+  if (M <= 64) {
+    const gb300::Fp4TcShape s = M <= 16 ? gb300::kFp4Swap16 : M <= 32 ? gb300::kFp4Swap32 : gb300::kFp4Swap64;
+    return plan_tiles(N, M, K, s, sms, 2, true, p);
+  }
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  if (pairs > 0 && tiles >= pairs) return plan_tiles(M, N, K, gb300::kFp4Pair, pairs, 4, true, p);
+  return plan_tiles(M, N, K, gb300::kFp4Single128, sms, 4, true, p);
+}
+
+// C = A B^T with the plan's partial sums at `partials` (after the counters at `ws`).
+sgemm_status_t run_product(const Product& p, const fp4_matrix_t& A, const fp4_matrix_t& B, int dtype, void* C,
+                           int64_t ldc, void* ws, void* partials, const LibDevice& d, cudaStream_t stream) {
+  const gb300::Fp4TcTile t = gb300::fp4_tc_tile(p.shape);
+  const fp4_matrix_t& R = t.swap ? B : A;
+  const fp4_matrix_t& Q = t.swap ? A : B;
+  const int64_t es = dtype_bytes(dtype);
+  const int per_stage = int(64 / block_of(A.format));
+  CUtensorMap maps[5];
+  sgemm_status_t st = gb300::lib_encode_bytes(R.codes, R.rows, code_pitch(R.cols), R.ld, 128, &maps[0]);
+  if (st == SGEMM_OK)
+    st = gb300::lib_encode_bytes(Q.codes, Q.rows, code_pitch(Q.cols), Q.ld, t.cols / t.ctas, &maps[1]);
+  for (int i = 0; i < 2 && st == SGEMM_OK; ++i) {
+    const fp4_matrix_t& q = i ? Q : R;
+    st = gb300::lib_encode_rows512(q.scales, scale_bytes(q.format, q.rows, q.cols) / 512, per_stage, &maps[2 + i]);
+  }
+  gb300::Fp4TcArgs a{};
+  a.rows = int32_t(R.rows);
+  a.cols = int32_t(Q.rows);
+  a.out = C;
+  a.ld = ldc;
+  a.factor_r = R.factor;
+  a.factor_c = Q.factor;
+  a.partials = static_cast<float*>(partials);
+  a.counters = static_cast<int32_t*>(ws);
+  a.status = d.status;
+  a.wait_limit_ns = d.wait_limit_ns;
+  a.tma_out = !t.swap && aligned(C, 16) && ldc * es % 16 == 0 && Q.rows * es < (int64_t(1) << 31);
+  a.tma_edge = Q.rows * es % 16 == 0;
+  if (st == SGEMM_OK) {
+    if (a.tma_out)
+      st = gb300::lib_encode_bytes(C, A.rows, Q.rows * es, ldc * es, 32, &maps[4]);
+    else
+      maps[4] = maps[0];  // not used
+  }
+  if (st != SGEMM_OK) return st;
+  return status_of(gb300::launch_fp4_tc(dtype, A.format, p.shape, maps, a, p.sc, p.grid, stream));
+}
+
+// C = 0 for an empty sum.
+sgemm_status_t zero_output(int dtype, void* C, int64_t rows, int64_t cols, int64_t ldc, cudaStream_t stream) {
+  const size_t es = size_t(dtype_bytes(dtype));
+  return status_of(cudaMemset2DAsync(C, size_t(ldc) * es, 0, size_t(cols) * es, size_t(rows), stream));
+}
 
 }  // namespace
 
@@ -143,7 +249,16 @@ sgemm_status_t fp4_gemm(const fp4_matrix_t* A, const fp4_matrix_t* B, int dtype,
   LibDevice d;
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || A->rows == 0 || B->rows == 0) return st;
-  return status_of(gb300::launch_fp4_simple(*A, *B, dtype, C, ldc, stream));
+  if (A->cols == 0) return zero_output(dtype, C, A->rows, B->rows, ldc, stream);
+  Product p;
+  const int pairs = tc_pairs(d.dev);
+  if (pairs < 0) return SGEMM_ERR_LAUNCH;
+  if (!plan_product(A->rows, B->rows, A->cols, d.sms, pairs, &p)) return SGEMM_ERR_UNSUPPORTED;
+  void* ws = nullptr;
+  if (p.partial_bytes > 0) st = gb300::lib_workspace(d.dev, stream, gb300::kWorkspaceCounterBytes + p.partial_bytes, &ws);
+  if (st != SGEMM_OK) return st;
+  void* partials = ws ? static_cast<uint8_t*>(ws) + gb300::kWorkspaceCounterBytes : nullptr;
+  return run_product(p, *A, *B, dtype, C, ldc, ws, partials, d, stream);
 }
 
 sgemm_status_t fp4_linear(int dtype, const void* x, int64_t ldx, int64_t M, const float* x_factor,
@@ -166,15 +281,22 @@ sgemm_status_t fp4_linear(int dtype, const void* x, int64_t ldx, int64_t M, cons
   q.cols = W->cols;
   q.ld = code_pitch(W->cols);
   q.factor = x_factor;
-  const int64_t code_bytes = (M * q.ld + 255) / 256 * 256;
+  if (W->cols == 0) return zero_output(dtype, y, M, W->rows, ldy, stream);
+  Product p;
+  const int pairs = tc_pairs(d.dev);
+  if (pairs < 0) return SGEMM_ERR_LAUNCH;
+  if (!plan_product(M, W->rows, W->cols, d.sms, pairs, &p)) return SGEMM_ERR_UNSUPPORTED;
+  // Scratch: counters, partial sums, the codes and scales of x.
+  const size_t code_at = gb300::kWorkspaceCounterBytes + (p.partial_bytes + 255) / 256 * 256;
+  const size_t scale_at = code_at + size_t(M * q.ld + 255) / 256 * 256;
   void* ws = nullptr;
-  st = gb300::lib_workspace(d.dev, stream,
-                            gb300::kWorkspaceCounterBytes + code_bytes + scale_bytes(W->format, M, W->cols), &ws);
+  st = gb300::lib_workspace(d.dev, stream, scale_at + size_t(scale_bytes(W->format, M, W->cols)), &ws);
   if (st != SGEMM_OK) return st;
-  q.codes = static_cast<uint8_t*>(ws) + gb300::kWorkspaceCounterBytes;
-  q.scales = q.codes + code_bytes;
-  if (W->cols != 0 && gb300::launch_fp4_quantize(dtype, x, ldx, q, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-  return status_of(gb300::launch_fp4_simple(q, *W, dtype, y, ldy, stream));
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  q.codes = base + code_at;
+  q.scales = base + scale_at;
+  if (gb300::launch_fp4_quantize(dtype, x, ldx, q, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+  return run_product(p, q, *W, dtype, y, ldy, ws, base + gb300::kWorkspaceCounterBytes, d, stream);
 }
 
 sgemm_status_t fp4_experts_layout(int format, int64_t experts, int64_t d, int64_t f, int64_t* gate_up_bytes,

@@ -7,6 +7,7 @@
 #include <cuda_runtime_api.h>
 
 #include "fp4.h"
+#include "sgemm_plan.h"
 
 namespace gb300 {
 
@@ -17,9 +18,34 @@ cudaError_t launch_fp4_dequantize(const fp4_matrix_t& q, int dtype, void* y, int
 cudaError_t launch_fp4_pack(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales,
                             const fp4_matrix_t& q, cudaStream_t stream);
 
-// C (type dtype) = A B^T with bounds-checked loads (fp4_simple.cu).
-cudaError_t launch_fp4_simple(const fp4_matrix_t& A, const fp4_matrix_t& B, int dtype, void* C, int64_t ldc,
-                              cudaStream_t stream);
+// Products on the tensor cores (fp4_tc.cu): tiles of a row operand by a column
+// operand.  Swapped shapes take B as the row operand.
+enum Fp4TcShape { kFp4Pair, kFp4Single128, kFp4Swap16, kFp4Swap32, kFp4Swap64, kFp4TcShapes };
+struct Fp4TcTile {
+  int rows, cols, ctas;
+  bool swap;
+};
+Fp4TcTile fp4_tc_tile(Fp4TcShape shape);
+// Sets the kernels' attributes on the current device; the CTA pairs that run at once, or < 0.
+int fp4_tc_prepare();
+struct Fp4TcArgs {
+  int32_t rows, cols;  // of the row and the column operand
+  void* out;
+  int64_t ld;
+  const float* factor_r;
+  const float* factor_c;
+  float* partials;    // shares of split tiles: (tiles split + units - 1) slots of a tile
+  int32_t* counters;  // one per CTA of a split tile, zero on entry and on exit
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+  int32_t tma_out;    // the output's rows can be addressed by TMA (map_out)
+  int32_t tma_edge;   // and its row bytes are a multiple of 16
+};
+// maps: codes of the row and the column operand (boxes of 128 rows and of the
+// columns that one CTA stages), their scales (boxes of the atoms of 256
+// columns), the output (boxes of 32 rows x 128 bytes).
+cudaError_t launch_fp4_tc(int dtype, int format, Fp4TcShape shape, const CUtensorMap (&maps)[5],
+                          const Fp4TcArgs& args, const Sched& sc, int grid, cudaStream_t stream);
 
 // The expert weights' order (fp4_moe.cu): tiles of 16 rows; a tile's rows are
 // cut into chunks of 128 columns, stored one after another.

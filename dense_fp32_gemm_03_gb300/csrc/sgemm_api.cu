@@ -725,6 +725,19 @@ sgemm_status_t lib_encode_bytes(const void* base, int64_t rows, int64_t row_byte
              : SGEMM_ERR_LAUNCH;
 }
 
+sgemm_status_t lib_encode_rows512(const void* base, int64_t rows, int box_rows, CUtensorMap* map) {
+  std::memset(map, 0, sizeof(*map));
+  const cuuint32_t estr[2] = {1, 1};
+  const cuuint64_t dims[2] = {128, cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {512};
+  const cuuint32_t box[2] = {128, cuuint32_t(box_rows)};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? SGEMM_OK
+             : SGEMM_ERR_LAUNCH;
+}
+
 }  // namespace gb300
 
 extern "C" {

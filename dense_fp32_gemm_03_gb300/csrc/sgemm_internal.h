@@ -130,5 +130,7 @@ sgemm_status_t lib_workspace(int dev, cudaStream_t stream, size_t need, void** o
 // apart, read in boxes of 128 bytes x box_rows with the 128-byte swizzle.
 sgemm_status_t lib_encode_bytes(const void* base, int64_t rows, int64_t row_bytes, int64_t pitch, int box_rows,
                                 CUtensorMap* map);
+// A 2-D tensor map of contiguous 512-byte rows read in boxes of box_rows whole rows.
+sgemm_status_t lib_encode_rows512(const void* base, int64_t rows, int box_rows, CUtensorMap* map);
 
 }  // namespace gb300

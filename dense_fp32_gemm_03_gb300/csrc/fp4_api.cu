@@ -379,13 +379,14 @@ sgemm_status_t fp4_moe(int dtype, const void* x, int64_t ldx, int64_t M, const f
   a.top = top;
   a.renormalize = renormalize;
   a.logits = reinterpret_cast<float*>(base + s.logits);
-  a.pick = reinterpret_cast<int32_t*>(base + s.pick);
-  a.weight = reinterpret_cast<float*>(base + s.weight);
   a.x_scale = reinterpret_cast<float*>(base + s.x_scale);
   a.h_max = reinterpret_cast<uint32_t*>(base + s.h_max);
   a.x_frag = base + s.x_frag;
   a.h = reinterpret_cast<float*>(base + s.h);
+  a.partial = reinterpret_cast<float*>(base + s.partial);
   a.counters = static_cast<int32_t*>(ws);
+  a.tile_counters = a.counters + 32;
+  a.tile_counter_count = int32_t(gb300::kWorkspaceCounterBytes / 4) - 32;
   a.status = d.status;
   a.wait_limit_ns = d.wait_limit_ns;
   const int64_t bytes = dtype_bytes(dtype);

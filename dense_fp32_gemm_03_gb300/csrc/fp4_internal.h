@@ -70,18 +70,19 @@ struct MoeArgs {
   int32_t tokens, experts, d, f, top, renormalize;
   // Scratch.
   float* logits;      // tokens x experts
-  int32_t* pick;      // tokens x top
-  float* weight;      // tokens x top
   float* x_scale;     // tokens: the power of two that x was multiplied by
   uint32_t* h_max;    // tokens: the largest |h| of the token's pairs, as bits
   void* x_frag;       // x as 16-bit floats in fragment order
   float* h;           // (tokens x top) x f rounded up to 128
+  float* partial;     // shares of the tiles of y: tile x part x token x row
   int32_t* counters;  // three, zero on entry and on exit
+  int32_t* tile_counters;  // one per tile of y (16 rows), zero on entry and on exit
+  int32_t tile_counter_count;
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
 struct MoeScratch {
-  size_t logits, pick, weight, x_scale, h_max, x_frag, h, bytes;  // offsets, and the size of all
+  size_t logits, x_scale, h_max, x_frag, h, partial, bytes;  // offsets, and the size of all
 };
 MoeScratch fp4_moe_scratch(int dtype, int64_t tokens, int64_t experts, int64_t d, int64_t f, int64_t top);
 cudaError_t launch_fp4_moe(int dtype, int format, const MoeArgs& args, int sms, cudaStream_t stream);

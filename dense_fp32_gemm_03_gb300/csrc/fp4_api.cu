@@ -306,9 +306,8 @@ sgemm_status_t fp4_experts_layout(int format, int64_t experts, int64_t d, int64_
   if (st == SGEMM_OK) st = check_extent(experts, 0);
   if (st != SGEMM_OK) return st;
   if (experts > 1024) return SGEMM_ERR_UNSUPPORTED;
-  const int64_t chunk = gb300::fp4_expert_chunk_bytes(format);
-  if (gate_up_bytes) *gate_up_bytes = experts * ((f + 7) / 8) * ((d + 127) / 128) * chunk;
-  if (down_bytes) *down_bytes = experts * ((d + 15) / 16) * ((f + 127) / 128) * chunk;
+  if (gate_up_bytes) *gate_up_bytes = gb300::fp4_gate_up_bytes(format, experts, d, f);
+  if (down_bytes) *down_bytes = gb300::fp4_down_bytes(format, experts, d, f);
   return SGEMM_OK;
 }
 
@@ -359,7 +358,12 @@ sgemm_status_t fp4_moe(int dtype, const void* x, int64_t ldx, int64_t M, const f
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || M == 0) return st;
   const int64_t most = M < gb300::kMoeTokens ? M : gb300::kMoeTokens;
-  const gb300::MoeScratch s = gb300::fp4_moe_scratch(dtype, most, w->experts, w->d, w->f, top);
+  const int64_t used = w->experts < most * top ? w->experts : most * top;
+  // Stage counts of a phase are 32-bit numbers.
+  if (used * ((w->f + 63) / 64) * ((w->d + 255) / 256) > 0x7fffffffLL ||
+      used * ((w->f + 255) / 256) * ((w->d + 127) / 128) > 0x7fffffffLL)
+    return SGEMM_ERR_UNSUPPORTED;
+  const gb300::MoeScratch s = gb300::fp4_moe_scratch(dtype, w->format, most, w->experts, w->d, w->f, top, d.sms);
   void* ws = nullptr;
   st = gb300::lib_workspace(d.dev, stream, gb300::kWorkspaceCounterBytes + s.bytes, &ws);
   if (st != SGEMM_OK) return st;
@@ -379,14 +383,14 @@ sgemm_status_t fp4_moe(int dtype, const void* x, int64_t ldx, int64_t M, const f
   a.top = top;
   a.renormalize = renormalize;
   a.logits = reinterpret_cast<float*>(base + s.logits);
-  a.x_scale = reinterpret_cast<float*>(base + s.x_scale);
-  a.h_max = reinterpret_cast<uint32_t*>(base + s.h_max);
-  a.x_frag = base + s.x_frag;
-  a.h = reinterpret_cast<float*>(base + s.h);
+  a.x_exp = reinterpret_cast<int32_t*>(base + s.x_exp);
+  a.x_norm = reinterpret_cast<float*>(base + s.x_norm);
+  a.x_image = base + s.x_image;
+  a.h_image = base + s.h_image;
   a.partial = reinterpret_cast<float*>(base + s.partial);
+  a.bound = gb300::fp4_expert_bounds(*w);
+  a.cols = s.cols;
   a.counters = static_cast<int32_t*>(ws);
-  a.tile_counters = a.counters + 32;
-  a.tile_counter_count = int32_t(gb300::kWorkspaceCounterBytes / 4) - 32;
   a.status = d.status;
   a.wait_limit_ns = d.wait_limit_ns;
   const int64_t bytes = dtype_bytes(dtype);

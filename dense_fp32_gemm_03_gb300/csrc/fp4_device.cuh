@@ -64,6 +64,13 @@ __device__ __forceinline__ float decode_e4m3(uint32_t byte) {
   return __low2float(*reinterpret_cast<__half2*>(&h));
 }
 
+// Two scale bytes, low one first.
+__device__ __forceinline__ float2 decode_e4m3x2(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(two)));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
 // 2^(byte - 127); 255: NaN.
 __device__ __forceinline__ float decode_e8m0(uint32_t byte) {
   const uint32_t bits = byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23;

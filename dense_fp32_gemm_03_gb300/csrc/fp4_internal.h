@@ -47,9 +47,11 @@ struct Fp4TcArgs {
 cudaError_t launch_fp4_tc(int dtype, int format, Fp4TcShape shape, const CUtensorMap (&maps)[5],
                           const Fp4TcArgs& args, const Sched& sc, int grid, cudaStream_t stream);
 
-// The expert weights' order (fp4_moe.cu): tiles of 16 rows; a tile's rows are
-// cut into chunks of 128 columns, stored one after another.
-int64_t fp4_expert_chunk_bytes(int format);
+// The expert weights' order (fp4_moe.cu): blocks of 128 rows x 256 columns as
+// one stage of the layer's kernel takes them; after the gate-and-up blocks one 32-bit bound an expert.
+int64_t fp4_gate_up_bytes(int format, int64_t experts, int64_t d, int64_t f);
+int64_t fp4_down_bytes(int format, int64_t experts, int64_t d, int64_t f);
+const uint32_t* fp4_expert_bounds(const fp4_experts_t& w);
 cudaError_t launch_fp4_experts_pack(const fp4_matrix_t& gate_up, const fp4_matrix_t& down,
                                     const fp4_experts_t& w, cudaStream_t stream);
 
@@ -68,23 +70,25 @@ struct MoeArgs {
   int32_t* ids;
   float* p;
   int32_t tokens, experts, d, f, top, renormalize;
+  const uint32_t* bound;  // per expert (fp4_expert_bounds)
+  int32_t cols;           // columns of a product: tokens x terms, rounded up to 16
   // Scratch.
   float* logits;      // tokens x experts
-  float* x_scale;     // tokens: the power of two that x was multiplied by
-  uint32_t* h_max;    // tokens: the largest |h| of the token's pairs, as bits
-  void* x_frag;       // x as 16-bit floats in fragment order
-  float* h;           // (tokens x top) x f rounded up to 128
-  float* partial;     // shares of the tiles of y: tile x part x token x row
-  int32_t* counters;  // three, zero on entry and on exit
-  int32_t* tile_counters;  // one per tile of y (16 rows), zero on entry and on exit
-  int32_t tile_counter_count;
+  int32_t* x_exp;     // tokens: x was multiplied by 2^x_exp
+  float* x_norm;      // tokens: log2 of x's 2-norm
+  uint8_t* x_image;   // x as terms: a block of columns for each 256 of d
+  uint8_t* h_image;   // h as terms: the same for each expert in use and 256 of f
+  float* partial;     // shares of units cut between CTAs: CTA x 2 x token x row
+  int32_t* counters;  // the workspace's counters, zero on entry and on exit
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
 struct MoeScratch {
-  size_t logits, x_scale, h_max, x_frag, h, partial, bytes;  // offsets, and the size of all
+  size_t logits, x_exp, x_norm, x_image, h_image, partial, bytes;  // offsets, and the size of all
+  int cols;
 };
-MoeScratch fp4_moe_scratch(int dtype, int64_t tokens, int64_t experts, int64_t d, int64_t f, int64_t top);
+MoeScratch fp4_moe_scratch(int dtype, int format, int64_t tokens, int64_t experts, int64_t d, int64_t f, int64_t top,
+                           int sms);
 cudaError_t launch_fp4_moe(int dtype, int format, const MoeArgs& args, int sms, cudaStream_t stream);
 
 }  // namespace gb300

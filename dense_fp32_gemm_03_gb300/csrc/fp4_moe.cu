@@ -3,16 +3,23 @@
 //
 // Mathematics.  A token takes part in `top` of the experts, so a few tokens
 // touch each expert's weights for one or two columns only: the layer is bound
-// by reading the weights once.  Weights become 16-bit floats (exact) in
-// registers and are multiplied by mma.m16n8k16, 16 weight rows by eight
-// columns.  Activations enter as 16-bit floats relative to a power of two of
-// the token: one column a token where x has 16 bits, two (the value rounded
-// to 11 bits, and the rest) where it has 32.  A block's products are summed
-// first and then scaled by its unit, in 32 bits.
+// by reading the weights once.  Turning each weight into a wider number in
+// registers takes more instructions than the memory allows time for (an
+// mma.m16n8k16 form of this kernel ran at a quarter of the bandwidth), so the
+// weights go to the tensor core as they are stored, block-scaled 4-bit, and the
+// activations are brought to the same form without loss that matters: a value is
+// the sum of kTerms terms 4^-j u_j q_j, each the 4-bit quantisation of what the
+// terms before it left (times 4, so that an 8-bit scale can follow).  A term takes off
+// a factor of 6 or more in the worst case and about 8 in the mean.  With 4
+// terms (bfloat16) the rest is about 2^-13 of the block's largest value, with 6
+// (16-bit float) 2^-19 and with 8 (32 bits) 2^-25: below the rounding of the
+// types, in the mean.  A token and term is one column of the product, and the
+// columns' 32-bit sums are added with their powers of 4 at the end.
 #include <cuda_runtime.h>
 
 #include "fp4_device.cuh"
 #include "fp4_internal.h"
+#include "fp4_tc.cuh"
 #include "sgemm_device.cuh"
 
 namespace gb300 {
@@ -23,210 +30,200 @@ using namespace fp4;
 constexpr int kPackThreads = 256;
 constexpr int kThreads = 512;  // of the layer's kernel, one CTA to an SM
 constexpr int kWarps = kThreads / 32;
-constexpr int kTeamWarps = 4;  // warps that share a gate-and-up tile
-constexpr int kTeams = kWarps / kTeamWarps;
-constexpr int kRing = 4;  // chunks that a warp has under way
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTop = 32;
 constexpr int kMaxPairs = kMoeTokens * kMaxTop;
-constexpr int kMaxParts = 8;
+constexpr int kMaxStages = 8;
 constexpr uint32_t kStatusTimeout = 3;
+constexpr int kSmemBytes = 232448;
 
+template <typename T>
+struct Terms {
+  static constexpr int kCount = 8;  // 32 bits
+};
+template <>
+struct Terms<__nv_bfloat16> {
+  static constexpr int kCount = 4;
+};
+template <>
+struct Terms<__half> {
+  static constexpr int kCount = 6;
+};
+static_assert(kMoeTokens * 8 <= 128, "columns of one product");
+
+// 128 rows x 256 columns of weights: the codes as the 128-byte swizzle lays them
+// out in shared memory, then the scale atoms.  One stage of the ring; the
+// columns' blocks (`cols` rows x 256) have the same form.
 template <int kFormat>
-struct Chunk {  // 16 rows x 128 columns
-  static constexpr int kScaleBytes = 16 * 128 / Format<kFormat>::kBlock;
-  static constexpr int kBytes = 1024 + kScaleBytes;
+struct Block {
+  static constexpr int kAtoms = Format<kFormat>::kAtomsPerStage;
+  static constexpr uint32_t kScales = kAtoms * 512;
+  static constexpr uint32_t kBytes = 16384 + kScales;
 };
 
+// Byte of 16-byte piece `piece` of row r in a block's codes.
+__host__ __device__ __forceinline__ uint32_t piece_at(uint32_t r, uint32_t piece) {
+  return r * 128 + ((piece ^ (r & 7)) << 4);
+}
+// Byte of the scale of row r, block b (of 256 / kBlock) among a block's scales.
+__host__ __device__ __forceinline__ uint32_t scale_at(uint32_t r, uint32_t b) {
+  return (b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3);
+}
+
 // ------------------------------------------------------------------ packing
-// One thread makes the 16 bytes of one lane and half of a chunk.  Row g and
-// row g + 8 of a gate-and-up tile are gate row 8 tile + g and up row 8 tile + g.
+// One thread moves one 16-byte piece of codes, and the first threads of a row
+// its scales.  A gate-and-up tile has 64 gate rows and the 64 up rows beside them.
 template <int kFormat, bool kGateUp>
 __global__ void __launch_bounds__(kPackThreads)
     pack_experts_kernel(const fp4_matrix_t q, int64_t experts, int64_t rows_per, uint8_t* __restrict__ out) {
-  using F = Format<kFormat>;
-  const int64_t tiles = kGateUp ? (rows_per + 7) / 8 : (rows_per + 15) / 16;
-  const int64_t chunks = (q.cols + 127) / 128;
-  const int64_t atoms = (q.cols + 255) / 256 * F::kAtomsPerStage;
-  const int64_t items = experts * tiles * chunks * 64;
+  using B = Block<kFormat>;
+  const int64_t tiles = kGateUp ? (rows_per + 63) / 64 : (rows_per + 127) / 128;
+  const int64_t stages = (q.cols + 255) / 256, atoms = stages * B::kAtoms;
+  const int64_t pitch = (q.cols + 31) / 32 * 16;
+  const int64_t items = experts * tiles * stages * 1024;
   for (int64_t i = int64_t(blockIdx.x) * kPackThreads + threadIdx.x; i < items;
        i += int64_t(gridDim.x) * kPackThreads) {
-    const int lane = int(i & 31), half = int(i >> 5) & 1;
-    const int64_t c = (i >> 6) % chunks, tile = (i >> 6) / chunks % tiles, e = (i >> 6) / chunks / tiles;
-    const int g = lane >> 2, t = lane & 3;
-    int64_t row[2];
-    bool in[2];
+    const int piece = int(i & 7), r = int(i >> 3) & 127;
+    const int64_t block = i >> 10, s = block % stages, tile = block / stages % tiles, e = block / stages / tiles;
+    int64_t row;
+    bool in;
     if (kGateUp) {
-      const int64_t r = tile * 8 + g;
-      in[0] = in[1] = r < rows_per;
-      row[0] = e * 2 * rows_per + r;
-      row[1] = row[0] + rows_per;
+      const int64_t f = tile * 64 + (r & 63);
+      in = f < rows_per;
+      row = (2 * e + (r >> 6)) * rows_per + f;
     } else {
-      for (int s = 0; s < 2; ++s) {
-        const int64_t r = tile * 16 + g + 8 * s;
-        in[s] = r < rows_per;
-        row[s] = e * rows_per + r;
+      const int64_t d = tile * 128 + r;
+      in = d < rows_per;
+      row = e * rows_per + d;
+    }
+    uint8_t* dst = out + block * B::kBytes;
+    const int64_t at = s * 128 + piece * 16;
+    *reinterpret_cast<uint4*>(dst + piece_at(r, piece)) =
+        in && at < pitch ? *reinterpret_cast<const uint4*>(q.codes + row * q.ld + at) : make_uint4(0u, 0u, 0u, 0u);
+    if (piece < B::kAtoms)
+      *reinterpret_cast<uint32_t*>(dst + 16384 + scale_at(r, piece * 4)) =
+          in ? *reinterpret_cast<const uint32_t*>(q.scales + scale_offset(row, (s * B::kAtoms + piece) * 4, atoms)) : 0u;
+  }
+}
+
+// bound[e] = the largest |gate row| |up row| (2-norms, with the factor) of expert e, as
+// bits: with the token's norm it bounds h.  One warp to a pair of rows.
+template <int kFormat>
+__global__ void __launch_bounds__(kPackThreads)
+    bound_kernel(const fp4_matrix_t q, int64_t experts, int64_t f, uint32_t* __restrict__ bound) {
+  using F = Format<kFormat>;
+  const int lane = threadIdx.x & 31;
+  const int64_t atoms = (q.cols + 255) / 256 * F::kAtomsPerStage;
+  const float g = kFormat == FP4_NVFP4 && q.factor != nullptr ? __ldg(q.factor) : 1.f;
+  const int64_t warps = int64_t(gridDim.x) * (kPackThreads / 32);
+  for (int64_t i = int64_t(blockIdx.x) * (kPackThreads / 32) + (threadIdx.x >> 5); i < experts * f; i += warps) {
+    const int64_t e = i / f, row = 2 * e * f + (i - e * f);
+    float sum[2] = {0.f, 0.f};
+    for (int s = 0; s < 2; ++s)
+      for (int64_t c = lane * 8; c < q.cols; c += 256) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q.codes + (row + s * f) * q.ld + c / 2));
+        const float u = decode_scale<kFormat>(__ldg(q.scales + scale_offset(row + s * f, c / F::kBlock, atoms))) * g;
+        const float2 v[4] = {__half22float2(decode2<0>(w)), __half22float2(decode2<1>(w)),
+                             __half22float2(decode2<2>(w)), __half22float2(decode2<3>(w))};
+        float part = 0.f;
+        for (int j = 0; j < 4; ++j) part += v[j].x * v[j].x + v[j].y * v[j].y;
+        sum[s] += part * u * u;
       }
+    for (int s = 16; s; s >>= 1) {
+      sum[0] += __shfl_xor_sync(kFull, sum[0], s);
+      sum[1] += __shfl_xor_sync(kFull, sum[1], s);
     }
-    uint8_t* dst = out + ((e * tiles + tile) * chunks + c) * Chunk<kFormat>::kBytes;
-    uint32_t word[4];
-    for (int j = 0; j < 4; ++j) {
-      const int64_t k = c * 128 + half * 64 + j * 16 + t * 4;
-      uint32_t v[2];
-      for (int s = 0; s < 2; ++s)
-        v[s] = in[s] && k < q.cols ? *reinterpret_cast<const uint16_t*>(q.codes + row[s] * q.ld + k / 2) : 0u;
-      word[j] = (v[0] & 0xffu) | (v[1] & 0xffu) << 8 | (v[0] >> 8) << 16 | (v[1] >> 8) << 24;
-    }
-    reinterpret_cast<uint4*>(dst)[half * 32 + lane] = make_uint4(word[0], word[1], word[2], word[3]);
-    // Scales of row pair g: the blocks of row g, then those of row g + 8.
-    constexpr int kPer = 128 / F::kBlock;
-    if (half == 0 && t < 2) {
-      for (int b = 0; b < kPer; ++b) {
-        const int64_t k = c * kPer + b;
-        dst[1024 + g * 2 * kPer + t * kPer + b] =
-            in[t] && k * F::kBlock < q.cols ? q.scales[scale_offset(row[t], k, atoms)] : 0;
-      }
-    }
+    if (lane == 0) atomicMax(bound + e, __float_as_uint(sqrtf(sum[0]) * sqrtf(sum[1])));
   }
 }
 
 // ------------------------------------------------------------------ helpers
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint2 b) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+__device__ __forceinline__ float pow2f(int e) {  // 2^e for -126 <= e <= 127
+  return __uint_as_float(uint32_t(127 + e) << 23);
 }
 
-__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-
-// The power of two that brings a largest magnitude (as bits) to [2^14, 2^15),
-// well inside a 16-bit float; at most 2^126, and 1 for 0, NaN and infinity.
-__device__ __forceinline__ float pow2_scale(uint32_t top) {
-  if (top == 0 || top >= 0x7f800000u) return 1.f;
-  const int e = int(top >> 23);  // 127 + floor(log2)
-  return __uint_as_float(uint32_t(min(127 + 14 + 127 - e, 253)) << 23);
-}
-
-// Column of the mma: token and part.  kSplit: columns 2 n and 2 n + 1 are the
-// rounded value and the rest of token n.
-template <bool kSplit>
-struct Columns {
-  static constexpr int kTokens = kSplit ? 4 : 8;  // per group of eight columns
-  __device__ static int token(int group, int col) { return group * kTokens + (kSplit ? col >> 1 : col); }
-};
-
-// Four values (times `scale`) as the two B registers of this lane.
-template <bool kSplit>
-__device__ __forceinline__ uint2 to_frag(const float4& v, float scale, int col) {
-  const float x[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
-  __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
-  if (kSplit && (col & 1)) {
-    const float2 fa = __half22float2(a), fb = __half22float2(b);
-    a = __floats2half2_rn(x[0] - fa.x, x[1] - fa.y);
-    b = __floats2half2_rn(x[2] - fb.x, x[3] - fb.y);
-  }
-  return make_uint2(h2_bits(a), h2_bits(b));
-}
-
-// A chunk of weights on its way through registers: codes of 64 columns each,
-// and the scale bytes of row g (first half) and row g + 8.
+// Scale byte of a term whose block's largest magnitude has the bits `top`, and its
+// unit: nearest 8-bit float to a / 6, or the smallest power of two from a / 6 up.
 template <int kFormat>
-struct ChunkRegs {
-  static constexpr int kPer = 128 / Format<kFormat>::kBlock;  // blocks of a row
-  uint4 w[2];
-  uint32_t sc[2][kPer / 4];
-
-  __device__ __forceinline__ void load(const uint8_t* __restrict__ chunk, int lane) {
-    const uint4* codes = reinterpret_cast<const uint4*>(chunk);
-    w[0] = __ldg(codes + lane);
-    w[1] = __ldg(codes + 32 + lane);
-    if constexpr (kPer == 8) {
-      const uint4 s = __ldg(reinterpret_cast<const uint4*>(chunk + 1024) + (lane >> 2));
-      sc[0][0] = s.x, sc[0][1] = s.y, sc[1][0] = s.z, sc[1][1] = s.w;
-    } else {
-      const uint2 s = __ldg(reinterpret_cast<const uint2*>(chunk + 1024) + (lane >> 2));
-      sc[0][0] = s.x, sc[1][0] = s.y;
-    }
+__device__ __forceinline__ uint32_t term_scale(uint32_t top, float& unit) {
+  if (top >= 0x7f800000u) {
+    unit = 0.f;
+    return kFormat == FP4_MXFP4 ? 255u : 127u;
   }
-};
-
-// acc[q] += (16 rows x 128 columns of weights) * (128 x 8 columns of group q),
-// for the groups in `mask`.  frag(q, s) gives the lane's B registers of the
-// steps 2 s and 2 s + 1.
-template <int kFormat, int kGroups, typename Frag>
-__device__ __forceinline__ void chunk_mma(const ChunkRegs<kFormat>& in, uint32_t mask, float (&acc)[kGroups][4],
-                                          Frag frag) {
-  constexpr int kSteps = Format<kFormat>::kBlock / 16;  // mma steps of a block
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {  // two steps, 32 columns
-    uint32_t a[2][4];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int step = 2 * p + s;
-      const uint4& h = in.w[step >> 2];
-      const uint32_t word = (step & 3) == 0 ? h.x : (step & 3) == 1 ? h.y : (step & 3) == 2 ? h.z : h.w;
-      a[s][0] = h2_bits(decode2<0>(word));
-      a[s][1] = h2_bits(decode2<1>(word));
-      a[s][2] = h2_bits(decode2<2>(word));
-      a[s][3] = h2_bits(decode2<3>(word));
-    }
-    float u[2][2 / kSteps];  // units: row g or g + 8, block
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int s = 0; s < 2 / kSteps; ++s) {
-        const int b = p * (2 / kSteps) + s;
-        u[r][s] = decode_scale<kFormat>((in.sc[r][b / 4] >> (8 * (b & 3))) & 0xffu);
-      }
-#pragma unroll
-    for (int q = 0; q < kGroups; ++q) {
-      if (kGroups > 1 && !(mask >> q & 1)) continue;
-      const uint4 f = frag(q, p);
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mma16816(d, a[0][0], a[0][1], a[0][2], a[0][3], make_uint2(f.x, f.y));
-      if constexpr (kSteps == 1) {
-        acc[q][0] = fmaf(u[0][0], d[0], acc[q][0]);
-        acc[q][1] = fmaf(u[0][0], d[1], acc[q][1]);
-        acc[q][2] = fmaf(u[1][0], d[2], acc[q][2]);
-        acc[q][3] = fmaf(u[1][0], d[3], acc[q][3]);
-        d[0] = d[1] = d[2] = d[3] = 0.f;
-      }
-      mma16816(d, a[1][0], a[1][1], a[1][2], a[1][3], make_uint2(f.z, f.w));
-      constexpr int kLast = 2 / kSteps - 1;
-      acc[q][0] = fmaf(u[0][kLast], d[0], acc[q][0]);
-      acc[q][1] = fmaf(u[0][kLast], d[1], acc[q][1]);
-      acc[q][2] = fmaf(u[1][kLast], d[2], acc[q][2]);
-      acc[q][3] = fmaf(u[1][kLast], d[3], acc[q][3]);
-    }
+  const float s = __uint_as_float(top) * (1.f / 6.f);
+  if constexpr (kFormat == FP4_MXFP4) {
+    const uint32_t bits = __float_as_uint(s);
+    const uint32_t byte = min((bits >> 23) + ((bits & 0x7fffffu) != 0 ? 1u : 0u), 254u);
+    unit = byte == 0 ? 0.f : __uint_as_float(byte << 23);
+    return byte;
+  } else {
+    const uint32_t byte = encode_e4m3(s);
+    unit = decode_e4m3(byte);
+    return byte;
   }
 }
 
-// Sum over `warps` warps' accumulators of (row, token): red is [warp][group][4][32].
-template <bool kSplit, int kGroups>
-__device__ __forceinline__ float reduce(const float* red, int warps, int row, int token) {
-  const int q = token / Columns<kSplit>::kTokens, n = token % Columns<kSplit>::kTokens;
-  const int g = row & 7, upper = (row >> 3) * 2;
-  float sum = 0.f;
-#pragma unroll 4
-  for (int w = 0; w < warps; ++w) {
-    const float* p = red + (w * kGroups + q) * 128;
-    if (kSplit)
-      sum += p[upper * 32 + g * 4 + n] + p[(upper + 1) * 32 + g * 4 + n];
+// The code of r / unit; r becomes what the term leaves, times 4.
+__device__ __forceinline__ uint32_t term_code(float& r, float unit, float inv) {
+  const uint32_t code = encode2(r * inv, 0.f) & 15u;
+  r = fmaf(-__low2float(decode2<0>(code)), unit, r) * 4.f;
+  return code;
+}
+
+// One block of a row of activations, held by one thread, as kTerms rows of `image`
+// (a block of columns): rows row .. row + kTerms - 1, columns from `col`.
+template <int kFormat, int kTerms>
+__device__ __forceinline__ void write_terms(float (&v)[Format<kFormat>::kBlock], uint8_t* image, uint32_t cols,
+                                            uint32_t row, uint32_t col) {
+  constexpr int kBlock = Format<kFormat>::kBlock;
+#pragma unroll 1
+  for (int j = 0; j < kTerms; ++j, ++row) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kBlock; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    float unit;
+    const uint32_t byte = term_scale<kFormat>(top, unit);
+    const float inv = unit > 0.f ? __frcp_rn(unit) : 0.f;
+    uint32_t w[kBlock / 8];
+#pragma unroll
+    for (int i = 0; i < kBlock / 8; ++i) {
+      w[i] = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[i] |= term_code(v[8 * i + k], unit, inv) << (4 * k);
+    }
+    uint8_t* at = image + piece_at(row, col >> 5) + (col & 16) / 2;
+    if constexpr (kBlock == 32)
+      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
     else
-      sum += p[(upper + (n & 1)) * 32 + g * 4 + (n >> 1)];
+      *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+    image[cols * 128 + scale_at(row, col / kBlock)] = uint8_t(byte);
   }
-  return sum;
 }
 
-template <int kGroups>
-__device__ __forceinline__ void publish(float* red, const float (&acc)[kGroups][4], int warp, int lane) {
+// The same for 32 columns from `col`, a value to a lane.
+template <int kFormat, int kTerms>
+__device__ __forceinline__ void write_terms_warp(float r, uint8_t* image, uint32_t cols, uint32_t row, uint32_t col,
+                                                 int lane) {
+  constexpr int kBlock = Format<kFormat>::kBlock;
 #pragma unroll
-  for (int q = 0; q < kGroups; ++q)
+  for (int j = 0; j < kTerms; ++j, ++row) {
+    uint32_t top = __float_as_uint(r) & 0x7fffffffu;
+    if constexpr (kBlock == 32) {
+      top = __reduce_max_sync(kFull, top);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[((warp * kGroups + q) * 4 + i) * 32 + lane] = acc[q][i];
+      for (int s = 8; s; s >>= 1) top = max(top, __shfl_xor_sync(kFull, top, s));
+    }
+    float unit;
+    const uint32_t byte = term_scale<kFormat>(top, unit);
+    uint32_t w = term_code(r, unit, unit > 0.f ? __frcp_rn(unit) : 0.f);
+    w |= __shfl_xor_sync(kFull, w, 1) << 4;
+    w |= __shfl_xor_sync(kFull, w, 2) << 8;
+    w |= __shfl_xor_sync(kFull, w, 4) << 16;
+    if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(image + piece_at(row, col >> 5) + lane / 2) = w;
+    if (lane % kBlock == 0) image[cols * 128 + scale_at(row, (col + lane) / kBlock)] = uint8_t(byte);
+  }
 }
 
 // ------------------------------------------------------------------ routing
@@ -290,6 +287,42 @@ __device__ __forceinline__ void select_top(const float* logits, int experts, int
   }
 }
 
+// The same for any number of experts, reading the logits again for each choice.
+__device__ __forceinline__ void select_top_any(const float* logits, int experts, int top, int renorm, int lane,
+                                               uint16_t* ids, float* weight) {
+  float peak = -INFINITY, sum = 0.f;
+  for (int e = lane; e < experts; e += 32) peak = fmaxf(peak, __ldcg(logits + e));
+  for (int s = 16; s; s >>= 1) peak = fmaxf(peak, __shfl_xor_sync(kFull, peak, s));
+  for (int e = lane; e < experts; e += 32) sum += expf(__ldcg(logits + e) - peak);
+  for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
+  uint64_t last = ~0ull;  // larger key and smaller index first
+  float mine = 0.f;
+  int mine_id = 0;
+  for (int j = 0; j < top; ++j) {
+    uint64_t best = 0;
+    for (int e = lane; e < experts; e += 32) {
+      const uint64_t k = uint64_t(order_key(__ldcg(logits + e))) << 32 | (0xffffffffu - uint32_t(e));
+      if (k < last && k > best) best = k;
+    }
+    for (int s = 16; s; s >>= 1) {
+      const uint64_t o = __shfl_xor_sync(kFull, best, s);
+      best = o > best ? o : best;
+    }
+    last = best;
+    const int id = int(0xffffffffu - uint32_t(best));
+    if (lane == j) mine = expf(__ldcg(logits + id) - peak) / sum, mine_id = id;
+  }
+  if (renorm) {
+    float total = mine;
+    for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(kFull, total, s);
+    mine /= total;
+  }
+  if (lane < top) {
+    ids[lane] = uint16_t(mine_id);
+    weight[lane] = mine;
+  }
+}
+
 // Four consecutive values of a row, zeros beyond `n`.
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p, int k, int n, bool vector) {
@@ -335,37 +368,122 @@ __device__ __forceinline__ bool grid_barrier(int32_t* counter, const MoeArgs& ar
 }
 
 // -------------------------------------------------------------------- layer
+// A phase's work: `units` sums of `steps` stages each, cut into equal runs of
+// stages, one to a CTA.  A unit that ends in another CTA's run than it began is
+// joined by the last of its CTAs to finish, in their order.
+struct Runs {
+  int steps, base, extra;
+  __device__ __forceinline__ Runs(int units, int steps_, int ctas) : steps(steps_) {
+    const int total = units * steps;
+    base = total / ctas;
+    extra = total - base * ctas;
+  }
+  __device__ __forceinline__ int start(int cta) const { return cta * base + min(cta, extra); }
+  __device__ __forceinline__ int owner(int at) const {
+    const int big = extra * (base + 1);
+    return at < big ? at / (base + 1) : extra + (at - big) / base;
+  }
+};
+
+struct Smem {
+  float weight[kMoeTokens][kMaxTop];
+  float gate_up[kMoeTokens][128];       // finished sums of a tile, by the expert's tokens
+  float red[kWarps];
+  float norm[kWarps];
+  int x_exp[kMoeTokens], h_exp[kMoeTokens];  // x and h are multiplied by these powers of two
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+  uint16_t ids[kMoeTokens][kMaxTop];
+  uint16_t mask[kMaxExperts];           // tokens that go to an expert
+  uint16_t active[kMaxPairs];           // experts in use, in order
+  uint8_t slot[kMaxPairs][kMoeTokens];  // place of an expert in use among a token's, or 255
+  uint8_t nth[kMaxPairs][kMoeTokens];   // the tokens of an expert in use
+  uint32_t tmem, top;
+  int count, flag, last;
+  volatile int abort;
+};
+constexpr int kStageArea = kSmemBytes - 1024 - int((sizeof(Smem) + 127) / 128 * 128);
+
+// Ring position: slot, and how often the ring went round.
+struct At {
+  uint32_t slot = 0, lap = 0;
+  __device__ __forceinline__ void next(uint32_t stages) {
+    if (++slot == stages) slot = 0, ++lap;
+  }
+};
+
+// Orders global writes of ordinary stores before later bulk copies, and the other way round.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// This lane's row of kTerms columns of tensor memory, as one value.
+template <int kTerms>
+__device__ __forceinline__ float read_terms(uint32_t taddr) {
+  float v[8];
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  if constexpr (kTerms == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
+  else
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  float sum = v[kTerms - 1];
+#pragma unroll
+  for (int j = kTerms - 2; j >= 0; --j) sum = fmaf(sum, 0.25f, v[j]);
+  return sum;
+}
+
 // Three phases with a grid barrier between them.
 //  1. Router: a CTA to an expert computes the logits of all tokens; a CTA to a
-//     token makes its fragments.
-//  2. Every CTA selects the experts (the same way), then teams of four warps
-//     compute gate-and-up tiles (8 values of h), K shared among the warps.
-//  3. The CTA's 16 warps share the K of all experts in use for one tile of 16
-//     rows of y; where whole tiles leave SMs idle, a tile's experts are cut into
-//     `parts`, joined in order by the last CTA to finish one.
-// Weights stream through a ring of four chunks a warp, across tile borders.
-template <typename T, int kFormat, bool kSplitX, int kGroupsX, bool kSplitH, int kGroupsH>
+//     token turns x into terms.
+//  2. Every CTA selects the experts (the same way).  Units are (expert in use,
+//     64 values of h); a stage is 256 columns of x.
+//  3. Units are 128 rows of y; the stages run over all experts in use, h of a token
+//     that does not go to one being zero there.
+// In phases 2 and 3 one thread streams stages (weights and columns, one bulk copy
+// each), one issues the MMAs, and four warps join, activate and store.  The
+// weights of phase 3's first stages are asked for before its barrier.
+template <typename T, int kFormat>
 __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
-  constexpr int kRedX = kTeams * kTeamWarps * kGroupsX * 128, kRedH = kWarps * kGroupsH * 128;
-  __shared__ float s_red[kRedX > kRedH ? kRedX : kRedH];
-  __shared__ float s_weight[kMoeTokens][kMaxTop];
-  __shared__ uint16_t s_ids[kMoeTokens][kMaxTop];
-  __shared__ uint16_t s_mask[kMaxExperts];        // tokens that go to an expert
-  __shared__ uint16_t s_active[kMaxPairs];        // experts in use, in order
-  __shared__ uint8_t s_slot[kMaxPairs][kMoeTokens];  // place of an expert in use among a token's
-  __shared__ int s_count, s_flag;
-  __shared__ uint32_t s_top;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  using B = Block<kFormat>;
+  constexpr int kTerms = Terms<T>::kCount, kBlock = Format<kFormat>::kBlock;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* area = smem_raw + ((1024u - (dev::smem_addr(smem_raw) & 1023u)) & 1023u);
+  Smem& sm = *reinterpret_cast<Smem*>(area + kStageArea);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x, ctas = gridDim.x;
   const int tokens = args.tokens, experts = args.experts, top = args.top, d = args.d, f = args.f;
-  const int d_chunks = (d + 127) / 128, f_chunks = (f + 127) / 128;
+  const int d_steps = (d + 255) / 256, f_steps = (f + 255) / 256;
+  const uint32_t cols = uint32_t(args.cols), col_bytes = cols * 128 + B::kScales;
+  const uint32_t stage_bytes = B::kBytes + col_bytes;
+  const uint32_t stages = min(uint32_t(kStageArea) / stage_bytes, uint32_t(kMaxStages));
+  const uint64_t limit = args.wait_limit_ns;
 
-  // ---- router and fragments
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dev::smem_addr(&sm.tmem)),
+                 "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      dev::mbar_init(&sm.full[s], 1);
+      dev::mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      dev::mbar_init(&sm.acc_full[b], 1);
+      dev::mbar_init(&sm.acc_empty[b], 4);
+    }
+    dev::mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    dev::mbar_init_fence();
+  }
+
+  // ---- phase 1
   {
     const T* x = static_cast<const T*>(args.x);
     const bool vec_x = (reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T))) == 0 && args.ldx % 4 == 0;
     const bool vec_r = (reinterpret_cast<uintptr_t>(args.router) & 15u) == 0 && args.ldr % 4 == 0;
     const int share = kWarps / tokens;  // warps to a token
-    for (int item = blockIdx.x; item < experts + tokens; item += gridDim.x) {
+    for (int item = cta; item < experts + tokens; item += ctas) {
       if (item < experts) {
         const float* r = args.router + item * args.ldr;
         float sum = 0.f;
@@ -378,19 +496,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
             sum = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, sum))));
           }
           for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
-          if (lane == 0) s_red[warp] = sum;
+          if (lane == 0) sm.red[warp] = sum;
         }
         __syncthreads();
         if (threadIdx.x < tokens) {
           float total = 0.f;
-          for (int w = 0; w < share; ++w) total += s_red[threadIdx.x * share + w];
+          for (int w = 0; w < share; ++w) total += sm.red[threadIdx.x * share + w];
           args.logits[threadIdx.x * experts + item] = total;
         }
         __syncthreads();
       } else {
         const int t = item - experts;
         const T* xt = x + t * args.ldx;
-        if (threadIdx.x == 0) s_top = 0;
+        if (threadIdx.x == 0) sm.top = 0;
         __syncthreads();
         uint32_t most = 0;
         for (int k = threadIdx.x * 4; k < d; k += kThreads * 4) {
@@ -399,336 +517,385 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
                      max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
         }
         most = __reduce_max_sync(kFull, most);
-        if (lane == 0) atomicMax(&s_top, most);
+        if (lane == 0) atomicMax(&sm.top, most);
         __syncthreads();
-        const float scale = pow2_scale(s_top);
-        const int group = t / Columns<kSplitX>::kTokens, n = t % Columns<kSplitX>::kTokens;
-        // Fragments: steps 2 s and 2 s + 1 of a lane (column, l) lie together.
-        uint2* frag = static_cast<uint2*>(args.x_frag) + int64_t(group) * d_chunks * 256;
-        for (int i = threadIdx.x; i < d_chunks * 32; i += kThreads) {
-          const float4 v = load4(xt, i * 4, d, vec_x);
-          const int step = i >> 2, l = i & 3;
+        // x 2^e has its largest magnitude in [2^10, 2^11), under 6 times the largest scale.
+        int e = 0;
+        if (sm.top != 0 && sm.top < 0x7f800000u) e = max(min(10 - (int(sm.top >> 23) - 127), 126), -126);
+        const float scale = pow2f(e);
+        float square = 0.f;
+        for (int b = threadIdx.x; b < d_steps * (256 / kBlock); b += kThreads) {
+          float v[kBlock];
 #pragma unroll
-          for (int part = 0; part < (kSplitX ? 2 : 1); ++part) {
-            const int col = kSplitX ? 2 * n + part : n;
-            frag[((step >> 1) * 32 + col * 4 + l) * 2 + (step & 1)] = to_frag<kSplitX>(v, scale, col);
+          for (int i = 0; i < kBlock; i += 4) {
+            const float4 q = load4(xt, b * kBlock + i, d, vec_x);
+            v[i] = q.x * scale, v[i + 1] = q.y * scale, v[i + 2] = q.z * scale, v[i + 3] = q.w * scale;
+            square += v[i] * v[i] + v[i + 1] * v[i + 1] + v[i + 2] * v[i + 2] + v[i + 3] * v[i + 3];
+          }
+          const uint32_t at = uint32_t(b) * kBlock;
+          write_terms<kFormat, kTerms>(v, args.x_image + int64_t(at >> 8) * col_bytes, cols, uint32_t(t * kTerms), at & 255u);
+        }
+        if (t == tokens - 1) {  // columns beyond the tokens' are zero
+          const uint32_t spare = cols - uint32_t(tokens * kTerms);
+          for (uint32_t i = threadIdx.x; i < spare * 8 * uint32_t(d_steps); i += kThreads) {
+            const uint32_t s = i / (spare * 8), row = uint32_t(tokens * kTerms) + i / 8 % spare, piece = i & 7;
+            uint8_t* image = args.x_image + int64_t(s) * col_bytes;
+            *reinterpret_cast<uint4*>(image + piece_at(row, piece)) = make_uint4(0u, 0u, 0u, 0u);
+            if (piece < B::kAtoms) *reinterpret_cast<uint32_t*>(image + cols * 128 + scale_at(row, piece * 4)) = 0u;
           }
         }
+        for (int s = 16; s; s >>= 1) square += __shfl_xor_sync(kFull, square, s);
+        if (lane == 0) sm.norm[warp] = square;
+        __syncthreads();
         if (threadIdx.x == 0) {
-          args.x_scale[t] = scale;
-          args.h_max[t] = 0;
+          float total = 0.f;
+          for (int w = 0; w < kWarps; ++w) total += sm.norm[w];
+          args.x_exp[t] = e;
+          args.x_norm[t] = 0.5f * log2f(total) - float(e);  // log2 of x's 2-norm
         }
         __syncthreads();
       }
     }
+    for (int e = threadIdx.x; e < experts; e += kThreads) sm.mask[e] = 0;
   }
-  if (!grid_barrier(args.counters, args, &s_flag)) return;
+  fence_proxy_async_all();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  bool ok = grid_barrier(args.counters, args, &sm.flag);
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = sm.tmem;
 
   // ---- selection, the same in every CTA
-  for (int e = threadIdx.x; e < experts; e += kThreads) s_mask[e] = 0;
-  if (warp < tokens) {
+  if (ok && warp < tokens) {
     const float* l = args.logits + warp * experts;
     if (experts <= 64)
-      select_top<2>(l, experts, top, args.renormalize, lane, s_ids[warp], s_weight[warp]);
+      select_top<2>(l, experts, top, args.renormalize, lane, sm.ids[warp], sm.weight[warp]);
     else if (experts <= 256)
-      select_top<8>(l, experts, top, args.renormalize, lane, s_ids[warp], s_weight[warp]);
+      select_top<8>(l, experts, top, args.renormalize, lane, sm.ids[warp], sm.weight[warp]);
     else
-      select_top<32>(l, experts, top, args.renormalize, lane, s_ids[warp], s_weight[warp]);
+      select_top_any(l, experts, top, args.renormalize, lane, sm.ids[warp], sm.weight[warp]);
     __syncwarp();
-    if (blockIdx.x == 0 && lane < top) {
-      if (args.ids) args.ids[warp * top + lane] = s_ids[warp][lane];
-      if (args.p) args.p[warp * top + lane] = s_weight[warp][lane];
+    // |h| <= p |gate row| |up row| |x|^2: the power of two that keeps h under 6 times the largest scale.
+    float bound = -INFINITY;
+    if (lane < top)
+      bound = log2f(sm.weight[warp][lane]) + log2f(__uint_as_float(__ldg(args.bound + sm.ids[warp][lane])));
+    for (int s = 16; s; s >>= 1) bound = fmaxf(bound, __shfl_xor_sync(kFull, bound, s));
+    if (lane == 0) {
+      const float e = floorf(11.3f - bound - 2.f * __ldcg(args.x_norm + warp));
+      sm.h_exp[warp] = e >= -126.f && e <= 126.f ? int(e) : e > 126.f ? 126 : e < -126.f ? -126 : 0;
+      sm.x_exp[warp] = __ldcg(args.x_exp + warp);
+    }
+    if (cta == 0 && lane < top) {
+      if (args.ids) args.ids[warp * top + lane] = sm.ids[warp][lane];
+      if (args.p) args.p[warp * top + lane] = sm.weight[warp][lane];
     }
   }
   __syncthreads();
-  if (warp == 0) {
+  if (ok && warp == 0) {
     // Masks token by token (a token's experts differ), then the experts in use in order.
     for (int t = 0; t < tokens; ++t) {
-      if (lane < top) s_mask[s_ids[t][lane]] |= uint16_t(1u << t);
+      if (lane < top) sm.mask[sm.ids[t][lane]] |= uint16_t(1u << t);
       __syncwarp();
     }
     int count = 0;
     for (int e0 = 0; e0 < experts; e0 += 32) {
       const int e = e0 + lane;
-      const bool in = e < experts && s_mask[e] != 0;
+      const bool in = e < experts && sm.mask[e] != 0;
       const uint32_t vote = __ballot_sync(kFull, in);
-      if (in) s_active[count + __popc(vote & ((1u << lane) - 1u))] = uint16_t(e);
+      if (in) sm.active[count + __popc(vote & ((1u << lane) - 1u))] = uint16_t(e);
       count += __popc(vote);
     }
-    if (lane == 0) s_count = count;
+    if (lane == 0) sm.count = count;
   }
   __syncthreads();
-  const int used = s_count;
+  const int used = ok ? sm.count : 0;
   for (int i = threadIdx.x; i < used * tokens; i += kThreads) {
-    const int a = i / tokens, t = i - a * tokens, e = s_active[a];
+    const int a = i / tokens, t = i - a * tokens, e = sm.active[a];
+    const uint32_t m = sm.mask[e];
     int slot = 255;
-    if (s_mask[e] >> t & 1)
+    if (m >> t & 1) {
       for (int j = 0; j < top; ++j)
-        if (s_ids[t][j] == e) slot = j;
-    s_slot[a][t] = uint8_t(slot);
+        if (sm.ids[t][j] == e) slot = j;
+      sm.nth[a][__popc(m & ((1u << t) - 1u))] = uint8_t(t);
+    }
+    sm.slot[a][t] = uint8_t(slot);
   }
   __syncthreads();
 
-  // ---- gate and up
-  {
-    const int team = warp / kTeamWarps, member = warp % kTeamWarps, tid = threadIdx.x % (32 * kTeamWarps);
-    const int tiles = (f + 7) / 8, total = used * tiles, stride = int(gridDim.x) * kTeams;
-    const int rounds = (d_chunks + kTeamWarps - 1) / kTeamWarps;  // chunks of a warp and tile
-    float* red = s_red + team * (kTeamWarps * kGroupsX * 128);
-    const uint4* frags = static_cast<const uint4*>(args.x_frag);
-    const float factor = args.gate_up_factor ? __ldg(args.gate_up_factor) : 1.f;
-    ChunkRegs<kFormat> ring[kRing];
-    // Neighbouring teams take neighbouring CTAs' tiles, so that a last, partial
-    // round spreads over the SMs.
-    int load_unit = team * int(gridDim.x) + int(blockIdx.x), load_i = 0, unit = load_unit, i = 0;
-    const uint8_t* load_base = nullptr;
-    auto locate = [&]() {
-      if (load_unit < total) {
-        const int a = load_unit / tiles;
-        load_base = args.gate_up + (int64_t(s_active[a]) * tiles + (load_unit - a * tiles)) * d_chunks * Chunk<kFormat>::kBytes;
-      }
-    };
-    auto load_next = [&](ChunkRegs<kFormat>& r) {
-      const int c = load_i * kTeamWarps + member;
-      if (load_unit < total && c < d_chunks) r.load(load_base + int64_t(c) * Chunk<kFormat>::kBytes, lane);
-      if (++load_i == rounds) {
-        load_i = 0;
-        load_unit += stride;
-        locate();
-      }
-    };
-    locate();
-#pragma unroll
-    for (int s = 0; s < kRing; ++s) load_next(ring[s]);
-    float acc[kGroupsX][4] = {};
-    int a = unit < total ? unit / tiles : 0;
-    auto groups_of = [&](int active) {
-      uint32_t m = 0;
-      if (unit < total) {
-        const uint32_t t = s_mask[s_active[active]];
-#pragma unroll
-        for (int q = 0; q < kGroupsX; ++q)
-          if (t >> (q * Columns<kSplitX>::kTokens) & ((1u << Columns<kSplitX>::kTokens) - 1u)) m |= 1u << q;
-      }
-      return m;
-    };
-    uint32_t mask = groups_of(a);
-    while (unit < total) {
-#pragma unroll
-      for (int s = 0; s < kRing; ++s) {
-        if (unit < total) {
-          const int c = i * kTeamWarps + member;
-          if (c < d_chunks)
-            chunk_mma<kFormat, kGroupsX>(ring[s], mask, acc,
-                                         [&](int q, int p) { return frags[(int64_t(q) * d_chunks + c) * 128 + p * 32 + lane]; });
-          load_next(ring[s]);
-          if (++i == rounds) {
-            publish<kGroupsX>(red, acc, member, lane);
-            dev::named_barrier(1 + team, 32 * kTeamWarps);
-            const int t = tid >> 3, r = tid & 7, slot = t < tokens ? s_slot[a][t] : 255;
-            if (slot != 255) {
-              const float u = factor / args.x_scale[t];
-              const float gate = reduce<kSplitX, kGroupsX>(red, kTeamWarps, r, t) * u;
-              const float up = reduce<kSplitX, kGroupsX>(red, kTeamWarps, r + 8, t) * u;
-              const float h = gate / (1.f + expf(-gate)) * up * s_weight[t][slot];
-              args.h[int64_t(t * top + slot) * f_chunks * 128 + (unit - a * tiles) * 8 + r] = h;
-              atomicMax(args.h_max + t, __float_as_uint(h) & 0x7fffffffu);
-            }
-            dev::named_barrier(1 + team, 32 * kTeamWarps);
-#pragma unroll
-            for (int q = 0; q < kGroupsX; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
-            i = 0;
-            unit += stride;
-            a = unit < total ? unit / tiles : 0;
-            mask = groups_of(a);
-          }
-        }
-      }
-    }
-  }
-  if (!grid_barrier(args.counters + 1, args, &s_flag)) return;
+  // ---- phases 2 and 3
+  const int f_tiles = (f + 63) / 64, d_tiles = (d + 127) / 128;
+  const Runs up(used * f_tiles, d_steps, ctas), down(used > 0 ? d_tiles : 0, max(used * f_steps, 1), ctas);
+  const int up_begin = up.start(cta), up_end = up.start(cta + 1);
+  const int down_begin = down.start(cta), down_end = down.start(cta + 1);
+  At put, got;             // of the producer and of the MMA thread
+  uint32_t runs_done = 0;  // accumulators handed over so far (MMA thread and epilogue)
 
-  // ---- down
-  {
-    const int tiles = (d + 15) / 16, f8 = (f + 7) / 8 * 8, list = used * f_chunks, ctas = int(gridDim.x);
-    // Parts of a tile: the fewest that keep the CTAs within a few percent of the
-    // best balance, with two chunks a warp at least.
-    int parts = 1;
-    {
-      float best = float((tiles + ctas - 1) / ctas);
-      for (int p = 2; p <= kMaxParts && list / p >= 2 * kWarps && tiles <= args.tile_counter_count; ++p) {
-        const float cost = float((tiles * p + ctas - 1) / ctas) / float(p);
-        if (cost < 0.95f * best) best = cost, parts = p;
-      }
+  auto fail = [&]() {
+    if (!sm.abort) {
+      sm.abort = 1;
+      dev::record_status(args.status, kStatusTimeout, kWaitTileStage);
     }
-    const int total = tiles * parts, per = (list + parts - 1) / parts;
+  };
+  // One stage: `weights` unless null, `columns` unless null; both together or weights first.
+  auto produce_weights = [&](const uint8_t* weights) {
+    if (put.lap > 0 && !dev::mbar_wait_abortable(&sm.empty[put.slot], (put.lap - 1) & 1u, limit, &sm.abort)) fail();
+    if (sm.abort) return false;
+    dev::mbar_arrive_expect_tx(&sm.full[put.slot], stage_bytes);
+    dev::bulk_load(area + put.slot * stage_bytes, weights, B::kBytes, &sm.full[put.slot]);
+    return true;
+  };
+  auto produce_columns = [&](const uint8_t* columns, uint32_t slot) {
+    dev::bulk_load(area + slot * stage_bytes + B::kBytes, columns, col_bytes, &sm.full[slot]);
+  };
+  auto multiply = [&](const Runs& runs, int begin, int end) {
+    for (int at = begin; at < end;) {
+      const int stop = min(end, at - at % runs.steps + runs.steps);
+      const uint32_t b = runs_done & 1u, nb = runs_done >> 1;
+      if (nb > 0 && !dev::mbar_wait_abortable(&sm.acc_empty[b], (nb - 1) & 1u, limit, &sm.abort)) fail();
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      for (int i = at; i < stop; ++i) {
+        if (!dev::mbar_wait_abortable(&sm.full[got.slot], got.lap & 1u, limit, &sm.abort)) fail();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (!sm.abort) {
+          const uint32_t base = dev::smem_addr(area + got.slot * stage_bytes);
+          const uint32_t sr = tmem + 256 + got.slot * (8 * B::kAtoms), sc = sr + 4 * B::kAtoms;
+          const uint64_t drs = scale_desc(base + 16384), dcs = scale_desc(base + B::kBytes + cols * 128);
+#pragma unroll
+          for (int a = 0; a < B::kAtoms; ++a) {
+            copy_scales<1>(sr + 4 * a, drs + 32 * a);
+            copy_scales<1>(sc + 4 * a, dcs + 32 * a);
+          }
+          const uint64_t dr = operand_desc(base), dc = operand_desc(base + B::kBytes);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            constexpr int kPer = 4 / B::kAtoms;  // MMAs that share an atom
+            const int a = j / kPer;
+            mma<kFormat, 1>(tmem + b * 128, dr + 2 * j, dc + 2 * j,
+                            instr_desc<kFormat>(128, cols, kPer == 2 ? (j & 1) * 2 : 0), sr + 4 * a, sc + 4 * a,
+                            (i != at || j != 0) ? 1u : 0u);
+          }
+        }
+        commit<1>(&sm.empty[got.slot]);
+        got.next(stages);
+      }
+      commit<1>(&sm.acc_full[b]);
+      ++runs_done;
+      at = stop;
+    }
+  };
+  // The epilogue of one phase.  value(k, v) takes the finished sum of the unit's k-th token (of `count(unit)`).
+  const int q = warp & 3, row_local = 32 * q + lane, etid = threadIdx.x - 64;
+  auto join = [&](const Runs& runs, int begin, int end, int32_t* counters, auto count, auto token, auto value,
+                  auto done) {
+    const int first_unit = begin / runs.steps;
+    for (int at = begin; at < end;) {
+      const int unit = at / runs.steps, unit_at = unit * runs.steps, stop = min(end, unit_at + runs.steps);
+      const uint32_t b = runs_done & 1u, nb = runs_done >> 1;
+      if (!dev::mbar_wait_abortable(&sm.acc_full[b], nb & 1u, limit, &sm.abort)) fail();
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      __syncwarp();
+      const uint32_t taddr = tmem + b * 128 + (uint32_t(32 * q) << 16);
+      const int n = count(unit);
+      const bool whole = stop - at == runs.steps;
+      // Shares: [cta][0: of its first unit, 1: of its last][token][row].
+      float* mine = args.partial + (int64_t(cta) * 2 + (unit == first_unit ? 0 : 1)) * (kMoeTokens * 128) + row_local;
+      for (int k = 0; k < n; ++k) {
+        const float v = read_terms<kTerms>(taddr + token(unit, k) * kTerms);
+        if (whole)
+          value(unit, k, v);
+        else
+          __stcg(mine + k * 128, v);
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&sm.acc_empty[b]);
+      ++runs_done;
+      bool finish = whole;
+      if (!whole) {
+        const int c_first = runs.owner(unit_at), c_last = runs.owner(unit_at + runs.steps - 1);
+        dev::named_barrier(1, 128);
+        if (etid == 0) {
+          __threadfence();
+          const bool last = atomicAdd(counters + c_first, 1) == c_last - c_first;
+          if (last) counters[c_first] = 0;
+          __threadfence();
+          sm.last = last;
+        }
+        dev::named_barrier(1, 128);
+        finish = sm.last != 0;
+        if (finish) {
+          for (int k = 0; k < n; ++k) {
+            float v = 0.f;
+            for (int c = c_first; c <= c_last; ++c)
+              v += __ldcg(args.partial + (int64_t(c) * 2 + (runs.start(c) / runs.steps == unit ? 0 : 1)) * (kMoeTokens * 128) +
+                          k * 128 + row_local);
+            value(unit, k, v);
+          }
+        }
+      }
+      if (finish) done(unit, n);
+      dev::named_barrier(1, 128);  // sm.last and sm.gate_up may be written again
+      at = stop;
+    }
+  };
+
+  // Phase 2, and phase 3's first weights.
+  int ahead = 0;
+  auto up_weights = [&](int at) {
+    const int unit = at / d_steps, a = unit / f_tiles;
+    return args.gate_up + ((int64_t(sm.active[a]) * f_tiles + (unit - a * f_tiles)) * d_steps + at % d_steps) * B::kBytes;
+  };
+  auto down_weights = [&](int at) {
+    const int tile = at / down.steps, i = at - tile * down.steps, a = i / f_steps;
+    return args.down + ((int64_t(sm.active[a]) * d_tiles + tile) * f_steps + (i - a * f_steps)) * B::kBytes;
+  };
+  auto down_columns = [&](int at) { return args.h_image + int64_t(at % down.steps) * col_bytes; };
+  if (warp == 0 && lane == 0) {
+    fence_proxy_async_all();
+    for (int at = up_begin; at < up_end; ++at) {
+      if (!produce_weights(up_weights(at))) break;
+      produce_columns(args.x_image + int64_t(at % d_steps) * col_bytes, put.slot);
+      put.next(stages);
+    }
+    for (int at = down_begin; at < down_end && ahead < int(stages); ++at, ++ahead) {
+      if (!produce_weights(down_weights(at))) break;
+      put.next(stages);
+    }
+  } else if (warp == 1 && lane == 0) {
+    multiply(up, up_begin, up_end);
+  } else if (warp >= 2 && warp < 6) {
+    const float factor = args.gate_up_factor ? __ldg(args.gate_up_factor) : 1.f;
+    join(
+        up, up_begin, up_end, args.counters + 64, [&](int unit) { return __popc(uint32_t(sm.mask[sm.active[unit / f_tiles]])); },
+        [&](int unit, int k) { return int(sm.nth[unit / f_tiles][k]); },
+        [&](int, int k, float v) { sm.gate_up[k][row_local] = v; },
+        [&](int unit, int n) {
+          dev::named_barrier(1, 128);
+          const int a = unit / f_tiles, tile = unit - a * f_tiles;
+          uint8_t* image = args.h_image + (int64_t(a) * f_steps + tile / 4) * col_bytes;
+          const uint32_t col = uint32_t(tile % 4) * 64, half = uint32_t(q & 1);
+          for (int k = q >> 1; k < n; k += 2) {
+            const int t = sm.nth[a][k];
+            const float u = factor * pow2f(-sm.x_exp[t]);
+            const float g = sm.gate_up[k][32 * half + lane] * u, up_value = sm.gate_up[k][64 + 32 * half + lane] * u;
+            const float h = g / (1.f + expf(-g)) * up_value * sm.weight[t][sm.slot[a][t]];
+            write_terms_warp<kFormat, kTerms>(h * pow2f(sm.h_exp[t]), image, cols, uint32_t(t * kTerms), col + 32 * half, lane);
+          }
+          // Zeros in the other columns, and beyond f up to the stage's end.
+          const uint32_t end = tile == f_tiles - 1 ? 256 : col + 64;
+          for (uint32_t row = uint32_t(etid); row < cols; row += 128) {
+            const int t = int(row) / kTerms;
+            const bool taken = t < tokens && sm.slot[a][t] != 255;
+            for (uint32_t c = taken ? col + 64 : col; c < end; c += 32) {
+              *reinterpret_cast<uint4*>(image + piece_at(row, c >> 5)) = make_uint4(0u, 0u, 0u, 0u);
+              for (uint32_t i = 0; i < 32 / kBlock; ++i) image[cols * 128 + scale_at(row, c / kBlock + i)] = 0;
+            }
+          }
+        });
+  }
+  __syncwarp();
+  fence_proxy_async_all();
+  if (ok && !grid_barrier(args.counters + 1, args, &sm.flag)) ok = false;
+  if (!ok) sm.abort = 1;
+
+  // Phase 3.
+  if (warp == 0 && lane == 0) {
+    fence_proxy_async_all();
+    // The columns of the stages whose weights are on their way: the last `ahead` slots.
+    uint32_t slot = (put.slot + stages - uint32_t(ahead)) % stages;
+    for (int i = 0; i < ahead; ++i) {
+      produce_columns(down_columns(down_begin + i), slot);
+      if (++slot == stages) slot = 0;
+    }
+    for (int at = down_begin + ahead; at < down_end; ++at) {
+      if (!produce_weights(down_weights(at))) break;
+      produce_columns(down_columns(at), put.slot);
+      put.next(stages);
+    }
+  } else if (warp == 1 && lane == 0) {
+    multiply(down, down_begin, down_end);
+    commit<1>(&sm.drain);
+    dev::mbar_wait(&sm.drain, 0u, limit);
+  } else if (warp >= 2 && warp < 6) {
     const float factor = args.down_factor ? __ldg(args.down_factor) : 1.f;
-    const int col = lane >> 2;
-    float scale[kGroupsH];
-    int token[kGroupsH];
-#pragma unroll
-    for (int q = 0; q < kGroupsH; ++q) {
-      token[q] = Columns<kSplitH>::token(q, col);
-      scale[q] = token[q] < tokens ? pow2_scale(__ldcg(args.h_max + token[q])) : 0.f;
-    }
-    ChunkRegs<kFormat> ring[kRing];
-    int load_unit = blockIdx.x, load_at = 0, load_end = 0, unit = blockIdx.x, at = 0, end = 0;
-    auto span = [&](int u, int& begin, int& stop) {
-      const int p = u % parts;
-      begin = min(p * per, list);
-      stop = min(begin + per, list);
-    };
-    auto load_next = [&](ChunkRegs<kFormat>& r) {
-      if (load_unit < total) {
-        const int l = load_at + warp;
-        if (l < load_end) {
-          const int e = l / f_chunks, c = l - e * f_chunks;
-          r.load(args.down + ((int64_t(s_active[e]) * tiles + load_unit / parts) * f_chunks + c) * Chunk<kFormat>::kBytes,
-                 lane);
-        }
-        load_at += kWarps;
-        if (load_at >= load_end) {
-          load_unit += ctas;
-          span(load_unit, load_at, load_end);
-        }
-      }
-    };
-    span(load_unit, load_at, load_end);
-    span(unit, at, end);
-#pragma unroll
-    for (int s = 0; s < kRing; ++s) load_next(ring[s]);
-    float acc[kGroupsH][4] = {};
-    while (unit < total) {
-#pragma unroll
-      for (int s = 0; s < kRing; ++s) {
-        if (unit < total) {
-          const int l = at + warp;
-          if (l < end) {
-            const int e = l / f_chunks, c = l - e * f_chunks;
-            const float* rows[kGroupsH];
-            uint32_t mask = 0;
-#pragma unroll
-            for (int q = 0; q < kGroupsH; ++q) {
-              const int slot = token[q] < tokens ? s_slot[e][token[q]] : 255;
-              rows[q] = slot != 255 ? args.h + int64_t(token[q] * top + slot) * f_chunks * 128 : nullptr;
-              if (__any_sync(kFull, slot != 255)) mask |= 1u << q;
-            }
-            chunk_mma<kFormat, kGroupsH>(ring[s], mask, acc, [&](int q, int p) {
-              uint2 b[2];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int k = c * 128 + (2 * p + j) * 16 + (lane & 3) * 4;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (rows[q] != nullptr && k < f8) v = *reinterpret_cast<const float4*>(rows[q] + k);
-                b[j] = to_frag<kSplitH>(v, scale[q], col);
-              }
-              return make_uint4(b[0].x, b[0].y, b[1].x, b[1].y);
-            });
-          }
-          load_next(ring[s]);
-          at += kWarps;
-          if (at >= end) {
-            const int tile = unit / parts, part = unit - tile * parts;
-            publish<kGroupsH>(s_red, acc, warp, lane);
-            __syncthreads();
-            const int t = threadIdx.x >> 4, r = threadIdx.x & 15, row = tile * 16 + r;
-            const bool mine = t < tokens;  // threads beyond 16 tokens: none
-            float y = 0.f;
-            if (mine) y = reduce<kSplitH, kGroupsH>(s_red, kWarps, r, t);
-            bool store = true;
-            if (parts > 1) {
-              float* share = args.partial + int64_t(tile) * parts * (16 * kMoeTokens);
-              if (mine) __stcg(share + part * (16 * kMoeTokens) + t * 16 + r, y);
-              __syncthreads();
-              if (threadIdx.x == 0) {
-                __threadfence();
-                s_flag = atomicAdd(args.tile_counters + tile, 1) == parts - 1;
-                __threadfence();
-              }
-              __syncthreads();
-              store = s_flag != 0;
-              if (store) {
-                if (mine) {
-                  y = 0.f;
-                  for (int p = 0; p < parts; ++p) y += __ldcg(share + p * (16 * kMoeTokens) + t * 16 + r);
-                }
-                if (threadIdx.x == 0) args.tile_counters[tile] = 0;
-              }
-            }
-            if (store && mine && row < d)
-              static_cast<T*>(args.y)[t * args.ldy + row] =
-                  from_f32<T>(y * (factor / pow2_scale(__ldcg(args.h_max + t))));
-            __syncthreads();
-#pragma unroll
-            for (int q = 0; q < kGroupsH; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
-            unit += ctas;
-            span(unit, at, end);
-          }
-        }
-      }
-    }
+    join(
+        down, down_begin, down_end, args.counters + 1088, [&](int) { return tokens; }, [&](int, int k) { return k; },
+        [&](int unit, int k, float v) {
+          const int row = unit * 128 + row_local;
+          if (row < d) static_cast<T*>(args.y)[k * args.ldy + row] = from_f32<T>(v * factor * pow2f(-sm.h_exp[k]));
+        },
+        [&](int, int) {});
+  }
+  __syncwarp();
+  if (sm.abort && threadIdx.x == 0) {
+    // Copies still under way get a bounded time to land before the CTA's memory goes.
+    const uint64_t t0 = dev::global_timer_ns();
+    while (dev::global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
   // The last CTA to leave clears the barriers' counters for the next call.
-  if (threadIdx.x == 0 && atomicAdd(args.counters + 2, 1) == int(gridDim.x) - 1) {
+  if (threadIdx.x == 0 && atomicAdd(args.counters + 2, 1) == ctas - 1) {
     args.counters[0] = 0;
     args.counters[1] = 0;
     args.counters[2] = 0;
   }
 }
 
-template <typename T, int kFormat, bool kSplitX, int kGroupsX, bool kSplitH, int kGroupsH>
+template <typename T, int kFormat>
 cudaError_t launch_t(const MoeArgs& args, int sms, cudaStream_t stream) {
+  const void* kernel = reinterpret_cast<const void*>(&moe_kernel<T, kFormat>);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
   MoeArgs copy = args;
   void* params[] = {&copy};
-  return cudaLaunchCooperativeKernel(
-      reinterpret_cast<const void*>(&moe_kernel<T, kFormat, kSplitX, kGroupsX, kSplitH, kGroupsH>), dim3(unsigned(sms)),
-      dim3(kThreads), params, 0, stream);
-}
-
-// Columns of eight that the tokens take, for x and for h: a 32-bit x and its h
-// are split in two; h beside a 16-bit float x too, since one rounding to its 11
-// bits would show in the result; bfloat16 has 8.
-template <int kFormat>
-cudaError_t launch_format(int dtype, const MoeArgs& args, int sms, cudaStream_t stream) {
-  const int t = args.tokens;
-  switch (dtype) {
-    case FP4_F32:
-      if (t <= 4) return launch_t<float, kFormat, true, 1, true, 1>(args, sms, stream);
-      if (t <= 8) return launch_t<float, kFormat, true, 2, true, 2>(args, sms, stream);
-      return launch_t<float, kFormat, true, 4, true, 4>(args, sms, stream);
-    case FP4_BF16:
-      if (t <= 8) return launch_t<__nv_bfloat16, kFormat, false, 1, false, 1>(args, sms, stream);
-      return launch_t<__nv_bfloat16, kFormat, false, 2, false, 2>(args, sms, stream);
-    default:
-      if (t <= 4) return launch_t<__half, kFormat, false, 1, true, 1>(args, sms, stream);
-      if (t <= 8) return launch_t<__half, kFormat, false, 1, true, 2>(args, sms, stream);
-      return launch_t<__half, kFormat, false, 2, true, 4>(args, sms, stream);
-  }
+  return cudaLaunchCooperativeKernel(kernel, dim3(unsigned(sms)), dim3(kThreads), params, kSmemBytes, stream);
 }
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
-}  // namespace
+int64_t block_bytes(int format) { return format == FP4_MXFP4 ? Block<FP4_MXFP4>::kBytes : Block<FP4_NVFP4>::kBytes; }
 
-int64_t fp4_expert_chunk_bytes(int format) {
-  return format == FP4_MXFP4 ? Chunk<FP4_MXFP4>::kBytes : Chunk<FP4_NVFP4>::kBytes;
+int64_t gate_up_blocks(int64_t experts, int64_t d, int64_t f) { return experts * ((f + 63) / 64) * ((d + 255) / 256); }
+int64_t down_blocks(int64_t experts, int64_t d, int64_t f) { return experts * ((d + 127) / 128) * ((f + 255) / 256); }
+
+int terms_of(int dtype) {
+  return dtype == FP4_F32 ? Terms<float>::kCount : dtype == FP4_BF16 ? Terms<__nv_bfloat16>::kCount : Terms<__half>::kCount;
 }
 
-MoeScratch fp4_moe_scratch(int dtype, int64_t tokens, int64_t experts, int64_t d, int64_t f, int64_t top) {
+}  // namespace
+
+int64_t fp4_gate_up_bytes(int format, int64_t experts, int64_t d, int64_t f) {
+  return gate_up_blocks(experts, d, f) * block_bytes(format) + (experts + 3) / 4 * 16;
+}
+int64_t fp4_down_bytes(int format, int64_t experts, int64_t d, int64_t f) {
+  return down_blocks(experts, d, f) * block_bytes(format);
+}
+const uint32_t* fp4_expert_bounds(const fp4_experts_t& w) {
+  return reinterpret_cast<const uint32_t*>(w.gate_up + gate_up_blocks(w.experts, w.d, w.f) * block_bytes(w.format));
+}
+
+MoeScratch fp4_moe_scratch(int dtype, int format, int64_t tokens, int64_t experts, int64_t d, int64_t f, int64_t top,
+                           int sms) {
   MoeScratch s{};
   size_t at = 0;
-  auto take = [&](size_t bytes) {
+  auto take = [&](int64_t bytes) {
     const size_t here = at;
-    at += round_up(bytes);
+    at += round_up(size_t(bytes));
     return here;
   };
-  const int64_t per = dtype == FP4_F32 ? 4 : 8;
+  const int64_t used = experts < tokens * top ? experts : tokens * top;
+  s.cols = int((tokens * terms_of(dtype) + 15) / 16 * 16);
+  const int64_t col_bytes = s.cols * 128 + block_bytes(format) - 16384;
   s.logits = take(tokens * experts * 4);
-  s.x_scale = take(tokens * 4);
-  s.h_max = take(tokens * 4);
-  s.x_frag = take((tokens + per - 1) / per * ((d + 127) / 128) * 8 * 32 * 8);
-  s.h = take(tokens * top * ((f + 127) / 128) * 128 * 4);
-  s.partial = take(((d + 15) / 16) * kMaxParts * 16 * kMoeTokens * 4);
+  s.x_exp = take(tokens * 4);
+  s.x_norm = take(tokens * 4);
+  s.x_image = take((d + 255) / 256 * col_bytes);
+  s.h_image = take(used * ((f + 255) / 256) * col_bytes);
+  s.partial = take(int64_t(sms) * 2 * kMoeTokens * 128 * 4);
   s.bytes = at;
   return s;
 }
@@ -739,21 +906,34 @@ cudaError_t launch_fp4_experts_pack(const fp4_matrix_t& gate_up, const fp4_matri
     const int64_t b = (items + kPackThreads - 1) / kPackThreads;
     return unsigned(b < (1 << 20) ? b : (1 << 20));
   };
-  const int64_t up_items = w.experts * ((w.f + 7) / 8) * ((w.d + 127) / 128) * 64;
-  const int64_t down_items = w.experts * ((w.d + 15) / 16) * ((w.f + 127) / 128) * 64;
+  uint32_t* bound = const_cast<uint32_t*>(fp4_expert_bounds(w));
+  const cudaError_t e = cudaMemsetAsync(bound, 0, size_t(w.experts) * 4, stream);
+  if (e != cudaSuccess) return e;
+  const unsigned up = grid(gate_up_blocks(w.experts, w.d, w.f) * 1024), dn = grid(down_blocks(w.experts, w.d, w.f) * 1024);
+  const unsigned bd = grid(w.experts * w.f * 32);
   if (w.format == FP4_MXFP4) {
-    pack_experts_kernel<FP4_MXFP4, true><<<grid(up_items), kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, w.gate_up);
-    pack_experts_kernel<FP4_MXFP4, false><<<grid(down_items), kPackThreads, 0, stream>>>(down, w.experts, w.d, w.down);
+    pack_experts_kernel<FP4_MXFP4, true><<<up, kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, w.gate_up);
+    pack_experts_kernel<FP4_MXFP4, false><<<dn, kPackThreads, 0, stream>>>(down, w.experts, w.d, w.down);
+    bound_kernel<FP4_MXFP4><<<bd, kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, bound);
   } else {
-    pack_experts_kernel<FP4_NVFP4, true><<<grid(up_items), kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, w.gate_up);
-    pack_experts_kernel<FP4_NVFP4, false><<<grid(down_items), kPackThreads, 0, stream>>>(down, w.experts, w.d, w.down);
+    pack_experts_kernel<FP4_NVFP4, true><<<up, kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, w.gate_up);
+    pack_experts_kernel<FP4_NVFP4, false><<<dn, kPackThreads, 0, stream>>>(down, w.experts, w.d, w.down);
+    bound_kernel<FP4_NVFP4><<<bd, kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, bound);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_fp4_moe(int dtype, int format, const MoeArgs& args, int sms, cudaStream_t stream) {
-  return format == FP4_MXFP4 ? launch_format<FP4_MXFP4>(dtype, args, sms, stream)
-                             : launch_format<FP4_NVFP4>(dtype, args, sms, stream);
+  const bool mx = format == FP4_MXFP4;
+  switch (dtype) {
+    case FP4_F32:
+      return mx ? launch_t<float, FP4_MXFP4>(args, sms, stream) : launch_t<float, FP4_NVFP4>(args, sms, stream);
+    case FP4_BF16:
+      return mx ? launch_t<__nv_bfloat16, FP4_MXFP4>(args, sms, stream)
+                : launch_t<__nv_bfloat16, FP4_NVFP4>(args, sms, stream);
+    default:
+      return mx ? launch_t<__half, FP4_MXFP4>(args, sms, stream) : launch_t<__half, FP4_NVFP4>(args, sms, stream);
+  }
 }
 
 }  // namespace gb300

@@ -94,7 +94,7 @@ def test_more_experts_than_the_layer_takes(lib):
     assert lib.fp4_experts_layout(0, 1025, 64, 64, None, None) == binding.ERR_UNSUPPORTED
     up, down = ctypes.c_int64(), ctypes.c_int64()
     assert lib.fp4_experts_layout(1, 3, 130, 20, ctypes.byref(up), ctypes.byref(down)) == binding.OK
-    assert (up.value, down.value) == (3 * 3 * 2 * 1152, 3 * 9 * 1 * 1152)
+    assert (up.value, down.value) == (3 * 1 * 1 * 18432 + 16, 3 * 2 * 1 * 18432)
 
 
 def test_host_tensors_are_refused():

@@ -387,7 +387,7 @@ sgemm_status_t fp4_moe(int dtype, const void* x, int64_t ldx, int64_t M, const f
   a.x_norm = reinterpret_cast<float*>(base + s.x_norm);
   a.x_image = base + s.x_image;
   a.h_image = base + s.h_image;
-  a.partial = reinterpret_cast<float*>(base + s.partial);
+  a.share = reinterpret_cast<uint64_t*>(base + s.share);
   a.bound = gb300::fp4_expert_bounds(*w);
   a.cols = s.cols;
   a.counters = static_cast<int32_t*>(ws);

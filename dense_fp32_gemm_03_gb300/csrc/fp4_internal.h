@@ -78,13 +78,13 @@ struct MoeArgs {
   float* x_norm;      // tokens: log2 of x's 2-norm
   uint8_t* x_image;   // x as terms: a block of columns for each 256 of d
   uint8_t* h_image;   // h as terms: the same for each expert in use and 256 of f
-  float* partial;     // shares of units cut between CTAs: CTA x 2 x token x row
+  uint64_t* share;    // shares of units cut between CTAs: CTA x phase (2, 3) x token x row
   int32_t* counters;  // the workspace's counters, zero on entry and on exit
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
 struct MoeScratch {
-  size_t logits, x_exp, x_norm, x_image, h_image, partial, bytes;  // offsets, and the size of all
+  size_t logits, x_exp, x_norm, x_image, h_image, share, bytes;  // offsets, and the size of all
   int cols;
 };
 MoeScratch fp4_moe_scratch(int dtype, int format, int64_t tokens, int64_t experts, int64_t d, int64_t f, int64_t top,

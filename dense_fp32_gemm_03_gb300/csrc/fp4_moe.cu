@@ -184,7 +184,7 @@ __device__ __forceinline__ void write_terms(float (&v)[Format<kFormat>::kBlock],
     for (int i = 0; i < kBlock; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
     float unit;
     const uint32_t byte = term_scale<kFormat>(top, unit);
-    const float inv = unit > 0.f ? __frcp_rn(unit) : 0.f;
+    const float inv = unit > 0.f ? __fdividef(1.f, unit) : 0.f;
     uint32_t w[kBlock / 8];
 #pragma unroll
     for (int i = 0; i < kBlock / 8; ++i) {
@@ -217,7 +217,7 @@ __device__ __forceinline__ void write_terms_warp(float r, uint8_t* image, uint32
     }
     float unit;
     const uint32_t byte = term_scale<kFormat>(top, unit);
-    uint32_t w = term_code(r, unit, unit > 0.f ? __frcp_rn(unit) : 0.f);
+    uint32_t w = term_code(r, unit, unit > 0.f ? __fdividef(1.f, unit) : 0.f);
     w |= __shfl_xor_sync(kFull, w, 1) << 4;
     w |= __shfl_xor_sync(kFull, w, 2) << 8;
     w |= __shfl_xor_sync(kFull, w, 4) << 16;
@@ -266,16 +266,17 @@ __device__ __forceinline__ void select_top(const float* logits, int experts, int
     for (int i = kPerLane - 1; i >= 0; --i)
       if (key[i] == peak_key) at = lane + 32 * i;
     const int id = int(__reduce_min_sync(kFull, unsigned(at)));
-    float p = 0.f;
+    float logit = 0.f;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i)
       if (lane + 32 * i == id) {
         key[i] = 0;
-        p = expf(v[i] - peak) / sum;
+        logit = v[i];
       }
-    p = __shfl_sync(kFull, p, id & 31);
-    if (lane == j) mine = p, mine_id = id;
+    logit = __shfl_sync(kFull, logit, id & 31);
+    if (lane == j) mine = logit, mine_id = id;
   }
+  mine = lane < top ? expf(mine - peak) / sum : 0.f;
   if (renorm) {
     float total = mine;
     for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(kFull, total, s);
@@ -343,14 +344,31 @@ __device__ __forceinline__ float4 load4(const T* p, int k, int n, bool vector) {
   return v;
 }
 
+// Four consecutive values as they are stored.
+template <typename T>
+struct Four {
+  uint2 raw;
+  __device__ __forceinline__ void load(const T* p) { raw = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ float4 value() const {
+    const T* t = reinterpret_cast<const T*>(&raw);
+    return make_float4(to_f32(t[0]), to_f32(t[1]), to_f32(t[2]), to_f32(t[3]));
+  }
+};
+template <>
+struct Four<float> {
+  float4 raw;
+  __device__ __forceinline__ void load(const float* p) { raw = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ float4 value() const { return raw; }
+};
+
 // ------------------------------------------------------------- grid barrier
 // All CTAs are resident (cooperative launch).  Every thread returns the same
 // answer: false once the bounded wait ran out.
 __device__ __forceinline__ bool grid_barrier(int32_t* counter, const MoeArgs& args, int* s_ok) {
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(counter, 1);
+    // The release covers the CTA's writes, which the barrier above ordered before it.
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter) : "memory");
     int ok = 1;
     const uint64_t t0 = dev::global_timer_ns();
     while (dev::ld_acquire_gpu(counter) < int(gridDim.x)) {
@@ -360,7 +378,6 @@ __device__ __forceinline__ bool grid_barrier(int32_t* counter, const MoeArgs& ar
         break;
       }
     }
-    __threadfence();
     *s_ok = ok;
   }
   __syncthreads();
@@ -368,17 +385,19 @@ __device__ __forceinline__ bool grid_barrier(int32_t* counter, const MoeArgs& ar
 }
 
 // -------------------------------------------------------------------- layer
-// A phase's work: `units` sums of `steps` stages each, cut into equal runs of
-// stages, one to a CTA.  A unit that ends in another CTA's run than it began is
-// joined by the last of its CTAs to finish, in their order.
+// A phase's work: `units` sums of `steps` stages each, cut into runs of nearly
+// equal length, one to a CTA, of kLeast stages at least where there are few.  A
+// unit that is cut between CTAs is finished by the first of them.
+constexpr int kLeast = 4;
 struct Runs {
-  int steps, base, extra;
+  int steps, count, base, extra;
   __device__ __forceinline__ Runs(int units, int steps_, int ctas) : steps(steps_) {
-    const int total = units * steps;
-    base = total / ctas;
-    extra = total - base * ctas;
+    const int total = units * steps, runs = min(ctas, max(total / kLeast, 1));
+    base = total / runs;
+    extra = total - base * runs;
+    count = runs;
   }
-  __device__ __forceinline__ int start(int cta) const { return cta * base + min(cta, extra); }
+  __device__ __forceinline__ int start(int cta) const { return min(cta, count) * base + min(min(cta, count), extra); }
   __device__ __forceinline__ int owner(int at) const {
     const int big = extra * (base + 1);
     return at < big ? at / (base + 1) : extra + (at - big) / base;
@@ -393,12 +412,14 @@ struct Smem {
   int x_exp[kMoeTokens], h_exp[kMoeTokens];  // x and h are multiplied by these powers of two
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   uint16_t ids[kMoeTokens][kMaxTop];
-  uint16_t mask[kMaxExperts];           // tokens that go to an expert
+  alignas(16) uint8_t slot[kMaxPairs][kMoeTokens];  // place of an expert in use among a token's, or 255
+  uint8_t nth[kMaxPairs][kMoeTokens];               // the tokens of an expert in use
+  uint32_t mask[kMaxExperts];           // tokens that go to an expert
+  float bound[kMaxExperts];             // log2 of MoeArgs::bound
+  uint16_t index[kMaxExperts];          // place of an expert among those in use
   uint16_t active[kMaxPairs];           // experts in use, in order
-  uint8_t slot[kMaxPairs][kMoeTokens];  // place of an expert in use among a token's, or 255
-  uint8_t nth[kMaxPairs][kMoeTokens];   // the tokens of an expert in use
   uint32_t tmem, top;
-  int count, flag, last;
+  int count, flag;
   volatile int abort;
 };
 constexpr int kStageArea = kSmemBytes - 1024 - int((sizeof(Smem) + 127) / 128 * 128);
@@ -431,6 +452,16 @@ __device__ __forceinline__ float read_terms(uint32_t taddr) {
 #pragma unroll
   for (int j = kTerms - 2; j >= 0; --j) sum = fmaf(sum, 0.25f, v[j]);
   return sum;
+}
+
+// A share's value and the mark that it is there, in one 64-bit word: no flag, no fence.
+__device__ __forceinline__ void put_share(uint64_t* p, float v) {
+  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(uint64_t(1) << 32 | __float_as_uint(v)) : "memory");
+}
+__device__ __forceinline__ uint64_t peek_share(const uint64_t* p) {
+  uint64_t w;
+  asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w) : "l"(p) : "memory");
+  return w;
 }
 
 // Three phases with a grid barrier between them.
@@ -479,6 +510,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
 
   // ---- phase 1
   {
+    for (int e = threadIdx.x; e < experts; e += kThreads) {
+      sm.mask[e] = 0;
+      sm.bound[e] = log2f(__uint_as_float(__ldg(args.bound + e)));
+    }
+    for (int i = threadIdx.x; i < kMaxPairs; i += kThreads)
+      *reinterpret_cast<uint4*>(sm.slot[i]) = make_uint4(~0u, ~0u, ~0u, ~0u);
+    // This CTA's shares, in both phases, are not there yet.
+    for (int i = threadIdx.x; i < 2 * tokens * 64; i += kThreads)
+      *reinterpret_cast<uint4*>(args.share + (int64_t(cta) * 2 + i / (tokens * 64)) * (kMoeTokens * 128) +
+                                i % (tokens * 64) * 2) = make_uint4(0u, 0u, 0u, 0u);
     const T* x = static_cast<const T*>(args.x);
     const bool vec_x = (reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T))) == 0 && args.ldx % 4 == 0;
     const bool vec_r = (reinterpret_cast<uintptr_t>(args.router) & 15u) == 0 && args.ldr % 4 == 0;
@@ -490,10 +531,30 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
         const int t = warp / share, part = warp % share;
         if (t < tokens) {
           const T* xt = x + t * args.ldx;
-#pragma unroll 4
-          for (int k = (part * 32 + lane) * 4; k < d; k += share * 128) {
-            const float4 a = load4(xt, k, d, vec_x), b = load4(r, k, d, vec_r);
-            sum = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, sum))));
+          const int step = share * 128;
+          int k = (part * 32 + lane) * 4;
+          if (vec_x && vec_r && d % 4 == 0) {
+            // Eight pieces of both rows under way at a time.
+            for (; k < d; k += 8 * step) {
+              Four<T> a[8];
+              float4 b[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const bool in = k + j * step < d;
+                a[j].load(xt + (in ? k + j * step : 0));
+                b[j] = in ? __ldg(reinterpret_cast<const float4*>(r + k + j * step)) : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float4 v = k + j * step < d ? a[j].value() : make_float4(0.f, 0.f, 0.f, 0.f);
+                sum = fmaf(v.x, b[j].x, fmaf(v.y, b[j].y, fmaf(v.z, b[j].z, fmaf(v.w, b[j].w, sum))));
+              }
+            }
+          } else {
+            for (; k < d; k += step) {
+              const float4 a = load4(xt, k, d, vec_x), b = load4(r, k, d, vec_r);
+              sum = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, sum))));
+            }
           }
           for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
           if (lane == 0) sm.red[warp] = sum;
@@ -511,26 +572,30 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
         if (threadIdx.x == 0) sm.top = 0;
         __syncthreads();
         uint32_t most = 0;
+        float square = 0.f;
         for (int k = threadIdx.x * 4; k < d; k += kThreads * 4) {
           const float4 v = load4(xt, k, d, vec_x);
           most = max(max(max(most, __float_as_uint(v.x) & 0x7fffffffu), __float_as_uint(v.y) & 0x7fffffffu),
                      max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
+          square += v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
         }
         most = __reduce_max_sync(kFull, most);
-        if (lane == 0) atomicMax(&sm.top, most);
+        for (int s = 16; s; s >>= 1) square += __shfl_xor_sync(kFull, square, s);
+        if (lane == 0) {
+          atomicMax(&sm.top, most);
+          sm.norm[warp] = square;
+        }
         __syncthreads();
         // x 2^e has its largest magnitude in [2^10, 2^11), under 6 times the largest scale.
         int e = 0;
         if (sm.top != 0 && sm.top < 0x7f800000u) e = max(min(10 - (int(sm.top >> 23) - 127), 126), -126);
         const float scale = pow2f(e);
-        float square = 0.f;
         for (int b = threadIdx.x; b < d_steps * (256 / kBlock); b += kThreads) {
           float v[kBlock];
 #pragma unroll
           for (int i = 0; i < kBlock; i += 4) {
             const float4 q = load4(xt, b * kBlock + i, d, vec_x);
             v[i] = q.x * scale, v[i + 1] = q.y * scale, v[i + 2] = q.z * scale, v[i + 3] = q.w * scale;
-            square += v[i] * v[i] + v[i + 1] * v[i + 1] + v[i + 2] * v[i + 2] + v[i + 3] * v[i + 3];
           }
           const uint32_t at = uint32_t(b) * kBlock;
           write_terms<kFormat, kTerms>(v, args.x_image + int64_t(at >> 8) * col_bytes, cols, uint32_t(t * kTerms), at & 255u);
@@ -544,21 +609,21 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
             if (piece < B::kAtoms) *reinterpret_cast<uint32_t*>(image + cols * 128 + scale_at(row, piece * 4)) = 0u;
           }
         }
-        for (int s = 16; s; s >>= 1) square += __shfl_xor_sync(kFull, square, s);
-        if (lane == 0) sm.norm[warp] = square;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          float total = 0.f;
-          for (int w = 0; w < kWarps; ++w) total += sm.norm[w];
-          args.x_exp[t] = e;
-          args.x_norm[t] = 0.5f * log2f(total) - float(e);  // log2 of x's 2-norm
+        if (warp == 0) {
+          float total = lane < kWarps ? sm.norm[lane] : 0.f;
+          for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(kFull, total, s);
+          if (lane == 0) {
+            // log2 of x's 2-norm, or of a bound where its square leaves the range of 32 bits.
+            args.x_norm[t] = total > 1e-30f && total < 1e30f ? 0.5f * log2f(total)
+                                                             : log2f(__uint_as_float(sm.top)) + 0.5f * log2f(float(d));
+            args.x_exp[t] = e;
+          }
         }
+        fence_proxy_async_all();
         __syncthreads();
       }
     }
-    for (int e = threadIdx.x; e < experts; e += kThreads) sm.mask[e] = 0;
   }
-  fence_proxy_async_all();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   bool ok = grid_barrier(args.counters, args, &sm.flag);
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -576,8 +641,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     __syncwarp();
     // |h| <= p |gate row| |up row| |x|^2: the power of two that keeps h under 6 times the largest scale.
     float bound = -INFINITY;
-    if (lane < top)
-      bound = log2f(sm.weight[warp][lane]) + log2f(__uint_as_float(__ldg(args.bound + sm.ids[warp][lane])));
+    if (lane < top) {
+      const int e = sm.ids[warp][lane];
+      bound = log2f(sm.weight[warp][lane]) + sm.bound[e];
+      atomicOr(&sm.mask[e], 1u << warp);
+    }
     for (int s = 16; s; s >>= 1) bound = fmaxf(bound, __shfl_xor_sync(kFull, bound, s));
     if (lane == 0) {
       const float e = floorf(11.3f - bound - 2.f * __ldcg(args.x_norm + warp));
@@ -590,34 +658,27 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     }
   }
   __syncthreads();
-  if (ok && warp == 0) {
-    // Masks token by token (a token's experts differ), then the experts in use in order.
-    for (int t = 0; t < tokens; ++t) {
-      if (lane < top) sm.mask[sm.ids[t][lane]] |= uint16_t(1u << t);
-      __syncwarp();
-    }
+  if (ok && warp == 0) {  // the experts in use, in order
     int count = 0;
     for (int e0 = 0; e0 < experts; e0 += 32) {
       const int e = e0 + lane;
       const bool in = e < experts && sm.mask[e] != 0;
       const uint32_t vote = __ballot_sync(kFull, in);
-      if (in) sm.active[count + __popc(vote & ((1u << lane) - 1u))] = uint16_t(e);
+      const int at = count + __popc(vote & ((1u << lane) - 1u));
+      if (in) {
+        sm.active[at] = uint16_t(e);
+        sm.index[e] = uint16_t(at);
+      }
       count += __popc(vote);
     }
     if (lane == 0) sm.count = count;
   }
   __syncthreads();
   const int used = ok ? sm.count : 0;
-  for (int i = threadIdx.x; i < used * tokens; i += kThreads) {
-    const int a = i / tokens, t = i - a * tokens, e = sm.active[a];
-    const uint32_t m = sm.mask[e];
-    int slot = 255;
-    if (m >> t & 1) {
-      for (int j = 0; j < top; ++j)
-        if (sm.ids[t][j] == e) slot = j;
-      sm.nth[a][__popc(m & ((1u << t) - 1u))] = uint8_t(t);
-    }
-    sm.slot[a][t] = uint8_t(slot);
+  for (int i = threadIdx.x; ok && i < tokens * top; i += kThreads) {
+    const int t = i / top, j = i - t * top, e = sm.ids[t][j], a = sm.index[e];
+    sm.slot[a][t] = uint8_t(j);
+    sm.nth[a][__popc(sm.mask[e] & ((1u << t) - 1u))] = uint8_t(t);
   }
   __syncthreads();
 
@@ -635,7 +696,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       dev::record_status(args.status, kStatusTimeout, kWaitTileStage);
     }
   };
-  // One stage: `weights` unless null, `columns` unless null; both together or weights first.
   auto produce_weights = [&](const uint8_t* weights) {
     if (put.lap > 0 && !dev::mbar_wait_abortable(&sm.empty[put.slot], (put.lap - 1) & 1u, limit, &sm.abort)) fail();
     if (sm.abort) return false;
@@ -645,6 +705,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   };
   auto produce_columns = [&](const uint8_t* columns, uint32_t slot) {
     dev::bulk_load(area + slot * stage_bytes + B::kBytes, columns, col_bytes, &sm.full[slot]);
+  };
+  // Streams the stages [begin, end) of a phase.  weights(at) and columns(at) are called for
+  // consecutive stages.  The first stages' weights, which nothing in this kernel writes,
+  // go ahead of the fence (and of the barrier, by a call of its own) that the columns wait for.
+  int ahead = 0;
+  auto produce_ahead = [&](int begin, int end, auto& weights) {
+    for (ahead = 0; ahead < int(stages) && begin + ahead < end; ++ahead) {
+      if (!produce_weights(weights.next())) break;
+      put.next(stages);
+    }
+  };
+  auto produce = [&](int begin, int end, auto& weights, auto& columns) {
+    fence_proxy_async_all();
+    uint32_t slot = (put.slot + stages - uint32_t(ahead)) % stages;
+    for (int i = 0; i < ahead; ++i) {
+      produce_columns(columns.next(), slot);
+      if (++slot == stages) slot = 0;
+    }
+    for (int at = begin + ahead; at < end; ++at) {
+      if (!produce_weights(weights.next())) break;
+      produce_columns(columns.next(), put.slot);
+      put.next(stages);
+    }
   };
   auto multiply = [&](const Runs& runs, int begin, int end) {
     for (int at = begin; at < end;) {
@@ -682,90 +765,141 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       at = stop;
     }
   };
-  // The epilogue of one phase.  value(k, v) takes the finished sum of the unit's k-th token (of `count(unit)`).
+  // The epilogue of one phase: value(unit, k, v) takes this lane's row of the finished sum of a
+  // unit's k-th token, of count(unit), whose columns are token(unit, k)'s; then done(unit, n).
   const int q = warp & 3, row_local = 32 * q + lane, etid = threadIdx.x - 64;
-  auto join = [&](const Runs& runs, int begin, int end, int32_t* counters, auto count, auto token, auto value,
-                  auto done) {
-    const int first_unit = begin / runs.steps;
-    for (int at = begin; at < end;) {
-      const int unit = at / runs.steps, unit_at = unit * runs.steps, stop = min(end, unit_at + runs.steps);
+  auto join = [&](const Runs& runs, int begin, int end, uint64_t* shares, auto count, auto token, auto value, auto done) {
+    int unit = begin < end ? begin / runs.steps : 0;
+    for (int at = begin; at < end; ++unit) {
+      const int unit_at = unit * runs.steps, unit_end = unit_at + runs.steps, stop = min(end, unit_end);
       const uint32_t b = runs_done & 1u, nb = runs_done >> 1;
       if (!dev::mbar_wait_abortable(&sm.acc_full[b], nb & 1u, limit, &sm.abort)) fail();
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       __syncwarp();
       const uint32_t taddr = tmem + b * 128 + (uint32_t(32 * q) << 16);
       const int n = count(unit);
-      const bool whole = stop - at == runs.steps;
-      // Shares: [cta][0: of its first unit, 1: of its last][token][row].
-      float* mine = args.partial + (int64_t(cta) * 2 + (unit == first_unit ? 0 : 1)) * (kMoeTokens * 128) + row_local;
-      for (int k = 0; k < n; ++k) {
-        const float v = read_terms<kTerms>(taddr + token(unit, k) * kTerms);
-        if (whole)
-          value(unit, k, v);
-        else
-          __stcg(mine + k * 128, v);
+      if (at != unit_at) {  // begun by another CTA: this is a share (each CTA has one such run at most)
+        uint64_t* mine = shares + int64_t(cta) * 2 * (kMoeTokens * 128) + row_local;
+        for (int k = 0; k < n; ++k) put_share(mine + k * 128, read_terms<kTerms>(taddr + token(unit, k) * kTerms));
+      } else {
+        const int c_last = stop == unit_end ? cta : runs.owner(unit_end - 1);
+        for (int k0 = 0; k0 < n; k0 += 4) {
+          float v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = k0 + k < n ? read_terms<kTerms>(taddr + token(unit, k0 + k) * kTerms) : 0.f;
+          // The other shares in the CTAs' order, four by four tokens under way at a time.
+          for (int c0 = cta + 1; c0 <= c_last; c0 += 4) {
+            uint64_t w[4][4];
+            const uint64_t* from = shares + int64_t(c0) * 2 * (kMoeTokens * 128) + k0 * 128 + row_local;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[c][k] = c0 + c <= c_last && k0 + k < n ? peek_share(from + int64_t(c) * 2 * (kMoeTokens * 128) + k * 128)
+                                                         : uint64_t(1) << 32;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (uint32_t(w[c][k] >> 32) == 0) {
+                  const uint64_t t0 = dev::global_timer_ns();
+                  do {
+                    w[c][k] = peek_share(from + int64_t(c) * 2 * (kMoeTokens * 128) + k * 128);
+                    if (sm.abort || dev::global_timer_ns() - t0 > limit) {
+                      fail();
+                      break;
+                    }
+                  } while (uint32_t(w[c][k] >> 32) == 0);
+                }
+                v[k] += __uint_as_float(uint32_t(w[c][k]));
+              }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k0 + k < n) value(unit, k0 + k, v[k]);
+        }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(&sm.acc_empty[b]);
       ++runs_done;
-      bool finish = whole;
-      if (!whole) {
-        const int c_first = runs.owner(unit_at), c_last = runs.owner(unit_at + runs.steps - 1);
-        dev::named_barrier(1, 128);
-        if (etid == 0) {
-          __threadfence();
-          const bool last = atomicAdd(counters + c_first, 1) == c_last - c_first;
-          if (last) counters[c_first] = 0;
-          __threadfence();
-          sm.last = last;
-        }
-        dev::named_barrier(1, 128);
-        finish = sm.last != 0;
-        if (finish) {
-          for (int k = 0; k < n; ++k) {
-            float v = 0.f;
-            for (int c = c_first; c <= c_last; ++c)
-              v += __ldcg(args.partial + (int64_t(c) * 2 + (runs.start(c) / runs.steps == unit ? 0 : 1)) * (kMoeTokens * 128) +
-                          k * 128 + row_local);
-            value(unit, k, v);
-          }
-        }
-      }
-      if (finish) done(unit, n);
-      dev::named_barrier(1, 128);  // sm.last and sm.gate_up may be written again
+      if (at == unit_at) done(unit, n);
       at = stop;
     }
   };
 
-  // Phase 2, and phase 3's first weights.
-  int ahead = 0;
-  auto up_weights = [&](int at) {
-    const int unit = at / d_steps, a = unit / f_tiles;
-    return args.gate_up + ((int64_t(sm.active[a]) * f_tiles + (unit - a * f_tiles)) * d_steps + at % d_steps) * B::kBytes;
-  };
-  auto down_weights = [&](int at) {
-    const int tile = at / down.steps, i = at - tile * down.steps, a = i / f_steps;
-    return args.down + ((int64_t(sm.active[a]) * d_tiles + tile) * f_steps + (i - a * f_steps)) * B::kBytes;
-  };
-  auto down_columns = [&](int at) { return args.h_image + int64_t(at % down.steps) * col_bytes; };
-  if (warp == 0 && lane == 0) {
-    fence_proxy_async_all();
-    for (int at = up_begin; at < up_end; ++at) {
-      if (!produce_weights(up_weights(at))) break;
-      produce_columns(args.x_image + int64_t(at % d_steps) * col_bytes, put.slot);
-      put.next(stages);
+  // Where the stages' bytes are.  Blocks of an expert follow one another tile by tile.
+  struct UpWeights {
+    const uint8_t* base;
+    const Smem& sm;
+    int per_expert, a, left;  // blocks of an expert; expert in use; blocks of it still to come
+    const uint8_t* at;
+    __device__ const uint8_t* next() {
+      if (left == 0) {
+        ++a;
+        left = per_expert;
+        at = base + int64_t(sm.active[a]) * per_expert * B::kBytes;
+      }
+      const uint8_t* p = at;
+      at += B::kBytes;
+      --left;
+      return p;
     }
-    for (int at = down_begin; at < down_end && ahead < int(stages); ++at, ++ahead) {
-      if (!produce_weights(down_weights(at))) break;
-      put.next(stages);
+  };
+  struct DownWeights {
+    const uint8_t* base;
+    const Smem& sm;
+    int used, tiles, steps, tile, a, left;
+    const uint8_t* at;
+    __device__ const uint8_t* next() {
+      if (left == 0) {
+        if (++a == used) a = 0, ++tile;
+        left = steps;
+        at = base + (int64_t(sm.active[a]) * tiles + tile) * steps * B::kBytes;
+      }
+      const uint8_t* p = at;
+      at += B::kBytes;
+      --left;
+      return p;
+    }
+  };
+  struct Columns {
+    const uint8_t* base;
+    uint32_t bytes;
+    int steps, step;
+    __device__ const uint8_t* next() {
+      const uint8_t* p = base + int64_t(step) * bytes;
+      if (++step == steps) step = 0;
+      return p;
+    }
+  };
+
+  // Phase 2, and phase 3's first weights.
+  DownWeights down_weights{args.down, sm, used, d_tiles, f_steps, 0, 0, 0, nullptr};
+  if (warp == 0 && lane == 0) {
+    if (up_begin < up_end) {
+      const int per = f_tiles * d_steps, a = up_begin / per;
+      UpWeights weights{args.gate_up, sm, per, a, per - (up_begin - a * per),
+                        args.gate_up + (int64_t(sm.active[a]) * per + (up_begin - a * per)) * B::kBytes};
+      Columns columns{args.x_image, col_bytes, d_steps, up_begin % d_steps};
+      produce_ahead(up_begin, up_end, weights);
+      produce(up_begin, up_end, weights, columns);
+    }
+    ahead = 0;
+    if (down_begin < down_end) {
+      const int tile = down_begin / down.steps, i = down_begin - tile * down.steps, a = i / f_steps;
+      down_weights.tile = tile;
+      down_weights.a = a;
+      down_weights.left = f_steps - (i - a * f_steps);
+      down_weights.at = args.down + ((int64_t(sm.active[a]) * d_tiles + tile) * f_steps + (i - a * f_steps)) * B::kBytes;
+      produce_ahead(down_begin, down_end, down_weights);
     }
   } else if (warp == 1 && lane == 0) {
     multiply(up, up_begin, up_end);
   } else if (warp >= 2 && warp < 6) {
     const float factor = args.gate_up_factor ? __ldg(args.gate_up_factor) : 1.f;
     join(
-        up, up_begin, up_end, args.counters + 64, [&](int unit) { return __popc(uint32_t(sm.mask[sm.active[unit / f_tiles]])); },
+        up, up_begin, up_end, args.share, [&](int unit) { return __popc(uint32_t(sm.mask[sm.active[unit / f_tiles]])); },
         [&](int unit, int k) { return int(sm.nth[unit / f_tiles][k]); },
         [&](int, int k, float v) { sm.gate_up[k][row_local] = v; },
         [&](int unit, int n) {
@@ -790,26 +924,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
               for (uint32_t i = 0; i < 32 / kBlock; ++i) image[cols * 128 + scale_at(row, c / kBlock + i)] = 0;
             }
           }
+          dev::named_barrier(1, 128);  // sm.gate_up may be written again
         });
+    fence_proxy_async_all();
   }
   __syncwarp();
-  fence_proxy_async_all();
   if (ok && !grid_barrier(args.counters + 1, args, &sm.flag)) ok = false;
   if (!ok) sm.abort = 1;
 
   // Phase 3.
   if (warp == 0 && lane == 0) {
-    fence_proxy_async_all();
-    // The columns of the stages whose weights are on their way: the last `ahead` slots.
-    uint32_t slot = (put.slot + stages - uint32_t(ahead)) % stages;
-    for (int i = 0; i < ahead; ++i) {
-      produce_columns(down_columns(down_begin + i), slot);
-      if (++slot == stages) slot = 0;
-    }
-    for (int at = down_begin + ahead; at < down_end; ++at) {
-      if (!produce_weights(down_weights(at))) break;
-      produce_columns(down_columns(at), put.slot);
-      put.next(stages);
+    if (down_begin < down_end) {
+      Columns columns{args.h_image, col_bytes, down.steps, down_begin % down.steps};
+      produce(down_begin, down_end, down_weights, columns);
     }
   } else if (warp == 1 && lane == 0) {
     multiply(down, down_begin, down_end);
@@ -818,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   } else if (warp >= 2 && warp < 6) {
     const float factor = args.down_factor ? __ldg(args.down_factor) : 1.f;
     join(
-        down, down_begin, down_end, args.counters + 1088, [&](int) { return tokens; }, [&](int, int k) { return k; },
+        down, down_begin, down_end, args.share + kMoeTokens * 128, [&](int) { return tokens; }, [&](int, int k) { return k; },
         [&](int unit, int k, float v) {
           const int row = unit * 128 + row_local;
           if (row < d) static_cast<T*>(args.y)[k * args.ldy + row] = from_f32<T>(v * factor * pow2f(-sm.h_exp[k]));
@@ -895,7 +1022,7 @@ MoeScratch fp4_moe_scratch(int dtype, int format, int64_t tokens, int64_t expert
   s.x_norm = take(tokens * 4);
   s.x_image = take((d + 255) / 256 * col_bytes);
   s.h_image = take(used * ((f + 255) / 256) * col_bytes);
-  s.partial = take(int64_t(sms) * 2 * kMoeTokens * 128 * 4);
+  s.share = take(int64_t(sms) * 2 * kMoeTokens * 128 * 8);
   s.bytes = at;
   return s;
 }

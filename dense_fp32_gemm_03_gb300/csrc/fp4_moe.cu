@@ -696,15 +696,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       dev::record_status(args.status, kStatusTimeout, kWaitTileStage);
     }
   };
+  // The whole warp walks the schedule and waits; one elected lane issues.  (From a
+  // branch of a single lane a tcgen05 instruction takes 60 to 170 cycles to issue, 8
+  // copies of scales and 4 MMAs 1282; so they take 257.)
   auto produce_weights = [&](const uint8_t* weights) {
     if (put.lap > 0 && !dev::mbar_wait_abortable(&sm.empty[put.slot], (put.lap - 1) & 1u, limit, &sm.abort)) fail();
-    if (sm.abort) return false;
-    dev::mbar_arrive_expect_tx(&sm.full[put.slot], stage_bytes);
-    dev::bulk_load(area + put.slot * stage_bytes, weights, B::kBytes, &sm.full[put.slot]);
+    if (__shfl_sync(kFull, sm.abort, 0)) return false;
+    if (dev::elect_one()) {
+      dev::mbar_arrive_expect_tx(&sm.full[put.slot], stage_bytes);
+      dev::bulk_load(area + put.slot * stage_bytes, weights, B::kBytes, &sm.full[put.slot]);
+    }
+    __syncwarp();
     return true;
   };
   auto produce_columns = [&](const uint8_t* columns, uint32_t slot) {
-    dev::bulk_load(area + slot * stage_bytes + B::kBytes, columns, col_bytes, &sm.full[slot]);
+    if (dev::elect_one())
+      dev::bulk_load(area + slot * stage_bytes + B::kBytes, columns, col_bytes, &sm.full[slot]);
+    __syncwarp();
   };
   // Streams the stages [begin, end) of a phase.  weights(at) and columns(at) are called for
   // consecutive stages.  The first stages' weights, which nothing in this kernel writes,
@@ -738,29 +746,33 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       for (int i = at; i < stop; ++i) {
         if (!dev::mbar_wait_abortable(&sm.full[got.slot], got.lap & 1u, limit, &sm.abort)) fail();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (!sm.abort) {
-          const uint32_t base = dev::smem_addr(area + got.slot * stage_bytes);
-          const uint32_t sr = tmem + 256 + got.slot * (8 * B::kAtoms), sc = sr + 4 * B::kAtoms;
-          const uint64_t drs = scale_desc(base + 16384), dcs = scale_desc(base + B::kBytes + cols * 128);
+        if (dev::elect_one()) {
+          if (!sm.abort) {
+            const uint32_t base = dev::smem_addr(area + got.slot * stage_bytes);
+            const uint32_t sr = tmem + 256 + got.slot * (8 * B::kAtoms), sc = sr + 4 * B::kAtoms;
+            const uint64_t drs = scale_desc(base + 16384), dcs = scale_desc(base + B::kBytes + cols * 128);
 #pragma unroll
-          for (int a = 0; a < B::kAtoms; ++a) {
-            copy_scales<1>(sr + 4 * a, drs + 32 * a);
-            copy_scales<1>(sc + 4 * a, dcs + 32 * a);
-          }
-          const uint64_t dr = operand_desc(base), dc = operand_desc(base + B::kBytes);
+            for (int a = 0; a < B::kAtoms; ++a) {
+              copy_scales<1>(sr + 4 * a, drs + 32 * a);
+              copy_scales<1>(sc + 4 * a, dcs + 32 * a);
+            }
+            const uint64_t dr = operand_desc(base), dc = operand_desc(base + B::kBytes);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            constexpr int kPer = 4 / B::kAtoms;  // MMAs that share an atom
-            const int a = j / kPer;
-            mma<kFormat, 1>(tmem + b * 128, dr + 2 * j, dc + 2 * j,
-                            instr_desc<kFormat>(128, cols, kPer == 2 ? (j & 1) * 2 : 0), sr + 4 * a, sc + 4 * a,
-                            (i != at || j != 0) ? 1u : 0u);
+            for (int j = 0; j < 4; ++j) {
+              constexpr int kPer = 4 / B::kAtoms;  // MMAs that share an atom
+              const int a = j / kPer;
+              mma<kFormat, 1>(tmem + b * 128, dr + 2 * j, dc + 2 * j,
+                              instr_desc<kFormat>(128, cols, kPer == 2 ? (j & 1) * 2 : 0), sr + 4 * a, sc + 4 * a,
+                              (i != at || j != 0) ? 1u : 0u);
+            }
           }
+          commit<1>(&sm.empty[got.slot]);
         }
-        commit<1>(&sm.empty[got.slot]);
+        __syncwarp();
         got.next(stages);
       }
-      commit<1>(&sm.acc_full[b]);
+      if (dev::elect_one()) commit<1>(&sm.acc_full[b]);
+      __syncwarp();
       ++runs_done;
       at = stop;
     }
@@ -876,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
 
   // Phase 2, and phase 3's first weights.
   DownWeights down_weights{args.down, sm, used, d_tiles, f_steps, 0, 0, 0, nullptr};
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     if (up_begin < up_end) {
       const int per = f_tiles * d_steps, a = up_begin / per;
       UpWeights weights{args.gate_up, sm, per, a, per - (up_begin - a * per),
@@ -894,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       down_weights.at = args.down + ((int64_t(sm.active[a]) * d_tiles + tile) * f_steps + (i - a * f_steps)) * B::kBytes;
       produce_ahead(down_begin, down_end, down_weights);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     multiply(up, up_begin, up_end);
   } else if (warp >= 2 && warp < 6) {
     const float factor = args.gate_up_factor ? __ldg(args.gate_up_factor) : 1.f;
@@ -933,14 +945,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   if (!ok) sm.abort = 1;
 
   // Phase 3.
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     if (down_begin < down_end) {
       Columns columns{args.h_image, col_bytes, down.steps, down_begin % down.steps};
       produce(down_begin, down_end, down_weights, columns);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     multiply(down, down_begin, down_end);
-    commit<1>(&sm.drain);
+    if (dev::elect_one()) commit<1>(&sm.drain);
+    __syncwarp();
     dev::mbar_wait(&sm.drain, 0u, limit);
   } else if (warp >= 2 && warp < 6) {
     const float factor = args.down_factor ? __ldg(args.down_factor) : 1.f;

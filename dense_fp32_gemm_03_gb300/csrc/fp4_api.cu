@@ -201,7 +201,7 @@ sgemm_status_t fp4_quantize(int dtype, const void* x, int64_t ldx, const fp4_mat
   LibDevice d;
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
-  return status_of(gb300::launch_fp4_quantize(dtype, x, ldx, *q, stream));
+  return status_of(gb300::launch_fp4_quantize(dtype, x, ldx, *q, d.sms, stream));
 }
 
 sgemm_status_t fp4_pack(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales,
@@ -220,7 +220,7 @@ sgemm_status_t fp4_pack(const uint8_t* codes, int64_t ld_codes, const uint8_t* s
   }
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
-  return status_of(gb300::launch_fp4_pack(codes, ld_codes, scales, ld_scales, *q, stream));
+  return status_of(gb300::launch_fp4_pack(codes, ld_codes, scales, ld_scales, *q, d.sms, stream));
 }
 
 sgemm_status_t fp4_dequantize(const fp4_matrix_t* q, int dtype, void* y, int64_t ldy, cudaStream_t stream) {
@@ -232,7 +232,7 @@ sgemm_status_t fp4_dequantize(const fp4_matrix_t* q, int dtype, void* y, int64_t
   LibDevice d;
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
-  return status_of(gb300::launch_fp4_dequantize(*q, dtype, y, ldy, stream));
+  return status_of(gb300::launch_fp4_dequantize(*q, dtype, y, ldy, d.sms, stream));
 }
 
 sgemm_status_t fp4_gemm(const fp4_matrix_t* A, const fp4_matrix_t* B, int dtype, void* C, int64_t ldc,
@@ -295,7 +295,7 @@ sgemm_status_t fp4_linear(int dtype, const void* x, int64_t ldx, int64_t M, cons
   uint8_t* base = static_cast<uint8_t*>(ws);
   q.codes = base + code_at;
   q.scales = base + scale_at;
-  if (gb300::launch_fp4_quantize(dtype, x, ldx, q, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+  if (gb300::launch_fp4_quantize(dtype, x, ldx, q, d.sms, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
   return run_product(p, q, *W, dtype, y, ldy, ws, base + gb300::kWorkspaceCounterBytes, d, stream);
 }
 

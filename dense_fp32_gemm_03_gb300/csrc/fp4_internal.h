@@ -11,12 +11,12 @@
 
 namespace gb300 {
 
-cudaError_t launch_fp4_quantize(int dtype, const void* x, int64_t ldx, const fp4_matrix_t& q,
+cudaError_t launch_fp4_quantize(int dtype, const void* x, int64_t ldx, const fp4_matrix_t& q, int sms,
                                 cudaStream_t stream);
-cudaError_t launch_fp4_dequantize(const fp4_matrix_t& q, int dtype, void* y, int64_t ldy,
+cudaError_t launch_fp4_dequantize(const fp4_matrix_t& q, int dtype, void* y, int64_t ldy, int sms,
                                   cudaStream_t stream);
 cudaError_t launch_fp4_pack(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales,
-                            const fp4_matrix_t& q, cudaStream_t stream);
+                            const fp4_matrix_t& q, int sms, cudaStream_t stream);
 
 // Products on the tensor cores (fp4_tc.cu): tiles of a row operand by a column
 // operand.  Swapped shapes take B as the row operand.

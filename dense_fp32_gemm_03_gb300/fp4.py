@@ -68,8 +68,10 @@ def load():
 
 
 # -------------------------------------------------------------------- arguments
+# The calls are short (a few microseconds on the GPU for a token), so the checks
+# ask each tensor for each property once.
 def _dense(t, name, cols=None):
-    """Row stride of a 2-D CUDA tensor of an unquantised type."""
+    """(row stride, rows, columns) of a 2-D CUDA tensor of an unquantised type."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.dtype not in _DTYPES or t.dim() != 2:
@@ -82,10 +84,10 @@ def _dense(t, name, cols=None):
     if cols is not None and n != cols:
         raise ValueError(f"{name} has {n} columns, expected {cols}")
     if rows <= 1:
-        return max(n, 1)
+        return n or 1, rows, n
     if stride < n:
         raise ValueError(f"{name} has overlapping rows (row stride {stride}, {n} columns)")
-    return max(stride, 1)
+    return stride or 1, rows, n
 
 
 def _format(fmt):
@@ -94,29 +96,31 @@ def _format(fmt):
     return FORMATS[fmt]
 
 
-def _scale(scale, fmt, device, name="scale"):
+def _scale(scale, fmt, index, name="scale"):
+    """Address of nvfp4's factor, or 0."""
     if scale is None:
-        return None
+        return 0
     if fmt != "nvfp4":
         raise ValueError(f"{name} belongs to nvfp4 only")
     if not isinstance(scale, torch.Tensor) or scale.dtype != torch.float32 or scale.numel() != 1 \
-            or scale.device != device:
-        raise ValueError(f"{name} must be a one-element float32 tensor on {device}")
-    return scale
+            or scale.get_device() != index:
+        raise ValueError(f"{name} must be a one-element float32 tensor on cuda:{index}")
+    return scale.data_ptr()
 
 
-def _same_device(device, *tensors):
+def _same_device(index, *tensors):
     for t in tensors:
-        if t.device != device:
-            raise ValueError(f"operands are on different devices ({device} and {t.device})")
+        other = t.index if isinstance(t, (Fp4Matrix, Fp4Experts)) else t.get_device()
+        if other != index:
+            raise ValueError(f"operands are on different devices (cuda:{index} and cuda:{other})")
 
 
-def _call(what, device, stream, fn, *args):
-    handle = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-    if torch.cuda.current_device() == device.index:
+def _call(what, index, stream, fn, *args):
+    handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
         st = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = fn(*args, handle)
     if st != OK:
         raise SgemmError(st, what)
@@ -130,47 +134,56 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _output(out, shape, dtype, device, stream):
+def _output(out, shape, dtype, device, index, stream):
+    """(out or a new tensor, its row stride)"""
     if out is None:
-        return _empty(shape, dtype, device, stream), max(shape[1], 1)
-    ld = _dense(out, "out")
-    if tuple(out.shape) != shape or out.dtype != dtype:
-        raise ValueError(f"out must be {shape} {dtype}, got {tuple(out.shape)} {out.dtype}")
-    _same_device(device, out)
+        return _empty(shape, dtype, device, stream), shape[1] or 1
+    ld, rows, cols = _dense(out, "out")
+    if (rows, cols) != shape or out.dtype != dtype:
+        raise ValueError(f"out must be {shape} {dtype}, got {(rows, cols)} {out.dtype}")
+    _same_device(index, out)
     return out, ld
 
 
 # --------------------------------------------------------------------- matrices
 class Fp4Matrix:
-    """A quantised matrix on the GPU: ``shape``, ``format``, ``codes``, ``scales`` and ``scale`` (nvfp4's factor).
+    """A quantised matrix on the GPU: ``shape``, ``format``, ``device``, ``codes``, ``scales``, ``scale`` (nvfp4's factor).
 
     ``codes`` holds two codes a byte, row by row; ``scales`` the scale bytes in
     the tensor core's order (``include/fp4.h``).  Made by :func:`fp4_quantize`
     or, from a checkpoint's arrays, by :func:`fp4_matrix`.
     """
 
+    __slots__ = ("format", "shape", "device", "index", "scale", "_memory", "_start", "_ld", "_c", "_ref", "__weakref__")
+
     def __init__(self, rows, cols, fmt, scale=None, device="cuda", stream=None):
         number = _format(fmt)
-        ld, codes, scales = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
-        st = load().fp4_layout(number, rows, cols, ctypes.byref(ld), ctypes.byref(codes), ctypes.byref(scales))
-        if st != OK:
-            raise SgemmError(st, "fp4_layout")
         device = torch.device(device)
         if device.type != "cuda":
             raise ValueError(f"a quantised matrix lives on a CUDA device, not on {device}")
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
-        self.format, self.shape, self.device = fmt, (rows, cols), device
-        self.scale = _scale(scale, fmt, device)
-        # One allocation: the codes, then the scales at the next 256 bytes.
-        start = (codes.value + 255) // 256 * 256
-        both = _empty((start + scales.value,), torch.uint8, device, stream)
-        self.codes = both[:codes.value].view(rows, ld.value) if rows and cols else both[:0].view(rows, 0)
-        self.scales = both[start:]
-        base = both.data_ptr()
-        self._c = _Matrix(number, rows, cols, base, ld.value, base + start,
-                          0 if self.scale is None else self.scale.data_ptr())
-        self._ref = ctypes.addressof(self._c)
+        index = device.index
+        # fp4_layout()'s sizes, in one allocation: the codes, then the scales at the next 256 bytes.
+        ld = (cols + 31) // 32 * 16
+        start = (rows * ld + 255) // 256 * 256
+        memory = _empty((start + (rows + 127) // 128 * ((cols + 255) // 256) * (1024 << number),), torch.uint8, device,
+                        stream)
+        self.format, self.shape, self.device, self.index, self.scale = fmt, (rows, cols), device, index, scale
+        self._memory, self._start, self._ld = memory, start, ld
+        base = memory.data_ptr()
+        self._c = c = _Matrix(number, rows, cols, base, ld, base + start, _scale(scale, fmt, index))
+        self._ref = ctypes.addressof(c)
+
+    @property
+    def codes(self):
+        """rows x pitch bytes, two codes a byte."""
+        return self._memory[:self.shape[0] * self._ld].view(self.shape[0], self._ld)
+
+    @property
+    def scales(self):
+        """The scale bytes, in the tensor core's order."""
+        return self._memory[self._start:]
 
     def dequantize(self, dtype=torch.float32):
         """The values the codes stand for (:func:`fp4_dequantize`)."""
@@ -193,17 +206,17 @@ def fp4_quantize(x, format="mxfp4", scale=None, out=None, stream=None):
     ``Fp4Matrix`` of x's shape and this format) is filled if given, with its
     own ``scale``.
     """
-    ld = _dense(x, "x")
+    ld, rows, cols = _dense(x, "x")
     if out is None:
-        out = Fp4Matrix(*x.shape, format, scale, x.device, stream)
+        out = Fp4Matrix(rows, cols, format, scale, x.device, stream)
     else:
         _quantized(out, "out")
-        if out.shape != tuple(x.shape) or out.format != format:
-            raise ValueError(f"out is {out}, expected {tuple(x.shape)} {format}")
+        if out.shape != (rows, cols) or out.format != format:
+            raise ValueError(f"out is {out}, expected {(rows, cols)} {format}")
         if scale is not None and scale is not out.scale:
             raise ValueError("out has its own scale: make it with this one")
-        _same_device(x.device, out)
-    _call("fp4_quantize", x.device, stream, load().fp4_quantize, _DTYPES[x.dtype], x.data_ptr(), ld, out._ref)
+        _same_device(x.get_device(), out)
+    _call("fp4_quantize", out.index, stream, load().fp4_quantize, _DTYPES[x.dtype], x.data_ptr(), ld, out._ref)
     return out
 
 
@@ -223,15 +236,17 @@ def fp4_matrix(codes, scales, format="mxfp4", cols=None, scale=None, stream=None
             raise ValueError(f"{name} must be a 2-D CUDA tensor of bytes")
         if t.shape[1] > 1 and t.stride(1) != 1:
             raise ValueError(f"{name} must be row-major (unit column stride)")
+        if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+            raise ValueError(f"{name} has overlapping rows")
     rows = codes.shape[0]
     cols = 2 * codes.shape[1] if cols is None else int(cols)
     blocks = -(-cols // BLOCK[format])
     if tuple(codes.shape) != (rows, (cols + 1) // 2) or tuple(scales.shape) != (rows, blocks):
         raise ValueError(f"{rows} x {cols} values in {format} take codes {(rows, (cols + 1) // 2)} and scales "
                          f"{(rows, blocks)}, got {tuple(codes.shape)} and {tuple(scales.shape)}")
-    _same_device(codes.device, scales)
+    _same_device(codes.get_device(), scales)
     q = Fp4Matrix(rows, cols, format, scale, codes.device, stream)
-    _call("fp4_pack", codes.device, stream, load().fp4_pack, codes.data_ptr(), max(codes.stride(0), codes.shape[1], 1),
+    _call("fp4_pack", q.index, stream, load().fp4_pack, codes.data_ptr(), max(codes.stride(0), codes.shape[1], 1),
           scales.data_ptr(), max(scales.stride(0), scales.shape[1], 1), q._ref)
     return q
 
@@ -243,8 +258,8 @@ def fp4_dequantize(q, dtype=torch.float32, out=None, stream=None):
         dtype = out.dtype
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    out, ld = _output(out, q.shape, dtype, q.device, stream)
-    _call("fp4_dequantize", q.device, stream, load().fp4_dequantize, q._ref, _DTYPES[dtype], out.data_ptr(), ld)
+    out, ld = _output(out, q.shape, dtype, q.device, q.index, stream)
+    _call("fp4_dequantize", q.index, stream, load().fp4_dequantize, q._ref, _DTYPES[dtype], out.data_ptr(), ld)
     return out
 
 
@@ -261,13 +276,13 @@ def fp4_gemm(A, B, out=None, out_dtype=torch.float32, stream=None):
         raise ValueError(f"inner dimensions differ: {A.shape} @ {B.shape}.T")
     if A.format != B.format:
         raise ValueError(f"formats differ: {A.format} and {B.format}")
-    _same_device(A.device, B)
+    _same_device(A.index, B)
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in _DTYPES:
         raise ValueError(f"out_dtype must be float32, bfloat16 or float16, got {out_dtype}")
-    out, ld = _output(out, (A.shape[0], B.shape[0]), out_dtype, A.device, stream)
-    _call("fp4_gemm", A.device, stream, load().fp4_gemm, A._ref, B._ref, _DTYPES[out_dtype], out.data_ptr(), ld)
+    out, ld = _output(out, (A.shape[0], B.shape[0]), out_dtype, A.device, A.index, stream)
+    _call("fp4_gemm", A.index, stream, load().fp4_gemm, A._ref, B._ref, _DTYPES[out_dtype], out.data_ptr(), ld)
     return out
 
 
@@ -278,13 +293,14 @@ def fp4_linear(x, W, x_scale=None, out=None, stream=None):
     of :func:`fp4_quantize` followed by :func:`fp4_gemm`.
     """
     _quantized(W, "W")
-    ldx = _dense(x, "x", W.shape[1])
-    device = W.device
-    _same_device(device, x)
-    factor = _scale(x_scale, W.format, device, "x_scale")
-    out, ldy = _output(out, (x.shape[0], W.shape[0]), x.dtype, device, stream)
-    _call("fp4_linear", device, stream, load().fp4_linear, _DTYPES[x.dtype], x.data_ptr(), ldx, x.shape[0],
-          0 if factor is None else factor.data_ptr(), W._ref, out.data_ptr(), ldy)
+    n, k = W.shape
+    ldx, m, _ = _dense(x, "x", k)
+    index, dtype = W.index, x.dtype
+    _same_device(index, x)
+    factor = _scale(x_scale, W.format, index, "x_scale")
+    out, ldy = _output(out, (m, n), dtype, W.device, index, stream)
+    _call("fp4_linear", index, stream, load().fp4_linear, _DTYPES[dtype], x.data_ptr(), ldx, m, factor, W._ref,
+          out.data_ptr(), ldy)
     return out
 
 
@@ -298,7 +314,7 @@ class Fp4Experts:
         st = load().fp4_experts_layout(number, experts, d, f, ctypes.byref(up), ctypes.byref(down))
         if st != OK:
             raise SgemmError(st, "fp4_experts_layout")
-        self.experts, self.d, self.f, self.format, self.device = experts, d, f, fmt, device
+        self.experts, self.d, self.f, self.format, self.device, self.index = experts, d, f, fmt, device, device.index
         self.gate_up = _empty((up.value,), torch.uint8, device, stream)
         self.down = _empty((down.value,), torch.uint8, device, stream)
         self.gate_up_scale, self.down_scale = gate_up_scale, down_scale
@@ -326,9 +342,9 @@ def fp4_experts(gate_up, down, experts, stream=None):
                          f"{gate_up.shape} and {down.shape}")
     if gate_up.format != down.format:
         raise ValueError(f"formats differ: {gate_up.format} and {down.format}")
-    _same_device(gate_up.device, down)
+    _same_device(gate_up.index, down)
     w = Fp4Experts(experts, d, f, gate_up.format, gate_up.scale, down.scale, gate_up.device, stream)
-    _call("fp4_experts_pack", w.device, stream, load().fp4_experts_pack, gate_up._ref, down._ref, w._ref)
+    _call("fp4_experts_pack", w.index, stream, load().fp4_experts_pack, gate_up._ref, down._ref, w._ref)
     return w
 
 
@@ -344,21 +360,20 @@ def fp4_moe(x, router, experts, top_k, renormalize=True, out=None, return_routin
     """
     if not isinstance(experts, Fp4Experts):
         raise TypeError("experts must be an Fp4Experts")
-    ldx = _dense(x, "x", experts.d)
-    ldr = _dense(router, "router", experts.d)
-    if router.dtype != torch.float32 or router.shape[0] != experts.experts:
-        raise ValueError(f"router must be {experts.experts} x {experts.d} float32, got {tuple(router.shape)} "
-                         f"{router.dtype}")
-    device, tokens, top_k = experts.device, x.shape[0], int(top_k)
-    _same_device(device, x, router)
+    ldx, tokens, d = _dense(x, "x", experts.d)
+    ldr, rows, _ = _dense(router, "router", d)
+    if router.dtype != torch.float32 or rows != experts.experts:
+        raise ValueError(f"router must be {experts.experts} x {d} float32, got {tuple(router.shape)} {router.dtype}")
+    device, index, top_k, dtype = experts.device, experts.index, int(top_k), x.dtype
+    _same_device(index, x, router)
     if not 1 <= top_k <= min(32, experts.experts):
         raise ValueError(f"top_k must be between 1 and {min(32, experts.experts)}, got {top_k}")
-    out, ldy = _output(out, (tokens, experts.d), x.dtype, device, stream)
+    out, ldy = _output(out, (tokens, d), dtype, device, index, stream)
     ids = p = None
     if return_routing:
         ids = _empty((tokens, top_k), torch.int32, device, stream)
         p = _empty((tokens, top_k), torch.float32, device, stream)
-    _call("fp4_moe", device, stream, load().fp4_moe, _DTYPES[x.dtype], x.data_ptr(), ldx, tokens, router.data_ptr(),
-          ldr, experts._ref, top_k, 1 if renormalize else 0, out.data_ptr(), ldy,
-          ids.data_ptr() if return_routing else 0, p.data_ptr() if return_routing else 0)
+    _call("fp4_moe", index, stream, load().fp4_moe, _DTYPES[dtype], x.data_ptr(), ldx, tokens, router.data_ptr(), ldr,
+          experts._ref, top_k, 1 if renormalize else 0, out.data_ptr(), ldy, ids.data_ptr() if return_routing else 0,
+          p.data_ptr() if return_routing else 0)
     return (out, ids, p) if return_routing else out

@@ -2,6 +2,7 @@
 // argument validation, scratch and launches.
 #include <cuda_runtime.h>
 
+#include <array>
 #include <cstdint>
 #include <map>
 #include <mutex>
@@ -131,6 +132,42 @@ bool plan_product(int64_t M, int64_t N, int64_t K, int sms, int pairs, Product* 
   const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
   if (pairs > 0 && tiles >= pairs) return plan_tiles(M, N, K, gb300::kFp4Pair, pairs, 4, true, p);
   return plan_tiles(M, N, K, gb300::kFp4Single128, sms, 4, true, p);
+}
+
+// The linear layer for few tokens: K over the CTAs of a cluster, a tile of 128
+// rows of W to a cluster at a time.  The cluster size with the fewest stages one
+// after another in a CTA; the smallest such, since joining costs.
+struct Clusters {
+  int ctas, clusters;
+  int64_t steps, per;
+};
+std::map<int, std::array<int, 4>> g_clusters;  // of 1, 2, 4 and 8 CTAs that run at once, by device
+
+bool plan_linear(int64_t M, int64_t N, int64_t K, int dev, Clusters* c) {
+  if (M > gb300::fp4_linear_tokens()) return false;
+  std::array<int, 4> most;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    auto it = g_clusters.find(dev);
+    if (it == g_clusters.end()) {
+      int n[4];
+      if (!gb300::fp4_linear_prepare(n)) n[0] = n[1] = n[2] = n[3] = 0;
+      it = g_clusters.emplace(dev, std::array<int, 4>{n[0], n[1], n[2], n[3]}).first;
+    }
+    most = it->second;
+  }
+  const int64_t tiles = (N + 127) / 128, steps = (K + 255) / 256;
+  int64_t best = INT64_MAX;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t per = (steps + (1 << i) - 1) >> i;
+    if (most[i] <= 0 || per > gb300::fp4_linear_steps()) continue;
+    const int64_t rounds = (tiles + most[i] - 1) / most[i], cost = rounds * per;
+    if (cost < best) {
+      best = cost;
+      *c = Clusters{1 << i, int(tiles < most[i] ? tiles : most[i]), steps, per};
+    }
+  }
+  return best != INT64_MAX;
 }
 
 // C = A B^T with the plan's partial sums at `partials` (after the counters at `ws`).
@@ -282,6 +319,29 @@ sgemm_status_t fp4_linear(int dtype, const void* x, int64_t ldx, int64_t M, cons
   q.ld = code_pitch(W->cols);
   q.factor = x_factor;
   if (W->cols == 0) return zero_output(dtype, y, M, W->rows, ldy, stream);
+  Clusters c;
+  if (plan_linear(M, W->rows, W->cols, d.dev, &c)) {
+    CUtensorMap map;
+    st = gb300::lib_encode_bytes(W->codes, W->rows, code_pitch(W->cols), W->ld, 128, &map);
+    if (st != SGEMM_OK) return st;
+    gb300::Fp4LinearArgs a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.x_factor = x_factor;
+    a.scales = W->scales;
+    a.w_factor = W->factor;
+    a.y = y;
+    a.ldy = ldy;
+    a.tokens = int32_t(M);
+    a.n = int32_t(W->rows);
+    a.k = int32_t(W->cols);
+    a.steps = int32_t(c.steps);
+    a.ctas = c.ctas;
+    a.per = int32_t(c.per);
+    a.status = d.status;
+    a.wait_limit_ns = d.wait_limit_ns;
+    return status_of(gb300::launch_fp4_linear(dtype, W->format, map, a, c.clusters, stream));
+  }
   Product p;
   const int pairs = tc_pairs(d.dev);
   if (pairs < 0) return SGEMM_ERR_LAUNCH;

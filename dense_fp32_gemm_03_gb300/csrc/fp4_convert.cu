@@ -139,16 +139,6 @@ struct Piece {
   }
 };
 
-// x / unit, correctly rounded.  With r the correctly rounded reciprocal, the
-// quotient x r corrected once by its residual is correctly rounded (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990) as long as the residual is not subnormal, which holds for units between
-// 2^-100 and 2^100 wherever the quotient is not far below the smallest level.
-__device__ __forceinline__ float quotient(float x, float unit, float r) {
-  const float q = x * r;
-  return fmaf(fmaf(-q, unit, x), r, q);
-}
-
 template <typename T, int kFormat, bool kAligned>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(const T* __restrict__ x, int64_t ldx, const float* __restrict__ factor, int rows,
@@ -156,9 +146,7 @@ __global__ void __launch_bounds__(kThreads)
   using F = Format<kFormat>;
   constexpr int kLanes = F::kBlock / kLaneCols;  // lanes of a block
   const int lane = threadIdx.x & 31;
-  const float g = kFormat == FP4_NVFP4 && factor != nullptr ? __ldg(factor) : 1.f;
-  const float g6 = 6.f * g, g6_inv = __frcp_rn(g6);
-  const bool plain = g6 >= 0x1p-100f && g6 <= 0x1p100f;
+  const Quantizer<kFormat> quantizer(factor);
   const int code_cols = (cols + 31) / 32 * 32, scale_cols = (cols + 255) / 256 * 256;
   const int64_t atoms = int64_t(scale_cols / F::kAtom);
   PieceIter it(rows, (cols + kPieceCols - 1) / kPieceCols, int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5),
@@ -171,42 +159,11 @@ __global__ void __launch_bounds__(kThreads)
     in.values(v, lane);
     it.next();
     if (it.valid()) in.load(x + int64_t(it.r) * ldx, cols, it.piece, lane);  // on its way during the arithmetic
-    float a = fabsf(v[0]);
-#pragma unroll
-    for (int i = 1; i < kLaneCols; ++i) a = max_abs(a, v[i]);
+    float a = largest(v), unit;
     if (kLanes == 2) a = max_abs(a, __shfl_xor_sync(kFull, a, 1));
-    const uint32_t top = __float_as_uint(a);  // NaN and infinity: from 0x7f800000 on
-
-    uint32_t byte, word[2] = {0u, 0u};
-    if constexpr (kFormat == FP4_MXFP4) {
-      // floor(log2 a) is the exponent field; a subnormal a clamps to -127 as field 0 does.
-      const int e = max(int(top >> 23) - 127 - 2, -127);
-      byte = top >= 0x7f800000u ? 255u : top == 0 ? 0u : uint32_t(e + 127);
-      const float inv = __uint_as_float(uint32_t(127 - e) << 23);  // 2^-e, at most 2^127
-#pragma unroll
-      for (int i = 0; i < kLaneCols; ++i) v[i] *= inv;
-      word[0] = encode8(v);
-      word[1] = encode8(v + 8);
-    } else {
-      const float s = plain ? quotient(a, g6, g6_inv) : __fdiv_rn(a, g6);
-      byte = top >= 0x7f800000u ? 127u : top == 0 ? 0u : encode_e4m3(s);
-      const float unit = decode_e4m3(byte) * g;
-      if (unit >= 0x1p-100f && unit <= 0x1p100f) {
-        const float inv = __frcp_rn(unit);
-#pragma unroll
-        for (int i = 0; i < kLaneCols; ++i) v[i] = quotient(v[i], unit, inv);
-        word[0] = encode8(v);
-        word[1] = encode8(v + 8);
-      } else if (unit > 0.f) {
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          float q[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) q[k] = __fdiv_rn(i ? v[8 + k] : v[k], unit);
-          word[i] = encode8(q);
-        }
-      }
-    }
+    const uint32_t byte = quantizer.scale(a, unit);
+    uint32_t word[2];
+    quantizer.encode(v, unit, word);
     if (c < code_cols) *reinterpret_cast<uint2*>(codes + int64_t(r) * ld + c / 2) = make_uint2(word[0], word[1]);
     const uint32_t four = join_scales<kLanes>(byte, lane);
     if (lane % (4 * kLanes) == 0 && c < scale_cols)

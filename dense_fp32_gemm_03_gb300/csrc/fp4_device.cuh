@@ -116,5 +116,85 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// x / unit, correctly rounded.  With r the correctly rounded reciprocal, the
+// quotient x r corrected once by its residual is correctly rounded (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990) as long as the residual is not subnormal, which holds for units between
+// 2^-100 and 2^100 wherever the quotient is not far below the smallest level.
+__device__ __forceinline__ float quotient(float x, float unit, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, unit, x), r, q);
+}
+
+// Quantisation of a block, 16 of its values at a time (fp4.h has the definition).
+template <int kFormat>
+struct Quantizer {
+  float g, g6, g6_inv;
+  bool plain;
+
+  __device__ __forceinline__ explicit Quantizer(const float* factor) {
+    g = kFormat == FP4_NVFP4 && factor != nullptr ? __ldg(factor) : 1.f;
+    g6 = 6.f * g;
+    g6_inv = __frcp_rn(g6);
+    plain = g6 >= 0x1p-100f && g6 <= 0x1p100f;
+  }
+
+  // The scale byte of a block whose largest magnitude is `a` (NaN if one value is),
+  // and what encode() needs: the unit, or for powers of two its inverse.
+  __device__ __forceinline__ uint32_t scale(float a, float& unit) const {
+    const uint32_t top = __float_as_uint(a);  // NaN and infinity: from 0x7f800000 on
+    if constexpr (kFormat == FP4_MXFP4) {
+      // floor(log2 a) is the exponent field; a subnormal a clamps to -127 as field 0 does.
+      const int e = max(int(top >> 23) - 127 - 2, -127);
+      unit = __uint_as_float(uint32_t(127 - e) << 23);  // 2^-e, at most 2^127
+      return top >= 0x7f800000u ? 255u : top == 0 ? 0u : uint32_t(e + 127);
+    } else {
+      const float s = plain ? quotient(a, g6, g6_inv) : __fdiv_rn(a, g6);
+      const uint32_t byte = top >= 0x7f800000u ? 127u : top == 0 ? 0u : encode_e4m3(s);
+      unit = decode_e4m3(byte) * g;
+      return byte;
+    }
+  }
+
+  __device__ __forceinline__ void encode(float (&v)[16], float unit, uint32_t (&word)[2]) const {
+    if constexpr (kFormat == FP4_MXFP4) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] *= unit;
+      word[0] = encode8(v);
+      word[1] = encode8(v + 8);
+    } else {
+      word[0] = word[1] = 0u;
+      if (unit >= 0x1p-100f && unit <= 0x1p100f) {
+        const float inv = __frcp_rn(unit);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = quotient(v[i], unit, inv);
+        word[0] = encode8(v);
+        word[1] = encode8(v + 8);
+      } else if (unit > 0.f) {
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          float q[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) q[k] = __fdiv_rn(i ? v[8 + k] : v[k], unit);
+          const uint32_t w = encode8(q);
+          if (i) word[1] = w; else word[0] = w;
+        }
+      }
+    }
+  }
+};
+
+// The largest magnitude of 16 values; NaN if there is one.
+__device__ __forceinline__ float largest(const float (&v)[16]) {
+  float a[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = max_abs(v[i], v[i + 8]);
+#pragma unroll
+  for (int n = 4; n; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; ++i) a[i] = max_abs(a[i], a[i + n]);
+  return a[0];
+}
+
 }  // namespace fp4
 }  // namespace gb300

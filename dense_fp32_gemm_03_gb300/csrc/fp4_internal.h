@@ -47,6 +47,28 @@ struct Fp4TcArgs {
 cudaError_t launch_fp4_tc(int dtype, int format, Fp4TcShape shape, const CUtensorMap (&maps)[5],
                           const Fp4TcArgs& args, const Sched& sc, int grid, cudaStream_t stream);
 
+// The linear layer for few tokens (fp4_linear.cu).
+int fp4_linear_tokens();  // the most
+int fp4_linear_steps();   // stages (256 columns) of K that one CTA of a cluster takes at most
+struct Fp4LinearArgs {
+  const void* x;
+  int64_t ldx;
+  const float* x_factor;
+  const uint8_t* scales;  // W's
+  const float* w_factor;
+  void* y;
+  int64_t ldy;
+  int32_t tokens, n, k;
+  int32_t steps, ctas, per;  // stages of K, CTAs of a cluster, stages of each
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+// Sets the kernels' attributes on the current device; the clusters of 1, 2, 4 and 8 CTAs that run at once.
+bool fp4_linear_prepare(int (&clusters)[4]);
+// map: W's codes in boxes of 128 rows x 128 bytes, 128-byte swizzle.
+cudaError_t launch_fp4_linear(int dtype, int format, const CUtensorMap& map, const Fp4LinearArgs& args, int clusters,
+                              cudaStream_t stream);
+
 // The expert weights' order (fp4_moe.cu): blocks of 128 rows x 256 columns as
 // one stage of the layer's kernel takes them; after the gate-and-up blocks one 32-bit bound an expert.
 int64_t fp4_gate_up_bytes(int format, int64_t experts, int64_t d, int64_t f);

@@ -19,7 +19,7 @@
 
 #include "fp4_device.cuh"
 #include "fp4_internal.h"
-#include "fp4_tc.cuh"
+#include "fp4_stream.cuh"
 #include "sgemm_device.cuh"
 
 namespace gb300 {
@@ -34,9 +34,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTop = 32;
 constexpr int kMaxPairs = kMoeTokens * kMaxTop;
-constexpr int kMaxStages = 8;
 constexpr uint32_t kStatusTimeout = 3;
-constexpr int kSmemBytes = 232448;
 
 template <typename T>
 struct Terms {
@@ -51,25 +49,6 @@ struct Terms<__half> {
   static constexpr int kCount = 6;
 };
 static_assert(kMoeTokens * 8 <= 128, "columns of one product");
-
-// 128 rows x 256 columns of weights: the codes as the 128-byte swizzle lays them
-// out in shared memory, then the scale atoms.  One stage of the ring; the
-// columns' blocks (`cols` rows x 256) have the same form.
-template <int kFormat>
-struct Block {
-  static constexpr int kAtoms = Format<kFormat>::kAtomsPerStage;
-  static constexpr uint32_t kScales = kAtoms * 512;
-  static constexpr uint32_t kBytes = 16384 + kScales;
-};
-
-// Byte of 16-byte piece `piece` of row r in a block's codes.
-__host__ __device__ __forceinline__ uint32_t piece_at(uint32_t r, uint32_t piece) {
-  return r * 128 + ((piece ^ (r & 7)) << 4);
-}
-// Byte of the scale of row r, block b (of 256 / kBlock) among a block's scales.
-__host__ __device__ __forceinline__ uint32_t scale_at(uint32_t r, uint32_t b) {
-  return (b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3);
-}
 
 // ------------------------------------------------------------------ packing
 // One thread moves one 16-byte piece of codes, and the first threads of a row
@@ -424,17 +403,6 @@ struct Smem {
 };
 constexpr int kStageArea = kSmemBytes - 1024 - int((sizeof(Smem) + 127) / 128 * 128);
 
-// Ring position: slot, and how often the ring went round.
-struct At {
-  uint32_t slot = 0, lap = 0;
-  __device__ __forceinline__ void next(uint32_t stages) {
-    if (++slot == stages) slot = 0, ++lap;
-  }
-};
-
-// Orders global writes of ordinary stores before later bulk copies, and the other way round.
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
-
 // This lane's row of kTerms columns of tensor memory, as one value.
 template <int kTerms>
 __device__ __forceinline__ float read_terms(uint32_t taddr) {
@@ -452,16 +420,6 @@ __device__ __forceinline__ float read_terms(uint32_t taddr) {
 #pragma unroll
   for (int j = kTerms - 2; j >= 0; --j) sum = fmaf(sum, 0.25f, v[j]);
   return sum;
-}
-
-// A share's value and the mark that it is there, in one 64-bit word: no flag, no fence.
-__device__ __forceinline__ void put_share(uint64_t* p, float v) {
-  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(uint64_t(1) << 32 | __float_as_uint(v)) : "memory");
-}
-__device__ __forceinline__ uint64_t peek_share(const uint64_t* p) {
-  uint64_t w;
-  asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w) : "l"(p) : "memory");
-  return w;
 }
 
 // Three phases with a grid barrier between them.
@@ -792,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       const int n = count(unit);
       if (at != unit_at) {  // begun by another CTA: this is a share (each CTA has one such run at most)
         uint64_t* mine = shares + int64_t(cta) * 2 * (kMoeTokens * 128) + row_local;
-        for (int k = 0; k < n; ++k) put_share(mine + k * 128, read_terms<kTerms>(taddr + token(unit, k) * kTerms));
+        for (int k = 0; k < n; ++k) put_share(mine + k * 128, read_terms<kTerms>(taddr + token(unit, k) * kTerms), 1u);
       } else {
         const int c_last = stop == unit_end ? cta : runs.owner(unit_end - 1);
         for (int k0 = 0; k0 < n; k0 += 4) {

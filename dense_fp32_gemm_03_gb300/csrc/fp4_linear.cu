@@ -79,14 +79,6 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uin
   }
 }
 
-__device__ __forceinline__ void load_map(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dev::smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(dev::smem_addr(bar))
-      : "memory");
-}
-
 // Sixteen consecutive values of a row as they are stored, zeros beyond `n`.
 template <typename T>
 struct Sixteen {
@@ -119,7 +111,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   __shared__ Barriers bars;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int ctas = args.ctas, cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas, rank = blockIdx.x % ctas;
   const int tokens = args.tokens, tiles = (args.n + 127) / 128;
   // This CTA's stages of K.
@@ -135,10 +127,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 
   auto load_stage = [&](int tile, int step, uint32_t slot) {
     unsigned char* stage = s_w + slot * L::kWeights;
-    dev::mbar_arrive_expect_tx(&bars.full[slot], L::kWeights);
-    load_map(stage, &map_w, (first + step) * 128, tile * 128, &bars.full[slot]);
-    dev::bulk_load(stage + 16384, args.scales + (int64_t(tile) * args.steps + first + step) * B::kScales, B::kScales,
-                   &bars.full[slot]);
+    const uint32_t e = elected();
+    expect_bytes(e, &bars.full[slot], L::kWeights);
+    load_box<1>(e, stage, &map_w, (first + step) * 128, tile * 128, dev::smem_addr(&bars.full[slot]));
+    load_bytes(e, stage + 16384, args.scales + (int64_t(tile) * args.steps + first + step) * B::kScales, B::kScales,
+               &bars.full[slot]);
   };
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dev::smem_addr(&s_tmem)),
@@ -164,8 +157,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     __syncwarp();
     // The ring's first stages need no other warp: they go out before the CTA's barrier.
     for (uint32_t n = 0; n < stages && int(n) < steps; ++n) {
-      if (dev::elect_one()) load_stage(cluster, int(n), n);
-      __syncwarp();
+      load_stage(cluster, int(n), n);
     }
   }
   // So do the first values of x.
@@ -186,7 +178,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   __syncthreads();
   if (ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = s_tmem;
+  constexpr uint32_t tmem = kTmemBase;
   auto fail = [&]() {
     if (!s_abort) {
       s_abort = 1;
@@ -209,8 +201,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         if (put.lap > 0 && !dev::mbar_wait_abortable(&bars.empty[put.slot], (put.lap - 1) & 1u, limit, &s_abort)) fail();
         go = __shfl_sync(kFull, s_abort, 0) == 0;
         if (!go) break;
-        if (dev::elect_one()) load_stage(tile, i, put.slot);
-        __syncwarp();
+        load_stage(tile, i, put.slot);
       }
   } else if (warp == 1) {
     // ---- MMAs
@@ -224,36 +215,30 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         if (done == 0 && !dev::mbar_wait_abortable(&bars.x[i], 0u, limit, &s_abort)) fail();
         if (!dev::mbar_wait_abortable(&bars.full[got.slot], got.lap & 1u, limit, &s_abort)) fail();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (dev::elect_one()) {
-          if (!s_abort) {
-            const uint32_t base = dev::smem_addr(s_w + got.slot * L::kWeights), xs = dev::smem_addr(s_x + i * L::kStep);
-            const uint32_t sr = tmem + 256 + got.slot * (8 * B::kAtoms), sc = sr + 4 * B::kAtoms;
-            const uint64_t drs = scale_desc(base + 16384), dcs = scale_desc(xs + L::kCodes);
+        const uint32_t e = elected();
+        const uint32_t base = dev::smem_addr(s_w + got.slot * L::kWeights), xs = dev::smem_addr(s_x + i * L::kStep);
+        const uint32_t sr = tmem + 256 + got.slot * (8 * B::kAtoms), sc = sr + 4 * B::kAtoms;
+        const uint64_t drs = scale_desc(base + 16384), dcs = scale_desc(xs + L::kCodes);
 #pragma unroll
-            for (int a = 0; a < B::kAtoms; ++a) {
-              copy_scales<1>(sr + 4 * a, drs + 32 * a);
-              copy_scales<1>(sc + 4 * a, dcs + 32 * a);
-            }
-            const uint64_t dr = operand_desc(base), dc = operand_desc(xs);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              constexpr int kPer = 4 / B::kAtoms;  // MMAs that share an atom
-              const int a = j / kPer;
-              mma<kFormat, 1>(tmem + b * kCols, dr + 2 * j, dc + 2 * j,
-                              instr_desc<kFormat>(128, kCols, kPer == 2 ? (j & 1) * 2 : 0), sr + 4 * a, sc + 4 * a,
-                              (i != 0 || j != 0) ? 1u : 0u);
-            }
-          }
-          commit<1>(&bars.empty[got.slot]);
+        for (int a = 0; a < B::kAtoms; ++a) {
+          copy_scales<1>(e, sr + 4 * a, drs + 32 * a);
+          copy_scales<1>(e, sc + 4 * a, dcs + 32 * a);
         }
-        __syncwarp();
+        const uint64_t dr = operand_desc(base), dc = operand_desc(xs);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          constexpr int kPer = 4 / B::kAtoms;  // MMAs that share an atom
+          const int a = j / kPer;
+          mma<kFormat, 1>(e, tmem + b * kCols, dr + 2 * j, dc + 2 * j,
+                          instr_desc<kFormat>(128, kCols, kPer == 2 ? (j & 1) * 2 : 0), sr + 4 * a, sc + 4 * a,
+                          (i != 0 || j != 0) ? 1u : 0u);
+        }
+        commit<1>(e, &bars.empty[got.slot]);
         got.next(stages);
       }
-      if (dev::elect_one()) commit<1>(&bars.acc_full[b]);
-      __syncwarp();
+      commit<1>(elected(), &bars.acc_full[b]);
     }
-    if (dev::elect_one()) commit<1>(&bars.drain);
-    __syncwarp();
+    commit<1>(elected(), &bars.drain);
     dev::mbar_wait(&bars.drain, 0u, limit);
   } else if (warp < 6) {
     // ---- joining and storing: a lane has one row of W, 16 tokens

@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* area = smem_raw + ((1024u - (dev::smem_addr(smem_raw) & 1023u)) & 1023u);
   Smem& sm = *reinterpret_cast<Smem*>(area + kStageArea);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x, ctas = gridDim.x;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31, cta = blockIdx.x, ctas = gridDim.x;
   const int tokens = args.tokens, experts = args.experts, top = args.top, d = args.d, f = args.f;
   const int d_steps = (d + 255) / 256, f_steps = (f + 255) / 256;
   const uint32_t cols = uint32_t(args.cols), col_bytes = cols * 128 + B::kScales;
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   bool ok = grid_barrier(args.counters, args, &sm.flag);
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = sm.tmem;
+  constexpr uint32_t tmem = kTmemBase;
 
   // ---- selection, the same in every CTA
   if (ok && warp < tokens) {
@@ -654,23 +654,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       dev::record_status(args.status, kStatusTimeout, kWaitTileStage);
     }
   };
-  // The whole warp walks the schedule and waits; one elected lane issues.  (From a
-  // branch of a single lane a tcgen05 instruction takes 60 to 170 cycles to issue, 8
-  // copies of scales and 4 MMAs 1282; so they take 257.)
   auto produce_weights = [&](const uint8_t* weights) {
     if (put.lap > 0 && !dev::mbar_wait_abortable(&sm.empty[put.slot], (put.lap - 1) & 1u, limit, &sm.abort)) fail();
     if (__shfl_sync(kFull, sm.abort, 0)) return false;
-    if (dev::elect_one()) {
-      dev::mbar_arrive_expect_tx(&sm.full[put.slot], stage_bytes);
-      dev::bulk_load(area + put.slot * stage_bytes, weights, B::kBytes, &sm.full[put.slot]);
-    }
-    __syncwarp();
+    const uint32_t e = elected();
+    expect_bytes(e, &sm.full[put.slot], stage_bytes);
+    load_bytes(e, area + put.slot * stage_bytes, weights, B::kBytes, &sm.full[put.slot]);
     return true;
   };
   auto produce_columns = [&](const uint8_t* columns, uint32_t slot) {
-    if (dev::elect_one())
-      dev::bulk_load(area + slot * stage_bytes + B::kBytes, columns, col_bytes, &sm.full[slot]);
-    __syncwarp();
+    load_bytes(elected(), area + slot * stage_bytes + B::kBytes, columns, col_bytes, &sm.full[slot]);
   };
   // Streams the stages [begin, end) of a phase.  weights(at) and columns(at) are called for
   // consecutive stages.  The first stages' weights, which nothing in this kernel writes,
@@ -704,33 +697,28 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       for (int i = at; i < stop; ++i) {
         if (!dev::mbar_wait_abortable(&sm.full[got.slot], got.lap & 1u, limit, &sm.abort)) fail();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (dev::elect_one()) {
-          if (!sm.abort) {
-            const uint32_t base = dev::smem_addr(area + got.slot * stage_bytes);
-            const uint32_t sr = tmem + 256 + got.slot * (8 * B::kAtoms), sc = sr + 4 * B::kAtoms;
-            const uint64_t drs = scale_desc(base + 16384), dcs = scale_desc(base + B::kBytes + cols * 128);
+        const uint32_t e = elected();
+        const uint32_t base = dev::smem_addr(area + got.slot * stage_bytes);
+        const uint32_t sr = tmem + 256 + got.slot * (8 * B::kAtoms), sc = sr + 4 * B::kAtoms;
+        const uint64_t drs = scale_desc(base + 16384), dcs = scale_desc(base + B::kBytes + cols * 128);
 #pragma unroll
-            for (int a = 0; a < B::kAtoms; ++a) {
-              copy_scales<1>(sr + 4 * a, drs + 32 * a);
-              copy_scales<1>(sc + 4 * a, dcs + 32 * a);
-            }
-            const uint64_t dr = operand_desc(base), dc = operand_desc(base + B::kBytes);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              constexpr int kPer = 4 / B::kAtoms;  // MMAs that share an atom
-              const int a = j / kPer;
-              mma<kFormat, 1>(tmem + b * 128, dr + 2 * j, dc + 2 * j,
-                              instr_desc<kFormat>(128, cols, kPer == 2 ? (j & 1) * 2 : 0), sr + 4 * a, sc + 4 * a,
-                              (i != at || j != 0) ? 1u : 0u);
-            }
-          }
-          commit<1>(&sm.empty[got.slot]);
+        for (int a = 0; a < B::kAtoms; ++a) {
+          copy_scales<1>(e, sr + 4 * a, drs + 32 * a);
+          copy_scales<1>(e, sc + 4 * a, dcs + 32 * a);
         }
-        __syncwarp();
+        const uint64_t dr = operand_desc(base), dc = operand_desc(base + B::kBytes);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          constexpr int kPer = 4 / B::kAtoms;  // MMAs that share an atom
+          const int a = j / kPer;
+          mma<kFormat, 1>(e, tmem + b * 128, dr + 2 * j, dc + 2 * j,
+                          instr_desc<kFormat>(128, cols, kPer == 2 ? (j & 1) * 2 : 0), sr + 4 * a, sc + 4 * a,
+                          (i != at || j != 0) ? 1u : 0u);
+        }
+        commit<1>(e, &sm.empty[got.slot]);
         got.next(stages);
       }
-      if (dev::elect_one()) commit<1>(&sm.acc_full[b]);
-      __syncwarp();
+      commit<1>(elected(), &sm.acc_full[b]);
       ++runs_done;
       at = stop;
     }
@@ -910,8 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     }
   } else if (warp == 1) {
     multiply(down, down_begin, down_end);
-    if (dev::elect_one()) commit<1>(&sm.drain);
-    __syncwarp();
+    commit<1>(elected(), &sm.drain);
     dev::mbar_wait(&sm.drain, 0u, limit);
   } else if (warp >= 2 && warp < 6) {
     const float factor = args.down_factor ? __ldg(args.down_factor) : 1.f;

@@ -67,22 +67,6 @@ struct Tile {
 };
 
 template <int kCtas>
-__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  if constexpr (kCtas == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dev::smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dev::smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
-template <int kCtas>
 __device__ __forceinline__ uint32_t barrier_of_first(uint64_t* bar) {
   if constexpr (kCtas == 1) return dev::smem_addr(bar);
   uint32_t d;
@@ -157,7 +141,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap& map_r, const CUtensor
   volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1) + 1;
   int* s_last = reinterpret_cast<int*>(drain + 1) + 2;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   uint32_t rank = 0;
   if constexpr (kCtas == 2) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const bool first = rank == 0;
@@ -192,7 +176,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap& map_r, const CUtensor
   __syncthreads();
   if constexpr (kCtas == 2) cluster_sync();  // the peer's barriers exist before anything signals them
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = kTmemBase;
 
   auto fail = [&]() {
     if (!*s_abort) {
@@ -225,18 +209,14 @@ __device__ __forceinline__ void tc_body(const CUtensorMap& map_r, const CUtensor
         if (n > 0 && !dev::mbar_wait_abortable(&empty[s], (n - 1) & 1u, limit, s_abort)) fail();
         go = __shfl_sync(0xffffffffu, *s_abort, 0) == 0;
         if (!go) break;
-        if (dev::elect_one()) {
-          const uint32_t bar = barrier_of_first<kCtas>(&full[s]);
-          if (first) dev::mbar_arrive_expect_tx(&full[s], kCtas * S::kStageBytes);
-          load_box<kCtas>(s_r + s * S::kRBytes, &map_r, k * int(kSliceBytes), r0, bar);
-          load_box<kCtas>(s_c + s * S::kCBytes, &map_c, k * int(kSliceBytes), c0, bar);
-          load_box<kCtas>(s_rs + s * S::kRScale, &map_rs, 0, rs0 + k * S::kAtoms, bar);
+        const uint32_t bar = barrier_of_first<kCtas>(&full[s]), e = elected();
+        if (first) expect_bytes(e, &full[s], kCtas * S::kStageBytes);
+        load_box<kCtas>(e, s_r + s * S::kRBytes, &map_r, k * int(kSliceBytes), r0, bar);
+        load_box<kCtas>(e, s_c + s * S::kCBytes, &map_c, k * int(kSliceBytes), c0, bar);
+        load_box<kCtas>(e, s_rs + s * S::kRScale, &map_rs, 0, rs0 + k * S::kAtoms, bar);
 #pragma unroll
-          for (int t = 0; t < S::kColTiles; ++t)
-            load_box<kCtas>(s_cs + s * S::kCScale + t * S::kAtoms * 512, &map_cs, 0, cs0 + t * atoms + k * S::kAtoms,
-                            bar);
-        }
-        __syncwarp();
+        for (int t = 0; t < S::kColTiles; ++t)
+          load_box<kCtas>(e, s_cs + s * S::kCScale + t * S::kAtoms * 512, &map_cs, 0, cs0 + t * atoms + k * S::kAtoms, bar);
       }
     }
     // After a failure, the copies in flight get a bounded time to land (they
@@ -264,39 +244,33 @@ __device__ __forceinline__ void tc_body(const CUtensorMap& map_r, const CUtensor
           const uint32_t s = it % S::kStages;
           if (!dev::mbar_wait_abortable(&full[s], (it / S::kStages) & 1u, limit, s_abort)) fail();
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (dev::elect_one()) {
-            if (!*s_abort) {
-              const uint32_t sr = tmem + S::kScaleBase + s * S::kScaleCols, scl = sr + 4 * S::kAtoms;
-              const uint64_t drs = scale_desc(dev::smem_addr(s_rs + s * S::kRScale));
-              const uint64_t dcs = scale_desc(dev::smem_addr(s_cs + s * S::kCScale));
+          const uint32_t e = elected();
+          const uint32_t sr = tmem + S::kScaleBase + s * S::kScaleCols, scl = sr + 4 * S::kAtoms;
+          const uint64_t drs = scale_desc(dev::smem_addr(s_rs + s * S::kRScale));
+          const uint64_t dcs = scale_desc(dev::smem_addr(s_cs + s * S::kCScale));
 #pragma unroll
-              for (int a = 0; a < S::kAtoms; ++a) {
-                copy_scales<kCtas>(sr + 4 * a, drs + 32 * a);
+          for (int a = 0; a < S::kAtoms; ++a) {
+            copy_scales<kCtas>(e, sr + 4 * a, drs + 32 * a);
 #pragma unroll
-                for (int t = 0; t < S::kColTiles; ++t)
-                  copy_scales<kCtas>(scl + 4 * (a * S::kColTiles + t), dcs + 32 * (t * S::kAtoms + a));
-              }
-              const uint64_t dr = operand_desc(dev::smem_addr(s_r + s * S::kRBytes));
-              const uint64_t dc = operand_desc(dev::smem_addr(s_c + s * S::kCBytes));
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                constexpr int kPer = 4 / S::kAtoms;  // MMAs that share an atom
-                const int a = j / kPer;
-                mma<kFormat, kCtas>(d, dr + 2 * j, dc + 2 * j,
-                                    instr_desc<kFormat>(128 * kCtas, kN, kPer == 2 ? (j & 1) * 2 : 0), sr + 4 * a,
-                                    scl + 4 * a * S::kColTiles + shift, (k != u.kb || j != 0) ? 1u : 0u);
-              }
-            }
-            commit<kCtas>(&empty[s]);
+            for (int t = 0; t < S::kColTiles; ++t)
+              copy_scales<kCtas>(e, scl + 4 * (a * S::kColTiles + t), dcs + 32 * (t * S::kAtoms + a));
           }
-          __syncwarp();
+          const uint64_t dr = operand_desc(dev::smem_addr(s_r + s * S::kRBytes));
+          const uint64_t dc = operand_desc(dev::smem_addr(s_c + s * S::kCBytes));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            constexpr int kPer = 4 / S::kAtoms;  // MMAs that share an atom
+            const int a = j / kPer;
+            mma<kFormat, kCtas>(e, d, dr + 2 * j, dc + 2 * j,
+                                instr_desc<kFormat>(128 * kCtas, kN, kPer == 2 ? (j & 1) * 2 : 0), sr + 4 * a,
+                                scl + 4 * a * S::kColTiles + shift, (k != u.kb || j != 0) ? 1u : 0u);
+          }
+          commit<kCtas>(e, &empty[s]);
         }
-        if (dev::elect_one()) commit<kCtas>(&acc_full[b]);
-        __syncwarp();
+        commit<kCtas>(elected(), &acc_full[b]);
         ++ui;
       }
-      if (dev::elect_one()) commit<kCtas>(drain);
-      __syncwarp();
+      commit<kCtas>(elected(), drain);
       dev::mbar_wait(drain, 0u, limit);
     }
   } else {

@@ -150,33 +150,27 @@ __device__ __forceinline__ uint32_t term_code(float& r, float unit, float inv) {
   return code;
 }
 
-// One block of a row of activations, held by one thread, as kTerms rows of `image`
-// (a block of columns): rows row .. row + kTerms - 1, columns from `col`.
+// Four values of a row of activations, columns col .. col + 3, as kTerms rows of `image` (a
+// block of columns) from `row` on.  A block is kBlock / 4 neighbouring lanes.
 template <int kFormat, int kTerms>
-__device__ __forceinline__ void write_terms(float (&v)[Format<kFormat>::kBlock], uint8_t* image, uint32_t cols,
-                                            uint32_t row, uint32_t col) {
+__device__ __forceinline__ void write_terms(float4 x, uint8_t* image, uint32_t cols, uint32_t row, uint32_t col) {
   constexpr int kBlock = Format<kFormat>::kBlock;
-#pragma unroll 1
+  float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
   for (int j = 0; j < kTerms; ++j, ++row) {
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kBlock; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int s = 1; s < kBlock / 4; s *= 2) top = max(top, __shfl_xor_sync(kFull, top, s));
     float unit;
     const uint32_t byte = term_scale<kFormat>(top, unit);
     const float inv = unit > 0.f ? __fdividef(1.f, unit) : 0.f;
-    uint32_t w[kBlock / 8];
+    uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < kBlock / 8; ++i) {
-      w[i] = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[i] |= term_code(v[8 * i + k], unit, inv) << (4 * k);
-    }
-    uint8_t* at = image + piece_at(row, col >> 5) + (col & 16) / 2;
-    if constexpr (kBlock == 32)
-      *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-    else
-      *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-    image[cols * 128 + scale_at(row, col / kBlock)] = uint8_t(byte);
+    for (int i = 0; i < 4; ++i) w |= term_code(v[i], unit, inv) << (4 * i);
+    *reinterpret_cast<uint16_t*>(image + piece_at(row, col >> 5) + (col & 31) / 2) = uint16_t(w);
+    if (col % kBlock == 0) image[cols * 128 + scale_at(row, col / kBlock)] = uint8_t(byte);
   }
 }
 
@@ -212,50 +206,53 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x7fffffffu) > 0x7f800000u ? 1u : b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ float logit_of(uint32_t key) {
+  return __uint_as_float(key == 1u ? 0x7fffffffu : key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
 // One warp: the `top` largest of one token's logits (equal ones by index) and
 // their softmax weights.  A lane keeps the logits of its experts in registers.
 template <int kPerLane>
 __device__ __forceinline__ void select_top(const float* logits, int experts, int top, int renorm, int lane,
                                            uint16_t* ids, float* weight) {
-  float v[kPerLane];
   uint32_t key[kPerLane];
-  float peak = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const int e = lane + 32 * i;
-    v[i] = e < experts ? __ldcg(logits + e) : -INFINITY;
-    key[i] = e < experts ? order_key(v[i]) : 0u;
+    key[i] = e < experts ? order_key(__ldcg(logits + e)) : 0u;
   }
+  uint32_t first = 0;
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) peak = fmaxf(peak, v[i]);
-  for (int s = 16; s; s >>= 1) peak = fmaxf(peak, __shfl_xor_sync(kFull, peak, s));
+  for (int i = 0; i < kPerLane; ++i) first = max(first, key[i]);
+  first = __reduce_max_sync(kFull, first);
+  const float peak = logit_of(first);
+  float sum = 1.f;
+  if (!renorm) {  // the sum over all experts cancels otherwise
+    sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i)
-    if (lane + 32 * i < experts) sum += expf(v[i] - peak);
-  for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
-  float mine = 0.f;
+    for (int i = 0; i < kPerLane; ++i)
+      if (key[i] != 0) sum += expf(logit_of(key[i]) - peak);
+    for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
+  }
+  uint32_t mine_key = 0;
   int mine_id = 0;
   for (int j = 0; j < top; ++j) {
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) best = max(best, key[i]);
-    const uint32_t peak_key = __reduce_max_sync(kFull, best);
-    int at = kMaxExperts;
+    best = __reduce_max_sync(kFull, best);
+    int id = -1;  // the lowest expert with that logit
 #pragma unroll
-    for (int i = kPerLane - 1; i >= 0; --i)
-      if (key[i] == peak_key) at = lane + 32 * i;
-    const int id = int(__reduce_min_sync(kFull, unsigned(at)));
-    float logit = 0.f;
+    for (int i = 0; i < kPerLane; ++i) {
+      const uint32_t vote = __ballot_sync(kFull, key[i] == best);
+      if (id < 0 && vote != 0) id = 32 * i + __ffs(int(vote)) - 1;
+    }
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i)
-      if (lane + 32 * i == id) {
-        key[i] = 0;
-        logit = v[i];
-      }
-    logit = __shfl_sync(kFull, logit, id & 31);
-    if (lane == j) mine = logit, mine_id = id;
+      if (lane + 32 * i == id) key[i] = 0;
+    if (lane == j) mine_key = best, mine_id = id;
   }
-  mine = lane < top ? expf(mine - peak) / sum : 0.f;
+  float mine = lane < top ? expf(logit_of(mine_key) - peak) / sum : 0.f;
   if (renorm) {
     float total = mine;
     for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(kFull, total, s);
@@ -548,15 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
         int e = 0;
         if (sm.top != 0 && sm.top < 0x7f800000u) e = max(min(10 - (int(sm.top >> 23) - 127), 126), -126);
         const float scale = pow2f(e);
-        for (int b = threadIdx.x; b < d_steps * (256 / kBlock); b += kThreads) {
-          float v[kBlock];
-#pragma unroll
-          for (int i = 0; i < kBlock; i += 4) {
-            const float4 q = load4(xt, b * kBlock + i, d, vec_x);
-            v[i] = q.x * scale, v[i + 1] = q.y * scale, v[i + 2] = q.z * scale, v[i + 3] = q.w * scale;
-          }
-          const uint32_t at = uint32_t(b) * kBlock;
-          write_terms<kFormat, kTerms>(v, args.x_image + int64_t(at >> 8) * col_bytes, cols, uint32_t(t * kTerms), at & 255u);
+        for (int k = threadIdx.x * 4; k < d_steps * 256; k += kThreads * 4) {
+          float4 v = load4(xt, k, d, vec_x);
+          v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+          write_terms<kFormat, kTerms>(v, args.x_image + int64_t(k >> 8) * col_bytes, cols, uint32_t(t * kTerms),
+                                       uint32_t(k) & 255u);
         }
         if (t == tokens - 1) {  // columns beyond the tokens' are zero
           const uint32_t spare = cols - uint32_t(tokens * kTerms);
@@ -590,6 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   // ---- selection, the same in every CTA
   if (ok && warp < tokens) {
     const float* l = args.logits + warp * experts;
+    const float norm = __ldcg(args.x_norm + warp);
+    const int exponent = __ldcg(args.x_exp + warp);
     if (experts <= 64)
       select_top<2>(l, experts, top, args.renormalize, lane, sm.ids[warp], sm.weight[warp]);
     else if (experts <= 256)
@@ -606,9 +601,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     }
     for (int s = 16; s; s >>= 1) bound = fmaxf(bound, __shfl_xor_sync(kFull, bound, s));
     if (lane == 0) {
-      const float e = floorf(11.3f - bound - 2.f * __ldcg(args.x_norm + warp));
+      const float e = floorf(11.3f - bound - 2.f * norm);
       sm.h_exp[warp] = e >= -126.f && e <= 126.f ? int(e) : e > 126.f ? 126 : e < -126.f ? -126 : 0;
-      sm.x_exp[warp] = __ldcg(args.x_exp + warp);
+      sm.x_exp[warp] = exponent;
     }
     if (cta == 0 && lane < top) {
       if (args.ids) args.ids[warp * top + lane] = sm.ids[warp][lane];
@@ -642,9 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
 
   // ---- phases 2 and 3
   const int f_tiles = (f + 63) / 64, d_tiles = (d + 127) / 128;
-  const Runs up(used * f_tiles, d_steps, ctas), down(used > 0 ? d_tiles : 0, max(used * f_steps, 1), ctas);
+  const Runs up(used * f_tiles, d_steps, ctas);
   const int up_begin = up.start(cta), up_end = up.start(cta + 1);
-  const int down_begin = down.start(cta), down_end = down.start(cta + 1);
   At put, got;             // of the producer and of the MMA thread
   uint32_t runs_done = 0;  // accumulators handed over so far (MMA thread and epilogue)
 
@@ -749,28 +743,34 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
           for (int c0 = cta + 1; c0 <= c_last; c0 += 4) {
             uint64_t w[4][4];
             const uint64_t* from = shares + int64_t(c0) * 2 * (kMoeTokens * 128) + k0 * 128 + row_local;
+            uint32_t missing = 0;
+            uint64_t t0 = 0;
+            for (uint32_t tries = 0;; ++tries) {
+              missing = 0;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (tries == 0 || uint32_t(w[c][k] >> 32) == 0)
+                    w[c][k] = c0 + c <= c_last && k0 + k < n
+                                  ? peek_share(from + int64_t(c) * 2 * (kMoeTokens * 128) + k * 128)
+                                  : uint64_t(1) << 32;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) missing += uint32_t(w[c][k] >> 32) == 0 ? 1u : 0u;
+              if (missing == 0) break;
+              if (tries == 0) t0 = dev::global_timer_ns();
+              if (sm.abort || (tries % 32 == 31 && dev::global_timer_ns() - t0 > limit)) {
+                fail();
+                break;
+              }
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                w[c][k] = c0 + c <= c_last && k0 + k < n ? peek_share(from + int64_t(c) * 2 * (kMoeTokens * 128) + k * 128)
-                                                         : uint64_t(1) << 32;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (uint32_t(w[c][k] >> 32) == 0) {
-                  const uint64_t t0 = dev::global_timer_ns();
-                  do {
-                    w[c][k] = peek_share(from + int64_t(c) * 2 * (kMoeTokens * 128) + k * 128);
-                    if (sm.abort || dev::global_timer_ns() - t0 > limit) {
-                      fail();
-                      break;
-                    }
-                  } while (uint32_t(w[c][k] >> 32) == 0);
-                }
-                v[k] += __uint_as_float(uint32_t(w[c][k]));
-              }
+                if (c0 + c <= c_last && k0 + k < n) v[k] += __uint_as_float(uint32_t(w[c][k]));
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -844,6 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       produce(up_begin, up_end, weights, columns);
     }
     ahead = 0;
+    const Runs down(used > 0 ? d_tiles : 0, max(used * f_steps, 1), ctas);
+    const int down_begin = down.start(cta), down_end = down.start(cta + 1);
     if (down_begin < down_end) {
       const int tile = down_begin / down.steps, i = down_begin - tile * down.steps, a = i / f_steps;
       down_weights.tile = tile;
@@ -887,6 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     fence_proxy_async_all();
   }
   __syncwarp();
+  const Runs down(used > 0 ? d_tiles : 0, max(used * f_steps, 1), ctas);
+  const int down_begin = down.start(cta), down_end = down.start(cta + 1);
   if (ok && !grid_barrier(args.counters + 1, args, &sm.flag)) ok = false;
   if (!ok) sm.abort = 1;
 

@@ -479,7 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     const bool vec_x = (reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T))) == 0 && args.ldx % 4 == 0;
     const bool vec_r = (reinterpret_cast<uintptr_t>(args.router) & 15u) == 0 && args.ldr % 4 == 0;
     const int share = kWarps / tokens;  // warps to a token
-    for (int item = cta; item < experts + tokens; item += ctas) {
+    // CTAs to a token's terms, of those that the experts leave: each finds the token's
+    // largest value and writes its part of the columns.  One more item: the spare columns.
+    const int slices = max(min((ctas - experts - 1) / tokens, 4), 1);
+    const int items = experts + tokens * slices + 1;
+    for (int item = cta; item < items; item += ctas) {
       if (item < experts) {
         const float* r = args.router + item * args.ldr;
         float sum = 0.f;
@@ -521,8 +525,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
           args.logits[threadIdx.x * experts + item] = total;
         }
         __syncthreads();
+      } else if (item == items - 1) {
+        const uint32_t spare = cols - uint32_t(tokens * kTerms);  // columns beyond the tokens' are zero
+        for (int s = warp; spare != 0 && s < d_steps; s += kWarps) {
+          uint8_t* image = args.x_image + int64_t(s) * col_bytes;
+          for (uint32_t i = uint32_t(lane); i < spare * 8; i += 32) {
+            const uint32_t row = uint32_t(tokens * kTerms) + (i >> 3), piece = i & 7;
+            *reinterpret_cast<uint4*>(image + piece_at(row, piece)) = make_uint4(0u, 0u, 0u, 0u);
+            if (piece < B::kAtoms) *reinterpret_cast<uint32_t*>(image + cols * 128 + scale_at(row, piece * 4)) = 0u;
+          }
+        }
+        fence_proxy_async_all();
       } else {
-        const int t = item - experts;
+        const int t = (item - experts) / slices, slice = (item - experts) - t * slices;
         const T* xt = x + t * args.ldx;
         if (threadIdx.x == 0) sm.top = 0;
         __syncthreads();
@@ -545,22 +560,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
         int e = 0;
         if (sm.top != 0 && sm.top < 0x7f800000u) e = max(min(10 - (int(sm.top >> 23) - 127), 126), -126);
         const float scale = pow2f(e);
-        for (int k = threadIdx.x * 4; k < d_steps * 256; k += kThreads * 4) {
+        const int width = (d_steps + slices - 1) / slices * 256, stop = min((slice + 1) * width, d_steps * 256);
+        for (int k = slice * width + threadIdx.x * 4; k < stop; k += kThreads * 4) {
           float4 v = load4(xt, k, d, vec_x);
           v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
           write_terms<kFormat, kTerms>(v, args.x_image + int64_t(k >> 8) * col_bytes, cols, uint32_t(t * kTerms),
                                        uint32_t(k) & 255u);
         }
-        if (t == tokens - 1) {  // columns beyond the tokens' are zero
-          const uint32_t spare = cols - uint32_t(tokens * kTerms);
-          for (uint32_t i = threadIdx.x; i < spare * 8 * uint32_t(d_steps); i += kThreads) {
-            const uint32_t s = i / (spare * 8), row = uint32_t(tokens * kTerms) + i / 8 % spare, piece = i & 7;
-            uint8_t* image = args.x_image + int64_t(s) * col_bytes;
-            *reinterpret_cast<uint4*>(image + piece_at(row, piece)) = make_uint4(0u, 0u, 0u, 0u);
-            if (piece < B::kAtoms) *reinterpret_cast<uint32_t*>(image + cols * 128 + scale_at(row, piece * 4)) = 0u;
-          }
-        }
-        if (warp == 0) {
+        if (warp == kWarps - 1 && slice == 0) {
           float total = lane < kWarps ? sm.norm[lane] : 0.f;
           for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(kFull, total, s);
           if (lane == 0) {

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <array>
+#include <cmath>
 #include <cstdint>
 #include <map>
 #include <mutex>
@@ -90,28 +91,57 @@ struct Product {
   gb300::Sched sc;
   int grid;
   size_t partial_bytes;
+  double us;  // estimated time, launch aside
 };
 
-// Whole tiles fill complete waves of `units`; the tiles of the last, partial
-// wave are cut over K in shares of at least `least` slices if `split`.
-bool plan_tiles(int64_t rows, int64_t cols, int64_t K, gb300::Fp4TcShape shape, int units, int least, bool split,
-                Product* p) {
+// Time (us) of a 256-column step of K of one tile, of what a tile adds to its
+// steps, and of joining tiles that are split over K.  Fitted to GB300 timings from
+// 512 x 512 x 8192 to 8192^3; the joins are what a forced split cost beyond the
+// steps that it saved (1024 x 1024 x 16384: 17.9 us split, 16.1 us whole; 20 x 8192 x
+// 8192: 13.0 and 10.8; pairs of CTAs, 4096^3: 50 and 35, so pairs never split).  One
+// CTA adds up a tile's shares, one after another (100 x 128 x 40000 in 152: 118 us).
+struct ShapeCost {
+  double step, tile, join, share;
+};
+ShapeCost shape_cost(gb300::Fp4TcShape s) {
+  switch (s) {
+    case gb300::kFp4Pair: return {0.37, 1.5, 0.0, 0.0};
+    case gb300::kFp4Single128: return {0.225, 0.4, 9.0, 0.7};
+    default: return {0.2, 0.3, 6.0, 0.25};
+  }
+}
+
+// Tiles go to `units` CTAs (pairs) in waves.  If that is estimated to be faster, those of
+// the last, partial wave are cut over K in equal shares, one to a unit, but no more
+// than balance the steps that a share saves with what adding it costs.
+bool plan_tiles(int64_t rows, int64_t cols, int64_t K, gb300::Fp4TcShape shape, int units, Product* p) {
   const gb300::Fp4TcTile t = gb300::fp4_tc_tile(shape);
   const int64_t tm = (rows + t.rows - 1) / t.rows, tn = (cols + t.cols - 1) / t.cols, tiles = tm * tn;
-  if (tiles > 0x7fffffffLL) return false;
+  if (tiles > 0x7fffffffLL || units <= 0) return false;
+  const ShapeCost c = shape_cost(shape);
+  const int64_t steps = (K + 255) / 256, waves = (tiles + units - 1) / units, rest = tiles % units;
   p->shape = shape;
   p->sc = gb300::Sched{};
   p->sc.tiles_m = int32_t(tm);
   p->sc.tiles_n = int32_t(tn);
   p->sc.group_m = gb300::kGroupM;
-  p->sc.iters_per_tile = int32_t((K + 255) / 256);
+  p->sc.iters_per_tile = int32_t(steps);
   p->sc.dp_tiles = int32_t(tiles);
   p->grid = int(tiles < units ? tiles : units);
   p->partial_bytes = 0;
-  const int64_t rest = tiles % units, total = rest * p->sc.iters_per_tile;
-  int64_t shares = total / least < units ? total / least : units;
-  if (!split || shares <= rest) return true;
-  if (rest * t.ctas > int64_t(gb300::kWorkspaceCounterBytes / 4)) return true;
+  p->us = double(waves) * (double(steps) * c.step + c.tile);
+  const int64_t total = rest * steps;
+  if (t.ctas != 1 || rest == 0 || rest > int64_t(gb300::kWorkspaceCounterBytes / 4)) return true;
+  const double balance = std::sqrt(double(steps) * c.step / c.share);
+  int64_t shares = int64_t(balance) * rest;
+  if (shares > units) shares = units;
+  if (shares > total) shares = total;
+  if (shares <= rest) return true;
+  const double split_us = double(waves - 1) * (double(steps) * c.step + c.tile) +
+                          double((total + shares - 1) / shares) * c.step + c.tile + c.join +
+                          double(shares) / double(rest) * c.share;
+  if (split_us >= p->us) return true;
+  p->us = split_us;
   p->sc.dp_tiles = int32_t(tiles - rest);
   p->sc.sk_tiles = int32_t(rest);
   p->sc.sk_ctas = int32_t(shares);
@@ -123,15 +153,18 @@ bool plan_tiles(int64_t rows, int64_t cols, int64_t K, gb300::Fp4TcShape shape, 
 }
 
 // Few rows of A: B supplies the tile rows and A the columns, as few as hold
-// them.  Otherwise pairs of CTAs, or single ones where pairs would leave SMs idle.
+// them.  Otherwise pairs of CTAs or single ones, whichever is estimated to be faster.
 bool plan_product(int64_t M, int64_t N, int64_t K, int sms, int pairs, Product* p) {
   if (M <= 64) {
     const gb300::Fp4TcShape s = M <= 16 ? gb300::kFp4Swap16 : M <= 32 ? gb300::kFp4Swap32 : gb300::kFp4Swap64;
-    return plan_tiles(N, M, K, s, sms, 2, true, p);
+    return plan_tiles(N, M, K, s, sms, p);
   }
-  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
-  if (pairs > 0 && tiles >= pairs) return plan_tiles(M, N, K, gb300::kFp4Pair, pairs, 4, true, p);
-  return plan_tiles(M, N, K, gb300::kFp4Single128, sms, 4, true, p);
+  Product single{}, pair{};
+  const bool s = plan_tiles(M, N, K, gb300::kFp4Single128, sms, &single);
+  const bool q = plan_tiles(M, N, K, gb300::kFp4Pair, pairs, &pair);
+  if (!s && !q) return false;
+  *p = !s || (q && pair.us < single.us) ? pair : single;
+  return true;
 }
 
 // The linear layer for few tokens: K over the CTAs of a cluster, a tile of 128

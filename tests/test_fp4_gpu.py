@@ -201,7 +201,7 @@ def check_product(got, a, b, what, exact=False):
 
 PRODUCTS = [(1, 1, 1), (1, 8, 32), (2, 130, 64), (17, 33, 65), (128, 256, 256), (129, 257, 300), (300, 520, 200),
             (256, 256, 512), (33, 4096, 1024), (700, 40, 2049), (512, 768, 1536), (1, 1000, 5000), (16, 640, 4096),
-            (2048, 300, 96)]
+            (2048, 300, 96), (100, 128, 40000), (3, 200, 60000), (2600, 2100, 300)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

@@ -252,7 +252,7 @@ sgemm_status_t zero_output(int dtype, void* C, int64_t rows, int64_t cols, int64
 
 extern "C" {
 
-sgemm_status_t fp4_layout(int format, int64_t rows, int64_t cols, int64_t* ld, int64_t* codes, int64_t* scales) {
+sgemm_status_t fp4_layout(int format, int64_t rows, int64_t cols, int64_t* ld, int64_t* codes, int64_t* scales) try {
   sgemm_status_t st = check_format(format);
   if (st == SGEMM_OK) st = check_extent(rows, cols);
   if (st != SGEMM_OK) return st;
@@ -260,9 +260,11 @@ sgemm_status_t fp4_layout(int format, int64_t rows, int64_t cols, int64_t* ld, i
   if (codes) *codes = rows * code_pitch(cols);
   if (scales) *scales = scale_bytes(format, rows, cols);
   return SGEMM_OK;
+} catch (...) {  // no exception leaves a C entry: only the caches allocate
+  return SGEMM_ERR_ALLOC;
 }
 
-sgemm_status_t fp4_quantize(int dtype, const void* x, int64_t ldx, const fp4_matrix_t* q, cudaStream_t stream) {
+sgemm_status_t fp4_quantize(int dtype, const void* x, int64_t ldx, const fp4_matrix_t* q, cudaStream_t stream) try {
   sgemm_status_t st = check_quantized(q);
   if (st == SGEMM_OK) st = check_dense(dtype, x, q->rows, q->cols, ldx);
   if (st != SGEMM_OK) return st;
@@ -272,10 +274,12 @@ sgemm_status_t fp4_quantize(int dtype, const void* x, int64_t ldx, const fp4_mat
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
   return status_of(gb300::launch_fp4_quantize(dtype, x, ldx, *q, d.sms, stream));
+} catch (...) {  // no exception leaves a C entry: only the caches allocate
+  return SGEMM_ERR_ALLOC;
 }
 
 sgemm_status_t fp4_pack(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales,
-                        const fp4_matrix_t* q, cudaStream_t stream) {
+                        const fp4_matrix_t* q, cudaStream_t stream) try {
   sgemm_status_t st = check_quantized(q);
   if (st != SGEMM_OK) return st;
   LibDevice d;
@@ -291,9 +295,11 @@ sgemm_status_t fp4_pack(const uint8_t* codes, int64_t ld_codes, const uint8_t* s
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
   return status_of(gb300::launch_fp4_pack(codes, ld_codes, scales, ld_scales, *q, d.sms, stream));
+} catch (...) {  // no exception leaves a C entry: only the caches allocate
+  return SGEMM_ERR_ALLOC;
 }
 
-sgemm_status_t fp4_dequantize(const fp4_matrix_t* q, int dtype, void* y, int64_t ldy, cudaStream_t stream) {
+sgemm_status_t fp4_dequantize(const fp4_matrix_t* q, int dtype, void* y, int64_t ldy, cudaStream_t stream) try {
   sgemm_status_t st = check_quantized(q);
   if (st == SGEMM_OK) st = check_dense(dtype, y, q->rows, q->cols, ldy);
   if (st != SGEMM_OK) return st;
@@ -303,10 +309,12 @@ sgemm_status_t fp4_dequantize(const fp4_matrix_t* q, int dtype, void* y, int64_t
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
   return status_of(gb300::launch_fp4_dequantize(*q, dtype, y, ldy, d.sms, stream));
+} catch (...) {  // no exception leaves a C entry: only the caches allocate
+  return SGEMM_ERR_ALLOC;
 }
 
 sgemm_status_t fp4_gemm(const fp4_matrix_t* A, const fp4_matrix_t* B, int dtype, void* C, int64_t ldc,
-                        cudaStream_t stream) {
+                        cudaStream_t stream) try {
   sgemm_status_t st = check_quantized(A);
   if (st == SGEMM_OK) st = check_quantized(B);
   if (st != SGEMM_OK) return st;
@@ -329,10 +337,12 @@ sgemm_status_t fp4_gemm(const fp4_matrix_t* A, const fp4_matrix_t* B, int dtype,
   if (st != SGEMM_OK) return st;
   void* partials = ws ? static_cast<uint8_t*>(ws) + gb300::kWorkspaceCounterBytes : nullptr;
   return run_product(p, *A, *B, dtype, C, ldc, ws, partials, d, stream);
+} catch (...) {  // no exception leaves a C entry: only the caches allocate
+  return SGEMM_ERR_ALLOC;
 }
 
 sgemm_status_t fp4_linear(int dtype, const void* x, int64_t ldx, int64_t M, const float* x_factor,
-                          const fp4_matrix_t* W, void* y, int64_t ldy, cudaStream_t stream) {
+                          const fp4_matrix_t* W, void* y, int64_t ldy, cudaStream_t stream) try {
   sgemm_status_t st = check_quantized(W);
   if (st == SGEMM_OK) st = check_dense(dtype, x, M, W->cols, ldx);
   if (st == SGEMM_OK) st = check_dense(dtype, y, M, W->rows, ldy);
@@ -390,10 +400,12 @@ sgemm_status_t fp4_linear(int dtype, const void* x, int64_t ldx, int64_t M, cons
   q.scales = base + scale_at;
   if (gb300::launch_fp4_quantize(dtype, x, ldx, q, d.sms, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
   return run_product(p, q, *W, dtype, y, ldy, ws, base + gb300::kWorkspaceCounterBytes, d, stream);
+} catch (...) {  // no exception leaves a C entry: only the caches allocate
+  return SGEMM_ERR_ALLOC;
 }
 
 sgemm_status_t fp4_experts_layout(int format, int64_t experts, int64_t d, int64_t f, int64_t* gate_up_bytes,
-                                  int64_t* down_bytes) {
+                                  int64_t* down_bytes) try {
   sgemm_status_t st = check_format(format);
   if (st == SGEMM_OK) st = check_extent(d, f);
   if (st == SGEMM_OK) st = check_extent(experts, 0);
@@ -402,6 +414,8 @@ sgemm_status_t fp4_experts_layout(int format, int64_t experts, int64_t d, int64_
   if (gate_up_bytes) *gate_up_bytes = gb300::fp4_gate_up_bytes(format, experts, d, f);
   if (down_bytes) *down_bytes = gb300::fp4_down_bytes(format, experts, d, f);
   return SGEMM_OK;
+} catch (...) {  // no exception leaves a C entry: only the caches allocate
+  return SGEMM_ERR_ALLOC;
 }
 
 static sgemm_status_t check_experts(const fp4_experts_t* w) {
@@ -416,7 +430,7 @@ static sgemm_status_t check_experts(const fp4_experts_t* w) {
 }
 
 sgemm_status_t fp4_experts_pack(const fp4_matrix_t* gate_up, const fp4_matrix_t* down, const fp4_experts_t* w,
-                                cudaStream_t stream) {
+                                cudaStream_t stream) try {
   sgemm_status_t st = check_quantized(gate_up);
   if (st == SGEMM_OK) st = check_quantized(down);
   if (st == SGEMM_OK) st = check_experts(w);
@@ -428,11 +442,13 @@ sgemm_status_t fp4_experts_pack(const fp4_matrix_t* gate_up, const fp4_matrix_t*
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || w->experts == 0 || w->d == 0 || w->f == 0) return st;
   return status_of(gb300::launch_fp4_experts_pack(*gate_up, *down, *w, stream));
+} catch (...) {  // no exception leaves a C entry: only the caches allocate
+  return SGEMM_ERR_ALLOC;
 }
 
 sgemm_status_t fp4_moe(int dtype, const void* x, int64_t ldx, int64_t M, const float* router, int64_t ldr,
                        const fp4_experts_t* w, int32_t top, int32_t renormalize, void* y, int64_t ldy, int32_t* ids,
-                       float* p, cudaStream_t stream) {
+                       float* p, cudaStream_t stream) try {
   sgemm_status_t st = check_experts(w);
   if (st == SGEMM_OK) st = check_dense(dtype, x, M, w->d, ldx);
   if (st == SGEMM_OK) st = check_dense(FP4_F32, router, w->experts, w->d, ldr);
@@ -496,6 +512,8 @@ sgemm_status_t fp4_moe(int dtype, const void* x, int64_t ldx, int64_t M, const f
     if (gb300::launch_fp4_moe(dtype, w->format, a, d.sms, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
   }
   return SGEMM_OK;
+} catch (...) {  // no exception leaves a C entry: only the caches allocate
+  return SGEMM_ERR_ALLOC;
 }
 
 }  // extern "C"

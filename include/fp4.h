@@ -148,12 +148,14 @@ sgemm_status_t fp4_experts_pack(const fp4_matrix_t *gate_up, const fp4_matrix_t 
  *
  * y is M x d (row stride ldy) of x's type.  ids (int32) and p (32-bit), M x top
  * each and contiguous, are written if not NULL.  1 <= top <= 32, top <=
- * experts <= 1024.  Activations are not quantised; sums and the softmax are
- * in 32 bits.  A 32-bit x and h enter the products as the sum of two 16-bit
- * floats (22 bits of the largest value of the token), a 16-bit x as itself
- * and its h as one (11 bits).  Values that are not finite give results that
- * are not finite, in their token alone.  Meant for few tokens: more than 16
- * are done 16 at a time.
+ * experts <= 1024.  Activations are not quantised to one 4-bit number: x and h
+ * enter the products as sums of 4-bit terms with the format's block scales, each
+ * the quantisation of what the terms before it left: 4 terms for bfloat16, 6 for
+ * 16-bit float, 8 for 32 bits.  What is left is below the types' own rounding
+ * (about 2^-13, 2^-19 and 2^-25 of a block's largest value).  Logits, softmax and sums are
+ * in 32 bits.  Values that are not finite give results that are not finite, in
+ * their token alone.  Meant for few tokens: more than 16 are done 16 at a time.
+ * One kernel on all SMs, launched cooperatively: it waits for the whole GPU.
  */
 sgemm_status_t fp4_moe(int dtype, const void *x, int64_t ldx, int64_t M, const float *router,
                        int64_t ldr, const fp4_experts_t *w, int32_t top, int32_t renormalize,

@@ -298,6 +298,15 @@ def test_linear_non_finite_row(m):
     assert bool(torch.isnan(y[0]).all()) and bool(torch.isfinite(y[1:]).all())
 
 
+@pytest.mark.parametrize("m", [1, 16])
+def test_linear_longer_than_a_cluster_holds(m):
+    """K beyond what one kernel keeps of x in shared memory: quantised first, then multiplied."""
+    w, wv = made(130, 90000, "mxfp4", 8)
+    x = normal(m, 90000, 9, torch.bfloat16, spread=False)
+    codes, scales = ref.quantize(ref.as_numpy(x), "mxfp4")
+    check_product(sg.fp4_linear(x, w), ref.values(codes, scales, "mxfp4"), wv, f"long {m}")
+
+
 def test_no_columns_gives_zeros():
     w = sg.fp4_quantize(torch.zeros(6, 0, device="cuda"), "mxfp4")
     assert bool((sg.fp4_linear(torch.zeros(3, 0, device="cuda"), w) == 0).all())
@@ -372,6 +381,35 @@ def test_layer_strided():
     wy, _, _ = ref.moe(ref.as_numpy(wide[:, 5:105]), ref.as_numpy(router), upv, downv, 2, True)
     assert np.allclose(ref.as_numpy(out[:, 3:103]), wy, rtol=0, atol=1e-5 * np.abs(wy).max())
     assert bool((out[:, :3] == 2).all()) and bool((out[:, 103:] == 2).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_layer_norms_beyond_32_bits(fmt):
+    """Tokens whose squares leave the range of 32 bits (their norm is bounded otherwise) keep their precision."""
+    w, router, upv, downv = layer(6, 128, 64, fmt, 75)
+    x = normal(4, 128, 76, spread=False) * torch.tensor([1e-17, 1e-12, 1.0, 1e16], device="cuda")[:, None]
+    check_layer(x, router * 1e-17, w, upv, downv, 2, True, "norms")
+
+
+def test_matrix_sizes_are_the_librarys():
+    import ctypes
+    from dense_fp32_gemm_03_gb300 import fp4
+    for fmt, number in fp4.FORMATS.items():
+        for rows, cols in ((1, 1), (128, 256), (129, 257), (1000, 5003), (0, 64)):
+            q = sg.Fp4Matrix(rows, cols, fmt)
+            ld, codes, scales = (ctypes.c_int64() for _ in range(3))
+            assert fp4.load().fp4_layout(number, rows, cols, *map(ctypes.byref, (ld, codes, scales))) == 0
+            assert q.codes.shape == (rows, ld.value) and q.codes.numel() == codes.value and q.scales.numel() == scales.value
+
+
+def test_workspaces_may_be_released_between_calls():
+    w, router, _, _ = layer(8, 128, 64, "nvfp4", 77)
+    b, _ = made(300, 512, "nvfp4", 78)
+    x, xm = normal(100, 512, 79, torch.bfloat16, spread=False), normal(3, 128, 80, spread=False)
+    want = sg.fp4_linear(x, b), sg.fp4_moe(xm, router, w, 2)
+    sg.release_workspaces()
+    got = sg.fp4_linear(x, b), sg.fp4_moe(xm, router, w, 2)
+    assert all(torch.equal(g, t) for g, t in zip(got, want))
 
 
 # -------------------------------------------------------- streams and repeats

@@ -2,6 +2,7 @@
 // argument validation, scratch and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <array>
 #include <cmath>
 #include <cstdint>
@@ -94,27 +95,38 @@ struct Product {
   double us;  // estimated time, launch aside
 };
 
-// Time (us) of a 256-column step of K of one tile, of what a tile adds to its
-// steps, and of joining tiles that are split over K.  Fitted to GB300 timings from
-// 512 x 512 x 8192 to 8192^3; the joins are what a forced split cost beyond the
-// steps that it saved (1024 x 1024 x 16384: 17.9 us split, 16.1 us whole; 20 x 8192 x
-// 8192: 13.0 and 10.8; pairs of CTAs, 4096^3: 50 and 35, so pairs never split).  One
-// CTA adds up a tile's shares, one after another (100 x 128 x 40000 in 152: 118 us).
+// Times (us), fitted to GB300 timings from 512 x 512 x 8192 to 8192^3: a 256-column
+// step of K of one tile; what a tile adds to its steps; storing a tile of 32-bit
+// outputs, beside the next tile's steps or after the last; what a launch of pairs
+// adds; joining tiles that are split over K, beyond the steps that it saves (1024 x
+// 1024 x 16384: 17.9 us split, 16.1 us whole; 20 x 8192 x 8192: 13.0 and 10.8; pairs of
+// CTAs, 4096^3: 50 and 35, so pairs never split).  One CTA adds up a tile's shares, one
+// after another (100 x 128 x 40000 in 152: 118 us).
 struct ShapeCost {
-  double step, tile, join, share;
+  double step, tile, store, launch, join, share;
 };
 ShapeCost shape_cost(gb300::Fp4TcShape s) {
   switch (s) {
-    case gb300::kFp4Pair: return {0.37, 1.5, 0.0, 0.0};
-    case gb300::kFp4Single128: return {0.225, 0.4, 9.0, 0.7};
-    default: return {0.2, 0.3, 6.0, 0.25};
+    case gb300::kFp4Pair256: return {0.36, 0.9, 3.4, 0.6, 0.0, 0.0};
+    case gb300::kFp4Pair128: return {0.205, 0.4, 2.6, 0.6, 0.0, 0.0};
+    case gb300::kFp4Single128: return {0.225, 0.4, 2.5, 0.0, 9.0, 0.7};
+    default: return {0.2, 0.3, 0.0, 0.0, 6.0, 0.25};
   }
+}
+
+// Stores of 16-bit outputs, and of rows that TMA does not reach (4096 x 4097 x 1024:
+// 34.8 us in 32 bits, 4096 x 4096 x 1024: 19.6; in 16 bits 22.9 and 16.8).
+double store_cost(bool bytes4, bool tma) { return tma ? (bytes4 ? 1.0 : 0.85) : (bytes4 ? 2.35 : 1.35); }
+
+bool stores_by_tma(const void* C, int64_t ldc, int64_t cols, int64_t es) {
+  return aligned(C, 16) && ldc * es % 16 == 0 && cols * es < (int64_t(1) << 31);
 }
 
 // Tiles go to `units` CTAs (pairs) in waves.  If that is estimated to be faster, those of
 // the last, partial wave are cut over K in equal shares, one to a unit, but no more
 // than balance the steps that a share saves with what adding it costs.
-bool plan_tiles(int64_t rows, int64_t cols, int64_t K, gb300::Fp4TcShape shape, int units, Product* p) {
+bool plan_tiles(int64_t rows, int64_t cols, int64_t K, gb300::Fp4TcShape shape, int units, double stores,
+                Product* p) {
   const gb300::Fp4TcTile t = gb300::fp4_tc_tile(shape);
   const int64_t tm = (rows + t.rows - 1) / t.rows, tn = (cols + t.cols - 1) / t.cols, tiles = tm * tn;
   if (tiles > 0x7fffffffLL || units <= 0) return false;
@@ -129,7 +141,8 @@ bool plan_tiles(int64_t rows, int64_t cols, int64_t K, gb300::Fp4TcShape shape, 
   p->sc.dp_tiles = int32_t(tiles);
   p->grid = int(tiles < units ? tiles : units);
   p->partial_bytes = 0;
-  p->us = double(waves) * (double(steps) * c.step + c.tile);
+  const double store = stores * c.store, whole = std::max(double(steps) * c.step + c.tile, store);
+  p->us = double(waves) * whole + store + c.launch;
   const int64_t total = rest * steps;
   if (t.ctas != 1 || rest == 0 || rest > int64_t(gb300::kWorkspaceCounterBytes / 4)) return true;
   const double balance = std::sqrt(double(steps) * c.step / c.share);
@@ -137,8 +150,8 @@ bool plan_tiles(int64_t rows, int64_t cols, int64_t K, gb300::Fp4TcShape shape, 
   if (shares > units) shares = units;
   if (shares > total) shares = total;
   if (shares <= rest) return true;
-  const double split_us = double(waves - 1) * (double(steps) * c.step + c.tile) +
-                          double((total + shares - 1) / shares) * c.step + c.tile + c.join +
+  const double split_us = double(waves - 1) * whole + double((total + shares - 1) / shares) * c.step + c.tile + store +
+                          c.join +
                           double(shares) / double(rest) * c.share;
   if (split_us >= p->us) return true;
   p->us = split_us;
@@ -153,18 +166,25 @@ bool plan_tiles(int64_t rows, int64_t cols, int64_t K, gb300::Fp4TcShape shape, 
 }
 
 // Few rows of A: B supplies the tile rows and A the columns, as few as hold
-// them.  Otherwise pairs of CTAs or single ones, whichever is estimated to be faster.
-bool plan_product(int64_t M, int64_t N, int64_t K, int sms, int pairs, Product* p) {
+// them.  Otherwise the tiles that are estimated to be fastest: pairs of CTAs share what
+// they read, 256 columns more of it than 128 (8192^3: 166 us, 128 columns 177, single
+// CTAs 213), and smaller tiles fill the last wave better (4096^3: 32.0, 29.2, 32.3) or
+// the only one (1024^3: 7.1, 6.0, 5.2).
+bool plan_product(int64_t M, int64_t N, int64_t K, int sms, int pairs, int64_t es, const void* C, int64_t ldc,
+                  Product* p) {
   if (M <= 64) {
     const gb300::Fp4TcShape s = M <= 16 ? gb300::kFp4Swap16 : M <= 32 ? gb300::kFp4Swap32 : gb300::kFp4Swap64;
-    return plan_tiles(N, M, K, s, sms, p);
+    return plan_tiles(N, M, K, s, sms, 0.0, p);
   }
-  Product single{}, pair{};
-  const bool s = plan_tiles(M, N, K, gb300::kFp4Single128, sms, &single);
-  const bool q = plan_tiles(M, N, K, gb300::kFp4Pair, pairs, &pair);
-  if (!s && !q) return false;
-  *p = !s || (q && pair.us < single.us) ? pair : single;
-  return true;
+  const double stores = store_cost(es == 4, stores_by_tma(C, ldc, N, es));
+  bool any = false;
+  for (const gb300::Fp4TcShape s : {gb300::kFp4Pair256, gb300::kFp4Pair128, gb300::kFp4Single128}) {
+    Product q{};
+    if (!plan_tiles(M, N, K, s, s == gb300::kFp4Single128 ? sms : pairs, stores, &q)) continue;
+    if (!any || q.us < p->us) *p = q;
+    any = true;
+  }
+  return any;
 }
 
 // The linear layer for few tokens: K over the CTAs of a cluster, a tile of 128
@@ -230,7 +250,7 @@ sgemm_status_t run_product(const Product& p, const fp4_matrix_t& A, const fp4_ma
   a.counters = static_cast<int32_t*>(ws);
   a.status = d.status;
   a.wait_limit_ns = d.wait_limit_ns;
-  a.tma_out = !t.swap && aligned(C, 16) && ldc * es % 16 == 0 && Q.rows * es < (int64_t(1) << 31);
+  a.tma_out = !t.swap && stores_by_tma(C, ldc, Q.rows, es);
   a.tma_edge = Q.rows * es % 16 == 0;
   if (st == SGEMM_OK) {
     if (a.tma_out)
@@ -331,7 +351,7 @@ sgemm_status_t fp4_gemm(const fp4_matrix_t* A, const fp4_matrix_t* B, int dtype,
   Product p;
   const int pairs = tc_pairs(d.dev);
   if (pairs < 0) return SGEMM_ERR_LAUNCH;
-  if (!plan_product(A->rows, B->rows, A->cols, d.sms, pairs, &p)) return SGEMM_ERR_UNSUPPORTED;
+  if (!plan_product(A->rows, B->rows, A->cols, d.sms, pairs, dtype_bytes(dtype), C, ldc, &p)) return SGEMM_ERR_UNSUPPORTED;
   void* ws = nullptr;
   if (p.partial_bytes > 0) st = gb300::lib_workspace(d.dev, stream, gb300::kWorkspaceCounterBytes + p.partial_bytes, &ws);
   if (st != SGEMM_OK) return st;
@@ -388,7 +408,7 @@ sgemm_status_t fp4_linear(int dtype, const void* x, int64_t ldx, int64_t M, cons
   Product p;
   const int pairs = tc_pairs(d.dev);
   if (pairs < 0) return SGEMM_ERR_LAUNCH;
-  if (!plan_product(M, W->rows, W->cols, d.sms, pairs, &p)) return SGEMM_ERR_UNSUPPORTED;
+  if (!plan_product(M, W->rows, W->cols, d.sms, pairs, dtype_bytes(dtype), y, ldy, &p)) return SGEMM_ERR_UNSUPPORTED;
   // Scratch: counters, partial sums, the codes and scales of x.
   const size_t code_at = gb300::kWorkspaceCounterBytes + (p.partial_bytes + 255) / 256 * 256;
   const size_t scale_at = code_at + size_t(M * q.ld + 255) / 256 * 256;

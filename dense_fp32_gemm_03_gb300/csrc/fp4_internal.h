@@ -20,7 +20,7 @@ cudaError_t launch_fp4_pack(const uint8_t* codes, int64_t ld_codes, const uint8_
 
 // Products on the tensor cores (fp4_tc.cu): tiles of a row operand by a column
 // operand.  Swapped shapes take B as the row operand.
-enum Fp4TcShape { kFp4Pair, kFp4Single128, kFp4Swap16, kFp4Swap32, kFp4Swap64, kFp4TcShapes };
+enum Fp4TcShape { kFp4Pair256, kFp4Pair128, kFp4Single128, kFp4Swap16, kFp4Swap32, kFp4Swap64, kFp4TcShapes };
 struct Fp4TcTile {
   int rows, cols, ctas;
   bool swap;

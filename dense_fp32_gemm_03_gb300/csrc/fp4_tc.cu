@@ -19,6 +19,16 @@
 //  * the epilogue warps read an accumulator into registers, give it back, and
 //    store it or join it with the other shares of a tile split over K
 //    (published in the workspace, added in CTA order by the last to arrive).
+//
+// What bounds it, measured.  A pair's 256 x 256 tile takes 34.8 KB a 256-column slice
+// into each SM for 4 x 256 x 256 x 64 products, so that 8192^3 (nvfp4 to bf16, 166 us,
+// 6.6 PFLOP/s) runs the tensor pipe 77 % of the time; L2 feeds an SM about 64 bytes a
+// clock meanwhile, which is what a 128 x 128 tile of a single CTA takes for half the
+// products (213 us).  The rest is a tile's accumulator, read before the next tile's
+// first product since two do not fit beside the scales (7 %), and the stores.  A pair's
+// 256 x 128 tile has two accumulators and fills a last wave better (4096^3 29.2 us, 32.0
+// with 256 columns).  A deeper ring is worth more than a second store buffer: one stage
+// less costs 256 x 128 tiles 5 % at 8192^3.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -401,12 +411,20 @@ __device__ __forceinline__ void tc_body(const CUtensorMap& map_r, const CUtensor
               }
             } else {
               __syncwarp();
-              for (int r = 0; r < 32 && row0 + r < args.rows; ++r)
+              // Eight rows' reads before their stores: one row at a time waits out each read.
+#pragma unroll 1
+              for (int r0 = 0; r0 < 32; r0 += 8)
 #pragma unroll
-                for (int e = lane; e < kPer; e += 32)
-                  if (col0 + c + e < args.cols)
-                    out[int64_t(row0 + r) * args.ld + col0 + c + e] =
-                        reinterpret_cast<const T*>(buf + r * 128)[((e / (kPer / 8)) ^ (r & 7)) * (kPer / 8) + e % (kPer / 8)];
+                for (int e = lane; e < kPer; e += 32) {
+                  T t[8];
+#pragma unroll
+                  for (int r = 0; r < 8; ++r)
+                    t[r] = reinterpret_cast<const T*>(buf + (r0 + r) * 128)[((e / (kPer / 8)) ^ r) * (kPer / 8) + e % (kPer / 8)];
+                  T* at = out + int64_t(row0 + r0) * args.ld + col0 + c + e;
+#pragma unroll
+                  for (int r = 0; r < 8; ++r)
+                    if (col0 + c + e < args.cols && row0 + r0 + r < args.rows) at[r * args.ld] = t[r];
+                }
               __syncwarp();
             }
           }
@@ -429,12 +447,12 @@ __device__ __forceinline__ void tc_body(const CUtensorMap& map_r, const CUtensor
   }
 }
 
-template <typename T, int kFormat>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Tile<kFormat, 2, 256>::kThreads, 1)
+template <typename T, int kFormat, int kN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Tile<kFormat, 2, kN>::kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_c,
                 const __grid_constant__ CUtensorMap map_rs, const __grid_constant__ CUtensorMap map_cs,
                 const __grid_constant__ CUtensorMap map_out, const Fp4TcArgs args, const Sched sc) {
-  tc_body<T, kFormat, 2, 256, false>(map_r, map_c, map_rs, map_cs, map_out, args, sc);
+  tc_body<T, kFormat, 2, kN, false>(map_r, map_c, map_rs, map_cs, map_out, args, sc);
 }
 
 template <typename T, int kFormat, int kN, bool kSwap>
@@ -457,8 +475,10 @@ template <typename T, int kFormat>
 Instance instance_t(Fp4TcShape shape) {
   auto single = [](auto* k, size_t smem, int threads) { return Instance{Kernel(k), smem, threads}; };
   using P = Tile<kFormat, 2, 256>;
+  using Q = Tile<kFormat, 2, 128>;
   switch (shape) {
-    case kFp4Pair: return single(pair_kernel<T, kFormat>, P::kSmem, P::kThreads);
+    case kFp4Pair256: return single(pair_kernel<T, kFormat, 256>, P::kSmem, P::kThreads);
+    case kFp4Pair128: return single(pair_kernel<T, kFormat, 128>, Q::kSmem, Q::kThreads);
 #define GB300_FP4_SINGLE(N, SWAP) \
   single(single_kernel<T, kFormat, N, SWAP>, Tile<kFormat, 1, N>::kSmem, Tile<kFormat, 1, N>::kThreads)
     case kFp4Single128: return GB300_FP4_SINGLE(128, false);
@@ -484,7 +504,8 @@ Instance instance(int dtype, int format, Fp4TcShape shape) {
 
 Fp4TcTile fp4_tc_tile(Fp4TcShape shape) {
   switch (shape) {
-    case kFp4Pair: return {256, 256, 2, false};
+    case kFp4Pair256: return {256, 256, 2, false};
+    case kFp4Pair128: return {256, 128, 2, false};
     case kFp4Single128: return {128, 128, 1, false};
     case kFp4Swap16: return {128, 16, 1, true};
     case kFp4Swap32: return {128, 32, 1, true};
@@ -501,7 +522,7 @@ int fp4_tc_prepare() {
         if (cudaFuncSetAttribute(reinterpret_cast<const void*>(in.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(in.smem)) != cudaSuccess)
           return -1;
-        if (shape == kFp4Pair) {
+        if (fp4_tc_tile(Fp4TcShape(shape)).ctas == 2) {
           cudaLaunchConfig_t cfg = {};
           cfg.gridDim = dim3(2, 1, 1);
           cfg.blockDim = dim3(in.threads, 1, 1);

@@ -213,6 +213,16 @@ def test_product(m, n, k, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("m,n,k", [(2000, 2504, 4000), (4100, 3801, 4000), (1400, 3500, 3100), (2500, 3501, 100),
+                                   (2561, 3500, 64)])
+def test_product_of_many_tiles(m, n, k, fmt):
+    """Pairs of CTAs with 128 and with 256 columns a tile, rows that TMA stores and rows that it does not."""
+    (a, av), (b, bv) = made(m, k, fmt, 3), made(n, k, fmt, 4)
+    for dtype in DTYPES:
+        check_product(sg.fp4_gemm(a, b, out_dtype=dtype), av, bv, f"{(m, n, k)} {fmt} {dtype}")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("m,n,k", [(128, 256, 256), (130, 300, 700), (5, 260, 4096), (1024, 512, 1024)])
 def test_integer_products_are_exact(m, n, k, fmt):
     """Codes that stand for integers times powers of two, every block with a scale of its own."""

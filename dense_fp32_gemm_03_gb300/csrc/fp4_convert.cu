@@ -153,6 +153,9 @@ __global__ void __launch_bounds__(kThreads)
                int64_t(gridDim.x) * kWarps);
   Piece<T, kAligned> in;
   if (it.valid()) in.load(x + int64_t(it.r) * ldx, cols, it.piece, lane);
+  // A product of what this kernel writes may set itself up meanwhile; it waits for the
+  // end (linear 17 x 4096 x 4096 bf16 9.2 -> 8.6 us, 1000 x 4096 x 4096 17.4 -> 16.6).
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   while (it.valid()) {
     const int r = it.r, c = it.piece * kPieceCols + lane * kLaneCols;
     float v[kLaneCols];

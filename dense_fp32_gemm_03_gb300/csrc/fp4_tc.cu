@@ -187,6 +187,8 @@ __device__ __forceinline__ void tc_body(const CUtensorMap& map_r, const CUtensor
   if constexpr (kCtas == 2) cluster_sync();  // the peer's barriers exist before anything signals them
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   constexpr uint32_t tmem = kTmemBase;
+  // The matrices may still be on their way from a kernel that let this one start early.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   auto fail = [&]() {
     if (!*s_abort) {
@@ -536,11 +538,20 @@ int fp4_tc_prepare() {
 }
 
 cudaError_t launch_fp4_tc(int dtype, int format, Fp4TcShape shape, const CUtensorMap (&maps)[5],
-                          const Fp4TcArgs& args, const Sched& sc, int grid, cudaStream_t stream) {
+                          const Fp4TcArgs& args, const Sched& sc, int grid, bool early, cudaStream_t stream) {
   const Instance in = instance(dtype, format, shape);
   const int ctas = fp4_tc_tile(shape).ctas;
-  in.kernel<<<grid * ctas, in.threads, in.smem, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4], args, sc);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid * ctas), 1, 1);
+  cfg.blockDim = dim3(unsigned(in.threads), 1, 1);
+  cfg.dynamicSmemBytes = in.smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, in.kernel, maps[0], maps[1], maps[2], maps[3], maps[4], args, sc);
 }
 
 }  // namespace gb300

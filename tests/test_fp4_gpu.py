@@ -509,3 +509,19 @@ def test_refusals():
     for kind, call in bad:
         with pytest.raises(kind):
             call()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_linear_calls_in_a_row_share_scratch(fmt):
+    """Calls of several sizes one after another on one stream: a product reads only its own call's codes of x."""
+    w, _ = made(700, 1000, fmt, 21)
+    xs = [torch.randn(m, 1000, generator=gen(60 + m), device="cuda") for m in (17, 300, 64, 1500, 40, 300, 129)]
+    g = torch.full((1,), 2.0 ** -8, device="cuda") if fmt == "nvfp4" else None
+    want = []
+    for x in xs:
+        want.append(sg.fp4_gemm(sg.fp4_quantize(x, fmt, scale=g), w))
+        torch.cuda.synchronize()
+    for _ in range(5):
+        got = [sg.fp4_linear(x, w, x_scale=g) for x in xs]
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

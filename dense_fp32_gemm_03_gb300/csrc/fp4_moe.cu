@@ -211,46 +211,46 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 }
 
 // One warp: the `top` largest of one token's logits (equal ones by index) and
-// their softmax weights.  A lane keeps the logits of its experts in registers.
-template <int kPerLane>
+// their softmax weights.  A lane keeps the logits of its experts in registers, and
+// its largest at hand: a choice is two reductions over the warp.  chosen() is called with
+// the experts' numbers stored, before the weights, which nobody waits for as long.
+template <int kPerLane, typename Chosen>
 __device__ __forceinline__ void select_top(const float* logits, int experts, int top, int renorm, int lane,
-                                           uint16_t* ids, float* weight) {
+                                           uint16_t* ids, float* weight, Chosen chosen) {
   uint32_t key[kPerLane];
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const int e = lane + 32 * i;
     key[i] = e < experts ? order_key(__ldcg(logits + e)) : 0u;
   }
-  uint32_t first = 0;
+  float exps[kPerLane];
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) first = max(first, key[i]);
-  first = __reduce_max_sync(kFull, first);
-  const float peak = logit_of(first);
+  for (int i = 0; i < kPerLane; ++i) exps[i] = key[i] != 0 ? logit_of(key[i]) : -INFINITY;
+  uint32_t mine_key = 0, peak_key = 0;
+  int mine_id = 0;
+  for (int j = 0; j < top; ++j) {
+    uint32_t most = 0, at = 0;  // the lane's largest, the first of equal ones
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      if (key[i] > most) most = key[i], at = uint32_t(lane + 32 * i);
+    const uint32_t best = __reduce_max_sync(kFull, most);
+    const uint32_t id = __reduce_min_sync(kFull, most == best ? at : ~0u);
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      if (uint32_t(lane + 32 * i) == id) key[i] = 0;
+    if (j == 0) peak_key = best;
+    if (lane == j) mine_key = best, mine_id = int(id);
+  }
+  if (lane < top) ids[lane] = uint16_t(mine_id);
+  chosen(mine_id);
+  const float peak = logit_of(peak_key);
   float sum = 1.f;
   if (!renorm) {  // the sum over all experts cancels otherwise
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i)
-      if (key[i] != 0) sum += expf(logit_of(key[i]) - peak);
+      if (lane + 32 * i < experts) sum += expf(exps[i] - peak);
     for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(kFull, sum, s);
-  }
-  uint32_t mine_key = 0;
-  int mine_id = 0;
-  for (int j = 0; j < top; ++j) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) best = max(best, key[i]);
-    best = __reduce_max_sync(kFull, best);
-    int id = -1;  // the lowest expert with that logit
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const uint32_t vote = __ballot_sync(kFull, key[i] == best);
-      if (id < 0 && vote != 0) id = 32 * i + __ffs(int(vote)) - 1;
-    }
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i)
-      if (lane + 32 * i == id) key[i] = 0;
-    if (lane == j) mine_key = best, mine_id = id;
   }
   float mine = lane < top ? expf(logit_of(mine_key) - peak) / sum : 0.f;
   if (renorm) {
@@ -258,15 +258,13 @@ __device__ __forceinline__ void select_top(const float* logits, int experts, int
     for (int s = 16; s; s >>= 1) total += __shfl_xor_sync(kFull, total, s);
     mine /= total;
   }
-  if (lane < top) {
-    ids[lane] = uint16_t(mine_id);
-    weight[lane] = mine;
-  }
+  if (lane < top) weight[lane] = mine;
 }
 
 // The same for any number of experts, reading the logits again for each choice.
+template <typename Chosen>
 __device__ __forceinline__ void select_top_any(const float* logits, int experts, int top, int renorm, int lane,
-                                               uint16_t* ids, float* weight) {
+                                               uint16_t* ids, float* weight, Chosen chosen) {
   float peak = -INFINITY, sum = 0.f;
   for (int e = lane; e < experts; e += 32) peak = fmaxf(peak, __ldcg(logits + e));
   for (int s = 16; s; s >>= 1) peak = fmaxf(peak, __shfl_xor_sync(kFull, peak, s));
@@ -298,6 +296,7 @@ __device__ __forceinline__ void select_top_any(const float* logits, int experts,
     ids[lane] = uint16_t(mine_id);
     weight[lane] = mine;
   }
+  chosen(mine_id);
 }
 
 // Four consecutive values of a row, zeros beyond `n`.
@@ -587,60 +586,78 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   constexpr uint32_t tmem = kTmemBase;
 
-  // ---- selection, the same in every CTA
-  if (ok && warp < tokens) {
-    const float* l = args.logits + warp * experts;
-    const float norm = __ldcg(args.x_norm + warp);
-    const int exponent = __ldcg(args.x_exp + warp);
-    if (experts <= 64)
-      select_top<2>(l, experts, top, args.renormalize, lane, sm.ids[warp], sm.weight[warp]);
-    else if (experts <= 256)
-      select_top<8>(l, experts, top, args.renormalize, lane, sm.ids[warp], sm.weight[warp]);
-    else
-      select_top_any(l, experts, top, args.renormalize, lane, sm.ids[warp], sm.weight[warp]);
-    __syncwarp();
-    // |h| <= p |gate row| |up row| |x|^2: the power of two that keeps h under 6 times the largest scale.
-    float bound = -INFINITY;
-    if (lane < top) {
-      const int e = sm.ids[warp][lane];
-      bound = log2f(sm.weight[warp][lane]) + sm.bound[e];
-      atomicOr(&sm.mask[e], 1u << warp);
-    }
-    for (int s = 16; s; s >>= 1) bound = fmaxf(bound, __shfl_xor_sync(kFull, bound, s));
-    if (lane == 0) {
-      const float e = floorf(11.3f - bound - 2.f * norm);
-      sm.h_exp[warp] = e >= -126.f && e <= 126.f ? int(e) : e > 126.f ? 126 : e < -126.f ? -126 : 0;
-      sm.x_exp[warp] = exponent;
-    }
-    if (cta == 0 && lane < top) {
-      if (args.ids) args.ids[warp * top + lane] = sm.ids[warp][lane];
-      if (args.p) args.p[warp * top + lane] = sm.weight[warp][lane];
+  // ---- selection, the same in every CTA: the experts' numbers first, which the weights'
+  // copies wait for; the softmax weights and the places of tokens beside the first copies.
+  // A token to a warp from the last one down: with up to 14 tokens the producer and the MMA
+  // warp take none.
+  const int token = kWarps - 1 - warp;
+  if (!ok) {
+    for (int e = threadIdx.x; e < experts; e += kThreads) sm.mask[e] = 0;
+    __syncthreads();
+  } else {
+    if (token < tokens) {
+      const float* l = args.logits + token * experts;
+      const float norm = __ldcg(args.x_norm + token);
+      const int exponent = __ldcg(args.x_exp + token);
+      auto chosen = [&](int e) {
+        if (lane < top) atomicOr(&sm.mask[e], 1u << token);
+        __syncthreads();
+      };
+      uint16_t* ids = sm.ids[token];
+      float* weight = sm.weight[token];
+      if (experts <= 64)
+        select_top<2>(l, experts, top, args.renormalize, lane, ids, weight, chosen);
+      else if (experts <= 128)
+        select_top<4>(l, experts, top, args.renormalize, lane, ids, weight, chosen);
+      else if (experts <= 256)
+        select_top<8>(l, experts, top, args.renormalize, lane, ids, weight, chosen);
+      else
+        select_top_any(l, experts, top, args.renormalize, lane, ids, weight, chosen);
+      __syncwarp();
+      // |h| <= p |gate row| |up row| |x|^2: the power of two that keeps h under 6 times the largest scale.
+      float bound = -INFINITY;
+      if (lane < top) bound = log2f(weight[lane]) + sm.bound[ids[lane]];
+      for (int s = 16; s; s >>= 1) bound = fmaxf(bound, __shfl_xor_sync(kFull, bound, s));
+      if (lane == 0) {
+        const float e = floorf(11.3f - bound - 2.f * norm);
+        sm.h_exp[token] = e >= -126.f && e <= 126.f ? int(e) : e > 126.f ? 126 : e < -126.f ? -126 : 0;
+        sm.x_exp[token] = exponent;
+      }
+      if (cta == 0 && lane < top) {
+        if (args.ids) args.ids[token * top + lane] = ids[lane];
+        if (args.p) args.p[token * top + lane] = weight[lane];
+      }
+    } else {
+      __syncthreads();
     }
   }
-  __syncthreads();
-  if (ok && warp == 0) {  // the experts in use, in order
-    int count = 0;
+  // The experts in use, in order: the producer's warp writes them down, the MMA warp counts.
+  int used = 0;
+  if (warp < 2) {
     for (int e0 = 0; e0 < experts; e0 += 32) {
       const int e = e0 + lane;
       const bool in = e < experts && sm.mask[e] != 0;
       const uint32_t vote = __ballot_sync(kFull, in);
-      const int at = count + __popc(vote & ((1u << lane) - 1u));
-      if (in) {
+      const int at = used + __popc(vote & ((1u << lane) - 1u));
+      if (in && warp == 0) {
         sm.active[at] = uint16_t(e);
         sm.index[e] = uint16_t(at);
       }
-      count += __popc(vote);
+      used += __popc(vote);
     }
-    if (lane == 0) sm.count = count;
+    if (threadIdx.x == 0) sm.count = used;
+    __syncwarp();
+    asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");
+  } else {
+    dev::named_barrier(2, kThreads);
+    used = sm.count;
+    for (int i = threadIdx.x - 64; ok && i < tokens * top; i += kThreads - 64) {
+      const int t = i / top, j = i - t * top, e = sm.ids[t][j], a = sm.index[e];
+      sm.slot[a][t] = uint8_t(j);
+      sm.nth[a][__popc(sm.mask[e] & ((1u << t) - 1u))] = uint8_t(t);
+    }
+    dev::named_barrier(3, kThreads - 64);
   }
-  __syncthreads();
-  const int used = ok ? sm.count : 0;
-  for (int i = threadIdx.x; ok && i < tokens * top; i += kThreads) {
-    const int t = i / top, j = i - t * top, e = sm.ids[t][j], a = sm.index[e];
-    sm.slot[a][t] = uint8_t(j);
-    sm.nth[a][__popc(sm.mask[e] & ((1u << t) - 1u))] = uint8_t(t);
-  }
-  __syncthreads();
 
   // ---- phases 2 and 3
   const int f_tiles = (f + 63) / 64, d_tiles = (d + 127) / 128;

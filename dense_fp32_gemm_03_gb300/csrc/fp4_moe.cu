@@ -684,8 +684,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     load_bytes(elected(), area + slot * stage_bytes + B::kBytes, columns, col_bytes, &sm.full[slot]);
   };
   // Streams the stages [begin, end) of a phase.  weights(at) and columns(at) are called for
-  // consecutive stages.  The first stages' weights, which nothing in this kernel writes,
-  // go ahead of the fence (and of the barrier, by a call of its own) that the columns wait for.
+  // consecutive stages.  Phase 3's first weights, which nothing in this kernel writes, go
+  // ahead of the barrier that the columns wait for.  Elsewhere each stage's columns follow its
+  // weights: after a ring of weights they would arrive last (1 token 17.2 us, not 16.5; a
+  // second warp for them, whose copies queue behind the same weights, 17.2 too).
   int ahead = 0;
   auto produce_ahead = [&](int begin, int end, auto& weights) {
     for (ahead = 0; ahead < int(stages) && begin + ahead < end; ++ahead) {
@@ -864,7 +866,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       UpWeights weights{args.gate_up, sm, per, a, per - (up_begin - a * per),
                         args.gate_up + (int64_t(sm.active[a]) * per + (up_begin - a * per)) * B::kBytes};
       Columns columns{args.x_image, col_bytes, d_steps, up_begin % d_steps};
-      produce_ahead(up_begin, up_end, weights);
       produce(up_begin, up_end, weights, columns);
     }
     ahead = 0;

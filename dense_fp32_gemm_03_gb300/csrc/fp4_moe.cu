@@ -30,6 +30,7 @@ using namespace fp4;
 constexpr int kPackThreads = 256;
 constexpr int kThreads = 512;  // of the layer's kernel, one CTA to an SM
 constexpr int kWarps = kThreads / 32;
+constexpr int kGroups = 3;  // of four warps that join, activate and store
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTop = 32;
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     }
     for (int b = 0; b < 2; ++b) {
       dev::mbar_init(&sm.acc_full[b], 1);
-      dev::mbar_init(&sm.acc_empty[b], 4);
+      dev::mbar_init(&sm.acc_empty[b], 4 * kGroups);
     }
     dev::mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -745,7 +746,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   };
   // The epilogue of one phase: value(unit, k, v) takes this lane's row of the finished sum of a
   // unit's k-th token, of count(unit), whose columns are token(unit, k)'s; then done(unit, n).
-  const int q = warp & 3, row_local = 32 * q + lane, etid = threadIdx.x - 64;
+  // The groups of four warps take four tokens each in turn: one group alone waits for one
+  // token's shares after another's (16 tokens 148 us).
+  const int q = warp & 3, group = (warp - 2) >> 2, row_local = 32 * q + lane, etid = threadIdx.x - 64;
   auto join = [&](const Runs& runs, int begin, int end, uint64_t* shares, auto count, auto token, auto value, auto done) {
     int unit = begin < end ? begin / runs.steps : 0;
     for (int at = begin; at < end; ++unit) {
@@ -758,10 +761,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       const int n = count(unit);
       if (at != unit_at) {  // begun by another CTA: this is a share (each CTA has one such run at most)
         uint64_t* mine = shares + int64_t(cta) * 2 * (kMoeTokens * 128) + row_local;
-        for (int k = 0; k < n; ++k) put_share(mine + k * 128, read_terms<kTerms>(taddr + token(unit, k) * kTerms), 1u);
+        for (int k = group; k < n; k += kGroups)
+          put_share(mine + k * 128, read_terms<kTerms>(taddr + token(unit, k) * kTerms), 1u);
       } else {
         const int c_last = stop == unit_end ? cta : runs.owner(unit_end - 1);
-        for (int k0 = 0; k0 < n; k0 += 4) {
+        for (int k0 = 4 * group; k0 < n; k0 += 4 * kGroups) {
           float v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[k] = k0 + k < n ? read_terms<kTerms>(taddr + token(unit, k0 + k) * kTerms) : 0.f;
@@ -881,18 +885,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     }
   } else if (warp == 1) {
     multiply(up, up_begin, up_end);
-  } else if (warp >= 2 && warp < 6) {
+  } else if (warp < 2 + 4 * kGroups) {
     const float factor = args.gate_up_factor ? __ldg(args.gate_up_factor) : 1.f;
     join(
         up, up_begin, up_end, args.share, [&](int unit) { return __popc(uint32_t(sm.mask[sm.active[unit / f_tiles]])); },
         [&](int unit, int k) { return int(sm.nth[unit / f_tiles][k]); },
         [&](int, int k, float v) { sm.gate_up[k][row_local] = v; },
         [&](int unit, int n) {
-          dev::named_barrier(1, 128);
+          dev::named_barrier(1, 128 * kGroups);
           const int a = unit / f_tiles, tile = unit - a * f_tiles;
           uint8_t* image = args.h_image + (int64_t(a) * f_steps + tile / 4) * col_bytes;
           const uint32_t col = uint32_t(tile % 4) * 64, half = uint32_t(q & 1);
-          for (int k = q >> 1; k < n; k += 2) {
+          for (int k = 2 * group + (q >> 1); k < n; k += 2 * kGroups) {
             const int t = sm.nth[a][k];
             const float u = factor * pow2f(-sm.x_exp[t]);
             const float g = sm.gate_up[k][32 * half + lane] * u, up_value = sm.gate_up[k][64 + 32 * half + lane] * u;
@@ -901,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
           }
           // Zeros in the other columns, and beyond f up to the stage's end.
           const uint32_t end = tile == f_tiles - 1 ? 256 : col + 64;
-          for (uint32_t row = uint32_t(etid); row < cols; row += 128) {
+          for (uint32_t row = uint32_t(etid); row < cols; row += 128 * kGroups) {
             const int t = int(row) / kTerms;
             const bool taken = t < tokens && sm.slot[a][t] != 255;
             for (uint32_t c = taken ? col + 64 : col; c < end; c += 32) {
@@ -909,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
               for (uint32_t i = 0; i < 32 / kBlock; ++i) image[cols * 128 + scale_at(row, c / kBlock + i)] = 0;
             }
           }
-          dev::named_barrier(1, 128);  // sm.gate_up may be written again
+          dev::named_barrier(1, 128 * kGroups);  // sm.gate_up may be written again
         });
     fence_proxy_async_all();
   }
@@ -929,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     multiply(down, down_begin, down_end);
     commit<1>(elected(), &sm.drain);
     dev::mbar_wait(&sm.drain, 0u, limit);
-  } else if (warp >= 2 && warp < 6) {
+  } else if (warp < 2 + 4 * kGroups) {
     const float factor = args.down_factor ? __ldg(args.down_factor) : 1.f;
     join(
         down, down_begin, down_end, args.share + kMoeTokens * 128, [&](int) { return tokens; }, [&](int, int k) { return k; },

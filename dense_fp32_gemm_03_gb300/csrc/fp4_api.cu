@@ -80,6 +80,16 @@ bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 std::mutex g_mu;
 std::map<int, int> g_pairs;  // CTA pairs that run at once, by device
 
+// The experts' kernels, prepared once a device.
+std::map<int, bool> g_moe;
+
+bool moe_ready(int dev) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  auto it = g_moe.find(dev);
+  if (it == g_moe.end()) it = g_moe.emplace(dev, gb300::fp4_moe_prepare()).first;
+  return it->second;
+}
+
 int tc_pairs(int dev) {
   std::lock_guard<std::mutex> lock(g_mu);
   auto it = g_pairs.find(dev);
@@ -488,6 +498,7 @@ sgemm_status_t fp4_moe(int dtype, const void* x, int64_t ldx, int64_t M, const f
   LibDevice d;
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || M == 0) return st;
+  if (!moe_ready(d.dev)) return SGEMM_ERR_LAUNCH;
   const int64_t most = M < gb300::kMoeTokens ? M : gb300::kMoeTokens;
   const int64_t used = w->experts < most * top ? w->experts : most * top;
   // Stage counts of a phase are 32-bit numbers.

@@ -112,6 +112,7 @@ struct MoeScratch {
 };
 MoeScratch fp4_moe_scratch(int dtype, int format, int64_t tokens, int64_t experts, int64_t d, int64_t f, int64_t top,
                            int sms);
+bool fp4_moe_prepare();  // the kernels' attributes on the current device
 cudaError_t launch_fp4_moe(int dtype, int format, const MoeArgs& args, int sms, cudaStream_t stream);
 
 }  // namespace gb300

@@ -14,6 +14,10 @@
 //
 // Roles: warp 0 streams W, warp 1 issues the MMAs, warps 2 to 5 join and store,
 // the others quantise x.
+//
+// What bounds it, measured.  1 x 4096 x 4096 (nvfp4, bf16; 9.4 MB) takes 5.5 to 6.2 us, of which
+// the bytes are 1.4: launch, quantising x beside the first copies, one round to memory, the
+// cluster's sum.  16 x 8192 x 8192 (mxfp4; 36 MB) takes 11.5 to 12.2 us, the bytes 5.3.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -234,10 +234,8 @@ bool plan_linear(int64_t M, int64_t N, int64_t K, int dev, Clusters* c) {
 }
 
 // C = A B^T with the plan's partial sums at `partials` (after the counters at `ws`).
-// `early`: the kernel before on the stream is the quantisation of A, whose end the
-// product waits for by itself.
 sgemm_status_t run_product(const Product& p, const fp4_matrix_t& A, const fp4_matrix_t& B, int dtype, void* C,
-                           int64_t ldc, void* ws, void* partials, bool early, const LibDevice& d, cudaStream_t stream) {
+                           int64_t ldc, void* ws, void* partials, const LibDevice& d, cudaStream_t stream) {
   const gb300::Fp4TcTile t = gb300::fp4_tc_tile(p.shape);
   const fp4_matrix_t& R = t.swap ? B : A;
   const fp4_matrix_t& Q = t.swap ? A : B;
@@ -271,7 +269,7 @@ sgemm_status_t run_product(const Product& p, const fp4_matrix_t& A, const fp4_ma
       maps[4] = maps[0];  // not used
   }
   if (st != SGEMM_OK) return st;
-  return status_of(gb300::launch_fp4_tc(dtype, A.format, p.shape, maps, a, p.sc, p.grid, early, stream));
+  return status_of(gb300::launch_fp4_tc(dtype, A.format, p.shape, maps, a, p.sc, p.grid, stream));
 }
 
 // C = 0 for an empty sum.
@@ -368,7 +366,7 @@ sgemm_status_t fp4_gemm(const fp4_matrix_t* A, const fp4_matrix_t* B, int dtype,
   if (p.partial_bytes > 0) st = gb300::lib_workspace(d.dev, stream, gb300::kWorkspaceCounterBytes + p.partial_bytes, &ws);
   if (st != SGEMM_OK) return st;
   void* partials = ws ? static_cast<uint8_t*>(ws) + gb300::kWorkspaceCounterBytes : nullptr;
-  return run_product(p, *A, *B, dtype, C, ldc, ws, partials, false, d, stream);
+  return run_product(p, *A, *B, dtype, C, ldc, ws, partials, d, stream);
 } catch (...) {  // no exception leaves a C entry: only the caches allocate
   return SGEMM_ERR_ALLOC;
 }
@@ -431,7 +429,7 @@ sgemm_status_t fp4_linear(int dtype, const void* x, int64_t ldx, int64_t M, cons
   q.codes = base + code_at;
   q.scales = base + scale_at;
   if (gb300::launch_fp4_quantize(dtype, x, ldx, q, d.sms, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-  return run_product(p, q, *W, dtype, y, ldy, ws, base + gb300::kWorkspaceCounterBytes, true, d, stream);
+  return run_product(p, q, *W, dtype, y, ldy, ws, base + gb300::kWorkspaceCounterBytes, d, stream);
 } catch (...) {  // no exception leaves a C entry: only the caches allocate
   return SGEMM_ERR_ALLOC;
 }

@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kThreads)
   using F = Format<kFormat>;
   constexpr int kLanes = F::kBlock / kLaneCols;  // lanes of a block
   const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Quantizer<kFormat> quantizer(factor);
   const int code_cols = (cols + 31) / 32 * 32, scale_cols = (cols + 255) / 256 * 256;
   const int64_t atoms = int64_t(scale_cols / F::kAtom);
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(kThreads)
   using F = Format<kFormat>;
   constexpr int kV = 16 / int(sizeof(T)), kParts = 256 / (32 * kV);  // values of a lane and part
   const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const float g = kFormat == FP4_NVFP4 && factor != nullptr ? __ldg(factor) : 1.f;
   const int64_t atoms = int64_t(pieces) * F::kAtomsPerStage;
   PieceIter it(rows, pieces, int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5), int64_t(gridDim.x) * kWarps);
@@ -330,21 +332,36 @@ bool vector_ok(const void* p, int64_t ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % int64_t(16 / sizeof(T)) == 0;
 }
 
+// A kernel that may start beside the end of the one before on the stream and waits for it by itself
+// (16 x 4096 quantised and read back in a graph: 3.6 us in order, 2.8 so).
+template <typename... P>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, cudaStream_t stream, P... params) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, params...);
+}
+
 template <typename T, int kFormat>
 cudaError_t quantize_t(const void* x, int64_t ldx, const fp4_matrix_t& q, int pieces, int sms,
                        cudaStream_t stream) {
   auto* kernel = vector_ok<T>(x, ldx) ? quantize_kernel<T, kFormat, true> : quantize_kernel<T, kFormat, false>;
-  kernel<<<grid_of(q.rows, pieces, sms), kThreads, 0, stream>>>(static_cast<const T*>(x), ldx, q.factor, int(q.rows),
-                                                                int(q.cols), q.codes, q.ld, q.scales);
-  return cudaGetLastError();
+  return launch_early(kernel, grid_of(q.rows, pieces, sms), stream, static_cast<const T*>(x), ldx,
+                      static_cast<const float*>(q.factor), int(q.rows), int(q.cols), q.codes, q.ld, q.scales);
 }
 
 template <typename T, int kFormat>
 cudaError_t dequantize_t(const fp4_matrix_t& q, void* y, int64_t ldy, int pieces, int sms, cudaStream_t stream) {
   auto* kernel = vector_ok<T>(y, ldy) ? dequantize_kernel<T, kFormat, true> : dequantize_kernel<T, kFormat, false>;
-  kernel<<<grid_of(q.rows, pieces, sms), kThreads, 0, stream>>>(q.codes, q.ld, q.scales, q.factor, int(q.rows),
-                                                           int(q.cols), pieces, static_cast<T*>(y), ldy);
-  return cudaGetLastError();
+  return launch_early(kernel, grid_of(q.rows, pieces, sms), stream, static_cast<const uint8_t*>(q.codes), q.ld,
+                      static_cast<const uint8_t*>(q.scales), static_cast<const float*>(q.factor), int(q.rows),
+                      int(q.cols), pieces, static_cast<T*>(y), ldy);
 }
 
 }  // namespace

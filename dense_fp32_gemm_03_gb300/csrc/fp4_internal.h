@@ -44,9 +44,9 @@ struct Fp4TcArgs {
 // maps: codes of the row and the column operand (boxes of 128 rows and of the
 // columns that one CTA stages), their scales (boxes of the atoms of 256
 // columns), the output (boxes of 32 rows x 128 bytes).
-// `early`: start beside the kernel before on the stream, once that says so, and wait for its end.
+// The kernel may start beside the end of the one before on the stream, and waits for it by itself.
 cudaError_t launch_fp4_tc(int dtype, int format, Fp4TcShape shape, const CUtensorMap (&maps)[5],
-                          const Fp4TcArgs& args, const Sched& sc, int grid, bool early, cudaStream_t stream);
+                          const Fp4TcArgs& args, const Sched& sc, int grid, cudaStream_t stream);
 
 // The linear layer for few tokens (fp4_linear.cu).
 int fp4_linear_tokens();  // the most

@@ -15,9 +15,9 @@
 // Roles: warp 0 streams W, warp 1 issues the MMAs, warps 2 to 5 join and store,
 // the others quantise x.
 //
-// What bounds it, measured.  1 x 4096 x 4096 (nvfp4, bf16; 9.4 MB) takes 5.5 to 6.2 us, of which
+// What bounds it, measured.  1 x 4096 x 4096 (nvfp4, bf16; 9.4 MB) takes 5.4 to 6.3 us, of which
 // the bytes are 1.4: launch, quantising x beside the first copies, one round to memory, the
-// cluster's sum.  16 x 8192 x 8192 (mxfp4; 36 MB) takes 11.5 to 12.2 us, the bytes 5.3.
+// cluster's sum.  16 x 8192 x 8192 (mxfp4; 36 MB) takes 10.0 to 11.9 us, the bytes 5.3.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -159,11 +159,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     }
     dev::mbar_init_fence();
     __syncwarp();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // The ring's first stages need no other warp: they go out before the CTA's barrier.
     for (uint32_t n = 0; n < stages && int(n) < steps; ++n) {
       load_stage(cluster, int(n), n);
     }
   }
+  // The kernel before on the stream may still run up to here (16 x 8192 x 8192, one call after
+  // another: 12.3 us launched in order, 10.0 so).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // So do the first values of x.
   const int team = (warp - 6) / team_warps, token = (warp - 6) % team_warps * 2 + (lane >> 4), chunk = lane & 15;
   const bool quantises = warp >= 6 && warp - 6 < teams * team_warps, in = quantises && token < tokens;
@@ -382,17 +386,19 @@ Instance instance(int dtype, int format) {
                              : instance_t<__half>(format);
 }
 
-cudaLaunchConfig_t config(const Instance& in, int clusters, int ctas, int quant_warps, cudaLaunchAttribute* attribute) {
-  attribute->id = cudaLaunchAttributeClusterDimension;
-  attribute->val.clusterDim.x = unsigned(ctas);
-  attribute->val.clusterDim.y = 1;
-  attribute->val.clusterDim.z = 1;
+cudaLaunchConfig_t config(const Instance& in, int clusters, int ctas, int quant_warps, cudaLaunchAttribute (&attributes)[2]) {
+  attributes[0].id = cudaLaunchAttributeClusterDimension;
+  attributes[0].val.clusterDim.x = unsigned(ctas);
+  attributes[0].val.clusterDim.y = 1;
+  attributes[0].val.clusterDim.z = 1;
+  attributes[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attributes[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(clusters * ctas), 1, 1);
   cfg.blockDim = dim3(unsigned(32 * (6 + quant_warps)), 1, 1);
   cfg.dynamicSmemBytes = in.smem;
-  cfg.attrs = attribute;
-  cfg.numAttrs = 1;
+  cfg.attrs = attributes;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
@@ -409,8 +415,8 @@ bool fp4_linear_prepare(int (&clusters)[4]) {
       if (cudaFuncSetAttribute(in.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(in.smem)) != cudaSuccess)
         return false;
       for (int i = 0; i < 4; ++i) {
-        cudaLaunchAttribute attribute;
-        const cudaLaunchConfig_t cfg = config(in, 1, 1 << i, kMaxQuantWarps, &attribute);
+        cudaLaunchAttribute attributes[2] = {};
+        const cudaLaunchConfig_t cfg = config(in, 1, 1 << i, kMaxQuantWarps, attributes);
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, in.kernel, &cfg) != cudaSuccess) {
           cudaGetLastError();
@@ -425,11 +431,11 @@ bool fp4_linear_prepare(int (&clusters)[4]) {
 cudaError_t launch_fp4_linear(int dtype, int format, const CUtensorMap& map, const Fp4LinearArgs& args, int clusters,
                               cudaStream_t stream) {
   const Instance in = instance(dtype, format);
-  cudaLaunchAttribute attribute;
+  cudaLaunchAttribute attributes[2] = {};
   // As many teams as there are stages to quantise, up to the most warps: idle warps only delay the start.
   const int team_warps = (args.tokens + 1) / 2, wanted = team_warps * args.per;
   cudaLaunchConfig_t cfg =
-      config(in, clusters, args.ctas, wanted < kMaxQuantWarps ? wanted : kMaxQuantWarps, &attribute);
+      config(in, clusters, args.ctas, wanted < kMaxQuantWarps ? wanted : kMaxQuantWarps, attributes);
   cfg.stream = stream;
   CUtensorMap m = map;
   Fp4LinearArgs a = args;

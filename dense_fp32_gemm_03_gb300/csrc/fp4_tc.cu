@@ -187,7 +187,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap& map_r, const CUtensor
   if constexpr (kCtas == 2) cluster_sync();  // the peer's barriers exist before anything signals them
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   constexpr uint32_t tmem = kTmemBase;
-  // The matrices may still be on their way from a kernel that let this one start early.
+  // The kernel before on the stream may still run up to here (300 x 520 x 200 in a graph 5.0 -> 4.6 us).
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   auto fail = [&]() {
@@ -538,7 +538,7 @@ int fp4_tc_prepare() {
 }
 
 cudaError_t launch_fp4_tc(int dtype, int format, Fp4TcShape shape, const CUtensorMap (&maps)[5],
-                          const Fp4TcArgs& args, const Sched& sc, int grid, bool early, cudaStream_t stream) {
+                          const Fp4TcArgs& args, const Sched& sc, int grid, cudaStream_t stream) {
   const Instance in = instance(dtype, format, shape);
   const int ctas = fp4_tc_tile(shape).ctas;
   cudaLaunchAttribute attr = {};
@@ -550,7 +550,7 @@ cudaError_t launch_fp4_tc(int dtype, int format, Fp4TcShape shape, const CUtenso
   cfg.dynamicSmemBytes = in.smem;
   cfg.stream = stream;
   cfg.attrs = &attr;
-  cfg.numAttrs = early ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, in.kernel, maps[0], maps[1], maps[2], maps[3], maps[4], args, sc);
 }
 

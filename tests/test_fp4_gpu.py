@@ -525,3 +525,57 @@ def test_linear_calls_in_a_row_share_scratch(fmt):
         got = [sg.fp4_linear(x, w, x_scale=g) for x in xs]
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_calls_start_after_what_they_read():
+    """Calls that may start early read what kernels, copies and other streams wrote just before, eager and in a graph."""
+    w = sg.fp4_quantize(torch.randn(256, 512, generator=gen(1), device="cuda"), "mxfp4")
+    src = [torch.randn(m, 512, generator=gen(m), device="cuda") for m in (4, 40, 300)]
+    x = [torch.zeros_like(t) for t in src]
+    other = torch.cuda.Stream()
+
+    def chain(k):
+        main = torch.cuda.current_stream()
+        res = []
+        for a, s in zip(x, src):
+            big = torch.full((1 << 22,), float(k), device="cuda")          # keeps the GPU busy before the copy
+            a.copy_(s * k + 0 * big[0])
+            q = sg.fp4_quantize(a, "mxfp4")
+            other.wait_stream(main)
+            with torch.cuda.stream(other):
+                r = sg.fp4_gemm(q, w)
+                a.mul_(2)
+            main.wait_stream(other)
+            r.record_stream(main)
+            res += [r, sg.fp4_linear(a, w), sg.fp4_dequantize(q, torch.float32)]
+        return res
+
+    def want(k):
+        res = []
+        for s in src:
+            a = s * k
+            q = sg.fp4_quantize(a, "mxfp4")
+            torch.cuda.synchronize()
+            r, v = sg.fp4_gemm(q, w), sg.fp4_dequantize(q, torch.float32)
+            torch.cuda.synchronize()
+            b = a * 2
+            torch.cuda.synchronize()
+            res += [r, sg.fp4_linear(b, w), v]
+            torch.cuda.synchronize()
+        return res
+    for k in (1, 2, 3):
+        for a, b in zip(chain(k), want(k)):
+            assert torch.equal(a, b)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        chain(1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        res = chain(5)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(res, want(5)):
+            assert torch.equal(a, b)

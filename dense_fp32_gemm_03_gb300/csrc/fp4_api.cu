@@ -525,6 +525,8 @@ sgemm_status_t fp4_moe(int dtype, const void* x, int64_t ldx, int64_t M, const f
   a.logits = reinterpret_cast<float*>(base + s.logits);
   a.x_exp = reinterpret_cast<int32_t*>(base + s.x_exp);
   a.x_norm = reinterpret_cast<float*>(base + s.x_norm);
+  a.h_max = reinterpret_cast<uint32_t*>(base + s.h_max);
+  a.h = reinterpret_cast<float*>(base + s.h);
   a.x_image = base + s.x_image;
   a.h_image = base + s.h_image;
   a.share = reinterpret_cast<uint64_t*>(base + s.share);

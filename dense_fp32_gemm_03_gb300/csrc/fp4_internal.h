@@ -99,6 +99,8 @@ struct MoeArgs {
   float* logits;      // tokens x experts
   int32_t* x_exp;     // tokens: x was multiplied by 2^x_exp
   float* x_norm;      // tokens: log2 of x's 2-norm
+  uint32_t* h_max;    // tokens: largest |h|, as bits
+  float* h;           // h in 32 bits: token, place of the expert among its own, f rounded up to 64
   uint8_t* x_image;   // x as terms: a block of columns for each 256 of d
   uint8_t* h_image;   // h as terms: the same for each expert in use and 256 of f
   uint64_t* share;    // shares of units cut between CTAs: CTA x phase (2, 3) x token x row
@@ -107,7 +109,7 @@ struct MoeArgs {
   uint64_t wait_limit_ns;
 };
 struct MoeScratch {
-  size_t logits, x_exp, x_norm, x_image, h_image, share, bytes;  // offsets, and the size of all
+  size_t logits, x_exp, x_norm, h_max, h, x_image, h_image, share, bytes;  // offsets, and the size of all
   int cols;
 };
 MoeScratch fp4_moe_scratch(int dtype, int format, int64_t tokens, int64_t experts, int64_t d, int64_t f, int64_t top,

@@ -8,18 +8,29 @@
 // mma.m16n8k16 form of this kernel ran at a quarter of the bandwidth), so the
 // weights go to the tensor core as they are stored, block-scaled 4-bit, and the
 // activations are brought to the same form without loss that matters: a value is
-// the sum of kTerms terms 4^-j u_j q_j, each the 4-bit quantisation of what the
-// terms before it left (times 4, so that an 8-bit scale can follow).  A term takes off
-// a factor of 6 or more in the worst case and about 8 in the mean.  With 4
-// terms (bfloat16) the rest is about 2^-13 of the block's largest value, with 6
-// (16-bit float) 2^-19 and with 8 (32 bits) 2^-25: below the rounding of the
-// types, in the mean.  A token and term is one column of the product, and the
-// columns' 32-bit sums are added with their powers of 4 at the end.
+// the sum of kTerms terms 8^-j u_j q_j, each the 4-bit quantisation of what the
+// terms before it left, times 8: a term takes off a factor of about 8 in the mean, so
+// that the units stay where they began (at least 5.6 for nvfp4 and 5 for mxfp4, so a
+// block grows by 1.42 or 1.6 a term at most).  With 4 terms (bfloat16) the rest is
+// about 2^-13 of the block's largest value in the mean and 2^-10 at most, with 6 (16-bit
+// float) 2^-19 and 2^-16, with 8 (32 bits) 2^-25 and 2^-22.  A token and term is one column of the product, and the
+// columns' 32-bit sums are added with their powers of 8 at the end.
+//
+// nvfp4's units reach from 2^-6 to 448 at full precision (2^-9 at less), so each token's
+// x and h are brought near the top of that by a power of two first: blocks of 2^-10 of
+// the token's largest value and more keep the precision above, smaller ones lose bits
+// that lie 8^-kTerms 2^-14 below that value (h: 2^-6).  For h the largest
+// value is known only after phase 2, so its power of two is a guess from the norms of the
+// weights and of x, which is checked: phase 2 also keeps h in 32 bits and finds each
+// token's largest value, the barrier behind it carries one bit a token that says whether
+// some value was high enough and one for too high, and tokens whose guess was off are
+// written again with the measured power of two (a pass over h and a barrier: 4 us with 1
+// token of 64 experts of 2048 x 768, 10 with 16 of 4096 x 2048).
 //
 // What bounds it, measured.  16 tokens (nvfp4, 64 experts of 4096 x 2048, top 8: 800 MB of
-// weights) take 141 us, 5.7 TB/s; about 10 us of that are the start, the two grid barriers
+// weights) take 142 us, 5.6 TB/s; about 10 us of that are the start, the two grid barriers
 // and the last sums, between which nothing streams.  One token (64 of 2048 x 768: 22 MB) takes
-// 15.2 us, a chain of latencies: the router (3 us), a barrier (1), the selection (1), the first
+// 15.7 us, a chain of latencies: the router (3 us), a barrier (1), the selection (1), the first
 // weights' round to memory, sums and h (5), a barrier (1), the second products and sums (4).
 #include <cuda_runtime.h>
 
@@ -56,6 +67,20 @@ struct Terms<__half> {
   static constexpr int kCount = 6;
 };
 static_assert(kMoeTokens * 8 <= 128, "columns of one product");
+constexpr float kStep = 8.f;  // from one term to the next
+
+// Exponents of a token's largest value once it is scaled: x's is kHigh - 1; h's is aimed at
+// kAim and taken from kLow on below kHigh.  nvfp4: the block may grow 1.42 times a term and
+// stays below 6 * 448 (2^7 1.42^7 = 1490, 2^8 1.42^5 = 1478); from 2^kLow down there are three
+// octaves to the smallest unit of full precision.  mxfp4's units have all exponents.
+template <int kFormat, int kTerms>
+struct Window {
+  static constexpr int kHigh = kTerms == 8 ? 7 : 8, kAim = 5, kLow = 0;
+};
+template <int kTerms>
+struct Window<FP4_MXFP4, kTerms> {
+  static constexpr int kHigh = 90, kAim = 5, kLow = -60;
+};
 
 // ------------------------------------------------------------------ packing
 // One thread moves one 16-byte piece of codes, and the first threads of a row
@@ -150,10 +175,10 @@ __device__ __forceinline__ uint32_t term_scale(uint32_t top, float& unit) {
   }
 }
 
-// The code of r / unit; r becomes what the term leaves, times 4.
+// The code of r / unit; r becomes what the term leaves, times kStep.
 __device__ __forceinline__ uint32_t term_code(float& r, float unit, float inv) {
   const uint32_t code = encode2(r * inv, 0.f) & 15u;
-  r = fmaf(-__low2float(decode2<0>(code)), unit, r) * 4.f;
+  r = fmaf(-__low2float(decode2<0>(code)), unit, r) * kStep;
   return code;
 }
 
@@ -344,26 +369,38 @@ struct Four<float> {
 };
 
 // ------------------------------------------------------------- grid barrier
-// All CTAs are resident (cooperative launch).  Every thread returns the same
-// answer: false once the bounded wait ran out.
-__device__ __forceinline__ bool grid_barrier(int32_t* counter, const MoeArgs& args, int* s_ok) {
+// All CTAs are resident (cooperative launch).  `word` counts the CTAs in its low half and
+// takes up the flags that they bring in its high half: flags() is called by the whole first
+// warp once the CTA's threads have met, and answer[1] becomes all CTAs' flags together.
+// Every thread returns the same answer: false once the bounded wait ran out.
+template <typename Flags>
+__device__ __forceinline__ bool grid_barrier(uint64_t* word, const MoeArgs& args, uint32_t* answer, Flags flags) {
   __syncthreads();
-  if (threadIdx.x == 0) {
-    // The release covers the CTA's writes, which the barrier above ordered before it.
-    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter) : "memory");
-    int ok = 1;
-    const uint64_t t0 = dev::global_timer_ns();
-    while (dev::ld_acquire_gpu(counter) < int(gridDim.x)) {
-      if (dev::global_timer_ns() - t0 > args.wait_limit_ns) {
-        dev::record_status(args.status, kStatusTimeout, kWaitTileStage);
-        ok = 0;
-        break;
+  if (threadIdx.x < 32) {
+    const uint32_t mine = flags();
+    __syncwarp();
+    if (threadIdx.x == 0) {
+      if (mine != 0) asm volatile("red.relaxed.gpu.global.or.b64 [%0], %1;" ::"l"(word), "l"(uint64_t(mine) << 32) : "memory");
+      // The release covers the CTA's writes, which the barrier above ordered before it.
+      asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(word), "l"(uint64_t(1)) : "memory");
+      uint32_t ok = 1;
+      uint64_t seen;
+      const uint64_t t0 = dev::global_timer_ns();
+      for (;;) {
+        asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(seen) : "l"(word) : "memory");
+        if (uint32_t(seen) >= gridDim.x) break;
+        if (dev::global_timer_ns() - t0 > args.wait_limit_ns) {
+          dev::record_status(args.status, kStatusTimeout, kWaitTileStage);
+          ok = 0;
+          break;
+        }
       }
+      answer[0] = ok;
+      answer[1] = uint32_t(seen >> 32);
     }
-    *s_ok = ok;
   }
   __syncthreads();
-  return *s_ok != 0;
+  return answer[0] != 0;
 }
 
 // -------------------------------------------------------------------- layer
@@ -400,8 +437,9 @@ struct Smem {
   float bound[kMaxExperts];             // log2 of MoeArgs::bound
   uint16_t index[kMaxExperts];          // place of an expert among those in use
   uint16_t active[kMaxPairs];           // experts in use, in order
-  uint32_t tmem, top;
-  int count, flag;
+  uint32_t h_max[kMoeTokens];           // largest |h| of this CTA's, as bits; infinity where h is known to be 0
+  uint32_t tmem, top, flag[2];
+  int count;
   volatile int abort;
 };
 constexpr int kStageArea = kSmemBytes - 1024 - int((sizeof(Smem) + 127) / 128 * 128);
@@ -409,19 +447,16 @@ constexpr int kStageArea = kSmemBytes - 1024 - int((sizeof(Smem) + 127) / 128 * 
 // This lane's row of kTerms columns of tensor memory, as one value.
 template <int kTerms>
 __device__ __forceinline__ float read_terms(uint32_t taddr) {
+  static_assert(kTerms <= 8 && (kMoeTokens - 1) * kTerms + 8 <= 128, "columns of an accumulator");
   float v[8];
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  if constexpr (kTerms == 4)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr));
-  else
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
   float sum = v[kTerms - 1];
 #pragma unroll
-  for (int j = kTerms - 2; j >= 0; --j) sum = fmaf(sum, 0.25f, v[j]);
+  for (int j = kTerms - 2; j >= 0; --j) sum = fmaf(sum, 1.f / kStep, v[j]);
   return sum;
 }
 
@@ -429,7 +464,8 @@ __device__ __forceinline__ float read_terms(uint32_t taddr) {
 //  1. Router: a CTA to an expert computes the logits of all tokens; a CTA to a
 //     token turns x into terms.
 //  2. Every CTA selects the experts (the same way).  Units are (expert in use,
-//     64 values of h); a stage is 256 columns of x.
+//     64 values of h); a stage is 256 columns of x.  Where h's powers of two were guessed
+//     wrong, its terms are written again, behind one barrier more.
 //  3. Units are 128 rows of y; the stages run over all experts in use, h of a token
 //     that does not go to one being zero there.
 // In phases 2 and 3 one thread streams stages (weights and columns, one bulk copy
@@ -439,12 +475,15 @@ template <typename T, int kFormat>
 __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   using B = Block<kFormat>;
   constexpr int kTerms = Terms<T>::kCount, kBlock = Format<kFormat>::kBlock;
+  using W = Window<kFormat, kTerms>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* area = smem_raw + ((1024u - (dev::smem_addr(smem_raw) & 1023u)) & 1023u);
   Smem& sm = *reinterpret_cast<Smem*>(area + kStageArea);
   const int warp = uniform_warp(), lane = threadIdx.x & 31, cta = blockIdx.x, ctas = gridDim.x;
   const int tokens = args.tokens, experts = args.experts, top = args.top, d = args.d, f = args.f;
   const int d_steps = (d + 255) / 256, f_steps = (f + 255) / 256;
+  const int f_tiles = (f + 63) / 64, d_tiles = (d + 127) / 128;
+  uint64_t* words = reinterpret_cast<uint64_t*>(args.counters);  // of the grid barriers
   const uint32_t cols = uint32_t(args.cols), col_bytes = cols * 128 + B::kScales;
   const uint32_t stage_bytes = B::kBytes + col_bytes;
   const uint32_t stages = min(uint32_t(kStageArea) / stage_bytes, uint32_t(kMaxStages));
@@ -474,6 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     for (int e = threadIdx.x; e < experts; e += kThreads) {
       sm.mask[e] = 0;
       sm.bound[e] = log2f(__uint_as_float(__ldg(args.bound + e)));
+    }
+    if (threadIdx.x < kMoeTokens) {
+      sm.h_max[threadIdx.x] = 0;
+      if (cta == 0) args.h_max[threadIdx.x] = 0;
     }
     for (int i = threadIdx.x; i < kMaxPairs; i += kThreads)
       *reinterpret_cast<uint4*>(sm.slot[i]) = make_uint4(~0u, ~0u, ~0u, ~0u);
@@ -562,9 +605,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
           sm.norm[warp] = square;
         }
         __syncthreads();
-        // x 2^e has its largest magnitude in [2^10, 2^11), under 6 times the largest scale.
+        // x 2^e has its largest magnitude in [2^(kHigh - 1), 2^kHigh).
+        constexpr int kTop = kFormat == FP4_NVFP4 ? W::kHigh - 1 : W::kAim;
         int e = 0;
-        if (sm.top != 0 && sm.top < 0x7f800000u) e = max(min(10 - (int(sm.top >> 23) - 127), 126), -126);
+        if (sm.top != 0 && sm.top < 0x7f800000u) e = max(min(kTop - (int(sm.top >> 23) - 127), 126), -126);
         const float scale = pow2f(e);
         const int width = (d_steps + slices - 1) / slices * 256, stop = min((slice + 1) * width, d_steps * 256);
         for (int k = slice * width + threadIdx.x * 4; k < stop; k += kThreads * 4) {
@@ -589,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  bool ok = grid_barrier(args.counters, args, &sm.flag);
+  bool ok = grid_barrier(words, args, sm.flag, [] { return 0u; });
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   constexpr uint32_t tmem = kTmemBase;
 
@@ -621,13 +665,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       else
         select_top_any(l, experts, top, args.renormalize, lane, ids, weight, chosen);
       __syncwarp();
-      // |h| <= p |gate row| |up row| |x|^2: the power of two that keeps h under 6 times the largest scale.
+      // |h| <= p |gate row| |up row| |x|^2.  Where the rows and x have nothing to do with one another
+      // each product is about that over sqrt(d), and the largest of them eight times the usual h.
       float bound = -INFINITY;
       if (lane < top) bound = log2f(weight[lane]) + sm.bound[ids[lane]];
       for (int s = 16; s; s >>= 1) bound = fmaxf(bound, __shfl_xor_sync(kFull, bound, s));
       if (lane == 0) {
-        const float e = floorf(11.3f - bound - 2.f * norm);
+        bound += 2.f * norm;
+        const float e = floorf(float(W::kAim) - 3.f - bound + log2f(float(d)));
         sm.h_exp[token] = e >= -126.f && e <= 126.f ? int(e) : e > 126.f ? 126 : e < -126.f ? -126 : 0;
+        if (bound == -INFINITY) sm.h_max[token] = 0x7f800000u;
         sm.x_exp[token] = exponent;
       }
       if (cta == 0 && lane < top) {
@@ -667,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   }
 
   // ---- phases 2 and 3
-  const int f_tiles = (f + 63) / 64, d_tiles = (d + 127) / 128;
   const Runs up(used * f_tiles, d_steps, ctas);
   const int up_begin = up.start(cta), up_end = up.start(cta + 1);
   At put, got;             // of the producer and of the MMA thread
@@ -895,7 +941,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
             const int t = sm.nth[a][k];
             const float u = factor * pow2f(-sm.x_exp[t]);
             const float g = sm.gate_up[k][32 * half + lane] * u, up_value = sm.gate_up[k][64 + 32 * half + lane] * u;
-            const float h = g / (1.f + expf(-g)) * up_value * sm.weight[t][sm.slot[a][t]];
+            const int place = sm.slot[a][t];
+            const float h = g / (1.f + expf(-g)) * up_value * sm.weight[t][place];
+            const uint32_t most = __reduce_max_sync(kFull, __float_as_uint(h) & 0x7fffffffu);
+            if (lane == 0) atomicMax(&sm.h_max[t], most);
+            args.h[int64_t(t * top + place) * (f_tiles * 64) + tile * 64 + 32 * half + lane] = h;
             write_terms_warp<kFormat, kTerms>(h * pow2f(sm.h_exp[t]), image, cols, uint32_t(t * kTerms), col + 32 * half, lane);
           }
           // Zeros in the other columns, and beyond f up to the stage's end.
@@ -915,7 +965,46 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   __syncwarp();
   const Runs down(used > 0 ? d_tiles : 0, max(used * f_steps, 1), ctas);
   const int down_begin = down.start(cta), down_end = down.start(cta + 1);
-  if (ok && !grid_barrier(args.counters + 1, args, &sm.flag)) ok = false;
+  // One bit a token: some |h| reached the window (or there is nothing to check); 16 bits up: it passed it.
+  auto h_flags = [&]() {
+    bool seen = false, over = false;
+    if (lane < tokens) {
+      const uint32_t most = sm.h_max[lane];
+      const int exponent = int(most >> 23) - 127 + sm.h_exp[lane];
+      if (most != 0) asm volatile("red.relaxed.gpu.global.max.u32 [%0], %1;" ::"l"(args.h_max + lane), "r"(most) : "memory");
+      seen = most >= 0x7f800000u || (most != 0 && exponent >= W::kLow);
+      over = most < 0x7f800000u && exponent >= W::kHigh;
+    }
+    return __ballot_sync(kFull, seen) | __ballot_sync(kFull, over) << 16;
+  };
+  if (ok && !grid_barrier(words + 1, args, sm.flag, h_flags)) ok = false;
+  const uint32_t off = ok ? (~sm.flag[1] | sm.flag[1] >> 16) & ((1u << tokens) - 1u) : 0u;
+  if (off != 0) {
+    // The same in every CTA: h's terms again, with the tokens' largest values in [2^(kHigh - 1), 2^kHigh).
+    if (threadIdx.x < tokens && (off >> threadIdx.x & 1u) != 0) {
+      const uint32_t most = __ldcg(args.h_max + threadIdx.x);
+      constexpr int kTop = kFormat == FP4_NVFP4 ? W::kHigh - 1 : W::kAim;
+      sm.h_exp[threadIdx.x] =
+          most != 0 && most < 0x7f800000u ? max(min(kTop - (int(most >> 23) - 127), 126), -126) : 0;
+    }
+    __syncthreads();
+    const int chunks = f_tiles * 2;  // of 32 values
+    const int64_t items = int64_t(tokens * top) * chunks;
+    const int64_t stride = int64_t(ctas) * kWarps;
+    int64_t i = int64_t(cta) * kWarps + warp;
+    float ahead_h = i < items ? __ldcg(args.h + i * 32 + lane) : 0.f;  // on its way during the arithmetic
+    for (; i < items; i += stride) {
+      const int pair = int(i / chunks), chunk = int(i - int64_t(pair) * chunks), t = pair / top;
+      const float h = ahead_h;
+      if (i + stride < items) ahead_h = __ldcg(args.h + (i + stride) * 32 + lane);
+      if ((off >> t & 1u) == 0) continue;
+      const int a = sm.index[sm.ids[t][pair - t * top]];
+      write_terms_warp<kFormat, kTerms>(h * pow2f(sm.h_exp[t]), args.h_image + (int64_t(a) * f_steps + chunk / 8) * col_bytes,
+                                        cols, uint32_t(t * kTerms), uint32_t(chunk % 8) * 32, lane);
+    }
+    fence_proxy_async_all();
+    ok = grid_barrier(words + 2, args, sm.flag, [] { return 0u; });
+  }
   if (!ok) sm.abort = 1;
 
   // Phase 3.
@@ -951,10 +1040,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
   // The last CTA to leave clears the barriers' counters for the next call.
-  if (threadIdx.x == 0 && atomicAdd(args.counters + 2, 1) == ctas - 1) {
-    args.counters[0] = 0;
-    args.counters[1] = 0;
-    args.counters[2] = 0;
+  if (threadIdx.x == 0 && atomicAdd(args.counters + 6, 1) == ctas - 1) {
+    words[0] = words[1] = words[2] = 0;
+    args.counters[6] = 0;
   }
 }
 
@@ -1007,6 +1095,8 @@ MoeScratch fp4_moe_scratch(int dtype, int format, int64_t tokens, int64_t expert
   s.logits = take(tokens * experts * 4);
   s.x_exp = take(tokens * 4);
   s.x_norm = take(tokens * 4);
+  s.h_max = take(kMoeTokens * 4);
+  s.h = take(tokens * top * ((f + 63) / 64) * 64 * 4);
   s.x_image = take((d + 255) / 256 * col_bytes);
   s.h_image = take(used * ((f + 255) / 256) * col_bytes);
   s.share = take(int64_t(sms) * 2 * kMoeTokens * 128 * 8);

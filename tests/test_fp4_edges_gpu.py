@@ -1,0 +1,96 @@
+"""GPU tests of the 4-bit operators where their arithmetic is hardest: values far from usual, non-finite weights, streams.
+
+Tolerances, derived from the definitions in ``include/fp4.h``:
+
+* the experts' layer keeps x and h to 2^-25 (32 bits), 2^-19 (float16) or 2^-13 (bfloat16) of a block's largest value in the
+  mean; a block's largest value is about twice its root mean square, and x enters twice, h once, so y is within 2e-7,
+  1e-5 or 6e-4 in the 2-norm, and below that where the blocks' largest values are the usual ones.  Its 32-bit sums are
+  off by a few 2^-24 of their partial sums, which a pre-activation g away from zero turns into a relative error of h of a few |g| 2^-24: 3e-6 at |g| = 16.  So 5e-6 in 32 bits; with a 16-bit output the
+  half unit of the type decides, at most 2^-9 or 2^-12 of a value in the mean, and 2^-8 or 2^-10 leaves room.
+"""
+import numpy as np
+import pytest
+import torch
+
+import dense_fp32_gemm_03_gb300 as sg
+
+import fp4_ref as ref
+from test_fp4_gpu import DTYPES, FORMATS, _built, _status, gen, host_factor   # noqa: F401 (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+
+def stored(x, fmt):
+    """(library matrix, 64-bit values) of a float32 tensor quantised by the plain implementation."""
+    g = (x.abs().amax() / 2688).reshape(1) if fmt == "nvfp4" else None
+    codes, scales = ref.quantize(x.cpu().numpy(), fmt, host_factor(g))
+    q = sg.fp4_matrix(torch.from_numpy(ref.packed(codes)).cuda(), torch.from_numpy(scales.astype(np.uint8)).cuda(),
+                      fmt, cols=x.shape[1], scale=g)
+    return q, ref.values(codes, scales, fmt, host_factor(g))
+
+
+# ----------------------------------------------------- precision of the layer
+E, D, F, TOP = 4, 2048, 192, 2
+
+
+def layer_inputs(kind, tokens):
+    """x, router, gate-and-up and down weights whose h lies far from what the norms of x and of the weights suggest."""
+    x = torch.randn(tokens, D, generator=gen(1), device="cuda")
+    up = torch.randn(E, 2 * F, D, generator=gen(2), device="cuda") / D ** 0.5
+    down = torch.randn(E, D, F, generator=gen(3), device="cuda") / F ** 0.5
+    router = torch.randn(E, D, generator=gen(4), device="cuda") / D ** 0.5
+    if kind == "one large row":          # of an expert: its h is large, or next to zero where the gate is negative
+        up[:, 5] *= 30
+        up[:, F + 5] *= 30
+        x[:, :] += 0.5
+        up[:, 5] -= up[:, 5].mean(-1, keepdim=True) + 30 * 0.5 / D ** 0.5
+    elif kind.startswith("gates"):       # pre-activations around a negative number
+        x += 1
+        up[:, :F] -= (up[:, :F].sum(-1, keepdim=True) + float(kind.split()[1])) / D
+    elif kind == "ignored channels":     # large channels that the weights do not look at
+        x[:, 64:96] *= 1000
+        up[:, :, 64:96] = 0
+        router[:, 64:96] = 0
+    elif kind == "aligned":              # x along a row of the weights: h as large as the norms allow
+        x[0] = up[0, 3] * 40
+        up[:, F + 3] = up[:, 3]
+    elif kind == "small":
+        x *= 1e-4
+    elif kind == "tokens apart":         # one token's h says nothing about another's
+        x *= torch.logspace(-6, 1, tokens, device="cuda")[:, None]
+    return x, router, up.reshape(E * 2 * F, D), down.reshape(E * D, F)
+
+
+KINDS = ("normal", "one large row", "gates 6", "gates 12", "gates 16", "ignored channels", "aligned", "small", "tokens apart")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kind", KINDS)
+def test_layer_precision(kind, dtype, fmt):
+    x, router, up, down = layer_inputs(kind, 3)
+    x = x.to(dtype)
+    (qu, uv), (qd, dv) = stored(up, fmt), stored(down, fmt)
+    y, ids, p = sg.fp4_moe(x, router, sg.fp4_experts(qu, qd, E), TOP, return_routing=True)
+    wy, wids, wp = ref.moe(ref.as_numpy(x), ref.as_numpy(router), uv.reshape(E, 2 * F, D), dv.reshape(E, D, F), TOP, True)
+    assert np.array_equal(ids.cpu().numpy(), wids)
+    limit = {torch.float32: 5e-6, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -10}[dtype]
+    got = ref.as_numpy(y)
+    scale = np.linalg.norm(wy, axis=1)
+    if dtype == torch.float16:           # its subnormal numbers are 2^-24 apart
+        scale = np.maximum(scale, 2.0 ** -24 * D ** 0.5 / limit)
+    off = np.linalg.norm(got - wy, axis=1) / scale
+    assert off.max() <= limit, f"{kind}: relative errors {off}"
+
+
+def test_layer_zero_tokens_beside_others():
+    """Tokens without any h (x of zeros: padding) leave the others' precision alone."""
+    x, router, up, down = layer_inputs("gates 12", 5)
+    x[1] = x[4] = 0
+    (qu, uv), (qd, dv) = stored(up, "nvfp4"), stored(down, "nvfp4")
+    y = sg.fp4_moe(x, router, sg.fp4_experts(qu, qd, E), TOP)
+    wy, _, _ = ref.moe(ref.as_numpy(x), ref.as_numpy(router), uv.reshape(E, 2 * F, D), dv.reshape(E, D, F), TOP, True)
+    assert bool((y[1] == 0).all()) and bool((y[4] == 0).all())
+    keep = [0, 2, 3]
+    off = np.linalg.norm(ref.as_numpy(y)[keep] - wy[keep], axis=1) / np.linalg.norm(wy[keep], axis=1)
+    assert off.max() <= 5e-6

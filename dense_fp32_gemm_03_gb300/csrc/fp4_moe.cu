@@ -11,10 +11,12 @@
 // the sum of kTerms terms 8^-j u_j q_j, each the 4-bit quantisation of what the
 // terms before it left, times 8: a term takes off a factor of about 8 in the mean, so
 // that the units stay where they began (at least 5.6 for nvfp4 and 5 for mxfp4, so a
-// block grows by 1.42 or 1.6 a term at most).  With 4 terms (bfloat16) the rest is
-// about 2^-13 of the block's largest value in the mean and 2^-10 at most, with 6 (16-bit
-// float) 2^-19 and 2^-16, with 8 (32 bits) 2^-25 and 2^-22.  A token and term is one column of the product, and the
-// columns' 32-bit sums are added with their powers of 8 at the end.
+// block grows by 1.42 or 1.6 a term at most).  With 5 terms (bfloat16) the rest is
+// about 2^-16 of the block's largest value in the mean and 2^-13 at most, with 6 (16-bit
+// float) 2^-19 and 2^-16, with 8 (32 bits) 2^-25 and 2^-22.  (bfloat16 with 4 terms, 2^-13 in
+// the mean, rounded a few per cent of the outputs the other way: 1 token 15.7 us, 16 tokens
+// 142.1; with 5 16.1 and 143.1, with 6 16.6 and 145.3.)  A token and term is one column of
+// the product, and the columns' 32-bit sums are added with their powers of 8 at the end.
 //
 // nvfp4's units reach from 2^-6 to 448 at full precision (2^-9 at less), so each token's
 // x and h are brought near the top of that by a power of two first: blocks of 2^-10 of
@@ -28,9 +30,9 @@
 // token of 64 experts of 2048 x 768, 10 with 16 of 4096 x 2048).
 //
 // What bounds it, measured.  16 tokens (nvfp4, 64 experts of 4096 x 2048, top 8: 800 MB of
-// weights) take 142 us, 5.6 TB/s; about 10 us of that are the start, the two grid barriers
+// weights) take 143 us, 5.6 TB/s; about 10 us of that are the start, the two grid barriers
 // and the last sums, between which nothing streams.  One token (64 of 2048 x 768: 22 MB) takes
-// 15.7 us, a chain of latencies: the router (3 us), a barrier (1), the selection (1), the first
+// 16.1 us, a chain of latencies: the router (3 us), a barrier (1), the selection (1), the first
 // weights' round to memory, sums and h (5), a barrier (1), the second products and sums (4).
 #include <cuda_runtime.h>
 
@@ -60,7 +62,7 @@ struct Terms {
 };
 template <>
 struct Terms<__nv_bfloat16> {
-  static constexpr int kCount = 4;
+  static constexpr int kCount = 5;
 };
 template <>
 struct Terms<__half> {

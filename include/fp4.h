@@ -150,10 +150,10 @@ sgemm_status_t fp4_experts_pack(const fp4_matrix_t *gate_up, const fp4_matrix_t 
  * each and contiguous, are written if not NULL.  1 <= top <= 32, top <=
  * experts <= 1024.  Activations are not quantised to one 4-bit number: x and h
  * enter the products as sums of 4-bit terms with the format's block scales, each
- * the quantisation of what the terms before it left: 4 terms for bfloat16, 6 for
- * 16-bit float, 8 for 32 bits.  What is left is about 2^-13, 2^-19 and 2^-25 of a
- * block's largest value in the mean and 2^-10, 2^-16 and 2^-22 at most; or, where that
- * is more (FP4_NVFP4, blocks far below the token's largest value of x or h), 2^-18, 2^-24
+ * the quantisation of what the terms before it left: 5 terms for bfloat16, 6 for
+ * 16-bit float, 8 for 32 bits.  What is left is about 2^-16, 2^-19 and 2^-25 of a
+ * block's largest value in the mean and 2^-13, 2^-16 and 2^-22 at most; or, where that
+ * is more (FP4_NVFP4, blocks far below the token's largest value of x or h), 2^-21, 2^-24
  * and 2^-30 of that value.  Logits, softmax and sums are in 32 bits.  Values that
  * are not finite give results that are not finite, in their token alone.  Meant for few tokens: more than 16 are done 16 at a time.
  * One kernel on all SMs, launched cooperatively: it waits for the whole GPU.

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads)
     if (kLanes == 2) a = max_abs(a, __shfl_xor_sync(kFull, a, 1));
     const uint32_t byte = quantizer.scale(a, unit);
     uint32_t word[2];
-    quantizer.encode(v, unit, word);
+    quantizer.encode(v, a, unit, word);
     if (c < code_cols) *reinterpret_cast<uint2*>(codes + int64_t(r) * ld + c / 2) = make_uint2(word[0], word[1]);
     const uint32_t four = join_scales<kLanes>(byte, lane);
     if (lane % (4 * kLanes) == 0 && c < scale_cols)

@@ -120,7 +120,8 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 // quotient x r corrected once by its residual is correctly rounded (Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // 1990) as long as the residual is not subnormal, which holds for units between
-// 2^-100 and 2^100 wherever the quotient is not far below the smallest level.
+// 2^-100 and 2^100 wherever the quotient is not far below the smallest level, and as
+// long as x r does not overflow (infinity less infinity): the callers keep x below.
 __device__ __forceinline__ float quotient(float x, float unit, float r) {
   const float q = x * r;
   return fmaf(fmaf(-q, unit, x), r, q);
@@ -149,14 +150,16 @@ struct Quantizer {
       unit = __uint_as_float(uint32_t(127 - e) << 23);  // 2^-e, at most 2^127
       return top >= 0x7f800000u ? 255u : top == 0 ? 0u : uint32_t(e + 127);
     } else {
-      const float s = plain ? quotient(a, g6, g6_inv) : __fdiv_rn(a, g6);
+      // From 448 * 6 g on the scale is 448 (a / (6 g) may pass the largest number of 32 bits).
+      const float s = !plain ? __fdiv_rn(a, g6) : a < 448.f * g6 ? quotient(a, g6, g6_inv) : 448.f;
       const uint32_t byte = top >= 0x7f800000u ? 127u : top == 0 ? 0u : encode_e4m3(s);
       unit = decode_e4m3(byte) * g;
       return byte;
     }
   }
 
-  __device__ __forceinline__ void encode(float (&v)[16], float unit, uint32_t (&word)[2]) const {
+  // `a` and `unit`: as scale() got and gave them.
+  __device__ __forceinline__ void encode(float (&v)[16], float a, float unit, uint32_t (&word)[2]) const {
     if constexpr (kFormat == FP4_MXFP4) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] *= unit;
@@ -166,6 +169,10 @@ struct Quantizer {
       word[0] = word[1] = 0u;
       if (unit >= 0x1p-100f && unit <= 0x1p100f) {
         const float inv = __frcp_rn(unit);
+        if (a > 16.f * unit) {  // the scale is at its largest; from 6 units on every value has the last code
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = fminf(fmaxf(v[i], -16.f * unit), 16.f * unit);
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = quotient(v[i], unit, inv);
         word[0] = encode8(v);

@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
           if (Format<kFormat>::kBlock == 32) a = max_abs(a, __shfl_xor_sync(kFull, a, 1));
           const uint32_t byte = quantizer.scale(a, unit);
           uint32_t word[2];
-          quantizer.encode(v, unit, word);
+          quantizer.encode(v, a, unit, word);
           if (in) {
             unsigned char* columns = s_x + i * L::kStep;
             *reinterpret_cast<uint2*>(columns + piece_at(uint32_t(token), uint32_t(chunk >> 1)) + (chunk & 1) * 8) =

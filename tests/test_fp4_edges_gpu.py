@@ -18,7 +18,7 @@ import torch
 import dense_fp32_gemm_03_gb300 as sg
 
 import fp4_ref as ref
-from test_fp4_gpu import DTYPES, FORMATS, _built, _status, gen, host_factor   # noqa: F401 (fixtures)
+from test_fp4_gpu import DTYPES, FORMATS, _built, _status, check_product, gen, host_factor   # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,35 @@ def test_layer_zero_tokens_beside_others():
     keep = [0, 2, 3]
     off = np.linalg.norm(ref.as_numpy(y)[keep] - wy[keep], axis=1) / np.linalg.norm(wy[keep], axis=1)
     assert off.max() <= 5e-6
+
+
+# ---------------------------------------------------------------- quantisation
+def huge_beside_small():
+    """Finite blocks with both signs from 1 to the largest numbers of 32 bits."""
+    x = torch.randn(9, 96, generator=gen(11), device="cuda")
+    for i, s in enumerate((1.0, 1e10, 1e20, 1e30, 1e37, 5e37, 5e37, 1e25, 1e5)):
+        x[i, 16:64] *= s
+    x[5, 70], x[5, 71] = 3.4e38, -3.4e38
+    x[6] = 3.4e38 * torch.sign(x[6])
+    return x
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("g", [0.01, 1.0, 1e-12, 2.0 ** -90, 2.0 ** -101, 1e-35, 1e30])
+def test_values_far_above_the_factor_saturate(g, dtype):
+    """a / (6 g) beyond 32 bits: the largest scale, and codes of 6 with the values' signs."""
+    x = huge_beside_small().clamp(-3.3e38, 3.3e38).to(dtype)
+    g = torch.tensor([g], device="cuda")
+    codes, scales, _ = ref.read_codes(sg.fp4_quantize(x, "nvfp4", scale=g))
+    want_codes, want_scales = ref.quantize(ref.as_numpy(x), "nvfp4", g.item())
+    assert want_scales.max() <= 126
+    assert np.array_equal(scales, want_scales) and np.array_equal(codes, want_codes)
+
+
+@pytest.mark.parametrize("m", [2, 100])
+def test_linear_of_values_far_above_the_factor(m):
+    w, wv = stored(torch.randn(70, 96, generator=gen(12), device="cuda"), "nvfp4")
+    x = huge_beside_small()[3:5].repeat(m // 2, 1)
+    g = torch.tensor([2.0 ** -90], device="cuda")
+    codes, scales = ref.quantize(ref.as_numpy(x), "nvfp4", g.item())
+    check_product(sg.fp4_linear(x, w, x_scale=g), ref.values(codes, scales, "nvfp4", g.item()), wv, f"saturated {m}")

@@ -122,9 +122,10 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 // 1990) as long as the residual is not subnormal, which holds for units between
 // 2^-100 and 2^100 wherever the quotient is not far below the smallest level, and as
 // long as x r does not overflow (infinity less infinity): the callers keep x below.
+// The residual is taken as q unit - x: it is +0 where it vanishes, so that a q of -0 stays -0.
 __device__ __forceinline__ float quotient(float x, float unit, float r) {
   const float q = x * r;
-  return fmaf(fmaf(-q, unit, x), r, q);
+  return fmaf(-fmaf(q, unit, -x), r, q);
 }
 
 // Quantisation of a block, 16 of its values at a time (fp4.h has the definition).

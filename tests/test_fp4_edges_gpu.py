@@ -5,8 +5,8 @@ Tolerances, derived from the definitions in ``include/fp4.h``:
 * the experts' layer keeps x and h to 2^-25 (32 bits), 2^-19 (float16) or 2^-16 (bfloat16) of a block's largest value in the
   mean; a block's largest value is about twice its root mean square, and x enters twice, h once, so y is within 2e-7,
   1e-5 or 8e-5 in the 2-norm, and below that where the blocks' largest values are the usual ones.  Its 32-bit sums are
-  off by a few 2^-24 of their partial sums, which a pre-activation g away from zero turns into a relative error of h of a few |g| 2^-24: 3e-6 at |g| = 16.  So 5e-6 in 32 bits; with a 16-bit output the
-  half unit of the type decides, at most 2^-9 or 2^-12 of a value in the mean, and 2^-8 or 2^-10 leaves room;
+  off by a few 2^-24 of their partial sums, which a pre-activation g away from zero turns into a relative error of h of a
+  few |g| 2^-24: 3e-6 at |g| = 16.  So 5e-6 in 32 bits; with a 16-bit output the half unit of the type decides, at most 2^-9 or 2^-12 of a value in the mean, and 2^-8 or 2^-10 leaves room;
 * two results whose inner values differ by 3e-5 (2^-16 in the mean, three times) round to different bfloat16 numbers where a
   rounding boundary lies between them: for 3e-5 / 2^-8 = 0.8 % of the outputs, and a few times that counting the small ones.
   3 % is the limit.
@@ -140,3 +140,24 @@ def test_linear_of_values_far_above_the_factor(m):
     g = torch.tensor([2.0 ** -90], device="cuda")
     codes, scales = ref.quantize(ref.as_numpy(x), "nvfp4", g.item())
     check_product(sg.fp4_linear(x, w, x_scale=g), ref.values(codes, scales, "nvfp4", g.item()), wv, f"saturated {m}")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_zeros_keep_their_sign(dtype, fmt):
+    """-0, and negative values that round to zero, have the code of -0 beside values of any size."""
+    x = torch.randn(6, 64, generator=gen(13), device="cuda")
+    x[:, ::3] = -0.0
+    x[:, 1::6] = 0.0
+    x[0, 5], x[0, 6] = -1e-7, 1e-7
+    x[1, 5] = -1e-40
+    x[2] *= 1e4
+    x[3] *= 1e-4
+    x = x.to(dtype)
+    g = (x.abs().amax().float() / 2688).reshape(1) if fmt == "nvfp4" else None
+    q = sg.fp4_quantize(x, fmt, scale=g)
+    codes, scales, _ = ref.read_codes(q)
+    want_codes, want_scales = ref.quantize(ref.as_numpy(x), fmt, host_factor(g))
+    assert np.array_equal(scales, want_scales) and np.array_equal(codes, want_codes)
+    # (A block whose unit is 0 has zero codes by definition.)
+    assert np.array_equal(torch.signbit(q.dequantize()).cpu().numpy(), want_codes > 7)

@@ -87,9 +87,23 @@ struct Window<FP4_MXFP4, kTerms> {
 // ------------------------------------------------------------------ packing
 // One thread moves one 16-byte piece of codes, and the first threads of a row
 // its scales.  A gate-and-up tile has 64 gate rows and the 64 up rows beside them.
+//
+// The layer multiplies an expert's down weights also by the zeros of tokens that do not go
+// to it, so NaN may not enter that product: a down block whose scale is NaN is kept as
+// scale 0 with every code -0 (which no other block is left with), the expert's bound is
+// marked in its last bit, and the layer looks for such blocks in the rows of marked
+// experts, for the tokens that go to them.
+constexpr uint32_t kHidden = 0x88888888u;  // eight codes of -0
+
+template <int kFormat>
+__device__ __forceinline__ bool nan_scale(uint32_t byte) {
+  return kFormat == FP4_MXFP4 ? byte == 255u : (byte & 127u) == 127u;
+}
+
 template <int kFormat, bool kGateUp>
 __global__ void __launch_bounds__(kPackThreads)
-    pack_experts_kernel(const fp4_matrix_t q, int64_t experts, int64_t rows_per, uint8_t* __restrict__ out) {
+    pack_experts_kernel(const fp4_matrix_t q, int64_t experts, int64_t rows_per, uint8_t* __restrict__ out,
+                        uint32_t* __restrict__ bound) {
   using B = Block<kFormat>;
   const int64_t tiles = kGateUp ? (rows_per + 63) / 64 : (rows_per + 127) / 128;
   const int64_t stages = (q.cols + 255) / 256, atoms = stages * B::kAtoms;
@@ -112,16 +126,60 @@ __global__ void __launch_bounds__(kPackThreads)
     }
     uint8_t* dst = out + block * B::kBytes;
     const int64_t at = s * 128 + piece * 16;
-    *reinterpret_cast<uint4*>(dst + piece_at(r, piece)) =
-        in && at < pitch ? *reinterpret_cast<const uint4*>(q.codes + row * q.ld + at) : make_uint4(0u, 0u, 0u, 0u);
-    if (piece < B::kAtoms)
-      *reinterpret_cast<uint32_t*>(dst + 16384 + scale_at(r, piece * 4)) =
-          in ? *reinterpret_cast<const uint32_t*>(q.scales + scale_offset(row, (s * B::kAtoms + piece) * 4, atoms)) : 0u;
+    uint4 codes = in && at < pitch ? *reinterpret_cast<const uint4*>(q.codes + row * q.ld + at) : make_uint4(0u, 0u, 0u, 0u);
+    if (!kGateUp && in) {
+      constexpr int kBlocks = 32 / Format<kFormat>::kBlock;  // of a piece
+      uint32_t* w = reinterpret_cast<uint32_t*>(&codes);
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        const uint32_t byte = q.scales[scale_offset(row, (s * 8 + piece) * kBlocks + b, atoms)];
+        bool hidden = byte == 0;
+#pragma unroll
+        for (int j = 0; j < 4 / kBlocks; ++j) hidden = hidden && w[b * (4 / kBlocks) + j] == kHidden;
+#pragma unroll
+        for (int j = 0; j < 4 / kBlocks; ++j)
+          if (nan_scale<kFormat>(byte) || hidden) w[b * (4 / kBlocks) + j] = hidden ? 0u : kHidden;
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + piece_at(r, piece)) = codes;
+    if (piece < B::kAtoms) {
+      uint32_t four = in ? *reinterpret_cast<const uint32_t*>(q.scales + scale_offset(row, (s * B::kAtoms + piece) * 4, atoms)) : 0u;
+      if (!kGateUp) {
+        bool any = false;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (nan_scale<kFormat>(four >> (8 * b) & 255u)) any = true, four &= ~(255u << (8 * b));
+        if (any) atomicOr(bound + e, 1u);
+      }
+      *reinterpret_cast<uint32_t*>(dst + 16384 + scale_at(r, piece * 4)) = four;
+    }
   }
 }
 
+// Whether a row of an expert's down weights (one tile's blocks, `steps` of them) holds a hidden NaN.
+template <int kFormat>
+__device__ __noinline__ bool row_is_nan(const uint8_t* blocks, int row, int steps) {
+  using B = Block<kFormat>;
+  constexpr int kBlocks = 32 / Format<kFormat>::kBlock;
+  bool found = false;
+  for (int i = 0; i < steps * 8; ++i) {
+    const uint8_t* block = blocks + int64_t(i >> 3) * B::kBytes;
+    const uint4 codes = __ldg(reinterpret_cast<const uint4*>(block + piece_at(uint32_t(row), uint32_t(i & 7))));
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+      bool hidden = true;
+#pragma unroll
+      for (int j = 0; j < 4 / kBlocks; ++j) hidden = hidden && w[b * (4 / kBlocks) + j] == kHidden;
+      found = found || (hidden && __ldg(block + 16384 + scale_at(uint32_t(row), uint32_t((i & 7) * kBlocks + b))) == 0);
+    }
+  }
+  return found;
+}
+
 // bound[e] = the largest |gate row| |up row| (2-norms, with the factor) of expert e, as
-// bits: with the token's norm it bounds h.  One warp to a pair of rows.
+// bits: with the token's norm it bounds h.  The last bit is left for NaN among the down
+// weights.  One warp to a pair of rows.
 template <int kFormat>
 __global__ void __launch_bounds__(kPackThreads)
     bound_kernel(const fp4_matrix_t q, int64_t experts, int64_t f, uint32_t* __restrict__ bound) {
@@ -147,7 +205,7 @@ __global__ void __launch_bounds__(kPackThreads)
       sum[0] += __shfl_xor_sync(kFull, sum[0], s);
       sum[1] += __shfl_xor_sync(kFull, sum[1], s);
     }
-    if (lane == 0) atomicMax(bound + e, __float_as_uint(sqrtf(sum[0]) * sqrtf(sum[1])));
+    if (lane == 0) atomicMax(bound + e, __float_as_uint(sqrtf(sum[0]) * sqrtf(sum[1])) & ~1u);
   }
 }
 
@@ -436,7 +494,8 @@ struct Smem {
   alignas(16) uint8_t slot[kMaxPairs][kMoeTokens];  // place of an expert in use among a token's, or 255
   uint8_t nth[kMaxPairs][kMoeTokens];               // the tokens of an expert in use
   uint32_t mask[kMaxExperts];           // tokens that go to an expert
-  float bound[kMaxExperts];             // log2 of MoeArgs::bound
+  float bound[kMaxExperts];             // log2 of MoeArgs::bound; last bit: some down weights are NaN
+  uint32_t nan_down[kMoeTokens];        // which of a token's experts have such weights
   uint16_t index[kMaxExperts];          // place of an expert among those in use
   uint16_t active[kMaxPairs];           // experts in use, in order
   uint32_t h_max[kMoeTokens];           // largest |h| of this CTA's, as bits; infinity where h is known to be 0
@@ -514,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   {
     for (int e = threadIdx.x; e < experts; e += kThreads) {
       sm.mask[e] = 0;
-      sm.bound[e] = log2f(__uint_as_float(__ldg(args.bound + e)));
+      const uint32_t b = __ldg(args.bound + e);
+      sm.bound[e] = __uint_as_float((__float_as_uint(log2f(__uint_as_float(b & ~1u))) & ~1u) | (b & 1u));
     }
     if (threadIdx.x < kMoeTokens) {
       sm.h_max[threadIdx.x] = 0;
@@ -669,10 +729,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
       __syncwarp();
       // |h| <= p |gate row| |up row| |x|^2.  Where the rows and x have nothing to do with one another
       // each product is about that over sqrt(d), and the largest of them eight times the usual h.
-      float bound = -INFINITY;
-      if (lane < top) bound = log2f(weight[lane]) + sm.bound[ids[lane]];
+      float bound = lane < top ? sm.bound[ids[lane]] : 0.f;
+      const uint32_t marked = __ballot_sync(kFull, lane < top && (__float_as_uint(bound) & 1u) != 0);
+      bound = lane < top ? log2f(weight[lane]) + bound : -INFINITY;
       for (int s = 16; s; s >>= 1) bound = fmaxf(bound, __shfl_xor_sync(kFull, bound, s));
       if (lane == 0) {
+        sm.nan_down[token] = marked;
         bound += 2.f * norm;
         const float e = floorf(float(W::kAim) - 3.f - bound + log2f(float(d)));
         sm.h_exp[token] = e >= -126.f && e <= 126.f ? int(e) : e > 126.f ? 126 : e < -126.f ? -126 : 0;
@@ -1025,6 +1087,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
         down, down_begin, down_end, args.share + kMoeTokens * 128, [&](int) { return tokens; }, [&](int, int k) { return k; },
         [&](int unit, int k, float v) {
           const int row = unit * 128 + row_local;
+          for (uint32_t m = sm.nan_down[k]; m != 0 && row < d; m &= m - 1) {
+            const int64_t e = sm.ids[k][__ffs(int(m)) - 1];
+            if (row_is_nan<kFormat>(args.down + (e * d_tiles + unit) * f_steps * B::kBytes, row_local, f_steps))
+              v = __uint_as_float(0x7fffffffu);
+          }
           if (row < d) static_cast<T*>(args.y)[k * args.ldy + row] = from_f32<T>(v * factor * pow2f(-sm.h_exp[k]));
         },
         [&](int, int) {});
@@ -1118,13 +1185,13 @@ cudaError_t launch_fp4_experts_pack(const fp4_matrix_t& gate_up, const fp4_matri
   const unsigned up = grid(gate_up_blocks(w.experts, w.d, w.f) * 1024), dn = grid(down_blocks(w.experts, w.d, w.f) * 1024);
   const unsigned bd = grid(w.experts * w.f * 32);
   if (w.format == FP4_MXFP4) {
-    pack_experts_kernel<FP4_MXFP4, true><<<up, kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, w.gate_up);
-    pack_experts_kernel<FP4_MXFP4, false><<<dn, kPackThreads, 0, stream>>>(down, w.experts, w.d, w.down);
+    pack_experts_kernel<FP4_MXFP4, true><<<up, kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, w.gate_up, nullptr);
     bound_kernel<FP4_MXFP4><<<bd, kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, bound);
+    pack_experts_kernel<FP4_MXFP4, false><<<dn, kPackThreads, 0, stream>>>(down, w.experts, w.d, w.down, bound);
   } else {
-    pack_experts_kernel<FP4_NVFP4, true><<<up, kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, w.gate_up);
-    pack_experts_kernel<FP4_NVFP4, false><<<dn, kPackThreads, 0, stream>>>(down, w.experts, w.d, w.down);
+    pack_experts_kernel<FP4_NVFP4, true><<<up, kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, w.gate_up, nullptr);
     bound_kernel<FP4_NVFP4><<<bd, kPackThreads, 0, stream>>>(gate_up, w.experts, w.f, bound);
+    pack_experts_kernel<FP4_NVFP4, false><<<dn, kPackThreads, 0, stream>>>(down, w.experts, w.d, w.down, bound);
   }
   return cudaGetLastError();
 }

@@ -154,8 +154,9 @@ sgemm_status_t fp4_experts_pack(const fp4_matrix_t *gate_up, const fp4_matrix_t 
  * 16-bit float, 8 for 32 bits.  What is left is about 2^-16, 2^-19 and 2^-25 of a
  * block's largest value in the mean and 2^-13, 2^-16 and 2^-22 at most; or, where that
  * is more (FP4_NVFP4, blocks far below the token's largest value of x or h), 2^-21, 2^-24
- * and 2^-30 of that value.  Logits, softmax and sums are in 32 bits.  Values that
- * are not finite give results that are not finite, in their token alone.  Meant for few tokens: more than 16 are done 16 at a time.
+ * and 2^-30 of that value.  Logits, softmax and sums are in 32 bits.  Values of x
+ * that are not finite give results that are not finite, in their token alone; blocks of
+ * the weights that are NaN do so for the tokens that go to their expert alone.  Meant for few tokens: more than 16 are done 16 at a time.
  * One kernel on all SMs, launched cooperatively: it waits for the whole GPU.
  */
 sgemm_status_t fp4_moe(int dtype, const void *x, int64_t ldx, int64_t M, const float *router,

@@ -161,3 +161,52 @@ def test_zeros_keep_their_sign(dtype, fmt):
     assert np.array_equal(scales, want_scales) and np.array_equal(codes, want_codes)
     # (A block whose unit is 0 has zero codes by definition.)
     assert np.array_equal(torch.signbit(q.dequantize()).cpu().numpy(), want_codes > 7)
+
+
+# -------------------------------------------------------- non-finite weights
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("where", ("down", "gate and up"))
+def test_nan_weights_reach_the_tokens_of_their_expert_only(where, dtype, fmt):
+    """Token 0 goes to experts 0 and 1, token 1 to 1 and 2, token 2 to 2 and 3; NaN blocks are in experts 0 and 3."""
+    experts, d, f = 5, 200, 300
+    up = torch.randn(experts, 2 * f, d, generator=gen(21), device="cuda") / d ** 0.5
+    down = torch.randn(experts, d, f, generator=gen(22), device="cuda") / f ** 0.5
+    if where == "down":
+        down[0, 5, 0] = down[0, 130, 299] = down[3, 199, 256] = float("nan")
+        down[1, 7, 16:64] = -0.0            # blocks of -0 with the scale 0 are not NaN
+        down[2, :, :] *= torch.where(torch.arange(f, device="cuda") < 32, -0.0, 1.0)
+    else:
+        up[0, 17, 3] = up[3, f + 299, 199] = float("nan")
+    (qu, uv), (qd, dv) = stored(up.reshape(-1, d).nan_to_num(7.0), fmt), stored(down.reshape(-1, f).nan_to_num(7.0), fmt)
+    for q, v, t in ((qu, uv, up.reshape(-1, d)), (qd, dv, down.reshape(-1, f))):   # a NaN scale for the marked blocks
+        n = ref.BLOCK[fmt]
+        codes, scales, _ = ref.read_codes(q)
+        for r, c in torch.isnan(t).nonzero().tolist():
+            scales[r, c // n] = 255 if fmt == "mxfp4" else 127
+            v[r, c // n * n: c // n * n + n] = np.nan
+        if bool(torch.isnan(t).any()):
+            fresh = sg.fp4_matrix(torch.from_numpy(ref.packed(codes)).cuda(), torch.from_numpy(scales.astype(np.uint8)).cuda(),
+                                  fmt, cols=t.shape[1], scale=q.scale)
+            if t.shape[1] == d:
+                qu = fresh
+            else:
+                qd = fresh
+    x = torch.randn(4, d, generator=gen(23), device="cuda").to(dtype)
+    router = torch.zeros(experts, d, device="cuda")
+    basis = torch.linalg.pinv(x.float())                        # logits of the tokens as wanted
+    wanted = torch.tensor([[5, 4, 1, 0, -1], [0, 4, 5, 1, -1], [0, 1, 4, 5, -1], [-1, 4, 0, 1, 5]], device="cuda")
+    router[:] = (basis @ wanted.float()).t()
+    y, ids, p = sg.fp4_moe(x, router, sg.fp4_experts(qu, qd, experts), 2, return_routing=True)
+    with np.errstate(invalid="ignore"):
+        wy, wids, _ = ref.moe(ref.as_numpy(x), ref.as_numpy(router), uv.reshape(experts, 2 * f, d),
+                              dv.reshape(experts, d, f), 2, True)
+    got = ref.as_numpy(y)
+    assert wids.tolist() == [[0, 1], [2, 1], [3, 2], [4, 1]] and np.array_equal(ids.cpu().numpy(), wids)
+    assert np.isnan(wy[0]).any() and np.isnan(wy[2]).any() and np.isfinite(wy[[1, 3]]).all()
+    assert np.array_equal(np.isnan(got), np.isnan(wy))
+    limit = {torch.float32: 5e-6, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -10}[dtype]
+    good = np.isfinite(wy)
+    for t in range(4):
+        if good[t].any():
+            assert np.linalg.norm((got - wy)[t][good[t]]) <= limit * np.linalg.norm(wy[t][good[t]])

@@ -310,10 +310,12 @@ template <int kPerLane, typename Chosen>
 __device__ __forceinline__ void select_top(const float* logits, int experts, int top, int renorm, int lane,
                                            uint16_t* ids, float* weight, Chosen chosen) {
   uint32_t key[kPerLane];
+  bool nan = false;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const int e = lane + 32 * i;
     key[i] = e < experts ? order_key(__ldcg(logits + e)) : 0u;
+    nan = nan || key[i] == 1u;
   }
   float exps[kPerLane];
 #pragma unroll
@@ -336,8 +338,8 @@ __device__ __forceinline__ void select_top(const float* logits, int experts, int
   if (lane < top) ids[lane] = uint16_t(mine_id);
   chosen(mine_id);
   const float peak = logit_of(peak_key);
-  float sum = 1.f;
-  if (!renorm) {  // the sum over all experts cancels otherwise
+  float sum = __any_sync(kFull, nan) ? __uint_as_float(0x7fffffffu) : 1.f;
+  if (!renorm) {  // the sum over all experts cancels otherwise, unless it is NaN
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i)

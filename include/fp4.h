@@ -141,7 +141,7 @@ sgemm_status_t fp4_experts_pack(const fp4_matrix_t *gate_up, const fp4_matrix_t 
  *
  *   logits = x R^T                       R: router, experts x d, 32-bit, row stride ldr
  *   ids    = the `top` experts of the largest logits, in that order; equal
- *            logits in the order of their index
+ *            logits in the order of their index, NaN after every number
  *   p      = softmax(logits)[ids], divided by its sum if `renormalize`
  *   h_j    = silu(G x) * (U x)           G, U, D: gate, up and down of expert ids[j]
  *   y      = sum_j p_j D h_j

@@ -210,3 +210,24 @@ def test_nan_weights_reach_the_tokens_of_their_expert_only(where, dtype, fmt):
     for t in range(4):
         if good[t].any():
             assert np.linalg.norm((got - wy)[t][good[t]]) <= limit * np.linalg.norm(wy[t][good[t]])
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("experts", [6, 100, 200, 300])
+def test_nan_router_row_spoils_the_weights(experts, renorm):
+    """A NaN among a token's logits makes its softmax NaN, whichever experts are chosen; NaN comes after every number."""
+    d, f = 64, 16
+    up = torch.randn(experts * 2 * f, d, generator=gen(31), device="cuda")
+    down = torch.randn(experts * d, f, generator=gen(32), device="cuda")
+    w = sg.fp4_experts(sg.fp4_quantize(up, "mxfp4"), sg.fp4_quantize(down, "mxfp4"), experts)
+    router = torch.randn(experts, d, generator=gen(33), device="cuda")
+    x = torch.randn(3, d, generator=gen(34), device="cuda")
+    x[:, 5] = torch.tensor([0.0, 1.0, 2.0], device="cuda")
+    router[4, 5] = float("inf")          # times 0: NaN; times a positive number: infinity
+    y, ids, p = sg.fp4_moe(x, router, w, 2, renormalize=renorm, return_routing=True)
+    assert bool(torch.isnan(p).all()) and bool(torch.isnan(y).all())
+    assert 4 not in ids[0].tolist() and ids[1, 0] == 4 and ids[2, 0] == 4
+    router[4, 5] = -float("inf")         # no weight where it is a number
+    y, ids, p = sg.fp4_moe(x, router, w, 2, renormalize=renorm, return_routing=True)
+    assert bool(torch.isnan(p[0]).all()) and bool(torch.isnan(y[0]).all())
+    assert bool(torch.isfinite(p[1:]).all()) and bool(torch.isfinite(y[1:]).all()) and 4 not in ids[1:].flatten().tolist()

@@ -11,6 +11,10 @@ Formats (``include/fp4.h`` has the full definition):
 * ``"nvfp4"``: blocks of 16 values with an 8-bit float scale byte, times one
   32-bit factor of the whole matrix (a one-element tensor, usually
   ``x.abs().amax() / 2688``; ``None`` means 1).
+
+Every call takes a ``stream`` (default: the current one).  It does not wait for
+the stream on which its inputs were made; a ``stream`` that was passed is
+recorded on them, so they may be dropped once the call returned.
 """
 from __future__ import annotations
 
@@ -134,6 +138,13 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _read_on(stream, *tensors):
+    """A stream that was passed in uses these tensors: their memory is not given out again before it is done with them."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _output(out, shape, dtype, device, index, stream):
     """(out or a new tensor, its row stride)"""
     if out is None:
@@ -216,6 +227,8 @@ def fp4_quantize(x, format="mxfp4", scale=None, out=None, stream=None):
         if scale is not None and scale is not out.scale:
             raise ValueError("out has its own scale: make it with this one")
         _same_device(x.get_device(), out)
+    if stream is not None:
+        _read_on(stream, x, out._memory, out.scale)
     _call("fp4_quantize", out.index, stream, load().fp4_quantize, _DTYPES[x.dtype], x.data_ptr(), ld, out._ref)
     return out
 
@@ -246,6 +259,8 @@ def fp4_matrix(codes, scales, format="mxfp4", cols=None, scale=None, stream=None
                          f"{(rows, blocks)}, got {tuple(codes.shape)} and {tuple(scales.shape)}")
     _same_device(codes.get_device(), scales)
     q = Fp4Matrix(rows, cols, format, scale, codes.device, stream)
+    if stream is not None:
+        _read_on(stream, codes, scales)
     _call("fp4_pack", q.index, stream, load().fp4_pack, codes.data_ptr(), max(codes.stride(0), codes.shape[1], 1),
           scales.data_ptr(), max(scales.stride(0), scales.shape[1], 1), q._ref)
     return q
@@ -259,6 +274,8 @@ def fp4_dequantize(q, dtype=torch.float32, out=None, stream=None):
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
     out, ld = _output(out, q.shape, dtype, q.device, q.index, stream)
+    if stream is not None:
+        _read_on(stream, q._memory, q.scale, out)
     _call("fp4_dequantize", q.index, stream, load().fp4_dequantize, q._ref, _DTYPES[dtype], out.data_ptr(), ld)
     return out
 
@@ -282,6 +299,8 @@ def fp4_gemm(A, B, out=None, out_dtype=torch.float32, stream=None):
     if out_dtype not in _DTYPES:
         raise ValueError(f"out_dtype must be float32, bfloat16 or float16, got {out_dtype}")
     out, ld = _output(out, (A.shape[0], B.shape[0]), out_dtype, A.device, A.index, stream)
+    if stream is not None:
+        _read_on(stream, A._memory, A.scale, B._memory, B.scale, out)
     _call("fp4_gemm", A.index, stream, load().fp4_gemm, A._ref, B._ref, _DTYPES[out_dtype], out.data_ptr(), ld)
     return out
 
@@ -299,6 +318,8 @@ def fp4_linear(x, W, x_scale=None, out=None, stream=None):
     _same_device(index, x)
     factor = _scale(x_scale, W.format, index, "x_scale")
     out, ldy = _output(out, (m, n), dtype, W.device, index, stream)
+    if stream is not None:
+        _read_on(stream, x, x_scale, W._memory, W.scale, out)
     _call("fp4_linear", index, stream, load().fp4_linear, _DTYPES[dtype], x.data_ptr(), ldx, m, factor, W._ref,
           out.data_ptr(), ldy)
     return out
@@ -344,6 +365,8 @@ def fp4_experts(gate_up, down, experts, stream=None):
         raise ValueError(f"formats differ: {gate_up.format} and {down.format}")
     _same_device(gate_up.index, down)
     w = Fp4Experts(experts, d, f, gate_up.format, gate_up.scale, down.scale, gate_up.device, stream)
+    if stream is not None:
+        _read_on(stream, gate_up._memory, gate_up.scale, down._memory, down.scale)
     _call("fp4_experts_pack", w.index, stream, load().fp4_experts_pack, gate_up._ref, down._ref, w._ref)
     return w
 
@@ -373,6 +396,8 @@ def fp4_moe(x, router, experts, top_k, renormalize=True, out=None, return_routin
     if return_routing:
         ids = _empty((tokens, top_k), torch.int32, device, stream)
         p = _empty((tokens, top_k), torch.float32, device, stream)
+    if stream is not None:
+        _read_on(stream, x, router, experts.gate_up, experts.down, experts.gate_up_scale, experts.down_scale, out)
     _call("fp4_moe", index, stream, load().fp4_moe, _DTYPES[dtype], x.data_ptr(), ldx, tokens, router.data_ptr(), ldr,
           experts._ref, top_k, 1 if renormalize else 0, out.data_ptr(), ldy, ids.data_ptr() if return_routing else 0,
           p.data_ptr() if return_routing else 0)

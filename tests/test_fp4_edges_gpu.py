@@ -6,7 +6,8 @@ Tolerances, derived from the definitions in ``include/fp4.h``:
   mean; a block's largest value is about twice its root mean square, and x enters twice, h once, so y is within 2e-7,
   1e-5 or 8e-5 in the 2-norm, and below that where the blocks' largest values are the usual ones.  Its 32-bit sums are
   off by a few 2^-24 of their partial sums, which a pre-activation g away from zero turns into a relative error of h of a
-  few |g| 2^-24: 3e-6 at |g| = 16.  So 5e-6 in 32 bits; with a 16-bit output the half unit of the type decides, at most 2^-9 or 2^-12 of a value in the mean, and 2^-8 or 2^-10 leaves room;
+  few |g| 2^-24: 3e-6 at |g| = 16.  So 5e-6 in 32 bits; with a 16-bit output the half unit of the type decides, at most
+  2^-9 or 2^-12 of a value in the mean, and 2^-8 or 2^-10 leaves room;
 * two results whose inner values differ by 3e-5 (2^-16 in the mean, three times) round to different bfloat16 numbers where a
   rounding boundary lies between them: for 3e-5 / 2^-8 = 0.8 % of the outputs, and a few times that counting the small ones.
   3 % is the limit.
@@ -231,3 +232,43 @@ def test_nan_router_row_spoils_the_weights(experts, renorm):
     y, ids, p = sg.fp4_moe(x, router, w, 2, renormalize=renorm, return_routing=True)
     assert bool(torch.isnan(p[0]).all()) and bool(torch.isnan(y[0]).all())
     assert bool(torch.isfinite(p[1:]).all()) and bool(torch.isfinite(y[1:]).all()) and 4 not in ids[1:].flatten().tolist()
+
+
+# ------------------------------------------------------------------- streams
+def test_inputs_may_be_dropped_behind_a_call_on_another_stream():
+    """Memory that a call on another stream still reads is not given out again: everything is dropped and overwritten
+    while that stream is held up."""
+    experts, d, f = 4, 256, 128
+    s = torch.cuda.Stream()
+
+    def inputs():
+        up, down = (torch.randn(r, c, generator=gen(41 + c), device="cuda") for r, c in ((experts * 2 * f, d), (experts * d, f)))
+        x, router = torch.randn(40, d, generator=gen(42), device="cuda"), torch.randn(experts, d, generator=gen(43), device="cuda")
+        codes = torch.randint(0, 256, (300, d // 2), generator=gen(44), device="cuda", dtype=torch.uint8)
+        scales = torch.randint(30, 90, (300, d // 16), generator=gen(45), device="cuda", dtype=torch.uint8)
+        q = [sg.fp4_quantize(t, "nvfp4", scale=torch.full((1,), 0.01, device="cuda")) for t in (up, down)]
+        return [x, router, codes, scales, torch.full((1,), 0.02, device="cuda"), *q]
+
+    def calls(stream, x, router, codes, scales, factor, up, down):
+        w = sg.fp4_experts(up, down, experts, stream=stream)
+        m = sg.fp4_matrix(codes, scales, "nvfp4", scale=factor, stream=stream)
+        xq = sg.fp4_quantize(x, "nvfp4", scale=factor, stream=stream)
+        return [w.gate_up, w.down, sg.fp4_dequantize(m, stream=stream), sg.fp4_linear(x, m, x_scale=factor, stream=stream),
+                sg.fp4_gemm(xq, m, stream=stream), sg.fp4_dequantize(up, stream=stream),
+                sg.fp4_moe(x[:5], router, w, 2, stream=stream)]
+
+    for _ in range(2):   # the second time every workspace is there
+        args = inputs()
+        torch.cuda.synchronize()
+        want = calls(None, *args)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(200_000_000)   # about a tenth of a second
+        got = calls(s, *args)
+        sizes = [t.untyped_storage().nbytes() for t in args[:5]] + [q._memory.untyped_storage().nbytes() for q in args[5:]]
+        del args
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        del junk

@@ -165,7 +165,7 @@ class Fp4Matrix:
     or, from a checkpoint's arrays, by :func:`fp4_matrix`.
     """
 
-    __slots__ = ("format", "shape", "device", "index", "scale", "_memory", "_start", "_ld", "_c", "_ref", "__weakref__")
+    __slots__ = ("format", "shape", "device", "index", "_scale", "_memory", "_start", "_ld", "_c", "_ref", "__weakref__")
 
     def __init__(self, rows, cols, fmt, scale=None, device="cuda", stream=None):
         number = _format(fmt)
@@ -180,11 +180,16 @@ class Fp4Matrix:
         start = (rows * ld + 255) // 256 * 256
         memory = _empty((start + (rows + 127) // 128 * ((cols + 255) // 256) * (1024 << number),), torch.uint8, device,
                         stream)
-        self.format, self.shape, self.device, self.index, self.scale = fmt, (rows, cols), device, index, scale
+        self.format, self.shape, self.device, self.index, self._scale = fmt, (rows, cols), device, index, scale
         self._memory, self._start, self._ld = memory, start, ld
         base = memory.data_ptr()
         self._c = c = _Matrix(number, rows, cols, base, ld, base + start, _scale(scale, fmt, index))
         self._ref = ctypes.addressof(c)
+
+    @property
+    def scale(self):
+        """nvfp4's factor.  The library has its address: another factor takes another matrix, or a write into this tensor."""
+        return self._scale
 
     @property
     def codes(self):
@@ -336,12 +341,18 @@ class Fp4Experts:
         if st != OK:
             raise SgemmError(st, "fp4_experts_layout")
         self.experts, self.d, self.f, self.format, self.device, self.index = experts, d, f, fmt, device, device.index
-        self.gate_up = _empty((up.value,), torch.uint8, device, stream)
-        self.down = _empty((down.value,), torch.uint8, device, stream)
-        self.gate_up_scale, self.down_scale = gate_up_scale, down_scale
+        # The library has the addresses of these four: they stay.
+        self._gate_up = _empty((up.value,), torch.uint8, device, stream)
+        self._down = _empty((down.value,), torch.uint8, device, stream)
+        self._gate_up_scale, self._down_scale = gate_up_scale, down_scale
         self._c = _Experts(number, experts, d, f, self.gate_up.data_ptr(), self.down.data_ptr(),
                            *(0 if s is None else s.data_ptr() for s in (gate_up_scale, down_scale)))
         self._ref = ctypes.addressof(self._c)
+
+    gate_up = property(lambda self: self._gate_up)
+    down = property(lambda self: self._down)
+    gate_up_scale = property(lambda self: self._gate_up_scale)
+    down_scale = property(lambda self: self._down_scale)
 
     def __repr__(self):
         return f"Fp4Experts({self.experts} experts, d {self.d}, f {self.f}, {self.format}, {self.device})"

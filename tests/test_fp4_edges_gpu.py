@@ -272,3 +272,19 @@ def test_inputs_may_be_dropped_behind_a_call_on_another_stream():
         for a, b in zip(got, want):
             assert torch.equal(a, b)
         del junk
+
+
+def test_tensors_that_the_library_has_addresses_of_stay():
+    """Assigning another factor would leave the library with the address of the first, whose memory may be gone."""
+    one, two = torch.ones(1, device="cuda"), torch.full((1,), 2.0, device="cuda")
+    q = sg.fp4_quantize(torch.randn(64, 64, generator=gen(51), device="cuda"), "nvfp4", scale=one)
+    before = q.dequantize()
+    with pytest.raises(AttributeError):
+        q.scale = two
+    w = sg.fp4_experts(q, sg.fp4_quantize(torch.randn(64, 32, generator=gen(52), device="cuda"), "nvfp4", scale=one), 1)
+    for name in ("gate_up", "down", "gate_up_scale", "down_scale"):
+        with pytest.raises(AttributeError):
+            setattr(w, name, two)
+    assert q.scale is one and w.gate_up_scale is one
+    one.fill_(2)                      # a write into the factor counts
+    assert torch.equal(q.dequantize(), 2 * before)

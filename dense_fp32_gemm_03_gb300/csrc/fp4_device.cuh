@@ -104,6 +104,15 @@ __device__ __forceinline__ float decode_scale(uint32_t byte) {
   return kFormat == FP4_MXFP4 ? decode_e8m0(byte) : decode_e4m3(byte);
 }
 
+// The two matrices' factors, by which a finished sum is multiplied one after the other:
+// their product and 1, as long as that is a normal number, else the smaller one first.  (One
+// factor may be far above and the other far below 1: sum * 1e35 * 1e-30 would overflow on
+// the way.)
+__device__ __forceinline__ float2 join_factors(float a, float b) {
+  const float p = a * b, m = fabsf(p);
+  return m >= 0x1p-126f && m <= 0x1.fffffep127f ? make_float2(p, 1.f) : fabsf(a) <= fabsf(b) ? make_float2(a, b) : make_float2(b, a);
+}
+
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }

@@ -251,11 +251,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   } else if (warp < 6) {
     // ---- joining and storing: a lane has one row of W, 16 tokens
     const int q = warp & 3, row_local = 32 * q + lane;
-    float alpha_w = 1.f, alpha_x = 1.f;
-    if (kFormat == FP4_NVFP4) {
-      if (args.w_factor) alpha_w = __ldg(args.w_factor);
-      if (args.x_factor) alpha_x = __ldg(args.x_factor);
-    }
+    float2 alpha = make_float2(1.f, 1.f);
+    if (kFormat == FP4_NVFP4)
+      alpha = join_factors(args.w_factor ? __ldg(args.w_factor) : 1.f, args.x_factor ? __ldg(args.x_factor) : 1.f);
     T* y = static_cast<T*>(args.y);
     wait_started();
     uint32_t done = 0;
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         if (row < args.n) {
 #pragma unroll
           for (int t = 0; t < kCols; ++t)
-            if (t < tokens) y[int64_t(t) * args.ldy + row] = from_f32<T>(sum[t] * alpha_w * alpha_x);
+            if (t < tokens) y[int64_t(t) * args.ldy + row] = from_f32<T>(sum[t] * alpha.x * alpha.y);
         }
         continue;
       }
@@ -314,7 +312,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
           const float* p = mine + own_row * kSumRow + t;
           float total = p[0];
           for (int c = 1; c < ctas; ++c) total += p[c * own * kSumRow];
-          y[int64_t(t) * args.ldy + out_row] = from_f32<T>(total * alpha_w * alpha_x);
+          y[int64_t(t) * args.ldy + out_row] = from_f32<T>(total * alpha.x * alpha.y);
         }
       }
       __syncwarp();

@@ -292,11 +292,9 @@ __device__ __forceinline__ void tc_body(const CUtensorMap& map_r, const CUtensor
     const int row_local = 32 * q + lane, col_local = half * kV;
     const int etid = threadIdx.x - 64;
     constexpr int64_t kSlot = int64_t(S::kRows) * kN / 4;  // one CTA's share of a tile, in float4
-    float alpha_r = 1.f, alpha_c = 1.f;
-    if (kFormat == FP4_NVFP4) {
-      if (args.factor_r) alpha_r = __ldg(args.factor_r);
-      if (args.factor_c) alpha_c = __ldg(args.factor_c);
-    }
+    float2 alpha = make_float2(1.f, 1.f);
+    if (kFormat == FP4_NVFP4)
+      alpha = join_factors(args.factor_r ? __ldg(args.factor_r) : 1.f, args.factor_c ? __ldg(args.factor_c) : 1.f);
     UnitIter w;
     w.init(sc, unit_id);
     Unit u;
@@ -373,7 +371,7 @@ __device__ __forceinline__ void tc_body(const CUtensorMap& map_r, const CUtensor
       }
       if (store && ok) {
 #pragma unroll
-        for (int c = 0; c < kV; ++c) v[c] = v[c] * alpha_r * alpha_c;
+        for (int c = 0; c < kV; ++c) v[c] = v[c] * alpha.x * alpha.y;
         const int row = tm * S::kBM + int(rank) * S::kRows + row_local, col0 = tn * kN + col_local;
         T* out = static_cast<T*>(args.out);
         if constexpr (kSwap) {

@@ -288,3 +288,33 @@ def test_tensors_that_the_library_has_addresses_of_stay():
     assert q.scale is one and w.gate_up_scale is one
     one.fill_(2)                      # a write into the factor counts
     assert torch.equal(q.dequantize(), 2 * before)
+
+
+# ------------------------------------------------------------------- factors
+@pytest.mark.parametrize("ga,gb", [(1e-30, 1e35), (1e35, 1e-30), (1e-37, 1e-3), (1e-20, 1e-20), (1e34, 1e34), (0.0, 1e35)])
+@pytest.mark.parametrize("m,n,k", [(1, 200, 600), (9, 300, 5000), (40, 130, 256), (200, 300, 256), (2100, 2500, 128)])
+def test_factors_far_apart(m, n, k, ga, gb):
+    """Sums are multiplied by both factors without leaving the range of 32 bits on the way."""
+    rng = np.random.default_rng(m)
+
+    def side(rows, g):
+        codes, scales = rng.integers(0, 16, (rows, k)), rng.integers(40, 70, (rows, -(-k // 16)))
+        t = torch.tensor([g], device="cuda")
+        q = sg.fp4_matrix(torch.from_numpy(ref.packed(codes)).cuda(), torch.from_numpy(scales.astype(np.uint8)).cuda(), "nvfp4",
+                          cols=k, scale=t)
+        return q, ref.values(codes, scales, "nvfp4", t.item())
+    (a, av), (b, bv) = side(m, ga), side(n, gb)
+    want, size = av @ bv.T, np.abs(av) @ np.abs(bv).T
+    got = ref.as_numpy(sg.fp4_gemm(a, b))
+    fits = size < 3e38                       # beyond, the result is infinite or not, as the sums fall
+    bound = (k + 4) * 2.0 ** -23 * size + 2.0 ** -149
+    assert np.all(np.abs(got - want)[fits] <= bound[fits])
+    # The linear layer: x holds exactly what its codes stand for at this factor.
+    if ga and np.abs(av).max() < 3e38 and np.abs(av)[av != 0].min() > 2.0 ** -120:
+        x = torch.from_numpy(av).float().cuda()
+        codes, scales = ref.quantize(x.cpu().numpy(), "nvfp4", ga)
+        xv = ref.values(codes, scales, "nvfp4", a.scale.item())
+        want, size = xv @ bv.T, np.abs(xv) @ np.abs(bv).T
+        fits = size < 3e38
+        got = ref.as_numpy(sg.fp4_linear(x, b, x_scale=a.scale))
+        assert np.all(np.abs(got - want)[fits] <= ((k + 4) * 2.0 ** -23 * size + 2.0 ** -149)[fits])

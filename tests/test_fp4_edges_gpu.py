@@ -318,3 +318,96 @@ def test_factors_far_apart(m, n, k, ga, gb):
         fits = size < 3e38
         got = ref.as_numpy(sg.fp4_linear(x, b, x_scale=a.scale))
         assert np.all(np.abs(got - want)[fits] <= ((k + 4) * 2.0 ** -23 * size + 2.0 ** -149)[fits])
+
+
+# --------------------------------------------- paths of the kernels beyond one tile
+def random_matrix(rows, cols, fmt, seed):
+    """(library matrix, 64-bit values on the GPU) of random codes and scales."""
+    n = ref.BLOCK[fmt]
+    codes = torch.randint(0, 16, (rows, cols + cols % 2), generator=gen(seed), device="cuda", dtype=torch.uint8)
+    if cols % 2:
+        codes[:, -1] = 0
+    low, high = (122, 130) if fmt == "mxfp4" else (40, 70)
+    scales = torch.randint(low, high, (rows, -(-cols // n)), generator=gen(seed + 1), device="cuda", dtype=torch.uint8)
+    q = sg.fp4_matrix(codes[:, 0::2] | codes[:, 1::2] << 4, scales, fmt, cols=cols)
+    table = torch.from_numpy(np.concatenate((ref.LEVELS, -ref.LEVELS))).cuda()
+    unit = torch.exp2(scales.double() - 127) if fmt == "mxfp4" else torch.from_numpy(ref.E4M3).cuda()[scales.long()]
+    return q, table[codes[:, :cols].long()] * unit.repeat_interleave(n, 1)[:, :cols]
+
+
+def check_sums(got, a, b, what):
+    """As check_product, on the GPU."""
+    want, size = a @ b.t(), a.abs() @ b.abs().t()
+    unit = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}[got.dtype]
+    bound = (a.shape[1] + 4) * 2.0 ** -23 * size + unit * want.abs() + (2.0 ** -24 if got.dtype == torch.float16 else 0)
+    assert bool(((got.double() - want).abs() <= bound).all()), what
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", [
+    (16, 5120, 8192),     # clusters of 8 CTAs, three tiles each, the ring of stages goes round
+    (5, 40001, 4096),     # of 4, nine tiles
+    (7, 77947, 510),      # of 2, nine tiles
+    (3, 160001, 200),     # single CTAs, nine tiles
+    (1, 20000, 1300)])    # a part of K that some CTAs of a cluster do not have
+def test_linear_of_few_tokens_over_many_tiles(m, n, k, dtype, fmt):
+    w, wv = random_matrix(n, k, fmt, 61)
+    x = torch.randn(m, k, generator=gen(62), device="cuda").to(dtype) / 64
+    codes, scales = ref.quantize(ref.as_numpy(x), fmt)
+    xv = torch.from_numpy(ref.values(codes, scales, fmt)).cuda()
+    got = [sg.fp4_linear(x, w) for _ in range(10)]
+    check_sums(got[0], xv, wv, f"{(m, n, k)} {fmt} {dtype}")
+    assert all(torch.equal(g, got[0]) for g in got[1:])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("m,n,k", [(17, 20000, 1000), (20, 8192, 8192), (33, 40000, 520), (64, 300, 30000), (50, 4096, 4096)])
+def test_linear_of_some_tokens(m, n, k, fmt):
+    """Swapped tiles: more than one wave of them, and tiles that are cut over K."""
+    w, wv = random_matrix(n, k, fmt, 63)
+    x = torch.randn(m, k, generator=gen(64), device="cuda").bfloat16() / 64
+    codes, scales = ref.quantize(ref.as_numpy(x), fmt)
+    xv = torch.from_numpy(ref.values(codes, scales, fmt)).cuda()
+    got = [sg.fp4_linear(x, w) for _ in range(5)]
+    check_sums(got[0], xv, wv, f"{(m, n, k)} {fmt}")
+    assert all(torch.equal(g, got[0]) for g in got[1:])
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("experts,top", [(64, 3), (65, 5), (100, 32), (128, 1), (129, 7), (200, 20), (256, 4)])
+def test_selection_among_many_experts(experts, top, renorm):
+    d, f = 96, 16
+    up = torch.randn(experts * 2 * f, d, generator=gen(71), device="cuda")
+    down = torch.randn(experts * d, f, generator=gen(72), device="cuda")
+    (qu, uv), (qd, dv) = stored(up, "mxfp4"), stored(down, "mxfp4")
+    router = torch.randint(-1, 2, (experts, d), generator=gen(73), device="cuda").float()   # equal logits, exact sums
+    router[experts - 1] = router[experts // 3]
+    x = torch.randint(-2, 3, (5, d), generator=gen(74), device="cuda").float() / 8
+    y, ids, p = sg.fp4_moe(x, router, sg.fp4_experts(qu, qd, experts), top, renormalize=renorm, return_routing=True)
+    wy, wids, wp = ref.moe(ref.as_numpy(x), ref.as_numpy(router), uv.reshape(experts, 2 * f, d), dv.reshape(experts, d, f),
+                           top, renorm)
+    assert np.array_equal(ids.cpu().numpy(), wids)
+    assert np.allclose(ref.as_numpy(p), wp, rtol=2e-5, atol=0)
+    assert (np.linalg.norm(ref.as_numpy(y) - wy, axis=1) <= 1e-5 * np.linalg.norm(wy, axis=1)).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("rows,cols,pad", [(37, 290, 1), (37, 290, 3), (5, 1025, 2), (3, 40, 5)])
+def test_values_read_back_into_rows_at_any_address(rows, cols, pad, fmt, dtype):
+    q, _ = random_matrix(rows, cols, fmt, 81)
+    if fmt == "nvfp4":
+        g = torch.tensor([0.0371], device="cuda")
+        codes, scales, _ = ref.read_codes(q)
+        q = sg.fp4_matrix(torch.from_numpy(ref.packed(codes)).cuda(), torch.from_numpy(scales.astype(np.uint8)).cuda(), fmt,
+                          cols=cols, scale=g)
+    codes, scales, _ = ref.read_codes(q)
+    unit = ref.values(np.full((rows, cols), 2), scales, fmt).astype(np.float32)
+    if fmt == "nvfp4":
+        unit = unit * np.float32(0.0371)
+    level = (ref.LEVELS[codes & 7] * np.where(codes & 8, -1.0, 1.0)).astype(np.float32)
+    out = torch.full((rows, cols + 7), 5.0, device="cuda", dtype=dtype)
+    sg.fp4_dequantize(q, out=out[:, pad:pad + cols])
+    assert torch.equal(out[:, pad:pad + cols].cpu(), torch.from_numpy(level * unit).to(dtype))
+    assert bool((out[:, :pad] == 5).all()) and bool((out[:, pad + cols:] == 5).all())

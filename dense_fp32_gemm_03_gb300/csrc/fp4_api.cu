@@ -74,7 +74,11 @@ Range code_range(const fp4_matrix_t* q) {
   return range(q->codes, q->rows && q->cols ? (q->rows - 1) * q->ld + code_pitch(q->cols) : 0);
 }
 Range scale_range(const fp4_matrix_t* q) { return range(q->scales, scale_bytes(q->format, q->rows, q->cols)); }
+Range factor_range(const float* f) { return range(f, f ? 4 : 0); }
 bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+bool overlap(Range a, const fp4_matrix_t* q) {
+  return overlap(a, code_range(q)) || overlap(a, scale_range(q)) || overlap(a, factor_range(q->factor));
+}
 
 // ------------------------------------------------------------------- products
 std::mutex g_mu;
@@ -299,7 +303,8 @@ sgemm_status_t fp4_quantize(int dtype, const void* x, int64_t ldx, const fp4_mat
   if (st == SGEMM_OK) st = check_dense(dtype, x, q->rows, q->cols, ldx);
   if (st != SGEMM_OK) return st;
   const Range r = dense_range(dtype, x, q->rows, q->cols, ldx);
-  if (overlap(r, code_range(q)) || overlap(r, scale_range(q))) return SGEMM_ERR_INVALID_VALUE;
+  for (const Range& out : {code_range(q), scale_range(q)})
+    if (overlap(out, r) || overlap(out, factor_range(q->factor))) return SGEMM_ERR_INVALID_VALUE;
   LibDevice d;
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
@@ -334,7 +339,7 @@ sgemm_status_t fp4_dequantize(const fp4_matrix_t* q, int dtype, void* y, int64_t
   if (st == SGEMM_OK) st = check_dense(dtype, y, q->rows, q->cols, ldy);
   if (st != SGEMM_OK) return st;
   const Range r = dense_range(dtype, y, q->rows, q->cols, ldy);
-  if (overlap(r, code_range(q)) || overlap(r, scale_range(q))) return SGEMM_ERR_INVALID_VALUE;
+  if (overlap(r, q)) return SGEMM_ERR_INVALID_VALUE;
   LibDevice d;
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || q->rows == 0 || q->cols == 0) return st;
@@ -352,8 +357,7 @@ sgemm_status_t fp4_gemm(const fp4_matrix_t* A, const fp4_matrix_t* B, int dtype,
   st = check_dense(dtype, C, A->rows, B->rows, ldc);
   if (st != SGEMM_OK) return st;
   const Range r = dense_range(dtype, C, A->rows, B->rows, ldc);
-  for (const fp4_matrix_t* q : {A, B})
-    if (overlap(r, code_range(q)) || overlap(r, scale_range(q))) return SGEMM_ERR_INVALID_VALUE;
+  if (overlap(r, A) || overlap(r, B)) return SGEMM_ERR_INVALID_VALUE;
   LibDevice d;
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || A->rows == 0 || B->rows == 0) return st;
@@ -379,8 +383,7 @@ sgemm_status_t fp4_linear(int dtype, const void* x, int64_t ldx, int64_t M, cons
   if (st != SGEMM_OK) return st;
   if (!aligned(x_factor, 4)) return SGEMM_ERR_INVALID_VALUE;
   const Range r = dense_range(dtype, y, M, W->rows, ldy);
-  if (overlap(r, code_range(W)) || overlap(r, scale_range(W)) ||
-      overlap(r, dense_range(dtype, x, M, W->cols, ldx)))
+  if (overlap(r, W) || overlap(r, factor_range(x_factor)) || overlap(r, dense_range(dtype, x, M, W->cols, ldx)))
     return SGEMM_ERR_INVALID_VALUE;
   LibDevice d;
   st = gb300::lib_device(&d);
@@ -486,13 +489,18 @@ sgemm_status_t fp4_moe(int dtype, const void* x, int64_t ldx, int64_t M, const f
   if (st != SGEMM_OK) return st;
   if (top < 1 || top > 32 || top > w->experts || !aligned(ids, 4) || !aligned(p, 4)) return SGEMM_ERR_INVALID_VALUE;
   if (w->d == 0 || w->f == 0) return SGEMM_ERR_INVALID_VALUE;
-  const Range r = dense_range(dtype, y, M, w->d, ldy);
   int64_t up_bytes = 0, down_bytes = 0;
   fp4_experts_layout(w->format, w->experts, w->d, w->f, &up_bytes, &down_bytes);
-  if (overlap(r, dense_range(dtype, x, M, w->d, ldx)) ||
-      overlap(r, dense_range(FP4_F32, router, w->experts, w->d, ldr)) || overlap(r, range(w->gate_up, up_bytes)) ||
-      overlap(r, range(w->down, down_bytes)))
-    return SGEMM_ERR_INVALID_VALUE;
+  const Range outs[3] = {dense_range(dtype, y, M, w->d, ldy), range(ids, ids ? M * top * 4 : 0), range(p, p ? M * top * 4 : 0)};
+  const Range ins[6] = {dense_range(dtype, x, M, w->d, ldx), dense_range(FP4_F32, router, w->experts, w->d, ldr),
+                        range(w->gate_up, up_bytes),         range(w->down, down_bytes),
+                        factor_range(w->gate_up_factor),     factor_range(w->down_factor)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& in : ins)
+      if (overlap(outs[i], in)) return SGEMM_ERR_INVALID_VALUE;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(outs[i], outs[j])) return SGEMM_ERR_INVALID_VALUE;
+  }
   LibDevice d;
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || M == 0) return st;

@@ -30,7 +30,7 @@
  * stream) cache (so calls on one stream must not be made from several host
  * threads at the same time, and the first call that needs more scratch is
  * made outside stream capture).  Outputs are write-only and must not overlap
- * inputs.
+ * inputs (factors included) or one another.
  */
 #ifndef GB300_FP4_H
 #define GB300_FP4_H

@@ -52,3 +52,19 @@ def test_a_layer_over_its_factors_is_rejected(lib, factor):
     for factors in ((factor, 0), (0, factor)):
         w = fp4._Experts(1, 8, 64, 32, P_Q, P_S, *factors)
         assert lib.fp4_moe(0, P_X, 64, 4, P_R, 64, ctypes.addressof(w), 2, 1, P_Y, 64, 0, 0, 0) == BAD
+
+
+def test_package_is_imported_without_torch():
+    """As before the 4-bit operators: addresses and the build need no torch, and no time for it."""
+    import os
+    import subprocess
+    import sys
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import dense_fp32_gemm_03_gb300 as p\n"
+            "assert callable(p.sgemm_raw) and 'fp4_moe' in dir(p) and 'fp4_moe' in p.__all__\n"
+            "del sys.modules['torch']\n"
+            "assert callable(p.fp4_moe) and p.Fp4Matrix.__module__ == p.__name__ + '.fp4'\n"
+            "try:\n    p.fp5\nexcept AttributeError:\n    print('fine')\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.stdout.strip() == "fine", r.stderr

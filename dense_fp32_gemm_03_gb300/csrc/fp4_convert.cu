@@ -139,8 +139,9 @@ struct Piece {
   }
 };
 
+// Four blocks an SM, that is 64 registers: with 72 three run, and 8192^2 nvfp4 fp32 takes 50.6 us, not 47.8.
 template <typename T, int kFormat, bool kAligned>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     quantize_kernel(const T* __restrict__ x, int64_t ldx, const float* __restrict__ factor, int rows,
                     int cols, uint8_t* __restrict__ codes, int64_t ld, uint8_t* __restrict__ scales) {
   using F = Format<kFormat>;
@@ -321,7 +322,9 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Blocks that cover the pieces once, or as many as run at once: those walk on.
+// Blocks that cover the pieces once, or eight an SM, whose warps walk on: four to six run at once
+// (40 to 64 registers), the others follow and even out the end.  8192^2 nvfp4 fp32 there and
+// back with 4, 8 and 16 an SM: 137, 112 and 108 us; 1000 x 5003: 12.5, 11.4 and 12.3.
 unsigned grid_of(int64_t rows, int pieces, int sms) {
   const int64_t blocks = (rows * pieces + kWarps - 1) / kWarps, most = int64_t(sms) * 8;
   return unsigned(blocks < most ? blocks : most);

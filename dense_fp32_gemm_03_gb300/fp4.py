@@ -314,7 +314,8 @@ def fp4_linear(x, W, x_scale=None, out=None, stream=None):
     """y = Q(x) @ W.T: x (M x K) quantised in W's format within the call, W an :class:`Fp4Matrix` (N x K).
 
     ``x_scale`` is nvfp4's factor for x.  y has x's type.  The result is that
-    of :func:`fp4_quantize` followed by :func:`fp4_gemm`.
+    of :func:`fp4_quantize` followed by :func:`fp4_gemm` (up to M = 16 with the
+    32-bit sums in another order).
     """
     _quantized(W, "W")
     n, k = W.shape

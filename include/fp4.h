@@ -103,7 +103,8 @@ sgemm_status_t fp4_gemm(const fp4_matrix_t *A, const fp4_matrix_t *B, int dtype,
  * y = Q(x) * W^T: x (M x W->cols, type `dtype`, row stride ldx) is quantised
  * in W's format, with factor x_factor (device pointer, NULL: 1) for
  * FP4_NVFP4, and multiplied by W (N x K); y (M x N, row stride ldy) has x's
- * type.  The result is that of fp4_quantize() and fp4_gemm().
+ * type.  The result is that of fp4_quantize() and fp4_gemm(), up to M = 16 with the 32-bit
+ * sums in another order.
  */
 sgemm_status_t fp4_linear(int dtype, const void *x, int64_t ldx, int64_t M, const float *x_factor,
                           const fp4_matrix_t *W, void *y, int64_t ldy, cudaStream_t stream);

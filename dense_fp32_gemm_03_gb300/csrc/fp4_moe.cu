@@ -14,8 +14,8 @@
 // block grows by 1.42 or 1.6 a term at most).  With 5 terms (bfloat16) the rest is
 // about 2^-16 of the block's largest value in the mean and 2^-13 at most, with 6 (16-bit
 // float) 2^-19 and 2^-16, with 8 (32 bits) 2^-25 and 2^-22.  (bfloat16 with 4 terms, 2^-13 in
-// the mean, rounded a few per cent of the outputs the other way: 1 token 15.7 us, 16 tokens
-// 142.1; with 5 16.1 and 143.1, with 6 16.6 and 145.3.)  A token and term is one column of
+// the mean, rounded a few per cent of the outputs the other way: 1 token 15.5 us, 16 tokens
+// 142.2; with 5 15.9 and 142.8, with 6 16.3 and 145.0.)  A token and term is one column of
 // the product, and the columns' 32-bit sums are added with their powers of 8 at the end.
 //
 // nvfp4's units reach from 2^-6 to 448 at full precision (2^-9 at less), so each token's
@@ -26,13 +26,13 @@
 // weights and of x, which is checked: phase 2 also keeps h in 32 bits and finds each
 // token's largest value, the barrier behind it carries one bit a token that says whether
 // some value was high enough and one for too high, and tokens whose guess was off are
-// written again with the measured power of two (a pass over h and a barrier: 4 us with 1
-// token of 64 experts of 2048 x 768, 10 with 16 of 4096 x 2048).
+// written again with the measured power of two (a pass over h between two more barriers: 5 us
+// with 1 token of 64 experts of 2048 x 768, 10 with 16 of 4096 x 2048).
 //
 // What bounds it, measured.  16 tokens (nvfp4, 64 experts of 4096 x 2048, top 8: 800 MB of
-// weights) take 143 us, 5.6 TB/s; about 10 us of that are the start, the two grid barriers
+// weights) take 142.5 us, 5.6 TB/s; about 10 us of that are the start, the two grid barriers
 // and the last sums, between which nothing streams.  One token (64 of 2048 x 768: 22 MB) takes
-// 16.1 us, a chain of latencies: the router (3 us), a barrier (1), the selection (1), the first
+// 15.9 us, a chain of latencies: the router (3 us), a barrier (1), the selection (1), the first
 // weights' round to memory, sums and h (5), a barrier (1), the second products and sums (4).
 #include <cuda_runtime.h>
 
@@ -442,9 +442,11 @@ __device__ __forceinline__ bool grid_barrier(uint64_t* word, const MoeArgs& args
     const uint32_t mine = flags();
     __syncwarp();
     if (threadIdx.x == 0) {
+      // The fence covers the CTA's writes, which the barrier above ordered before it.  The two
+      // updates of one word stay in their order without another wait for the first to arrive.
+      asm volatile("fence.acq_rel.gpu;" ::: "memory");
       if (mine != 0) asm volatile("red.relaxed.gpu.global.or.b64 [%0], %1;" ::"l"(word), "l"(uint64_t(mine) << 32) : "memory");
-      // The release covers the CTA's writes, which the barrier above ordered before it.
-      asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(word), "l"(uint64_t(1)) : "memory");
+      asm volatile("red.relaxed.gpu.global.add.u64 [%0], %1;" ::"l"(word), "l"(uint64_t(1)) : "memory");
       uint32_t ok = 1;
       uint64_t seen;
       const uint64_t t0 = dev::global_timer_ns();
@@ -528,7 +530,7 @@ __device__ __forceinline__ float read_terms(uint32_t taddr) {
 //     token turns x into terms.
 //  2. Every CTA selects the experts (the same way).  Units are (expert in use,
 //     64 values of h); a stage is 256 columns of x.  Where h's powers of two were guessed
-//     wrong, its terms are written again, behind one barrier more.
+//     wrong, its terms are written again, between two more barriers.
 //  3. Units are 128 rows of y; the stages run over all experts in use, h of a token
 //     that does not go to one being zero there.
 // In phases 2 and 3 one thread streams stages (weights and columns, one bulk copy
@@ -1037,7 +1039,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     if (lane < tokens) {
       const uint32_t most = sm.h_max[lane];
       const int exponent = int(most >> 23) - 127 + sm.h_exp[lane];
-      if (most != 0) asm volatile("red.relaxed.gpu.global.max.u32 [%0], %1;" ::"l"(args.h_max + lane), "r"(most) : "memory");
       seen = most >= 0x7f800000u || (most != 0 && exponent >= W::kLow);
       over = most < 0x7f800000u && exponent >= W::kHigh;
     }
@@ -1047,6 +1048,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
   const uint32_t off = ok ? (~sm.flag[1] | sm.flag[1] >> 16) & ((1u << tokens) - 1u) : 0u;
   if (off != 0) {
     // The same in every CTA: h's terms again, with the tokens' largest values in [2^(kHigh - 1), 2^kHigh).
+    if (threadIdx.x < tokens)
+      asm volatile("red.relaxed.gpu.global.max.u32 [%0], %1;" ::"l"(args.h_max + threadIdx.x), "r"(sm.h_max[threadIdx.x])
+                   : "memory");
+    ok = grid_barrier(words + 2, args, sm.flag, [] { return 0u; });
+  }
+  if (off != 0 && ok) {
     if (threadIdx.x < tokens && (off >> threadIdx.x & 1u) != 0) {
       const uint32_t most = __ldcg(args.h_max + threadIdx.x);
       constexpr int kTop = kFormat == FP4_NVFP4 ? W::kHigh - 1 : W::kAim;
@@ -1069,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
                                         cols, uint32_t(t * kTerms), uint32_t(chunk % 8) * 32, lane);
     }
     fence_proxy_async_all();
-    ok = grid_barrier(words + 2, args, sm.flag, [] { return 0u; });
+    ok = grid_barrier(words + 3, args, sm.flag, [] { return 0u; });
   }
   if (!ok) sm.abort = 1;
 
@@ -1111,9 +1118,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const MoeArgs args) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
   // The last CTA to leave clears the barriers' counters for the next call.
-  if (threadIdx.x == 0 && atomicAdd(args.counters + 6, 1) == ctas - 1) {
-    words[0] = words[1] = words[2] = 0;
-    args.counters[6] = 0;
+  if (threadIdx.x == 0 && atomicAdd(args.counters + 8, 1) == ctas - 1) {
+    words[0] = words[1] = words[2] = words[3] = 0;
+    args.counters[8] = 0;
   }
 }
 

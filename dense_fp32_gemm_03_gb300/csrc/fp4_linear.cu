@@ -15,7 +15,7 @@
 // Roles: warp 0 streams W, warp 1 issues the MMAs, warps 2 to 5 join and store,
 // the others quantise x.
 //
-// What bounds it, measured.  1 x 4096 x 4096 (nvfp4, bf16; 9.4 MB) takes 5.4 to 6.3 us, of which
+// What bounds it, measured.  1 x 4096 x 4096 (nvfp4, bf16; 9.4 MB) takes 5.4 to 6.4 us, of which
 // the bytes are 1.4: launch, quantising x beside the first copies, one round to memory, the
 // cluster's sum.  16 x 8192 x 8192 (mxfp4; 36 MB) takes 10.0 to 11.9 us, the bytes 5.3.
 #include <cuda.h>

@@ -11,8 +11,9 @@
  *
  *   FP4_MXFP4  blocks of 32, a scale byte b, u = 2^(b - 127); 255 means NaN.
  *   FP4_NVFP4  blocks of 16, a scale byte that is an unsigned 8-bit float s (4
- *              exponent bits, bias 7, 3 fraction bits; 127 means NaN), and one
- *              32-bit factor g of the whole matrix; u = s * g.
+ *              exponent bits, bias 7, 3 fraction bits; 127 means NaN, from 128 on
+ *              a byte is no scale), and one 32-bit factor g >= 0 of the whole
+ *              matrix; u = s * g.
  *
  * Quantising a block whose largest magnitude is a gives
  *

@@ -1,0 +1,527 @@
+// int8_convert.cu -- conversions of the 8-bit integer operators: rows to
+// integers and back, operands of the products, checkpoints, and the gated
+// activation that keeps its inputs in 8 bits.
+//
+// All of them are bound by memory: each element is read once and written once.  A
+// thread takes eight consecutive values (16 bytes of 16-bit types, 8 of integers) at a time.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "int8_device.cuh"
+#include "int8_internal.h"
+
+namespace gb300 {
+namespace {
+
+using namespace int8;
+
+constexpr int kThreads = 256;
+
+bool aligned16(const void* p, int64_t ld_bytes) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld_bytes % 16 == 0; }
+
+// Waits for the kernel before on the stream; the next one may then set itself up beside this one.
+__device__ __forceinline__ void begin() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t stream, const A&... args) {
+  if (grid <= 0) return cudaSuccess;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid), 1, 1);
+  cfg.blockDim = dim3(unsigned(threads), 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+#define GB300_INT8_BY_TYPE(dtype, call)      \
+  switch (dtype) {                           \
+    case INT8_F32: {                         \
+      using T = float;                       \
+      return call;                           \
+    }                                        \
+    case INT8_BF16: {                        \
+      using T = __nv_bfloat16;               \
+      return call;                           \
+    }                                        \
+    default: {                               \
+      using T = __half;                      \
+      return call;                           \
+    }                                        \
+  }
+
+// ------------------------------------------------------------------------- rows
+enum RowForm { kBytes, kWide };  // integers as bytes, or as 16-bit floats
+
+struct RowArgs {
+  const void* x;
+  int64_t ldx;
+  int64_t rows, cols;
+  void* out;
+  int64_t ld;  // of out, in its elements
+  float* scales;
+  int32_t vec;
+};
+
+// kGroup threads to a row: the row's first 32 kGroup values stay in registers between the search
+// for the largest and the rounding, the rest is read again (from L2).
+template <typename T, int kGroup, RowForm kForm>
+__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads) rows_kernel(const RowArgs a) {
+  begin();
+  constexpr int kRows = kGroup >= kThreads ? 1 : kThreads / kGroup, kKept = 4;
+  const int t = threadIdx.x % kGroup;
+  const int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / kGroup;
+  if (kGroup <= 32 && row >= a.rows) return;  // whole warps
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const int64_t chunks = (a.cols + 7) / 8;
+  float v[kKept][8], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int64_t c = t + i * kGroup;
+    if (c < chunks) {
+      load8(x + 8 * c, a.cols - 8 * c, a.vec, v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+    }
+    top = max_abs(top, largest8(v[i]));
+  }
+#pragma unroll 1
+  for (int64_t c = t + kKept * kGroup; c < chunks; c += kGroup) {
+    float w[8];
+    load8(x + 8 * c, a.cols - 8 * c, a.vec, w);
+    top = max_abs(top, largest8(w));
+  }
+#pragma unroll
+  for (int d = 16; d; d /= 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if constexpr (kGroup > 32) {
+    __shared__ float warps[kGroup / 32];
+    if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = top;
+    __syncthreads();
+    top = warps[threadIdx.x % (kGroup / 32)];
+#pragma unroll
+    for (int d = kGroup / 64; d; d /= 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, d));
+  }
+  const float s = row_scale(top), inv = __frcp_rn(s);
+  if (t == 0) a.scales[row] = s;
+  const int64_t out_chunks = kForm == kBytes ? (a.cols + 15) / 16 * 2 : chunks;
+  auto write = [&](int64_t c, const float (&w)[8]) {
+    int q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = nearest(w[e], s, inv);
+    if constexpr (kForm == kBytes) {
+      *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.out) + row * a.ld + 8 * c) =
+          make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+    } else {
+      uint4 h;
+      __half2* p = reinterpret_cast<__half2*>(&h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = __halves2half2(__int2half_rn(q[2 * e]), __int2half_rn(q[2 * e + 1]));
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.ld + 8 * c) = h;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (t + i * kGroup < out_chunks) write(t + i * kGroup, v[i]);
+#pragma unroll 1
+  for (int64_t c = t + kKept * kGroup; c < out_chunks; c += kGroup) {
+    float w[8];
+    load8(x + 8 * c, a.cols - 8 * c, a.vec, w);
+    write(c, w);
+  }
+}
+
+template <RowForm kForm>
+cudaError_t launch_rows(int dtype, const RowArgs& a, cudaStream_t stream) {
+  const int64_t few = (a.rows + kThreads / 32 - 1) / (kThreads / 32);
+  if (a.cols <= 1024) GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 32, kForm>, few, kThreads, stream, a))
+  if (a.cols <= 8192) GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 256, kForm>, a.rows, kThreads, stream, a))
+  GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 1024, kForm>, a.rows, 1024, stream, a))
+}
+
+struct BackArgs {
+  const int8_t* codes;
+  int64_t ld;
+  const float* scales;
+  int64_t rows, cols;
+  void* out;
+  int64_t ld_out;
+  int32_t vec;
+};
+
+// Chunks of eight over all threads; a chunk's row and place come from one division.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const BackArgs a) {
+  begin();
+  const int64_t chunks = (a.cols + 7) / 8, all = a.rows * chunks;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
+    const int64_t row = i / chunks, c = i - row * chunks;
+    const int2 w = *reinterpret_cast<const int2*>(a.codes + row * a.ld + 8 * c);
+    const float s = a.scales[row];
+    const int8_t* q = reinterpret_cast<const int8_t*>(&w);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = float(q[e]) * s;
+    store8(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, a.cols - 8 * c, a.vec, v);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) widen_kernel(const BackArgs a) {
+  begin();
+  const int64_t chunks = (a.cols + 7) / 8, all = a.rows * chunks;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
+    const int64_t row = i / chunks, c = i - row * chunks;
+    const int2 w = *reinterpret_cast<const int2*>(a.codes + row * a.ld + 8 * c);
+    const int8_t* q = reinterpret_cast<const int8_t*>(&w);
+    uint4 h;
+    __half* p = reinterpret_cast<__half*>(&h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = __int2half_rn(8 * c + e < a.cols ? q[e] : 0);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + 8 * c) = h;
+  }
+}
+
+// ---------------------------------------------------------------- gradients' terms
+struct SplitArgs {
+  const void* x;
+  int64_t ldx;
+  int64_t rows, cols;
+  uint16_t* out;
+  int64_t ld;
+  int32_t vec;
+};
+
+// The upper 16 bits of v's 32 (v's first eight significant bits), and v less that; a value that is
+// not finite is its own first term.
+__device__ __forceinline__ uint32_t take16(float& v) {
+  const uint32_t b = __float_as_uint(v);
+  if ((b & 0x7fffffffu) >= 0x7f800000u) {
+    v = 0.f;
+    return (b & 0x7fffffffu) > 0x7f800000u ? 0x7fc0u : b >> 16;
+  }
+  v -= __uint_as_float(b & 0xffff0000u);
+  return b >> 16;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
+  begin();
+  const int64_t chunks = (a.cols + 7) / 8, all = a.rows * chunks;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
+    const int64_t row = i / chunks, c = i - row * chunks;
+    float v[8];
+    load8(static_cast<const T*>(a.x) + row * a.ldx + 8 * c, a.cols - 8 * c, a.vec, v);
+    uint16_t* out = a.out + row * a.ld + 8 * c;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        uint4 w;
+        uint16_t* p = reinterpret_cast<uint16_t*>(&w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = uint16_t(take16(v[e]));
+        *reinterpret_cast<uint4*>(out + t * a.rows * a.ld) = w;
+      }
+    } else {
+      store8(reinterpret_cast<T*>(out), 8, true, v);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ checkpoints
+struct KeepArgs {
+  const void* x;
+  int64_t ldx;
+  int64_t rows, cols;
+  int8_t* codes;
+  int64_t ld;
+  uint16_t* units;
+  int64_t ldu;
+  int32_t vec;
+  int32_t tiles_t;
+};
+
+// A tile of 128 tokens x 128 channels, turned in shared memory.  A thread takes eight
+// channels of four tokens (a quarter of a block of 32), and writes for each channel
+// a word of four tokens; the word of tokens 4 m.. of channel k is at k * 32 + (m ^ 2 (k / 8 % 16)):
+// no two lanes of a warp (16 groups of channels, two m) meet in a bank, and 16-byte reads along a
+// channel find their four words within one group of four.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) keep_kernel(const KeepArgs a) {
+  begin();
+  constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
+  __shared__ uint32_t codes[128 * 32];
+  __shared__ __align__(16) uint16_t units[4][128];
+  const int64_t t0 = int64_t(blockIdx.x % a.tiles_t) * 128, k0 = int64_t(blockIdx.x / a.tiles_t) * 128;
+  const int g = threadIdx.x % 16;  // group of eight channels
+  const T* x = static_cast<const T*>(a.x) + k0 + 8 * g;
+  const int64_t left = a.cols - k0 - 8 * g;
+#pragma unroll 1
+  for (int m = threadIdx.x / 16; m < 32; m += kThreads / 16) {
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + 4 * m + i;
+      load8(x + t * a.ldx, t < a.rows ? left : 0, a.vec, v[i]);
+    }
+    int q[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float top = largest8(v[i]);
+      top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float inverse = unit_inverse<kHalf>(top);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[i][e] = kept(v[i][e], inverse);
+      if (g % 4 == 0) units[g / 4][4 * m + i] = t0 + 4 * m + i < a.rows ? uint16_t(unit_bits<kHalf>(top)) : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) codes[(8 * g + e) * 32 + (m ^ (2 * g))] = pack4(q[0][e], q[1][e], q[2][e], q[3][e]);
+  }
+  __syncthreads();
+  // 16 tokens of a channel a thread; `ld` covers the tokens rounded up to 16.
+  const int64_t end = (a.rows + 15) / 16 * 16;
+#pragma unroll
+  for (int i = 0; i < 128 * 8 / kThreads; ++i) {
+    const int k = (threadIdx.x + i * kThreads) / 8, p = threadIdx.x % 8, s = 2 * (k / 8);
+    if (k0 + k < a.cols && t0 + 16 * p < end) {
+      uint4 w = *reinterpret_cast<const uint4*>(&codes[k * 32 + ((4 * p) ^ (s & ~3))]);
+      if (s & 2) w = make_uint4(w.z, w.w, w.x, w.y);
+      *reinterpret_cast<uint4*>(a.codes + (k0 + k) * a.ld + t0 + 16 * p) = w;
+    }
+  }
+  if (threadIdx.x < 64) {
+    const int b = threadIdx.x / 16, p = threadIdx.x % 16;
+    if (k0 + 32 * b < a.cols && t0 + 8 * p < (a.rows + 7) / 8 * 8)
+      *reinterpret_cast<uint4*>(a.units + (k0 / 32 + b) * a.ldu + t0 + 8 * p) = *reinterpret_cast<const uint4*>(&units[b][8 * p]);
+  }
+}
+
+struct RestoreArgs {
+  const int8_t* codes;
+  int64_t ld;
+  const uint16_t* units;
+  int64_t ldu;
+  int64_t rows, cols;
+  int32_t half;
+  void* out;
+  int64_t ld_out;
+  int32_t vec;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) restore_tokens_kernel(const RestoreArgs a) {
+  begin();
+  const int64_t chunks = (a.cols + 7) / 8, all = a.rows * chunks;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
+    const int64_t row = i / chunks, c = i - row * chunks;
+    const int2 w = *reinterpret_cast<const int2*>(a.codes + row * a.ld + 8 * c);
+    const float u = unit_value(a.units[row * a.ldu + c / 4], a.half);
+    const int8_t* q = reinterpret_cast<const int8_t*>(&w);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = float(q[e]) * u;
+    store8(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, a.cols - 8 * c, a.vec, v);
+  }
+}
+
+// Tiles of 32 channels (a block) x 64 tokens: reads 16 tokens of a channel, writes 8 channels of a token.
+template <typename T>
+__global__ void __launch_bounds__(128) restore_channels_kernel(const RestoreArgs a) {
+  begin();
+  __shared__ int8_t tile[32][68];
+  const int64_t blocks = (a.cols + 31) / 32, tiles = (a.rows + 63) / 64 * blocks;
+  for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+    const int64_t t0 = i / blocks * 64, b = i % blocks;
+    const int k = threadIdx.x / 4, p = threadIdx.x % 4;
+    int4 w = make_int4(0, 0, 0, 0);
+    if (32 * b + k < a.cols && t0 + 16 * p < a.rows)
+      w = *reinterpret_cast<const int4*>(a.codes + (32 * b + k) * a.ld + t0 + 16 * p);
+    int32_t* to = reinterpret_cast<int32_t*>(&tile[k][16 * p]);
+    to[0] = w.x, to[1] = w.y, to[2] = w.z, to[3] = w.w;
+    __syncthreads();
+    for (int j = threadIdx.x; j < 256; j += 128) {
+      const int t = j / 4, c = j % 4;
+      if (t0 + t < a.rows) {
+        const float u = unit_value(a.units[b * a.ldu + t0 + t], a.half);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = float(tile[8 * c + e][t]) * u;
+        store8(static_cast<T*>(a.out) + (t0 + t) * a.ld_out + 32 * b + 8 * c, a.cols - 32 * b - 8 * c, a.vec, v);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------- gated activation
+struct SwigluArgs {
+  const void *gate, *up;
+  int64_t ldg, ldu;
+  int64_t rows, cols;
+  void* h;
+  int64_t ldh;
+  int8_t *kg, *ku;
+  int64_t ldkg, ldku;
+  uint16_t *ug, *uu;
+  int64_t ldug, lduu;
+  int32_t vec;
+};
+
+__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.f + expf(-x)); }
+
+// Keeps eight of a block's values (the four lanes of a block together).
+template <bool kHalf>
+__device__ __forceinline__ void keep8(const float (&v)[8], int8_t* codes, uint16_t* unit, bool first, bool write) {
+  float top = largest8(v);
+  top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const float inverse = unit_inverse<kHalf>(top);
+  int q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = kept(v[e], inverse);
+  if (write) *reinterpret_cast<uint2*>(codes) = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+  if (write && first) *unit = uint16_t(unit_bits<kHalf>(top));
+}
+
+// Four lanes to a block; columns rounded up to whole blocks so that a block's lanes stay together.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
+  begin();
+  constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
+  const int64_t blocks = (a.cols + 31) / 32, chunks = 4 * blocks, all = a.rows * chunks;
+  for (int64_t i0 = int64_t(blockIdx.x) * kThreads; i0 < all; i0 += int64_t(gridDim.x) * kThreads) {
+    const int64_t i = i0 + threadIdx.x;
+    const bool here = i < all;
+    const int64_t row = here ? i / chunks : 0, c = here ? i - row * chunks : 0, left = here ? a.cols - 8 * c : 0;
+    float g[8], u[8], h[8];
+    load8(static_cast<const T*>(a.gate) + row * a.ldg + 8 * c, left, a.vec, g);
+    load8(static_cast<const T*>(a.up) + row * a.ldu + 8 * c, left, a.vec, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = g[e] * sigmoid(g[e]) * u[e];
+    if (left > 0) store8(static_cast<T*>(a.h) + row * a.ldh + 8 * c, left, a.vec, h);
+    const bool write = here && 8 * c < (a.cols + 15) / 16 * 16;
+    keep8<kHalf>(g, a.kg + row * a.ldkg + 8 * c, a.ug + row * a.ldug + c / 4, c % 4 == 0, write);
+    keep8<kHalf>(u, a.ku + row * a.ldku + 8 * c, a.uu + row * a.lduu + c / 4, c % 4 == 0, write);
+    // Units that pad the row.
+    if (here && c % 4 == 0 && c / 4 == blocks - 1)
+      for (int64_t b = blocks; b < (blocks + 7) / 8 * 8; ++b) a.ug[row * a.ldug + b] = a.uu[row * a.lduu + b] = 0;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluArgs a, const T* dh, int64_t lddh, T* dgate,
+                                                                   int64_t lddg, T* dup, int64_t lddu) {
+  begin();
+  constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
+  const int64_t chunks = (a.cols + 7) / 8, all = a.rows * chunks;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
+    const int64_t row = i / chunks, c = i - row * chunks, left = a.cols - 8 * c;
+    const int2 wg = *reinterpret_cast<const int2*>(a.kg + row * a.ldkg + 8 * c);
+    const int2 wu = *reinterpret_cast<const int2*>(a.ku + row * a.ldku + 8 * c);
+    const float ug = unit_value(a.ug[row * a.ldug + c / 4], kHalf), uu = unit_value(a.uu[row * a.lduu + c / 4], kHalf);
+    float d[8], dg[8], du[8];
+    load8(dh + row * lddh + 8 * c, left, a.vec, d);
+    const int8_t *qg = reinterpret_cast<const int8_t*>(&wg), *qu = reinterpret_cast<const int8_t*>(&wu);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float g = float(qg[e]) * ug, u = float(qu[e]) * uu, s = sigmoid(g);
+      dg[e] = d[e] * u * s * (1.f + g * (1.f - s));
+      du[e] = d[e] * (g * s);
+    }
+    store8(dgate + row * lddg + 8 * c, left, a.vec, dg);
+    store8(dup + row * lddu + 8 * c, left, a.vec, du);
+  }
+}
+
+int64_t spread(int64_t items, int sms) { return std::min((items + kThreads - 1) / kThreads, int64_t(sms) * 8); }
+int64_t bytes_of(int dtype) { return dtype == INT8_F32 ? 4 : 2; }
+
+}  // namespace
+
+cudaError_t launch_int8_quantize(int dtype, const void* x, int64_t ldx, const int8_matrix_t& q, cudaStream_t stream) {
+  const RowArgs a{x, ldx, q.rows, q.cols, q.codes, q.ld, q.scales, aligned16(x, ldx * bytes_of(dtype))};
+  return launch_rows<kBytes>(dtype, a, stream);
+}
+
+cudaError_t launch_int8_rows16(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
+                               int64_t ld, float* scales, cudaStream_t stream) {
+  const RowArgs a{x, ldx, rows, cols, out, ld, scales, aligned16(x, ldx * bytes_of(dtype))};
+  return launch_rows<kWide>(dtype, a, stream);
+}
+
+cudaError_t launch_int8_dequantize(const int8_matrix_t& q, int dtype, void* y, int64_t ldy, int sms,
+                                   cudaStream_t stream) {
+  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, y, ldy, aligned16(y, ldy * bytes_of(dtype))};
+  const int64_t grid = spread(q.rows * ((q.cols + 7) / 8), sms);
+  GB300_INT8_BY_TYPE(dtype, launch(dequantize_kernel<T>, grid, kThreads, stream, a))
+}
+
+cudaError_t launch_int8_widen(const int8_matrix_t& q, uint16_t* out, int64_t ld, int sms, cudaStream_t stream) {
+  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, out, ld, 1};
+  return launch(widen_kernel, spread(q.rows * ((q.cols + 7) / 8), sms), kThreads, stream, a);
+}
+
+int int8_terms(int dtype) { return dtype == INT8_F32 ? 3 : 1; }
+
+cudaError_t launch_int8_split(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
+                              int64_t ld, int sms, cudaStream_t stream) {
+  const SplitArgs a{x, ldx, rows, cols, out, ld, aligned16(x, ldx * bytes_of(dtype))};
+  const int64_t grid = spread(rows * ((cols + 7) / 8), sms);
+  GB300_INT8_BY_TYPE(dtype, launch(split_kernel<T>, grid, kThreads, stream, a))
+}
+
+cudaError_t launch_int8_keep(const void* x, int64_t ldx, const int8_checkpoint_t& c, cudaStream_t stream) {
+  const int64_t tiles_t = (c.rows + 127) / 128, tiles = tiles_t * ((c.cols + 127) / 128);
+  const KeepArgs a{x, ldx, c.rows, c.cols, c.codes, c.ld, c.units, c.ld_units, aligned16(x, ldx * bytes_of(c.dtype)),
+                   int32_t(tiles_t)};
+  GB300_INT8_BY_TYPE(c.dtype, launch(keep_kernel<T>, tiles, kThreads, stream, a))
+}
+
+cudaError_t launch_int8_restore(const int8_checkpoint_t& c, int dtype, void* y, int64_t ldy, int sms,
+                                cudaStream_t stream) {
+  const RestoreArgs a{c.codes, c.ld, c.units, c.ld_units, c.rows, c.cols, c.dtype == INT8_F16, y, ldy,
+                      aligned16(y, ldy * bytes_of(dtype))};
+  if (c.order == INT8_TOKENS) {
+    const int64_t grid = spread(c.rows * ((c.cols + 7) / 8), sms);
+    GB300_INT8_BY_TYPE(dtype, launch(restore_tokens_kernel<T>, grid, kThreads, stream, a))
+  }
+  const int64_t tiles = std::min((c.rows + 63) / 64 * ((c.cols + 31) / 32), int64_t(sms) * 16);
+  GB300_INT8_BY_TYPE(dtype, launch(restore_channels_kernel<T>, tiles, 128, stream, a))
+}
+
+cudaError_t launch_int8_swiglu(int dtype, int64_t M, int64_t F, const void* gate, int64_t ldg, const void* up,
+                               int64_t ldu, void* h, int64_t ldh, const int8_checkpoint_t& kg,
+                               const int8_checkpoint_t& ku, int sms, cudaStream_t stream) {
+  const int64_t es = bytes_of(dtype);
+  const SwigluArgs a{gate, up, ldg, ldu, M, F, h, ldh, kg.codes, ku.codes, kg.ld, ku.ld, kg.units, ku.units,
+                     kg.ld_units, ku.ld_units,
+                     aligned16(gate, ldg * es) && aligned16(up, ldu * es) && aligned16(h, ldh * es)};
+  const int64_t grid = spread(M * ((F + 31) / 32) * 4, sms);
+  GB300_INT8_BY_TYPE(dtype, launch(swiglu_kernel<T>, grid, kThreads, stream, a))
+}
+
+cudaError_t launch_int8_swiglu_backward(const void* dh, int64_t lddh, const int8_checkpoint_t& kg,
+                                        const int8_checkpoint_t& ku, void* dgate, int64_t ldg, void* dup, int64_t ldu,
+                                        int sms, cudaStream_t stream) {
+  const int64_t es = bytes_of(kg.dtype);
+  SwigluArgs a{};
+  a.rows = kg.rows;
+  a.cols = kg.cols;
+  a.kg = kg.codes, a.ku = ku.codes, a.ldkg = kg.ld, a.ldku = ku.ld;
+  a.ug = kg.units, a.uu = ku.units, a.ldug = kg.ld_units, a.lduu = ku.ld_units;
+  a.vec = aligned16(dh, lddh * es) && aligned16(dgate, ldg * es) && aligned16(dup, ldu * es);
+  const int64_t grid = spread(kg.rows * ((kg.cols + 7) / 8), sms);
+  GB300_INT8_BY_TYPE(kg.dtype,
+                     launch(swiglu_backward_kernel<T>, grid, kThreads, stream, a, static_cast<const T*>(dh), lddh,
+                            static_cast<T*>(dgate), ldg, static_cast<T*>(dup), ldu))
+}
+
+}  // namespace gb300

@@ -1,0 +1,112 @@
+// int8_device.cuh -- device helpers of the 8-bit integer operators: loads of
+// eight values, quantisation of a row's and of a block's values.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "fp4_device.cuh"
+#include "int8.h"
+
+namespace gb300 {
+namespace int8 {
+
+using fp4::from_f32;
+using fp4::max_abs;
+using fp4::to_f32;
+
+constexpr int kBlock = 32;  // channels that share a checkpoint's unit
+
+// Eight consecutive values from p on in 32 bits, of which `left` exist (the others are 0); `vec`: p is 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int64_t left, bool vec, float (&v)[8]) {
+  if (vec && left >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      const uint4 w = *reinterpret_cast<const uint4*>(p);
+      const T* t = reinterpret_cast<const T*>(&w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(p[i]) : 0.f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int64_t left, bool vec, const float (&v)[8]) {
+  if (vec && left >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint4 w;
+      T* t = reinterpret_cast<T*>(&w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = from_f32<T>(v[i]);
+      *reinterpret_cast<uint4*>(p) = w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = from_f32<T>(v[i]);
+  }
+}
+
+__device__ __forceinline__ float largest8(const float (&v)[8]) {
+  return max_abs(max_abs(max_abs(v[0], v[1]), max_abs(v[2], v[3])), max_abs(max_abs(v[4], v[5]), max_abs(v[6], v[7])));
+}
+
+__device__ __forceinline__ bool finite(float a) { return __float_as_uint(a) < 0x7f800000u; }  // of a >= 0
+
+// The integer nearest to x / s, ties to even, for |x| <= 127 s (1 + 2^-22) and s >= 2^-126,
+// with inv the rounded reciprocal of s.  x inv is within 2^-15 of x / s, so its nearest
+// integer n is the answer or next to it, and the remainder x - n s says which: it is a
+// multiple of the last place of s and at most s, so that the fma gives it exactly.
+__device__ __forceinline__ int nearest(float x, float s, float inv) {
+  const float n = rintf(x * inv), r = fmaf(-n, s, x), h = 0.5f * s;
+  int q = int(n);
+  if (fabsf(r) > h || (fabsf(r) == h && (q & 1))) q += r > 0.f ? 1 : -1;
+  return q;
+}
+
+// A row's scale (NaN unless every value is finite) from its largest magnitude.
+__device__ __forceinline__ float row_scale(float a) {
+  return finite(a) ? fmaxf(a * (1.f / 127.f), 0x1p-126f) : __uint_as_float(0x7fffffffu);
+}
+
+// Four integers in bytes, the first lowest.
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+  return __byte_perm(__byte_perm(uint32_t(a), uint32_t(b), 0x0040), __byte_perm(uint32_t(c), uint32_t(d), 0x0040), 0x5410);
+}
+
+// Exponent of a block's unit from its largest magnitude (finite).
+template <bool kHalf>
+__device__ __forceinline__ int unit_exponent(float a) {
+  return max(int(__float_as_uint(a) >> 23) - 127 - 6, kHalf ? -24 : -126);  // the field of a subnormal clamps too
+}
+// The unit's 16 bits: bfloat16, or a 16-bit float (-24 to 9: subnormal below -14).
+template <bool kHalf>
+__device__ __forceinline__ uint32_t unit_bits(float a) {
+  if (!finite(a)) return kHalf ? 0x7e00u : 0x7fc0u;
+  const int e = unit_exponent<kHalf>(a);
+  return kHalf ? (e >= -14 ? uint32_t(e + 15) << 10 : 1u << (e + 24)) : uint32_t(e + 127) << 7;
+}
+__device__ __forceinline__ float unit_value(uint32_t bits, bool half) {
+  return half ? __half2float(__ushort_as_half(uint16_t(bits))) : __uint_as_float(bits << 16);
+}
+// What a block's values are multiplied by before they are rounded: 1 / u (exact; 0 where the block is not finite).
+template <bool kHalf>
+__device__ __forceinline__ float unit_inverse(float a) {
+  return finite(a) ? __uint_as_float(uint32_t(127 - unit_exponent<kHalf>(a)) << 23) : 0.f;
+}
+// x / u rounded to an integer; not finite only if its block is not (x * 0 = NaN becomes 0 in the conversion).
+__device__ __forceinline__ int kept(float x, float inverse) { return max(-127, min(127, __float2int_rn(x * inverse))); }
+
+}  // namespace int8
+}  // namespace gb300

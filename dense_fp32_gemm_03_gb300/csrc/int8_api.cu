@@ -2,8 +2,11 @@
 // (include/int8.h): argument validation, scratch and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <initializer_list>
+#include <map>
+#include <mutex>
 
 #include "int8.h"
 #include "int8_internal.h"
@@ -123,25 +126,97 @@ struct Scratch {
   }
 };
 
-// y (M x N) = A W^T, from A's rows as 16-bit floats.
-gb300::Int8Product integer_product(const int8_matrix_t& W, int64_t M, const uint16_t* rows16, int64_t ld16, const float* scales,
-                                   int dtype, void* y, int64_t ldy) {
-  gb300::Int8Product p{};
-  p.rows = int32_t(W.rows);
-  p.cols = int32_t(M);
-  p.depth = int32_t(W.cols);
-  p.a = W.codes;
-  p.lda = W.ld;
-  p.b = rows16;
-  p.ldb = ld16;
-  p.half = 1;
-  p.terms = 1;
-  p.scale_r = W.scales;
-  p.scale_c = scales;
-  p.dtype = dtype;
-  p.out = y;
-  p.ld = ldy;
-  return p;
+// ------------------------------------------------------------------- products
+std::mutex g_mu;
+std::map<int, int> g_pairs;  // CTA pairs that run at once, by device
+
+int tc_pairs(int dev) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  auto it = g_pairs.find(dev);
+  if (it == g_pairs.end()) it = g_pairs.emplace(dev, gb300::int8_tc_prepare()).first;
+  return it->second;
+}
+
+// A product's operands (int8_internal.h), before it is planned.
+struct Operands {
+  const int8_t* a;
+  int64_t lda;
+  const uint16_t* units;  // NULL: integers
+  int64_t ldu;
+  const uint16_t* b;
+  int64_t ldb;
+  int terms;
+};
+
+// Tiles, and the shares that k is cut into where there are fewer tiles than pairs of CTAs: a share has
+// four stages of k at least, since its sums are written and read once more.
+sgemm_status_t plan(gb300::Int8TcShape shape, int64_t rows, int64_t cols, int64_t depth, int terms, int pairs,
+                    gb300::Int8TcArgs* a) {
+  const int64_t steps = round_up(depth, gb300::int8_tc_step()) / gb300::int8_tc_step();
+  const int64_t tr = (rows + 255) / 256, tc = (cols + gb300::int8_tc_cols(shape) - 1) / gb300::int8_tc_cols(shape), tiles = tr * tc;
+  if (pairs <= 0) return SGEMM_ERR_LAUNCH;
+  if (tiles > 0x3fffffffLL || terms * depth > 0x7fffffffLL) return SGEMM_ERR_UNSUPPORTED;
+  a->rows = int32_t(rows);
+  a->cols = int32_t(cols);
+  a->depth = int32_t(depth);
+  a->steps = int32_t(steps);
+  a->steps_all = int32_t(steps * terms);
+  a->tiles_r = int32_t(tr);
+  a->tiles_c = int32_t(tc);
+  a->splits = int32_t(std::max<int64_t>(1, std::min(pairs / tiles, steps * terms / 4)));
+  a->units = int32_t(tiles * a->splits);
+  return SGEMM_OK;
+}
+size_t partial_bytes(const gb300::Int8TcArgs& a) {
+  return a.splits > 1 ? size_t(a.splits) * size_t(a.rows) * size_t(a.cols) * 4 : 0;
+}
+
+sgemm_status_t run_product(gb300::Int8TcShape shape, const Operands& o, gb300::Int8TcArgs a, int pairs, const LibDevice& d,
+                           cudaStream_t stream) {
+  CUtensorMap maps[3];
+  const int64_t cols8 = round_up(a.cols, 8), depth8 = round_up(a.depth, 8);
+  sgemm_status_t st = gb300::lib_encode_bytes(o.a, a.rows, round_up(a.depth, 16), o.lda, 128, &maps[0]);
+  if (st != SGEMM_OK) return st;
+  if (o.units) {
+    st = gb300::lib_encode_bytes(o.units, (a.rows + 31) / 32, 2 * depth8, 2 * o.ldu, 4, &maps[1]);
+    if (st == SGEMM_OK) st = gb300::lib_encode_bytes(o.b, int64_t(o.terms) * a.depth, 2 * cols8, 2 * o.ldb, gb300::int8_tc_step(), &maps[2]);
+  } else {
+    maps[1] = maps[0];  // not used
+    st = gb300::lib_encode_bytes(o.b, a.cols, 2 * depth8, 2 * o.ldb, gb300::int8_tc_cols(shape) / 2, &maps[2]);
+  }
+  if (st != SGEMM_OK) return st;
+  a.status = d.status;
+  a.wait_limit_ns = d.wait_limit_ns;
+  return status_of(gb300::launch_int8_tc(shape, maps, a, pairs, d.sms, stream));
+}
+
+// C (M x N, row stride ldc) = A B^T, from A's rows as 16-bit floats or, with x, quantised on the way.
+sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* x, int64_t ldx, int64_t M, const int8_matrix_t& B,
+                               int dtype, void* C, int64_t ldc, const LibDevice& d, cudaStream_t stream) {
+  const gb300::Int8TcShape shape = M <= 32 ? gb300::kInt8Whole32 : M <= 64 ? gb300::kInt8Whole64 : gb300::kInt8Whole128;
+  const int pairs = tc_pairs(d.dev);
+  gb300::Int8TcArgs a{};
+  sgemm_status_t st = plan(shape, B.rows, M, B.cols, 1, pairs, &a);
+  if (st != SGEMM_OK) return st;
+  const int64_t ld16 = round_up(B.cols, 8);
+  Scratch s;
+  const size_t scales_at = s.take(M * 4), rows_at = s.take(M * ld16 * 2), partials_at = s.take(int64_t(partial_bytes(a)));
+  void* ws = nullptr;
+  st = gb300::lib_workspace(d.dev, stream, s.bytes, &ws);
+  if (st != SGEMM_OK) return st;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  uint16_t* rows16 = reinterpret_cast<uint16_t*>(base + rows_at);
+  float* scales = reinterpret_cast<float*>(base + scales_at);
+  const cudaError_t e = A ? gb300::launch_int8_widen(*A, rows16, ld16, d.sms, stream)
+                          : gb300::launch_int8_rows16(dtype_x, x, ldx, M, B.cols, rows16, ld16, scales, stream);
+  if (e != cudaSuccess) return SGEMM_ERR_LAUNCH;
+  a.scale_r = B.scales;
+  a.scale_c = A ? A->scales : scales;
+  a.dtype = dtype;
+  a.out = C;
+  a.ld = ldc;
+  a.partials = reinterpret_cast<uint32_t*>(base + partials_at);
+  return run_product(shape, Operands{B.codes, B.ld, nullptr, 0, rows16, ld16, 1}, a, pairs, d, stream);
 }
 
 }  // namespace
@@ -190,15 +265,7 @@ sgemm_status_t int8_gemm(const int8_matrix_t* A, const int8_matrix_t* B, int dty
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || A->rows == 0 || B->rows == 0) return st;
   if (A->cols == 0) return zero_output(dtype, C, A->rows, B->rows, ldc, stream);
-  const int64_t ld16 = round_up(A->cols, 8);
-  Scratch s;
-  const size_t at = s.take(A->rows * ld16 * 2);
-  void* ws = nullptr;
-  st = gb300::lib_workspace(d.dev, stream, s.bytes, &ws);
-  if (st != SGEMM_OK) return st;
-  uint16_t* rows16 = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + at);
-  if (gb300::launch_int8_widen(*A, rows16, ld16, d.sms, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-  return status_of(gb300::launch_int8_product(integer_product(*B, A->rows, rows16, ld16, A->scales, dtype, C, ldc), stream));
+  return integer_product(A, 0, nullptr, 0, A->rows, *B, dtype, C, ldc, d, stream);
 } GB300_INT8_CATCH
 
 sgemm_status_t int8_linear(int dtype, const void* x, int64_t ldx, int64_t M, const int8_matrix_t* W, void* y,
@@ -214,17 +281,7 @@ sgemm_status_t int8_linear(int dtype, const void* x, int64_t ldx, int64_t M, con
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || M == 0 || W->rows == 0) return st;
   if (W->cols == 0) return zero_output(dtype, y, M, W->rows, ldy, stream);
-  const int64_t ld16 = round_up(W->cols, 8);
-  Scratch s;
-  const size_t scales_at = s.take(M * 4), at = s.take(M * ld16 * 2);
-  void* ws = nullptr;
-  st = gb300::lib_workspace(d.dev, stream, s.bytes, &ws);
-  if (st != SGEMM_OK) return st;
-  uint8_t* base = static_cast<uint8_t*>(ws);
-  uint16_t* rows16 = reinterpret_cast<uint16_t*>(base + at);
-  float* scales = reinterpret_cast<float*>(base + scales_at);
-  if (gb300::launch_int8_rows16(dtype, x, ldx, M, W->cols, rows16, ld16, scales, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
-  return status_of(gb300::launch_int8_product(integer_product(*W, M, rows16, ld16, scales, dtype, y, ldy), stream));
+  return integer_product(nullptr, dtype, x, ldx, M, *W, dtype, y, ldy, d, stream);
 } GB300_INT8_CATCH
 
 sgemm_status_t int8_checkpoint_layout(int order, int64_t rows, int64_t cols, int64_t* ld, int64_t* ld_units,
@@ -278,35 +335,33 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || N == 0 || c->cols == 0) return st;
   if (c->rows == 0) return accumulate ? SGEMM_OK : zero_output(dtype, dw, N, c->cols, ldw, stream);
-  gb300::Int8Product p{};
-  p.rows = int32_t(c->cols);
-  p.cols = int32_t(N);
-  p.depth = int32_t(c->rows);
-  p.a = c->codes;
-  p.lda = c->ld;
-  p.units = c->units;
-  p.ldu = c->ld_units;
-  p.half = c->dtype == INT8_F16;
-  p.terms = gb300::int8_terms(c->dtype);
-  p.dtype = dtype;
-  p.accumulate = accumulate != 0;
-  p.out = dw;
-  p.ld = ldw;
-  if (p.terms == 1 && aligned(dy, 16) && lddy % 8 == 0) {  // read where it is
-    p.b = static_cast<const uint16_t*>(dy);
-    p.ldb = lddy;
-  } else {
-    p.ldb = round_up(N, 8);
-    Scratch s;
-    const size_t at = s.take(p.terms * c->rows * p.ldb * 2);
-    void* ws = nullptr;
-    st = gb300::lib_workspace(d.dev, stream, s.bytes, &ws);
-    if (st != SGEMM_OK) return st;
-    uint16_t* terms = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + at);
-    p.b = terms;
-    if (gb300::launch_int8_split(c->dtype, dy, lddy, c->rows, N, terms, p.ldb, d.sms, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+  // 32-bit results are added up 1024 products at a time.
+  const bool half = c->dtype == INT8_F16, runs = dtype == INT8_F32;
+  const gb300::Int8TcShape shape = half ? (runs ? gb300::kInt8F16Runs : gb300::kInt8F16) : (runs ? gb300::kInt8Bf16Runs : gb300::kInt8Bf16);
+  const int pairs = tc_pairs(d.dev), terms = gb300::int8_terms(c->dtype);
+  gb300::Int8TcArgs a{};
+  st = plan(shape, c->cols, N, c->rows, terms, pairs, &a);
+  if (st != SGEMM_OK) return st;
+  const bool in_place = terms == 1 && aligned(dy, 16) && (lddy % 8 == 0 || c->rows == 1);
+  Operands o{c->codes, c->ld, c->units, c->ld_units, static_cast<const uint16_t*>(dy), round_up(lddy, 8), terms};
+  if (!in_place) o.ldb = round_up(N, 8);
+  Scratch s;
+  const size_t terms_at = s.take(in_place ? 0 : terms * c->rows * o.ldb * 2), partials_at = s.take(int64_t(partial_bytes(a)));
+  void* ws = nullptr;
+  st = gb300::lib_workspace(d.dev, stream, s.bytes, &ws);
+  if (st != SGEMM_OK) return st;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  if (!in_place) {
+    uint16_t* terms_out = reinterpret_cast<uint16_t*>(base + terms_at);
+    o.b = terms_out;
+    if (gb300::launch_int8_split(c->dtype, dy, lddy, c->rows, N, terms_out, o.ldb, d.sms, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
   }
-  return status_of(gb300::launch_int8_product(p, stream));
+  a.dtype = dtype;
+  a.accumulate = accumulate != 0;
+  a.out = dw;
+  a.ld = ldw;
+  a.partials = reinterpret_cast<uint32_t*>(base + partials_at);
+  return run_product(shape, o, a, pairs, d, stream);
 } GB300_INT8_CATCH
 
 sgemm_status_t int8_swiglu(int dtype, int64_t M, int64_t F, const void* gate, int64_t ld_gate, const void* up,

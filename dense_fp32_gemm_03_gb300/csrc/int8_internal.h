@@ -34,26 +34,32 @@ cudaError_t launch_int8_swiglu_backward(const void* dh, int64_t lddh, const int8
                                         const int8_checkpoint_t& ku, void* dgate, int64_t ldg, void* dup, int64_t ldu,
                                         int sms, cudaStream_t stream);
 
-// ---- products (int8_product.cu)
-// D[r, c] = sum over k of a[r, k] b[c, k], stored at out[c * ld + r]: `a` integers (rows x depth, depth contiguous),
-// times units[(r / 32) * ld_units + k] if there are units.
-struct Int8Product {
+// ---- products on the tensor cores (int8_tc.cu)
+// D[r, c] = sum over k of a[r, k] b[c, k], stored at out[c * ld + r]; `a` 8-bit integers, times units if it is a
+// checkpoint; b 16-bit floats.
+enum Int8TcShape { kInt8Whole32, kInt8Whole64, kInt8Whole128, kInt8Bf16, kInt8Bf16Runs, kInt8F16, kInt8F16Runs, kInt8TcShapes };
+int int8_tc_cols(Int8TcShape shape);  // columns of a tile (of 256 rows)
+int int8_tc_step();                   // elements of k a stage
+// Sets the kernels' attributes on the current device; the CTA pairs that run at once, or < 0.
+int int8_tc_prepare();
+struct Int8TcArgs {
   int32_t rows, cols, depth;
-  const int8_t* a;
-  int64_t lda;
-  const uint16_t* units;  // NULL: b holds integers as 16-bit floats, sums are integers
-  int64_t ldu;
-  const uint16_t* b;      // without units cols x depth, depth contiguous; with them depth x cols, cols contiguous
-  int64_t ldb;            // elements, a multiple of 8
-  int32_t half;           // units and b are 16-bit floats, not bfloat16
-  int32_t terms;          // matrices b one after the other (depth * ldb elements each) whose products are added
-  const float* scale_r;   // without units
+  int32_t steps, steps_all;  // stages of k, and those of all terms (matrices b one after the other, depth rows each)
+  int32_t tiles_r, tiles_c, splits, units;  // units = tiles x splits
+  const float* scale_r;      // of integers
   const float* scale_c;
-  int32_t dtype;          // of out
-  int32_t accumulate;     // with units: out += D
+  int32_t dtype;             // of out
+  int32_t accumulate;        // out += D
   void* out;
   int64_t ld;
+  uint32_t* partials;        // splits x cols x rows 32-bit sums, if splits > 1
+  uint32_t* status;
+  uint64_t wait_limit_ns;
 };
-cudaError_t launch_int8_product(const Int8Product& p, cudaStream_t stream);
+// maps: `a` (boxes of 128 rows x 128 bytes), its units (4 rows x 128 bytes), b (rows of k in boxes of half the tile's
+// columns x 128 bytes, or for checkpoints rows of columns in boxes of 128 rows x 128 bytes).  May start beside the end of the kernel
+// before on the stream, and waits for it by itself.
+cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], const Int8TcArgs& args, int pairs, int sms,
+                           cudaStream_t stream);
 
 }  // namespace gb300

@@ -1,0 +1,590 @@
+// int8_tc.cu -- products of the 8-bit integer operators on the 5th-generation
+// tensor cores.
+//
+// Mathematics.  D[r, c] = sum over k of a[r, k] b[c, k] with `a` 8-bit integers.
+// The chip has no fast integer tensor instruction, but 16-bit floats hold
+// 8-bit integers exactly and their products have at most 15 bits, so that
+// kind::f16 with its 32-bit accumulator adds up to 1024 of them exactly
+// (128 * 128 * 1024 = 2^24).  Integer sums are taken 1024 products at a time and
+// added as integers.  A checkpoint's values q * u (q at most seven bits, u a
+// power of two) are exact in 16 bits too; a gradient's sums stay in the
+// accumulator for 16-bit outputs, and are added up 1024 products at a time in
+// registers for 32-bit ones (the tensor core cuts what it shifts out; over thousands
+// of additions that shows in 32 bits).
+//
+// Structure.  Two CTAs on two SMs share a tile of 256 rows x kN columns
+// (tcgen05.mma.cta_group::2): each supplies 128 rows of `a` and stages half of b's columns.
+//  * warp 0 streams `a` (bytes, as they are in memory) and a checkpoint's units, warp
+//    1 b, through two rings in shared memory (TMA, 128-byte swizzle);
+//  * two groups of four warps take a's stages in turn, a row a lane: they turn
+//    128 bytes into 16-bit floats in registers and write them to tensor
+//    memory, from where the MMA takes its first operand.  Shared memory then moves 8
+//    bits of `a` where 16 would pass twice, and no pass over `a` comes before;
+//  * warp 2 of the pair's first CTA issues the MMAs;
+//  * eight warps read a finished accumulator while the next one is filled.
+// Lanes are rows of D, which is stored as columns (out[c * ld + r]): a warp's 32
+// values of a column are consecutive.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "fp4_tc.cuh"
+#include "int8_device.cuh"
+#include "int8_internal.h"
+#include "sgemm_device.cuh"
+#include "sgemm_internal.h"
+
+namespace gb300 {
+namespace {
+
+using namespace int8;
+using fp4::elected;
+using fp4::expect_bytes;
+using fp4::load_box;
+using fp4::operand_desc;
+using fp4::uniform_warp;
+
+constexpr uint32_t kStatusTimeout = 3;
+constexpr int kStep = 128;               // elements of k a stage
+constexpr int kRunSteps = 1024 / kStep;  // stages whose sums stay exact
+constexpr int kRows = 128;               // of a CTA
+
+// kIntegers: 16-bit floats of integers, b K-major.  Others: a checkpoint's values in bfloat16 or 16-bit floats, b MN-major.
+enum Kind { kIntegers, kBf16, kF16 };
+
+template <Kind kKind_, int kN_, bool kRuns_>
+struct Tile {
+  static constexpr Kind kKind = kKind_;
+  static constexpr int kN = kN_;
+  static constexpr bool kRuns = kRuns_;  // sums leave the accumulator every 1024 products
+  static constexpr bool kUnits = kKind != kIntegers;
+  static constexpr int kCols = kN / 2;   // of b, a CTA
+  static constexpr uint32_t kABytes = kRows * kStep, kUBytes = kUnits ? 1024 : 0, kBBytes = kCols * kStep * 2;
+  static constexpr int kAccs = 2;
+  static constexpr int kSlotCols = kStep / 2;  // tensor memory columns of a stage of `a`
+  static constexpr int kSlots0 = (512 - kAccs * kN) / kSlotCols;
+  static constexpr int kSlots = kSlots0 < 6 ? kSlots0 : 6;
+  static constexpr int kStages0 = int((232448 - 1024 - 512) / (kABytes + kUBytes + kBBytes));
+  static constexpr int kStages = kStages0 < 8 ? kStages0 : 8;
+  static constexpr int kThreads = 640;
+  static constexpr int kV = kN / 2;  // columns of an epilogue warp
+  static constexpr int kBarriers = 4 * kStages + 2 * kSlots + 2 * kAccs + 1;
+  static constexpr size_t kSmem = 1024 + kStages * size_t(kABytes + kUBytes + kBBytes) + kBarriers * 8 + 16;
+  static_assert(kSmem <= 232448 && kAccs * kN + kSlots * kSlotCols <= 512, "memory");
+  // 32-bit accumulator; A from tensor memory, B K-major or MN-major (bit 16); M = 256.
+  static constexpr uint32_t kDesc = (1u << 4) | (kKind == kBf16 ? (1u << 7) | (1u << 10) : 0u) | (kUnits ? 1u << 16 : 0u) |
+                                    (uint32_t(kN >> 3) << 17) | (256u >> 4 << 24);
+};
+
+__device__ __forceinline__ uint32_t in_first(uint64_t* bar) {
+  uint32_t d;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(dev::smem_addr(bar)), "r"(0));
+  return d;
+}
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void mma(uint32_t e, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(e)
+      : "memory");
+}
+
+// MN-major rows of 128 bytes (64 columns) with the 128-byte swizzle: groups of eight k
+// 1024 bytes apart, the next 64 columns kStep rows on.
+__device__ __forceinline__ uint64_t columns_desc(uint32_t addr) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | uint64_t(kStep * 128 >> 4) << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 |
+         uint64_t(2) << 61;
+}
+
+template <int kCount>
+__device__ __forceinline__ void read_tmem(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+  for (int c = 0; c < kCount; c += 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[c]), "=r"(r[c + 1]), "=r"(r[c + 2]), "=r"(r[c + 3]), "=r"(r[c + 4]), "=r"(r[c + 5]), "=r"(r[c + 6]),
+          "=r"(r[c + 7]), "=r"(r[c + 8]), "=r"(r[c + 9]), "=r"(r[c + 10]), "=r"(r[c + 11]), "=r"(r[c + 12]),
+          "=r"(r[c + 13]), "=r"(r[c + 14]), "=r"(r[c + 15])
+        : "r"(taddr + c));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void write_tmem32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+      "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+      "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Two of a word's four integers as 16-bit floats: in the low bits of 1024 + 128 + q, of which
+// 1024 + 128 is taken off.  `biased`: the word with each byte's top bit flipped (q + 128).
+template <int kPair>
+__device__ __forceinline__ uint32_t to_f16(uint32_t biased) {
+  return hsub2(__byte_perm(biased, 0x64646464u, kPair ? 0x4342 : 0x4140), 0x64806480u);
+}
+// The same in bfloat16, whose 128 + (low seven bits) has 128 taken off where q >= 0 and 256 where
+// q < 0: that number is 0x4300 and q's top bit.
+template <int kPair>
+__device__ __forceinline__ uint32_t to_bf16(uint32_t word) {
+  const uint32_t p = __byte_perm(word, 0x43434343u, kPair ? 0x4342 : 0x4140);
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(p & 0xff7fff7fu), "r"(p & 0xff80ff80u));
+  return d;
+}
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A unit of work: a tile and a range of its stages of k.
+struct Work {
+  int r0, c0, kb, ke, part;
+};
+__device__ __forceinline__ Work work_of(const Int8TcArgs& a, int unit, int kn) {
+  const int tile = unit / a.splits, part = unit - tile * a.splits;
+  // Tiles in bands of kBand rows of tiles, column by column, so that the pairs at work read few rows and columns.
+  constexpr int kBand = 8;
+  const int band = tile / (kBand * a.tiles_c), in_band = tile - band * kBand * a.tiles_c;
+  const int height = min(kBand, a.tiles_r - band * kBand);
+  const int tc = in_band / height, tr = band * kBand + in_band - tc * height;
+  const int64_t all = a.steps_all;
+  return {tr * 2 * kRows, tc * kn, int(all * part / a.splits), int(all * (part + 1) / a.splits), part};
+}
+
+template <typename T>
+__device__ __forceinline__ void put(const Int8TcArgs& a, int64_t at, float v) {
+  T* out = static_cast<T*>(a.out) + at;
+  if (a.accumulate) v += to_f32(*out);
+  *out = from_f32<T>(v);
+}
+__device__ __forceinline__ void put_value(const Int8TcArgs& a, int64_t at, float v) {
+  if (a.dtype == INT8_F32)
+    put<float>(a, at, v);
+  else if (a.dtype == INT8_BF16)
+    put<__nv_bfloat16>(a, at, v);
+  else
+    put<__half>(a, at, v);
+}
+// A sum of integers times its scales, the smaller first (NaN stays).
+__device__ __forceinline__ float scaled(int sum, float s, float t) {
+  const bool first = fabsf(s) <= fabsf(t);
+  return float(sum) * (first ? s : t) * (first ? t : s);
+}
+
+template <typename S>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_u,
+                   const __grid_constant__ CUtensorMap map_b, const Int8TcArgs args) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = dev::smem_addr(smem_raw);
+  unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  unsigned char* s_a = smem;
+  unsigned char* s_b = s_a + S::kStages * S::kABytes;
+  unsigned char* s_u = s_b + S::kStages * S::kBBytes;
+  uint64_t* a_full = reinterpret_cast<uint64_t*>(s_u + S::kStages * S::kUBytes);
+  uint64_t* a_empty = a_full + S::kStages;
+  uint64_t* b_full = a_empty + S::kStages;     // used in the first CTA
+  uint64_t* b_empty = b_full + S::kStages;
+  uint64_t* slot_full = b_empty + S::kStages;  // used in the first CTA
+  uint64_t* slot_empty = slot_full + S::kSlots;
+  uint64_t* acc_full = slot_empty + S::kSlots;
+  uint64_t* acc_empty = acc_full + S::kAccs;   // used in the first CTA
+  uint64_t* drain = acc_empty + S::kAccs;
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1) + 1;
+
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
+  uint32_t rank;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const bool first = rank == 0;
+  const int unit0 = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const uint64_t limit = args.wait_limit_ns;
+
+  if (warp == 3) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     dev::smem_addr(const_cast<uint32_t*>(tmem_slot))), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      dev::mbar_init(&a_full[s], 1);
+      dev::mbar_init(&a_empty[s], 4);
+      dev::mbar_init(&b_full[s], 1);
+      dev::mbar_init(&b_empty[s], 1);
+    }
+    for (int s = 0; s < S::kSlots; ++s) {
+      dev::mbar_init(&slot_full[s], 8);
+      dev::mbar_init(&slot_empty[s], 1);
+    }
+    for (int b = 0; b < S::kAccs; ++b) {
+      dev::mbar_init(&acc_full[b], 1);
+      dev::mbar_init(&acc_empty[b], 16);
+    }
+    dev::mbar_init(drain, 1);
+    *s_abort = 0;
+    dev::mbar_init_fence();
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();  // the peer's barriers exist before anything signals them
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  constexpr uint32_t tmem = fp4::kTmemBase, slots = tmem + S::kAccs * S::kN;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  auto fail = [&]() {
+    if (!*s_abort) {
+      *s_abort = 1;
+      dev::record_status(args.status, kStatusTimeout, kWaitTileStage);
+    }
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!dev::mbar_wait_abortable(bar, parity, limit, s_abort)) fail();
+  };
+  // After a failure, the copies in flight get a bounded time to land before shared memory is released.
+  auto settle = [&]() {
+    const uint64_t t0 = dev::global_timer_ns();
+    while (dev::global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
+  };
+  auto going = [&]() { return __shfl_sync(0xffffffffu, *s_abort, 0) == 0; };
+
+  if (warp == 0) {
+    // ---- `a` and its units, of this CTA's rows
+    uint32_t i = 0;
+    bool go = true;
+    for (int unit = unit0; go && unit < args.units; unit += pairs) {
+      const Work w = work_of(args, unit, S::kN);
+      const int r0 = w.r0 + int(rank) * kRows;
+      for (int k = w.kb; k < w.ke; ++k, ++i) {
+        const uint32_t s = i % S::kStages, n = i / S::kStages;
+        if (n > 0) wait(&a_empty[s], (n - 1) & 1u);
+        if (!(go = going())) break;
+        const uint32_t e = elected(), bar = dev::smem_addr(&a_full[s]);
+        const int at = (k % args.steps) * kStep;
+        expect_bytes(e, &a_full[s], S::kABytes + S::kUBytes);
+        load_box<1>(e, s_a + s * S::kABytes, &map_a, at, r0, bar);
+        if constexpr (S::kUnits) {
+          load_box<1>(e, s_u + s * S::kUBytes, &map_u, 2 * at, r0 / kBlock, bar);
+          load_box<1>(e, s_u + s * S::kUBytes + 512, &map_u, 2 * at + 128, r0 / kBlock, bar);
+        }
+      }
+    }
+    if (!go) settle();
+  } else if (warp == 1) {
+    // ---- b, this CTA's half of the columns; completes on the first CTA's barrier
+    uint32_t i = 0;
+    bool go = true;
+    for (int unit = unit0; go && unit < args.units; unit += pairs) {
+      const Work w = work_of(args, unit, S::kN);
+      const int c0 = w.c0 + int(rank) * S::kCols;
+      for (int k = w.kb; k < w.ke; ++k, ++i) {
+        const uint32_t s = i % S::kStages, n = i / S::kStages;
+        if (n > 0) wait(&b_empty[s], (n - 1) & 1u);
+        if (!(go = going())) break;
+        const uint32_t e = elected(), bar = in_first(&b_full[s]);
+        if (first) expect_bytes(e, &b_full[s], 2 * S::kBBytes);
+        unsigned char* to = s_b + s * S::kBBytes;
+        if constexpr (S::kUnits) {
+          const int term = k / args.steps, at = (k - term * args.steps) * kStep + term * args.depth;
+#pragma unroll
+          for (int j = 0; j < S::kCols / 64; ++j) load_box<2>(e, to + j * kStep * 128, &map_b, 2 * (c0 + 64 * j), at, bar);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) load_box<2>(e, to + j * S::kCols * 128, &map_b, 2 * kStep * k + 128 * j, c0, bar);
+        }
+      }
+    }
+    if (!go) settle();
+  } else if (warp == 2) {
+    if (first) {
+      // ---- MMAs
+      uint32_t i = 0, runs = 0;
+      for (int unit = unit0; unit < args.units; unit += pairs) {
+        const Work w = work_of(args, unit, S::kN);
+        for (int k = w.kb; k < w.ke; ++k, ++i) {
+          const uint32_t s = i % S::kStages, t = i % S::kSlots;
+          const bool starts = S::kRuns ? (k - w.kb) % kRunSteps == 0 : k == w.kb;
+          const bool ends = k + 1 == w.ke || (S::kRuns && (k - w.kb) % kRunSteps == kRunSteps - 1);
+          const uint32_t b = runs % S::kAccs;
+          if (starts && runs >= S::kAccs) wait(&acc_empty[b], (runs / S::kAccs - 1) & 1u);
+          wait(&b_full[s], (i / S::kStages) & 1u);
+          wait(&slot_full[t], (i / S::kSlots) & 1u);
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t e = elected(), d = tmem + b * S::kN, a = slots + t * S::kSlotCols;
+          const uint32_t base = dev::smem_addr(s_b + s * S::kBBytes);
+#pragma unroll
+          for (int j = 0; j < kStep / 16; ++j) {
+            const uint64_t db = S::kUnits ? columns_desc(base) + j * (16 * 128 >> 4)
+                                          : operand_desc(base) + j / 4 * (S::kCols * 128 >> 4) + j % 4 * 2;
+            mma(e, d, a + 8 * j, db, S::kDesc, !starts || j != 0 ? 1u : 0u);
+          }
+          fp4::commit<2>(e, &b_empty[s]);
+          fp4::commit<2>(e, &slot_empty[t]);
+          if (ends) {
+            fp4::commit<2>(e, &acc_full[b]);
+            ++runs;
+          }
+        }
+      }
+      fp4::commit<2>(elected(), drain);
+      dev::mbar_wait(drain, 0u, limit);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ---- `a` to 16 bits, in tensor memory
+    const int q = warp & 3, group = (warp - 4) >> 2, row = 32 * q + lane;
+    const uint32_t lanes = uint32_t(32 * q) << 16;
+    uint32_t i = 0;
+    for (int unit = unit0; unit < args.units; unit += pairs) {
+      const Work w = work_of(args, unit, S::kN);
+      for (int k = w.kb; k < w.ke; ++k, ++i) {
+        if (int(i & 1) != group) continue;
+        const uint32_t s = i % S::kStages, t = i % S::kSlots;
+        wait(&a_full[s], (i / S::kStages) & 1u);
+        __syncwarp();
+        const uint4* from = reinterpret_cast<const uint4*>(s_a + s * S::kABytes + row * 128);
+        const unsigned char* units = s_u + s * S::kUBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 in[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) in[j] = from[(4 * h + j) ^ (row & 7)];
+          uint32_t out[32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t word[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
+            if constexpr (S::kUnits) {
+              // 16 units, two 16-byte pieces of row q (its second 64 in the second box) of the swizzled boxes.
+              uint32_t u[8];
+#pragma unroll
+              for (int p = 0; p < 2; ++p)
+                *reinterpret_cast<uint4*>(u + 4 * p) = *reinterpret_cast<const uint4*>(
+                    units + h * 512 + q * 128 + (((2 * j + p) ^ (q + 4 * h)) << 4));
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                if constexpr (S::kKind == kBf16) {
+                  out[8 * j + 2 * x] = bmul2(to_bf16<0>(word[x]), u[2 * x]);
+                  out[8 * j + 2 * x + 1] = bmul2(to_bf16<1>(word[x]), u[2 * x + 1]);
+                } else {
+                  const uint32_t v = word[x] ^ 0x80808080u;
+                  out[8 * j + 2 * x] = hmul2(to_f16<0>(v), u[2 * x]);
+                  out[8 * j + 2 * x + 1] = hmul2(to_f16<1>(v), u[2 * x + 1]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t v = word[x] ^ 0x80808080u;
+                out[8 * j + 2 * x] = to_f16<0>(v);
+                out[8 * j + 2 * x + 1] = to_f16<1>(v);
+              }
+            }
+          }
+          if (h == 0) {
+            if (i >= S::kSlots) wait(&slot_empty[t], (i / S::kSlots - 1) & 1u);
+            __syncwarp();
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          } else {
+            __syncwarp();
+            if (lane == 0) dev::mbar_arrive(&a_empty[s]);
+          }
+          write_tmem32(slots + t * S::kSlotCols + 32 * h + lanes, out);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive_first(&slot_full[t]);
+      }
+    }
+  } else if (warp >= 12) {
+    // ---- epilogue: 32 rows x kV columns a warp
+    const int q = warp & 3, half = (warp - 12) >> 2;
+    const uint32_t lanes = uint32_t(32 * q) << 16;
+    uint32_t runs = 0;
+    for (int unit = unit0; unit < args.units; unit += pairs) {
+      const Work w = work_of(args, unit, S::kN);
+      const int row = w.r0 + int(rank) * kRows + 32 * q + lane, col0 = w.c0 + half * S::kV;
+      const bool mine = row < args.rows;
+      const float scale = S::kKind == kIntegers && mine && args.splits == 1 ? args.scale_r[row] : 0.f;
+      constexpr int kPart = S::kV < 32 ? S::kV : 32;
+      auto store = [&](int c, uint32_t bits) {
+        if (!mine || col0 + c >= args.cols) return;
+        const int64_t at = int64_t(col0 + c) * args.ld + row;
+        if (args.splits > 1)
+          args.partials[int64_t(w.part) * args.rows * args.cols + int64_t(col0 + c) * args.rows + row] = bits;
+        else if (S::kKind == kIntegers)
+          put_value(args, at, scaled(int(bits), scale, args.scale_c[col0 + c]));
+        else
+          put_value(args, at, __uint_as_float(bits));
+      };
+      if constexpr (S::kRuns) {
+        uint32_t sum[S::kV];
+#pragma unroll
+        for (int c = 0; c < S::kV; ++c) sum[c] = 0;
+        for (int k = w.kb; k < w.ke; k += kRunSteps, ++runs) {
+          const uint32_t b = runs % S::kAccs;
+          wait(&acc_full[b], (runs / S::kAccs) & 1u);
+          __syncwarp();
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+          for (int c = 0; c < S::kV; c += kPart) {
+            float v[kPart];
+            read_tmem<kPart>(tmem + b * S::kN + half * S::kV + c + lanes, v);
+#pragma unroll
+            for (int x = 0; x < kPart; ++x)
+              sum[c + x] = S::kKind == kIntegers ? sum[c + x] + uint32_t(__float2int_rn(v[x]))
+                                                 : __float_as_uint(__uint_as_float(sum[c + x]) + v[x]);
+          }
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) arrive_first(&acc_empty[b]);
+        }
+        if (going()) {
+#pragma unroll
+          for (int c = 0; c < S::kV; ++c) store(c, sum[c]);
+        }
+      } else {
+        const uint32_t b = runs % S::kAccs;
+        wait(&acc_full[b], (runs / S::kAccs) & 1u);
+        __syncwarp();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const bool ok = going();
+#pragma unroll
+        for (int c = 0; c < S::kV; c += kPart) {
+          float v[kPart];
+          read_tmem<kPart>(tmem + b * S::kN + half * S::kV + c + lanes, v);
+          if (c + kPart == S::kV) {
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive_first(&acc_empty[b]);
+          }
+          if (ok) {
+#pragma unroll
+            for (int x = 0; x < kPart; ++x) store(c + x, __float_as_uint(v[x]));
+          }
+        }
+        ++runs;
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();  // nothing of either CTA is still signalled or read by the other
+  if (warp == 3) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// Adds the shares of a product split over k, in their order, and stores it.
+template <bool kWhole>
+__global__ void __launch_bounds__(256) join_kernel(const Int8TcArgs args) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t all = int64_t(args.rows) * args.cols;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const int64_t c = i / args.rows, r = i - c * args.rows;
+    if constexpr (kWhole) {
+      uint32_t sum = 0;
+      for (int p = 0; p < args.splits; ++p) sum += args.partials[p * all + i];
+      put_value(args, c * args.ld + r, scaled(int(sum), args.scale_r[r], args.scale_c[c]));
+    } else {
+      float sum = 0.f;
+      for (int p = 0; p < args.splits; ++p) sum += __uint_as_float(args.partials[p * all + i]);
+      put_value(args, c * args.ld + r, sum);
+    }
+  }
+}
+
+typedef void (*Kernel)(CUtensorMap, CUtensorMap, CUtensorMap, Int8TcArgs);
+struct Instance {
+  Kernel kernel;
+  size_t smem;
+  int threads, cols;
+};
+template <Kind kKind, int kN, bool kRuns>
+Instance instance_of() {
+  using S = Tile<kKind, kN, kRuns>;
+  return {Kernel(product_kernel<S>), S::kSmem, S::kThreads, kN};
+}
+
+Instance instance(int shape) {
+  switch (shape) {
+    case kInt8Whole32: return instance_of<kIntegers, 32, true>();
+    case kInt8Whole64: return instance_of<kIntegers, 64, true>();
+    case kInt8Whole128: return instance_of<kIntegers, 128, true>();
+    case kInt8Bf16: return instance_of<kBf16, 128, false>();
+    case kInt8Bf16Runs: return instance_of<kBf16, 128, true>();
+    case kInt8F16: return instance_of<kF16, 128, false>();
+    default: return instance_of<kF16, 128, true>();
+  }
+}
+
+}  // namespace
+
+int int8_tc_cols(Int8TcShape shape) { return instance(shape).cols; }
+int int8_tc_step() { return kStep; }
+
+int int8_tc_prepare() {
+  int pairs = 0;
+  for (int shape = 0; shape < kInt8TcShapes; ++shape) {
+    const Instance in = instance(shape);
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(in.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(in.smem)) != cudaSuccess)
+      return -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(in.threads, 1, 1);
+    cfg.dynamicSmemBytes = in.smem;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(in.kernel), &cfg) != cudaSuccess) return -1;
+    if (pairs == 0 || n < pairs) pairs = n;
+  }
+  return pairs;
+}
+
+cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], const Int8TcArgs& args, int pairs, int sms,
+                           cudaStream_t stream) {
+  const Instance in = instance(shape);
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(2 * std::min(pairs, args.units)), 1, 1);
+  cfg.blockDim = dim3(unsigned(in.threads), 1, 1);
+  cfg.dynamicSmemBytes = in.smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, in.kernel, maps[0], maps[1], maps[2], args);
+  if (e != cudaSuccess || args.splits == 1) return e;
+  const int64_t all = int64_t(args.rows) * args.cols;
+  cfg.gridDim = dim3(unsigned(std::min((all + 255) / 256, int64_t(sms) * 8)), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, args.scale_r ? join_kernel<true> : join_kernel<false>, args);
+}
+
+}  // namespace gb300

@@ -160,10 +160,11 @@ sgemm_status_t plan(gb300::Int8TcShape shape, int64_t rows, int64_t cols, int64_
   a->cols = int32_t(cols);
   a->depth = int32_t(depth);
   a->steps = int32_t(steps);
-  a->steps_all = int32_t(steps * terms);
+  a->terms = terms;
+  a->run = terms == 1 ? 1024 / gb300::int8_tc_step() : 4;
   a->tiles_r = int32_t(tr);
   a->tiles_c = int32_t(tc);
-  a->splits = int32_t(std::max<int64_t>(1, std::min(pairs / tiles, steps * terms / 4)));
+  a->splits = int32_t(std::max<int64_t>(1, std::min(pairs / tiles, steps / 4)));
   a->units = int32_t(tiles * a->splits);
   return SGEMM_OK;
 }

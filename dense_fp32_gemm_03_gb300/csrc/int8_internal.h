@@ -44,7 +44,8 @@ int int8_tc_step();                   // elements of k a stage
 int int8_tc_prepare();
 struct Int8TcArgs {
   int32_t rows, cols, depth;
-  int32_t steps, steps_all;  // stages of k, and those of all terms (matrices b one after the other, depth rows each)
+  int32_t steps, terms;      // stages of k; matrices b, one after the other with depth rows each, whose products are added
+  int32_t run;               // stages of k whose sums an accumulator takes, where it does not take all
   int32_t tiles_r, tiles_c, splits, units;  // units = tiles x splits
   const float* scale_r;      // of integers
   const float* scale_c;

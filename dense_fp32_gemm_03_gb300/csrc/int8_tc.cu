@@ -47,7 +47,6 @@ using fp4::uniform_warp;
 
 constexpr uint32_t kStatusTimeout = 3;
 constexpr int kStep = 128;               // elements of k a stage
-constexpr int kRunSteps = 1024 / kStep;  // stages whose sums stay exact
 constexpr int kRows = 128;               // of a CTA
 
 // kIntegers: 16-bit floats of integers, b K-major.  Others: a checkpoint's values in bfloat16 or 16-bit floats, b MN-major.
@@ -61,7 +60,7 @@ struct Tile {
   static constexpr bool kUnits = kKind != kIntegers;
   static constexpr int kCols = kN / 2;   // of b, a CTA
   static constexpr uint32_t kABytes = kRows * kStep, kUBytes = kUnits ? 1024 : 0, kBBytes = kCols * kStep * 2;
-  static constexpr int kAccs = 2;
+  static constexpr int kAccs = kN <= 128 ? 2 : 1;
   static constexpr int kSlotCols = kStep / 2;  // tensor memory columns of a stage of `a`
   static constexpr int kSlots0 = (512 - kAccs * kN) / kSlotCols;
   static constexpr int kSlots = kSlots0 < 6 ? kSlots0 : 6;
@@ -82,8 +81,10 @@ __device__ __forceinline__ uint32_t in_first(uint64_t* bar) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(dev::smem_addr(bar)), "r"(0));
   return d;
 }
+// What these arrivals hand over is in tensor memory and ordered by tcgen05.fence; with the release at cluster scope,
+// which waits for all of the warp's earlier accesses, a stage took 3400 cycles instead of 1640.
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -172,28 +173,47 @@ __device__ __forceinline__ Work work_of(const Int8TcArgs& a, int unit, int kn) {
   const int band = tile / (kBand * a.tiles_c), in_band = tile - band * kBand * a.tiles_c;
   const int height = min(kBand, a.tiles_r - band * kBand);
   const int tc = in_band / height, tr = band * kBand + in_band - tc * height;
-  const int64_t all = a.steps_all;
+  const int64_t all = a.steps;
   return {tr * 2 * kRows, tc * kn, int(all * part / a.splits), int(all * (part + 1) / a.splits), part};
 }
 
-template <typename T>
-__device__ __forceinline__ void put(const Int8TcArgs& a, int64_t at, float v) {
-  T* out = static_cast<T*>(a.out) + at;
-  if (a.accumulate) v += to_f32(*out);
-  *out = from_f32<T>(v);
+template <typename T2>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  T2 v;
+  v.x = from_f32<decltype(v.x)>(a);
+  v.y = from_f32<decltype(v.y)>(b);
+  return *reinterpret_cast<uint32_t*>(&v);
 }
-__device__ __forceinline__ void put_value(const Int8TcArgs& a, int64_t at, float v) {
-  if (a.dtype == INT8_F32)
-    put<float>(a, at, v);
-  else if (a.dtype == INT8_BF16)
-    put<__nv_bfloat16>(a, at, v);
-  else
-    put<__half>(a, at, v);
-}
+
 // A sum of integers times its scales, the smaller first (NaN stays).
 __device__ __forceinline__ float scaled(int sum, float s, float t) {
   const bool first = fabsf(s) <= fabsf(t);
   return float(sum) * (first ? s : t) * (first ? t : s);
+}
+
+// Stores kCount columns of a row of D (`out`: the first; `left`: those that exist), added to what is there if asked.
+template <typename T, int kCount>
+__device__ __forceinline__ void put_columns(T* out, int64_t ld, int left, bool add, const float (&v)[kCount]) {
+  constexpr int kPart = kCount < 16 ? kCount : 16;
+#pragma unroll
+  for (int c0 = 0; c0 < kCount; c0 += kPart) {
+    float old[kPart];
+#pragma unroll
+    for (int c = 0; c < kPart; ++c) old[c] = add && c0 + c < left ? to_f32(out[(c0 + c) * ld]) : 0.f;
+#pragma unroll
+    for (int c = 0; c < kPart; ++c)
+      if (c0 + c < left) out[(c0 + c) * ld] = from_f32<T>(add ? v[c0 + c] + old[c] : v[c0 + c]);
+  }
+}
+template <int kCount>
+__device__ __forceinline__ void put_columns(const Int8TcArgs& a, int64_t row, int col, const float (&v)[kCount]) {
+  const int64_t at = int64_t(col) * a.ld + row;
+  if (a.dtype == INT8_F32)
+    put_columns(static_cast<float*>(a.out) + at, a.ld, a.cols - col, a.accumulate, v);
+  else if (a.dtype == INT8_BF16)
+    put_columns(static_cast<__nv_bfloat16*>(a.out) + at, a.ld, a.cols - col, a.accumulate, v);
+  else
+    put_columns(static_cast<__half*>(a.out) + at, a.ld, a.cols - col, a.accumulate, v);
 }
 
 template <typename S>
@@ -272,6 +292,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
   };
   auto going = [&]() { return __shfl_sync(0xffffffffu, *s_abort, 0) == 0; };
 
+  // 640 threads have 96 registers each; the four warps below give up what the epilogue's sums need.
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
   if (warp == 0) {
     // ---- `a` and its units, of this CTA's rows
     uint32_t i = 0;
@@ -284,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
         if (n > 0) wait(&a_empty[s], (n - 1) & 1u);
         if (!(go = going())) break;
         const uint32_t e = elected(), bar = dev::smem_addr(&a_full[s]);
-        const int at = (k % args.steps) * kStep;
+        const int at = k * kStep;
         expect_bytes(e, &a_full[s], S::kABytes + S::kUBytes);
         load_box<1>(e, s_a + s * S::kABytes, &map_a, at, r0, bar);
         if constexpr (S::kUnits) {
@@ -301,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
     for (int unit = unit0; go && unit < args.units; unit += pairs) {
       const Work w = work_of(args, unit, S::kN);
       const int c0 = w.c0 + int(rank) * S::kCols;
-      for (int k = w.kb; k < w.ke; ++k, ++i) {
+      for (int x = w.kb * args.terms; x < w.ke * args.terms; ++x, ++i) {
         const uint32_t s = i % S::kStages, n = i / S::kStages;
         if (n > 0) wait(&b_empty[s], (n - 1) & 1u);
         if (!(go = going())) break;
@@ -309,12 +332,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
         if (first) expect_bytes(e, &b_full[s], 2 * S::kBBytes);
         unsigned char* to = s_b + s * S::kBBytes;
         if constexpr (S::kUnits) {
-          const int term = k / args.steps, at = (k - term * args.steps) * kStep + term * args.depth;
+          const int k = x / args.terms, at = k * kStep + (x - k * args.terms) * args.depth;
 #pragma unroll
           for (int j = 0; j < S::kCols / 64; ++j) load_box<2>(e, to + j * kStep * 128, &map_b, 2 * (c0 + 64 * j), at, bar);
         } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) load_box<2>(e, to + j * S::kCols * 128, &map_b, 2 * kStep * k + 128 * j, c0, bar);
+          for (int j = 0; j < 2; ++j) load_box<2>(e, to + j * S::kCols * 128, &map_b, 2 * kStep * x + 128 * j, c0, bar);
         }
       }
     }
@@ -322,27 +345,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
   } else if (warp == 2) {
     if (first) {
       // ---- MMAs
-      uint32_t i = 0, runs = 0;
+      uint32_t i = 0, ib = 0, runs = 0;
       for (int unit = unit0; unit < args.units; unit += pairs) {
         const Work w = work_of(args, unit, S::kN);
         for (int k = w.kb; k < w.ke; ++k, ++i) {
-          const uint32_t s = i % S::kStages, t = i % S::kSlots;
-          const bool starts = S::kRuns ? (k - w.kb) % kRunSteps == 0 : k == w.kb;
-          const bool ends = k + 1 == w.ke || (S::kRuns && (k - w.kb) % kRunSteps == kRunSteps - 1);
-          const uint32_t b = runs % S::kAccs;
+          const uint32_t t = i % S::kSlots, b = runs % S::kAccs;
+          const bool starts = S::kRuns ? (k - w.kb) % args.run == 0 : k == w.kb;
+          const bool ends = k + 1 == w.ke || (S::kRuns && (k - w.kb) % args.run == args.run - 1);
           if (starts && runs >= S::kAccs) wait(&acc_empty[b], (runs / S::kAccs - 1) & 1u);
-          wait(&b_full[s], (i / S::kStages) & 1u);
           wait(&slot_full[t], (i / S::kSlots) & 1u);
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t e = elected(), d = tmem + b * S::kN, a = slots + t * S::kSlotCols;
-          const uint32_t base = dev::smem_addr(s_b + s * S::kBBytes);
+          const uint32_t d = tmem + b * S::kN, a = slots + t * S::kSlotCols;
+          for (int term = 0; term < args.terms; ++term, ++ib) {
+            const uint32_t s = ib % S::kStages;
+            wait(&b_full[s], (ib / S::kStages) & 1u);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t e = elected(), base = dev::smem_addr(s_b + s * S::kBBytes);
 #pragma unroll
-          for (int j = 0; j < kStep / 16; ++j) {
-            const uint64_t db = S::kUnits ? columns_desc(base) + j * (16 * 128 >> 4)
-                                          : operand_desc(base) + j / 4 * (S::kCols * 128 >> 4) + j % 4 * 2;
-            mma(e, d, a + 8 * j, db, S::kDesc, !starts || j != 0 ? 1u : 0u);
+            for (int j = 0; j < kStep / 16; ++j) {
+              const uint64_t db = S::kUnits ? columns_desc(base) + j * (16 * 128 >> 4)
+                                            : operand_desc(base) + j / 4 * (S::kCols * 128 >> 4) + j % 4 * 2;
+              mma(e, d, a + 8 * j, db, S::kDesc, !starts || term != 0 || j != 0 ? 1u : 0u);
+            }
+            fp4::commit<2>(e, &b_empty[s]);
           }
-          fp4::commit<2>(e, &b_empty[s]);
+          const uint32_t e = elected();
           fp4::commit<2>(e, &slot_empty[t]);
           if (ends) {
             fp4::commit<2>(e, &acc_full[b]);
@@ -353,73 +379,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
       fp4::commit<2>(elected(), drain);
       dev::mbar_wait(drain, 0u, limit);
     }
-  } else if (warp >= 4 && warp < 12) {
-    // ---- `a` to 16 bits, in tensor memory
+  }
+  } else if (warp < 12) {
+    // ---- `a` to 16 bits, in tensor memory.  A stage's bytes are read before the stage before is handed over.
     const int q = warp & 3, group = (warp - 4) >> 2, row = 32 * q + lane;
-    const uint32_t lanes = uint32_t(32 * q) << 16;
-    uint32_t i = 0;
+    const uint32_t to = slots + (uint32_t(32 * q) << 16);
+    // Stages of this pair, over all of its units.
+    uint32_t all = 0;
     for (int unit = unit0; unit < args.units; unit += pairs) {
       const Work w = work_of(args, unit, S::kN);
-      for (int k = w.kb; k < w.ke; ++k, ++i) {
-        if (int(i & 1) != group) continue;
-        const uint32_t s = i % S::kStages, t = i % S::kSlots;
-        wait(&a_full[s], (i / S::kStages) & 1u);
-        __syncwarp();
-        const uint4* from = reinterpret_cast<const uint4*>(s_a + s * S::kABytes + row * 128);
-        const unsigned char* units = s_u + s * S::kUBytes;
+      all += uint32_t(w.ke - w.kb);
+    }
+    uint4 in[8];
+    auto fetch = [&](uint32_t i) {
+      const uint32_t s = i % S::kStages;
+      wait(&a_full[s], (i / S::kStages) & 1u);
+      const uint4* from = reinterpret_cast<const uint4*>(s_a + s * S::kABytes + row * 128);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 in[4];
+      for (int j = 0; j < 8; ++j) in[j] = from[j ^ (row & 7)];
+    };
+    if (uint32_t(group) < all) fetch(group);
+    for (uint32_t i = group; i < all; i += 2) {
+      const uint32_t s = i % S::kStages, t = i % S::kSlots;
+      const unsigned char* units = s_u + s * S::kUBytes;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) in[j] = from[(4 * h + j) ^ (row & 7)];
-          uint32_t out[32];
+      for (int h = 0; h < 2; ++h) {
+        uint32_t out[32];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t word[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
-            if constexpr (S::kUnits) {
-              // 16 units, two 16-byte pieces of row q (its second 64 in the second box) of the swizzled boxes.
-              uint32_t u[8];
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t word[4] = {in[4 * h + j].x, in[4 * h + j].y, in[4 * h + j].z, in[4 * h + j].w};
+          if constexpr (S::kUnits) {
+            // 16 units, two 16-byte pieces of row q (its second 64 in the second box) of the swizzled boxes.
+            uint32_t u[8];
 #pragma unroll
-              for (int p = 0; p < 2; ++p)
-                *reinterpret_cast<uint4*>(u + 4 * p) = *reinterpret_cast<const uint4*>(
-                    units + h * 512 + q * 128 + (((2 * j + p) ^ (q + 4 * h)) << 4));
+            for (int p = 0; p < 2; ++p)
+              *reinterpret_cast<uint4*>(u + 4 * p) = *reinterpret_cast<const uint4*>(
+                  units + h * 512 + q * 128 + (((2 * j + p) ^ (q + 4 * h)) << 4));
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                if constexpr (S::kKind == kBf16) {
-                  out[8 * j + 2 * x] = bmul2(to_bf16<0>(word[x]), u[2 * x]);
-                  out[8 * j + 2 * x + 1] = bmul2(to_bf16<1>(word[x]), u[2 * x + 1]);
-                } else {
-                  const uint32_t v = word[x] ^ 0x80808080u;
-                  out[8 * j + 2 * x] = hmul2(to_f16<0>(v), u[2 * x]);
-                  out[8 * j + 2 * x + 1] = hmul2(to_f16<1>(v), u[2 * x + 1]);
-                }
-              }
-            } else {
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 4; ++x) {
+              if constexpr (S::kKind == kBf16) {
+                out[8 * j + 2 * x] = bmul2(to_bf16<0>(word[x]), u[2 * x]);
+                out[8 * j + 2 * x + 1] = bmul2(to_bf16<1>(word[x]), u[2 * x + 1]);
+              } else {
                 const uint32_t v = word[x] ^ 0x80808080u;
-                out[8 * j + 2 * x] = to_f16<0>(v);
-                out[8 * j + 2 * x + 1] = to_f16<1>(v);
+                out[8 * j + 2 * x] = hmul2(to_f16<0>(v), u[2 * x]);
+                out[8 * j + 2 * x + 1] = hmul2(to_f16<1>(v), u[2 * x + 1]);
               }
             }
-          }
-          if (h == 0) {
-            if (i >= S::kSlots) wait(&slot_empty[t], (i / S::kSlots - 1) & 1u);
-            __syncwarp();
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           } else {
-            __syncwarp();
-            if (lane == 0) dev::mbar_arrive(&a_empty[s]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t v = word[x] ^ 0x80808080u;
+              out[8 * j + 2 * x] = to_f16<0>(v);
+              out[8 * j + 2 * x + 1] = to_f16<1>(v);
+            }
           }
-          write_tmem32(slots + t * S::kSlotCols + 32 * h + lanes, out);
         }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) arrive_first(&slot_full[t]);
+        if (h == 0) {
+          if (i >= S::kSlots) wait(&slot_empty[t], (i / S::kSlots - 1) & 1u);
+          __syncwarp();
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        } else {
+          __syncwarp();
+          if (lane == 0) dev::mbar_arrive(&a_empty[s]);
+        }
+        write_tmem32(to + t * S::kSlotCols + 32 * h, out);
       }
+      if (i + 2 < all) fetch(i + 2);
+      __syncwarp();
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive_first(&slot_full[t]);
     }
-  } else if (warp >= 12) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ---- epilogue: 32 rows x kV columns a warp
     const int q = warp & 3, half = (warp - 12) >> 2;
     const uint32_t lanes = uint32_t(32 * q) << 16;
@@ -428,65 +462,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
       const Work w = work_of(args, unit, S::kN);
       const int row = w.r0 + int(rank) * kRows + 32 * q + lane, col0 = w.c0 + half * S::kV;
       const bool mine = row < args.rows;
-      const float scale = S::kKind == kIntegers && mine && args.splits == 1 ? args.scale_r[row] : 0.f;
       constexpr int kPart = S::kV < 32 ? S::kV : 32;
-      auto store = [&](int c, uint32_t bits) {
-        if (!mine || col0 + c >= args.cols) return;
-        const int64_t at = int64_t(col0 + c) * args.ld + row;
-        if (args.splits > 1)
-          args.partials[int64_t(w.part) * args.rows * args.cols + int64_t(col0 + c) * args.rows + row] = bits;
-        else if (S::kKind == kIntegers)
-          put_value(args, at, scaled(int(bits), scale, args.scale_c[col0 + c]));
-        else
-          put_value(args, at, __uint_as_float(bits));
+      auto put_partials = [&](int c0, const uint32_t* bits) {
+        uint32_t* out = args.partials + (int64_t(w.part) * args.cols + col0 + c0) * args.rows + row;
+#pragma unroll
+        for (int c = 0; c < kPart; ++c)
+          if (mine && col0 + c0 + c < args.cols) out[int64_t(c) * args.rows] = bits[c];
+      };
+      auto acc_wait = [&]() {
+        wait(&acc_full[runs % S::kAccs], (runs / S::kAccs) & 1u);
+        __syncwarp();
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        return tmem + (runs % S::kAccs) * S::kN + half * S::kV + lanes;
+      };
+      auto acc_free = [&]() {
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive_first(&acc_empty[runs % S::kAccs]);
+        ++runs;
       };
       if constexpr (S::kRuns) {
+        // Scales of this warp's columns, 32 a register; a row's.
+        float scale_c[(S::kV + 31) / 32], scale_r = 0.f;
+        if (S::kKind == kIntegers && args.splits == 1) {
+#pragma unroll
+          for (int c = 0; c < S::kV; c += 32) scale_c[c / 32] = col0 + c + lane < args.cols ? args.scale_c[col0 + c + lane] : 0.f;
+          if (mine) scale_r = args.scale_r[row];
+        }
         uint32_t sum[S::kV];
 #pragma unroll
         for (int c = 0; c < S::kV; ++c) sum[c] = 0;
-        for (int k = w.kb; k < w.ke; k += kRunSteps, ++runs) {
-          const uint32_t b = runs % S::kAccs;
-          wait(&acc_full[b], (runs / S::kAccs) & 1u);
-          __syncwarp();
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        for (int k = w.kb; k < w.ke; k += args.run) {
+          const uint32_t at = acc_wait();
 #pragma unroll
           for (int c = 0; c < S::kV; c += kPart) {
             float v[kPart];
-            read_tmem<kPart>(tmem + b * S::kN + half * S::kV + c + lanes, v);
+            read_tmem<kPart>(at + c, v);
 #pragma unroll
             for (int x = 0; x < kPart; ++x)
               sum[c + x] = S::kKind == kIntegers ? sum[c + x] + uint32_t(__float2int_rn(v[x]))
                                                  : __float_as_uint(__uint_as_float(sum[c + x]) + v[x]);
           }
-          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) arrive_first(&acc_empty[b]);
+          acc_free();
         }
-        if (going()) {
-#pragma unroll
-          for (int c = 0; c < S::kV; ++c) store(c, sum[c]);
-        }
-      } else {
-        const uint32_t b = runs % S::kAccs;
-        wait(&acc_full[b], (runs / S::kAccs) & 1u);
-        __syncwarp();
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const bool ok = going();
+        if (!going()) continue;
 #pragma unroll
         for (int c = 0; c < S::kV; c += kPart) {
-          float v[kPart];
-          read_tmem<kPart>(tmem + b * S::kN + half * S::kV + c + lanes, v);
-          if (c + kPart == S::kV) {
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) arrive_first(&acc_empty[b]);
+          if (args.splits > 1) {
+            put_partials(c, sum + c);
+            continue;
           }
-          if (ok) {
+          float v[kPart];
 #pragma unroll
-            for (int x = 0; x < kPart; ++x) store(c + x, __float_as_uint(v[x]));
+          for (int x = 0; x < kPart; ++x)
+            v[x] = S::kKind == kIntegers ? scaled(int(sum[c + x]), scale_r, __shfl_sync(0xffffffffu, scale_c[c / 32], x))
+                                         : __uint_as_float(sum[c + x]);
+          if (mine) put_columns(args, row, col0 + c, v);
+        }
+      } else {
+        const uint32_t at = acc_wait();
+        const bool ok = going();
+        if (args.splits > 1) {
+#pragma unroll
+          for (int c = 0; c < S::kV; c += kPart) {
+            uint32_t v[kPart];
+            read_tmem<kPart>(at + c, reinterpret_cast<float*>(v));
+            if (ok) put_partials(c, v);
+          }
+          acc_free();
+        } else if (args.accumulate) {
+#pragma unroll
+          for (int c = 0; c < S::kV; c += kPart) {
+            float v[kPart];
+            read_tmem<kPart>(at + c, v);
+            if (ok && mine) put_columns(args, row, col0 + c, v);
+          }
+          acc_free();
+        } else {
+          // Rounded to the 16-bit type as they are read, so that the accumulator is free before the stores.
+          uint32_t two[S::kV / 2];
+#pragma unroll
+          for (int c = 0; c < S::kV; c += kPart) {
+            float v[kPart];
+            read_tmem<kPart>(at + c, v);
+#pragma unroll
+            for (int x = 0; x < kPart; x += 2) two[(c + x) / 2] = args.dtype == INT8_BF16 ? pack2<__nv_bfloat162>(v[x], v[x + 1]) : pack2<__half2>(v[x], v[x + 1]);
+          }
+          acc_free();
+          uint16_t* out = static_cast<uint16_t*>(args.out) + int64_t(col0) * args.ld + row;
+          const int left = args.cols - col0;
+          if (ok && mine) {
+#pragma unroll
+            for (int c = 0; c < S::kV; ++c)
+              if (c < left) out[c * args.ld] = uint16_t(two[c / 2] >> (c % 2 * 16));
           }
         }
-        ++runs;
       }
     }
   }
@@ -506,15 +576,15 @@ __global__ void __launch_bounds__(256) join_kernel(const Int8TcArgs args) {
   const int64_t all = int64_t(args.rows) * args.cols;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
     const int64_t c = i / args.rows, r = i - c * args.rows;
+    float v[1] = {0.f};
     if constexpr (kWhole) {
       uint32_t sum = 0;
       for (int p = 0; p < args.splits; ++p) sum += args.partials[p * all + i];
-      put_value(args, c * args.ld + r, scaled(int(sum), args.scale_r[r], args.scale_c[c]));
+      v[0] = scaled(int(sum), args.scale_r[r], args.scale_c[c]);
     } else {
-      float sum = 0.f;
-      for (int p = 0; p < args.splits; ++p) sum += __uint_as_float(args.partials[p * all + i]);
-      put_value(args, c * args.ld + r, sum);
+      for (int p = 0; p < args.splits; ++p) v[0] += __uint_as_float(args.partials[p * all + i]);
     }
+    put_columns(args, r, int(c), v);
   }
 }
 
@@ -535,9 +605,9 @@ Instance instance(int shape) {
     case kInt8Whole32: return instance_of<kIntegers, 32, true>();
     case kInt8Whole64: return instance_of<kIntegers, 64, true>();
     case kInt8Whole128: return instance_of<kIntegers, 128, true>();
-    case kInt8Bf16: return instance_of<kBf16, 128, false>();
+    case kInt8Bf16: return instance_of<kBf16, 256, false>();
     case kInt8Bf16Runs: return instance_of<kBf16, 128, true>();
-    case kInt8F16: return instance_of<kF16, 128, false>();
+    case kInt8F16: return instance_of<kF16, 256, false>();
     default: return instance_of<kF16, 128, true>();
   }
 }

@@ -162,6 +162,15 @@ __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// A place in a ring of kCount and the parity of its round.
+template <int kCount>
+struct At {
+  uint32_t i = 0, parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == uint32_t(kCount)) i = 0, parity ^= 1u;
+  }
+};
+
 // A unit of work: a tile and a range of its stages of k.
 struct Work {
   int r0, c0, kb, ke, part;
@@ -297,82 +306,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
   asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
   if (warp == 0) {
     // ---- `a` and its units, of this CTA's rows
-    uint32_t i = 0;
+    At<S::kStages> s;
     bool go = true;
     for (int unit = unit0; go && unit < args.units; unit += pairs) {
       const Work w = work_of(args, unit, S::kN);
       const int r0 = w.r0 + int(rank) * kRows;
-      for (int k = w.kb; k < w.ke; ++k, ++i) {
-        const uint32_t s = i % S::kStages, n = i / S::kStages;
-        if (n > 0) wait(&a_empty[s], (n - 1) & 1u);
+      for (int k = w.kb; k < w.ke; ++k, s.next()) {
+        wait(&a_empty[s.i], s.parity ^ 1u);  // (passes in the first round)
         if (!(go = going())) break;
-        const uint32_t e = elected(), bar = dev::smem_addr(&a_full[s]);
+        const uint32_t e = elected(), bar = dev::smem_addr(&a_full[s.i]);
         const int at = k * kStep;
-        expect_bytes(e, &a_full[s], S::kABytes + S::kUBytes);
-        load_box<1>(e, s_a + s * S::kABytes, &map_a, at, r0, bar);
+        expect_bytes(e, &a_full[s.i], S::kABytes + S::kUBytes);
+        load_box<1>(e, s_a + s.i * S::kABytes, &map_a, at, r0, bar);
         if constexpr (S::kUnits) {
-          load_box<1>(e, s_u + s * S::kUBytes, &map_u, 2 * at, r0 / kBlock, bar);
-          load_box<1>(e, s_u + s * S::kUBytes + 512, &map_u, 2 * at + 128, r0 / kBlock, bar);
+          load_box<1>(e, s_u + s.i * S::kUBytes, &map_u, 2 * at, r0 / kBlock, bar);
+          load_box<1>(e, s_u + s.i * S::kUBytes + 512, &map_u, 2 * at + 128, r0 / kBlock, bar);
         }
       }
     }
     if (!go) settle();
   } else if (warp == 1) {
     // ---- b, this CTA's half of the columns; completes on the first CTA's barrier
-    uint32_t i = 0;
+    At<S::kStages> s;
     bool go = true;
     for (int unit = unit0; go && unit < args.units; unit += pairs) {
       const Work w = work_of(args, unit, S::kN);
       const int c0 = w.c0 + int(rank) * S::kCols;
-      for (int x = w.kb * args.terms; x < w.ke * args.terms; ++x, ++i) {
-        const uint32_t s = i % S::kStages, n = i / S::kStages;
-        if (n > 0) wait(&b_empty[s], (n - 1) & 1u);
-        if (!(go = going())) break;
-        const uint32_t e = elected(), bar = in_first(&b_full[s]);
-        if (first) expect_bytes(e, &b_full[s], 2 * S::kBBytes);
-        unsigned char* to = s_b + s * S::kBBytes;
-        if constexpr (S::kUnits) {
-          const int k = x / args.terms, at = k * kStep + (x - k * args.terms) * args.depth;
+      for (int k = w.kb; go && k < w.ke; ++k)
+        for (int term = 0; term < args.terms; ++term, s.next()) {
+          wait(&b_empty[s.i], s.parity ^ 1u);
+          if (!(go = going())) break;
+          const uint32_t e = elected(), bar = in_first(&b_full[s.i]);
+          if (first) expect_bytes(e, &b_full[s.i], 2 * S::kBBytes);
+          unsigned char* to = s_b + s.i * S::kBBytes;
+          if constexpr (S::kUnits) {
 #pragma unroll
-          for (int j = 0; j < S::kCols / 64; ++j) load_box<2>(e, to + j * kStep * 128, &map_b, 2 * (c0 + 64 * j), at, bar);
-        } else {
+            for (int j = 0; j < S::kCols / 64; ++j)
+              load_box<2>(e, to + j * kStep * 128, &map_b, 2 * (c0 + 64 * j), k * kStep + term * args.depth, bar);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) load_box<2>(e, to + j * S::kCols * 128, &map_b, 2 * kStep * x + 128 * j, c0, bar);
+            for (int j = 0; j < 2; ++j) load_box<2>(e, to + j * S::kCols * 128, &map_b, 2 * kStep * k + 128 * j, c0, bar);
+          }
         }
-      }
     }
     if (!go) settle();
   } else if (warp == 2) {
     if (first) {
-      // ---- MMAs
-      uint32_t i = 0, ib = 0, runs = 0;
+      // ---- MMAs.  The loop's own instructions have to be few: a stage's MMAs take 512 cycles with 128 columns.
+      At<S::kSlots> t;
+      At<S::kStages> s;
+      At<S::kAccs> b;
+      const uint64_t desc0 = S::kUnits ? columns_desc(dev::smem_addr(s_b)) : operand_desc(dev::smem_addr(s_b));
       for (int unit = unit0; unit < args.units; unit += pairs) {
         const Work w = work_of(args, unit, S::kN);
-        for (int k = w.kb; k < w.ke; ++k, ++i) {
-          const uint32_t t = i % S::kSlots, b = runs % S::kAccs;
-          const bool starts = S::kRuns ? (k - w.kb) % args.run == 0 : k == w.kb;
-          const bool ends = k + 1 == w.ke || (S::kRuns && (k - w.kb) % args.run == args.run - 1);
-          if (starts && runs >= S::kAccs) wait(&acc_empty[b], (runs / S::kAccs - 1) & 1u);
-          wait(&slot_full[t], (i / S::kSlots) & 1u);
-          const uint32_t d = tmem + b * S::kN, a = slots + t * S::kSlotCols;
-          for (int term = 0; term < args.terms; ++term, ++ib) {
-            const uint32_t s = ib % S::kStages;
-            wait(&b_full[s], (ib / S::kStages) & 1u);
+        int left = 0;  // stages until the accumulator changes
+        for (int k = w.kb; k < w.ke; ++k, t.next()) {
+          uint32_t add = 1u;
+          if (left == 0) {
+            left = S::kRuns ? min(args.run, w.ke - k) : w.ke - k;
+            add = 0u;
+            wait(&acc_empty[b.i], b.parity ^ 1u);
+          }
+          wait(&slot_full[t.i], t.parity);
+          const uint32_t d = tmem + b.i * S::kN, a = slots + t.i * S::kSlotCols;
+          for (int term = 0; term < args.terms; ++term, s.next()) {
+            wait(&b_full[s.i], s.parity);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t e = elected(), base = dev::smem_addr(s_b + s * S::kBBytes);
+            const uint32_t e = elected();
+            const uint64_t db = desc0 + s.i * (S::kBBytes >> 4);
 #pragma unroll
             for (int j = 0; j < kStep / 16; ++j) {
-              const uint64_t db = S::kUnits ? columns_desc(base) + j * (16 * 128 >> 4)
-                                            : operand_desc(base) + j / 4 * (S::kCols * 128 >> 4) + j % 4 * 2;
-              mma(e, d, a + 8 * j, db, S::kDesc, !starts || term != 0 || j != 0 ? 1u : 0u);
+              mma(e, d, a + 8 * j, db + (S::kUnits ? j * (16 * 128 >> 4) : j / 4 * (S::kCols * 128 >> 4) + j % 4 * 2), S::kDesc, add);
+              add = 1u;
             }
-            fp4::commit<2>(e, &b_empty[s]);
+            fp4::commit<2>(e, &b_empty[s.i]);
           }
           const uint32_t e = elected();
-          fp4::commit<2>(e, &slot_empty[t]);
-          if (ends) {
-            fp4::commit<2>(e, &acc_full[b]);
-            ++runs;
+          fp4::commit<2>(e, &slot_empty[t.i]);
+          if (--left == 0) {
+            fp4::commit<2>(e, &acc_full[b.i]);
+            b.next();
           }
         }
       }
@@ -391,17 +404,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
       all += uint32_t(w.ke - w.kb);
     }
     uint4 in[8];
-    auto fetch = [&](uint32_t i) {
-      const uint32_t s = i % S::kStages;
-      wait(&a_full[s], (i / S::kStages) & 1u);
-      const uint4* from = reinterpret_cast<const uint4*>(s_a + s * S::kABytes + row * 128);
+    At<S::kStages> s, ahead;
+    At<S::kSlots> t;
+    auto fetch = [&]() {
+      wait(&a_full[ahead.i], ahead.parity);
+      const uint4* from = reinterpret_cast<const uint4*>(s_a + ahead.i * S::kABytes + row * 128);
 #pragma unroll
       for (int j = 0; j < 8; ++j) in[j] = from[j ^ (row & 7)];
     };
-    if (uint32_t(group) < all) fetch(group);
+    if (group) s.next(), ahead.next(), t.next();
+    if (uint32_t(group) < all) fetch();
     for (uint32_t i = group; i < all; i += 2) {
-      const uint32_t s = i % S::kStages, t = i % S::kSlots;
-      const unsigned char* units = s_u + s * S::kUBytes;
+      const unsigned char* units = s_u + s.i * S::kUBytes;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t out[32];
@@ -436,28 +450,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
           }
         }
         if (h == 0) {
-          if (i >= S::kSlots) wait(&slot_empty[t], (i / S::kSlots - 1) & 1u);
+          wait(&slot_empty[t.i], t.parity ^ 1u);
           __syncwarp();
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         } else {
           __syncwarp();
-          if (lane == 0) dev::mbar_arrive(&a_empty[s]);
+          if (lane == 0) dev::mbar_arrive(&a_empty[s.i]);
         }
-        write_tmem32(to + t * S::kSlotCols + 32 * h, out);
+        write_tmem32(to + t.i * S::kSlotCols + 32 * h, out);
       }
-      if (i + 2 < all) fetch(i + 2);
+      ahead.next(), ahead.next();
+      if (i + 2 < all) fetch();
       __syncwarp();
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) arrive_first(&slot_full[t]);
+      if (lane == 0) arrive_first(&slot_full[t.i]);
+      s.next(), s.next(), t.next(), t.next();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ---- epilogue: 32 rows x kV columns a warp
     const int q = warp & 3, half = (warp - 12) >> 2;
     const uint32_t lanes = uint32_t(32 * q) << 16;
-    uint32_t runs = 0;
+    At<S::kAccs> b;
     for (int unit = unit0; unit < args.units; unit += pairs) {
       const Work w = work_of(args, unit, S::kN);
       const int row = w.r0 + int(rank) * kRows + 32 * q + lane, col0 = w.c0 + half * S::kV;
@@ -470,16 +486,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
           if (mine && col0 + c0 + c < args.cols) out[int64_t(c) * args.rows] = bits[c];
       };
       auto acc_wait = [&]() {
-        wait(&acc_full[runs % S::kAccs], (runs / S::kAccs) & 1u);
+        wait(&acc_full[b.i], b.parity);
         __syncwarp();
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        return tmem + (runs % S::kAccs) * S::kN + half * S::kV + lanes;
+        return tmem + b.i * S::kN + half * S::kV + lanes;
       };
       auto acc_free = [&]() {
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_first(&acc_empty[runs % S::kAccs]);
-        ++runs;
+        if (lane == 0) arrive_first(&acc_empty[b.i]);
+        b.next();
       };
       if constexpr (S::kRuns) {
         // Scales of this warp's columns, 32 a register; a row's.

@@ -74,9 +74,9 @@ struct RowArgs {
 // kGroup threads to a row: the row's first 32 kGroup values stay in registers between the search
 // for the largest and the rounding, the rest is read again (from L2).
 template <typename T, int kGroup, RowForm kForm>
-__global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads) rows_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(const RowArgs a) {
   begin();
-  constexpr int kRows = kGroup >= kThreads ? 1 : kThreads / kGroup, kKept = 4;
+  constexpr int kRows = kGroup <= 32 ? kThreads / kGroup : 1, kKept = 4;
   const int t = threadIdx.x % kGroup;
   const int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / kGroup;
   if (kGroup <= 32 && row >= a.rows) return;  // whole warps
@@ -114,17 +114,15 @@ __global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads) rows_ke
   if (t == 0) a.scales[row] = s;
   const int64_t out_chunks = kForm == kBytes ? (a.cols + 15) / 16 * 2 : chunks;
   auto write = [&](int64_t c, const float (&w)[8]) {
-    int q[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = nearest(w[e], s, inv);
+    float n[8];
+    nearest8(w, s, inv, n);
     if constexpr (kForm == kBytes) {
-      *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.out) + row * a.ld + 8 * c) =
-          make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+      *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.out) + row * a.ld + 8 * c) = pack8(n);
     } else {
       uint4 h;
       __half2* p = reinterpret_cast<__half2*>(&h);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = __halves2half2(__int2half_rn(q[2 * e]), __int2half_rn(q[2 * e + 1]));
+      for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(n[2 * e] - kRound, n[2 * e + 1] - kRound);
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.ld + 8 * c) = h;
     }
   };
@@ -139,13 +137,47 @@ __global__ void __launch_bounds__(kGroup > kThreads ? kGroup : kThreads) rows_ke
   }
 }
 
+// As few threads to a row as keep all of it.
 template <RowForm kForm>
 cudaError_t launch_rows(int dtype, const RowArgs& a, cudaStream_t stream) {
   const int64_t few = (a.rows + kThreads / 32 - 1) / (kThreads / 32);
   if (a.cols <= 1024) GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 32, kForm>, few, kThreads, stream, a))
-  if (a.cols <= 8192) GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 256, kForm>, a.rows, kThreads, stream, a))
+  if (a.cols <= 4096) GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 128, kForm>, a.rows, 128, stream, a))
+  if (a.cols <= 8192) GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 256, kForm>, a.rows, 256, stream, a))
   GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 1024, kForm>, a.rows, 1024, stream, a))
 }
+
+// A matrix's chunks of eight columns, divided into one run of consecutive chunks for each block.
+struct Chunks {
+  int64_t all, per_block;
+  int64_t row_chunks;
+  Divider div;
+};
+// This thread's chunk in each step of its block's run.
+struct Walk {
+  int64_t row0, left;
+  uint32_t c0;
+
+  __device__ __forceinline__ explicit Walk(const Chunks& n) {
+    const int64_t first = int64_t(blockIdx.x) * n.per_block;
+    row0 = first / n.row_chunks;
+    c0 = uint32_t(first - row0 * n.row_chunks);
+    left = min(n.per_block, n.all - first);
+  }
+  // Whether this thread has one; its row and its place in the row.
+  __device__ __forceinline__ bool at(const Chunks& n, int64_t& row, int64_t& c) const {
+    const uint32_t i = c0 + threadIdx.x, r = divide(i, n.div);
+    row = row0 + r;
+    c = i - r * n.div.d;
+    return threadIdx.x < left;
+  }
+  __device__ __forceinline__ void next(const Chunks& n) {
+    const uint32_t i = c0 + kThreads, r = divide(i, n.div);
+    row0 += r;
+    c0 = i - r * n.div.d;
+    left -= kThreads;
+  }
+};
 
 struct BackArgs {
   const int8_t* codes;
@@ -155,36 +187,43 @@ struct BackArgs {
   void* out;
   int64_t ld_out;
   int32_t vec;
+  Chunks n;
 };
 
-// Chunks of eight over all threads; a chunk's row and place come from one division.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const BackArgs a) {
   begin();
-  const int64_t chunks = (a.cols + 7) / 8, all = a.rows * chunks;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
-    const int64_t row = i / chunks, c = i - row * chunks;
-    const int2 w = *reinterpret_cast<const int2*>(a.codes + row * a.ld + 8 * c);
+  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
+    int64_t row, c;
+    if (!w.at(a.n, row, c)) break;
+    const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
     const float s = a.scales[row];
-    const int8_t* q = reinterpret_cast<const int8_t*>(&w);
     float v[8];
+    widen4(q.x, v);
+    widen4(q.y, v + 4);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = float(q[e]) * s;
+    for (int e = 0; e < 8; ++e) v[e] *= s;
     store8(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, a.cols - 8 * c, a.vec, v);
   }
 }
 
 __global__ void __launch_bounds__(kThreads) widen_kernel(const BackArgs a) {
   begin();
-  const int64_t chunks = (a.cols + 7) / 8, all = a.rows * chunks;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
-    const int64_t row = i / chunks, c = i - row * chunks;
-    const int2 w = *reinterpret_cast<const int2*>(a.codes + row * a.ld + 8 * c);
-    const int8_t* q = reinterpret_cast<const int8_t*>(&w);
-    uint4 h;
-    __half* p = reinterpret_cast<__half*>(&h);
+  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
+    int64_t row, c;
+    if (!w.at(a.n, row, c)) break;
+    const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
+    float v[8];
+    widen4(q.x, v);
+    widen4(q.y, v + 4);
+    if (8 * c + 8 > a.cols) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = __int2half_rn(8 * c + e < a.cols ? q[e] : 0);
+      for (int e = 0; e < 8; ++e) v[e] = 8 * c + e < a.cols ? v[e] : 0.f;
+    }
+    uint4 h;
+    __half2* p = reinterpret_cast<__half2*>(&h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + 8 * c) = h;
   }
 }
@@ -197,6 +236,7 @@ struct SplitArgs {
   uint16_t* out;
   int64_t ld;
   int32_t vec;
+  Chunks n;
 };
 
 // The upper 16 bits of v's 32 (v's first eight significant bits), and v less that; a value that is
@@ -214,9 +254,9 @@ __device__ __forceinline__ uint32_t take16(float& v) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
   begin();
-  const int64_t chunks = (a.cols + 7) / 8, all = a.rows * chunks;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
-    const int64_t row = i / chunks, c = i - row * chunks;
+  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
+    int64_t row, c;
+    if (!w.at(a.n, row, c)) break;
     float v[8];
     load8(static_cast<const T*>(a.x) + row * a.ldx + 8 * c, a.cols - 8 * c, a.vec, v);
     uint16_t* out = a.out + row * a.ld + 8 * c;
@@ -271,19 +311,19 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const KeepArgs a) {
       const int64_t t = t0 + 4 * m + i;
       load8(x + t * a.ldx, t < a.rows ? left : 0, a.vec, v[i]);
     }
-    int q[4][8];
+    float q[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float top = largest8(v[i]);
       top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float inverse = unit_inverse<kHalf>(top);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[i][e] = kept(v[i][e], inverse);
+      keep8(v[i], top, unit_inverse<kHalf>(top), q[i]);
       if (g % 4 == 0) units[g / 4][4 * m + i] = t0 + 4 * m + i < a.rows ? uint16_t(unit_bits<kHalf>(top)) : 0;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) codes[(8 * g + e) * 32 + (m ^ (2 * g))] = pack4(q[0][e], q[1][e], q[2][e], q[3][e]);
+    for (int e = 0; e < 8; ++e)
+      codes[(8 * g + e) * 32 + (m ^ (2 * g))] =
+          pack4(__float_as_int(q[0][e]), __float_as_int(q[1][e]), __float_as_int(q[2][e]), __float_as_int(q[3][e]));
   }
   __syncthreads();
   // 16 tokens of a channel a thread; `ld` covers the tokens rounded up to 16.
@@ -314,20 +354,22 @@ struct RestoreArgs {
   void* out;
   int64_t ld_out;
   int32_t vec;
+  Chunks n;
 };
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) restore_tokens_kernel(const RestoreArgs a) {
   begin();
-  const int64_t chunks = (a.cols + 7) / 8, all = a.rows * chunks;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
-    const int64_t row = i / chunks, c = i - row * chunks;
-    const int2 w = *reinterpret_cast<const int2*>(a.codes + row * a.ld + 8 * c);
+  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
+    int64_t row, c;
+    if (!w.at(a.n, row, c)) break;
+    const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
     const float u = unit_value(a.units[row * a.ldu + c / 4], a.half);
-    const int8_t* q = reinterpret_cast<const int8_t*>(&w);
     float v[8];
+    widen4(q.x, v);
+    widen4(q.y, v + 4);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = float(q[e]) * u;
+    for (int e = 0; e < 8; ++e) v[e] *= u;
     store8(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, a.cols - 8 * c, a.vec, v);
   }
 }
@@ -373,43 +415,52 @@ struct SwigluArgs {
   uint16_t *ug, *uu;
   int64_t ldug, lduu;
   int32_t vec;
+  Chunks n;
 };
 
-__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.f + expf(-x)); }
+// 16-bit types: the exponential of the rounded product x log2(e), within (|x| + 2) 2^-23 of itself, and a reciprocal
+// within 2^-23: far below the types' own steps.  32 bits: within 2^-22 whatever x is.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float x) {
+  if constexpr (sizeof(T) == 4) {
+    return __frcp_rn(1.f + expf(-x));
+  } else {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x)));
+    return r;
+  }
+}
 
 // Keeps eight of a block's values (the four lanes of a block together).
 template <bool kHalf>
-__device__ __forceinline__ void keep8(const float (&v)[8], int8_t* codes, uint16_t* unit, bool first, bool write) {
-  float top = largest8(v);
+__device__ __forceinline__ void keep_block(const float (&v)[8], int8_t* codes, uint16_t* unit, bool first, bool write) {
+  float top = largest8(v), t[8];
   top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const float inverse = unit_inverse<kHalf>(top);
-  int q[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = kept(v[e], inverse);
-  if (write) *reinterpret_cast<uint2*>(codes) = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+  keep8(v, top, unit_inverse<kHalf>(top), t);
+  if (write) *reinterpret_cast<uint2*>(codes) = pack8(t);
   if (write && first) *unit = uint16_t(unit_bits<kHalf>(top));
 }
 
-// Four lanes to a block; columns rounded up to whole blocks so that a block's lanes stay together.
+// Four lanes to a block; a row's columns are rounded up to whole blocks so that a block's lanes stay together.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
   begin();
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
-  const int64_t blocks = (a.cols + 31) / 32, chunks = 4 * blocks, all = a.rows * chunks;
-  for (int64_t i0 = int64_t(blockIdx.x) * kThreads; i0 < all; i0 += int64_t(gridDim.x) * kThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool here = i < all;
-    const int64_t row = here ? i / chunks : 0, c = here ? i - row * chunks : 0, left = here ? a.cols - 8 * c : 0;
+  const int64_t blocks = (a.cols + 31) / 32;
+  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
+    int64_t row, c;
+    const bool here = w.at(a.n, row, c);
+    const int64_t left = here ? a.cols - 8 * c : 0;
     float g[8], u[8], h[8];
     load8(static_cast<const T*>(a.gate) + row * a.ldg + 8 * c, left, a.vec, g);
     load8(static_cast<const T*>(a.up) + row * a.ldu + 8 * c, left, a.vec, u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = g[e] * sigmoid(g[e]) * u[e];
+    for (int e = 0; e < 8; ++e) h[e] = g[e] * sigmoid<T>(g[e]) * u[e];
     if (left > 0) store8(static_cast<T*>(a.h) + row * a.ldh + 8 * c, left, a.vec, h);
     const bool write = here && 8 * c < (a.cols + 15) / 16 * 16;
-    keep8<kHalf>(g, a.kg + row * a.ldkg + 8 * c, a.ug + row * a.ldug + c / 4, c % 4 == 0, write);
-    keep8<kHalf>(u, a.ku + row * a.ldku + 8 * c, a.uu + row * a.lduu + c / 4, c % 4 == 0, write);
+    keep_block<kHalf>(g, a.kg + row * a.ldkg + 8 * c, a.ug + row * a.ldug + c / 4, c % 4 == 0, write);
+    keep_block<kHalf>(u, a.ku + row * a.ldku + 8 * c, a.uu + row * a.lduu + c / 4, c % 4 == 0, write);
     // Units that pad the row.
     if (here && c % 4 == 0 && c / 4 == blocks - 1)
       for (int64_t b = blocks; b < (blocks + 7) / 8 * 8; ++b) a.ug[row * a.ldug + b] = a.uu[row * a.lduu + b] = 0;
@@ -421,27 +472,39 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluA
                                                                    int64_t lddg, T* dup, int64_t lddu) {
   begin();
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
-  const int64_t chunks = (a.cols + 7) / 8, all = a.rows * chunks;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
-    const int64_t row = i / chunks, c = i - row * chunks, left = a.cols - 8 * c;
-    const int2 wg = *reinterpret_cast<const int2*>(a.kg + row * a.ldkg + 8 * c);
-    const int2 wu = *reinterpret_cast<const int2*>(a.ku + row * a.ldku + 8 * c);
+  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
+    int64_t row, c;
+    if (!w.at(a.n, row, c)) break;
+    const int64_t left = a.cols - 8 * c;
+    const uint2 wg = *reinterpret_cast<const uint2*>(a.kg + row * a.ldkg + 8 * c);
+    const uint2 wu = *reinterpret_cast<const uint2*>(a.ku + row * a.ldku + 8 * c);
     const float ug = unit_value(a.ug[row * a.ldug + c / 4], kHalf), uu = unit_value(a.uu[row * a.lduu + c / 4], kHalf);
-    float d[8], dg[8], du[8];
+    float d[8], g[8], u[8];
     load8(dh + row * lddh + 8 * c, left, a.vec, d);
-    const int8_t *qg = reinterpret_cast<const int8_t*>(&wg), *qu = reinterpret_cast<const int8_t*>(&wu);
+    widen4(wg.x, g), widen4(wg.y, g + 4);
+    widen4(wu.x, u), widen4(wu.y, u + 4);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float g = float(qg[e]) * ug, u = float(qu[e]) * uu, s = sigmoid(g);
-      dg[e] = d[e] * u * s * (1.f + g * (1.f - s));
-      du[e] = d[e] * (g * s);
+      const float x = g[e] * ug, s = sigmoid<T>(x);
+      g[e] = d[e] * (u[e] * uu) * s * (1.f + x * (1.f - s));
+      u[e] = d[e] * (x * s);
     }
-    store8(dgate + row * lddg + 8 * c, left, a.vec, dg);
-    store8(dup + row * lddu + 8 * c, left, a.vec, du);
+    store8(dgate + row * lddg + 8 * c, left, a.vec, g);
+    store8(dup + row * lddu + 8 * c, left, a.vec, u);
   }
 }
 
-int64_t spread(int64_t items, int sms) { return std::min((items + kThreads - 1) / kThreads, int64_t(sms) * 8); }
+// Rows of `row_chunks` chunks over blocks, eight on an SM at most.
+Chunks chunks_of(int64_t rows, int64_t row_chunks, int sms) {
+  Chunks n{};
+  n.all = rows * row_chunks;
+  n.row_chunks = row_chunks;
+  n.div = divider(uint32_t(row_chunks));
+  const int64_t steps = (n.all + kThreads - 1) / kThreads, blocks = std::min(steps, int64_t(sms) * 8);
+  n.per_block = (steps + blocks - 1) / blocks * kThreads;
+  return n;
+}
+int64_t blocks_of(const Chunks& n) { return (n.all + n.per_block - 1) / n.per_block; }
 int64_t bytes_of(int dtype) { return dtype == INT8_F32 ? 4 : 2; }
 
 }  // namespace
@@ -459,23 +522,22 @@ cudaError_t launch_int8_rows16(int dtype, const void* x, int64_t ldx, int64_t ro
 
 cudaError_t launch_int8_dequantize(const int8_matrix_t& q, int dtype, void* y, int64_t ldy, int sms,
                                    cudaStream_t stream) {
-  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, y, ldy, aligned16(y, ldy * bytes_of(dtype))};
-  const int64_t grid = spread(q.rows * ((q.cols + 7) / 8), sms);
-  GB300_INT8_BY_TYPE(dtype, launch(dequantize_kernel<T>, grid, kThreads, stream, a))
+  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, y, ldy, aligned16(y, ldy * bytes_of(dtype)),
+                   chunks_of(q.rows, (q.cols + 7) / 8, sms)};
+  GB300_INT8_BY_TYPE(dtype, launch(dequantize_kernel<T>, blocks_of(a.n), kThreads, stream, a))
 }
 
 cudaError_t launch_int8_widen(const int8_matrix_t& q, uint16_t* out, int64_t ld, int sms, cudaStream_t stream) {
-  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, out, ld, 1};
-  return launch(widen_kernel, spread(q.rows * ((q.cols + 7) / 8), sms), kThreads, stream, a);
+  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, out, ld, 1, chunks_of(q.rows, (q.cols + 7) / 8, sms)};
+  return launch(widen_kernel, blocks_of(a.n), kThreads, stream, a);
 }
 
 int int8_terms(int dtype) { return dtype == INT8_F32 ? 3 : 1; }
 
 cudaError_t launch_int8_split(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
                               int64_t ld, int sms, cudaStream_t stream) {
-  const SplitArgs a{x, ldx, rows, cols, out, ld, aligned16(x, ldx * bytes_of(dtype))};
-  const int64_t grid = spread(rows * ((cols + 7) / 8), sms);
-  GB300_INT8_BY_TYPE(dtype, launch(split_kernel<T>, grid, kThreads, stream, a))
+  const SplitArgs a{x, ldx, rows, cols, out, ld, aligned16(x, ldx * bytes_of(dtype)), chunks_of(rows, (cols + 7) / 8, sms)};
+  GB300_INT8_BY_TYPE(dtype, launch(split_kernel<T>, blocks_of(a.n), kThreads, stream, a))
 }
 
 cudaError_t launch_int8_keep(const void* x, int64_t ldx, const int8_checkpoint_t& c, cudaStream_t stream) {
@@ -488,10 +550,9 @@ cudaError_t launch_int8_keep(const void* x, int64_t ldx, const int8_checkpoint_t
 cudaError_t launch_int8_restore(const int8_checkpoint_t& c, int dtype, void* y, int64_t ldy, int sms,
                                 cudaStream_t stream) {
   const RestoreArgs a{c.codes, c.ld, c.units, c.ld_units, c.rows, c.cols, c.dtype == INT8_F16, y, ldy,
-                      aligned16(y, ldy * bytes_of(dtype))};
+                      aligned16(y, ldy * bytes_of(dtype)), chunks_of(c.rows, (c.cols + 7) / 8, sms)};
   if (c.order == INT8_TOKENS) {
-    const int64_t grid = spread(c.rows * ((c.cols + 7) / 8), sms);
-    GB300_INT8_BY_TYPE(dtype, launch(restore_tokens_kernel<T>, grid, kThreads, stream, a))
+    GB300_INT8_BY_TYPE(dtype, launch(restore_tokens_kernel<T>, blocks_of(a.n), kThreads, stream, a))
   }
   const int64_t tiles = std::min((c.rows + 63) / 64 * ((c.cols + 31) / 32), int64_t(sms) * 16);
   GB300_INT8_BY_TYPE(dtype, launch(restore_channels_kernel<T>, tiles, 128, stream, a))
@@ -503,9 +564,9 @@ cudaError_t launch_int8_swiglu(int dtype, int64_t M, int64_t F, const void* gate
   const int64_t es = bytes_of(dtype);
   const SwigluArgs a{gate, up, ldg, ldu, M, F, h, ldh, kg.codes, ku.codes, kg.ld, ku.ld, kg.units, ku.units,
                      kg.ld_units, ku.ld_units,
-                     aligned16(gate, ldg * es) && aligned16(up, ldu * es) && aligned16(h, ldh * es)};
-  const int64_t grid = spread(M * ((F + 31) / 32) * 4, sms);
-  GB300_INT8_BY_TYPE(dtype, launch(swiglu_kernel<T>, grid, kThreads, stream, a))
+                     aligned16(gate, ldg * es) && aligned16(up, ldu * es) && aligned16(h, ldh * es),
+                     chunks_of(M, (F + 31) / 32 * 4, sms)};
+  GB300_INT8_BY_TYPE(dtype, launch(swiglu_kernel<T>, blocks_of(a.n), kThreads, stream, a))
 }
 
 cudaError_t launch_int8_swiglu_backward(const void* dh, int64_t lddh, const int8_checkpoint_t& kg,
@@ -518,9 +579,9 @@ cudaError_t launch_int8_swiglu_backward(const void* dh, int64_t lddh, const int8
   a.kg = kg.codes, a.ku = ku.codes, a.ldkg = kg.ld, a.ldku = ku.ld;
   a.ug = kg.units, a.uu = ku.units, a.ldug = kg.ld_units, a.lduu = ku.ld_units;
   a.vec = aligned16(dh, lddh * es) && aligned16(dgate, ldg * es) && aligned16(dup, ldu * es);
-  const int64_t grid = spread(kg.rows * ((kg.cols + 7) / 8), sms);
+  a.n = chunks_of(kg.rows, (kg.cols + 7) / 8, sms);
   GB300_INT8_BY_TYPE(kg.dtype,
-                     launch(swiglu_backward_kernel<T>, grid, kThreads, stream, a, static_cast<const T*>(dh), lddh,
+                     launch(swiglu_backward_kernel<T>, blocks_of(a.n), kThreads, stream, a, static_cast<const T*>(dh), lddh,
                             static_cast<T*>(dgate), ldg, static_cast<T*>(dup), ldu))
 }
 

@@ -105,8 +105,63 @@ template <bool kHalf>
 __device__ __forceinline__ float unit_inverse(float a) {
   return finite(a) ? __uint_as_float(uint32_t(127 - unit_exponent<kHalf>(a)) << 23) : 0.f;
 }
-// x / u rounded to an integer; not finite only if its block is not (x * 0 = NaN becomes 0 in the conversion).
-__device__ __forceinline__ int kept(float x, float inverse) { return max(-127, min(127, __float2int_rn(x * inverse))); }
+
+// 3 * 2^22: a number up to 2^22 in magnitude that is added to it is rounded to the nearest integer, ties to
+// even, which the low bits of the sum then hold.  (A conversion instruction has an eighth of the rate of an addition.)
+constexpr float kRound = 12582912.f;
+
+__device__ __forceinline__ uint2 pack8(const float (&t)[8]) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = pack4(__float_as_int(t[4 * i]), __float_as_int(t[4 * i + 1]), __float_as_int(t[4 * i + 2]), __float_as_int(t[4 * i + 3]));
+  return make_uint2(w[0], w[1]);
+}
+
+// Eight values of a block whose largest magnitude is `top`, as integers on kRound.
+__device__ __forceinline__ void keep8(const float (&v)[8], float top, float inverse, float (&t)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] = fmaf(v[e], inverse, kRound);
+  if (!(top * inverse < 127.5f)) {  // one may round to 128, or the block is not finite
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = finite(top) ? fminf(fmaxf(t[e], kRound - 127.f), kRound + 127.f) : kRound;
+  }
+}
+
+// Eight values of a row of scale s, as integers on kRound.  x inv is within 2^-16 of x / s, so its nearest integer
+// is the answer unless it lies within 2^-13 of a tie.
+__device__ __forceinline__ void nearest8(const float (&v)[8], float s, float inv, float (&t)[8]) {
+  float far = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    t[e] = fmaf(v[e], inv, kRound);
+    far = fmaxf(far, fabsf(fmaf(v[e], inv, kRound - t[e])));
+  }
+  if (far > 0.5f - 0x1p-13f || !(s < 0x1p127f)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = kRound + float(nearest(v[e], s, inv));
+  }
+}
+
+// A word's four integers as numbers: the low bits of 2^23 + 128 + q, of which 2^23 + 128 is taken off.
+__device__ __forceinline__ void widen4(uint32_t word, float* v) {
+  const uint32_t biased = word ^ 0x80808080u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7540 + e)) - 8388736.f;
+}
+
+// n / d for 0 <= n < 2^31, with m = floor(2^(31 + s) / d) + 1 and 2^s >= d: n m / 2^(31 + s) is above n / d by
+// less than 1 / d.
+struct Divider {
+  uint64_t m;
+  uint32_t s, d;
+};
+inline Divider divider(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < d) ++s;
+  return {(uint64_t(1) << (31 + s)) / d + 1, s, d};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divider& v) { return uint32_t(uint64_t(n) * v.m >> (31 + v.s)); }
 
 }  // namespace int8
 }  // namespace gb300

@@ -48,6 +48,7 @@ using fp4::uniform_warp;
 constexpr uint32_t kStatusTimeout = 3;
 constexpr int kStep = 128;               // elements of k a stage
 constexpr int kRows = 128;               // of a CTA
+constexpr int kGroups = 2;               // of four warps that turn `a` to 16 bits
 
 // kIntegers: 16-bit floats of integers, b K-major.  Others: a checkpoint's values in bfloat16 or 16-bit floats, b MN-major.
 enum Kind { kIntegers, kBf16, kF16 };
@@ -66,7 +67,7 @@ struct Tile {
   static constexpr int kSlots = kSlots0 < 6 ? kSlots0 : 6;
   static constexpr int kStages0 = int((232448 - 1024 - 512) / (kABytes + kUBytes + kBBytes));
   static constexpr int kStages = kStages0 < 8 ? kStages0 : 8;
-  static constexpr int kThreads = 640;
+  static constexpr int kThreads = 128 * (3 + kGroups);
   static constexpr int kV = kN / 2;  // columns of an epilogue warp
   static constexpr int kBarriers = 4 * kStages + 2 * kSlots + 2 * kAccs + 1;
   static constexpr size_t kSmem = 1024 + kStages * size_t(kABytes + kUBytes + kBBytes) + kBarriers * 8 + 16;
@@ -393,85 +394,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
       dev::mbar_wait(drain, 0u, limit);
     }
   }
-  } else if (warp < 12) {
-    // ---- `a` to 16 bits, in tensor memory.  A stage's bytes are read before the stage before is handed over.
+  } else if (warp < 4 + 4 * kGroups) {
+    // ---- `a` to 16 bits, in tensor memory
     const int q = warp & 3, group = (warp - 4) >> 2, row = 32 * q + lane;
     const uint32_t to = slots + (uint32_t(32 * q) << 16);
-    // Stages of this pair, over all of its units.
-    uint32_t all = 0;
+    At<S::kStages> s;
+    At<S::kSlots> t;
+    int turn = 0;
     for (int unit = unit0; unit < args.units; unit += pairs) {
       const Work w = work_of(args, unit, S::kN);
-      all += uint32_t(w.ke - w.kb);
-    }
-    uint4 in[8];
-    At<S::kStages> s, ahead;
-    At<S::kSlots> t;
-    auto fetch = [&]() {
-      wait(&a_full[ahead.i], ahead.parity);
-      const uint4* from = reinterpret_cast<const uint4*>(s_a + ahead.i * S::kABytes + row * 128);
+      for (int k = w.kb; k < w.ke; ++k, s.next(), t.next()) {
+        const bool mine = turn == group;
+        if (++turn == kGroups) turn = 0;
+        if (!mine) continue;
+        wait(&a_full[s.i], s.parity);
+        const uint4* from = reinterpret_cast<const uint4*>(s_a + s.i * S::kABytes + row * 128);
+        const unsigned char* units = s_u + s.i * S::kUBytes;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) in[j] = from[j ^ (row & 7)];
-    };
-    if (group) s.next(), ahead.next(), t.next();
-    if (uint32_t(group) < all) fetch();
-    for (uint32_t i = group; i < all; i += 2) {
-      const unsigned char* units = s_u + s.i * S::kUBytes;
+        for (int h = 0; h < 2; ++h) {
+          uint4 in[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t out[32];
+          for (int j = 0; j < 4; ++j) in[j] = from[(4 * h + j) ^ (row & 7)];
+          uint32_t out[32];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t word[4] = {in[4 * h + j].x, in[4 * h + j].y, in[4 * h + j].z, in[4 * h + j].w};
-          if constexpr (S::kUnits) {
-            // 16 units, two 16-byte pieces of row q (its second 64 in the second box) of the swizzled boxes.
-            uint32_t u[8];
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t word[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
+            if constexpr (S::kUnits) {
+              // 16 units, two 16-byte pieces of row q (its second 64 in the second box) of the swizzled boxes.
+              uint32_t u[8];
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-              *reinterpret_cast<uint4*>(u + 4 * p) = *reinterpret_cast<const uint4*>(
-                  units + h * 512 + q * 128 + (((2 * j + p) ^ (q + 4 * h)) << 4));
+              for (int p = 0; p < 2; ++p)
+                *reinterpret_cast<uint4*>(u + 4 * p) = *reinterpret_cast<const uint4*>(
+                    units + h * 512 + q * 128 + (((2 * j + p) ^ (q + 4 * h)) << 4));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              if constexpr (S::kKind == kBf16) {
-                out[8 * j + 2 * x] = bmul2(to_bf16<0>(word[x]), u[2 * x]);
-                out[8 * j + 2 * x + 1] = bmul2(to_bf16<1>(word[x]), u[2 * x + 1]);
-              } else {
+              for (int x = 0; x < 4; ++x) {
+                if constexpr (S::kKind == kBf16) {
+                  out[8 * j + 2 * x] = bmul2(to_bf16<0>(word[x]), u[2 * x]);
+                  out[8 * j + 2 * x + 1] = bmul2(to_bf16<1>(word[x]), u[2 * x + 1]);
+                } else {
+                  const uint32_t v = word[x] ^ 0x80808080u;
+                  out[8 * j + 2 * x] = hmul2(to_f16<0>(v), u[2 * x]);
+                  out[8 * j + 2 * x + 1] = hmul2(to_f16<1>(v), u[2 * x + 1]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
                 const uint32_t v = word[x] ^ 0x80808080u;
-                out[8 * j + 2 * x] = hmul2(to_f16<0>(v), u[2 * x]);
-                out[8 * j + 2 * x + 1] = hmul2(to_f16<1>(v), u[2 * x + 1]);
+                out[8 * j + 2 * x] = to_f16<0>(v);
+                out[8 * j + 2 * x + 1] = to_f16<1>(v);
               }
             }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t v = word[x] ^ 0x80808080u;
-              out[8 * j + 2 * x] = to_f16<0>(v);
-              out[8 * j + 2 * x + 1] = to_f16<1>(v);
-            }
           }
+          if (h == 0) {
+            wait(&slot_empty[t.i], t.parity ^ 1u);
+            __syncwarp();
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          } else {
+            __syncwarp();
+            if (lane == 0) dev::mbar_arrive(&a_empty[s.i]);
+          }
+          write_tmem32(to + t.i * S::kSlotCols + 32 * h, out);
         }
-        if (h == 0) {
-          wait(&slot_empty[t.i], t.parity ^ 1u);
-          __syncwarp();
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        } else {
-          __syncwarp();
-          if (lane == 0) dev::mbar_arrive(&a_empty[s.i]);
-        }
-        write_tmem32(to + t.i * S::kSlotCols + 32 * h, out);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive_first(&slot_full[t.i]);
       }
-      ahead.next(), ahead.next();
-      if (i + 2 < all) fetch();
-      __syncwarp();
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) arrive_first(&slot_full[t.i]);
-      s.next(), s.next(), t.next(), t.next();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ---- epilogue: 32 rows x kV columns a warp
-    const int q = warp & 3, half = (warp - 12) >> 2;
+    const int q = warp & 3, half = (warp - 4 - 4 * kGroups) >> 2;
     const uint32_t lanes = uint32_t(32 * q) << 16;
     At<S::kAccs> b;
     for (int unit = unit0; unit < args.units; unit += pairs) {

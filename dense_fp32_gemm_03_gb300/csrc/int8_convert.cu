@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "int8_device.cuh"
 #include "int8_internal.h"
@@ -68,12 +69,11 @@ struct RowArgs {
   void* out;
   int64_t ld;  // of out, in its elements
   float* scales;
-  int32_t vec;
 };
 
-// kGroup threads to a row: the row's first 32 kGroup values stay in registers between the search
-// for the largest and the rounding, the rest is read again (from L2).
-template <typename T, int kGroup, RowForm kForm>
+// kGroup threads to a row: the row's first 32 kGroup values stay in registers, as they are in memory, between
+// the search for the largest and the rounding; the rest is read again (from L2).
+template <typename T, int kGroup, RowForm kForm, bool kVec>
 __global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(const RowArgs a) {
   begin();
   constexpr int kRows = kGroup <= 32 ? kThreads / kGroup : 1, kKept = 4;
@@ -81,24 +81,34 @@ __global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(
   const int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / kGroup;
   if (kGroup <= 32 && row >= a.rows) return;  // whole warps
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-  const int64_t chunks = (a.cols + 7) / 8;
-  float v[kKept][8], top = 0.f;
+  const int cols = int(a.cols), chunks = (cols + 7) / 8;
+  Eight<T> kept[kKept];
+  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
-    const int64_t c = t + i * kGroup;
-    if (c < chunks) {
-      load8(x + 8 * c, a.cols - 8 * c, a.vec, v[i]);
+    const int c = t + i * kGroup;
+    if constexpr (kVec) {
+      if (c < chunks)
+        kept[i] = reinterpret_cast<const Eight<T>*>(x)[c];
+      else
+        kept[i] = Eight<T>{};
     } else {
+      T* to = reinterpret_cast<T*>(&kept[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      for (int e = 0; e < 8; ++e) to[e] = 8 * c + e < cols ? x[8 * c + e] : from_f32<T>(0.f);
     }
-    top = max_abs(top, largest8(v[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    float v[8];
+    values(kept[i], v);
+    top = max_abs(top, largest8(v));
   }
 #pragma unroll 1
-  for (int64_t c = t + kKept * kGroup; c < chunks; c += kGroup) {
-    float w[8];
-    load8(x + 8 * c, a.cols - 8 * c, a.vec, w);
-    top = max_abs(top, largest8(w));
+  for (int c = t + kKept * kGroup; c < chunks; c += kGroup) {
+    float v[8];
+    load8<kVec>(x + 8 * c, cols - 8 * c, v);
+    top = max_abs(top, largest8(v));
   }
 #pragma unroll
   for (int d = 16; d; d /= 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -112,8 +122,8 @@ __global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(
   }
   const float s = row_scale(top), inv = __frcp_rn(s);
   if (t == 0) a.scales[row] = s;
-  const int64_t out_chunks = kForm == kBytes ? (a.cols + 15) / 16 * 2 : chunks;
-  auto write = [&](int64_t c, const float (&w)[8]) {
+  const int out_chunks = kForm == kBytes ? (cols + 15) / 16 * 2 : chunks;
+  auto write = [&](int c, const float (&w)[8]) {
     float n[8];
     nearest8(w, s, inv, n);
     if constexpr (kForm == kBytes) {
@@ -127,24 +137,41 @@ __global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(
     }
   };
 #pragma unroll
-  for (int i = 0; i < kKept; ++i)
-    if (t + i * kGroup < out_chunks) write(t + i * kGroup, v[i]);
+  for (int i = 0; i < kKept; ++i) {
+    const int c = t + i * kGroup;
+    if (c < out_chunks) {
+      float v[8];
+      values(kept[i], v);
+      write(c, v);
+    }
+  }
 #pragma unroll 1
-  for (int64_t c = t + kKept * kGroup; c < out_chunks; c += kGroup) {
-    float w[8];
-    load8(x + 8 * c, a.cols - 8 * c, a.vec, w);
-    write(c, w);
+  for (int c = t + kKept * kGroup; c < out_chunks; c += kGroup) {
+    float v[8];
+    if (kVec && c >= chunks) {  // the chunk of zeros that fills 16 bytes
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    } else {
+      load8<kVec>(x + 8 * c, cols - 8 * c, v);
+    }
+    write(c, v);
   }
 }
 
+// Whether the kernels read and write 16 bytes at a time: rows start at multiples of 16 bytes and hold whole chunks.
+bool whole(int64_t cols, bool aligned) { return aligned && cols % 8 == 0; }
+
 // As few threads to a row as keep all of it.
+template <typename T, RowForm kForm, bool kVec>
+cudaError_t launch_rows_of(const RowArgs& a, cudaStream_t stream) {
+  if (a.cols <= 1024) return launch(rows_kernel<T, 32, kForm, kVec>, (a.rows + kThreads / 32 - 1) / (kThreads / 32), kThreads, stream, a);
+  if (a.cols <= 4096) return launch(rows_kernel<T, 128, kForm, kVec>, a.rows, 128, stream, a);
+  if (a.cols <= 8192) return launch(rows_kernel<T, 256, kForm, kVec>, a.rows, 256, stream, a);
+  return launch(rows_kernel<T, 1024, kForm, kVec>, a.rows, 1024, stream, a);
+}
 template <RowForm kForm>
-cudaError_t launch_rows(int dtype, const RowArgs& a, cudaStream_t stream) {
-  const int64_t few = (a.rows + kThreads / 32 - 1) / (kThreads / 32);
-  if (a.cols <= 1024) GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 32, kForm>, few, kThreads, stream, a))
-  if (a.cols <= 4096) GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 128, kForm>, a.rows, 128, stream, a))
-  if (a.cols <= 8192) GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 256, kForm>, a.rows, 256, stream, a))
-  GB300_INT8_BY_TYPE(dtype, launch(rows_kernel<T, 1024, kForm>, a.rows, 1024, stream, a))
+cudaError_t launch_rows(int dtype, const RowArgs& a, bool vec, cudaStream_t stream) {
+  GB300_INT8_BY_TYPE(dtype, (vec ? launch_rows_of<T, kForm, true>(a, stream) : launch_rows_of<T, kForm, false>(a, stream)))
 }
 
 // A matrix's chunks of eight columns, divided into one run of consecutive chunks for each block.
@@ -186,11 +213,10 @@ struct BackArgs {
   int64_t rows, cols;
   void* out;
   int64_t ld_out;
-  int32_t vec;
   Chunks n;
 };
 
-template <typename T>
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const BackArgs a) {
   begin();
   for (Walk w(a.n); w.left > 0; w.next(a.n)) {
@@ -203,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const BackArgs a) 
     widen4(q.y, v + 4);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= s;
-    store8(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, a.cols - 8 * c, a.vec, v);
+    store8<kVec>(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, a.cols - 8 * c, v);
   }
 }
 
@@ -235,7 +261,6 @@ struct SplitArgs {
   int64_t rows, cols;
   uint16_t* out;
   int64_t ld;
-  int32_t vec;
   Chunks n;
 };
 
@@ -251,14 +276,14 @@ __device__ __forceinline__ uint32_t take16(float& v) {
   return b >> 16;
 }
 
-template <typename T>
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
   begin();
   for (Walk w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
     if (!w.at(a.n, row, c)) break;
     float v[8];
-    load8(static_cast<const T*>(a.x) + row * a.ldx + 8 * c, a.cols - 8 * c, a.vec, v);
+    load8<kVec>(static_cast<const T*>(a.x) + row * a.ldx + 8 * c, a.cols - 8 * c, v);
     uint16_t* out = a.out + row * a.ld + 8 * c;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -270,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
         *reinterpret_cast<uint4*>(out + t * a.rows * a.ld) = w;
       }
     } else {
-      store8(reinterpret_cast<T*>(out), 8, true, v);
+      store8<true>(reinterpret_cast<T*>(out), 8, v);
     }
   }
 }
@@ -284,7 +309,7 @@ struct KeepArgs {
   int64_t ld;
   uint16_t* units;
   int64_t ldu;
-  int32_t vec;
+  int32_t vec;  // rows start at multiples of 16 bytes
   int32_t tiles_t;
 };
 
@@ -301,30 +326,40 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const KeepArgs a) {
   __shared__ __align__(16) uint16_t units[4][128];
   const int64_t t0 = int64_t(blockIdx.x % a.tiles_t) * 128, k0 = int64_t(blockIdx.x / a.tiles_t) * 128;
   const int g = threadIdx.x % 16;  // group of eight channels
-  const T* x = static_cast<const T*>(a.x) + k0 + 8 * g;
-  const int64_t left = a.cols - k0 - 8 * g;
+  const T* x = static_cast<const T*>(a.x) + t0 * a.ldx + k0 + 8 * g;
+  const int left_t = int(min(a.rows - t0, int64_t(128))), left_k = int(min(a.cols - k0, int64_t(128))) - 8 * g;
+  auto turn = [&](auto full) {
 #pragma unroll 1
-  for (int m = threadIdx.x / 16; m < 32; m += kThreads / 16) {
-    float v[4][8];
+    for (int m = threadIdx.x / 16; m < 32; m += kThreads / 16) {
+      float v[4][8], q[4][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = t0 + 4 * m + i;
-      load8(x + t * a.ldx, t < a.rows ? left : 0, a.vec, v[i]);
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * m + i;
+        if constexpr (decltype(full)::value) {
+          load8<true>(x + t * a.ldx, 8, v[i]);
+        } else {
+          load8<false>(x + t * a.ldx, t < left_t ? left_k : 0, v[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float top = largest8(v[i]);
+        top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const Unit u = unit_of<kHalf>(top);
+        keep8(v[i], top, u.inverse, q[i]);
+        if (g % 4 == 0) units[g / 4][4 * m + i] = decltype(full)::value || 4 * m + i < left_t ? uint16_t(u.bits) : 0;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        codes[(8 * g + e) * 32 + (m ^ (2 * g))] =
+            pack4(__float_as_int(q[0][e]), __float_as_int(q[1][e]), __float_as_int(q[2][e]), __float_as_int(q[3][e]));
     }
-    float q[4][8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float top = largest8(v[i]);
-      top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      keep8(v[i], top, unit_inverse<kHalf>(top), q[i]);
-      if (g % 4 == 0) units[g / 4][4 * m + i] = t0 + 4 * m + i < a.rows ? uint16_t(unit_bits<kHalf>(top)) : 0;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      codes[(8 * g + e) * 32 + (m ^ (2 * g))] =
-          pack4(__float_as_int(q[0][e]), __float_as_int(q[1][e]), __float_as_int(q[2][e]), __float_as_int(q[3][e]));
-  }
+  };
+  if (a.vec && left_t == 128 && k0 + 128 <= a.cols)
+    turn(std::true_type());
+  else
+    turn(std::false_type());
   __syncthreads();
   // 16 tokens of a channel a thread; `ld` covers the tokens rounded up to 16.
   const int64_t end = (a.rows + 15) / 16 * 16;
@@ -353,11 +388,10 @@ struct RestoreArgs {
   int32_t half;
   void* out;
   int64_t ld_out;
-  int32_t vec;
   Chunks n;
 };
 
-template <typename T>
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) restore_tokens_kernel(const RestoreArgs a) {
   begin();
   for (Walk w(a.n); w.left > 0; w.next(a.n)) {
@@ -370,12 +404,12 @@ __global__ void __launch_bounds__(kThreads) restore_tokens_kernel(const RestoreA
     widen4(q.y, v + 4);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= u;
-    store8(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, a.cols - 8 * c, a.vec, v);
+    store8<kVec>(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, a.cols - 8 * c, v);
   }
 }
 
 // Tiles of 32 channels (a block) x 64 tokens: reads 16 tokens of a channel, writes 8 channels of a token.
-template <typename T>
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(128) restore_channels_kernel(const RestoreArgs a) {
   begin();
   __shared__ int8_t tile[32][68];
@@ -391,12 +425,12 @@ __global__ void __launch_bounds__(128) restore_channels_kernel(const RestoreArgs
     __syncthreads();
     for (int j = threadIdx.x; j < 256; j += 128) {
       const int t = j / 4, c = j % 4;
-      if (t0 + t < a.rows) {
+      if (t0 + t < a.rows && 32 * b + 8 * c < a.cols) {
         const float u = unit_value(a.units[b * a.ldu + t0 + t], a.half);
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = float(tile[8 * c + e][t]) * u;
-        store8(static_cast<T*>(a.out) + (t0 + t) * a.ld_out + 32 * b + 8 * c, a.cols - 32 * b - 8 * c, a.vec, v);
+        store8<kVec>(static_cast<T*>(a.out) + (t0 + t) * a.ld_out + 32 * b + 8 * c, a.cols - 32 * b - 8 * c, v);
       }
     }
     __syncthreads();
@@ -414,7 +448,6 @@ struct SwigluArgs {
   int64_t ldkg, ldku;
   uint16_t *ug, *uu;
   int64_t ldug, lduu;
-  int32_t vec;
   Chunks n;
 };
 
@@ -437,13 +470,14 @@ __device__ __forceinline__ void keep_block(const float (&v)[8], int8_t* codes, u
   float top = largest8(v), t[8];
   top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  keep8(v, top, unit_inverse<kHalf>(top), t);
+  const Unit of = unit_of<kHalf>(top);
+  keep8(v, top, of.inverse, t);
   if (write) *reinterpret_cast<uint2*>(codes) = pack8(t);
-  if (write && first) *unit = uint16_t(unit_bits<kHalf>(top));
+  if (write && first) *unit = uint16_t(of.bits);
 }
 
 // Four lanes to a block; a row's columns are rounded up to whole blocks so that a block's lanes stay together.
-template <typename T>
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
   begin();
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
@@ -452,12 +486,14 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
     int64_t row, c;
     const bool here = w.at(a.n, row, c);
     const int64_t left = here ? a.cols - 8 * c : 0;
-    float g[8], u[8], h[8];
-    load8(static_cast<const T*>(a.gate) + row * a.ldg + 8 * c, left, a.vec, g);
-    load8(static_cast<const T*>(a.up) + row * a.ldu + 8 * c, left, a.vec, u);
+    float g[8] = {}, u[8] = {}, h[8];
+    if (left > 0) {
+      load8<kVec>(static_cast<const T*>(a.gate) + row * a.ldg + 8 * c, left, g);
+      load8<kVec>(static_cast<const T*>(a.up) + row * a.ldu + 8 * c, left, u);
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = g[e] * sigmoid<T>(g[e]) * u[e];
-    if (left > 0) store8(static_cast<T*>(a.h) + row * a.ldh + 8 * c, left, a.vec, h);
+    if (left > 0) store8<kVec>(static_cast<T*>(a.h) + row * a.ldh + 8 * c, left, h);
     const bool write = here && 8 * c < (a.cols + 15) / 16 * 16;
     keep_block<kHalf>(g, a.kg + row * a.ldkg + 8 * c, a.ug + row * a.ldug + c / 4, c % 4 == 0, write);
     keep_block<kHalf>(u, a.ku + row * a.ldku + 8 * c, a.uu + row * a.lduu + c / 4, c % 4 == 0, write);
@@ -467,7 +503,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
   }
 }
 
-template <typename T>
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluArgs a, const T* dh, int64_t lddh, T* dgate,
                                                                    int64_t lddg, T* dup, int64_t lddu) {
   begin();
@@ -480,7 +516,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluA
     const uint2 wu = *reinterpret_cast<const uint2*>(a.ku + row * a.ldku + 8 * c);
     const float ug = unit_value(a.ug[row * a.ldug + c / 4], kHalf), uu = unit_value(a.uu[row * a.lduu + c / 4], kHalf);
     float d[8], g[8], u[8];
-    load8(dh + row * lddh + 8 * c, left, a.vec, d);
+    load8<kVec>(dh + row * lddh + 8 * c, left, d);
     widen4(wg.x, g), widen4(wg.y, g + 4);
     widen4(wu.x, u), widen4(wu.y, u + 4);
 #pragma unroll
@@ -489,18 +525,19 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluA
       g[e] = d[e] * (u[e] * uu) * s * (1.f + x * (1.f - s));
       u[e] = d[e] * (x * s);
     }
-    store8(dgate + row * lddg + 8 * c, left, a.vec, g);
-    store8(dup + row * lddu + 8 * c, left, a.vec, u);
+    store8<kVec>(dgate + row * lddg + 8 * c, left, g);
+    store8<kVec>(dup + row * lddu + 8 * c, left, u);
   }
 }
 
-// Rows of `row_chunks` chunks over blocks, eight on an SM at most.
+// Rows of `row_chunks` chunks over blocks, 48 to an SM at most: with 8, which start and end together, the gated
+// activation of 8192 x 8192 bfloat16 takes 132 us instead of 113, and 101 instead of 89 back.
 Chunks chunks_of(int64_t rows, int64_t row_chunks, int sms) {
   Chunks n{};
   n.all = rows * row_chunks;
   n.row_chunks = row_chunks;
   n.div = divider(uint32_t(row_chunks));
-  const int64_t steps = (n.all + kThreads - 1) / kThreads, blocks = std::min(steps, int64_t(sms) * 8);
+  const int64_t steps = (n.all + kThreads - 1) / kThreads, blocks = std::min(steps, int64_t(sms) * 48);
   n.per_block = (steps + blocks - 1) / blocks * kThreads;
   return n;
 }
@@ -510,25 +547,25 @@ int64_t bytes_of(int dtype) { return dtype == INT8_F32 ? 4 : 2; }
 }  // namespace
 
 cudaError_t launch_int8_quantize(int dtype, const void* x, int64_t ldx, const int8_matrix_t& q, cudaStream_t stream) {
-  const RowArgs a{x, ldx, q.rows, q.cols, q.codes, q.ld, q.scales, aligned16(x, ldx * bytes_of(dtype))};
-  return launch_rows<kBytes>(dtype, a, stream);
+  const RowArgs a{x, ldx, q.rows, q.cols, q.codes, q.ld, q.scales};
+  return launch_rows<kBytes>(dtype, a, whole(q.cols, aligned16(x, ldx * bytes_of(dtype))), stream);
 }
 
 cudaError_t launch_int8_rows16(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
                                int64_t ld, float* scales, cudaStream_t stream) {
-  const RowArgs a{x, ldx, rows, cols, out, ld, scales, aligned16(x, ldx * bytes_of(dtype))};
-  return launch_rows<kWide>(dtype, a, stream);
+  const RowArgs a{x, ldx, rows, cols, out, ld, scales};
+  return launch_rows<kWide>(dtype, a, whole(cols, aligned16(x, ldx * bytes_of(dtype))), stream);
 }
 
 cudaError_t launch_int8_dequantize(const int8_matrix_t& q, int dtype, void* y, int64_t ldy, int sms,
                                    cudaStream_t stream) {
-  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, y, ldy, aligned16(y, ldy * bytes_of(dtype)),
-                   chunks_of(q.rows, (q.cols + 7) / 8, sms)};
-  GB300_INT8_BY_TYPE(dtype, launch(dequantize_kernel<T>, blocks_of(a.n), kThreads, stream, a))
+  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, y, ldy, chunks_of(q.rows, (q.cols + 7) / 8, sms)};
+  const bool vec = whole(q.cols, aligned16(y, ldy * bytes_of(dtype)));
+  GB300_INT8_BY_TYPE(dtype, launch(vec ? dequantize_kernel<T, true> : dequantize_kernel<T, false>, blocks_of(a.n), kThreads, stream, a))
 }
 
 cudaError_t launch_int8_widen(const int8_matrix_t& q, uint16_t* out, int64_t ld, int sms, cudaStream_t stream) {
-  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, out, ld, 1, chunks_of(q.rows, (q.cols + 7) / 8, sms)};
+  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, out, ld, chunks_of(q.rows, (q.cols + 7) / 8, sms)};
   return launch(widen_kernel, blocks_of(a.n), kThreads, stream, a);
 }
 
@@ -536,8 +573,9 @@ int int8_terms(int dtype) { return dtype == INT8_F32 ? 3 : 1; }
 
 cudaError_t launch_int8_split(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
                               int64_t ld, int sms, cudaStream_t stream) {
-  const SplitArgs a{x, ldx, rows, cols, out, ld, aligned16(x, ldx * bytes_of(dtype)), chunks_of(rows, (cols + 7) / 8, sms)};
-  GB300_INT8_BY_TYPE(dtype, launch(split_kernel<T>, blocks_of(a.n), kThreads, stream, a))
+  const SplitArgs a{x, ldx, rows, cols, out, ld, chunks_of(rows, (cols + 7) / 8, sms)};
+  const bool vec = whole(cols, aligned16(x, ldx * bytes_of(dtype)));
+  GB300_INT8_BY_TYPE(dtype, launch(vec ? split_kernel<T, true> : split_kernel<T, false>, blocks_of(a.n), kThreads, stream, a))
 }
 
 cudaError_t launch_int8_keep(const void* x, int64_t ldx, const int8_checkpoint_t& c, cudaStream_t stream) {
@@ -550,12 +588,13 @@ cudaError_t launch_int8_keep(const void* x, int64_t ldx, const int8_checkpoint_t
 cudaError_t launch_int8_restore(const int8_checkpoint_t& c, int dtype, void* y, int64_t ldy, int sms,
                                 cudaStream_t stream) {
   const RestoreArgs a{c.codes, c.ld, c.units, c.ld_units, c.rows, c.cols, c.dtype == INT8_F16, y, ldy,
-                      aligned16(y, ldy * bytes_of(dtype)), chunks_of(c.rows, (c.cols + 7) / 8, sms)};
+                      chunks_of(c.rows, (c.cols + 7) / 8, sms)};
+  const bool vec = whole(c.cols, aligned16(y, ldy * bytes_of(dtype)));
   if (c.order == INT8_TOKENS) {
-    GB300_INT8_BY_TYPE(dtype, launch(restore_tokens_kernel<T>, blocks_of(a.n), kThreads, stream, a))
+    GB300_INT8_BY_TYPE(dtype, launch(vec ? restore_tokens_kernel<T, true> : restore_tokens_kernel<T, false>, blocks_of(a.n), kThreads, stream, a))
   }
   const int64_t tiles = std::min((c.rows + 63) / 64 * ((c.cols + 31) / 32), int64_t(sms) * 16);
-  GB300_INT8_BY_TYPE(dtype, launch(restore_channels_kernel<T>, tiles, 128, stream, a))
+  GB300_INT8_BY_TYPE(dtype, launch(vec ? restore_channels_kernel<T, true> : restore_channels_kernel<T, false>, tiles, 128, stream, a))
 }
 
 cudaError_t launch_int8_swiglu(int dtype, int64_t M, int64_t F, const void* gate, int64_t ldg, const void* up,
@@ -563,10 +602,9 @@ cudaError_t launch_int8_swiglu(int dtype, int64_t M, int64_t F, const void* gate
                                const int8_checkpoint_t& ku, int sms, cudaStream_t stream) {
   const int64_t es = bytes_of(dtype);
   const SwigluArgs a{gate, up, ldg, ldu, M, F, h, ldh, kg.codes, ku.codes, kg.ld, ku.ld, kg.units, ku.units,
-                     kg.ld_units, ku.ld_units,
-                     aligned16(gate, ldg * es) && aligned16(up, ldu * es) && aligned16(h, ldh * es),
-                     chunks_of(M, (F + 31) / 32 * 4, sms)};
-  GB300_INT8_BY_TYPE(dtype, launch(swiglu_kernel<T>, blocks_of(a.n), kThreads, stream, a))
+                     kg.ld_units, ku.ld_units, chunks_of(M, (F + 31) / 32 * 4, sms)};
+  const bool vec = whole(F, aligned16(gate, ldg * es) && aligned16(up, ldu * es) && aligned16(h, ldh * es));
+  GB300_INT8_BY_TYPE(dtype, launch(vec ? swiglu_kernel<T, true> : swiglu_kernel<T, false>, blocks_of(a.n), kThreads, stream, a))
 }
 
 cudaError_t launch_int8_swiglu_backward(const void* dh, int64_t lddh, const int8_checkpoint_t& kg,
@@ -578,10 +616,10 @@ cudaError_t launch_int8_swiglu_backward(const void* dh, int64_t lddh, const int8
   a.cols = kg.cols;
   a.kg = kg.codes, a.ku = ku.codes, a.ldkg = kg.ld, a.ldku = ku.ld;
   a.ug = kg.units, a.uu = ku.units, a.ldug = kg.ld_units, a.lduu = ku.ld_units;
-  a.vec = aligned16(dh, lddh * es) && aligned16(dgate, ldg * es) && aligned16(dup, ldu * es);
+  const bool vec = whole(kg.cols, aligned16(dh, lddh * es) && aligned16(dgate, ldg * es) && aligned16(dup, ldu * es));
   a.n = chunks_of(kg.rows, (kg.cols + 7) / 8, sms);
   GB300_INT8_BY_TYPE(kg.dtype,
-                     launch(swiglu_backward_kernel<T>, blocks_of(a.n), kThreads, stream, a, static_cast<const T*>(dh), lddh,
+                     launch(vec ? swiglu_backward_kernel<T, true> : swiglu_backward_kernel<T, false>, blocks_of(a.n), kThreads, stream, a, static_cast<const T*>(dh), lddh,
                             static_cast<T*>(dgate), ldg, static_cast<T*>(dup), ldu))
 }
 

@@ -19,38 +19,37 @@ using fp4::to_f32;
 
 constexpr int kBlock = 32;  // channels that share a checkpoint's unit
 
-// Eight consecutive values from p on in 32 bits, of which `left` exist (the others are 0); `vec`: p is 16-byte aligned.
+// Eight consecutive values as they are in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int64_t left, bool vec, float (&v)[8]) {
-  if (vec && left >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 w = *reinterpret_cast<const uint4*>(p);
-      const T* t = reinterpret_cast<const T*>(&w);
+struct alignas(16) Eight {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void values(const Eight<T>& x, float (&v)[8]) {
+  const T* t = reinterpret_cast<const T*>(&x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
-    }
+  for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
+}
+
+// Eight consecutive values from p on in 32 bits, of which `left` exist (the others are 0).  kVec: p is 16-byte aligned and all exist.
+template <bool kVec, typename T>
+__device__ __forceinline__ void load8(const T* p, int64_t left, float (&v)[8]) {
+  if constexpr (kVec) {
+    values(*reinterpret_cast<const Eight<T>*>(p), v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(p[i]) : 0.f;
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int64_t left, bool vec, const float (&v)[8]) {
-  if (vec && left >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint4 w;
-      T* t = reinterpret_cast<T*>(&w);
+template <bool kVec, typename T>
+__device__ __forceinline__ void store8(T* p, int64_t left, const float (&v)[8]) {
+  if constexpr (kVec) {
+    Eight<T> x;
+    T* t = reinterpret_cast<T*>(&x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = from_f32<T>(v[i]);
-      *reinterpret_cast<uint4*>(p) = w;
-    }
+    for (int i = 0; i < 8; ++i) t[i] = from_f32<T>(v[i]);
+    *reinterpret_cast<Eight<T>*>(p) = x;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -85,25 +84,22 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
   return __byte_perm(__byte_perm(uint32_t(a), uint32_t(b), 0x0040), __byte_perm(uint32_t(c), uint32_t(d), 0x0040), 0x5410);
 }
 
-// Exponent of a block's unit from its largest magnitude (finite).
+// A block's unit from its largest magnitude.
+struct Unit {
+  uint32_t bits;  // bfloat16, or a 16-bit float (exponents -24 to 9: subnormal below -14)
+  float inverse;  // what values are multiplied by before they are rounded (exact): 0 where the block is not finite
+};
 template <bool kHalf>
-__device__ __forceinline__ int unit_exponent(float a) {
-  return max(int(__float_as_uint(a) >> 23) - 127 - 6, kHalf ? -24 : -126);  // the field of a subnormal clamps too
-}
-// The unit's 16 bits: bfloat16, or a 16-bit float (-24 to 9: subnormal below -14).
-template <bool kHalf>
-__device__ __forceinline__ uint32_t unit_bits(float a) {
-  if (!finite(a)) return kHalf ? 0x7e00u : 0x7fc0u;
-  const int e = unit_exponent<kHalf>(a);
-  return kHalf ? (e >= -14 ? uint32_t(e + 15) << 10 : 1u << (e + 24)) : uint32_t(e + 127) << 7;
+__device__ __forceinline__ Unit unit_of(float a) {
+  const int e = max(int(__float_as_uint(a) >> 23) - 127 - 6, kHalf ? -24 : -126);  // the field of a subnormal clamps too
+  Unit u;
+  u.bits = kHalf ? (e >= -14 ? uint32_t(e + 15) << 10 : 1u << (e + 24)) : uint32_t(e + 127) << 7;
+  u.inverse = __uint_as_float(uint32_t(127 - e) << 23);
+  if (!finite(a)) u.bits = kHalf ? 0x7e00u : 0x7fc0u, u.inverse = 0.f;
+  return u;
 }
 __device__ __forceinline__ float unit_value(uint32_t bits, bool half) {
   return half ? __half2float(__ushort_as_half(uint16_t(bits))) : __uint_as_float(bits << 16);
-}
-// What a block's values are multiplied by before they are rounded: 1 / u (exact; 0 where the block is not finite).
-template <bool kHalf>
-__device__ __forceinline__ float unit_inverse(float a) {
-  return finite(a) ? __uint_as_float(uint32_t(127 - unit_exponent<kHalf>(a)) << 23) : 0.f;
 }
 
 // 3 * 2^22: a number up to 2^22 in magnitude that is added to it is rounded to the nearest integer, ties to

@@ -35,7 +35,10 @@ __device__ __forceinline__ void values(const Eight<T>& x, float (&v)[8]) {
 template <bool kVec, typename T>
 __device__ __forceinline__ void load8(const T* p, int64_t left, float (&v)[8]) {
   if constexpr (kVec) {
-    values(*reinterpret_cast<const Eight<T>*>(p), v);
+    Eight<T> x;  // (read as vectors: values() of the memory itself would read one element at a time)
+#pragma unroll
+    for (uint32_t i = 0; i < sizeof(T) / 2; ++i) x.w[i] = reinterpret_cast<const uint4*>(p)[i];
+    values(x, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(p[i]) : 0.f;
@@ -49,7 +52,8 @@ __device__ __forceinline__ void store8(T* p, int64_t left, const float (&v)[8]) 
     T* t = reinterpret_cast<T*>(&x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = from_f32<T>(v[i]);
-    *reinterpret_cast<Eight<T>*>(p) = x;
+#pragma unroll
+    for (uint32_t i = 0; i < sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = x.w[i];
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

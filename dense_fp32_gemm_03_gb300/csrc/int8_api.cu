@@ -194,6 +194,23 @@ sgemm_status_t run_product(gb300::Int8TcShape shape, const Operands& o, gb300::I
 // C (M x N, row stride ldc) = A B^T, from A's rows as 16-bit floats or, with x, quantised on the way.
 sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* x, int64_t ldx, int64_t M, const int8_matrix_t& B,
                                int dtype, void* C, int64_t ldc, const LibDevice& d, cudaStream_t stream) {
+  if (M <= gb300::int8_few_tokens()) {
+    Scratch s;
+    const size_t scales_at = s.take(M * 4), image_at = s.take(round_up(M, 8) * round_up(B.cols, 64));
+    void* ws = nullptr;
+    const sgemm_status_t st = gb300::lib_workspace(d.dev, stream, s.bytes, &ws);
+    if (st != SGEMM_OK) return st;
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    int8_t* image = reinterpret_cast<int8_t*>(base + image_at);
+    float* scales = reinterpret_cast<float*>(base + scales_at);
+    const cudaError_t e = A ? gb300::launch_int8_image(*A, image, stream)
+                            : gb300::launch_int8_quantize_image(dtype_x, x, ldx, M, B.cols, image, scales, stream);
+    if (e != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    return status_of(gb300::launch_int8_few(
+        gb300::Int8FewArgs{B.codes, B.ld, B.scales, image, A ? A->scales : scales, C, ldc, int32_t(B.rows), int32_t(B.cols),
+                           int32_t(M), dtype},
+        stream));
+  }
   const gb300::Int8TcShape shape = M <= 32 ? gb300::kInt8Whole32 : M <= 64 ? gb300::kInt8Whole64 : gb300::kInt8Whole128;
   const int pairs = tc_pairs(d.dev);
   gb300::Int8TcArgs a{};

@@ -150,6 +150,30 @@ __device__ __forceinline__ void widen4(uint32_t word, float* v) {
   for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7540 + e)) - 8388736.f;
 }
 
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Two of a word's four integers as 16-bit floats: in the low bits of 1024 + 128 + q, of which
+// 1024 + 128 is taken off.  `biased`: the word with each byte's top bit flipped (q + 128).
+template <int kPair>
+__device__ __forceinline__ uint32_t to_f16(uint32_t biased) {
+  return hsub2(__byte_perm(biased, 0x64646464u, kPair ? 0x4342 : 0x4140), 0x64806480u);
+}
+// A sum of integers times its scales, the smaller first (NaN stays).
+__device__ __forceinline__ float scaled(int sum, float s, float t) {
+  const bool first = fabsf(s) <= fabsf(t);
+  return float(sum) * (first ? s : t) * (first ? t : s);
+}
+
+// Where eight integers (columns 8 c on) of a token are in the order in which the few-token product reads them: for every
+// eight tokens and 64 columns, 16 bytes a lane, lane = 4 (token % 8) + column / 16 % 4.
+__host__ __device__ __forceinline__ int64_t image_at(int64_t token, int c, int cols) {
+  const int64_t steps = (cols + 63) / 64;
+  return (((token >> 3) * steps + (c >> 3)) * 32 + (token & 7) * 4 + (c & 7) / 2) * 16 + (c & 1) * 8;
+}
+
 // n / d for 0 <= n < 2^31, with m = floor(2^(31 + s) / d) + 1 and 2^s >= d: n m / 2^(31 + s) is above n / d by
 // less than 1 / d.
 struct Divider {

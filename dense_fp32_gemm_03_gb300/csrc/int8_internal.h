@@ -19,6 +19,10 @@ cudaError_t launch_int8_rows16(int dtype, const void* x, int64_t ldx, int64_t ro
                                int64_t ld, float* scales, cudaStream_t stream);
 // ... or from integers.
 cudaError_t launch_int8_widen(const int8_matrix_t& q, uint16_t* out, int64_t ld, int sms, cudaStream_t stream);
+// The same for the few-token product: (rows rounded up to 8) x (cols rounded up to 64) bytes.
+cudaError_t launch_int8_quantize_image(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* out,
+                                       float* scales, cudaStream_t stream);
+cudaError_t launch_int8_image(const int8_matrix_t& q, int8_t* out, cudaStream_t stream);
 // x (rows x cols, 16-bit or 32-bit) as `terms` matrices of 16 bits one after the other, `ld` elements (a multiple of 8,
 // zeros behind cols) a row: 16-bit types as they are (1 term), 32 bits as three bfloat16 whose sum they are.
 int int8_terms(int dtype);
@@ -62,5 +66,21 @@ struct Int8TcArgs {
 // before on the stream, and waits for it by itself.
 cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], const Int8TcArgs& args, int pairs, int sms,
                            cudaStream_t stream);
+
+// ---- the same for few tokens (int8_few.cu): y = X W^T, from X in the order above.
+int int8_few_tokens();  // the most
+struct Int8FewArgs {
+  const int8_t* w;
+  int64_t ldw;
+  const float* scale_w;
+  const int8_t* x;
+  const float* scale_x;
+  void* y;
+  int64_t ldy;
+  int32_t n, k, tokens;
+  int32_t dtype;
+};
+// Has to follow one of the two launches that write x: it reads w before that one ends.
+cudaError_t launch_int8_few(const Int8FewArgs& args, cudaStream_t stream);
 
 }  // namespace gb300

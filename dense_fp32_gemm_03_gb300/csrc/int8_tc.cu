@@ -131,23 +131,12 @@ __device__ __forceinline__ void write_tmem32(uint32_t taddr, const uint32_t (&r)
       : "memory");
 }
 
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-// Two of a word's four integers as 16-bit floats: in the low bits of 1024 + 128 + q, of which
-// 1024 + 128 is taken off.  `biased`: the word with each byte's top bit flipped (q + 128).
-template <int kPair>
-__device__ __forceinline__ uint32_t to_f16(uint32_t biased) {
-  return hsub2(__byte_perm(biased, 0x64646464u, kPair ? 0x4342 : 0x4140), 0x64806480u);
-}
 // The same in bfloat16, whose 128 + (low seven bits) has 128 taken off where q >= 0 and 256 where
 // q < 0: that number is 0x4300 and q's top bit.
 template <int kPair>
@@ -193,12 +182,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   v.x = from_f32<decltype(v.x)>(a);
   v.y = from_f32<decltype(v.y)>(b);
   return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// A sum of integers times its scales, the smaller first (NaN stays).
-__device__ __forceinline__ float scaled(int sum, float s, float t) {
-  const bool first = fabsf(s) <= fabsf(t);
-  return float(sum) * (first ? s : t) * (first ? t : s);
 }
 
 // Stores kCount columns of a row of D (`out`: the first; `left`: those that exist), added to what is there if asked.

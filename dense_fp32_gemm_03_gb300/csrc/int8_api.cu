@@ -196,18 +196,18 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
                                int dtype, void* C, int64_t ldc, const LibDevice& d, cudaStream_t stream) {
   if (M <= gb300::int8_few_tokens()) {
     Scratch s;
-    const size_t scales_at = s.take(M * 4), image_at = s.take(round_up(M, 8) * round_up(B.cols, 64));
+    const size_t scales_at = s.take(M * 4), tokens_at = s.take(16 * round_up(B.cols, 64));
     void* ws = nullptr;
     const sgemm_status_t st = gb300::lib_workspace(d.dev, stream, s.bytes, &ws);
     if (st != SGEMM_OK) return st;
     uint8_t* base = static_cast<uint8_t*>(ws);
-    int8_t* image = reinterpret_cast<int8_t*>(base + image_at);
+    uint16_t* tokens = reinterpret_cast<uint16_t*>(base + tokens_at);
     float* scales = reinterpret_cast<float*>(base + scales_at);
-    const cudaError_t e = A ? gb300::launch_int8_image(*A, image, stream)
-                            : gb300::launch_int8_quantize_image(dtype_x, x, ldx, M, B.cols, image, scales, stream);
+    const cudaError_t e = A ? gb300::launch_int8_widen_few(*A, tokens, stream)
+                            : gb300::launch_int8_quantize_few(dtype_x, x, ldx, M, B.cols, tokens, scales, stream);
     if (e != cudaSuccess) return SGEMM_ERR_LAUNCH;
     return status_of(gb300::launch_int8_few(
-        gb300::Int8FewArgs{B.codes, B.ld, B.scales, image, A ? A->scales : scales, C, ldc, int32_t(B.rows), int32_t(B.cols),
+        gb300::Int8FewArgs{B.codes, B.ld, B.scales, tokens, A ? A->scales : scales, C, ldc, int32_t(B.rows), int32_t(B.cols),
                            int32_t(M), dtype},
         stream));
   }
@@ -233,6 +233,7 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
   a.dtype = dtype;
   a.out = C;
   a.ld = ldc;
+  a.early = 1;
   a.partials = reinterpret_cast<uint32_t*>(base + partials_at);
   return run_product(shape, Operands{B.codes, B.ld, nullptr, 0, rows16, ld16, 1}, a, pairs, d, stream);
 }
@@ -374,6 +375,7 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
     o.b = terms_out;
     if (gb300::launch_int8_split(c->dtype, dy, lddy, c->rows, N, terms_out, o.ldb, d.sms, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
   }
+  a.early = !in_place;
   a.dtype = dtype;
   a.accumulate = accumulate != 0;
   a.out = dw;

@@ -60,13 +60,12 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t
   }
 
 // ------------------------------------------------------------------------- rows
-enum RowForm { kBytes, kWide, kImage };  // integers as bytes, as 16-bit floats, or as bytes in the few-token product's order
+enum RowForm { kBytes, kWide, kFew };  // integers as bytes, as 16-bit floats, or as those in the few-token product's order
 
 struct RowArgs {
   const void* x;
   int64_t ldx;
   int64_t rows, cols;
-  int64_t out_rows;  // the image's tokens come in eights
   void* out;
   int64_t ld;  // of out, in its elements
   float* scales;
@@ -80,8 +79,8 @@ __global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(
   constexpr int kRows = kGroup <= 32 ? kThreads / kGroup : 1, kKept = 4;
   const int t = threadIdx.x % kGroup;
   const int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / kGroup;
-  if (kGroup <= 32 && row >= a.out_rows) return;  // whole warps
-  const T* x = static_cast<const T*>(a.x) + (kForm == kImage ? min(row, a.rows - 1) : row) * a.ldx;
+  if (kGroup <= 32 && row >= a.rows) return;  // whole warps
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const int cols = int(a.cols), chunks = (cols + 7) / 8;
   Eight<T> kept[kKept];
   float top = 0.f;
@@ -122,21 +121,22 @@ __global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(
     for (int d = kGroup / 64; d; d /= 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, d));
   }
   const float s = row_scale(top), inv = __frcp_rn(s);
-  if (t == 0 && row < a.rows) a.scales[row] = s;
+  if (t == 0) a.scales[row] = s;
   const int out_chunks = kForm == kBytes ? (cols + 15) / 16 * 2 : kForm == kWide ? chunks : (cols + 63) / 64 * 8;
   auto write = [&](int c, const float (&w)[8]) {
     float n[8];
     nearest8(w, s, inv, n);
     if constexpr (kForm == kBytes) {
       *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.out) + row * a.ld + 8 * c) = pack8(n);
-    } else if constexpr (kForm == kImage) {
-      *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.out) + image_at(row, c, cols)) = row < a.rows ? pack8(n) : make_uint2(0, 0);
     } else {
       uint4 h;
       __half2* p = reinterpret_cast<__half2*>(&h);
 #pragma unroll
       for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(n[2 * e] - kRound, n[2 * e + 1] - kRound);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.ld + 8 * c) = h;
+      if constexpr (kForm == kWide)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.ld + 8 * c) = h;
+      else
+        static_cast<uint4*>(a.out)[few_at(int(row), c)] = h;
     }
   };
 #pragma unroll
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(
 #pragma unroll 1
   for (int c = t + kKept * kGroup; c < out_chunks; c += kGroup) {
     float v[8];
-    if (kVec && c >= chunks) {  // the chunk of zeros that fills 16 bytes
+    if (kVec && c >= chunks) {  // zeros that fill up
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = 0.f;
     } else {
@@ -167,10 +167,10 @@ bool whole(int64_t cols, bool aligned) { return aligned && cols % 8 == 0; }
 // As few threads to a row as keep all of it.
 template <typename T, RowForm kForm, bool kVec>
 cudaError_t launch_rows_of(const RowArgs& a, cudaStream_t stream) {
-  if (a.cols <= 1024) return launch(rows_kernel<T, 32, kForm, kVec>, (a.out_rows + kThreads / 32 - 1) / (kThreads / 32), kThreads, stream, a);
-  if (a.cols <= 4096) return launch(rows_kernel<T, 128, kForm, kVec>, a.out_rows, 128, stream, a);
-  if (a.cols <= 8192) return launch(rows_kernel<T, 256, kForm, kVec>, a.out_rows, 256, stream, a);
-  return launch(rows_kernel<T, 1024, kForm, kVec>, a.out_rows, 1024, stream, a);
+  if (a.cols <= 1024) return launch(rows_kernel<T, 32, kForm, kVec>, (a.rows + kThreads / 32 - 1) / (kThreads / 32), kThreads, stream, a);
+  if (a.cols <= 4096) return launch(rows_kernel<T, 128, kForm, kVec>, a.rows, 128, stream, a);
+  if (a.cols <= 8192) return launch(rows_kernel<T, 256, kForm, kVec>, a.rows, 256, stream, a);
+  return launch(rows_kernel<T, 1024, kForm, kVec>, a.rows, 1024, stream, a);
 }
 template <RowForm kForm>
 cudaError_t launch_rows(int dtype, const RowArgs& a, bool vec, cudaStream_t stream) {
@@ -257,20 +257,22 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const BackArgs a) {
   }
 }
 
-// Rows of integers in the few-token product's order.
-__global__ void __launch_bounds__(kThreads) image_kernel(const BackArgs a) {
+// A row of integers in the few-token product's order.
+__global__ void __launch_bounds__(kThreads) widen_few_kernel(const BackArgs a) {
   begin();
-  const int cols = int(a.cols), chunks = (cols + 63) / 64 * 8;
-  const int64_t row = blockIdx.x;
-  for (int c = threadIdx.x; c < chunks; c += kThreads) {
-    uint2 w = make_uint2(0, 0);
-    if (row < a.rows && 8 * c < cols) w = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
-    const int left = cols - 8 * c;  // codes behind the row's end may be anything
-    if (left < 8) {
-      w.x = left >= 4 ? w.x : left <= 0 ? 0u : w.x & (0xffffffffu >> (32 - 8 * left));
-      w.y = left <= 4 ? 0u : w.y & (0xffffffffu >> (64 - 8 * left));
+  const int cols = int(a.cols), row = blockIdx.x;
+  for (int c = threadIdx.x; c < (cols + 63) / 64 * 8; c += kThreads) {
+    float v[8] = {};
+    if (8 * c < cols) {
+      const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
+      widen4(q.x, v);
+      widen4(q.y, v + 4);
     }
-    *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.out) + image_at(row, c, cols)) = w;
+    uint4 h;
+    __half2* p = reinterpret_cast<__half2*>(&h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(8 * c + 2 * e < cols ? v[2 * e] : 0.f, 8 * c + 2 * e + 1 < cols ? v[2 * e + 1] : 0.f);
+    static_cast<uint4*>(a.out)[few_at(row, c)] = h;
   }
 }
 
@@ -568,25 +570,25 @@ int64_t bytes_of(int dtype) { return dtype == INT8_F32 ? 4 : 2; }
 }  // namespace
 
 cudaError_t launch_int8_quantize(int dtype, const void* x, int64_t ldx, const int8_matrix_t& q, cudaStream_t stream) {
-  const RowArgs a{x, ldx, q.rows, q.cols, q.rows, q.codes, q.ld, q.scales};
+  const RowArgs a{x, ldx, q.rows, q.cols, q.codes, q.ld, q.scales};
   return launch_rows<kBytes>(dtype, a, whole(q.cols, aligned16(x, ldx * bytes_of(dtype))), stream);
 }
 
 cudaError_t launch_int8_rows16(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
                                int64_t ld, float* scales, cudaStream_t stream) {
-  const RowArgs a{x, ldx, rows, cols, rows, out, ld, scales};
+  const RowArgs a{x, ldx, rows, cols, out, ld, scales};
   return launch_rows<kWide>(dtype, a, whole(cols, aligned16(x, ldx * bytes_of(dtype))), stream);
 }
 
-cudaError_t launch_int8_quantize_image(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* out,
-                                       float* scales, cudaStream_t stream) {
-  const RowArgs a{x, ldx, rows, cols, (rows + 7) / 8 * 8, out, 0, scales};
-  return launch_rows<kImage>(dtype, a, whole(cols, aligned16(x, ldx * bytes_of(dtype))), stream);
+cudaError_t launch_int8_quantize_few(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
+                                     float* scales, cudaStream_t stream) {
+  const RowArgs a{x, ldx, rows, cols, out, 0, scales};
+  return launch_rows<kFew>(dtype, a, whole(cols, aligned16(x, ldx * bytes_of(dtype))), stream);
 }
 
-cudaError_t launch_int8_image(const int8_matrix_t& q, int8_t* out, cudaStream_t stream) {
+cudaError_t launch_int8_widen_few(const int8_matrix_t& q, uint16_t* out, cudaStream_t stream) {
   const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, out, 0, Chunks{}};
-  return launch(image_kernel, (q.rows + 7) / 8 * 8, kThreads, stream, a);
+  return launch(widen_few_kernel, q.rows, kThreads, stream, a);
 }
 
 cudaError_t launch_int8_dequantize(const int8_matrix_t& q, int dtype, void* y, int64_t ldy, int sms,

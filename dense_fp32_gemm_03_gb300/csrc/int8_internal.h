@@ -19,10 +19,10 @@ cudaError_t launch_int8_rows16(int dtype, const void* x, int64_t ldx, int64_t ro
                                int64_t ld, float* scales, cudaStream_t stream);
 // ... or from integers.
 cudaError_t launch_int8_widen(const int8_matrix_t& q, uint16_t* out, int64_t ld, int sms, cudaStream_t stream);
-// The same for the few-token product: (rows rounded up to 8) x (cols rounded up to 64) bytes.
-cudaError_t launch_int8_quantize_image(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* out,
-                                       float* scales, cudaStream_t stream);
-cudaError_t launch_int8_image(const int8_matrix_t& q, int8_t* out, cudaStream_t stream);
+// The same for the few-token product, up to eight rows: 16 bytes for each (cols rounded up to 64).
+cudaError_t launch_int8_quantize_few(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
+                                     float* scales, cudaStream_t stream);
+cudaError_t launch_int8_widen_few(const int8_matrix_t& q, uint16_t* out, cudaStream_t stream);
 // x (rows x cols, 16-bit or 32-bit) as `terms` matrices of 16 bits one after the other, `ld` elements (a multiple of 8,
 // zeros behind cols) a row: 16-bit types as they are (1 term), 32 bits as three bfloat16 whose sum they are.
 int int8_terms(int dtype);
@@ -57,6 +57,7 @@ struct Int8TcArgs {
   int32_t accumulate;        // out += D
   void* out;
   int64_t ld;
+  int32_t early;             // the launch before prepared b (one of those above): `a` is read before it ends
   uint32_t* partials;        // splits x cols x rows 32-bit sums, if splits > 1
   uint32_t* status;
   uint64_t wait_limit_ns;
@@ -67,18 +68,18 @@ struct Int8TcArgs {
 cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], const Int8TcArgs& args, int pairs, int sms,
                            cudaStream_t stream);
 
-// ---- the same for few tokens (int8_few.cu): y = X W^T, from X in the order above.
+// ---- the same for few tokens (int8_few.cu): y = X W^T
 int int8_few_tokens();  // the most
 struct Int8FewArgs {
   const int8_t* w;
   int64_t ldw;
   const float* scale_w;
-  const int8_t* x;
+  const void* x;         // the tokens as the launches above order them, and their scales
   const float* scale_x;
   void* y;
   int64_t ldy;
   int32_t n, k, tokens;
-  int32_t dtype;
+  int32_t dtype;         // of y
 };
 // Has to follow one of the two launches that write x: it reads w before that one ends.
 cudaError_t launch_int8_few(const Int8FewArgs& args, cudaStream_t stream);

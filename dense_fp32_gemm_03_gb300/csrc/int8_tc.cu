@@ -267,7 +267,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
   cluster_sync();  // the peer's barriers exist before anything signals them
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   constexpr uint32_t tmem = fp4::kTmemBase, slots = tmem + S::kAccs * S::kN;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Whoever reads what the kernel before wrote waits for it, which is everybody unless that kernel only
+  // prepared b and itself waited for the ones before: `a` can be read beside it then.
+  const bool early = args.early && (warp == 0 || (warp >= 4 && warp < 4 + 4 * kGroups));
+  if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   auto fail = [&]() {
     if (!*s_abort) {

@@ -195,6 +195,22 @@ sgemm_status_t run_product(gb300::Int8TcShape shape, const Operands& o, gb300::I
 sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* x, int64_t ldx, int64_t M, const int8_matrix_t& B,
                                int dtype, void* C, int64_t ldc, const LibDevice& d, cudaStream_t stream) {
   if (M <= gb300::int8_few_tokens()) {
+    gb300::Int8FewArgs f{};
+    f.w = B.codes;
+    f.ldw = B.ld;
+    f.scale_w = B.scales;
+    f.y = C;
+    f.ldy = ldc;
+    f.n = int32_t(B.rows);
+    f.k = int32_t(B.cols);
+    f.tokens = int32_t(M);
+    f.dtype = dtype;
+    if (!A && gb300::int8_few_quantises(M, B.cols)) {
+      f.x = x;
+      f.ldx = ldx;
+      f.vec = aligned(x, 16) && (M == 1 || ldx * dtype_bytes(dtype_x) % 16 == 0);
+      return status_of(gb300::launch_int8_few(dtype_x, f, stream));
+    }
     Scratch s;
     const size_t scales_at = s.take(M * 4), tokens_at = s.take(16 * round_up(B.cols, 64));
     void* ws = nullptr;
@@ -206,10 +222,9 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
     const cudaError_t e = A ? gb300::launch_int8_widen_few(*A, tokens, stream)
                             : gb300::launch_int8_quantize_few(dtype_x, x, ldx, M, B.cols, tokens, scales, stream);
     if (e != cudaSuccess) return SGEMM_ERR_LAUNCH;
-    return status_of(gb300::launch_int8_few(
-        gb300::Int8FewArgs{B.codes, B.ld, B.scales, tokens, A ? A->scales : scales, C, ldc, int32_t(B.rows), int32_t(B.cols),
-                           int32_t(M), dtype},
-        stream));
+    f.x = tokens;
+    f.scale_x = A ? A->scales : scales;
+    return status_of(gb300::launch_int8_few(-1, f, stream));
   }
   const gb300::Int8TcShape shape = M <= 32 ? gb300::kInt8Whole32 : M <= 64 ? gb300::kInt8Whole64 : gb300::kInt8Whole128;
   const int pairs = tc_pairs(d.dev);

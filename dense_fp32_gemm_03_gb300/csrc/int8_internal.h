@@ -74,14 +74,17 @@ struct Int8FewArgs {
   const int8_t* w;
   int64_t ldw;
   const float* scale_w;
-  const void* x;         // the tokens as the launches above order them, and their scales
+  const void* x;         // the tokens as the launches above order them, and their scales; or unquantised
   const float* scale_x;
+  int64_t ldx;           // of unquantised ones
+  int32_t vec;           // whose rows start at multiples of 16 bytes
   void* y;
   int64_t ldy;
   int32_t n, k, tokens;
   int32_t dtype;         // of y
 };
-// Has to follow one of the two launches that write x: it reads w before that one ends.
-cudaError_t launch_int8_few(const Int8FewArgs& args, cudaStream_t stream);
+bool int8_few_quantises(int64_t tokens, int64_t k);  // whether it takes unquantised tokens
+// type_x: their type, or < 0: it has to follow one of the two launches that write x, and reads w before that one ends.
+cudaError_t launch_int8_few(int type_x, const Int8FewArgs& args, cudaStream_t stream);
 
 }  // namespace gb300

@@ -73,13 +73,14 @@ def load():
 # -------------------------------------------------------------------- arguments
 def _same_device(index, *others):
     for t in others:
-        other = t.get_device() if isinstance(t, torch.Tensor) else t.index
+        other = t.index if type(t) is Int8Matrix or type(t) is Int8Checkpoint else t.get_device()
         if other != index:
             raise ValueError(f"operands are on different devices (cuda:{index} and cuda:{other})")
 
 
 def _cuda_device(device):
-    device = torch.device(device)
+    if type(device) is not torch.device:
+        device = torch.device(device)
     if device.type != "cuda":
         raise ValueError(f"an 8-bit matrix lives on a CUDA device, not on {device}")
     return device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
@@ -98,26 +99,41 @@ class Int8Matrix:
     Made by :func:`int8_quantize` or, from a checkpoint's arrays, by :func:`int8_matrix`.
     """
 
-    __slots__ = ("shape", "device", "index", "_codes", "_scales", "_c", "_ref", "__weakref__")
+    __slots__ = ("shape", "device", "index", "_memory", "_arrays", "_c", "_ref", "__weakref__")
 
     def __init__(self, rows, cols, device="cuda", stream=None):
         device = _cuda_device(device)
+        # One allocation: the codes, then the scales.
         pitch = (cols + 15) // 16 * 16
-        self._set(_empty((rows, pitch), torch.int8, device, stream)[:, :cols],
-                  _empty((rows,), torch.float32, device, stream), device)
+        memory = _empty((rows * (pitch + 4),), torch.uint8, device, stream)
+        self.shape, self.device, self.index, self._memory, self._arrays = (rows, cols), device, device.index, (memory,), None
+        base = memory.data_ptr()
+        self._c = c = _Matrix(rows, cols, base, pitch, base + rows * pitch)
+        self._ref = ctypes.addressof(c)
 
-    def _set(self, codes, scales, device):
+    @classmethod
+    def _of(cls, codes, scales):
+        """The matrix that these arrays (as the library takes them) are."""
+        self = cls.__new__(cls)
         rows, cols = codes.shape
-        self.shape, self.device, self.index = (rows, cols), device, device.index
         # The library has the addresses of these two: they stay.
-        self._codes, self._scales = codes, scales
+        self.shape, self.device, self.index, self._memory, self._arrays = (
+            (rows, cols), codes.device, codes.get_device(), (codes, scales), (codes, scales))
         ld = codes.stride(0) if rows > 1 else (cols + 15) // 16 * 16
         self._c = _Matrix(rows, cols, codes.data_ptr(), ld, scales.data_ptr())
         self._ref = ctypes.addressof(self._c)
         return self
 
-    codes = property(lambda self: self._codes)
-    scales = property(lambda self: self._scales)
+    def _views(self):
+        if self._arrays is None:
+            (rows, cols), memory = self.shape, self._memory[0]
+            pitch = (cols + 15) // 16 * 16
+            self._arrays = (memory[:rows * pitch].view(torch.int8).view(rows, pitch)[:, :cols],
+                            memory[rows * pitch:].view(torch.float32))
+        return self._arrays
+
+    codes = property(lambda self: self._views()[0])
+    scales = property(lambda self: self._views()[1])
 
     def dequantize(self, dtype=torch.float32):
         """The values (:func:`int8_dequantize`)."""
@@ -146,7 +162,7 @@ def int8_quantize(x, out=None, stream=None):
             raise ValueError(f"out is {out}, expected {(rows, cols)}")
         _same_device(x.get_device(), out)
     if stream is not None:
-        _read_on(stream, x, out.codes, out.scales)
+        _read_on(stream, x, *out._memory)
     _call("int8_quantize", out.index, stream, load().int8_quantize, _DTYPES[x.dtype], x.data_ptr(), ld, out._ref)
     return out
 
@@ -179,8 +195,7 @@ def int8_matrix(codes, scales, stream=None):
             memory = torch.zeros((rows, pitch), dtype=torch.int8, device=device)
             memory[:, :cols].copy_(codes)
             codes = memory[:, :cols]
-        q = Int8Matrix.__new__(Int8Matrix)
-        return q._set(codes, scales.contiguous(), device)
+        return Int8Matrix._of(codes, scales.contiguous())
 
 
 def int8_dequantize(q, dtype=torch.float32, out=None, stream=None):
@@ -191,7 +206,7 @@ def int8_dequantize(q, dtype=torch.float32, out=None, stream=None):
     number = _type(dtype)
     out, ld = _output(out, q.shape, dtype, q.device, q.index, stream)
     if stream is not None:
-        _read_on(stream, q.codes, q.scales, out)
+        _read_on(stream, *q._memory, out)
     _call("int8_dequantize", q.index, stream, load().int8_dequantize, q._ref, number, out.data_ptr(), ld)
     return out
 
@@ -214,7 +229,7 @@ def int8_gemm(A, B, out=None, out_dtype=torch.float32, stream=None):
     number = _type(out_dtype, "out_dtype")
     out, ld = _output(out, (A.shape[0], B.shape[0]), out_dtype, A.device, A.index, stream)
     if stream is not None:
-        _read_on(stream, A.codes, A.scales, B.codes, B.scales, out)
+        _read_on(stream, *A._memory, *B._memory, out)
     _call("int8_gemm", A.index, stream, load().int8_gemm, A._ref, B._ref, number, out.data_ptr(), ld)
     return out
 
@@ -232,7 +247,7 @@ def int8_linear(x, W, out=None, stream=None):
     _same_device(index, x)
     out, ldy = _output(out, (m, n), dtype, W.device, index, stream)
     if stream is not None:
-        _read_on(stream, x, W.codes, W.scales, out)
+        _read_on(stream, x, *W._memory, out)
     _call("int8_linear", index, stream, load().int8_linear, _DTYPES[dtype], x.data_ptr(), ldx, m, W._ref, out.data_ptr(),
           ldy)
     return out
@@ -263,8 +278,8 @@ class Int8Checkpoint:
         self.shape, self.dtype, self.order, self.device, self.index = (rows, cols), dtype, order, device, device.index
         self._memory, self._split = _empty((split + unit_lines * ldu * 2,), torch.uint8, device, stream), (lines, ld, unit_lines, ldu)
         base = self._memory.data_ptr()
-        self._c = _Checkpoint(number, ORDERS.index(order), rows, cols, base, ld, base + split, ldu)
-        self._ref = ctypes.addressof(self._c)
+        self._c = c = _Checkpoint(number, 0 if order == "channels" else 1, rows, cols, base, ld, base + split, ldu)
+        self._ref = ctypes.addressof(c)
 
     @property
     def codes(self):
@@ -368,7 +383,7 @@ def int8_swiglu(gate, up, out=None, stream=None):
         raise ValueError(f"gate and up differ: {tuple(gate.shape)} {gate.dtype} and {tuple(up.shape)} {up.dtype}")
     index, dtype, device = gate.get_device(), gate.dtype, gate.device
     _same_device(index, up)
-    kept = tuple(Int8Checkpoint(rows, cols, dtype, "tokens", device, stream) for _ in range(2))
+    kept = Int8Checkpoint(rows, cols, dtype, "tokens", device, stream), Int8Checkpoint(rows, cols, dtype, "tokens", device, stream)
     out, ldh = _output(out, (rows, cols), dtype, device, index, stream)
     if stream is not None:
         _read_on(stream, gate, up, out)
@@ -385,7 +400,7 @@ def int8_swiglu_backward(dh, kept, out=None, stream=None):
     """
     if not isinstance(kept, (tuple, list)) or len(kept) != 2:
         raise TypeError("kept must be the pair that int8_swiglu returned")
-    g, u = (_kept(c, "kept", "tokens") for c in kept)
+    g, u = _kept(kept[0], "kept", "tokens"), _kept(kept[1], "kept", "tokens")
     if u.shape != g.shape or u.dtype != g.dtype:
         raise ValueError(f"kept values differ: {g} and {u}")
     lddh, rows, _ = _dense(dh, "dh", g.shape[1])
@@ -393,11 +408,12 @@ def int8_swiglu_backward(dh, kept, out=None, stream=None):
         raise ValueError(f"dh must be {g.shape} {g.dtype}, got {tuple(dh.shape)} {dh.dtype}")
     _same_device(g.index, u, dh)
     if out is None:
-        both = _empty((rows, 2 * g.shape[1]), g.dtype, g.device, stream)
-        out = both[:, :g.shape[1]], both[:, g.shape[1]:]
+        dgate, dup = _empty((rows, 2, g.shape[1]), g.dtype, g.device, stream).unbind(1)
+        ldg = ldu = 2 * g.shape[1] or 1
     elif not isinstance(out, (tuple, list)) or len(out) != 2:
         raise TypeError("out must be a pair of tensors")
-    (dgate, ldg), (dup, ldu) = (_output(t, g.shape, g.dtype, g.device, g.index, stream) for t in out)
+    else:
+        (dgate, ldg), (dup, ldu) = (_output(t, g.shape, g.dtype, g.device, g.index, stream) for t in out)
     if stream is not None:
         _read_on(stream, dh, g._memory, u._memory, dgate, dup)
     _call("int8_swiglu_backward", g.index, stream, load().int8_swiglu_backward, dh.data_ptr(), lddh, g._ref, u._ref,

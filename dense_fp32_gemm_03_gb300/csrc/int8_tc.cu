@@ -211,12 +211,16 @@ __device__ __forceinline__ void put_columns(T* out, int64_t ld, int left, bool a
   constexpr int kPart = kCount < 16 ? kCount : 16;
 #pragma unroll
   for (int c0 = 0; c0 < kCount; c0 += kPart) {
-    float old[kPart];
+    float old[kPart] = {};
+    if (add) {
+      const T* from = out;
 #pragma unroll
-    for (int c = 0; c < kPart; ++c) old[c] = add && c0 + c < left ? to_f32(out[(c0 + c) * ld]) : 0.f;
+      for (int c = 0; c < kPart; ++c, from += ld)
+        if (c0 + c < left) old[c] = to_f32(*from);
+    }
 #pragma unroll
-    for (int c = 0; c < kPart; ++c)
-      if (c0 + c < left) out[(c0 + c) * ld] = from_f32<T>(add ? v[c0 + c] + old[c] : v[c0 + c]);
+    for (int c = 0; c < kPart; ++c, out += ld)
+      if (c0 + c < left) *out = from_f32<T>(add ? v[c0 + c] + old[c] : v[c0 + c]);
   }
 }
 template <int kCount>
@@ -228,6 +232,18 @@ __device__ __forceinline__ void put_columns(const Int8TcArgs& a, int64_t row, in
     put_columns(static_cast<__nv_bfloat16*>(a.out) + at, a.ld, a.cols - col, a.accumulate, v);
   else
     put_columns(static_cast<__half*>(a.out) + at, a.ld, a.cols - col, a.accumulate, v);
+}
+
+// Stores kCount columns of a row, two 16-bit values in a register.  (The address is counted on from column to column: as
+// c * ld from the first, the tiles of 4096 x 4096 x 1008 took 63 us instead of 25.)
+template <int kCount>
+__device__ __forceinline__ void put_pairs(uint16_t* out, int64_t ld, int left, const uint32_t (&two)[kCount / 2]) {
+#pragma unroll
+  for (int c = 0; c < kCount; c += 2) {
+    if (c < left) out[0] = uint16_t(two[c / 2]);
+    if (c + 1 < left) out[ld] = uint16_t(two[c / 2] >> 16);
+    out += 2 * ld;
+  }
 }
 
 template <typename S>
@@ -484,8 +500,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
       auto put_partials = [&](int c0, const uint32_t* bits) {
         uint32_t* out = args.partials + (int64_t(w.part) * args.cols + col0 + c0) * args.rows + row;
 #pragma unroll
-        for (int c = 0; c < kPart; ++c)
-          if (mine && col0 + c0 + c < args.cols) out[int64_t(c) * args.rows] = bits[c];
+        for (int c = 0; c < kPart; ++c, out += args.rows)
+          if (mine && col0 + c0 + c < args.cols) *out = bits[c];
       };
       auto acc_wait = [&]() {
         wait(&acc_full[b.i], b.parity);
@@ -535,7 +551,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
           for (int x = 0; x < kPart; ++x)
             v[x] = S::kKind == kIntegers ? scaled(int(sum[c + x]), scale_r, __shfl_sync(0xffffffffu, scale_c[c / 32], x))
                                          : __uint_as_float(sum[c + x]);
-          if (mine) put_columns(args, row, col0 + c, v);
+          if (S::kKind == kIntegers && args.dtype != INT8_F32) {
+            uint32_t two[kPart / 2];
+#pragma unroll
+            for (int x = 0; x < kPart; x += 2) two[x / 2] = args.dtype == INT8_BF16 ? pack2<__nv_bfloat162>(v[x], v[x + 1]) : pack2<__half2>(v[x], v[x + 1]);
+            if (mine) put_pairs<kPart>(static_cast<uint16_t*>(args.out) + int64_t(col0 + c) * args.ld + row, args.ld, args.cols - col0 - c, two);
+          } else if (mine) {
+            put_columns(args, row, col0 + c, v);
+          }
         }
       } else {
         const uint32_t at = acc_wait();
@@ -567,13 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
             for (int x = 0; x < kPart; x += 2) two[(c + x) / 2] = args.dtype == INT8_BF16 ? pack2<__nv_bfloat162>(v[x], v[x + 1]) : pack2<__half2>(v[x], v[x + 1]);
           }
           acc_free();
-          uint16_t* out = static_cast<uint16_t*>(args.out) + int64_t(col0) * args.ld + row;
-          const int left = args.cols - col0;
-          if (ok && mine) {
-#pragma unroll
-            for (int c = 0; c < S::kV; ++c)
-              if (c < left) out[c * args.ld] = uint16_t(two[c / 2] >> (c % 2 * 16));
-          }
+          if (ok && mine) put_pairs<S::kV>(static_cast<uint16_t*>(args.out) + int64_t(col0) * args.ld + row, args.ld, args.cols - col0, two);
         }
       }
     }

@@ -148,25 +148,41 @@ struct Operands {
   int terms;
 };
 
-// Tiles, and the shares that k is cut into where there are fewer tiles than pairs of CTAs: a share has
-// four stages of k at least, since its sums are written and read once more.
-sgemm_status_t plan(gb300::Int8TcShape shape, int64_t rows, int64_t cols, int64_t depth, int terms, int pairs,
-                    gb300::Int8TcArgs* a) {
-  const int64_t steps = round_up(depth, gb300::int8_tc_step()) / gb300::int8_tc_step();
-  const int64_t tr = (rows + 255) / 256, tc = (cols + gb300::int8_tc_cols(shape) - 1) / gb300::int8_tc_cols(shape), tiles = tr * tc;
+// The tiles, and the shares that k is cut into where there are fewer tiles than pairs of CTAs, that are estimated to
+// be fastest (us, fitted to GB300 timings).  A stage of 128 of k takes its MMAs, 0.53 for 256 columns and 0.34 for 128
+// or fewer (reading `a` from tensor memory takes as long), which is also what turning `a` to 16 bits takes; a
+// tile fills and empties the pipeline (1.5); shares are written, and read by a kernel that adds them (4.5, and
+// 4 bytes each way at 4 TB/s).  Equal ones: the narrower tiles, which read less of b.
+sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t rows, int64_t cols, int64_t depth, int terms, int pairs,
+                    gb300::Int8TcArgs* a, gb300::Int8TcShape* best) {
+  const int64_t steps = round_up(depth, gb300::int8_tc_step()) / gb300::int8_tc_step(), tr = (rows + 255) / 256;
   if (pairs <= 0) return SGEMM_ERR_LAUNCH;
-  if (tiles > 0x3fffffffLL || terms * depth > 0x7fffffffLL) return SGEMM_ERR_UNSUPPORTED;
+  if (terms * depth > 0x7fffffffLL) return SGEMM_ERR_UNSUPPORTED;
   a->rows = int32_t(rows);
   a->cols = int32_t(cols);
   a->depth = int32_t(depth);
   a->steps = int32_t(steps);
   a->terms = terms;
   a->run = terms == 1 ? 1024 / gb300::int8_tc_step() : 4;
-  a->tiles_r = int32_t(tr);
-  a->tiles_c = int32_t(tc);
-  a->splits = int32_t(std::max<int64_t>(1, std::min(pairs / tiles, steps / 4)));
-  a->units = int32_t(tiles * a->splits);
-  return SGEMM_OK;
+  double least = 0.0;
+  for (const gb300::Int8TcShape shape : shapes) {
+    const int64_t n = gb300::int8_tc_cols(shape), tc = (cols + n - 1) / n, tiles = tr * tc;
+    if (tiles > 0x3fffffffLL) continue;
+    const double stage = double(terms) * std::max(0.34, double(n) * (0.53 / 256));
+    for (const int64_t splits : {int64_t(1), std::min(pairs / tiles, steps / 4)}) {
+      if (splits < 1) continue;
+      const double us = double((tiles * splits + pairs - 1) / pairs) * (double((steps + splits - 1) / splits) * stage + 1.5) +
+                        (splits > 1 ? 4.5 + double(splits) * double(rows) * double(cols) * 2e-6 : 0.0);
+      if (least > 0.0 && us >= least) continue;
+      least = us;
+      *best = shape;
+      a->tiles_r = int32_t(tr);
+      a->tiles_c = int32_t(tc);
+      a->splits = int32_t(splits);
+      a->units = int32_t(tiles * splits);
+    }
+  }
+  return least > 0.0 ? SGEMM_OK : SGEMM_ERR_UNSUPPORTED;
 }
 size_t partial_bytes(const gb300::Int8TcArgs& a) {
   return a.splits > 1 ? size_t(a.splits) * size_t(a.rows) * size_t(a.cols) * 4 : 0;
@@ -226,10 +242,10 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
     f.scale_x = A ? A->scales : scales;
     return status_of(gb300::launch_int8_few(-1, f, stream));
   }
-  const gb300::Int8TcShape shape = M <= 32 ? gb300::kInt8Whole32 : M <= 64 ? gb300::kInt8Whole64 : gb300::kInt8Whole128;
   const int pairs = tc_pairs(d.dev);
   gb300::Int8TcArgs a{};
-  sgemm_status_t st = plan(shape, B.rows, M, B.cols, 1, pairs, &a);
+  gb300::Int8TcShape shape{};
+  sgemm_status_t st = plan({gb300::kInt8Whole32, gb300::kInt8Whole64, gb300::kInt8Whole128}, B.rows, M, B.cols, 1, pairs, &a, &shape);
   if (st != SGEMM_OK) return st;
   const int64_t ld16 = round_up(B.cols, 8);
   Scratch s;
@@ -370,11 +386,15 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   if (st != SGEMM_OK || N == 0 || c->cols == 0) return st;
   if (c->rows == 0) return accumulate ? SGEMM_OK : zero_output(dtype, dw, N, c->cols, ldw, stream);
   // 32-bit results are added up 1024 products at a time.
-  const bool half = c->dtype == INT8_F16, runs = dtype == INT8_F32;
-  const gb300::Int8TcShape shape = half ? (runs ? gb300::kInt8F16Runs : gb300::kInt8F16) : (runs ? gb300::kInt8Bf16Runs : gb300::kInt8Bf16);
   const int pairs = tc_pairs(d.dev), terms = gb300::int8_terms(c->dtype);
   gb300::Int8TcArgs a{};
-  st = plan(shape, c->cols, N, c->rows, terms, pairs, &a);
+  gb300::Int8TcShape shape{};
+  const bool half = c->dtype == INT8_F16;
+  if (dtype == INT8_F32)
+    st = plan({half ? gb300::kInt8F16Runs : gb300::kInt8Bf16Runs}, c->cols, N, c->rows, terms, pairs, &a, &shape);
+  else
+    st = plan({half ? gb300::kInt8F16N128 : gb300::kInt8Bf16N128, half ? gb300::kInt8F16N256 : gb300::kInt8Bf16N256}, c->cols, N, c->rows,
+              terms, pairs, &a, &shape);
   if (st != SGEMM_OK) return st;
   const bool in_place = terms == 1 && aligned(dy, 16) && (lddy % 8 == 0 || c->rows == 1);
   Operands o{c->codes, c->ld, c->units, c->ld_units, static_cast<const uint16_t*>(dy), round_up(lddy, 8), terms};

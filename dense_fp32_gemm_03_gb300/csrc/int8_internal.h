@@ -41,7 +41,13 @@ cudaError_t launch_int8_swiglu_backward(const void* dh, int64_t lddh, const int8
 // ---- products on the tensor cores (int8_tc.cu)
 // D[r, c] = sum over k of a[r, k] b[c, k], stored at out[c * ld + r]; `a` 8-bit integers, times units if it is a
 // checkpoint; b 16-bit floats.
-enum Int8TcShape { kInt8Whole32, kInt8Whole64, kInt8Whole128, kInt8Bf16, kInt8Bf16Runs, kInt8F16, kInt8F16Runs, kInt8TcShapes };
+// The kind of `a`, whether sums leave the accumulator every 1024 products, and the columns of a tile.
+enum Int8TcShape {
+  kInt8Whole32, kInt8Whole64, kInt8Whole128,
+  kInt8Bf16N128, kInt8Bf16N256, kInt8Bf16Runs,
+  kInt8F16N128, kInt8F16N256, kInt8F16Runs,
+  kInt8TcShapes
+};
 int int8_tc_cols(Int8TcShape shape);  // columns of a tile (of 256 rows)
 int int8_tc_step();                   // elements of k a stage
 // Sets the kernels' attributes on the current device; the CTA pairs that run at once, or < 0.

@@ -640,9 +640,11 @@ Instance instance(int shape) {
     case kInt8Whole32: return instance_of<kIntegers, 32, true>();
     case kInt8Whole64: return instance_of<kIntegers, 64, true>();
     case kInt8Whole128: return instance_of<kIntegers, 128, true>();
-    case kInt8Bf16: return instance_of<kBf16, 256, false>();
+    case kInt8Bf16N128: return instance_of<kBf16, 128, false>();
+    case kInt8Bf16N256: return instance_of<kBf16, 256, false>();
     case kInt8Bf16Runs: return instance_of<kBf16, 128, true>();
-    case kInt8F16: return instance_of<kF16, 256, false>();
+    case kInt8F16N128: return instance_of<kF16, 128, false>();
+    case kInt8F16N256: return instance_of<kF16, 256, false>();
     default: return instance_of<kF16, 128, true>();
   }
 }

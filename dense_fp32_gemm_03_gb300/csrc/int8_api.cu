@@ -157,7 +157,6 @@ sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t ro
                     gb300::Int8TcArgs* a, gb300::Int8TcShape* best) {
   const int64_t steps = round_up(depth, gb300::int8_tc_step()) / gb300::int8_tc_step(), tr = (rows + 255) / 256;
   if (pairs <= 0) return SGEMM_ERR_LAUNCH;
-  if (terms * depth > 0x7fffffffLL) return SGEMM_ERR_UNSUPPORTED;
   a->rows = int32_t(rows);
   a->cols = int32_t(cols);
   a->depth = int32_t(depth);
@@ -379,6 +378,7 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   if (st == SGEMM_OK) st = check_dense(dtype, dw, N, c->cols, ldw);
   if (st != SGEMM_OK) return st;
   if (dtype != c->dtype && dtype != INT8_F32) return SGEMM_ERR_INVALID_VALUE;
+  if (c->rows > kMaxExtent / 2 || N > kMaxExtent / 2) return SGEMM_ERR_UNSUPPORTED;  // bytes of a row, and rows of three terms, in 31 bits
   if (overlap_any(dense_range(dtype, dw, N, c->cols, ldw), {code_range(c), unit_range(c), dense_range(c->dtype, dy, c->rows, N, lddy)}))
     return SGEMM_ERR_INVALID_VALUE;
   LibDevice d;

@@ -152,7 +152,7 @@ def _rows(q, name):
 def int8_quantize(x, out=None, stream=None):
     """x (2-D float32, bfloat16 or float16 CUDA tensor, any row stride) in 8 bits with a scale a row: an :class:`Int8Matrix`.
 
-    ``out`` (an ``Int8Matrix`` of x's shape) is filled if given.
+    ``out`` (an ``Int8Matrix`` of x's shape that an earlier call returned) is filled if given.
     """
     ld, rows, cols = _dense(x, "x")
     if out is None:
@@ -160,6 +160,8 @@ def int8_quantize(x, out=None, stream=None):
     else:
         if _rows(out, "out").shape != (rows, cols):
             raise ValueError(f"out is {out}, expected {(rows, cols)}")
+        if len(out._memory) > 1:
+            raise ValueError("out is a matrix of a checkpoint's arrays, which may lie between others")
         _same_device(x.get_device(), out)
     if stream is not None:
         _read_on(stream, x, *out._memory)

@@ -48,8 +48,9 @@ typedef enum { INT8_F32 = 0, INT8_BF16 = 1, INT8_F16 = 2 } int8_dtype_t;
 /*
  * rows x cols integers, row r at codes + r * ld, and a scale for each row.
  * codes is 16-byte aligned and ld a multiple of 16.  Codes may hold any
- * integer from -128 on; what follows a row's cols codes is not used
- * (int8_quantize() zeroes it up to the next multiple of 16).
+ * integer from -128 on.  A row takes cols bytes rounded up to 16: what follows
+ * its codes there may be read and is not used, and int8_quantize() writes
+ * zeros to it.
  */
 typedef struct {
   int64_t rows, cols;
@@ -119,10 +120,12 @@ sgemm_status_t int8_restore(const int8_checkpoint_t *c, int dtype, void *y, int6
  * (c->rows x N, type c->dtype, row stride lddy) and X the values of c, of order
  * INT8_CHANNELS.  dW is N x c->cols (row stride ldw) of type `dtype`, which is
  * c->dtype or INT8_F32; if `accumulate`, dW is added to (read, and rounded once).
- * Every product is exact and sums are kept in 32 bits (INT8_F32 gradients are
- * taken as three bfloat16 terms, which hold all of their 24 bits above 2^-126; 16-bit
- * ones as they are).  No tokens: zeros, or dW as it was.  Sums over several million
- * tokens keep the precision of 32-bit sums of 1024 at a time for INT8_F32.
+ * Every product is exact and sums are kept in 32 bits: INT8_F32 gradients are
+ * taken as three bfloat16 terms, which hold all of their 24 bits from 2^-110
+ * on, 16-bit ones as they are.  The tensor core cuts off what is below an
+ * accumulator's last place; for dW of INT8_F32 the sums leave it every 1024
+ * products (512 tokens of three terms) and are added, correctly rounded,
+ * elsewhere.  No tokens: zeros, or dW as it was.  At most 2^29 tokens, and N.
  */
 sgemm_status_t int8_weight_grad(const void *dy, int64_t lddy, int64_t N, const int8_checkpoint_t *c, int dtype,
                                 int32_t accumulate, void *dw, int64_t ldw, cudaStream_t stream);

@@ -203,7 +203,7 @@ sgemm_status_t run_product(gb300::Int8TcShape shape, const Operands& o, gb300::I
   if (st != SGEMM_OK) return st;
   a.status = d.status;
   a.wait_limit_ns = d.wait_limit_ns;
-  return status_of(gb300::launch_int8_tc(shape, maps, a, pairs, d.sms, stream));
+  return status_of(gb300::launch_int8_tc(shape, maps, a, pairs, stream));
 }
 
 // C (M x N, row stride ldc) = A B^T, from A's rows as 16-bit floats or, with x, quantised on the way.

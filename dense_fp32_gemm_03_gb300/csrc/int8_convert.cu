@@ -18,6 +18,7 @@ namespace {
 using namespace int8;
 
 constexpr int kThreads = 256;
+constexpr int kPer = 2;  // chunks that a thread has on the way where it does little else
 
 bool aligned16(const void* p, int64_t ld_bytes) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld_bytes % 16 == 0; }
 
@@ -183,7 +184,8 @@ struct Chunks {
   int64_t row_chunks;
   Divider div;
 };
-// This thread's chunk in each step of its block's run.
+// This thread's kPer chunks in each step of its block's run.
+template <int kPer>
 struct Walk {
   int64_t row0, left;
   uint32_t c0;
@@ -194,18 +196,18 @@ struct Walk {
     c0 = uint32_t(first - row0 * n.row_chunks);
     left = min(n.per_block, n.all - first);
   }
-  // Whether this thread has one; its row and its place in the row.
-  __device__ __forceinline__ bool at(const Chunks& n, int64_t& row, int64_t& c) const {
-    const uint32_t i = c0 + threadIdx.x, r = divide(i, n.div);
+  // Whether this thread has a j-th one; its row and its place in the row.
+  __device__ __forceinline__ bool at(const Chunks& n, int j, int64_t& row, int64_t& c) const {
+    const uint32_t i = c0 + threadIdx.x + j * kThreads, r = divide(i, n.div);
     row = row0 + r;
     c = i - r * n.div.d;
-    return threadIdx.x < left;
+    return threadIdx.x + j * kThreads < left;
   }
   __device__ __forceinline__ void next(const Chunks& n) {
-    const uint32_t i = c0 + kThreads, r = divide(i, n.div);
+    const uint32_t i = c0 + kPer * kThreads, r = divide(i, n.div);
     row0 += r;
     c0 = i - r * n.div.d;
-    left -= kThreads;
+    left -= kPer * kThreads;
   }
 };
 
@@ -222,9 +224,9 @@ struct BackArgs {
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const BackArgs a) {
   begin();
-  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
+  for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
-    if (!w.at(a.n, row, c)) break;
+    if (!w.at(a.n, 0, row, c)) break;
     const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
     const float s = a.scales[row];
     float v[8];
@@ -238,22 +240,31 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const BackArgs a) 
 
 __global__ void __launch_bounds__(kThreads) widen_kernel(const BackArgs a) {
   begin();
-  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
-    int64_t row, c;
-    if (!w.at(a.n, row, c)) break;
-    const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
-    float v[8];
-    widen4(q.x, v);
-    widen4(q.y, v + 4);
-    if (8 * c + 8 > a.cols) {
+  for (Walk<kPer> w(a.n); w.left > 0; w.next(a.n)) {
+    int64_t row[kPer], c[kPer];
+    bool here[kPer];
+    uint2 q[kPer];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 8 * c + e < a.cols ? v[e] : 0.f;
+    for (int j = 0; j < kPer; ++j) {
+      here[j] = w.at(a.n, j, row[j], c[j]);
+      if (here[j]) q[j] = *reinterpret_cast<const uint2*>(a.codes + row[j] * a.ld + 8 * c[j]);
     }
-    uint4 h;
-    __half2* p = reinterpret_cast<__half2*>(&h);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.ld_out + 8 * c) = h;
+    for (int j = 0; j < kPer; ++j) {
+      if (!here[j]) break;
+      float v[8];
+      widen4(q[j].x, v);
+      widen4(q[j].y, v + 4);
+      if (8 * c[j] + 8 > a.cols) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 8 * c[j] + e < a.cols ? v[e] : 0.f;
+      }
+      uint4 h;
+      __half2* p = reinterpret_cast<__half2*>(&h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row[j] * a.ld_out + 8 * c[j]) = h;
+    }
   }
 }
 
@@ -301,23 +312,31 @@ __device__ __forceinline__ uint32_t take16(float& v) {
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
   begin();
-  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
-    int64_t row, c;
-    if (!w.at(a.n, row, c)) break;
-    float v[8];
-    load8<kVec>(static_cast<const T*>(a.x) + row * a.ldx + 8 * c, a.cols - 8 * c, v);
-    uint16_t* out = a.out + row * a.ld + 8 * c;
-    if constexpr (sizeof(T) == 4) {
+  for (Walk<kPer> w(a.n); w.left > 0; w.next(a.n)) {
+    int64_t row[kPer], c[kPer];
+    bool here[kPer];
+    float v[kPer][8];
 #pragma unroll
-      for (int t = 0; t < 3; ++t) {
-        uint4 w;
-        uint16_t* p = reinterpret_cast<uint16_t*>(&w);
+    for (int j = 0; j < kPer; ++j) {
+      here[j] = w.at(a.n, j, row[j], c[j]);
+      if (here[j]) load8<kVec>(static_cast<const T*>(a.x) + row[j] * a.ldx + 8 * c[j], a.cols - 8 * c[j], v[j]);
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = uint16_t(take16(v[e]));
-        *reinterpret_cast<uint4*>(out + t * a.rows * a.ld) = w;
+    for (int j = 0; j < kPer; ++j) {
+      if (!here[j]) break;
+      uint16_t* out = a.out + row[j] * a.ld + 8 * c[j];
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+          uint4 term;
+          uint16_t* p = reinterpret_cast<uint16_t*>(&term);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = uint16_t(take16(v[j][e]));
+          *reinterpret_cast<uint4*>(out + t * a.rows * a.ld) = term;
+        }
+      } else {
+        store8<true>(reinterpret_cast<T*>(out), 8, v[j]);
       }
-    } else {
-      store8<true>(reinterpret_cast<T*>(out), 8, v);
     }
   }
 }
@@ -416,9 +435,9 @@ struct RestoreArgs {
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) restore_tokens_kernel(const RestoreArgs a) {
   begin();
-  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
+  for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
-    if (!w.at(a.n, row, c)) break;
+    if (!w.at(a.n, 0, row, c)) break;
     const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
     const float u = unit_value(a.units[row * a.ldu + c / 4], a.half);
     float v[8];
@@ -505,9 +524,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
   begin();
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
   const int64_t blocks = (a.cols + 31) / 32;
-  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
+  for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
-    const bool here = w.at(a.n, row, c);
+    const bool here = w.at(a.n, 0, row, c);
     const int64_t left = here ? a.cols - 8 * c : 0;
     float g[8] = {}, u[8] = {}, h[8];
     if (left > 0) {
@@ -531,9 +550,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluA
                                                                    int64_t lddg, T* dup, int64_t lddu) {
   begin();
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
-  for (Walk w(a.n); w.left > 0; w.next(a.n)) {
+  for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
-    if (!w.at(a.n, row, c)) break;
+    if (!w.at(a.n, 0, row, c)) break;
     const int64_t left = a.cols - 8 * c;
     const uint2 wg = *reinterpret_cast<const uint2*>(a.kg + row * a.ldkg + 8 * c);
     const uint2 wu = *reinterpret_cast<const uint2*>(a.ku + row * a.ldku + 8 * c);
@@ -555,13 +574,13 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluA
 
 // Rows of `row_chunks` chunks over blocks, 96 to an SM at most: with 8, which start and end together, the gated
 // activation of 8192 x 8192 fp32 takes 163 us instead of 139, and 158 instead of 141 back.
-Chunks chunks_of(int64_t rows, int64_t row_chunks, int sms) {
+Chunks chunks_of(int64_t rows, int64_t row_chunks, int sms, int per = 1) {
   Chunks n{};
   n.all = rows * row_chunks;
   n.row_chunks = row_chunks;
   n.div = divider(uint32_t(row_chunks));
-  const int64_t steps = (n.all + kThreads - 1) / kThreads, blocks = std::min(steps, int64_t(sms) * 96);
-  n.per_block = (steps + blocks - 1) / blocks * kThreads;
+  const int64_t step = int64_t(per) * kThreads, steps = (n.all + step - 1) / step, blocks = std::min(steps, int64_t(sms) * 96);
+  n.per_block = (steps + blocks - 1) / blocks * step;
   return n;
 }
 int64_t blocks_of(const Chunks& n) { return (n.all + n.per_block - 1) / n.per_block; }
@@ -599,7 +618,7 @@ cudaError_t launch_int8_dequantize(const int8_matrix_t& q, int dtype, void* y, i
 }
 
 cudaError_t launch_int8_widen(const int8_matrix_t& q, uint16_t* out, int64_t ld, int sms, cudaStream_t stream) {
-  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, out, ld, chunks_of(q.rows, (q.cols + 7) / 8, sms)};
+  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, out, ld, chunks_of(q.rows, (q.cols + 7) / 8, sms, kPer)};
   return launch(widen_kernel, blocks_of(a.n), kThreads, stream, a);
 }
 
@@ -607,7 +626,7 @@ int int8_terms(int dtype) { return dtype == INT8_F32 ? 3 : 1; }
 
 cudaError_t launch_int8_split(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
                               int64_t ld, int sms, cudaStream_t stream) {
-  const SplitArgs a{x, ldx, rows, cols, out, ld, chunks_of(rows, (cols + 7) / 8, sms)};
+  const SplitArgs a{x, ldx, rows, cols, out, ld, chunks_of(rows, (cols + 7) / 8, sms, kPer)};
   const bool vec = whole(cols, aligned16(x, ldx * bytes_of(dtype)));
   GB300_INT8_BY_TYPE(dtype, launch(vec ? split_kernel<T, true> : split_kernel<T, false>, blocks_of(a.n), kThreads, stream, a))
 }

@@ -71,7 +71,7 @@ struct Int8TcArgs {
 // maps: `a` (boxes of 128 rows x 128 bytes), its units (4 rows x 128 bytes), b (rows of k in boxes of half the tile's
 // columns x 128 bytes, or for checkpoints rows of columns in boxes of 128 rows x 128 bytes).  May start beside the end of the kernel
 // before on the stream, and waits for it by itself.
-cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], const Int8TcArgs& args, int pairs, int sms,
+cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], const Int8TcArgs& args, int pairs,
                            cudaStream_t stream);
 
 // ---- the same for few tokens (int8_few.cu): y = X W^T

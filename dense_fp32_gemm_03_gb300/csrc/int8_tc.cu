@@ -604,23 +604,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
   }
 }
 
-// Adds the shares of a product split over k, in their order, and stores it.
+// Adds the shares of a product split over k, in their order, and stores it: kJoin columns of a row a thread.
+constexpr int kJoin = 2;
 template <bool kWhole>
 __global__ void __launch_bounds__(256) join_kernel(const Int8TcArgs args) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int r = blockIdx.x * 256 + threadIdx.x, c0 = blockIdx.y * kJoin;
+  if (r >= args.rows) return;
   const int64_t all = int64_t(args.rows) * args.cols;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
-    const int64_t c = i / args.rows, r = i - c * args.rows;
-    float v[1] = {0.f};
-    if constexpr (kWhole) {
-      uint32_t sum = 0;
-      for (int p = 0; p < args.splits; ++p) sum += args.partials[p * all + i];
-      v[0] = scaled(int(sum), args.scale_r[r], args.scale_c[c]);
-    } else {
-      for (int p = 0; p < args.splits; ++p) v[0] += __uint_as_float(args.partials[p * all + i]);
-    }
-    put_columns(args, r, int(c), v);
+  const uint32_t* from = args.partials + int64_t(c0) * args.rows + r;
+  uint32_t sum[kJoin] = {};
+#pragma unroll 4
+  for (int p = 0; p < args.splits; ++p, from += all) {
+    uint32_t x[kJoin];
+#pragma unroll
+    for (int c = 0; c < kJoin; ++c) x[c] = c0 + c < args.cols ? from[int64_t(c) * args.rows] : 0u;
+#pragma unroll
+    for (int c = 0; c < kJoin; ++c)
+      sum[c] = kWhole ? sum[c] + x[c] : __float_as_uint(__uint_as_float(sum[c]) + __uint_as_float(x[c]));
   }
+  float v[kJoin];
+#pragma unroll
+  for (int c = 0; c < kJoin; ++c)
+    v[c] = kWhole ? (c0 + c < args.cols ? scaled(int(sum[c]), args.scale_r[r], args.scale_c[c0 + c]) : 0.f) : __uint_as_float(sum[c]);
+  put_columns(args, r, c0, v);
 }
 
 typedef void (*Kernel)(CUtensorMap, CUtensorMap, CUtensorMap, Int8TcArgs);
@@ -672,7 +679,7 @@ int int8_tc_prepare() {
   return pairs;
 }
 
-cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], const Int8TcArgs& args, int pairs, int sms,
+cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], const Int8TcArgs& args, int pairs,
                            cudaStream_t stream) {
   const Instance in = instance(shape);
   cudaLaunchAttribute attr = {};
@@ -687,8 +694,8 @@ cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], cons
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, in.kernel, maps[0], maps[1], maps[2], args);
   if (e != cudaSuccess || args.splits == 1) return e;
-  const int64_t all = int64_t(args.rows) * args.cols;
-  cfg.gridDim = dim3(unsigned(std::min((all + 255) / 256, int64_t(sms) * 8)), 1, 1);
+  // (Fewer tiles than pairs of CTAs were split: the columns are some ten thousand at most.)
+  cfg.gridDim = dim3(unsigned((args.rows + 255) / 256), unsigned((args.cols + kJoin - 1) / kJoin), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, args.scale_r ? join_kernel<true> : join_kernel<false>, args);

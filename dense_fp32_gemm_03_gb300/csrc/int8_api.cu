@@ -128,12 +128,16 @@ struct Scratch {
 
 // ------------------------------------------------------------------- products
 std::mutex g_mu;
-std::map<int, int> g_pairs;  // CTA pairs that run at once, by device
+std::map<int, gb300::Int8TcClusters> g_clusters;  // by device; no pairs: not to be had
 
-int tc_pairs(int dev) {
+gb300::Int8TcClusters tc_clusters(int dev) {
   std::lock_guard<std::mutex> lock(g_mu);
-  auto it = g_pairs.find(dev);
-  if (it == g_pairs.end()) it = g_pairs.emplace(dev, gb300::int8_tc_prepare()).first;
+  auto it = g_clusters.find(dev);
+  if (it == g_clusters.end()) {
+    gb300::Int8TcClusters n;
+    if (!gb300::int8_tc_prepare(&n)) n = gb300::Int8TcClusters{};
+    it = g_clusters.emplace(dev, n).first;
+  }
   return it->second;
 }
 
@@ -152,10 +156,11 @@ struct Operands {
 // be fastest (us, fitted to GB300 timings).  A stage of 128 of k takes its MMAs, 0.53 for 256 columns and 0.34 for 128
 // or fewer (reading `a` from tensor memory takes as long), which is also what turning `a` to 16 bits takes; a
 // tile fills and empties the pipeline (1.5); shares are written, and read by a kernel that adds them (4.5, and
-// 4 bytes each way at 4 TB/s).  Equal ones: the narrower tiles, which read less of b.
-sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t rows, int64_t cols, int64_t depth, int terms, int pairs,
-                    gb300::Int8TcArgs* a, gb300::Int8TcShape* best) {
+// 4 bytes each way at 4 TB/s), or joined within a cluster (1).  Equal ones: the narrower tiles, which read less of b.
+sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t rows, int64_t cols, int64_t depth, int terms,
+                    const gb300::Int8TcClusters& most, gb300::Int8TcArgs* a, gb300::Int8TcShape* best) {
   const int64_t steps = round_up(depth, gb300::int8_tc_step()) / gb300::int8_tc_step(), tr = (rows + 255) / 256;
+  const int64_t pairs = most.pairs;
   if (pairs <= 0) return SGEMM_ERR_LAUNCH;
   a->rows = int32_t(rows);
   a->cols = int32_t(cols);
@@ -168,23 +173,27 @@ sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t ro
     const int64_t n = gb300::int8_tc_cols(shape), tc = (cols + n - 1) / n, tiles = tr * tc;
     if (tiles > 0x3fffffffLL) continue;
     const double stage = double(terms) * std::max(0.34, double(n) * (0.53 / 256));
-    for (const int64_t splits : {int64_t(1), std::min(pairs / tiles, steps / 4)}) {
-      if (splits < 1) continue;
+    auto consider = [&](int64_t splits, bool join) {
       const double us = double((tiles * splits + pairs - 1) / pairs) * (double((steps + splits - 1) / splits) * stage + 1.5) +
-                        (splits > 1 ? 4.5 + double(splits) * double(rows) * double(cols) * 2e-6 : 0.0);
-      if (least > 0.0 && us >= least) continue;
+                        (join ? 1.0 : splits > 1 ? 4.5 + double(splits) * double(rows) * double(cols) * 2e-6 : 0.0);
+      if (least > 0.0 && us >= least) return;
       least = us;
       *best = shape;
       a->tiles_r = int32_t(tr);
       a->tiles_c = int32_t(tc);
       a->splits = int32_t(splits);
       a->units = int32_t(tiles * splits);
-    }
+      a->join = join;
+    };
+    consider(1, false);
+    for (int64_t splits = 2; splits <= gb300::int8_tc_shares(shape); splits *= 2)
+      if (tiles <= (splits == 2 ? most.twos : most.fours) && splits <= steps) consider(splits, true);
+    if (std::min(pairs / tiles, steps / 4) > 1) consider(std::min(pairs / tiles, steps / 4), false);
   }
   return least > 0.0 ? SGEMM_OK : SGEMM_ERR_UNSUPPORTED;
 }
 size_t partial_bytes(const gb300::Int8TcArgs& a) {
-  return a.splits > 1 ? size_t(a.splits) * size_t(a.rows) * size_t(a.cols) * 4 : 0;
+  return a.splits > 1 && !a.join ? size_t(a.splits) * size_t(a.rows) * size_t(a.cols) * 4 : 0;
 }
 
 sgemm_status_t run_product(gb300::Int8TcShape shape, const Operands& o, gb300::Int8TcArgs a, int pairs, const LibDevice& d,
@@ -241,10 +250,10 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
     f.scale_x = A ? A->scales : scales;
     return status_of(gb300::launch_int8_few(-1, f, stream));
   }
-  const int pairs = tc_pairs(d.dev);
+  const gb300::Int8TcClusters most = tc_clusters(d.dev);
   gb300::Int8TcArgs a{};
   gb300::Int8TcShape shape{};
-  sgemm_status_t st = plan({gb300::kInt8Whole32, gb300::kInt8Whole64, gb300::kInt8Whole128}, B.rows, M, B.cols, 1, pairs, &a, &shape);
+  sgemm_status_t st = plan({gb300::kInt8Whole32, gb300::kInt8Whole64, gb300::kInt8Whole128}, B.rows, M, B.cols, 1, most, &a, &shape);
   if (st != SGEMM_OK) return st;
   const int64_t ld16 = round_up(B.cols, 8);
   Scratch s;
@@ -265,7 +274,7 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
   a.ld = ldc;
   a.early = 1;
   a.partials = reinterpret_cast<uint32_t*>(base + partials_at);
-  return run_product(shape, Operands{B.codes, B.ld, nullptr, 0, rows16, ld16, 1}, a, pairs, d, stream);
+  return run_product(shape, Operands{B.codes, B.ld, nullptr, 0, rows16, ld16, 1}, a, most.pairs, d, stream);
 }
 
 }  // namespace
@@ -386,15 +395,16 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   if (st != SGEMM_OK || N == 0 || c->cols == 0) return st;
   if (c->rows == 0) return accumulate ? SGEMM_OK : zero_output(dtype, dw, N, c->cols, ldw, stream);
   // 32-bit results are added up 1024 products at a time.
-  const int pairs = tc_pairs(d.dev), terms = gb300::int8_terms(c->dtype);
+  const gb300::Int8TcClusters most = tc_clusters(d.dev);
+  const int terms = gb300::int8_terms(c->dtype);
   gb300::Int8TcArgs a{};
   gb300::Int8TcShape shape{};
   const bool half = c->dtype == INT8_F16;
   if (dtype == INT8_F32)
-    st = plan({half ? gb300::kInt8F16Runs : gb300::kInt8Bf16Runs}, c->cols, N, c->rows, terms, pairs, &a, &shape);
+    st = plan({half ? gb300::kInt8F16Runs : gb300::kInt8Bf16Runs}, c->cols, N, c->rows, terms, most, &a, &shape);
   else
     st = plan({half ? gb300::kInt8F16N128 : gb300::kInt8Bf16N128, half ? gb300::kInt8F16N256 : gb300::kInt8Bf16N256}, c->cols, N, c->rows,
-              terms, pairs, &a, &shape);
+              terms, most, &a, &shape);
   if (st != SGEMM_OK) return st;
   const bool in_place = terms == 1 && aligned(dy, 16) && (lddy % 8 == 0 || c->rows == 1);
   Operands o{c->codes, c->ld, c->units, c->ld_units, static_cast<const uint16_t*>(dy), round_up(lddy, 8), terms};
@@ -416,7 +426,7 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   a.out = dw;
   a.ld = ldw;
   a.partials = reinterpret_cast<uint32_t*>(base + partials_at);
-  return run_product(shape, o, a, pairs, d, stream);
+  return run_product(shape, o, a, most.pairs, d, stream);
 } GB300_INT8_CATCH
 
 sgemm_status_t int8_swiglu(int dtype, int64_t M, int64_t F, const void* gate, int64_t ld_gate, const void* up,

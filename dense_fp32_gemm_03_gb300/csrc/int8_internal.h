@@ -50,8 +50,12 @@ enum Int8TcShape {
 };
 int int8_tc_cols(Int8TcShape shape);  // columns of a tile (of 256 rows)
 int int8_tc_step();                   // elements of k a stage
-// Sets the kernels' attributes on the current device; the CTA pairs that run at once, or < 0.
-int int8_tc_prepare();
+int int8_tc_shares(Int8TcShape shape);  // shares of k that a cluster's pairs can join among themselves
+// How many clusters of one, two and four pairs of CTAs run at once.
+struct Int8TcClusters {
+  int pairs, twos, fours;
+};
+bool int8_tc_prepare(Int8TcClusters* n);  // sets the kernels' attributes on the current device, too
 struct Int8TcArgs {
   int32_t rows, cols, depth;
   int32_t steps, terms;      // stages of k; matrices b, one after the other with depth rows each, whose products are added
@@ -64,7 +68,8 @@ struct Int8TcArgs {
   void* out;
   int64_t ld;
   int32_t early;             // the launch before prepared b (one of those above): `a` is read before it ends
-  uint32_t* partials;        // splits x cols x rows 32-bit sums, if splits > 1
+  int32_t join;              // a tile's shares are the pairs of a cluster, which add them; otherwise a kernel of its own does
+  uint32_t* partials;        // splits x cols x rows 32-bit sums for that
   uint32_t* status;
   uint64_t wait_limit_ns;
 };

@@ -65,27 +65,40 @@ struct Tile {
   static constexpr int kSlotCols = kStep / 2;  // tensor memory columns of a stage of `a`
   static constexpr int kSlots0 = (512 - kAccs * kN) / kSlotCols;
   static constexpr int kSlots = kSlots0 < 6 ? kSlots0 : 6;
-  static constexpr int kStages0 = int((232448 - 1024 - 512) / (kABytes + kUBytes + kBBytes));
+  // Narrow tiles' shares of k, of up to four pairs in a cluster, meet in the first pair's shared memory.
+  static constexpr int kMaxShares = kN == 32 ? 4 : 1;
+  static constexpr uint32_t kShareBytes = kRows * kN * 4, kJoinBytes = (kMaxShares - 1) * kShareBytes;
+  static constexpr int kStages0 = int((232448 - 1024 - 512 - kJoinBytes) / (kABytes + kUBytes + kBBytes));
   static constexpr int kStages = kStages0 < 8 ? kStages0 : 8;
   static constexpr int kThreads = 128 * (3 + kGroups);
   static constexpr int kV = kN / 2;  // columns of an epilogue warp
   static constexpr int kBarriers = 4 * kStages + 2 * kSlots + 2 * kAccs + 1;
-  static constexpr size_t kSmem = 1024 + kStages * size_t(kABytes + kUBytes + kBBytes) + kBarriers * 8 + 16;
+  static constexpr size_t kSmem = 1024 + kStages * size_t(kABytes + kUBytes + kBBytes) + kJoinBytes + kBarriers * 8 + 16;
   static_assert(kSmem <= 232448 && kAccs * kN + kSlots * kSlotCols <= 512, "memory");
   // 32-bit accumulator; A from tensor memory, B K-major or MN-major (bit 16); M = 256.
   static constexpr uint32_t kDesc = (1u << 4) | (kKind == kBf16 ? (1u << 7) | (1u << 10) : 0u) | (kUnits ? 1u << 16 : 0u) |
                                     (uint32_t(kN >> 3) << 17) | (256u >> 4 << 24);
 };
 
-__device__ __forceinline__ uint32_t in_first(uint64_t* bar) {
+// The same place in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t place_in(const void* p, uint32_t rank) {
   uint32_t d;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(dev::smem_addr(bar)), "r"(0));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(dev::smem_addr(p)), "r"(rank));
   return d;
 }
 // What these arrivals hand over is in tensor memory and ordered by tcgen05.fence; with the release at cluster scope,
 // which waits for all of the warp's earlier accesses, a stage took 3400 cycles instead of 1640.
-__device__ __forceinline__ void arrive_first(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Arrives on `bar` of the CTAs of `mask` once the tcgen05 operations issued so far completed.
+__device__ __forceinline__ void commit(uint32_t e, uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          dev::smem_addr(bar)),
+      "h"(mask), "r"(e)
+      : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -247,7 +260,7 @@ __device__ __forceinline__ void put_pairs(uint16_t* out, int64_t ld, int left, c
 }
 
 template <typename S>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
+__global__ void __launch_bounds__(S::kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_u,
                    const __grid_constant__ CUtensorMap map_b, const Int8TcArgs args) {
   extern __shared__ unsigned char smem_raw[];
@@ -256,7 +269,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
   unsigned char* s_a = smem;
   unsigned char* s_b = s_a + S::kStages * S::kABytes;
   unsigned char* s_u = s_b + S::kStages * S::kBBytes;
-  uint64_t* a_full = reinterpret_cast<uint64_t*>(s_u + S::kStages * S::kUBytes);
+  unsigned char* s_join = s_u + S::kStages * S::kUBytes;
+  uint64_t* a_full = reinterpret_cast<uint64_t*>(s_join + S::kJoinBytes);
   uint64_t* a_empty = a_full + S::kStages;
   uint64_t* b_full = a_empty + S::kStages;     // used in the first CTA
   uint64_t* b_empty = b_full + S::kStages;
@@ -269,9 +283,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1) + 1;
 
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
-  uint32_t rank;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  uint32_t cluster_rank;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(cluster_rank));
+  const uint32_t rank = cluster_rank & 1, leader = cluster_rank & ~1u;  // in the pair, and its first CTA
   const bool first = rank == 0;
+  const uint16_t both = uint16_t(3u << leader);
   const int unit0 = blockIdx.x / 2, pairs = gridDim.x / 2;
   const uint64_t limit = args.wait_limit_ns;
 
@@ -362,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
           go = going();
         }
         if (go) {
-          const uint32_t e = elected(), bar = in_first(&b_full[s.i]);
+          const uint32_t e = elected(), bar = place_in(&b_full[s.i], leader);
           if (first) expect_bytes(e, &b_full[s.i], 2 * S::kBBytes);
           unsigned char* to = s_b + s.i * S::kBBytes;
           if constexpr (S::kUnits) {
@@ -403,10 +419,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
             mma(e, d, a + 8 * j, db + (S::kUnits ? j * (16 * 128 >> 4) : j / 4 * (S::kCols * 128 >> 4) + j % 4 * 2), S::kDesc, add);
             add = 1u;
           }
-          fp4::commit<2>(e, &b_empty[s.i]);
-          if (last) fp4::commit<2>(e, &slot_empty[at.i]);
+          commit(e, &b_empty[s.i], both);
+          if (last) commit(e, &slot_empty[at.i], both);
           if (ends) {
-            fp4::commit<2>(e, &acc_full[b.i]);
+            commit(e, &acc_full[b.i], both);
             b.next();
           }
           s.next();
@@ -414,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
           if (last) t = at;
         });
       }
-      fp4::commit<2>(elected(), drain);
+      commit(elected(), drain, both);
       dev::mbar_wait(drain, 0u, limit);
     }
   }
@@ -483,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_first(&slot_full[t.i]);
+        if (lane == 0) arrive_at(place_in(&slot_full[t.i], leader));
       }
     }
   } else {
@@ -512,13 +528,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
       auto acc_free = [&]() {
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_first(&acc_empty[b.i]);
+        if (lane == 0) arrive_at(place_in(&acc_empty[b.i], leader));
         b.next();
       };
       if constexpr (S::kRuns) {
         // Scales of this warp's columns, 32 a register; a row's.
         float scale_c[(S::kV + 31) / 32], scale_r = 0.f;
-        if (S::kKind == kIntegers && args.splits == 1) {
+        if (S::kKind == kIntegers && (args.splits == 1 || args.join)) {
 #pragma unroll
           for (int c = 0; c < S::kV; c += 32) scale_c[c / 32] = col0 + c + lane < args.cols ? args.scale_c[col0 + c + lane] : 0.f;
           if (mine) scale_r = args.scale_r[row];
@@ -539,10 +555,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
           }
           acc_free();
         }
-        if (!going()) continue;
+        bool ok = going();
+        if constexpr (S::kMaxShares > 1) {
+          if (args.join) {
+            // The only unit of this pair: its sums go to the first pair, which has them after everybody's barrier.
+            const int at = half * S::kV * kRows + 32 * q + lane;
+            if (w.part != 0 && ok) {
+              const uint32_t to = place_in(s_join + (w.part - 1) * S::kShareBytes, rank) + 4 * at;
+#pragma unroll
+              for (int c = 0; c < S::kV; ++c) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 4 * kRows * c), "r"(sum[c]) : "memory");
+            }
+            __syncwarp();
+            cluster_sync();
+            ok = ok && w.part == 0;
+            if (ok)
+              for (int p = 1; p < args.splits; ++p) {
+                const uint32_t* from = reinterpret_cast<const uint32_t*>(s_join + (p - 1) * S::kShareBytes) + at;
+#pragma unroll
+                for (int c = 0; c < S::kV; ++c) sum[c] += from[kRows * c];
+              }
+          }
+        }
+        if (!ok) continue;
 #pragma unroll
         for (int c = 0; c < S::kV; c += kPart) {
-          if (args.splits > 1) {
+          if (args.splits > 1 && !args.join) {
             put_partials(c, sum + c);
             continue;
           }
@@ -595,9 +632,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(S::kThreads, 1)
       }
     }
   }
+  __syncwarp();
+  if (S::kMaxShares > 1 && args.join && warp < 4 + 4 * kGroups) cluster_sync();  // (the epilogue's warps were there)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  cluster_sync();  // nothing of either CTA is still signalled or read by the other
+  cluster_sync();  // nothing of any CTA is still signalled or read by another
   if (warp == 3) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
@@ -634,12 +673,12 @@ typedef void (*Kernel)(CUtensorMap, CUtensorMap, CUtensorMap, Int8TcArgs);
 struct Instance {
   Kernel kernel;
   size_t smem;
-  int threads, cols;
+  int threads, cols, shares;
 };
 template <Kind kKind, int kN, bool kRuns>
 Instance instance_of() {
   using S = Tile<kKind, kN, kRuns>;
-  return {Kernel(product_kernel<S>), S::kSmem, S::kThreads, kN};
+  return {Kernel(product_kernel<S>), S::kSmem, S::kThreads, kN, S::kMaxShares};
 }
 
 Instance instance(int shape) {
@@ -659,41 +698,55 @@ Instance instance(int shape) {
 }  // namespace
 
 int int8_tc_cols(Int8TcShape shape) { return instance(shape).cols; }
+int int8_tc_shares(Int8TcShape shape) { return instance(shape).shares; }
 int int8_tc_step() { return kStep; }
 
-int int8_tc_prepare() {
-  int pairs = 0;
+bool int8_tc_prepare(Int8TcClusters* n) {
+  *n = Int8TcClusters{};
   for (int shape = 0; shape < kInt8TcShapes; ++shape) {
     const Instance in = instance(shape);
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(in.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(in.smem)) != cudaSuccess)
-      return -1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(in.threads, 1, 1);
-    cfg.dynamicSmemBytes = in.smem;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(in.kernel), &cfg) != cudaSuccess) return -1;
-    if (pairs == 0 || n < pairs) pairs = n;
+      return false;
+    for (int pairs = 1; pairs <= in.shares; pairs *= 2) {
+      cudaLaunchAttribute attr = {};
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = unsigned(2 * pairs);
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(unsigned(2 * pairs), 1, 1);
+      cfg.blockDim = dim3(in.threads, 1, 1);
+      cfg.dynamicSmemBytes = in.smem;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int most = 0;
+      if (cudaOccupancyMaxActiveClusters(&most, reinterpret_cast<const void*>(in.kernel), &cfg) != cudaSuccess) return false;
+      int& to = pairs == 1 ? n->pairs : pairs == 2 ? n->twos : n->fours;
+      if (to == 0 || most < to) to = most;
+    }
   }
-  return pairs;
+  return n->pairs > 0;
 }
 
 cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], const Int8TcArgs& args, int pairs,
                            cudaStream_t stream) {
   const Instance in = instance(shape);
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(args.join ? 2 * args.splits : 2);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(2 * std::min(pairs, args.units)), 1, 1);
+  cfg.gridDim = dim3(unsigned(2 * (args.join ? args.units : std::min(pairs, args.units))), 1, 1);
   cfg.blockDim = dim3(unsigned(in.threads), 1, 1);
   cfg.dynamicSmemBytes = in.smem;
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, in.kernel, maps[0], maps[1], maps[2], args);
-  if (e != cudaSuccess || args.splits == 1) return e;
+  if (e != cudaSuccess || args.splits == 1 || args.join) return e;
+  cfg.numAttrs = 1;  // no clusters
   // (Fewer tiles than pairs of CTAs were split: the columns are some ten thousand at most.)
   cfg.gridDim = dim3(unsigned((args.rows + 255) / 256), unsigned((args.cols + kJoin - 1) / kJoin), 1);
   cfg.blockDim = dim3(256, 1, 1);

@@ -256,6 +256,18 @@ def int8_linear(x, W, out=None, stream=None):
 
 
 # ------------------------------------------------------------------ checkpoints
+def _lines(order, rows, cols):
+    """int8_checkpoint_layout()'s lines and pitches: of the codes, then of the units, which follow them in one allocation."""
+    blocks = (cols + 31) // 32
+    if order == "channels":
+        return cols, (rows + 15) // 16 * 16, blocks, (rows + 7) // 8 * 8
+    return rows, (cols + 15) // 16 * 16, rows, (blocks + 7) // 8 * 8
+
+
+def _bytes(lines):
+    return lines[0] * lines[1] + 2 * lines[2] * lines[3]
+
+
 class Int8Checkpoint:
     """Activations kept in 8 bits: ``shape`` (tokens, channels), ``dtype`` (of what was kept), ``order``, ``device``.
 
@@ -268,35 +280,33 @@ class Int8Checkpoint:
     __slots__ = ("shape", "dtype", "order", "device", "index", "_memory", "_split", "_c", "_ref", "__weakref__")
 
     def __init__(self, rows, cols, dtype, order, device="cuda", stream=None):
-        number = _type(dtype)
         if order not in ORDERS:
             raise ValueError(f"order must be one of {ORDERS}, got {order!r}")
-        device = _cuda_device(device)
-        # int8_checkpoint_layout()'s sizes, in one allocation: the codes, then the units.
-        blocks = (cols + 31) // 32
-        lines, entries, unit_lines, unit_entries = (cols, rows, blocks, rows) if order == "channels" else (rows, cols, rows, blocks)
-        ld, ldu = (entries + 15) // 16 * 16, (unit_entries + 7) // 8 * 8
-        split = lines * ld
+        number, device, lines = _type(dtype), _cuda_device(device), _lines(order, rows, cols)
+        self._set(rows, cols, dtype, number, order, device, lines, _empty((_bytes(lines),), torch.uint8, device, stream), 0)
+
+    def _set(self, rows, cols, dtype, number, order, device, lines, memory, start):
         self.shape, self.dtype, self.order, self.device, self.index = (rows, cols), dtype, order, device, device.index
-        self._memory, self._split = _empty((split + unit_lines * ldu * 2,), torch.uint8, device, stream), (lines, ld, unit_lines, ldu)
-        base = self._memory.data_ptr()
-        self._c = c = _Checkpoint(number, 0 if order == "channels" else 1, rows, cols, base, ld, base + split, ldu)
+        self._memory, self._split = memory, (start, *lines)
+        base = memory.data_ptr() + start
+        self._c = c = _Checkpoint(number, 0 if order == "channels" else 1, rows, cols, base, lines[1], base + lines[0] * lines[1], lines[3])
         self._ref = ctypes.addressof(c)
+        return self
 
     @property
     def codes(self):
         """The integers, int8 (lines x pitch)."""
-        lines, ld, _, _ = self._split
-        return self._memory[:lines * ld].view(torch.int8).view(lines, ld)
+        start, lines, ld, _, _ = self._split
+        return self._memory[start:start + lines * ld].view(torch.int8).view(lines, ld)
 
     @property
     def units(self):
         """The blocks' units (lines x pitch), bfloat16 or float16."""
-        lines, ld, unit_lines, ldu = self._split
-        kind = torch.float16 if self.dtype == torch.float16 else torch.bfloat16
-        return self._memory[lines * ld:].view(kind).view(unit_lines, ldu)
+        start, lines, ld, unit_lines, ldu = self._split
+        kind, start = torch.float16 if self.dtype == torch.float16 else torch.bfloat16, start + lines * ld
+        return self._memory[start:start + 2 * unit_lines * ldu].view(kind).view(unit_lines, ldu)
 
-    nbytes = property(lambda self: self._memory.numel())
+    nbytes = property(lambda self: _bytes(self._split[1:]))
 
     def restore(self, dtype=None):
         """The values (:func:`int8_restore`)."""
@@ -385,11 +395,15 @@ def int8_swiglu(gate, up, out=None, stream=None):
         raise ValueError(f"gate and up differ: {tuple(gate.shape)} {gate.dtype} and {tuple(up.shape)} {up.dtype}")
     index, dtype, device = gate.get_device(), gate.dtype, gate.device
     _same_device(index, up)
-    kept = Int8Checkpoint(rows, cols, dtype, "tokens", device, stream), Int8Checkpoint(rows, cols, dtype, "tokens", device, stream)
+    number, lines = _DTYPES[dtype], _lines("tokens", rows, cols)
+    size = _bytes(lines)                       # (a multiple of 16)
+    memory = _empty((2 * size,), torch.uint8, device, stream)
+    kept = tuple([Int8Checkpoint.__new__(Int8Checkpoint)._set(rows, cols, dtype, number, "tokens", device, lines, memory, start)
+                  for start in (0, size)])
     out, ldh = _output(out, (rows, cols), dtype, device, index, stream)
     if stream is not None:
         _read_on(stream, gate, up, out)
-    _call("int8_swiglu", index, stream, load().int8_swiglu, _DTYPES[dtype], rows, cols, gate.data_ptr(), ldg,
+    _call("int8_swiglu", index, stream, load().int8_swiglu, number, rows, cols, gate.data_ptr(), ldg,
           up.data_ptr(), ldu, out.data_ptr(), ldh, kept[0]._ref, kept[1]._ref)
     return out, kept
 
@@ -410,8 +424,10 @@ def int8_swiglu_backward(dh, kept, out=None, stream=None):
         raise ValueError(f"dh must be {g.shape} {g.dtype}, got {tuple(dh.shape)} {dh.dtype}")
     _same_device(g.index, u, dh)
     if out is None:
-        dgate, dup = _empty((rows, 2, g.shape[1]), g.dtype, g.device, stream).unbind(1)
-        ldg = ldu = 2 * g.shape[1] or 1
+        cols = g.shape[1]
+        both = _empty((rows, 2 * cols), g.dtype, g.device, stream)
+        dgate, dup = both.as_strided((rows, cols), (2 * cols, 1)), both.as_strided((rows, cols), (2 * cols, 1), cols)
+        ldg = ldu = 2 * cols or 1
     elif not isinstance(out, (tuple, list)) or len(out) != 2:
         raise TypeError("out must be a pair of tensors")
     else:

@@ -167,7 +167,7 @@ sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t ro
   a->depth = int32_t(depth);
   a->steps = int32_t(steps);
   a->terms = terms;
-  a->run = terms == 1 ? 1024 / gb300::int8_tc_step() : 4;
+  a->run = 1024 / gb300::int8_tc_step();
   double least = 0.0;
   for (const gb300::Int8TcShape shape : shapes) {
     const int64_t n = gb300::int8_tc_cols(shape), tc = (cols + n - 1) / n, tiles = tr * tc;
@@ -229,11 +229,10 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
     f.k = int32_t(B.cols);
     f.tokens = int32_t(M);
     f.dtype = dtype;
-    if (!A && gb300::int8_few_quantises(M, B.cols)) {
+    if (!A && gb300::int8_few_quantises(M, B.rows, B.cols, d.sms)) {
       f.x = x;
-      f.ldx = ldx;
-      f.vec = aligned(x, 16) && (M == 1 || ldx * dtype_bytes(dtype_x) % 16 == 0);
-      return status_of(gb300::launch_int8_few(dtype_x, f, stream));
+      f.vec = aligned(x, 16);
+      return status_of(gb300::launch_int8_few(dtype_x, f, d.sms, stream));
     }
     Scratch s;
     const size_t scales_at = s.take(M * 4), tokens_at = s.take(16 * round_up(B.cols, 64));
@@ -248,7 +247,7 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
     if (e != cudaSuccess) return SGEMM_ERR_LAUNCH;
     f.x = tokens;
     f.scale_x = A ? A->scales : scales;
-    return status_of(gb300::launch_int8_few(-1, f, stream));
+    return status_of(gb300::launch_int8_few(-1, f, d.sms, stream));
   }
   const gb300::Int8TcClusters most = tc_clusters(d.dev);
   gb300::Int8TcArgs a{};
@@ -394,7 +393,7 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || N == 0 || c->cols == 0) return st;
   if (c->rows == 0) return accumulate ? SGEMM_OK : zero_output(dtype, dw, N, c->cols, ldw, stream);
-  // 32-bit results are added up 1024 products at a time.
+  // 32-bit results are added up 512 tokens at a time.
   const gb300::Int8TcClusters most = tc_clusters(d.dev);
   const int terms = gb300::int8_terms(c->dtype);
   gb300::Int8TcArgs a{};
@@ -406,6 +405,7 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
     st = plan({half ? gb300::kInt8F16N128 : gb300::kInt8Bf16N128, half ? gb300::kInt8F16N256 : gb300::kInt8Bf16N256}, c->cols, N, c->rows,
               terms, most, &a, &shape);
   if (st != SGEMM_OK) return st;
+  a.run = 512 / gb300::int8_tc_step();
   const bool in_place = terms == 1 && aligned(dy, 16) && (lddy % 8 == 0 || c->rows == 1);
   Operands o{c->codes, c->ld, c->units, c->ld_units, static_cast<const uint16_t*>(dy), round_up(lddy, 8), terms};
   if (!in_place) o.ldb = round_up(N, 8);

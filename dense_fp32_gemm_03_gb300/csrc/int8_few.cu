@@ -9,9 +9,9 @@
 // an SM, its integer mma 27 for 16 x 8 x 32: 80 and 17 us for 8 tokens of 8192 x 8192.)
 //
 // Structure.  A block has 16 or 32 rows of W, and its warps take 64 columns of K in turn; each has
-// 8 KB of W on the way.  Products take the tokens as 16-bit floats in the lanes' order.  One or two tokens of
-// moderate length are quantised by every block for itself, into shared memory while its first loads of W
-// are on the way; more by a kernel of their own, and the first of W is requested before that is done.
+// 8 KB of W on the way.  Products take the tokens as 16-bit floats in the lanes' order.  A single token of
+// moderate length is quantised by every block for itself, into shared memory while its first loads of W
+// are on the way; others by a kernel of their own, and the first of W is requested before that is done.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -46,9 +46,9 @@ template <typename T, int kR, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int8FewArgs a) {
   constexpr int kThreads = 32 * kWarps, kAhead = 8 / kR, kXAhead = kR == 1 ? 4 : 2;
   constexpr bool kQuantise = !std::is_same<T, void>::value;
-  extern __shared__ __align__(16) unsigned char s_x[];  // 16 bytes for each step, half, token and t
+  extern __shared__ __align__(16) unsigned char s_x[];  // 16 bytes for each step, half and t
   __shared__ int sums[kWarps][kR * 4][32];
-  __shared__ uint32_t s_top[2];
+  __shared__ uint32_t s_top;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int row0 = blockIdx.x * 16 * kR, steps = (a.k + kStep - 1) / kStep;
   const int8_t* rows[kR][2];
@@ -69,47 +69,41 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int
     // W may be what the kernel before wrote.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x < 2) s_top[threadIdx.x] = 0;
+    if (threadIdx.x == 0) s_top = 0;
     __syncthreads();
     const int chunks = (a.k + 7) / 8;
-    auto read = [&](int m, int c, float (&v)[8]) {
-      const T* p = static_cast<const T*>(a.x) + m * a.ldx + 8 * c;
+    auto read = [&](int c, float (&v)[8]) {
+      const T* p = static_cast<const T*>(a.x) + 8 * c;
       if (a.vec && 8 * c + 8 <= a.k)
         load8<true>(p, 8, v);
       else
         load8<false>(p, a.k - 8 * c, v);
     };
     // Magnitudes compare as their bits do, NaN above infinity.
-    for (int m = 0; m < a.tokens; ++m) {
-      uint32_t top = 0;
-#pragma unroll 4
-      for (int c = threadIdx.x; c < chunks; c += kThreads) {
-        float v[8];
-        read(m, c, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
-      }
-      if (m == 0) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) fetch(j, step_of(j));
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) atomicMax(&s_top[m], top);
-    }
-    __syncthreads();
-    for (int m = 0; m < a.tokens; ++m) {
-      const float s = row_scale(__uint_as_float(s_top[m])), inv = __frcp_rn(s);
+    uint32_t top = 0;
 #pragma unroll 2
-      for (int c = threadIdx.x; c < 8 * steps; c += kThreads) {
-        float v[8], n[8];
-        read(m, c, v);
-        nearest8(v, s, inv, n);
-        uint4 h;
-        __half2* p = reinterpret_cast<__half2*>(&h);
+    for (int c = threadIdx.x; c < chunks; c += kThreads) {
+      float v[8];
+      read(c, v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(n[2 * e] - kRound, n[2 * e + 1] - kRound);
-        reinterpret_cast<uint4*>(s_x)[(((c >> 3) * 2 + (c & 1)) * a.tokens + m) * 4 + (c & 7) / 2] = h;
-      }
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) fetch(j, step_of(j));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) atomicMax(&s_top, top);
+    __syncthreads();
+    const float s = row_scale(__uint_as_float(s_top)), inv = __frcp_rn(s);
+#pragma unroll 2
+    for (int c = threadIdx.x; c < 8 * steps; c += kThreads) {
+      float v[8], n[8];
+      read(c, v);
+      nearest8(v, s, inv, n);
+      uint4 h;
+      __half2* p = reinterpret_cast<__half2*>(&h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(n[2 * e] - kRound, n[2 * e + 1] - kRound);
+      reinterpret_cast<uint4*>(s_x)[((c >> 3) * 2 + (c & 1)) * 4 + (c & 7) / 2] = h;
     }
     __syncthreads();
   } else {
@@ -121,12 +115,12 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int
 
   // Lanes of tokens that are not there keep zeros.
   const uint4* x = (kQuantise ? reinterpret_cast<const uint4*>(s_x) : static_cast<const uint4*>(a.x)) + lane;
-  const int pitch = kQuantise ? 4 * a.tokens : 32;  // of a half
+  constexpr int kPitch = kQuantise ? 4 : 32;  // of a half
   uint4 b[kXAhead][2] = {};
   auto fetch_x = [&](int slot, int step) {
     if (g < a.tokens && step < steps) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) b[slot][h] = x[(2 * step + h) * pitch];
+      for (int h = 0; h < 2; ++h) b[slot][h] = x[(2 * step + h) * kPitch];
     }
   };
 #pragma unroll
@@ -170,7 +164,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int
   for (int i = threadIdx.x; i < 16 * kR * a.tokens; i += kThreads) {
     const int row = i % (16 * kR), m = i / (16 * kR);
     if (row0 + row >= a.n) continue;
-    const float sw = a.scale_w[row0 + row], sx = kQuantise ? row_scale(__uint_as_float(s_top[m])) : a.scale_x[m];
+    const float sw = a.scale_w[row0 + row], sx = kQuantise ? row_scale(__uint_as_float(s_top)) : a.scale_x[m];
     int sum = 0;
 #pragma unroll
     for (int v = 0; v < kWarps; ++v) sum += sums[v][row / 16 * 4 + (row / 8 % 2) * 2 + m % 2][row % 8 * 4 + m / 2];
@@ -195,16 +189,26 @@ Kernel by_warps(int warps) {
 
 int int8_few_tokens() { return kMost; }
 
-// A block reads the tokens twice, 4 bytes a column and token of 16 bits, beside 16 of W.
-bool int8_few_quantises(int64_t tokens, int64_t k) { return tokens <= 2 && tokens * ((k + kStep - 1) / kStep * kStep) <= 16384; }
+// As many warps a block as leave all blocks at work at once, 16 warps on an SM (5000 x 4096 in 313 blocks of eight warps
+// takes 9.6 us, 4096 x 4096 in 256 7.1): 4096 rows are 256 blocks of eight warps, 8192 rows 512 of four.  Beyond four tokens a
+// block has 32 rows, so that its tokens are half as many bytes as its weights, where that leaves 200 blocks (8 tokens of
+// 8192 x 8192 18.2 -> 16.5 us; of 1024 x 8192, 32 blocks, 7 -> 10).
+static int64_t block_rows(int64_t tokens, int64_t n) { return tokens > 4 && n >= 32 * 200 ? 32 : 16; }
+static int block_warps(int64_t tokens, int64_t n, int sms) {
+  const int64_t blocks = (n + block_rows(tokens, n) - 1) / block_rows(tokens, n);
+  return blocks <= sms ? 16 : blocks <= 2 * sms ? 8 : 4;
+}
 
-cudaError_t launch_int8_few(int type_x, const Int8FewArgs& args, cudaStream_t stream) {
-  // Beyond four tokens a block's tokens are half as many bytes as its weights, with 32 rows.
-  const bool tall = args.tokens > 4;
-  const int64_t rows = tall ? 32 : 16, blocks = (args.n + rows - 1) / rows;
-  // 4096 rows are 256 blocks of eight warps, 8192 rows 512 of four: all at work at once.
-  const int warps = blocks >= 400 ? 4 : blocks >= 150 ? 8 : 16;
-  const Kernel kernel = tall ? by_warps<void, 2>(warps)
+// Up to 16 values a thread (1024 x 1024: 2.9 us in a graph, 4.0 with a kernel before; 4096 x 4096: 7.5 and 7.3, but 1.5 us
+// less of host time; 8192 x 8192, 64 a thread: 17.7 and 16.3).
+bool int8_few_quantises(int64_t tokens, int64_t n, int64_t k, int sms) {
+  return tokens == 1 && k <= 16 * 32 * block_warps(1, n, sms);
+}
+
+cudaError_t launch_int8_few(int type_x, const Int8FewArgs& args, int sms, cudaStream_t stream) {
+  const int warps = block_warps(args.tokens, args.n, sms);
+  const int64_t rows = block_rows(args.tokens, args.n), blocks = (args.n + rows - 1) / rows;
+  const Kernel kernel = rows == 32 ? by_warps<void, 2>(warps)
                         : type_x < 0 ? by_warps<void, 1>(warps)
                         : type_x == INT8_F32 ? by_warps<float, 1>(warps)
                         : type_x == INT8_BF16 ? by_warps<__nv_bfloat16, 1>(warps) : by_warps<__half, 1>(warps);
@@ -214,7 +218,7 @@ cudaError_t launch_int8_few(int type_x, const Int8FewArgs& args, cudaStream_t st
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(blocks), 1, 1);
   cfg.blockDim = dim3(32 * warps, 1, 1);
-  cfg.dynamicSmemBytes = type_x < 0 ? 0 : size_t(args.tokens) * ((args.k + kStep - 1) / kStep) * kStep * 2;
+  cfg.dynamicSmemBytes = type_x < 0 ? 0 : size_t((args.k + kStep - 1) / kStep) * kStep * 2;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

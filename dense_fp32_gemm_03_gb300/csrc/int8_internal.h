@@ -41,7 +41,7 @@ cudaError_t launch_int8_swiglu_backward(const void* dh, int64_t lddh, const int8
 // ---- products on the tensor cores (int8_tc.cu)
 // D[r, c] = sum over k of a[r, k] b[c, k], stored at out[c * ld + r]; `a` 8-bit integers, times units if it is a
 // checkpoint; b 16-bit floats.
-// The kind of `a`, whether sums leave the accumulator every 1024 products, and the columns of a tile.
+// The kind of `a`, whether sums leave the accumulator after some stages, and the columns of a tile.
 enum Int8TcShape {
   kInt8Whole32, kInt8Whole64, kInt8Whole128,
   kInt8Bf16N128, kInt8Bf16N256, kInt8Bf16Runs,
@@ -85,17 +85,16 @@ struct Int8FewArgs {
   const int8_t* w;
   int64_t ldw;
   const float* scale_w;
-  const void* x;         // the tokens as the launches above order them, and their scales; or unquantised
+  const void* x;         // the tokens as the launches above order them, and their scales; or one unquantised
   const float* scale_x;
-  int64_t ldx;           // of unquantised ones
-  int32_t vec;           // whose rows start at multiples of 16 bytes
+  int32_t vec;           // which starts at a multiple of 16 bytes
   void* y;
   int64_t ldy;
   int32_t n, k, tokens;
   int32_t dtype;         // of y
 };
-bool int8_few_quantises(int64_t tokens, int64_t k);  // whether it takes unquantised tokens
+bool int8_few_quantises(int64_t tokens, int64_t n, int64_t k, int sms);  // whether it takes unquantised tokens (one)
 // type_x: their type, or < 0: it has to follow one of the two launches that write x, and reads w before that one ends.
-cudaError_t launch_int8_few(int type_x, const Int8FewArgs& args, cudaStream_t stream);
+cudaError_t launch_int8_few(int type_x, const Int8FewArgs& args, int sms, cudaStream_t stream);
 
 }  // namespace gb300

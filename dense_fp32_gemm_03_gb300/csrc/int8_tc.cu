@@ -8,7 +8,7 @@
 // (128 * 128 * 1024 = 2^24).  Integer sums are taken 1024 products at a time and
 // added as integers.  A checkpoint's values q * u (q at most seven bits, u a
 // power of two) are exact in 16 bits too; a gradient's sums stay in the
-// accumulator for 16-bit outputs, and are added up 1024 products at a time in
+// accumulator for 16-bit outputs, and are added up 512 tokens at a time in
 // registers for 32-bit ones (the tensor core cuts what it shifts out; over thousands
 // of additions that shows in 32 bits).
 //
@@ -57,7 +57,7 @@ template <Kind kKind_, int kN_, bool kRuns_>
 struct Tile {
   static constexpr Kind kKind = kKind_;
   static constexpr int kN = kN_;
-  static constexpr bool kRuns = kRuns_;  // sums leave the accumulator every 1024 products
+  static constexpr bool kRuns = kRuns_;  // sums leave the accumulator every `run` stages
   static constexpr bool kUnits = kKind != kIntegers;
   static constexpr int kCols = kN / 2;   // of b, a CTA
   static constexpr uint32_t kABytes = kRows * kStep, kUBytes = kUnits ? 1024 : 0, kBBytes = kCols * kStep * 2;

@@ -386,7 +386,8 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   if (st == SGEMM_OK) st = check_dense(dtype, dw, N, c->cols, ldw);
   if (st != SGEMM_OK) return st;
   if (dtype != c->dtype && dtype != INT8_F32) return SGEMM_ERR_INVALID_VALUE;
-  if (c->rows > kMaxExtent / 2 || N > kMaxExtent / 2) return SGEMM_ERR_UNSUPPORTED;  // bytes of a row, and rows of three terms, in 31 bits
+  // A row's bytes stay within 31 bits, and a tile's tokens within a quarter of the kernel's time limit for a wait.
+  if (c->rows > kMaxExtent / 8 || N > kMaxExtent / 2) return SGEMM_ERR_UNSUPPORTED;
   if (overlap_any(dense_range(dtype, dw, N, c->cols, ldw), {code_range(c), unit_range(c), dense_range(c->dtype, dy, c->rows, N, lddy)}))
     return SGEMM_ERR_INVALID_VALUE;
   LibDevice d;

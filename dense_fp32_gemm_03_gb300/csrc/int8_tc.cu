@@ -24,6 +24,14 @@
 //  * eight warps read a finished accumulator while the next one is filled.
 // Lanes are rows of D, which is stored as columns (out[c * ld + r]): a warp's 32
 // values of a column are consecutive.
+//
+// What bounds it, measured.  16384 tokens, 4096 x 4096 (bfloat16, 256 columns): 313 us, 1756 TFLOP/s with the tensor pipe
+// active 96 % of the time at the 1.78 GHz that power leaves; with 128 columns the converting warps bound it (390 us).
+// 8192^3 of integers (128 columns, 8 runs a tile): 566 us, 1942 TFLOP/s, tensor pipe 87 %, L2 to SM 14.8 TB/s.  256 columns
+// have one accumulator, so that a tile's (or a run's) sums are read before the next one's first product; that costs
+// little after the 128 stages of a gradient's tile, and much after the 8 of a run, so products of integers have 128 columns
+// and two accumulators.  With the first operand in tensor memory an MMA of 32 or 64 columns takes as long as one of 128
+// (0.34 us a stage): small tiles only spread few columns over more SMs.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -150,8 +158,8 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// The same in bfloat16, whose 128 + (low seven bits) has 128 taken off where q >= 0 and 256 where
-// q < 0: that number is 0x4300 and q's top bit.
+// Two of a word's four integers in bfloat16: of 128 + (the low seven bits) 128 is taken off where q >= 0 and 256 where
+// q < 0, the number whose bits are 0x4300 and q's top bit.
 template <int kPair>
 __device__ __forceinline__ uint32_t to_bf16(uint32_t word) {
   const uint32_t p = __byte_perm(word, 0x43434343u, kPair ? 0x4342 : 0x4140);
@@ -341,99 +349,99 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   };
   auto going = [&]() { return __shfl_sync(0xffffffffu, *s_abort, 0) == 0; };
 
-  // 640 threads have 96 registers each; the four warps below give up what the epilogue's sums need.
+  // 640 threads have 96 registers each; these four warps give up what the epilogue's sums need.
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-  if (warp == 0) {
-    // ---- `a` and its units, of this CTA's rows
-    At<S::kStages> s;
-    bool go = true;
-    for (int unit = unit0; go && unit < args.units; unit += pairs) {
-      const Work w = work_of(args, unit, S::kN);
-      const int r0 = w.r0 + int(rank) * kRows;
-      for (int k = w.kb; k < w.ke; ++k, s.next()) {
-        wait(&a_empty[s.i], s.parity ^ 1u);  // (passes in the first round)
-        if (!(go = going())) break;
-        const uint32_t e = elected(), bar = dev::smem_addr(&a_full[s.i]);
-        const int at = k * kStep;
-        expect_bytes(e, &a_full[s.i], S::kABytes + S::kUBytes);
-        load_box<1>(e, s_a + s.i * S::kABytes, &map_a, at, r0, bar);
-        if constexpr (S::kUnits) {
-          load_box<1>(e, s_u + s.i * S::kUBytes, &map_u, 2 * at, r0 / kBlock, bar);
-          load_box<1>(e, s_u + s.i * S::kUBytes + 512, &map_u, 2 * at + 128, r0 / kBlock, bar);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 0) {
+      // ---- `a` and its units, of this CTA's rows
+      At<S::kStages> s;
+      bool go = true;
+      for (int unit = unit0; go && unit < args.units; unit += pairs) {
+        const Work w = work_of(args, unit, S::kN);
+        const int r0 = w.r0 + int(rank) * kRows;
+        for (int k = w.kb; k < w.ke; ++k, s.next()) {
+          wait(&a_empty[s.i], s.parity ^ 1u);  // (passes in the first round)
+          if (!(go = going())) break;
+          const uint32_t e = elected(), bar = dev::smem_addr(&a_full[s.i]);
+          const int at = k * kStep;
+          expect_bytes(e, &a_full[s.i], S::kABytes + S::kUBytes);
+          load_box<1>(e, s_a + s.i * S::kABytes, &map_a, at, r0, bar);
+          if constexpr (S::kUnits) {
+            load_box<1>(e, s_u + s.i * S::kUBytes, &map_u, 2 * at, r0 / kBlock, bar);
+            load_box<1>(e, s_u + s.i * S::kUBytes + 512, &map_u, 2 * at + 128, r0 / kBlock, bar);
+          }
         }
       }
-    }
-    if (!go) settle();
-  } else if (warp == 1) {
-    // ---- b, this CTA's half of the columns; completes on the first CTA's barrier
-    At<S::kStages> s;
-    bool go = true;
-    for (int unit = unit0; go && unit < args.units; unit += pairs) {
-      const Work w = work_of(args, unit, S::kN);
-      const int c0 = w.c0 + int(rank) * S::kCols;
-      for_stages<S>(args, w, [&](int k, int term, bool, bool) {
-        if (go) {
-          wait(&b_empty[s.i], s.parity ^ 1u);
-          go = going();
-        }
-        if (go) {
-          const uint32_t e = elected(), bar = place_in(&b_full[s.i], leader);
-          if (first) expect_bytes(e, &b_full[s.i], 2 * S::kBBytes);
-          unsigned char* to = s_b + s.i * S::kBBytes;
-          if constexpr (S::kUnits) {
-#pragma unroll
-            for (int j = 0; j < S::kCols / 64; ++j)
-              load_box<2>(e, to + j * kStep * 128, &map_b, 2 * (c0 + 64 * j), k * kStep + term * args.depth, bar);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) load_box<2>(e, to + j * S::kCols * 128, &map_b, 2 * kStep * k + 128 * j, c0, bar);
-          }
-          s.next();
-        }
-      });
-    }
-    if (!go) settle();
-  } else if (warp == 2) {
-    if (first) {
-      // ---- MMAs.  The loop's own instructions have to be few: a stage's MMAs take 512 cycles with 128 columns.
-      At<S::kSlots> t;
+      if (!go) settle();
+    } else if (warp == 1) {
+      // ---- b, this CTA's half of the columns; completes on the first CTA's barrier
       At<S::kStages> s;
-      At<S::kAccs> b;
-      const uint64_t desc0 = S::kUnits ? columns_desc(dev::smem_addr(s_b)) : operand_desc(dev::smem_addr(s_b));
-      for (int unit = unit0; unit < args.units; unit += pairs) {
+      bool go = true;
+      for (int unit = unit0; go && unit < args.units; unit += pairs) {
         const Work w = work_of(args, unit, S::kN);
-        At<S::kSlots> at = t;  // within the run
-        for_stages<S>(args, w, [&](int k, int term, bool starts, bool ends) {
-          const bool last = term == 0;  // of the stage's terms
-          if (starts) wait(&acc_empty[b.i], b.parity ^ 1u);
-          if (starts || (args.terms > 1 && (k - w.kb) % args.run == 0)) at = t;
-          if (term == args.terms - 1) wait(&slot_full[at.i], at.parity);
-          wait(&b_full[s.i], s.parity);
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t d = tmem + b.i * S::kN, a = slots + at.i * S::kSlotCols, e = elected();
-          const uint64_t db = desc0 + s.i * (S::kBBytes >> 4);
-          uint32_t add = starts ? 0u : 1u;
-#pragma unroll
-          for (int j = 0; j < kStep / 16; ++j) {
-            mma(e, d, a + 8 * j, db + (S::kUnits ? j * (16 * 128 >> 4) : j / 4 * (S::kCols * 128 >> 4) + j % 4 * 2), S::kDesc, add);
-            add = 1u;
+        const int c0 = w.c0 + int(rank) * S::kCols;
+        for_stages<S>(args, w, [&](int k, int term, bool, bool) {
+          if (go) {
+            wait(&b_empty[s.i], s.parity ^ 1u);
+            go = going();
           }
-          commit(e, &b_empty[s.i], both);
-          if (last) commit(e, &slot_empty[at.i], both);
-          if (ends) {
-            commit(e, &acc_full[b.i], both);
-            b.next();
+          if (go) {
+            const uint32_t e = elected(), bar = place_in(&b_full[s.i], leader);
+            if (first) expect_bytes(e, &b_full[s.i], 2 * S::kBBytes);
+            unsigned char* to = s_b + s.i * S::kBBytes;
+            if constexpr (S::kUnits) {
+  #pragma unroll
+              for (int j = 0; j < S::kCols / 64; ++j)
+                load_box<2>(e, to + j * kStep * 128, &map_b, 2 * (c0 + 64 * j), k * kStep + term * args.depth, bar);
+            } else {
+  #pragma unroll
+              for (int j = 0; j < 2; ++j) load_box<2>(e, to + j * S::kCols * 128, &map_b, 2 * kStep * k + 128 * j, c0, bar);
+            }
+            s.next();
           }
-          s.next();
-          at.next();
-          if (last) t = at;
         });
       }
-      commit(elected(), drain, both);
-      dev::mbar_wait(drain, 0u, limit);
+      if (!go) settle();
+    } else if (warp == 2) {
+      if (first) {
+        // ---- MMAs.  The loop's own instructions have to be few: a stage's MMAs take 512 cycles with 128 columns.
+        At<S::kSlots> t;
+        At<S::kStages> s;
+        At<S::kAccs> b;
+        const uint64_t desc0 = S::kUnits ? columns_desc(dev::smem_addr(s_b)) : operand_desc(dev::smem_addr(s_b));
+        for (int unit = unit0; unit < args.units; unit += pairs) {
+          const Work w = work_of(args, unit, S::kN);
+          At<S::kSlots> at = t;  // within the run
+          for_stages<S>(args, w, [&](int k, int term, bool starts, bool ends) {
+            const bool last = term == 0;  // of the stage's terms
+            if (starts) wait(&acc_empty[b.i], b.parity ^ 1u);
+            if (starts || (args.terms > 1 && (k - w.kb) % args.run == 0)) at = t;
+            if (term == args.terms - 1) wait(&slot_full[at.i], at.parity);
+            wait(&b_full[s.i], s.parity);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t d = tmem + b.i * S::kN, a = slots + at.i * S::kSlotCols, e = elected();
+            const uint64_t db = desc0 + s.i * (S::kBBytes >> 4);
+            uint32_t add = starts ? 0u : 1u;
+  #pragma unroll
+            for (int j = 0; j < kStep / 16; ++j) {
+              mma(e, d, a + 8 * j, db + (S::kUnits ? j * (16 * 128 >> 4) : j / 4 * (S::kCols * 128 >> 4) + j % 4 * 2), S::kDesc, add);
+              add = 1u;
+            }
+            commit(e, &b_empty[s.i], both);
+            if (last) commit(e, &slot_empty[at.i], both);
+            if (ends) {
+              commit(e, &acc_full[b.i], both);
+              b.next();
+            }
+            s.next();
+            at.next();
+            if (last) t = at;
+          });
+        }
+        commit(elected(), drain, both);
+        dev::mbar_wait(drain, 0u, limit);
+      }
     }
-  }
   } else if (warp < 4 + 4 * kGroups) {
     // ---- `a` to 16 bits, in tensor memory
     const int q = warp & 3, group = (warp - 4) >> 2, row = 32 * q + lane;

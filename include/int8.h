@@ -124,7 +124,7 @@ sgemm_status_t int8_restore(const int8_checkpoint_t *c, int dtype, void *y, int6
  * taken as three bfloat16 terms, which hold all of their 24 bits from 2^-110
  * on, 16-bit ones as they are.  The tensor core cuts off what is below an
  * accumulator's last place; for dW of INT8_F32 the sums leave it every 512
- * tokens and are added, correctly rounded, elsewhere.  No tokens: zeros, or dW as it was.  At most 2^29 tokens, and N.
+ * tokens and are added, correctly rounded, elsewhere.  No tokens: zeros, or dW as it was.  At most 2^27 tokens and an N of 2^29.
  */
 sgemm_status_t int8_weight_grad(const void *dy, int64_t lddy, int64_t N, const int8_checkpoint_t *c, int dtype,
                                 int32_t accumulate, void *dw, int64_t ldw, cudaStream_t stream);

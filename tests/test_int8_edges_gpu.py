@@ -125,6 +125,44 @@ def test_lopsided_gradients(dtype, m, n, k):
     check_gradient(sg.int8_weight_grad(dy, sg.int8_checkpoint(x)), dy, x, dtype == F16)
 
 
+@pytest.mark.parametrize("m,n,k", [(9, 8192, 1000), (16, 4096, 4096), (20, 1024, 8200), (32, 300, 3000), (33, 8192, 1024), (64, 1000, 9000),
+                                   (128, 500, 20000), (200, 256, 5000)])
+def test_sums_cut_over_k(m, n, k):
+    """Shapes whose sums are cut into shares, joined in a cluster or by a kernel."""
+    (a, sa), (b, sb) = integers(m, k, 1, -128), integers(n, k, 2, -128)
+    x, w = matrix(a, sa), matrix(b, sb)
+    want = ref.product(a, sa, b, sb, F32)
+    for _ in range(2):
+        same(sg.int8_gemm(x, w), want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("scale", [2.0 ** -14, 2.0 ** -20, 2.0 ** -24, 2.0 ** 8, 2.0 ** -100, 2.0 ** 100])
+def test_gradients_far_from_one(dtype, scale):
+    """Units and gradients at the ends of their types: tokens of one value each, so that dW is dY times it, exactly."""
+    if dtype == F16 and not 2.0 ** -24 <= scale <= 2.0 ** 8:
+        pytest.skip("beyond 16-bit floats of five exponent bits")
+    x = torch.eye(40, 64, dtype=F32, device="cuda") * scale
+    x[:, 40:] = 0
+    dy = values(40, 90, dtype, 3, 0, 1.0 / 64)
+    factor = 2.0 ** 10 if scale < 1 else 2.0 ** -6           # and the product far from the type's ends
+    dy = (dy.float() * factor).to(dtype)
+    dw = sg.int8_weight_grad(dy, sg.int8_checkpoint(x.to(dtype)), out_dtype=F32)
+    same(dw[:, :40], (dy.float() * scale).t())
+    if dtype != F16:
+        # Large times small.  The last of a 32-bit gradient's terms ends where bfloat16 does, at 2^-133: what a gradient has
+        # below that is cut off, less than 2^-133 of it, which the one product multiplies by the kept value.
+        tiny = (dy.float() / scale * 2.0 ** -4).to(dtype)
+        dw = sg.int8_weight_grad(tiny, sg.int8_checkpoint(x.to(dtype)), out_dtype=F32)[:, :40]
+        assert ((dw.double() - tiny.double().t() * scale).abs() <= (2.0 ** -133 * scale if dtype == F32 else 0.0)).all()
+
+
+def test_subnormal_gradients():
+    x = torch.eye(20, 32, dtype=F16, device="cuda") * 512
+    dy = (torch.arange(20 * 16, device="cuda").view(20, 16) - 150).half() * 2.0 ** -24
+    same(sg.int8_weight_grad(dy, sg.int8_checkpoint(x), out_dtype=F32)[:, :20], dy.float().t() * 512)
+
+
 # ------------------------------------------------------- what lies beside a call
 def test_codes_behind_a_row_are_not_used():
     """Rows of 33 bytes in 48: the other 15 hold anything."""

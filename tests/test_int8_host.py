@@ -123,7 +123,7 @@ def test_gradients_are_checked(lib):
 
 
 def test_too_many_tokens_are_refused(lib):
-    c = int8._Checkpoint(1, 0, (1 << 29) + 1, 32, 1 << 28, 1 << 30, 1 << 27, 1 << 30)
+    c = int8._Checkpoint(1, 0, (1 << 27) + 1, 32, 1 << 28, 1 << 30, 1 << 27, 1 << 30)
     assert lib.int8_weight_grad(1 << 40, 8, 8, at(c), 1, 0, 1 << 41, 32, 0) == UNSUPPORTED
     c = int8._Checkpoint(1, 0, 32, 32, 1 << 28, 32, 1 << 27, 32)
     assert lib.int8_weight_grad(1 << 40, 1 << 30, (1 << 29) + 1, at(c), 1, 0, 1 << 45, 32, 0) == UNSUPPORTED

@@ -19,6 +19,7 @@ recorded on them, so they may be dropped once the call returned.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -44,6 +45,9 @@ class _Checkpoint(ctypes.Structure):
                 ("units", ctypes.c_void_p), ("ld_units", ctypes.c_int64)]
 
 
+# The same structures as bytes, which the calls take where a structure is made at each of them.
+_pack_matrix = struct.Struct("@qqQqQ").pack
+_pack_checkpoint = struct.Struct("@iiqqQqQq").pack
 _lib = None
 
 
@@ -99,7 +103,7 @@ class Int8Matrix:
     Made by :func:`int8_quantize` or, from a checkpoint's arrays, by :func:`int8_matrix`.
     """
 
-    __slots__ = ("shape", "device", "index", "_memory", "_arrays", "_c", "_ref", "__weakref__")
+    __slots__ = ("shape", "device", "index", "_memory", "_arrays", "_ref", "__weakref__")
 
     def __init__(self, rows, cols, device="cuda", stream=None):
         device = _cuda_device(device)
@@ -108,8 +112,7 @@ class Int8Matrix:
         memory = _empty((rows * (pitch + 4),), torch.uint8, device, stream)
         self.shape, self.device, self.index, self._memory, self._arrays = (rows, cols), device, device.index, (memory,), None
         base = memory.data_ptr()
-        self._c = c = _Matrix(rows, cols, base, pitch, base + rows * pitch)
-        self._ref = ctypes.addressof(c)
+        self._ref = _pack_matrix(rows, cols, base, pitch, base + rows * pitch)
 
     @classmethod
     def _of(cls, codes, scales):
@@ -120,8 +123,7 @@ class Int8Matrix:
         self.shape, self.device, self.index, self._memory, self._arrays = (
             (rows, cols), codes.device, codes.get_device(), (codes, scales), (codes, scales))
         ld = codes.stride(0) if rows > 1 else (cols + 15) // 16 * 16
-        self._c = _Matrix(rows, cols, codes.data_ptr(), ld, scales.data_ptr())
-        self._ref = ctypes.addressof(self._c)
+        self._ref = _pack_matrix(rows, cols, codes.data_ptr(), ld, scales.data_ptr())
         return self
 
     def _views(self):
@@ -277,7 +279,7 @@ class Int8Checkpoint:
     ``include/int8.h`` describes, ``nbytes`` their size.
     """
 
-    __slots__ = ("shape", "dtype", "order", "device", "index", "_memory", "_split", "_c", "_ref", "__weakref__")
+    __slots__ = ("shape", "dtype", "order", "device", "index", "_memory", "_start", "_ref", "__weakref__")
 
     def __init__(self, rows, cols, dtype, order, device="cuda", stream=None):
         if order not in ORDERS:
@@ -287,26 +289,26 @@ class Int8Checkpoint:
 
     def _set(self, rows, cols, dtype, number, order, device, lines, memory, start):
         self.shape, self.dtype, self.order, self.device, self.index = (rows, cols), dtype, order, device, device.index
-        self._memory, self._split = memory, (start, *lines)
+        self._memory, self._start = memory, start
         base = memory.data_ptr() + start
-        self._c = c = _Checkpoint(number, 0 if order == "channels" else 1, rows, cols, base, lines[1], base + lines[0] * lines[1], lines[3])
-        self._ref = ctypes.addressof(c)
+        self._ref = _pack_checkpoint(number, 0 if order == "channels" else 1, rows, cols, base, lines[1],
+                                     base + lines[0] * lines[1], lines[3])
         return self
 
     @property
     def codes(self):
         """The integers, int8 (lines x pitch)."""
-        start, lines, ld, _, _ = self._split
-        return self._memory[start:start + lines * ld].view(torch.int8).view(lines, ld)
+        lines, ld, _, _ = _lines(self.order, *self.shape)
+        return self._memory[self._start:self._start + lines * ld].view(torch.int8).view(lines, ld)
 
     @property
     def units(self):
         """The blocks' units (lines x pitch), bfloat16 or float16."""
-        start, lines, ld, unit_lines, ldu = self._split
-        kind, start = torch.float16 if self.dtype == torch.float16 else torch.bfloat16, start + lines * ld
+        lines, ld, unit_lines, ldu = _lines(self.order, *self.shape)
+        kind, start = torch.float16 if self.dtype == torch.float16 else torch.bfloat16, self._start + lines * ld
         return self._memory[start:start + 2 * unit_lines * ldu].view(kind).view(unit_lines, ldu)
 
-    nbytes = property(lambda self: _bytes(self._split[1:]))
+    nbytes = property(lambda self: _bytes(_lines(self.order, *self.shape)))
 
     def restore(self, dtype=None):
         """The values (:func:`int8_restore`)."""
@@ -333,7 +335,9 @@ def int8_checkpoint(x, out=None, stream=None):
     """
     ld, rows, cols = _dense(x, "x")
     if out is None:
-        out = Int8Checkpoint(rows, cols, x.dtype, "channels", x.device, stream)
+        lines, device = _lines("channels", rows, cols), x.device
+        out = Int8Checkpoint.__new__(Int8Checkpoint)._set(rows, cols, x.dtype, _DTYPES[x.dtype], "channels", device, lines,
+                                                          _empty((_bytes(lines),), torch.uint8, device, stream), 0)
     else:
         if _kept(out, "out", "channels").shape != (rows, cols) or out.dtype != x.dtype:
             raise ValueError(f"out is {out}, expected {(rows, cols)} {x.dtype}")
@@ -411,8 +415,8 @@ def int8_swiglu(gate, up, out=None, stream=None):
 def int8_swiglu_backward(dh, kept, out=None, stream=None):
     """(dgate, dup) from h's gradient and the pair that :func:`int8_swiglu` kept.
 
-    ``out``, a pair of matrices (halves of one tensor, for instance), receives
-    them if given; by default they are the halves of one new tensor.
+    ``out``, a pair of matrices (the halves of one projection's gradient, for
+    instance), receives them if given.
     """
     if not isinstance(kept, (tuple, list)) or len(kept) != 2:
         raise TypeError("kept must be the pair that int8_swiglu returned")
@@ -424,10 +428,8 @@ def int8_swiglu_backward(dh, kept, out=None, stream=None):
         raise ValueError(f"dh must be {g.shape} {g.dtype}, got {tuple(dh.shape)} {dh.dtype}")
     _same_device(g.index, u, dh)
     if out is None:
-        cols = g.shape[1]
-        both = _empty((rows, 2 * cols), g.dtype, g.device, stream)
-        dgate, dup = both.as_strided((rows, cols), (2 * cols, 1)), both.as_strided((rows, cols), (2 * cols, 1), cols)
-        ldg = ldu = 2 * cols or 1
+        dgate, dup = _empty(g.shape, g.dtype, g.device, stream), _empty(g.shape, g.dtype, g.device, stream)
+        ldg = ldu = g.shape[1] or 1
     elif not isinstance(out, (tuple, list)) or len(out) != 2:
         raise TypeError("out must be a pair of tensors")
     else:

@@ -50,6 +50,13 @@ def at(s):
     return ctypes.addressof(s)
 
 
+def test_structures_as_bytes():
+    m = matrix(3, 70, P_Q, 80, P_S)
+    assert int8._pack_matrix(3, 70, P_Q, 80, P_S) == bytes(m)
+    c = kept(2, 1, 9, 100)
+    assert int8._pack_checkpoint(2, 1, 9, 100, P_Q, c.ld, P_S, c.ld_units) == bytes(c)
+
+
 @pytest.mark.parametrize("q,dtype,x,ldx,want", [
     (matrix(), 3, P_X, 64, BAD), (matrix(), -1, P_X, 64, BAD), (matrix(), 0, 0, 64, BAD), (matrix(), 0, P_X, 63, BAD),
     (matrix(), 0, P_X + 2, 64, BAD), (matrix(rows=-1), 0, P_X, 64, BAD), (matrix(codes=0), 0, P_X, 64, BAD),

@@ -224,17 +224,21 @@ struct BackArgs {
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const BackArgs a) {
   begin();
+  __shared__ __align__(16) float scratch_[kVec ? 4 : 8 * kThreads];
+  float* const scratch = scratch_ + (kVec ? 0 : threadIdx.x / 32 * 256);
   for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
-    if (!w.at(a.n, 0, row, c)) break;
-    const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
-    const float s = a.scales[row];
-    float v[8];
-    widen4(q.x, v);
-    widen4(q.y, v + 4);
+    const bool here = w.at(a.n, 0, row, c);
+    float v[8] = {};
+    if (here) {
+      const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
+      const float s = a.scales[row];
+      widen4(q.x, v);
+      widen4(q.y, v + 4);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= s;
-    store8<kVec>(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, a.cols - 8 * c, v);
+      for (int e = 0; e < 8; ++e) v[e] *= s;
+    }
+    write8<kVec>(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, here ? a.cols - 8 * c : 0, scratch, v);
   }
 }
 
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
           *reinterpret_cast<uint4*>(out + t * a.rows * a.ld) = term;
         }
       } else {
-        store8<true>(reinterpret_cast<T*>(out), 8, v[j]);
+        store8(reinterpret_cast<T*>(out), v[j]);
       }
     }
   }
@@ -435,17 +439,21 @@ struct RestoreArgs {
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) restore_tokens_kernel(const RestoreArgs a) {
   begin();
+  __shared__ __align__(16) float scratch_[kVec ? 4 : 8 * kThreads];
+  float* const scratch = scratch_ + (kVec ? 0 : threadIdx.x / 32 * 256);
   for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
-    if (!w.at(a.n, 0, row, c)) break;
-    const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
-    const float u = unit_value(a.units[row * a.ldu + c / 4], a.half);
-    float v[8];
-    widen4(q.x, v);
-    widen4(q.y, v + 4);
+    const bool here = w.at(a.n, 0, row, c);
+    float v[8] = {};
+    if (here) {
+      const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
+      const float u = unit_value(a.units[row * a.ldu + c / 4], a.half);
+      widen4(q.x, v);
+      widen4(q.y, v + 4);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= u;
-    store8<kVec>(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, a.cols - 8 * c, v);
+      for (int e = 0; e < 8; ++e) v[e] *= u;
+    }
+    write8<kVec>(static_cast<T*>(a.out) + row * a.ld_out + 8 * c, here ? a.cols - 8 * c : 0, scratch, v);
   }
 }
 
@@ -454,6 +462,8 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(128) restore_channels_kernel(const RestoreArgs a) {
   begin();
   __shared__ int8_t tile[32][68];
+  __shared__ __align__(16) float scratch_[kVec ? 4 : 8 * 128];
+  float* const scratch = scratch_ + (kVec ? 0 : threadIdx.x / 32 * 256);
   const int64_t blocks = (a.cols + 31) / 32, tiles = (a.rows + 63) / 64 * blocks;
   for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
     const int64_t t0 = i / blocks * 64, b = i % blocks;
@@ -466,13 +476,12 @@ __global__ void __launch_bounds__(128) restore_channels_kernel(const RestoreArgs
     __syncthreads();
     for (int j = threadIdx.x; j < 256; j += 128) {
       const int t = j / 4, c = j % 4;
-      if (t0 + t < a.rows && 32 * b + 8 * c < a.cols) {
-        const float u = unit_value(a.units[b * a.ldu + t0 + t], a.half);
-        float v[8];
+      const bool here = t0 + t < a.rows;
+      const float u = here ? unit_value(a.units[b * a.ldu + t0 + t], a.half) : 0.f;
+      float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = float(tile[8 * c + e][t]) * u;
-        store8<kVec>(static_cast<T*>(a.out) + (t0 + t) * a.ld_out + 32 * b + 8 * c, a.cols - 32 * b - 8 * c, v);
-      }
+      for (int e = 0; e < 8; ++e) v[e] = float(tile[8 * c + e][t]) * u;
+      write8<kVec>(static_cast<T*>(a.out) + (t0 + t) * a.ld_out + 32 * b + 8 * c, here ? a.cols - 32 * b - 8 * c : 0, scratch, v);
     }
     __syncthreads();
   }
@@ -522,6 +531,8 @@ __device__ __forceinline__ void keep_block(const float (&v)[8], int8_t* codes, u
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
   begin();
+  __shared__ __align__(16) float scratch_[kVec ? 4 : 8 * kThreads];
+  float* const scratch = scratch_ + (kVec ? 0 : threadIdx.x / 32 * 256);
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
   const int64_t blocks = (a.cols + 31) / 32;
   for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
@@ -535,7 +546,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = g[e] * sigmoid<T>(g[e]) * u[e];
-    if (left > 0) store8<kVec>(static_cast<T*>(a.h) + row * a.ldh + 8 * c, left, h);
+    write8<kVec>(static_cast<T*>(a.h) + row * a.ldh + 8 * c, left, scratch, h);
     const bool write = here && 8 * c < (a.cols + 15) / 16 * 16;
     keep_block<kHalf>(g, a.kg + row * a.ldkg + 8 * c, a.ug + row * a.ldug + c / 4, c % 4 == 0, write);
     keep_block<kHalf>(u, a.ku + row * a.ldku + 8 * c, a.uu + row * a.lduu + c / 4, c % 4 == 0, write);
@@ -550,15 +561,21 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluA
                                                                    int64_t lddg, T* dup, int64_t lddu) {
   begin();
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
+  __shared__ __align__(16) float scratch_[kVec ? 4 : 8 * kThreads];
+  float* const scratch = scratch_ + (kVec ? 0 : threadIdx.x / 32 * 256);
   for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
-    if (!w.at(a.n, 0, row, c)) break;
-    const int64_t left = a.cols - 8 * c;
-    const uint2 wg = *reinterpret_cast<const uint2*>(a.kg + row * a.ldkg + 8 * c);
-    const uint2 wu = *reinterpret_cast<const uint2*>(a.ku + row * a.ldku + 8 * c);
-    const float ug = unit_value(a.ug[row * a.ldug + c / 4], kHalf), uu = unit_value(a.uu[row * a.lduu + c / 4], kHalf);
-    float d[8], g[8], u[8];
-    load8<kVec>(dh + row * lddh + 8 * c, left, d);
+    const bool here = w.at(a.n, 0, row, c);
+    const int64_t left = here ? a.cols - 8 * c : 0;
+    float d[8] = {}, g[8], u[8];
+    uint2 wg = make_uint2(0, 0), wu = wg;
+    float ug = 0.f, uu = 0.f;
+    if (here) {
+      wg = *reinterpret_cast<const uint2*>(a.kg + row * a.ldkg + 8 * c);
+      wu = *reinterpret_cast<const uint2*>(a.ku + row * a.ldku + 8 * c);
+      ug = unit_value(a.ug[row * a.ldug + c / 4], kHalf), uu = unit_value(a.uu[row * a.lduu + c / 4], kHalf);
+      load8<kVec>(dh + row * lddh + 8 * c, left, d);
+    }
     widen4(wg.x, g), widen4(wg.y, g + 4);
     widen4(wu.x, u), widen4(wu.y, u + 4);
 #pragma unroll
@@ -567,8 +584,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluA
       g[e] = d[e] * (u[e] * uu) * s * (1.f + x * (1.f - s));
       u[e] = d[e] * (x * s);
     }
-    store8<kVec>(dgate + row * lddg + 8 * c, left, g);
-    store8<kVec>(dup + row * lddu + 8 * c, left, u);
+    write8<kVec>(dgate + row * lddg + 8 * c, left, scratch, g);
+    write8<kVec>(dup + row * lddu + 8 * c, left, scratch, u);
   }
 }
 

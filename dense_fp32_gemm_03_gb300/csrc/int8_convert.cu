@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(
     __shared__ float warps[kGroup / 32];
     if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = top;
     __syncthreads();
-    top = warps[threadIdx.x % (kGroup / 32)];
+    top = warps[threadIdx.x % 32 % (kGroup / 32)];  // (each of them in some lane)
 #pragma unroll
-    for (int d = kGroup / 64; d; d /= 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, d));
+    for (int d = 16; d; d /= 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, d));
   }
   const float s = row_scale(top), inv = __frcp_rn(s);
   if (t == 0) a.scales[row] = s;
@@ -169,7 +169,9 @@ bool whole(int64_t cols, bool aligned) { return aligned && cols % 8 == 0; }
 template <typename T, RowForm kForm, bool kVec>
 cudaError_t launch_rows_of(const RowArgs& a, cudaStream_t stream) {
   if (a.cols <= 1024) return launch(rows_kernel<T, 32, kForm, kVec>, (a.rows + kThreads / 32 - 1) / (kThreads / 32), kThreads, stream, a);
+  if (a.cols <= 2048) return launch(rows_kernel<T, 64, kForm, kVec>, a.rows, 64, stream, a);
   if (a.cols <= 4096) return launch(rows_kernel<T, 128, kForm, kVec>, a.rows, 128, stream, a);
+  if (a.cols <= 6144) return launch(rows_kernel<T, 192, kForm, kVec>, a.rows, 192, stream, a);
   if (a.cols <= 8192) return launch(rows_kernel<T, 256, kForm, kVec>, a.rows, 256, stream, a);
   return launch(rows_kernel<T, 1024, kForm, kVec>, a.rows, 1024, stream, a);
 }

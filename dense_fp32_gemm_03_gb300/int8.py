@@ -97,6 +97,11 @@ def _type(dtype, name="dtype"):
 
 
 # ------------------------------------------------------------------------- rows
+def _pitch(cols):
+    """Bytes of a row that is allocated here: a multiple of 16, long ones of 128 (whole lines of memory)."""
+    return (cols + 127) // 128 * 128 if cols > 2048 else (cols + 15) // 16 * 16
+
+
 class Int8Matrix:
     """Rows of integers with a scale each, on the GPU: ``shape``, ``device``, ``codes`` (int8, rows x cols), ``scales`` (float32).
 
@@ -108,7 +113,7 @@ class Int8Matrix:
     def __init__(self, rows, cols, device="cuda", stream=None):
         device = _cuda_device(device)
         # One allocation: the codes, then the scales.
-        pitch = (cols + 15) // 16 * 16
+        pitch = _pitch(cols)
         memory = _empty((rows * (pitch + 4),), torch.uint8, device, stream)
         self.shape, self.device, self.index, self._memory, self._arrays = (rows, cols), device, device.index, (memory,), None
         base = memory.data_ptr()
@@ -129,7 +134,7 @@ class Int8Matrix:
     def _views(self):
         if self._arrays is None:
             (rows, cols), memory = self.shape, self._memory[0]
-            pitch = (cols + 15) // 16 * 16
+            pitch = _pitch(cols)
             self._arrays = (memory[:rows * pitch].view(torch.int8).view(rows, pitch)[:, :cols],
                             memory[rows * pitch:].view(torch.float32))
         return self._arrays
@@ -196,7 +201,7 @@ def int8_matrix(codes, scales, stream=None):
         if codes.data_ptr() % 16 or (cols > 1 and codes.stride(1) != 1) or (
                 rows > 1 and (codes.stride(0) % 16 or codes.stride(0) < pitch)) or (
                 rows and size < (rows - 1) * codes.stride(0) + pitch):
-            memory = torch.zeros((rows, pitch), dtype=torch.int8, device=device)
+            memory = torch.zeros((rows, _pitch(cols)), dtype=torch.int8, device=device)
             memory[:, :cols].copy_(codes)
             codes = memory[:, :cols]
         return Int8Matrix._of(codes, scales.contiguous())

@@ -517,43 +517,60 @@ __device__ __forceinline__ float sigmoid(float x) {
   }
 }
 
-// Keeps eight of a block's values (the four lanes of a block together).
-template <bool kHalf>
-__device__ __forceinline__ void keep_block(const float (&v)[8], int8_t* codes, uint16_t* unit, bool first, bool write) {
-  float top = largest8(v), t[8];
+// Keeps kN of a block's values (the block's 32 / kN lanes together).
+template <bool kHalf, int kN>
+__device__ __forceinline__ void keep_block(const float (&v)[kN / 8][8], int8_t* codes, uint16_t* unit, bool first, bool write) {
+  float top = largest8(v[0]), t[8];
+  if constexpr (kN > 8) top = max_abs(top, largest8(v[1]));
   top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  if constexpr (kN == 8) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const Unit of = unit_of<kHalf>(top);
-  keep8(v, top, of.inverse, t);
-  if (write) *reinterpret_cast<uint2*>(codes) = pack8(t);
+  uint2 w[kN / 8];
+#pragma unroll
+  for (int p = 0; p < kN / 8; ++p) {
+    keep8(v[p], top, of.inverse, t);
+    w[p] = pack8(t);
+  }
+  if constexpr (kN == 8) {
+    if (write) *reinterpret_cast<uint2*>(codes) = w[0];
+  } else {
+    if (write) *reinterpret_cast<uint4*>(codes) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+  }
   if (write && first) *unit = uint16_t(of.bits);
 }
 
-// Four lanes to a block; a row's columns are rounded up to whole blocks so that a block's lanes stay together.
-template <typename T, bool kVec>
+// 32 / kN lanes to a block; a row's columns are rounded up to whole blocks so that a block's lanes stay together.
+template <typename T, bool kVec, int kN>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
   begin();
   __shared__ __align__(16) float scratch_[kVec ? 4 : 8 * kThreads];
   float* const scratch = scratch_ + (kVec ? 0 : threadIdx.x / 32 * 256);
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
+  constexpr int kLanes = 32 / kN;
   const int64_t blocks = (a.cols + 31) / 32;
   for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
     const bool here = w.at(a.n, 0, row, c);
-    const int64_t left = here ? a.cols - 8 * c : 0;
-    float g[8] = {}, u[8] = {}, h[8];
+    const int64_t left = here ? a.cols - kN * c : 0;
+    float g[kN / 8][8] = {}, u[kN / 8][8] = {}, h[8];
     if (left > 0) {
-      load8<kVec>(static_cast<const T*>(a.gate) + row * a.ldg + 8 * c, left, g);
-      load8<kVec>(static_cast<const T*>(a.up) + row * a.ldu + 8 * c, left, u);
+#pragma unroll
+      for (int p = 0; p < kN / 8; ++p) {
+        load8<kVec>(static_cast<const T*>(a.gate) + row * a.ldg + kN * c + 8 * p, left, g[p]);
+        load8<kVec>(static_cast<const T*>(a.up) + row * a.ldu + kN * c + 8 * p, left, u[p]);
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = g[e] * sigmoid<T>(g[e]) * u[e];
-    write8<kVec>(static_cast<T*>(a.h) + row * a.ldh + 8 * c, left, scratch, h);
-    const bool write = here && 8 * c < (a.cols + 15) / 16 * 16;
-    keep_block<kHalf>(g, a.kg + row * a.ldkg + 8 * c, a.ug + row * a.ldug + c / 4, c % 4 == 0, write);
-    keep_block<kHalf>(u, a.ku + row * a.ldku + 8 * c, a.uu + row * a.lduu + c / 4, c % 4 == 0, write);
+    for (int p = 0; p < kN / 8; ++p) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = g[p][e] * sigmoid<T>(g[p][e]) * u[p][e];
+      write8<kVec>(static_cast<T*>(a.h) + row * a.ldh + kN * c + 8 * p, left, scratch, h);
+    }
+    const bool write = here && kN * c < (a.cols + 15) / 16 * 16;
+    keep_block<kHalf, kN>(g, a.kg + row * a.ldkg + kN * c, a.ug + row * a.ldug + c / kLanes, c % kLanes == 0, write);
+    keep_block<kHalf, kN>(u, a.ku + row * a.ldku + kN * c, a.uu + row * a.lduu + c / kLanes, c % kLanes == 0, write);
     // Units that pad the row.
-    if (here && c % 4 == 0 && c / 4 == blocks - 1)
+    if (here && c % kLanes == 0 && c / kLanes == blocks - 1)
       for (int64_t b = blocks; b < (blocks + 7) / 8 * 8; ++b) a.ug[row * a.ldug + b] = a.uu[row * a.lduu + b] = 0;
   }
 }
@@ -673,10 +690,15 @@ cudaError_t launch_int8_swiglu(int dtype, int64_t M, int64_t F, const void* gate
                                int64_t ldu, void* h, int64_t ldh, const int8_checkpoint_t& kg,
                                const int8_checkpoint_t& ku, int sms, cudaStream_t stream) {
   const int64_t es = bytes_of(dtype);
-  const SwigluArgs a{gate, up, ldg, ldu, M, F, h, ldh, kg.codes, ku.codes, kg.ld, ku.ld, kg.units, ku.units,
-                     kg.ld_units, ku.ld_units, chunks_of(M, (F + 31) / 32 * 4, sms)};
   const bool vec = whole(F, aligned16(gate, ldg * es) && aligned16(up, ldu * es) && aligned16(h, ldh * es));
-  GB300_INT8_BY_TYPE(dtype, launch(vec ? swiglu_kernel<T, true> : swiglu_kernel<T, false>, blocks_of(a.n), kThreads, stream, a))
+  // 16 of a row's values a thread halve what it spends on addresses and on the block's largest (8192 x 8192 bf16 92 -> 82 us;
+  // back, where there is less of that, 83 -> 86), where that leaves a block to each SM (33 x 1024: 1.9 -> 2.3 us).
+  const int n = vec && es == 2 && F % 16 == 0 && M * F >= int64_t(sms) * kThreads * 16 ? 16 : 8;
+  const SwigluArgs a{gate, up, ldg, ldu, M, F, h, ldh, kg.codes, ku.codes, kg.ld, ku.ld, kg.units, ku.units,
+                     kg.ld_units, ku.ld_units, chunks_of(M, (F + 31) / 32 * (32 / n), sms)};
+  GB300_INT8_BY_TYPE(dtype, launch(n == 16 ? swiglu_kernel<T, true, sizeof(T) == 2 ? 16 : 8>
+                                           : vec ? swiglu_kernel<T, true, 8> : swiglu_kernel<T, false, 8>,
+                                   blocks_of(a.n), kThreads, stream, a))
 }
 
 cudaError_t launch_int8_swiglu_backward(const void* dh, int64_t lddh, const int8_checkpoint_t& kg,

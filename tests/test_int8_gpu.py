@@ -403,6 +403,26 @@ def test_swiglu_and_its_gradients(dtype, rows, cols, pad):
     finish()
 
 
+@pytest.mark.parametrize("dtype", (BF16, F16))
+@pytest.mark.parametrize("rows,cols,pad", [(700, 912, 16), (39000, 16, 0), (1, 655376, 0)])
+def test_swiglu_of_many_values(dtype, rows, cols, pad):
+    """Sizes where a thread takes 16 values: blocks of 16 at the end of a row, a block that is not finite."""
+    both = values(rows, 2 * cols, dtype, 17, pad, 2.0)
+    gate, up = both[:, :cols], both[:, cols:]
+    both[rows // 2, 3], both[rows // 2, cols + 11] = float("nan"), float("inf")
+    h, kept = sg.int8_swiglu(gate, up)
+    g, u = ref.array(gate), ref.array(up)
+    bad = ~np.isfinite(g * u)
+    got = h.double().cpu().numpy()
+    assert bad.sum() == 2 and np.isnan(got[rows // 2, 3]) and np.isinf(got[rows // 2, 11])
+    for c, v in zip(kept, (g, u)):
+        check_layout(c, *ref.keep(v, dtype == F16))
+    h[torch.tensor(bad)] = 0
+    g[bad] = u[bad] = 0
+    near(h, ref.swiglu(g, u), swiglu_bounds(g, g, u, dtype)[0], dtype)
+    finish()
+
+
 def test_swiglu_far_from_zero():
     g = torch.tensor([[0.0, 100.0, -100.0, 88.0, -88.0, 1e30, -1e30, -60.0, float("inf"), 20.0, -0.0, 3.4e38]]).cuda()
     u = torch.full_like(g, 2.0)

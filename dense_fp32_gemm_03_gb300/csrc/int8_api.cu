@@ -153,12 +153,14 @@ struct Operands {
 };
 
 // The tiles, and the shares that k is cut into where there are fewer tiles than pairs of CTAs, that are estimated to
-// be fastest (us, fitted to GB300 timings).  A stage of 128 of k takes its MMAs, 0.53 for 256 columns and 0.34 for 128
-// or fewer (reading `a` from tensor memory takes as long), which is also what turning `a` to 16 bits takes; a
-// tile fills and empties the pipeline (1.5); shares are written, and read by a kernel that adds them (4.5, and
-// 4 bytes each way at 4 TB/s), or joined within a cluster (1).  Equal ones: the narrower tiles, which read less of b.
+// be fastest (us, fitted to 41 products timed with every choice: the chosen ones are within 4 % of the best, and within
+// 5 % in 31 others).  A stage of
+// 128 of k takes its MMAs, 0.53 for 256 columns and 0.28 for 128 or fewer (reading `a` from tensor memory takes as long),
+// and at least what turning `a` to 16 bits takes, 0.37 with a checkpoint's units; a tile fills and empties the pipeline
+// (1.5), and the last one is stored.  Shares meet within a cluster, or are written and added by a kernel of its own, 4 bytes
+// each way: 16.6 and 14.2 us for 4096 x 1024 x 1024 bf16, one share 18.4.  Equal ones: the narrower tiles, which read less of b.
 sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t rows, int64_t cols, int64_t depth, int terms,
-                    const gb300::Int8TcClusters& most, gb300::Int8TcArgs* a, gb300::Int8TcShape* best) {
+                    bool units, const gb300::Int8TcClusters& most, gb300::Int8TcArgs* a, gb300::Int8TcShape* best) {
   const int64_t steps = round_up(depth, gb300::int8_tc_step()) / gb300::int8_tc_step(), tr = (rows + 255) / 256;
   const int64_t pairs = most.pairs;
   if (pairs <= 0) return SGEMM_ERR_LAUNCH;
@@ -172,10 +174,11 @@ sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t ro
   for (const gb300::Int8TcShape shape : shapes) {
     const int64_t n = gb300::int8_tc_cols(shape), tc = (cols + n - 1) / n, tiles = tr * tc;
     if (tiles > 0x3fffffffLL) continue;
-    const double stage = double(terms) * std::max(0.34, double(n) * (0.53 / 256));
+    const double stage = std::max(units ? 0.37 : 0.0, double(terms) * std::max(0.28, double(n) * (0.53 / 256)));
+    const double last = std::min(3.0, 0.02 * double(n - 32));
     auto consider = [&](int64_t splits, bool join) {
-      const double us = double((tiles * splits + pairs - 1) / pairs) * (double((steps + splits - 1) / splits) * stage + 1.5) +
-                        (join ? 1.0 : splits > 1 ? 4.5 + double(splits) * double(rows) * double(cols) * 2e-6 : 0.0);
+      const double us = double((tiles * splits + pairs - 1) / pairs) * (double((steps + splits - 1) / splits) * stage + 1.5) + last +
+                        (join ? 0.3 + 0.25 * double(splits) : splits > 1 ? 2.5 + double(splits) * double(rows) * double(cols) * 1e-6 : 0.0);
       if (least > 0.0 && us >= least) return;
       least = us;
       *best = shape;
@@ -252,7 +255,7 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
   const gb300::Int8TcClusters most = tc_clusters(d.dev);
   gb300::Int8TcArgs a{};
   gb300::Int8TcShape shape{};
-  sgemm_status_t st = plan({gb300::kInt8Whole32, gb300::kInt8Whole64, gb300::kInt8Whole128}, B.rows, M, B.cols, 1, most, &a, &shape);
+  sgemm_status_t st = plan({gb300::kInt8Whole32, gb300::kInt8Whole64, gb300::kInt8Whole128}, B.rows, M, B.cols, 1, false, most, &a, &shape);
   if (st != SGEMM_OK) return st;
   const int64_t ld16 = round_up(B.cols, 64);  // whole lines of 128 bytes (16384 x 1024 x 4104: 166 us in multiples of 8, 143)
   Scratch s;
@@ -401,10 +404,10 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   gb300::Int8TcShape shape{};
   const bool half = c->dtype == INT8_F16;
   if (dtype == INT8_F32)
-    st = plan({half ? gb300::kInt8F16Runs : gb300::kInt8Bf16Runs}, c->cols, N, c->rows, terms, most, &a, &shape);
+    st = plan({half ? gb300::kInt8F16Runs : gb300::kInt8Bf16Runs}, c->cols, N, c->rows, terms, true, most, &a, &shape);
   else
     st = plan({half ? gb300::kInt8F16N128 : gb300::kInt8Bf16N128, half ? gb300::kInt8F16N256 : gb300::kInt8Bf16N256}, c->cols, N, c->rows,
-              terms, most, &a, &shape);
+              terms, true, most, &a, &shape);
   if (st != SGEMM_OK) return st;
   a.run = 512 / gb300::int8_tc_step();
   const bool in_place = terms == 1 && aligned(dy, 16) && (lddy % 8 == 0 || c->rows == 1);

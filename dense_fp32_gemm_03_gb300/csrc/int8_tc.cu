@@ -22,6 +22,9 @@
 //    bits of `a` where 16 would pass twice, and no pass over `a` comes before;
 //  * warp 2 of the pair's first CTA issues the MMAs;
 //  * eight warps read a finished accumulator while the next one is filled.
+// Where there are few tiles, pairs of one cluster take shares of k, and each adds up its part of the columns from the others'
+// accumulators through shared memory: weight gradient 4096 x 1024 x 1024 bf16 14.2 us, with the shares written and added by
+// join_kernel 16.6 (16384 tokens, 512 x 512, 20.4 and 16.8: more than four shares are left to that).
 // Lanes are rows of D, which is stored as columns (out[c * ld + r]): a warp's 32
 // values of a column are consecutive.
 //
@@ -31,7 +34,7 @@
 // have one accumulator, so that a tile's (or a run's) sums are read before the next one's first product; that costs
 // little after the 128 stages of a gradient's tile, and much after the 8 of a run, so products of integers have 128 columns
 // and two accumulators.  With the first operand in tensor memory an MMA of 32 or 64 columns takes as long as one of 128
-// (0.34 us a stage): small tiles only spread few columns over more SMs.
+// (0.28 us a stage, 0.34 on every SM at once): small tiles only spread few columns over more SMs.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -73,15 +76,15 @@ struct Tile {
   static constexpr int kSlotCols = kStep / 2;  // tensor memory columns of a stage of `a`
   static constexpr int kSlots0 = (512 - kAccs * kN) / kSlotCols;
   static constexpr int kSlots = kSlots0 < 6 ? kSlots0 : 6;
-  // Narrow tiles' shares of k, of up to four pairs in a cluster, meet in the first pair's shared memory.
-  static constexpr int kMaxShares = kN == 32 ? 4 : 1;
-  static constexpr uint32_t kShareBytes = kRows * kN * 4, kJoinBytes = (kMaxShares - 1) * kShareBytes;
-  static constexpr int kStages0 = int((232448 - 1024 - 512 - kJoinBytes) / (kABytes + kUBytes + kBBytes));
+  // Shares of k of up to four pairs in a cluster meet where the stages were: each pair adds up its part of the columns.
+  static constexpr int kMaxShares = kN <= 128 ? 4 : 1;  // (a warp's sums are in registers then)
+  static constexpr int kStages0 = int((232448 - 1024 - 512) / (kABytes + kUBytes + kBBytes));
   static constexpr int kStages = kStages0 < 8 ? kStages0 : 8;
   static constexpr int kThreads = 128 * (3 + kGroups);
   static constexpr int kV = kN / 2;  // columns of an epilogue warp
   static constexpr int kBarriers = 4 * kStages + 2 * kSlots + 2 * kAccs + 1;
-  static constexpr size_t kSmem = 1024 + kStages * size_t(kABytes + kUBytes + kBBytes) + kJoinBytes + kBarriers * 8 + 16;
+  static constexpr size_t kSmem = 1024 + kStages * size_t(kABytes + kUBytes + kBBytes) + kBarriers * 8 + 16;
+  static_assert(kRows * kN * 4 <= kStages * (kABytes + kBBytes), "shares");
   static_assert(kSmem <= 232448 && kAccs * kN + kSlots * kSlotCols <= 512, "memory");
   // 32-bit accumulator; A from tensor memory, B K-major or MN-major (bit 16); M = 256.
   static constexpr uint32_t kDesc = (1u << 4) | (kKind == kBf16 ? (1u << 7) | (1u << 10) : 0u) | (kUnits ? 1u << 16 : 0u) |
@@ -226,6 +229,19 @@ __device__ __forceinline__ void for_stages(const Int8TcArgs& args, const Work& w
   }
 }
 
+template <int kValue>
+struct Int {
+  __device__ constexpr operator int() const { return kValue; }
+};
+// f(0) .. f(kCount - 1), constants.
+template <int kCount, int kFrom = 0, typename F>
+__device__ __forceinline__ void for_parts(F f) {
+  if constexpr (kFrom < kCount) {
+    f(Int<kFrom>());
+    for_parts<kCount, kFrom + 1>(f);
+  }
+}
+
 // Stores kCount columns of a row of D (`out`: the first; `left`: those that exist), added to what is there if asked.
 template <typename T, int kCount>
 __device__ __forceinline__ void put_columns(T* out, int64_t ld, int left, bool add, const float (&v)[kCount]) {
@@ -277,8 +293,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   unsigned char* s_a = smem;
   unsigned char* s_b = s_a + S::kStages * S::kABytes;
   unsigned char* s_u = s_b + S::kStages * S::kBBytes;
-  unsigned char* s_join = s_u + S::kStages * S::kUBytes;
-  uint64_t* a_full = reinterpret_cast<uint64_t*>(s_join + S::kJoinBytes);
+  uint64_t* a_full = reinterpret_cast<uint64_t*>(s_u + S::kStages * S::kUBytes);
   uint64_t* a_empty = a_full + S::kStages;
   uint64_t* b_full = a_empty + S::kStages;     // used in the first CTA
   uint64_t* b_empty = b_full + S::kStages;
@@ -351,7 +366,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 
   // 640 threads have 96 registers each; these four warps give up what the epilogue's sums need.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0) {
       // ---- `a` and its units, of this CTA's rows
       At<S::kStages> s;
@@ -511,7 +526,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     // ---- epilogue: 32 rows x kV columns a warp
     const int q = warp & 3, half = (warp - 4 - 4 * kGroups) >> 2;
     const uint32_t lanes = uint32_t(32 * q) << 16;
@@ -539,73 +554,101 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         if (lane == 0) arrive_at(place_in(&acc_empty[b.i], leader));
         b.next();
       };
-      if constexpr (S::kRuns) {
-        // Scales of this warp's columns, 32 a register; a row's.
-        float scale_c[(S::kV + 31) / 32], scale_r = 0.f;
-        if (S::kKind == kIntegers && (args.splits == 1 || args.join)) {
+      if constexpr (S::kMaxShares > 1) {
+        if (S::kRuns || args.join) {
+          // Scales of this warp's columns, 32 a register; a row's.
+          float scale_c[(S::kV + 31) / 32], scale_r = 0.f;
+          if (S::kKind == kIntegers && (args.splits == 1 || args.join)) {
 #pragma unroll
-          for (int c = 0; c < S::kV; c += 32) scale_c[c / 32] = col0 + c + lane < args.cols ? args.scale_c[col0 + c + lane] : 0.f;
-          if (mine) scale_r = args.scale_r[row];
-        }
-        uint32_t sum[S::kV];
-#pragma unroll
-        for (int c = 0; c < S::kV; ++c) sum[c] = 0;
-        for (int k = w.kb; k < w.ke; k += args.run) {
-          const uint32_t at = acc_wait();
-#pragma unroll
-          for (int c = 0; c < S::kV; c += kPart) {
-            float v[kPart];
-            read_tmem<kPart>(at + c, v);
-#pragma unroll
-            for (int x = 0; x < kPart; ++x)
-              sum[c + x] = S::kKind == kIntegers ? sum[c + x] + uint32_t(__float2int_rn(v[x]))
-                                                 : __float_as_uint(__uint_as_float(sum[c + x]) + v[x]);
+            for (int c = 0; c < S::kV; c += 32) scale_c[c / 32] = col0 + c + lane < args.cols ? args.scale_c[col0 + c + lane] : 0.f;
+            if (mine) scale_r = args.scale_r[row];
           }
-          acc_free();
-        }
-        bool ok = going();
-        if constexpr (S::kMaxShares > 1) {
-          if (args.join) {
-            // The only unit of this pair: its sums go to the first pair, which has them after everybody's barrier.
-            const int at = half * S::kV * kRows + 32 * q + lane;
-            if (w.part != 0 && ok) {
-              const uint32_t to = place_in(s_join + (w.part - 1) * S::kShareBytes, rank) + 4 * at;
+          uint32_t sum[S::kV];
+          if constexpr (S::kRuns) {
 #pragma unroll
-              for (int c = 0; c < S::kV; ++c) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 4 * kRows * c), "r"(sum[c]) : "memory");
+            for (int c = 0; c < S::kV; ++c) sum[c] = 0;
+            for (int k = w.kb; k < w.ke; k += args.run) {
+              const uint32_t at = acc_wait();
+#pragma unroll
+              for (int c = 0; c < S::kV; c += kPart) {
+                float v[kPart];
+                read_tmem<kPart>(at + c, v);
+#pragma unroll
+                for (int x = 0; x < kPart; ++x)
+                  sum[c + x] = S::kKind == kIntegers ? sum[c + x] + uint32_t(__float2int_rn(v[x]))
+                                                     : __float_as_uint(__uint_as_float(sum[c + x]) + v[x]);
+              }
+              acc_free();
+            }
+          } else {
+            read_tmem<S::kV>(acc_wait(), reinterpret_cast<float*>(sum));
+            acc_free();
+          }
+          const bool ok = going();
+          // Stores n of the columns from c on.
+          auto store = [&](auto c, auto n) {
+            float v[n];
+#pragma unroll
+            for (int x = 0; x < n; ++x)
+              v[x] = S::kKind == kIntegers ? scaled(int(sum[c + x]), scale_r, __shfl_sync(0xffffffffu, scale_c[(c + x) / 32], (c + x) % 32))
+                                           : __uint_as_float(sum[c + x]);
+            if (args.dtype != INT8_F32 && !args.accumulate) {
+              uint32_t two[n / 2];
+#pragma unroll
+              for (int x = 0; x < n; x += 2) two[x / 2] = args.dtype == INT8_BF16 ? pack2<__nv_bfloat162>(v[x], v[x + 1]) : pack2<__half2>(v[x], v[x + 1]);
+              if (mine) put_pairs<n>(static_cast<uint16_t*>(args.out) + int64_t(col0 + c) * args.ld + row, args.ld, args.cols - col0 - c, two);
+            } else if (mine) {
+              put_columns(args, row, col0 + c, v);
+            }
+          };
+          // The only unit of this pair, one of kShares in the cluster: of the columns each pair has a part to add up and store.
+          auto meet = [&](auto shares) {
+            constexpr int kShares = shares, kOwn = S::kV / kShares;
+            const int at = half * kOwn * kRows + 32 * q + lane;
+            cluster_sync();  // everybody's products are done: nothing uses the stages any more
+            if (ok) {
+              for_parts<kShares>([&](auto o) {
+                if (o == w.part) return;
+                const uint32_t to = place_in(smem + (w.part - (w.part > o)) * (2 * kOwn * kRows * 4), 2 * o + rank) + 4 * at;
+#pragma unroll
+                for (int c = 0; c < kOwn; ++c)
+                  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 4 * kRows * c), "r"(sum[o * kOwn + c]) : "memory");
+              });
             }
             __syncwarp();
             cluster_sync();
-            ok = ok && w.part == 0;
-            if (ok)
-              for (int p = 1; p < args.splits; ++p) {
-                const uint32_t* from = reinterpret_cast<const uint32_t*>(s_join + (p - 1) * S::kShareBytes) + at;
+            if (!ok) return;
+            for_parts<kShares>([&](auto o) {
+              if (o != w.part) return;
 #pragma unroll
-                for (int c = 0; c < S::kV; ++c) sum[c] += from[kRows * c];
+              for (int p = 0; p + 1 < kShares; ++p) {
+                const uint32_t* from = reinterpret_cast<const uint32_t*>(smem) + p * (2 * kOwn * kRows) + at;
+#pragma unroll
+                for (int c = 0; c < kOwn; ++c) {
+                  uint32_t& to = sum[o * kOwn + c];
+                  to = S::kKind == kIntegers ? to + from[kRows * c] : __float_as_uint(__uint_as_float(to) + __uint_as_float(from[kRows * c]));
+                }
               }
+              store(Int<o * kOwn>(), Int<kOwn>());
+            });
+          };
+          if (args.join) {
+            if (args.splits == 2)
+              meet(Int<2>());
+            else
+              meet(Int<4>());
+          } else if (ok) {
+            for_parts<S::kV / kPart>([&](auto i) {
+              if (args.splits > 1)
+                put_partials(i * kPart, sum + i * kPart);
+              else
+                store(Int<i * kPart>(), Int<kPart>());
+            });
           }
+          continue;
         }
-        if (!ok) continue;
-#pragma unroll
-        for (int c = 0; c < S::kV; c += kPart) {
-          if (args.splits > 1 && !args.join) {
-            put_partials(c, sum + c);
-            continue;
-          }
-          float v[kPart];
-#pragma unroll
-          for (int x = 0; x < kPart; ++x)
-            v[x] = S::kKind == kIntegers ? scaled(int(sum[c + x]), scale_r, __shfl_sync(0xffffffffu, scale_c[c / 32], x))
-                                         : __uint_as_float(sum[c + x]);
-          if (S::kKind == kIntegers && args.dtype != INT8_F32) {
-            uint32_t two[kPart / 2];
-#pragma unroll
-            for (int x = 0; x < kPart; x += 2) two[x / 2] = args.dtype == INT8_BF16 ? pack2<__nv_bfloat162>(v[x], v[x + 1]) : pack2<__half2>(v[x], v[x + 1]);
-            if (mine) put_pairs<kPart>(static_cast<uint16_t*>(args.out) + int64_t(col0 + c) * args.ld + row, args.ld, args.cols - col0 - c, two);
-          } else if (mine) {
-            put_columns(args, row, col0 + c, v);
-          }
-        }
-      } else {
+      }
+      if constexpr (!S::kRuns) {
         const uint32_t at = acc_wait();
         const bool ok = going();
         if (args.splits > 1) {
@@ -641,7 +684,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     }
   }
   __syncwarp();
-  if (S::kMaxShares > 1 && args.join && warp < 4 + 4 * kGroups) cluster_sync();  // (the epilogue's warps were there)
+  if (S::kMaxShares > 1 && args.join && warp < 4 + 4 * kGroups) cluster_sync(), cluster_sync();  // (the epilogue's warps were there)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   cluster_sync();  // nothing of any CTA is still signalled or read by another

@@ -153,12 +153,12 @@ struct Operands {
 };
 
 // The tiles, and the shares that k is cut into where there are fewer tiles than pairs of CTAs, that are estimated to
-// be fastest (us, fitted to 41 products timed with every choice: the chosen ones are within 4 % of the best, and within
-// 5 % in 31 others).  A stage of
-// 128 of k takes its MMAs, 0.53 for 256 columns and 0.28 for 128 or fewer (reading `a` from tensor memory takes as long),
-// and at least what turning `a` to 16 bits takes, 0.37 with a checkpoint's units; a tile fills and empties the pipeline
-// (1.5), and the last one is stored.  Shares meet within a cluster, or are written and added by a kernel of its own, 4 bytes
-// each way: 16.6 and 14.2 us for 4096 x 1024 x 1024 bf16, one share 18.4.  Equal ones: the narrower tiles, which read less of b.
+// be fastest (us, fitted to 41 products timed with every choice: the chosen ones are within 4 % of the best, and within 5 %
+// in 31 others).  A stage of 128 of k takes its MMAs, 0.53 for 256 columns and 0.28 for 128 or fewer (reading `a` from tensor
+// memory takes as long), and at least what turning `a` to 16 bits takes, 0.37 with a checkpoint's units; a tile fills and
+// empties the pipeline (1.5), and the last one is stored.  Shares meet within a cluster, or are written and added by a kernel
+// of its own, 4 bytes each way: 14.2 and 16.6 us for 4096 x 1024 x 1024 bf16, one share 18.4.  Equal ones: the narrower
+// tiles, which read less of b.
 sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t rows, int64_t cols, int64_t depth, int terms,
                     bool units, const gb300::Int8TcClusters& most, gb300::Int8TcArgs* a, gb300::Int8TcShape* best) {
   const int64_t steps = round_up(depth, gb300::int8_tc_step()) / gb300::int8_tc_step(), tr = (rows + 255) / 256;

@@ -136,6 +136,39 @@ def test_sums_cut_over_k(m, n, k):
         same(sg.int8_gemm(x, w), want)
 
 
+@pytest.mark.parametrize("m,n,k", [(120, 250, 1600), (260, 1000, 2100), (128, 1000, 4000), (100, 2500, 3000), (130, 4100, 3000), (700, 512, 4001)])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_products_whose_shares_meet(m, n, k, dtype):
+    """Two and four shares of k for each width of tile, in a part of a larger output."""
+    (a, sa), (b, sb) = integers(m, k, 3, -128), integers(n, k, 4, -128)
+    around = torch.full((m + 2, n + 9), 5.0, dtype=dtype, device="cuda")
+    x, w = matrix(a, sa), matrix(b, sb)
+    for _ in range(2):
+        sg.int8_gemm(x, w, out=around[1:-1, 1:n + 1])
+    same(around[1:-1, 1:n + 1].contiguous(), ref.product(a, sa, b, sb, dtype))
+    around[1:-1, 1:n + 1] = 5.0
+    assert (around == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("own", [True, False])
+@pytest.mark.parametrize("m,n,k", [(1000, 100, 200), (1300, 1001, 1024), (2600, 200, 519), (1200, 520, 700), (2049, 130, 300)])
+def test_gradients_whose_shares_meet(dtype, own, m, n, k):
+    x, dy = values(m, k, dtype, 5), values(m, n, dtype, 6, 3, 0.1)
+    c, kind = sg.int8_checkpoint(x), dtype if own else F32
+    around = torch.full((n + 2, k + 9), 5.0, dtype=kind, device="cuda")
+    out = around[1:-1, 1:k + 1]
+    sg.int8_weight_grad(dy, c, out=out)
+    check_gradient(out, dy, x, dtype == F16)
+    first = out.clone()
+    sg.int8_weight_grad(dy, c, out=out)
+    same(out.contiguous(), first)
+    sg.int8_weight_grad(dy, c, out=out, accumulate=True)
+    check_gradient(out, dy, x, dtype == F16, first)
+    out.fill_(5.0)
+    assert (around == 5.0).all()
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("scale", [2.0 ** -14, 2.0 ** -20, 2.0 ** -24, 2.0 ** 8, 2.0 ** -100, 2.0 ** 100])
 def test_gradients_far_from_one(dtype, scale):

@@ -160,7 +160,8 @@ struct Operands {
 // of its own, 4 bytes each way: 14.2 and 16.6 us for 4096 x 1024 x 1024 bf16, one share 18.4.  Equal ones: the narrower
 // tiles, which read less of b.
 sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t rows, int64_t cols, int64_t depth, int terms,
-                    bool units, const gb300::Int8TcClusters& most, gb300::Int8TcArgs* a, gb300::Int8TcShape* best) {
+                    bool units, const gb300::Int8TcClusters& most, gb300::Int8TcArgs* a, gb300::Int8TcShape* best,
+                    double* estimate = nullptr) {
   const int64_t steps = round_up(depth, gb300::int8_tc_step()) / gb300::int8_tc_step(), tr = (rows + 255) / 256;
   const int64_t pairs = most.pairs;
   if (pairs <= 0) return SGEMM_ERR_LAUNCH;
@@ -193,6 +194,7 @@ sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t ro
       if (tiles <= (splits == 2 ? most.twos : most.fours) && splits <= steps) consider(splits, true);
     if (std::min(pairs / tiles, steps / 4) > 1) consider(std::min(pairs / tiles, steps / 4), false);
   }
+  if (estimate) *estimate = least;
   return least > 0.0 ? SGEMM_OK : SGEMM_ERR_UNSUPPORTED;
 }
 size_t partial_bytes(const gb300::Int8TcArgs& a) {
@@ -221,7 +223,19 @@ sgemm_status_t run_product(gb300::Int8TcShape shape, const Operands& o, gb300::I
 // C (M x N, row stride ldc) = A B^T, from A's rows as 16-bit floats or, with x, quantised on the way.
 sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* x, int64_t ldx, int64_t M, const int8_matrix_t& B,
                                int dtype, void* C, int64_t ldc, const LibDevice& d, cudaStream_t stream) {
-  if (M <= gb300::int8_few_tokens()) {
+  const bool few = M <= gb300::int8_few_tokens();
+  gb300::Int8TcClusters most;
+  gb300::Int8TcArgs a{};
+  gb300::Int8TcShape shape{};
+  double estimate = 0.0;
+  if (!few) {
+    most = tc_clusters(d.dev);
+    const sgemm_status_t st = plan({gb300::kInt8Whole32, gb300::kInt8Whole64, gb300::kInt8Whole128}, B.rows, M, B.cols, 1, false, most, &a, &shape, &estimate);
+    if (st != SGEMM_OK) return st;
+    estimate += 4.0;  // the kernel that prepares b, and launches
+  }
+  // Eight tokens at a time: 300 x 520 x 200 4.0 us (in tiles 6.1), 512 x 1024 x 1024 13.5 (8.7).
+  if (few || gb300::int8_few_estimate(M, B.rows, B.cols) + (A ? 0.0 : 2.0) < estimate) {
     gb300::Int8FewArgs f{};
     f.w = B.codes;
     f.ldw = B.ld;
@@ -232,36 +246,37 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
     f.k = int32_t(B.cols);
     f.tokens = int32_t(M);
     f.dtype = dtype;
-    if (!A && gb300::int8_few_quantises(M, B.rows, B.cols, d.sms)) {
+    if (A) {
+      f.x = A->codes;
+      f.ldx = A->ld;
+      f.scale_x = A->scales;
+      return status_of(gb300::launch_int8_few(-1, f, d.sms, stream));
+    }
+    if (gb300::int8_few_quantises(M, B.rows, B.cols, d.sms)) {
       f.x = x;
       f.vec = aligned(x, 16);
       return status_of(gb300::launch_int8_few(dtype_x, f, d.sms, stream));
     }
     Scratch s;
-    const size_t scales_at = s.take(M * 4), tokens_at = s.take(16 * round_up(B.cols, 64));
+    const int64_t ld = round_up(B.cols, 16);
+    const size_t scales_at = s.take(M * 4), tokens_at = s.take(M * ld);
     void* ws = nullptr;
     const sgemm_status_t st = gb300::lib_workspace(d.dev, stream, s.bytes, &ws);
     if (st != SGEMM_OK) return st;
     uint8_t* base = static_cast<uint8_t*>(ws);
-    uint16_t* tokens = reinterpret_cast<uint16_t*>(base + tokens_at);
-    float* scales = reinterpret_cast<float*>(base + scales_at);
-    const cudaError_t e = A ? gb300::launch_int8_widen_few(*A, tokens, stream)
-                            : gb300::launch_int8_quantize_few(dtype_x, x, ldx, M, B.cols, tokens, scales, stream);
-    if (e != cudaSuccess) return SGEMM_ERR_LAUNCH;
-    f.x = tokens;
-    f.scale_x = A ? A->scales : scales;
+    const int8_matrix_t tokens{M, B.cols, reinterpret_cast<int8_t*>(base + tokens_at), ld, reinterpret_cast<float*>(base + scales_at)};
+    if (gb300::launch_int8_quantize(dtype_x, x, ldx, tokens, stream) != cudaSuccess) return SGEMM_ERR_LAUNCH;
+    f.x = tokens.codes;
+    f.ldx = ld;
+    f.scale_x = tokens.scales;
+    f.early = 1;
     return status_of(gb300::launch_int8_few(-1, f, d.sms, stream));
   }
-  const gb300::Int8TcClusters most = tc_clusters(d.dev);
-  gb300::Int8TcArgs a{};
-  gb300::Int8TcShape shape{};
-  sgemm_status_t st = plan({gb300::kInt8Whole32, gb300::kInt8Whole64, gb300::kInt8Whole128}, B.rows, M, B.cols, 1, false, most, &a, &shape);
-  if (st != SGEMM_OK) return st;
   const int64_t ld16 = round_up(B.cols, 64);  // whole lines of 128 bytes (16384 x 1024 x 4104: 166 us in multiples of 8, 143)
   Scratch s;
   const size_t scales_at = s.take(M * 4), rows_at = s.take(M * ld16 * 2), partials_at = s.take(int64_t(partial_bytes(a)));
   void* ws = nullptr;
-  st = gb300::lib_workspace(d.dev, stream, s.bytes, &ws);
+  const sgemm_status_t st = gb300::lib_workspace(d.dev, stream, s.bytes, &ws);
   if (st != SGEMM_OK) return st;
   uint8_t* base = static_cast<uint8_t*>(ws);
   uint16_t* rows16 = reinterpret_cast<uint16_t*>(base + rows_at);

@@ -61,7 +61,7 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t
   }
 
 // ------------------------------------------------------------------------- rows
-enum RowForm { kBytes, kWide, kFew };  // integers as bytes, as 16-bit floats, or as those in the few-token product's order
+enum RowForm { kBytes, kWide };  // integers as bytes, or as 16-bit floats
 
 struct RowArgs {
   const void* x;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(
   }
   const float s = row_scale(top), inv = __frcp_rn(s);
   if (t == 0) a.scales[row] = s;
-  const int out_chunks = kForm == kBytes ? (cols + 15) / 16 * 2 : kForm == kWide ? chunks : (cols + 63) / 64 * 8;
+  const int out_chunks = kForm == kBytes ? (cols + 15) / 16 * 2 : chunks;
   auto write = [&](int c, const float (&w)[8]) {
     float n[8];
     nearest8(w, s, inv, n);
@@ -134,10 +134,7 @@ __global__ void __launch_bounds__(kGroup <= 32 ? kThreads : kGroup) rows_kernel(
       __half2* p = reinterpret_cast<__half2*>(&h);
 #pragma unroll
       for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(n[2 * e] - kRound, n[2 * e + 1] - kRound);
-      if constexpr (kForm == kWide)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.ld + 8 * c) = h;
-      else
-        static_cast<uint4*>(a.out)[few_at(int(row), c)] = h;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.ld + 8 * c) = h;
     }
   };
 #pragma unroll
@@ -271,25 +268,6 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const BackArgs a) {
       for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row[j] * a.ld_out + 8 * c[j]) = h;
     }
-  }
-}
-
-// A row of integers in the few-token product's order.
-__global__ void __launch_bounds__(kThreads) widen_few_kernel(const BackArgs a) {
-  begin();
-  const int cols = int(a.cols), row = blockIdx.x;
-  for (int c = threadIdx.x; c < (cols + 63) / 64 * 8; c += kThreads) {
-    float v[8] = {};
-    if (8 * c < cols) {
-      const uint2 q = *reinterpret_cast<const uint2*>(a.codes + row * a.ld + 8 * c);
-      widen4(q.x, v);
-      widen4(q.y, v + 4);
-    }
-    uint4 h;
-    __half2* p = reinterpret_cast<__half2*>(&h);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = __floats2half2_rn(8 * c + 2 * e < cols ? v[2 * e] : 0.f, 8 * c + 2 * e + 1 < cols ? v[2 * e + 1] : 0.f);
-    static_cast<uint4*>(a.out)[few_at(row, c)] = h;
   }
 }
 
@@ -633,17 +611,6 @@ cudaError_t launch_int8_rows16(int dtype, const void* x, int64_t ldx, int64_t ro
                                int64_t ld, float* scales, cudaStream_t stream) {
   const RowArgs a{x, ldx, rows, cols, out, ld, scales};
   return launch_rows<kWide>(dtype, a, whole(cols, aligned16(x, ldx * bytes_of(dtype))), stream);
-}
-
-cudaError_t launch_int8_quantize_few(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
-                                     float* scales, cudaStream_t stream) {
-  const RowArgs a{x, ldx, rows, cols, out, 0, scales};
-  return launch_rows<kFew>(dtype, a, whole(cols, aligned16(x, ldx * bytes_of(dtype))), stream);
-}
-
-cudaError_t launch_int8_widen_few(const int8_matrix_t& q, uint16_t* out, cudaStream_t stream) {
-  const BackArgs a{q.codes, q.ld, q.scales, q.rows, q.cols, out, 0, Chunks{}};
-  return launch(widen_few_kernel, q.rows, kThreads, stream, a);
 }
 
 cudaError_t launch_int8_dequantize(const int8_matrix_t& q, int dtype, void* y, int64_t ldy, int sms,

@@ -189,12 +189,6 @@ __device__ __forceinline__ float scaled(int sum, float s, float t) {
   return float(sum) * (first ? s : t) * (first ? t : s);
 }
 
-// Where a token's 16-bit integers 8 c .. 8 c + 7 (16 bytes) are in the order in which the few-token product reads them:
-// for every 64 columns two halves of 16 bytes a lane, lane = 4 token + column / 16 % 4.
-__device__ __forceinline__ int few_at(int token, int c) {
-  return ((c >> 3) * 2 + (c & 1)) * 32 + token * 4 + (c & 7) / 2;
-}
-
 // n / d for 0 <= n < 2^31, with m = floor(2^(31 + s) / d) + 1 and 2^s >= d: n m / 2^(31 + s) is above n / d by
 // less than 1 / d.
 struct Divider {

@@ -9,9 +9,12 @@
 // an SM, its integer mma 27 for 16 x 8 x 32: 80 and 17 us for 8 tokens of 8192 x 8192.)
 //
 // Structure.  A block has 16 or 32 rows of W, and its warps take 128 columns of K in turn; each has
-// 8 KB of W on the way.  Products take the tokens as 16-bit floats in the lanes' order.  A single token of
-// moderate length is quantised by every block for itself, into shared memory while its first loads of W
-// are on the way; others by a kernel of their own, and the first of W is requested before that is done.
+// 8 KB of W on the way.  Tokens are integers, too, and turned to 16-bit floats in the same way (8192 x 8192 takes 15.2 us with the
+// kernel that quantises, 16.2 if that one writes 16-bit floats in the lanes' order); the first of W is requested before
+// that kernel is done.  A single token of moderate length is quantised by every block for itself, into shared memory
+// while its first loads of W are on the way.  More tokens are taken eight by eight where the product is so small that the
+// launches of the tiled kernel and of the one before it would be most of its time (300 x 520 x 200 6.1 -> 4.0 us, 128 tokens
+// of 512 x 512 6.8 -> 2.7).
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -41,23 +44,26 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// kR x 16 rows.  T: the tokens' type, void if they come quantised.
+// kR x 16 rows, eight tokens.  T: int8_t for tokens of integers, or an unquantised one's type.
 template <typename T, int kR, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int8FewArgs a) {
-  constexpr int kThreads = 32 * kWarps, kAhead = 8 / kR, kXAhead = kR == 1 ? 4 : 2;
-  constexpr bool kQuantise = !std::is_same<T, void>::value;
+  constexpr bool kQuantise = !std::is_same<T, int8_t>::value;
+  constexpr int kThreads = 32 * kWarps, kAhead = 8 / kR, kXAhead = 2 / kR;
   extern __shared__ __align__(16) unsigned char s_x[];  // 16 bytes for each step, half and t
   __shared__ int sums[kWarps][kR * 4][32];
   __shared__ uint32_t s_top;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int row0 = blockIdx.x * 16 * kR, steps = (a.k + kStep - 1) / kStep;
+  const int steps = (a.k + kStep - 1) / kStep, blocks = (a.n + 16 * kR - 1) / (16 * kR);  // of one group of tokens
+  const int group = kQuantise ? 0 : blockIdx.x / blocks, row0 = (blockIdx.x - group * blocks) * 16 * kR;
+  const int token0 = group * kMost, tokens = min(a.tokens - token0, kMost);
   const int8_t* rows[kR][2];
 #pragma unroll
   for (int r = 0; r < kR; ++r)
 #pragma unroll
     for (int h = 0; h < 2; ++h) rows[r][h] = a.w + min(row0 + 16 * r + 8 * h + g, a.n - 1) * a.ldw + 16 * t;
   // A warp's i-th step: pairs next to one another, so that it is a whole line of a row (16384 x 16384 51.1 -> 49.8 us).
-  auto step_of = [&](int i) { return (i >> 1) * (2 * kWarps) + 2 * warp + (i & 1); };
+  // `from`: that of an even one.
+  auto step_of = [&](int from, int i) { return from + (i >> 1) * (2 * kWarps) + (i & 1); };
   uint4 w[kAhead][kR][2];
   auto fetch = [&](int slot, int step) {
     const bool there = kStep * step + 16 * t < a.k;  // (what follows a row's end in its 16 bytes meets zeros of x)
@@ -90,7 +96,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int
       for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) fetch(j, step_of(j));
+    for (int j = 0; j < kAhead; ++j) fetch(j, step_of(2 * warp, j));
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) atomicMax(&s_top, top);
     __syncthreads();
@@ -108,24 +114,41 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int
     }
     __syncthreads();
   } else {
+    if (a.early) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) fetch(j, step_of(j));
+      for (int j = 0; j < kAhead; ++j) fetch(j, step_of(2 * warp, j));
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!a.early) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) fetch(j, step_of(2 * warp, j));
+    }
   }
 
-  // Lanes of tokens that are not there keep zeros.
-  const uint4* x = (kQuantise ? reinterpret_cast<const uint4*>(s_x) : static_cast<const uint4*>(a.x)) + lane;
-  constexpr int kPitch = kQuantise ? 4 : 32;  // of a half
-  uint4 b[kXAhead][2] = {};
+  // The tokens of eight lanes each: 16 bytes of integers a step, or from shared memory twice 16 of 16-bit floats.  (A
+  // token that is not there is another one, whose sums are not stored; lanes 4.. of a single one keep zeros.)
+  const int8_t* x_row = kQuantise ? nullptr : static_cast<const int8_t*>(a.x) + (token0 + min(g, tokens - 1)) * a.ldx + 16 * t;
+  uint4 b[kXAhead][kQuantise ? 2 : 1] = {};
   auto fetch_x = [&](int slot, int step) {
-    if (g < a.tokens && step < steps) {
+    if constexpr (kQuantise) {
+      if (g == 0 && step < steps) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) b[slot][h] = x[(2 * step + h) * kPitch];
+        for (int h = 0; h < 2; ++h) b[slot][h] = reinterpret_cast<const uint4*>(s_x)[(2 * step + h) * 4 + t];
+      }
+    } else {
+      const int left = a.k - kStep * step - 16 * t;  // what follows the row's end is made 0
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (left > 0) v = *reinterpret_cast<const uint4*>(x_row + int64_t(kStep) * step);
+      if (left > 0 && left < 16) {
+        auto some = [&](uint32_t word, int n) { return n <= 0 ? 0u : n >= 4 ? word : word & ((1u << 8 * n) - 1u); };
+        v = make_uint4(some(v.x, left), some(v.y, left - 4), some(v.z, left - 8), some(v.w, left - 12));
+      }
+      b[slot][0] = v;
     }
   };
 #pragma unroll
-  for (int j = 0; j < kXAhead; ++j) fetch_x(j, step_of(j));
+  for (int j = 0; j < kXAhead; ++j) fetch_x(j, step_of(2 * warp, j));
   float acc[kR][4] = {};
   int total[kR][4] = {}, run = 0;
   auto flush = [&]() {
@@ -135,12 +158,20 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int
       for (int i = 0; i < 4; ++i) total[r][i] += __float2int_rn(acc[r][i]), acc[r][i] = 0.f;
   };
 #pragma unroll 1
-  for (int base = 0; step_of(base) < steps; base += kAhead) {
+  for (int from = 2 * warp; from < steps; from += kAhead * kWarps) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (step_of(base + j) >= steps) break;
-      const uint4 b0 = b[j % kXAhead][0], b1 = b[j % kXAhead][1];
-      const uint32_t xs[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+      if (step_of(from, j) >= steps) break;
+      uint32_t xs[8];
+      const uint4 v = b[j % kXAhead][0];
+      if constexpr (kQuantise) {
+        const uint4 u = b[j % kXAhead][1];
+        xs[0] = v.x, xs[1] = v.y, xs[2] = v.z, xs[3] = v.w, xs[4] = u.x, xs[5] = u.y, xs[6] = u.z, xs[7] = u.w;
+      } else {
+        const uint32_t word[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xs[2 * i] = to_f16<0>(word[i]), xs[2 * i + 1] = to_f16<1>(word[i]);
+      }
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         const uint32_t lo[4] = {w[j][r][0].x, w[j][r][0].y, w[j][r][0].z, w[j][r][0].w};
@@ -151,8 +182,8 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int
           mma(acc[r], to_f16<0>(p), to_f16<0>(q), to_f16<1>(p), to_f16<1>(q), xs[2 * i], xs[2 * i + 1]);
         }
       }
-      fetch(j, step_of(base + j + kAhead));
-      fetch_x(j % kXAhead, step_of(base + j + kXAhead));
+      fetch(j, step_of(from, j + kAhead));
+      fetch_x(j % kXAhead, step_of(from, j + kXAhead));
     }
     if ((run += kAhead) == kRun) run = 0, flush();
   }
@@ -162,15 +193,15 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[warp][4 * r + i][lane] = total[r][i];
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * kR * a.tokens; i += kThreads) {
+  for (int i = threadIdx.x; i < 16 * kR * tokens; i += kThreads) {
     const int row = i % (16 * kR), m = i / (16 * kR);
     if (row0 + row >= a.n) continue;
-    const float sw = a.scale_w[row0 + row], sx = kQuantise ? row_scale(__uint_as_float(s_top)) : a.scale_x[m];
+    const float sw = a.scale_w[row0 + row], sx = kQuantise ? row_scale(__uint_as_float(s_top)) : a.scale_x[token0 + m];
     int sum = 0;
 #pragma unroll
     for (int v = 0; v < kWarps; ++v) sum += sums[v][row / 16 * 4 + (row / 8 % 2) * 2 + m % 2][row % 8 * 4 + m / 2];
     const float v = scaled(sum, sw, sx);
-    const int64_t to = m * a.ldy + row0 + row;
+    const int64_t to = (token0 + m) * a.ldy + row0 + row;
     if (a.dtype == INT8_F32)
       static_cast<float*>(a.y)[to] = v;
     else if (a.dtype == INT8_BF16)
@@ -185,40 +216,57 @@ template <typename T, int kR>
 Kernel by_warps(int warps) {
   return warps == 4 ? few_kernel<T, kR, 4> : warps == 8 ? few_kernel<T, kR, 8> : few_kernel<T, kR, 16>;
 }
+template <typename T>
+Kernel kernel_of(int64_t rows, int warps) {
+  return rows == 32 ? by_warps<T, 2>(warps) : by_warps<T, 1>(warps);
+}
+
+// How W is shared out.  Up to eight tokens, as many warps a block as leave all blocks at work at once, 16 warps on an SM (5000 x
+// 4096 in 313 blocks of eight warps takes 9.6 us, 4096 x 4096 in 256 7.1): 4096 rows are 256 blocks of eight warps, 8192 rows
+// 256 of eight or 512 of four.  A block has 32 rows, which halves what it spends on its tokens, where that leaves 200 blocks
+// (products with one token of integers, 16384 x 16384 55 -> 46.4 us, 14336 x 4096 16.2 -> 12.9; 8 tokens of 1024 x 8192, 32
+// blocks, 7 -> 10).  More tokens come eight by eight, in blocks of four warps where there are enough.
+struct Shares {
+  int64_t rows, blocks;
+  int warps;
+};
+Shares shares(int64_t tokens, int64_t n, int64_t k, int sms) {
+  const int64_t groups = (tokens + kMost - 1) / kMost;
+  const int64_t rows = groups == 1 ? (n >= 32 * 200 ? 32 : 16) : (n + 31) / 32 * groups >= 4 * sms ? 32 : 16;
+  const int64_t blocks = (n + rows - 1) / rows * groups;
+  if (groups > 1) return {rows, blocks, blocks <= 2 * sms && k > 512 ? 8 : 4};
+  return {rows, blocks, blocks <= sms ? 16 : blocks <= 2 * sms ? 8 : 4};
+}
 
 }  // namespace
 
 int int8_few_tokens() { return kMost; }
 
-// As many warps a block as leave all blocks at work at once, 16 warps on an SM (5000 x 4096 in 313 blocks of eight warps
-// takes 9.6 us, 4096 x 4096 in 256 7.1): 4096 rows are 256 blocks of eight warps, 8192 rows 512 of four.  Beyond four tokens a
-// block has 32 rows, so that its tokens are half as many bytes as its weights, where that leaves 200 blocks (8 tokens of
-// 8192 x 8192 18.2 -> 16.5 us; of 1024 x 8192, 32 blocks, 7 -> 10).
-static int64_t block_rows(int64_t tokens, int64_t n) { return tokens > 4 && n >= 32 * 200 ? 32 : 16; }
-static int block_warps(int64_t tokens, int64_t n, int sms) {
-  const int64_t blocks = (n + block_rows(tokens, n) - 1) / block_rows(tokens, n);
-  return blocks <= sms ? 16 : blocks <= 2 * sms ? 8 : 4;
+// us, fitted to 60 products of 16 to 512 tokens: the launch, what a block loads and converts, what it adds up and stores.  (A
+// kernel before it that quantises takes 2 more.)
+double int8_few_estimate(int64_t tokens, int64_t n, int64_t k) {
+  return 1.8 + double(tokens) * double(n) * (double(k) * 2.2e-8 + 8e-6);
 }
 
 // Up to 16 values a thread (1024 x 1024: 2.9 us in a graph, 4.0 with a kernel before; 4096 x 4096: 7.5 and 7.3, but 1.5 us
-// less of host time; 8192 x 8192, 64 a thread: 17.7 and 16.3).
+// less of host time; 8192 x 8192, 32 a thread: 17.7 and 16.3).
 bool int8_few_quantises(int64_t tokens, int64_t n, int64_t k, int sms) {
-  return tokens == 1 && k <= 16 * 32 * block_warps(1, n, sms);
+  return tokens == 1 && k <= 16 * 32 * shares(1, n, k, sms).warps;
 }
 
 cudaError_t launch_int8_few(int type_x, const Int8FewArgs& args, int sms, cudaStream_t stream) {
-  const int warps = block_warps(args.tokens, args.n, sms);
-  const int64_t rows = block_rows(args.tokens, args.n), blocks = (args.n + rows - 1) / rows;
-  const Kernel kernel = rows == 32 ? by_warps<void, 2>(warps)
-                        : type_x < 0 ? by_warps<void, 1>(warps)
-                        : type_x == INT8_F32 ? by_warps<float, 1>(warps)
-                        : type_x == INT8_BF16 ? by_warps<__nv_bfloat16, 1>(warps) : by_warps<__half, 1>(warps);
+  const Shares s = shares(args.tokens, args.n, args.k, sms);
+  if (s.blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const Kernel kernel = type_x == INT8_F32    ? kernel_of<float>(s.rows, s.warps)
+                        : type_x == INT8_BF16 ? kernel_of<__nv_bfloat16>(s.rows, s.warps)
+                        : type_x == INT8_F16  ? kernel_of<__half>(s.rows, s.warps)
+                                              : kernel_of<int8_t>(s.rows, s.warps);
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(blocks), 1, 1);
-  cfg.blockDim = dim3(32 * warps, 1, 1);
+  cfg.gridDim = dim3(unsigned(s.blocks), 1, 1);
+  cfg.blockDim = dim3(32 * s.warps, 1, 1);
   cfg.dynamicSmemBytes = type_x < 0 ? 0 : size_t((args.k + kStep - 1) / kStep) * kStep * 2;
   cfg.stream = stream;
   cfg.attrs = &attr;

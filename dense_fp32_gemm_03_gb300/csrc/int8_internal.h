@@ -19,10 +19,6 @@ cudaError_t launch_int8_rows16(int dtype, const void* x, int64_t ldx, int64_t ro
                                int64_t ld, float* scales, cudaStream_t stream);
 // ... or from integers.
 cudaError_t launch_int8_widen(const int8_matrix_t& q, uint16_t* out, int64_t ld, int sms, cudaStream_t stream);
-// The same for the few-token product, up to eight rows: 16 bytes for each (cols rounded up to 64).
-cudaError_t launch_int8_quantize_few(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
-                                     float* scales, cudaStream_t stream);
-cudaError_t launch_int8_widen_few(const int8_matrix_t& q, uint16_t* out, cudaStream_t stream);
 // x (rows x cols, 16-bit or 32-bit) as `terms` matrices of 16 bits one after the other, `ld` elements (a multiple of 8,
 // zeros behind cols) a row: 16-bit types as they are (1 term), 32 bits as three bfloat16 whose sum they are.
 int int8_terms(int dtype);
@@ -79,22 +75,25 @@ struct Int8TcArgs {
 cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], const Int8TcArgs& args, int pairs,
                            cudaStream_t stream);
 
-// ---- the same for few tokens (int8_few.cu): y = X W^T
-int int8_few_tokens();  // the most
+// ---- the same for few tokens and for small products (int8_few.cu): y = X W^T
+int int8_few_tokens();  // up to which it is always taken
 struct Int8FewArgs {
   const int8_t* w;
   int64_t ldw;
   const float* scale_w;
-  const void* x;         // the tokens as the launches above order them, and their scales; or one unquantised
+  const void* x;         // tokens of integers, pitch ldx, and their scales; or one unquantised
+  int64_t ldx;
   const float* scale_x;
-  int32_t vec;           // which starts at a multiple of 16 bytes
+  int32_t early;         // the launch before prepared x: w is read before it ends
+  int32_t vec;           // the unquantised one starts at a multiple of 16 bytes
   void* y;
   int64_t ldy;
   int32_t n, k, tokens;
   int32_t dtype;         // of y
 };
 bool int8_few_quantises(int64_t tokens, int64_t n, int64_t k, int sms);  // whether it takes unquantised tokens (one)
-// type_x: their type, or < 0: it has to follow one of the two launches that write x, and reads w before that one ends.
+double int8_few_estimate(int64_t tokens, int64_t n, int64_t k);          // its time with tokens of integers, us
+// type_x: the unquantised token's type, or < 0.
 cudaError_t launch_int8_few(int type_x, const Int8FewArgs& args, int sms, cudaStream_t stream);
 
 }  // namespace gb300

@@ -136,6 +136,38 @@ def test_sums_cut_over_k(m, n, k):
         same(sg.int8_gemm(x, w), want)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("m,n,k", [(9, 17, 33), (16, 40, 15), (17, 6401, 16), (65, 100, 1), (23, 33, 127), (40000, 3, 20), (120, 300, 777), (8, 6401, 130),
+                                   (700, 1001, 1031), (1030, 2047, 513), (300, 3001, 2100)])
+def test_products_by_eight_tokens_and_in_tiles(m, n, k, dtype):
+    (a, sa), (b, sb) = integers(m, k, 7, -128), integers(n, k, 8, -128)
+    w = matrix(b, sb)
+    around = torch.full((m + 2, n + 5), 5.0, dtype=dtype, device="cuda")
+    out = around[1:-1, 1:n + 1]
+    sg.int8_gemm(matrix(a, sa), w, out=out)
+    same(out.contiguous(), ref.product(a, sa, b, sb, dtype))
+    x = values(m, k, dtype, 9, 3)
+    sg.int8_linear(x, w, out=out)
+    same(out.contiguous(), ref.product(*ref.quantize(ref.array(x)), b, sb, dtype))
+    out.fill_(5.0)
+    assert (around == 5.0).all()
+
+
+@pytest.mark.parametrize("m", [3, 40])
+def test_codes_behind_both_rows_are_not_used(m):
+    """Integers behind the columns of either operand, in the 16 bytes that the kernels read."""
+    n, k = 50, 100
+    (a, sa), (b, sb) = integers(m, k, 1, -128), integers(n, k, 2, -128)
+    want = ref.product(a, sa, b, sb, F32)
+    held = []
+    for q, s in ((a, sa), (b, sb)):
+        memory = torch.full((len(q), 112), 77, dtype=torch.int8, device="cuda")
+        memory[:, :k] = torch.from_numpy(q).cuda()
+        held.append(sg.int8_matrix(memory[:, :k], torch.from_numpy(s).cuda()))
+        assert held[-1].codes.data_ptr() == memory.data_ptr()
+    same(sg.int8_gemm(*held), want)
+
+
 @pytest.mark.parametrize("m,n,k", [(120, 250, 1600), (260, 1000, 2100), (128, 1000, 4000), (100, 2500, 3000), (130, 4100, 3000), (700, 512, 4001)])
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 def test_products_whose_shares_meet(m, n, k, dtype):

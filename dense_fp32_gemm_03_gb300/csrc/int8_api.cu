@@ -234,7 +234,7 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
     if (st != SGEMM_OK) return st;
     estimate += 4.0;  // the kernel that prepares b, and launches
   }
-  // Eight tokens at a time: 300 x 520 x 200 4.0 us (in tiles 6.1), 512 x 1024 x 1024 13.5 (8.7).
+  // Eight tokens at a time: 300 x 520 x 200 3.6 us (in tiles 6.1), 512 x 1024 x 1024 13.5 (8.7).
   if (few || gb300::int8_few_estimate(M, B.rows, B.cols) + (A ? 0.0 : 2.0) < estimate) {
     gb300::Int8FewArgs f{};
     f.w = B.codes;

@@ -13,7 +13,7 @@
 // kernel that quantises, 16.2 if that one writes 16-bit floats in the lanes' order); the first of W is requested before
 // that kernel is done.  A single token of moderate length is quantised by every block for itself, into shared memory
 // while its first loads of W are on the way.  More tokens are taken eight by eight where the product is so small that the
-// launches of the tiled kernel and of the one before it would be most of its time (300 x 520 x 200 6.1 -> 4.0 us, 128 tokens
+// launches of the tiled kernel and of the one before it would be most of its time (300 x 520 x 200 6.1 -> 3.6 us, 128 tokens
 // of 512 x 512 6.8 -> 2.7).
 #include <cuda_runtime.h>
 
@@ -214,6 +214,9 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) few_kernel(const Int
 typedef void (*Kernel)(Int8FewArgs);
 template <typename T, int kR>
 Kernel by_warps(int warps) {
+  if constexpr (std::is_same<T, int8_t>::value) {
+    if (warps == 2) return few_kernel<T, kR, 2>;
+  }
   return warps == 4 ? few_kernel<T, kR, 4> : warps == 8 ? few_kernel<T, kR, 8> : few_kernel<T, kR, 16>;
 }
 template <typename T>
@@ -225,7 +228,8 @@ Kernel kernel_of(int64_t rows, int warps) {
 // 4096 in 313 blocks of eight warps takes 9.6 us, 4096 x 4096 in 256 7.1): 4096 rows are 256 blocks of eight warps, 8192 rows
 // 256 of eight or 512 of four.  A block has 32 rows, which halves what it spends on its tokens, where that leaves 200 blocks
 // (products with one token of integers, 16384 x 16384 55 -> 46.4 us, 14336 x 4096 16.2 -> 12.9; 8 tokens of 1024 x 8192, 32
-// blocks, 7 -> 10).  More tokens come eight by eight, in blocks of four warps where there are enough.
+// blocks, 7 -> 10).  More tokens come eight by eight, in blocks of two to eight warps (300 x 520 x 200, 646 blocks: four warps
+// each 4.3 us, two 3.6).
 struct Shares {
   int64_t rows, blocks;
   int warps;
@@ -234,7 +238,7 @@ Shares shares(int64_t tokens, int64_t n, int64_t k, int sms) {
   const int64_t groups = (tokens + kMost - 1) / kMost;
   const int64_t rows = groups == 1 ? (n >= 32 * 200 ? 32 : 16) : (n + 31) / 32 * groups >= 4 * sms ? 32 : 16;
   const int64_t blocks = (n + rows - 1) / rows * groups;
-  if (groups > 1) return {rows, blocks, blocks <= 2 * sms && k > 512 ? 8 : 4};
+  if (groups > 1) return {rows, blocks, blocks > 4 * sms ? 2 : blocks <= 2 * sms && k > 512 ? 8 : 4};
   return {rows, blocks, blocks <= sms ? 16 : blocks <= 2 * sms ? 8 : 4};
 }
 
@@ -245,7 +249,7 @@ int int8_few_tokens() { return kMost; }
 // us, fitted to 60 products of 16 to 512 tokens: the launch, what a block loads and converts, what it adds up and stores.  (A
 // kernel before it that quantises takes 2 more.)
 double int8_few_estimate(int64_t tokens, int64_t n, int64_t k) {
-  return 1.8 + double(tokens) * double(n) * (double(k) * 2.2e-8 + 8e-6);
+  return 1.8 + double(tokens) * double(n) * (double(k) * 2.2e-8 + 5e-6);
 }
 
 // Up to 16 values a thread (1024 x 1024: 2.9 us in a graph, 4.0 with a kernel before; 4096 x 4096: 7.5 and 7.3, but 1.5 us

@@ -252,8 +252,8 @@ double int8_few_estimate(int64_t tokens, int64_t n, int64_t k) {
   return 1.8 + double(tokens) * double(n) * (double(k) * 2.2e-8 + 5e-6);
 }
 
-// Up to 16 values a thread (1024 x 1024: 2.9 us in a graph, 4.0 with a kernel before; 4096 x 4096: 7.5 and 7.3, but 1.5 us
-// less of host time; 8192 x 8192, 32 a thread: 17.7 and 16.3).
+// Up to 16 values a thread (1024 x 1024: 2.8 us in a graph, 3.9 with a kernel before; 4096 x 4096: 6.6 and 6.9, and 1.5 us
+// less of host time; 8192 x 8192, 32 a thread: 15.4 and 14.6).
 bool int8_few_quantises(int64_t tokens, int64_t n, int64_t k, int sms) {
   return tokens == 1 && k <= 16 * 32 * shares(1, n, k, sms).warps;
 }

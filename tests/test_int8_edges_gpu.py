@@ -153,6 +153,17 @@ def test_products_by_eight_tokens_and_in_tiles(m, n, k, dtype):
     assert (around == 5.0).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("m,n,k,pad", [(1, 6401, 300, 0), (1, 7000, 4096, 0), (1, 12011, 1001, 1), (2, 6500, 1000, 3), (8, 12000, 200, 0), (5, 6400, 2064, 0)])
+def test_few_tokens_of_many_channels(dtype, m, n, k, pad):
+    (b, sb), x = integers(n, k, 11, -128), values(m, k, dtype, 12, pad)
+    w = matrix(b, sb)
+    want = ref.product(*ref.quantize(ref.array(x)), b, sb, dtype)
+    for _ in range(2):
+        same(sg.int8_linear(x, w), want)
+    same(sg.int8_gemm(sg.int8_quantize(x), w, out_dtype=dtype), want)
+
+
 @pytest.mark.parametrize("m", [3, 40])
 def test_codes_behind_both_rows_are_not_used(m):
     """Integers behind the columns of either operand, in the 16 bytes that the kernels read."""

@@ -418,14 +418,19 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   gb300::Int8TcArgs a{};
   gb300::Int8TcShape shape{};
   const bool half = c->dtype == INT8_F16;
+  double estimate = 0.0;
   if (dtype == INT8_F32)
-    st = plan({half ? gb300::kInt8F16Runs : gb300::kInt8Bf16Runs}, c->cols, N, c->rows, terms, true, most, &a, &shape);
+    st = plan({half ? gb300::kInt8F16Runs : gb300::kInt8Bf16Runs}, c->cols, N, c->rows, terms, true, most, &a, &shape, &estimate);
   else
     st = plan({half ? gb300::kInt8F16N128 : gb300::kInt8Bf16N128, half ? gb300::kInt8F16N256 : gb300::kInt8Bf16N256}, c->cols, N, c->rows,
-              terms, true, most, &a, &shape);
+              terms, true, most, &a, &shape, &estimate);
   if (st != SGEMM_OK) return st;
   a.run = 512 / gb300::int8_tc_step();
   const bool in_place = terms == 1 && aligned(dy, 16) && (lddy % 8 == 0 || c->rows == 1);
+  // Where the product takes so little that launches are most of it (2.2 us, with the kernel before it 3): int8_grad.cu.
+  const gb300::Int8GradArgs g{c->codes, c->ld, c->units, c->ld_units, dy, lddy, int32_t(c->rows), int32_t(c->cols), int32_t(N),
+                              dtype, accumulate != 0, dw, ldw};
+  if (gb300::int8_grad_estimate(c->dtype, g) < estimate + (in_place ? 2.2 : 3.0)) return status_of(gb300::launch_int8_grad(c->dtype, g, stream));
   Operands o{c->codes, c->ld, c->units, c->ld_units, static_cast<const uint16_t*>(dy), round_up(lddy, 8), terms};
   if (!in_place) o.ldb = round_up(N, 64);
   Scratch s;

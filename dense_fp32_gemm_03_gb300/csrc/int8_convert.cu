@@ -281,18 +281,6 @@ struct SplitArgs {
   Chunks n;
 };
 
-// The upper 16 bits of v's 32 (v's first eight significant bits), and v less that; a value that is
-// not finite is its own first term.
-__device__ __forceinline__ uint32_t take16(float& v) {
-  const uint32_t b = __float_as_uint(v);
-  if ((b & 0x7fffffffu) >= 0x7f800000u) {
-    v = 0.f;
-    return (b & 0x7fffffffu) > 0x7f800000u ? 0x7fc0u : b >> 16;
-  }
-  v -= __uint_as_float(b & 0xffff0000u);
-  return b >> 16;
-}
-
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) split_kernel(const SplitArgs a) {
   begin();

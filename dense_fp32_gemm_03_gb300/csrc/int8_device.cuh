@@ -183,6 +183,39 @@ template <int kPair>
 __device__ __forceinline__ uint32_t to_f16(uint32_t biased) {
   return hsub2(__byte_perm(biased, 0x64646464u, kPair ? 0x4342 : 0x4140), 0x64806480u);
 }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Two of a word's four integers in bfloat16: of 128 + (the low seven bits) 128 is taken off where q >= 0 and 256 where
+// q < 0, the number whose bits are 0x4300 and q's top bit.
+template <int kPair>
+__device__ __forceinline__ uint32_t to_bf16(uint32_t word) {
+  const uint32_t p = __byte_perm(word, 0x43434343u, kPair ? 0x4342 : 0x4140);
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(p & 0xff7fff7fu), "r"(p & 0xff80ff80u));
+  return d;
+}
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// The upper 16 bits of v's 32 (v's first eight significant bits), and v less that; a value that is
+// not finite is its own first term.
+__device__ __forceinline__ uint32_t take16(float& v) {
+  const uint32_t b = __float_as_uint(v);
+  if ((b & 0x7fffffffu) >= 0x7f800000u) {
+    v = 0.f;
+    return (b & 0x7fffffffu) > 0x7f800000u ? 0x7fc0u : b >> 16;
+  }
+  v -= __uint_as_float(b & 0xffff0000u);
+  return b >> 16;
+}
+
 // A sum of integers times its scales, the smaller first (NaN stays).
 __device__ __forceinline__ float scaled(int sum, float s, float t) {
   const bool first = fabsf(s) <= fabsf(t);

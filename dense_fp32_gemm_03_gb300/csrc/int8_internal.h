@@ -96,4 +96,20 @@ double int8_few_estimate(int64_t tokens, int64_t n, int64_t k);          // its 
 // type_x: the unquantised token's type, or < 0.
 cudaError_t launch_int8_few(int type_x, const Int8FewArgs& args, int sms, cudaStream_t stream);
 
+// ---- a small weight gradient (int8_grad.cu): dw (n x cols, + dw if asked) = dy^T X, dy of the type that was kept
+struct Int8GradArgs {
+  const int8_t* codes;  // channels x tokens
+  int64_t ld;
+  const uint16_t* units;  // blocks of 32 channels x tokens
+  int64_t ldu;
+  const void* dy;  // tokens x n
+  int64_t lddy;
+  int32_t tokens, cols, n;
+  int32_t dtype, accumulate;  // of dw
+  void* dw;
+  int64_t ldw;
+};
+double int8_grad_estimate(int dtype, const Int8GradArgs& args);  // us
+cudaError_t launch_int8_grad(int dtype, const Int8GradArgs& args, cudaStream_t stream);
+
 }  // namespace gb300

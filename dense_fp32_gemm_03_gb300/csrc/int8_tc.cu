@@ -155,27 +155,6 @@ __device__ __forceinline__ void write_tmem32(uint32_t taddr, const uint32_t (&r)
       : "memory");
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// Two of a word's four integers in bfloat16: of 128 + (the low seven bits) 128 is taken off where q >= 0 and 256 where
-// q < 0, the number whose bits are 0x4300 and q's top bit.
-template <int kPair>
-__device__ __forceinline__ uint32_t to_bf16(uint32_t word) {
-  const uint32_t p = __byte_perm(word, 0x43434343u, kPair ? 0x4342 : 0x4140);
-  uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(p & 0xff7fff7fu), "r"(p & 0xff80ff80u));
-  return d;
-}
-__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 // A place in a ring of kCount and the parity of its round.
 template <int kCount>
 struct At {

@@ -213,6 +213,42 @@ def test_gradients_whose_shares_meet(dtype, own, m, n, k):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("own", [True, False])
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (5, 70, 33), (64, 256, 256), (65, 33, 32), (200, 40, 65), (700, 31, 96), (333, 520, 1001), (333, 2050, 1501), (129, 4001, 1031)])
+def test_gradients_of_few_tokens(dtype, own, m, n, k):
+    """Small ones, and ones in tiles; dy with rows of 16 bytes and others."""
+    x, dy = values(m, k, dtype, 5), values(m, n, dtype, 6, 3 if m % 2 else 0, 0.1)
+    c, kind = sg.int8_checkpoint(x), dtype if own else F32
+    around = torch.full((n + 2, k + 9), 5.0, dtype=kind, device="cuda")
+    out = around[1:-1, 1:k + 1]
+    sg.int8_weight_grad(dy, c, out=out)
+    check_gradient(out, dy, x, dtype == F16)
+    first = out.clone()
+    sg.int8_weight_grad(dy, c, out=out)
+    same(out.contiguous(), first)
+    sg.int8_weight_grad(dy, c, out=out, accumulate=True)
+    check_gradient(out, dy, x, dtype == F16, first)
+    out.fill_(5.0)
+    assert (around == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_small_gradients_beside_nan(dtype):
+    """What is not finite in dy or in x reaches the sums that it is part of, and no others."""
+    m, n, k = 130, 50, 100
+    x, dy = values(m, k, dtype, 1), values(m, n, dtype, 2, 1, 0.1)
+    clean = sg.int8_weight_grad(dy, sg.int8_checkpoint(x))
+    x[7, 40], dy[129, 3], dy[0, 9] = float("nan"), float("inf"), float("nan")
+    got = sg.int8_weight_grad(dy, sg.int8_checkpoint(x))
+    bad = torch.zeros(n, k, dtype=torch.bool, device="cuda")
+    bad[:, 32:64] = bad[9] = True
+    assert got[bad].isnan().all()
+    assert not got[3].isfinite().any()
+    bad[3] = True
+    same(got[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
 @pytest.mark.parametrize("scale", [2.0 ** -14, 2.0 ** -20, 2.0 ** -24, 2.0 ** 8, 2.0 ** -100, 2.0 ** 100])
 def test_gradients_far_from_one(dtype, scale):
     """Units and gradients at the ends of their types: tokens of one value each, so that dW is dY times it, exactly."""

@@ -10,6 +10,7 @@
 
 #include "int8.h"
 #include "int8_internal.h"
+#include "int8_plan.h"
 #include "sgemm_internal.h"
 
 namespace {
@@ -152,51 +153,7 @@ struct Operands {
   int terms;
 };
 
-// The tiles, and the shares that k is cut into where there are fewer tiles than pairs of CTAs, that are estimated to
-// be fastest (us, fitted to 41 products timed with every choice: the chosen ones are within 4 % of the best, and within 5 %
-// in 31 others).  A stage of 128 of k takes its MMAs, 0.53 for 256 columns and 0.28 for 128 or fewer (reading `a` from tensor
-// memory takes as long), and at least what turning `a` to 16 bits takes, 0.37 with a checkpoint's units; a tile fills and
-// empties the pipeline (1.5), and the last one is stored.  Shares meet within a cluster, or are written and added by a kernel
-// of its own, 4 bytes each way: 14.2 and 16.6 us for 4096 x 1024 x 1024 bf16, one share 18.4.  Equal ones: the narrower
-// tiles, which read less of b.
-sgemm_status_t plan(std::initializer_list<gb300::Int8TcShape> shapes, int64_t rows, int64_t cols, int64_t depth, int terms,
-                    bool units, const gb300::Int8TcClusters& most, gb300::Int8TcArgs* a, gb300::Int8TcShape* best,
-                    double* estimate = nullptr) {
-  const int64_t steps = round_up(depth, gb300::int8_tc_step()) / gb300::int8_tc_step(), tr = (rows + 255) / 256;
-  const int64_t pairs = most.pairs;
-  if (pairs <= 0) return SGEMM_ERR_LAUNCH;
-  a->rows = int32_t(rows);
-  a->cols = int32_t(cols);
-  a->depth = int32_t(depth);
-  a->steps = int32_t(steps);
-  a->terms = terms;
-  a->run = 1024 / gb300::int8_tc_step();
-  double least = 0.0;
-  for (const gb300::Int8TcShape shape : shapes) {
-    const int64_t n = gb300::int8_tc_cols(shape), tc = (cols + n - 1) / n, tiles = tr * tc;
-    if (tiles > 0x3fffffffLL) continue;
-    const double stage = std::max(units ? 0.37 : 0.0, double(terms) * std::max(0.28, double(n) * (0.53 / 256)));
-    const double last = std::min(3.0, 0.02 * double(n - 32));
-    auto consider = [&](int64_t splits, bool join) {
-      const double us = double((tiles * splits + pairs - 1) / pairs) * (double((steps + splits - 1) / splits) * stage + 1.5) + last +
-                        (join ? 0.3 + 0.25 * double(splits) : splits > 1 ? 2.5 + double(splits) * double(rows) * double(cols) * 1e-6 : 0.0);
-      if (least > 0.0 && us >= least) return;
-      least = us;
-      *best = shape;
-      a->tiles_r = int32_t(tr);
-      a->tiles_c = int32_t(tc);
-      a->splits = int32_t(splits);
-      a->units = int32_t(tiles * splits);
-      a->join = join;
-    };
-    consider(1, false);
-    for (int64_t splits = 2; splits <= gb300::int8_tc_shares(shape); splits *= 2)
-      if (tiles <= (splits == 2 ? most.twos : most.fours) && splits <= steps) consider(splits, true);
-    if (std::min(pairs / tiles, steps / 4) > 1) consider(std::min(pairs / tiles, steps / 4), false);
-  }
-  if (estimate) *estimate = least;
-  return least > 0.0 ? SGEMM_OK : SGEMM_ERR_UNSUPPORTED;
-}
+sgemm_status_t no_plan(const gb300::Int8TcClusters& most) { return most.pairs > 0 ? SGEMM_ERR_UNSUPPORTED : SGEMM_ERR_LAUNCH; }
 size_t partial_bytes(const gb300::Int8TcArgs& a) {
   return a.splits > 1 && !a.join ? size_t(a.splits) * size_t(a.rows) * size_t(a.cols) * 4 : 0;
 }
@@ -209,10 +166,10 @@ sgemm_status_t run_product(gb300::Int8TcShape shape, const Operands& o, gb300::I
   if (st != SGEMM_OK) return st;
   if (o.units) {
     st = gb300::lib_encode_bytes(o.units, (a.rows + 31) / 32, 2 * depth8, 2 * o.ldu, 4, &maps[1]);
-    if (st == SGEMM_OK) st = gb300::lib_encode_bytes(o.b, int64_t(o.terms) * a.depth, 2 * cols8, 2 * o.ldb, gb300::int8_tc_step(), &maps[2]);
+    if (st == SGEMM_OK) st = gb300::lib_encode_bytes(o.b, int64_t(o.terms) * a.depth, 2 * cols8, 2 * o.ldb, int(gb300::kInt8TcStep), &maps[2]);
   } else {
     maps[1] = maps[0];  // not used
-    st = gb300::lib_encode_bytes(o.b, a.cols, 2 * depth8, 2 * o.ldb, gb300::int8_tc_cols(shape) / 2, &maps[2]);
+    st = gb300::lib_encode_bytes(o.b, a.cols, 2 * depth8, 2 * o.ldb, gb300::int8_tc_form(shape).cols / 2, &maps[2]);
   }
   if (st != SGEMM_OK) return st;
   a.status = d.status;
@@ -223,19 +180,10 @@ sgemm_status_t run_product(gb300::Int8TcShape shape, const Operands& o, gb300::I
 // C (M x N, row stride ldc) = A B^T, from A's rows as 16-bit floats or, with x, quantised on the way.
 sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* x, int64_t ldx, int64_t M, const int8_matrix_t& B,
                                int dtype, void* C, int64_t ldc, const LibDevice& d, cudaStream_t stream) {
-  const bool few = M <= gb300::int8_few_tokens();
-  gb300::Int8TcClusters most;
-  gb300::Int8TcArgs a{};
-  gb300::Int8TcShape shape{};
-  double estimate = 0.0;
-  if (!few) {
-    most = tc_clusters(d.dev);
-    const sgemm_status_t st = plan({gb300::kInt8Whole32, gb300::kInt8Whole64, gb300::kInt8Whole128}, B.rows, M, B.cols, 1, false, most, &a, &shape, &estimate);
-    if (st != SGEMM_OK) return st;
-    estimate += 4.0;  // the kernel that prepares b, and launches
-  }
-  // Eight tokens at a time: 300 x 520 x 200 3.6 us (in tiles 6.1), 512 x 1024 x 1024 13.5 (8.7).
-  if (few || gb300::int8_few_estimate(M, B.rows, B.cols) + (A ? 0.0 : 2.0) < estimate) {
+  const gb300::Int8TcClusters most = M <= gb300::kInt8FewTokens ? gb300::Int8TcClusters{} : tc_clusters(d.dev);
+  const gb300::Int8Plan p = gb300::int8_plan_product(M, B.rows, B.cols, A != nullptr, most);
+  if (!p.ok) return no_plan(most);
+  if (p.small) {
     gb300::Int8FewArgs f{};
     f.w = B.codes;
     f.ldw = B.ld;
@@ -272,6 +220,7 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
     f.early = 1;
     return status_of(gb300::launch_int8_few(-1, f, d.sms, stream));
   }
+  gb300::Int8TcArgs a = p.a;
   const int64_t ld16 = round_up(B.cols, 64);  // whole lines of 128 bytes (16384 x 1024 x 4104: 166 us in multiples of 8, 143)
   Scratch s;
   const size_t scales_at = s.take(M * 4), rows_at = s.take(M * ld16 * 2), partials_at = s.take(int64_t(partial_bytes(a)));
@@ -291,7 +240,7 @@ sgemm_status_t integer_product(const int8_matrix_t* A, int dtype_x, const void* 
   a.ld = ldc;
   a.early = 1;
   a.partials = reinterpret_cast<uint32_t*>(base + partials_at);
-  return run_product(shape, Operands{B.codes, B.ld, nullptr, 0, rows16, ld16, 1}, a, most.pairs, d, stream);
+  return run_product(p.shape, Operands{B.codes, B.ld, nullptr, 0, rows16, ld16, 1}, a, most.pairs, d, stream);
 }
 
 }  // namespace
@@ -412,25 +361,15 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   st = gb300::lib_device(&d);
   if (st != SGEMM_OK || N == 0 || c->cols == 0) return st;
   if (c->rows == 0) return accumulate ? SGEMM_OK : zero_output(dtype, dw, N, c->cols, ldw, stream);
-  // 32-bit results are added up 512 tokens at a time.
   const gb300::Int8TcClusters most = tc_clusters(d.dev);
   const int terms = gb300::int8_terms(c->dtype);
-  gb300::Int8TcArgs a{};
-  gb300::Int8TcShape shape{};
-  const bool half = c->dtype == INT8_F16;
-  double estimate = 0.0;
-  if (dtype == INT8_F32)
-    st = plan({half ? gb300::kInt8F16Runs : gb300::kInt8Bf16Runs}, c->cols, N, c->rows, terms, true, most, &a, &shape, &estimate);
-  else
-    st = plan({half ? gb300::kInt8F16N128 : gb300::kInt8Bf16N128, half ? gb300::kInt8F16N256 : gb300::kInt8Bf16N256}, c->cols, N, c->rows,
-              terms, true, most, &a, &shape, &estimate);
-  if (st != SGEMM_OK) return st;
-  a.run = 512 / gb300::int8_tc_step();
   const bool in_place = terms == 1 && aligned(dy, 16) && (lddy % 8 == 0 || c->rows == 1);
-  // Where the product takes so little that launches are most of it (2.2 us, with the kernel before it 3): int8_grad.cu.
   const gb300::Int8GradArgs g{c->codes, c->ld, c->units, c->ld_units, dy, lddy, int32_t(c->rows), int32_t(c->cols), int32_t(N),
                               dtype, accumulate != 0, dw, ldw};
-  if (gb300::int8_grad_estimate(c->dtype, g) < estimate + (in_place ? 2.2 : 3.0)) return status_of(gb300::launch_int8_grad(c->dtype, g, stream));
+  const gb300::Int8Plan p = gb300::int8_plan_gradient(c->dtype, dtype, in_place, gb300::int8_grad_vec(g), c->rows, N, c->cols, most);
+  if (!p.ok) return no_plan(most);
+  if (p.small) return status_of(gb300::launch_int8_grad(c->dtype, g, stream));
+  gb300::Int8TcArgs a = p.a;
   Operands o{c->codes, c->ld, c->units, c->ld_units, static_cast<const uint16_t*>(dy), round_up(lddy, 8), terms};
   if (!in_place) o.ldb = round_up(N, 64);
   Scratch s;
@@ -450,7 +389,7 @@ sgemm_status_t int8_weight_grad(const void* dy, int64_t lddy, int64_t N, const i
   a.out = dw;
   a.ld = ldw;
   a.partials = reinterpret_cast<uint32_t*>(base + partials_at);
-  return run_product(shape, o, a, most.pairs, d, stream);
+  return run_product(p.shape, o, a, most.pairs, d, stream);
 } GB300_INT8_CATCH
 
 sgemm_status_t int8_swiglu(int dtype, int64_t M, int64_t F, const void* gate, int64_t ld_gate, const void* up,

@@ -613,8 +613,6 @@ cudaError_t launch_int8_widen(const int8_matrix_t& q, uint16_t* out, int64_t ld,
   return launch(widen_kernel, blocks_of(a.n), kThreads, stream, a);
 }
 
-int int8_terms(int dtype) { return dtype == INT8_F32 ? 3 : 1; }
-
 cudaError_t launch_int8_split(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
                               int64_t ld, int sms, cudaStream_t stream) {
   const SplitArgs a{x, ldx, rows, cols, out, ld, chunks_of(rows, (cols + 7) / 8, sms, kPer)};

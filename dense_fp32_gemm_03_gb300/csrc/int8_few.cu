@@ -29,7 +29,7 @@ using namespace int8;
 
 constexpr int kStep = 64;           // columns of K of a warp's step
 constexpr int kRun = 1024 / kStep;  // steps whose sums stay exact
-constexpr int kMost = 8;            // tokens
+constexpr int kMost = kInt8FewTokens;
 
 __device__ __forceinline__ uint4 load_once(const int8_t* p) {
   uint4 v;
@@ -243,14 +243,6 @@ Shares shares(int64_t tokens, int64_t n, int64_t k, int sms) {
 }
 
 }  // namespace
-
-int int8_few_tokens() { return kMost; }
-
-// us, fitted to 60 products of 16 to 512 tokens: the launch, what a block loads and converts, what it adds up and stores.  (A
-// kernel before it that quantises takes 2 more.)
-double int8_few_estimate(int64_t tokens, int64_t n, int64_t k) {
-  return 1.8 + double(tokens) * double(n) * (double(k) * 2.2e-8 + 5e-6);
-}
 
 // Up to 16 values a thread (1024 x 1024: 2.8 us in a graph, 3.9 with a kernel before; 4096 x 4096: 6.6 and 6.9, and 1.5 us
 // less of host time; 8192 x 8192, 32 a thread: 15.4 and 14.6).

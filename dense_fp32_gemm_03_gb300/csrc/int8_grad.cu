@@ -23,7 +23,7 @@ namespace {
 
 using namespace int8;
 
-constexpr int kTile = 32, kWarps = 4, kThreads = 32 * kWarps, kStep = 64;
+constexpr int kTile = kInt8GradTile, kWarps = kInt8GradWarps, kThreads = 32 * kWarps, kStep = kInt8GradStep;
 
 template <bool kHalf>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -184,25 +184,18 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(const Int8GradArgs a) {
 
 }  // namespace
 
-static bool whole(const Int8GradArgs& a) {
+bool int8_grad_vec(const Int8GradArgs& a) {
+  // (32-bit values are split on the way)
   return reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && a.lddy % 8 == 0 && a.n % 8 == 0;
 }
 static int64_t blocks_of(const Int8GradArgs& a) {
   return (int64_t(a.cols) + kTile - 1) / kTile * ((int64_t(a.n) + kTile - 1) / kTile);
 }
 
-// us, fitted to 15 sizes of each form: the launch, a warp's steps one after the other, a block, and a block's steps.
-double int8_grad_estimate(int dtype, const Int8GradArgs& a) {
-  const double steps = double((int64_t(a.tokens) + kStep - 1) / kStep), rounds = double((int64_t(steps) + kWarps - 1) / kWarps);
-  const double blocks = double(blocks_of(a));
-  if (dtype == INT8_F32) return 2.0 + 2.5 * rounds + blocks * steps * 0.0035;
-  return whole(a) ? 1.5 + 0.9 * rounds + blocks * (0.0027 + 0.00047 * steps) : 1.4 + 1.4 * rounds + blocks * (0.003 + 0.0005 * steps);
-}
-
 cudaError_t launch_int8_grad(int dtype, const Int8GradArgs& args, cudaStream_t stream) {
   const int64_t blocks = blocks_of(args);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const bool vec = whole(args);
+  const bool vec = int8_grad_vec(args);
   void (*const kernel)(Int8GradArgs) = dtype == INT8_F32    ? grad_kernel<float, false>
                                        : dtype == INT8_BF16 ? vec ? grad_kernel<__nv_bfloat16, true> : grad_kernel<__nv_bfloat16, false>
                                        : vec                ? grad_kernel<__half, true>

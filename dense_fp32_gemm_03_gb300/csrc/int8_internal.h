@@ -20,8 +20,7 @@ cudaError_t launch_int8_rows16(int dtype, const void* x, int64_t ldx, int64_t ro
 // ... or from integers.
 cudaError_t launch_int8_widen(const int8_matrix_t& q, uint16_t* out, int64_t ld, int sms, cudaStream_t stream);
 // x (rows x cols, 16-bit or 32-bit) as `terms` matrices of 16 bits one after the other, `ld` elements (a multiple of 8,
-// zeros behind cols) a row: 16-bit types as they are (1 term), 32 bits as three bfloat16 whose sum they are.
-int int8_terms(int dtype);
+// zeros behind cols) a row: 16-bit types as they are, 32 bits as three bfloat16 whose sum they are.
 cudaError_t launch_int8_split(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint16_t* out,
                               int64_t ld, int sms, cudaStream_t stream);
 cudaError_t launch_int8_keep(const void* x, int64_t ldx, const int8_checkpoint_t& c, cudaStream_t stream);
@@ -40,13 +39,11 @@ cudaError_t launch_int8_swiglu_backward(const void* dh, int64_t lddh, const int8
 // The kind of `a`, whether sums leave the accumulator after some stages, and the columns of a tile.
 enum Int8TcShape {
   kInt8Whole32, kInt8Whole64, kInt8Whole128,
-  kInt8Bf16N128, kInt8Bf16N256, kInt8Bf16Runs,
-  kInt8F16N128, kInt8F16N256, kInt8F16Runs,
+  kInt8Bf16N128, kInt8Bf16N256, kInt8Bf16Runs, kInt8Bf16Runs256,
+  kInt8F16N128, kInt8F16N256, kInt8F16Runs, kInt8F16Runs256,
   kInt8TcShapes
 };
-int int8_tc_cols(Int8TcShape shape);  // columns of a tile (of 256 rows)
-int int8_tc_step();                   // elements of k a stage
-int int8_tc_shares(Int8TcShape shape);  // shares of k that a cluster's pairs can join among themselves
+constexpr int64_t kInt8TcStep = 128;  // elements of k a stage
 // How many clusters of one, two and four pairs of CTAs run at once.
 struct Int8TcClusters {
   int pairs, twos, fours;
@@ -76,7 +73,7 @@ cudaError_t launch_int8_tc(Int8TcShape shape, const CUtensorMap (&maps)[3], cons
                            cudaStream_t stream);
 
 // ---- the same for few tokens and for small products (int8_few.cu): y = X W^T
-int int8_few_tokens();  // up to which it is always taken
+constexpr int kInt8FewTokens = 8;  // up to which it is always taken
 struct Int8FewArgs {
   const int8_t* w;
   int64_t ldw;
@@ -92,7 +89,6 @@ struct Int8FewArgs {
   int32_t dtype;         // of y
 };
 bool int8_few_quantises(int64_t tokens, int64_t n, int64_t k, int sms);  // whether it takes unquantised tokens (one)
-double int8_few_estimate(int64_t tokens, int64_t n, int64_t k);          // its time with tokens of integers, us
 // type_x: the unquantised token's type, or < 0.
 cudaError_t launch_int8_few(int type_x, const Int8FewArgs& args, int sms, cudaStream_t stream);
 
@@ -109,7 +105,8 @@ struct Int8GradArgs {
   void* dw;
   int64_t ldw;
 };
-double int8_grad_estimate(int dtype, const Int8GradArgs& args);  // us
+constexpr int kInt8GradTile = 32, kInt8GradWarps = 4, kInt8GradStep = 64;  // channels and columns of dy a block, its warps, tokens of a warp's step
+bool int8_grad_vec(const Int8GradArgs& args);  // whether it reads dy 16 bytes at a time
 cudaError_t launch_int8_grad(int dtype, const Int8GradArgs& args, cudaStream_t stream);
 
 }  // namespace gb300

@@ -7,10 +7,10 @@
 // kind::f16 with its 32-bit accumulator adds up to 1024 of them exactly
 // (128 * 128 * 1024 = 2^24).  Integer sums are taken 1024 products at a time and
 // added as integers.  A checkpoint's values q * u (q at most seven bits, u a
-// power of two) are exact in 16 bits too; a gradient's sums stay in the
-// accumulator for 16-bit outputs, and are added up 512 tokens at a time in
-// registers for 32-bit ones (the tensor core cuts what it shifts out; over thousands
-// of additions that shows in 32 bits).
+// power of two) are exact in 16 bits too.  The tensor core cuts off what is below
+// the accumulator's last place, so a gradient's sums leave it every 512 tokens
+// for 32-bit outputs, and for 16-bit ones before it shows (int8_most_tokens()); they
+// are added up in registers.
 //
 // Structure.  Two CTAs on two SMs share a tile of 256 rows x kN columns
 // (tcgen05.mma.cta_group::2): each supplies 128 rows of `a` and stages half of b's columns.
@@ -32,8 +32,9 @@
 // active 96 % of the time at the 1.78 GHz that power leaves; with 128 columns the converting warps bound it (390 us).
 // 8192^3 of integers (128 columns, 8 runs a tile): 566 us, 1942 TFLOP/s, tensor pipe 87 %, L2 to SM 14.8 TB/s.  256 columns
 // have one accumulator, so that a tile's (or a run's) sums are read before the next one's first product; that costs
-// little after the 128 stages of a gradient's tile, and much after the 8 of a run, so products of integers have 128 columns
-// and two accumulators.  With the first operand in tensor memory an MMA of 32 or 64 columns takes as long as one of 128
+// little after the 128 stages of a gradient's tile, 5 % after runs of 16 (16384 tokens, 4096 x 4096 bfloat16: runs of 4, 8, 16 and 32 377, 348,
+// 331 and 334 us, without any 313; runs of 4 in tiles of 128 columns 397), and much after the 8 of a run of integers, whose products have
+// 128 columns and two accumulators.  With the first operand in tensor memory an MMA of 32 or 64 columns takes as long as one of 128
 // (0.28 us a stage, 0.34 on every SM at once): small tiles only spread few columns over more SMs.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -43,6 +44,7 @@
 #include "fp4_tc.cuh"
 #include "int8_device.cuh"
 #include "int8_internal.h"
+#include "int8_plan.h"
 #include "sgemm_device.cuh"
 #include "sgemm_internal.h"
 
@@ -57,7 +59,7 @@ using fp4::operand_desc;
 using fp4::uniform_warp;
 
 constexpr uint32_t kStatusTimeout = 3;
-constexpr int kStep = 128;               // elements of k a stage
+constexpr int kStep = int(kInt8TcStep);
 constexpr int kRows = 128;               // of a CTA
 constexpr int kGroups = 2;               // of four warps that turn `a` to 16 bits
 
@@ -70,6 +72,10 @@ struct Tile {
   static constexpr int kN = kN_;
   static constexpr bool kRuns = kRuns_;  // sums leave the accumulator every `run` stages
   static constexpr bool kUnits = kKind != kIntegers;
+  // The epilogue's sums of 256 columns take 128 registers a thread; the threads that turn `a` to 16 bits leave it theirs and
+  // write half as much at a time.
+  static constexpr bool kWideRuns = kRuns && kN == 256;
+  static constexpr int kWords = kWideRuns ? 16 : 32;
   static constexpr int kCols = kN / 2;   // of b, a CTA
   static constexpr uint32_t kABytes = kRows * kStep, kUBytes = kUnits ? 1024 : 0, kBBytes = kCols * kStep * 2;
   static constexpr int kAccs = kN <= 128 ? 2 : 1;
@@ -144,7 +150,14 @@ __device__ __forceinline__ void read_tmem(uint32_t taddr, float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void write_tmem32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void write_tmem(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void write_tmem(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
@@ -343,7 +356,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   };
   auto going = [&]() { return __shfl_sync(0xffffffffu, *s_abort, 0) == 0; };
 
-  // 640 threads have 96 registers each; these four warps give up what the epilogue's sums need.
+  // 640 threads have 96 registers each (61440); these four warps, and with 256 columns of runs the eight that turn `a`, give up
+  // what the epilogue's sums need: 128 * 32 + 256 * 96 + 256 * 128, or 128 * 32 + 256 * 56 + 256 * 168.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0) {
@@ -438,6 +452,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     }
   } else if (warp < 4 + 4 * kGroups) {
     // ---- `a` to 16 bits, in tensor memory
+    if constexpr (S::kWideRuns) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     const int q = warp & 3, group = (warp - 4) >> 2, row = 32 * q + lane;
     const uint32_t to = slots + (uint32_t(32 * q) << 16);
     At<S::kStages> s;
@@ -453,13 +468,13 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         const uint4* from = reinterpret_cast<const uint4*>(s_a + s.i * S::kABytes + row * 128);
         const unsigned char* units = s_u + s.i * S::kUBytes;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 in[4];
+        for (int h = 0; h < 64 / S::kWords; ++h) {
+          uint4 in[S::kWords / 8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) in[j] = from[(4 * h + j) ^ (row & 7)];
-          uint32_t out[32];
+          for (int j = 0; j < S::kWords / 8; ++j) in[j] = from[(S::kWords / 8 * h + j) ^ (row & 7)];
+          uint32_t out[S::kWords];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < S::kWords / 8; ++j) {
             const uint32_t word[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
             if constexpr (S::kUnits) {
               // 16 units, two 16-byte pieces of row q (its second 64 in the second box) of the swizzled boxes.
@@ -467,7 +482,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 #pragma unroll
               for (int p = 0; p < 2; ++p)
                 *reinterpret_cast<uint4*>(u + 4 * p) = *reinterpret_cast<const uint4*>(
-                    units + h * 512 + q * 128 + (((2 * j + p) ^ (q + 4 * h)) << 4));
+                    units + (S::kWords * h / 32) * 512 + q * 128 + (((2 * (S::kWords / 8 * h % 4 + j) + p) ^ (q + 4 * (S::kWords * h / 32))) << 4));
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 if constexpr (S::kKind == kBf16) {
@@ -492,11 +507,12 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             wait(&slot_empty[t.i], t.parity ^ 1u);
             __syncwarp();
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          } else {
+          }
+          if (h == 64 / S::kWords - 1) {
             __syncwarp();
             if (lane == 0) dev::mbar_arrive(&a_empty[s.i]);
           }
-          write_tmem32(to + t.i * S::kSlotCols + 32 * h, out);
+          write_tmem(to + t.i * S::kSlotCols + S::kWords * h, out);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -505,7 +521,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    if constexpr (S::kWideRuns)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     // ---- epilogue: 32 rows x kV columns a warp
     const int q = warp & 3, half = (warp - 4 - 4 * kGroups) >> 2;
     const uint32_t lanes = uint32_t(32 * q) << 16;
@@ -514,7 +533,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const Work w = work_of(args, unit, S::kN);
       const int row = w.r0 + int(rank) * kRows + 32 * q + lane, col0 = w.c0 + half * S::kV;
       const bool mine = row < args.rows;
-      constexpr int kPart = S::kV < 32 ? S::kV : 32;
+      constexpr int kPart = S::kWideRuns ? 16 : S::kV < 32 ? S::kV : 32;
       auto put_partials = [&](int c0, const uint32_t* bits) {
         uint32_t* out = args.partials + (int64_t(w.part) * args.cols + col0 + c0) * args.rows + row;
 #pragma unroll
@@ -533,7 +552,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         if (lane == 0) arrive_at(place_in(&acc_empty[b.i], leader));
         b.next();
       };
-      if constexpr (S::kMaxShares > 1) {
+      if constexpr (S::kRuns || S::kMaxShares > 1) {
         if (S::kRuns || args.join) {
           // Scales of this warp's columns, 32 a register; a row's.
           float scale_c[(S::kV + 31) / 32], scale_r = 0.f;
@@ -611,11 +630,13 @@ __global__ void __launch_bounds__(S::kThreads, 1)
               store(Int<o * kOwn>(), Int<kOwn>());
             });
           };
-          if (args.join) {
-            if (args.splits == 2)
-              meet(Int<2>());
-            else
-              meet(Int<4>());
+          if (S::kMaxShares > 1 && args.join) {
+            if constexpr (S::kMaxShares > 1) {
+              if (args.splits == 2)
+                meet(Int<2>());
+              else
+                meet(Int<4>());
+            }
           } else if (ok) {
             for_parts<S::kV / kPart>([&](auto i) {
               if (args.splits > 1)
@@ -703,33 +724,34 @@ typedef void (*Kernel)(CUtensorMap, CUtensorMap, CUtensorMap, Int8TcArgs);
 struct Instance {
   Kernel kernel;
   size_t smem;
-  int threads, cols, shares;
+  int threads;
 };
-template <Kind kKind, int kN, bool kRuns>
+template <int kShape, Kind kKind, int kN, bool kRuns>
 Instance instance_of() {
   using S = Tile<kKind, kN, kRuns>;
-  return {Kernel(product_kernel<S>), S::kSmem, S::kThreads, kN, S::kMaxShares};
+  constexpr Int8TcForm kForm = int8_tc_form(kShape);
+  static_assert(kForm.cols == kN && kForm.shares == S::kMaxShares && (kForm.run > 0) == kRuns, "what plans are made with");
+  static_assert(!kForm.terms || (kRuns && S::kSlots >= kForm.run), "a run's stages of `a` stay until its last term");
+  return {Kernel(product_kernel<S>), S::kSmem, S::kThreads};
 }
 
 Instance instance(int shape) {
   switch (shape) {
-    case kInt8Whole32: return instance_of<kIntegers, 32, true>();
-    case kInt8Whole64: return instance_of<kIntegers, 64, true>();
-    case kInt8Whole128: return instance_of<kIntegers, 128, true>();
-    case kInt8Bf16N128: return instance_of<kBf16, 128, false>();
-    case kInt8Bf16N256: return instance_of<kBf16, 256, false>();
-    case kInt8Bf16Runs: return instance_of<kBf16, 128, true>();
-    case kInt8F16N128: return instance_of<kF16, 128, false>();
-    case kInt8F16N256: return instance_of<kF16, 256, false>();
-    default: return instance_of<kF16, 128, true>();
+    case kInt8Whole32: return instance_of<kInt8Whole32, kIntegers, 32, true>();
+    case kInt8Whole64: return instance_of<kInt8Whole64, kIntegers, 64, true>();
+    case kInt8Whole128: return instance_of<kInt8Whole128, kIntegers, 128, true>();
+    case kInt8Bf16N128: return instance_of<kInt8Bf16N128, kBf16, 128, false>();
+    case kInt8Bf16N256: return instance_of<kInt8Bf16N256, kBf16, 256, false>();
+    case kInt8Bf16Runs: return instance_of<kInt8Bf16Runs, kBf16, 128, true>();
+    case kInt8Bf16Runs256: return instance_of<kInt8Bf16Runs256, kBf16, 256, true>();
+    case kInt8F16N128: return instance_of<kInt8F16N128, kF16, 128, false>();
+    case kInt8F16N256: return instance_of<kInt8F16N256, kF16, 256, false>();
+    case kInt8F16Runs256: return instance_of<kInt8F16Runs256, kF16, 256, true>();
+    default: return instance_of<kInt8F16Runs, kF16, 128, true>();
   }
 }
 
 }  // namespace
-
-int int8_tc_cols(Int8TcShape shape) { return instance(shape).cols; }
-int int8_tc_shares(Int8TcShape shape) { return instance(shape).shares; }
-int int8_tc_step() { return kStep; }
 
 bool int8_tc_prepare(Int8TcClusters* n) {
   *n = Int8TcClusters{};
@@ -738,7 +760,7 @@ bool int8_tc_prepare(Int8TcClusters* n) {
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(in.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(in.smem)) != cudaSuccess)
       return false;
-    for (int pairs = 1; pairs <= in.shares; pairs *= 2) {
+    for (int pairs = 1; pairs <= int8_tc_form(shape).shares; pairs *= 2) {
       cudaLaunchAttribute attr = {};
       attr.id = cudaLaunchAttributeClusterDimension;
       attr.val.clusterDim.x = unsigned(2 * pairs);

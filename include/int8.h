@@ -123,8 +123,10 @@ sgemm_status_t int8_restore(const int8_checkpoint_t *c, int dtype, void *y, int6
  * Every product is exact and sums are kept in 32 bits: INT8_F32 gradients are
  * taken as three bfloat16 terms, which hold all of their 24 bits from 2^-110
  * on, 16-bit ones as they are.  The tensor core cuts off what is below an
- * accumulator's last place; for dW of INT8_F32 the sums leave it every 512
- * tokens and are added, correctly rounded, elsewhere.  No tokens: zeros, or dW as it was.  At most 2^27 tokens and an N of 2^29.
+ * accumulator's last place, at most 6.5e-9 of a sum for each token (measured on sums of one sign); the sums
+ * leave it, and are added, correctly rounded, elsewhere, after at most 512 tokens for dW of INT8_F32,
+ * 2048 for INT8_F16 and 16384 for INT8_BF16, which is 1/30 of half a step of the 16-bit types.
+ * No tokens: zeros, or dW as it was.  At most 2^27 tokens and an N of 2^29.
  */
 sgemm_status_t int8_weight_grad(const void *dy, int64_t lddy, int64_t N, const int8_checkpoint_t *c, int dtype,
                                 int32_t accumulate, void *dw, int64_t ldw, cudaStream_t stream);

@@ -92,11 +92,12 @@ __device__ __forceinline__ bool finite(float a) { return __float_as_uint(a) < 0x
 // The integer nearest to x / s, ties to even, for |x| <= 127 s (1 + 2^-22) and s >= 2^-126,
 // with inv the rounded reciprocal of s.  x inv is within 2^-15 of x / s, so its nearest
 // integer n is the answer or next to it, and the remainder x - n s says which: it is a
-// multiple of the last place of s and at most s, so that the fma gives it exactly.
+// multiple of the last place of s and at most s, so that the fma gives it exactly.  Twice the remainder is exact too; half of
+// s would not be below 2^-125.
 __device__ __forceinline__ int nearest(float x, float s, float inv) {
-  const float n = rintf(x * inv), r = fmaf(-n, s, x), h = 0.5f * s;
+  const float n = rintf(x * inv), r = fmaf(-n, s, x), d = fabsf(r) + fabsf(r);
   int q = int(n);
-  if (fabsf(r) > h || (fabsf(r) == h && (q & 1))) q += r > 0.f ? 1 : -1;
+  if (d > s || (d == s && (q & 1))) q += r > 0.f ? 1 : -1;
   return q;
 }
 

@@ -28,6 +28,19 @@ constexpr Int8TcForm int8_tc_form(int shape) {
                                                                  : Int8TcForm{128, 4, 4, true};
 }
 
+// The fewest clusters of each size that any form of the kernel can have at once: none if one form cannot have them.
+class Int8LeastClusters {
+ public:
+  void take(int pairs, int clusters) {  // of 1, 2 or 4 pairs
+    int& least = least_[pairs / 2];
+    if (least < 0 || clusters < least) least = clusters;
+  }
+  Int8TcClusters clusters() const { return {std::max(least_[0], 0), std::max(least_[1], 0), std::max(least_[2], 0)}; }
+
+ private:
+  int least_[3] = {-1, -1, -1};  // (not known yet)
+};
+
 // Tokens whose sums may stay in one accumulator of the tensor core.  An MMA adds 16 of them and cuts off what is below the
 // accumulator's last place: with sums of one sign 6.5e-9 of the sum a token were measured to be lost (over 262144 tokens 1.7e-3).
 // For results of 32 bits sums leave it every 512 tokens.  For those of 16 bits the loss stays below 1/30 of half a step of the

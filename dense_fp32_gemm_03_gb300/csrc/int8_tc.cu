@@ -754,7 +754,7 @@ Instance instance(int shape) {
 }  // namespace
 
 bool int8_tc_prepare(Int8TcClusters* n) {
-  *n = Int8TcClusters{};
+  Int8LeastClusters least;
   for (int shape = 0; shape < kInt8TcShapes; ++shape) {
     const Instance in = instance(shape);
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(in.kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -773,10 +773,10 @@ bool int8_tc_prepare(Int8TcClusters* n) {
       cfg.numAttrs = 1;
       int most = 0;
       if (cudaOccupancyMaxActiveClusters(&most, reinterpret_cast<const void*>(in.kernel), &cfg) != cudaSuccess) return false;
-      int& to = pairs == 1 ? n->pairs : pairs == 2 ? n->twos : n->fours;
-      if (to == 0 || most < to) to = most;
+      least.take(pairs, most);
     }
   }
+  *n = least.clusters();
   return n->pairs > 0;
 }
 

@@ -1,5 +1,7 @@
 """Plans of the 8-bit integer operators' products (no GPU needed)."""
+import os
 import random
+import subprocess
 
 import pytest
 import torch
@@ -58,3 +60,34 @@ def test_plans_cover_the_product_once():
 def test_tiles_of_large_gradients(size, kept, out, want):
     p = int8_plans.gradient(*size, kept, out)
     assert not p.small and (p.cols, p.run) == want
+
+
+def test_clusters_that_one_form_cannot_have_are_not_planned(tmp_path):
+    """The counts that plans are made with are the least of all forms', a zero among them, whatever their order."""
+    source = tmp_path / "least.cpp"
+    source.write_text("""
+        #include <cstdio>
+        #include "int8_plan.h"
+        int main() {
+          for (int zero = 0; zero < 3; ++zero) {
+            gb300::Int8LeastClusters least;
+            for (int form = 0; form < 3; ++form) {
+              least.take(1, 76 - form);
+              least.take(2, form == zero ? 0 : 38 + form);
+            }
+            const gb300::Int8TcClusters n = least.clusters();
+            std::printf("%d %d %d\\n", n.pairs, n.twos, n.fours);
+          }
+        }""")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    exe = str(tmp_path / "least")
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(int8_plans.ROOT, "dense_fp32_gemm_03_gb300", "csrc"), "-I",
+                    os.path.join(int8_plans.ROOT, "include"), "-I", os.path.join(cuda, "include"), str(source), "-o", exe], check=True)
+    assert subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split("\n")[:3] == ["74 0 0"] * 3
+
+
+@pytest.mark.parametrize("clusters", [(76, 0, 18), (76, 38, 0), (76, 0, 0)])
+def test_plans_without_some_clusters(clusters):
+    for m, n, k in ((128, 4096, 4096), (4096, 1024, 1024), (1200, 520, 700)):
+        for p in (int8_plans.product(m, n, k, clusters=clusters), int8_plans.gradient(m, n, k, BF16, clusters=clusters)):
+            assert p.ok and (not p.join or clusters[p.splits // 2] > 0)

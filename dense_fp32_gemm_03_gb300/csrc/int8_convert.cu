@@ -335,7 +335,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) keep_kernel(const KeepArgs a) {
   begin();
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
-  __shared__ uint32_t codes[128 * 32];
+  __shared__ __align__(16) uint32_t codes[128 * 32];
   __shared__ __align__(16) uint16_t units[4][128];
   const int64_t t0 = int64_t(blockIdx.x % a.tiles_t) * 128, k0 = int64_t(blockIdx.x / a.tiles_t) * 128;
   const int g = threadIdx.x % 16;  // group of eight channels
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) restore_tokens_kernel(const RestoreA
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(128) restore_channels_kernel(const RestoreArgs a) {
   begin();
-  __shared__ int8_t tile[32][68];
+  __shared__ __align__(16) int8_t tile[32][68];
   __shared__ __align__(16) float scratch_[kVec ? 4 : 8 * 128];
   float* const scratch = scratch_ + (kVec ? 0 : threadIdx.x / 32 * 256);
   const int64_t blocks = (a.cols + 31) / 32, tiles = (a.rows + 63) / 64 * blocks;

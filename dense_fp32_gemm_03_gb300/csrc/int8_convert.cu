@@ -469,8 +469,9 @@ struct SwigluArgs {
   Chunks n;
 };
 
-// 16-bit types: the exponential of the rounded product x log2(e), within (|x| + 2) 2^-23 of itself, and a reciprocal
-// within 2^-23: far below the types' own steps.  32 bits: within 2^-22 whatever x is.
+// For x >= kFar.  16-bit types: the exponential of the rounded product x log2(e), within (|x| + 2) 2^-23 of itself, and a reciprocal
+// within 2^-23: far below the types' own steps.  32 bits: within 2^-22.
+constexpr float kFar = -80.f;
 template <typename T>
 __device__ __forceinline__ float sigmoid(float x) {
   if constexpr (sizeof(T) == 4) {
@@ -483,9 +484,37 @@ __device__ __forceinline__ float sigmoid(float x) {
   }
 }
 
-// Keeps kN of a block's values (the block's 32 / kN lanes together).
+// Below kFar the sigmoid is e^x, which leaves the range of 32 bits where a product with it need not (e^x times 1e38 counts
+// down to x = -176): what depends on such a gate is computed again, in 64 bits, and written over, by a second pass of the threads
+// that saw one (each over its own values: what other lanes wrote for it, write8() has ordered).  (fp16 cannot hold what comes out.)  Hardly any does; within the first pass it would cost that registers
+// (8192 x 8192 bf16, back: 84 us, 100 with a branch in the loop).
+__device__ __forceinline__ double far_sigmoid(float x) {
+  const double t = expf(0.5f * x);
+  return t * t;
+}
+template <typename T>
+__device__ __forceinline__ void far_swiglu(const T* gate, const T* up, T* h, int n) {
+#pragma unroll 1
+  for (int e = 0; e < n; ++e) {
+    const float g = to_f32(gate[e]);
+    if (g < kFar) h[e] = from_f32<T>(float(double(g) * far_sigmoid(g) * double(to_f32(up[e]))));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void far_gradients(const T* dh, const int8_t* kg, float ug, const int8_t* ku, float uu, T* dgate, T* dup, int n) {
+#pragma unroll 1
+  for (int e = 0; e < n; ++e) {
+    const float g = float(kg[e]) * ug, u = float(ku[e]) * uu;
+    if (!(g < kFar)) continue;
+    const double s = far_sigmoid(g), d = double(to_f32(dh[e])) * s;
+    dgate[e] = from_f32<T>(float(d * double(u) * (1.0 + double(g) * (1.0 - s))));
+    dup[e] = from_f32<T>(float(d * double(g)));
+  }
+}
+
+// Keeps kN of a block's values (the block's 32 / kN lanes together); the largest magnitude of them all.
 template <bool kHalf, int kN>
-__device__ __forceinline__ void keep_block(const float (&v)[kN / 8][8], int8_t* codes, uint16_t* unit, bool first, bool write) {
+__device__ __forceinline__ float keep_block(const float (&v)[kN / 8][8], int8_t* codes, uint16_t* unit, bool first, bool write) {
   float top = largest8(v[0]), t[8];
   if constexpr (kN > 8) top = max_abs(top, largest8(v[1]));
   top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -503,6 +532,7 @@ __device__ __forceinline__ void keep_block(const float (&v)[kN / 8][8], int8_t* 
     if (write) *reinterpret_cast<uint4*>(codes) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
   }
   if (write && first) *unit = uint16_t(of.bits);
+  return top;
 }
 
 // 32 / kN lanes to a block; a row's columns are rounded up to whole blocks so that a block's lanes stay together.
@@ -514,6 +544,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
   constexpr int kLanes = 32 / kN;
   const int64_t blocks = (a.cols + 31) / 32;
+  bool far = false;
   for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
     const bool here = w.at(a.n, 0, row, c);
@@ -533,21 +564,32 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluArgs a) {
       write8<kVec>(static_cast<T*>(a.h) + row * a.ldh + kN * c + 8 * p, left, scratch, h);
     }
     const bool write = here && kN * c < (a.cols + 15) / 16 * 16;
-    keep_block<kHalf, kN>(g, a.kg + row * a.ldkg + kN * c, a.ug + row * a.ldug + c / kLanes, c % kLanes == 0, write);
+    const float top = keep_block<kHalf, kN>(g, a.kg + row * a.ldkg + kN * c, a.ug + row * a.ldug + c / kLanes, c % kLanes == 0, write);
+    far = far || !(top <= -kFar);
     keep_block<kHalf, kN>(u, a.ku + row * a.ldku + kN * c, a.uu + row * a.lduu + c / kLanes, c % kLanes == 0, write);
     // Units that pad the row.
     if (here && c % kLanes == 0 && c / kLanes == blocks - 1)
       for (int64_t b = blocks; b < (blocks + 7) / 8 * 8; ++b) a.ug[row * a.ldug + b] = a.uu[row * a.lduu + b] = 0;
   }
+  if constexpr (!kHalf) {
+    if (!far) return;
+    for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
+      int64_t row, c;
+      if (w.at(a.n, 0, row, c))
+        far_swiglu(static_cast<const T*>(a.gate) + row * a.ldg + kN * c, static_cast<const T*>(a.up) + row * a.ldu + kN * c,
+                   static_cast<T*>(a.h) + row * a.ldh + kN * c, int(min(a.cols - kN * c, int64_t(kN))));
+    }
+  }
 }
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluArgs a, const T* dh, int64_t lddh, T* dgate,
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && kVec ? 8 : 5) swiglu_backward_kernel(const SwigluArgs a, const T* dh, int64_t lddh, T* dgate,
                                                                    int64_t lddg, T* dup, int64_t lddu) {
   begin();
   constexpr bool kHalf = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
   __shared__ __align__(16) float scratch_[kVec ? 4 : 8 * kThreads];
   float* const scratch = scratch_ + (kVec ? 0 : threadIdx.x / 32 * 256);
+  bool far = false;
   for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
     int64_t row, c;
     const bool here = w.at(a.n, 0, row, c);
@@ -571,6 +613,18 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluA
     }
     write8<kVec>(dgate + row * lddg + 8 * c, left, scratch, g);
     write8<kVec>(dup + row * lddu + 8 * c, left, scratch, u);
+    far = far || !(ug <= 0.5f);  // (a block whose values are below 64 has a unit of 1/2 or less)
+  }
+  if constexpr (!kHalf) {
+    if (!far) return;
+    for (Walk<1> w(a.n); w.left > 0; w.next(a.n)) {
+      int64_t row, c;
+      if (!w.at(a.n, 0, row, c)) continue;
+      const float ug = unit_value(a.ug[row * a.ldug + c / 4], false), uu = unit_value(a.uu[row * a.lduu + c / 4], false);
+      if (!(ug <= 0.5f))
+        far_gradients(dh + row * lddh + 8 * c, a.kg + row * a.ldkg + 8 * c, ug, a.ku + row * a.ldku + 8 * c, uu,
+                      dgate + row * lddg + 8 * c, dup + row * lddu + 8 * c, int(min(a.cols - 8 * c, int64_t(8))));
+    }
   }
 }
 

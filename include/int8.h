@@ -135,7 +135,10 @@ sgemm_status_t int8_weight_grad(const void *dy, int64_t lddy, int64_t N, const i
  * The gated activation h = gate * sigmoid(gate) * up, elementwise on M x F
  * matrices of type `dtype`, each with a row stride of its own; the two
  * checkpoints (M x F, that type, order INT8_TOKENS) receive gate and up for
- * the backward pass.  h is computed in 32 bits from gate and up themselves.
+ * the backward pass.  h is computed in 32 bits from gate and up themselves, the
+ * sigmoid within 2^-22 of itself, or for 16-bit types within (|gate| + 4) 2^-22 (approximate
+ * exponential and reciprocal).  Where the sigmoid leaves the range of 32 bits, for gates below -80,
+ * its products are computed in 64 (not for INT8_F16, which cannot hold what comes out).
  */
 sgemm_status_t int8_swiglu(int dtype, int64_t M, int64_t F, const void *gate, int64_t ld_gate, const void *up,
                            int64_t ld_up, void *h, int64_t ld_h, const int8_checkpoint_t *kept_gate,
@@ -143,8 +146,8 @@ sgemm_status_t int8_swiglu(int dtype, int64_t M, int64_t F, const void *gate, in
 
 /*
  * Its backward pass from the kept values g and u, with s = sigmoid(g):
- * dgate = dh * u * s * (1 + g * (1 - s)) and dup = dh * g * s, in 32 bits,
- * rounded once to the checkpoints' type, which all matrices have.
+ * dgate = dh * u * s * (1 + g * (1 - s)) and dup = dh * g * s, in 32 bits
+ * (from left to right; gates below -80 as above), rounded once to the checkpoints' type, which all matrices have.
  */
 sgemm_status_t int8_swiglu_backward(const void *dh, int64_t ld_dh, const int8_checkpoint_t *kept_gate,
                                     const int8_checkpoint_t *kept_up, void *dgate, int64_t ld_dgate, void *dup,

@@ -101,14 +101,17 @@ bool overlap_any(Range a, std::initializer_list<Range> others) {
     if (overlap(a, b)) return true;
   return false;
 }
-// Whether the rows of two matrices of one shape and type share memory; rows of one may lie between the other's
-// (halves of the rows of one tensor).
-bool rows_overlap(int64_t rows, int64_t bytes, const void* a, int64_t lda, const void* b, int64_t ldb) {
-  const Range ra = range(a, (rows - 1) * lda + bytes), rb = range(b, (rows - 1) * ldb + bytes);
-  if (rows <= 0 || bytes <= 0 || !overlap(ra, rb)) return false;
+// Whether the rows of two matrices (of bytes_a and bytes_b each) share memory; rows of one may lie between the other's (parts of
+// the rows of one tensor).
+bool rows_overlap(int64_t rows, int64_t bytes_a, const void* a, int64_t lda, int64_t bytes_b, const void* b, int64_t ldb) {
+  const Range ra = range(a, (rows - 1) * lda + bytes_a), rb = range(b, (rows - 1) * ldb + bytes_b);
+  if (rows <= 0 || bytes_a <= 0 || bytes_b <= 0 || !overlap(ra, rb)) return false;
   if (lda != ldb) return true;
   const int64_t shift = (int64_t(rb.lo - ra.lo) % lda + lda) % lda;  // from a row of a to the next of b's
-  return shift < bytes || shift + bytes > lda;
+  return shift < bytes_a || shift + bytes_b > lda;
+}
+bool rows_overlap(int64_t rows, int64_t bytes, const void* a, int64_t lda, const void* b, int64_t ldb) {
+  return rows_overlap(rows, bytes, a, lda, bytes, b, ldb);
 }
 
 // C = 0 for an empty sum.
@@ -299,7 +302,9 @@ sgemm_status_t int8_linear(int dtype, const void* x, int64_t ldx, int64_t M, con
   if (st == SGEMM_OK) st = check_dense(dtype, y, M, W->rows, ldy);
   if (st != SGEMM_OK) return st;
   if (W->cols > kMaxDepth) return SGEMM_ERR_UNSUPPORTED;
-  if (overlap_any(dense_range(dtype, y, M, W->rows, ldy), {code_range(W), scale_range(W), dense_range(dtype, x, M, W->cols, ldx)}))
+  const int64_t es = dtype_bytes(dtype);
+  if (overlap_any(dense_range(dtype, y, M, W->rows, ldy), {code_range(W), scale_range(W)}) ||
+      rows_overlap(M, W->rows * es, y, ldy * es, W->cols * es, x, ldx * es))
     return SGEMM_ERR_INVALID_VALUE;
   LibDevice d;
   st = gb300::lib_device(&d);

@@ -485,9 +485,10 @@ __device__ __forceinline__ float sigmoid(float x) {
 }
 
 // Below kFar the sigmoid is e^x, which leaves the range of 32 bits where a product with it need not (e^x times 1e38 counts
-// down to x = -176): what depends on such a gate is computed again, in 64 bits, and written over, by a second pass of the threads
-// that saw one (each over its own values: what other lanes wrote for it, write8() has ordered).  (fp16 cannot hold what comes out.)  Hardly any does; within the first pass it would cost that registers
-// (8192 x 8192 bf16, back: 84 us, 100 with a branch in the loop).
+// down to x = -176): what depends on such a gate is computed again, in 64 bits, and written over, by a second pass of the
+// threads that saw one.  (Each goes over its own values; what other lanes wrote for it, write8() has ordered.  fp16 cannot hold
+// what comes out.)  Hardly any thread does; within the first pass it would cost that registers (8192 x 8192 bf16, back: 84 us,
+// with a branch in the loop 100).
 __device__ __forceinline__ double far_sigmoid(float x) {
   const double t = expf(0.5f * x);
   return t * t;

@@ -57,7 +57,7 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
 
 // The same for rows that start anywhere, by whole warps: each lane's eight values pass through `scratch`, 256 numbers of the
 // warp's, so that 32 elements after one another are written at a time and not every eighth (dequantising 16384 x 4097
-// bfloat16 177 -> 61 us).  Reads are better off with every eighth, which the L1 cache serves (quantising it 65 us, with
+// bfloat16 177 -> 61 us).  Reads are better off with every eighth, which the L1 cache serves (quantising it 55 to 65 us, with
 // reads like this 123).  `left` may be anything; lanes of none do not touch memory.
 template <typename T>
 __device__ __forceinline__ void scatter8(T* p, int64_t left, float* scratch, const float (&v)[8]) {

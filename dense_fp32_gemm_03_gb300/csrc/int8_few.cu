@@ -13,7 +13,7 @@
 // kernel that quantises, 16.2 if that one writes 16-bit floats in the lanes' order); the first of W is requested before
 // that kernel is done.  A single token of moderate length is quantised by every block for itself, into shared memory
 // while its first loads of W are on the way.  More tokens are taken eight by eight where the product is so small that the
-// launches of the tiled kernel and of the one before it would be most of its time (300 x 520 x 200 6.1 -> 3.6 us, 128 tokens
+// launches of the tiled kernel and of the one before it would be most of its time (300 x 520 x 200 6.1 -> 3.4 us, 128 tokens
 // of 512 x 512 6.8 -> 2.7).
 #include <cuda_runtime.h>
 
@@ -225,11 +225,11 @@ Kernel kernel_of(int64_t rows, int warps) {
 }
 
 // How W is shared out.  Up to eight tokens, as many warps a block as leave all blocks at work at once, 16 warps on an SM (5000 x
-// 4096 in 313 blocks of eight warps takes 9.6 us, 4096 x 4096 in 256 7.1): 4096 rows are 256 blocks of eight warps, 8192 rows
+// 4096 in 313 blocks of eight warps takes 9.6 us, 4096 x 4096 in 256 6.9): 4096 rows are 256 blocks of eight warps, 8192 rows
 // 256 of eight or 512 of four.  A block has 32 rows, which halves what it spends on its tokens, where that leaves 200 blocks
 // (products with one token of integers, 16384 x 16384 55 -> 46.4 us, 14336 x 4096 16.2 -> 12.9; 8 tokens of 1024 x 8192, 32
 // blocks, 7 -> 10).  More tokens come eight by eight, in blocks of two to eight warps (300 x 520 x 200, 646 blocks: four warps
-// each 4.3 us, two 3.6).
+// each 4.3 us, two 3.4).
 struct Shares {
   int64_t rows, blocks;
   int warps;
@@ -244,7 +244,7 @@ Shares shares(int64_t tokens, int64_t n, int64_t k, int sms) {
 
 }  // namespace
 
-// Up to 16 values a thread (1024 x 1024: 2.8 us in a graph, 3.9 with a kernel before; 4096 x 4096: 6.6 and 6.9, and 1.5 us
+// Up to 16 values a thread (1024 x 1024: 2.8 us in a graph, 3.9 with a kernel before; 4096 x 4096, 6.9 us, 0.3 less, and 1.5 us
 // less of host time; 8192 x 8192, 32 a thread: 15.4 and 14.6).
 bool int8_few_quantises(int64_t tokens, int64_t n, int64_t k, int sms) {
   return tokens == 1 && k <= 16 * 32 * shares(1, n, k, sms).warps;

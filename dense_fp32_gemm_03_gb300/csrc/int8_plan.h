@@ -110,7 +110,7 @@ struct Int8Plan {
   Int8TcShape shape;
   Int8TcArgs a;
 };
-// Up to eight tokens int8_few.cu.  More go there eight by eight where that is estimated to be faster: 300 x 520 x 200 3.6 us (in
+// Up to eight tokens int8_few.cu.  More go there eight by eight where that is estimated to be faster: 300 x 520 x 200 3.4 us (in
 // tiles 6.1), 512 x 1024 x 1024 13.5 (8.7).  4 us: the kernel that prepares b, and launches.
 inline Int8Plan int8_plan_product(int64_t m, int64_t n, int64_t k, bool quantised, const Int8TcClusters& most) {
   Int8Plan p{true, true, kInt8Whole32, {}};

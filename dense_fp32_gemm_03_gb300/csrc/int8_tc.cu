@@ -32,9 +32,9 @@
 // active 96 % of the time at the 1.78 GHz that power leaves; with 128 columns the converting warps bound it (390 us).
 // 8192^3 of integers (128 columns, 8 runs a tile): 566 us, 1942 TFLOP/s, tensor pipe 87 %, L2 to SM 14.8 TB/s.  256 columns
 // have one accumulator, so that a tile's (or a run's) sums are read before the next one's first product; that costs
-// little after the 128 stages of a gradient's tile, 5 % after runs of 16 (16384 tokens, 4096 x 4096 bfloat16: runs of 4, 8, 16 and 32 377, 348,
-// 331 and 334 us, without any 313; runs of 4 in tiles of 128 columns 397), and much after the 8 of a run of integers, whose products have
-// 128 columns and two accumulators.  With the first operand in tensor memory an MMA of 32 or 64 columns takes as long as one of 128
+// little after the 128 stages of a gradient's tile, 5 % after runs of 16 (16384 tokens, 4096 x 4096 bfloat16: runs of 4, 8, 16
+// and 32 377, 348, 331 and 334 us, without any 313; runs of 4 in tiles of 128 columns 397), and much after the 8 of a run of
+// integers, whose products have 128 columns and two accumulators.  With the first operand in tensor memory an MMA of 32 or 64 columns takes as long as one of 128
 // (0.28 us a stage, 0.34 on every SM at once): small tiles only spread few columns over more SMs.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -72,10 +72,7 @@ struct Tile {
   static constexpr int kN = kN_;
   static constexpr bool kRuns = kRuns_;  // sums leave the accumulator every `run` stages
   static constexpr bool kUnits = kKind != kIntegers;
-  // The epilogue's sums of 256 columns take 128 registers a thread; the threads that turn `a` to 16 bits leave it theirs and
-  // write half as much at a time.
-  static constexpr bool kWideRuns = kRuns && kN == 256;
-  static constexpr int kWords = kWideRuns ? 16 : 32;
+  static constexpr bool kWideRuns = kRuns && kN == 256;  // the epilogue's sums take 128 registers a thread
   static constexpr int kCols = kN / 2;   // of b, a CTA
   static constexpr uint32_t kABytes = kRows * kStep, kUBytes = kUnits ? 1024 : 0, kBBytes = kCols * kStep * 2;
   static constexpr int kAccs = kN <= 128 ? 2 : 1;
@@ -150,14 +147,7 @@ __device__ __forceinline__ void read_tmem(uint32_t taddr, float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void write_tmem(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void write_tmem(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void write_tmem32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
@@ -357,7 +347,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   auto going = [&]() { return __shfl_sync(0xffffffffu, *s_abort, 0) == 0; };
 
   // 640 threads have 96 registers each (61440); these four warps, and with 256 columns of runs the eight that turn `a`, give up
-  // what the epilogue's sums need: 128 * 32 + 256 * 96 + 256 * 128, or 128 * 32 + 256 * 56 + 256 * 168.
+  // what the epilogue's sums need: 128 * 32 + 256 * 96 + 256 * 128, or 128 * 32 + 256 * 56 + 256 * 168.  (The eight do with 56; of
+  // the epilogue's 11 do not fit beside its 128 sums, and more for it cannot be had.)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == 0) {
@@ -468,13 +459,13 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         const uint4* from = reinterpret_cast<const uint4*>(s_a + s.i * S::kABytes + row * 128);
         const unsigned char* units = s_u + s.i * S::kUBytes;
 #pragma unroll
-        for (int h = 0; h < 64 / S::kWords; ++h) {
-          uint4 in[S::kWords / 8];
+        for (int h = 0; h < 2; ++h) {
+          uint4 in[4];
 #pragma unroll
-          for (int j = 0; j < S::kWords / 8; ++j) in[j] = from[(S::kWords / 8 * h + j) ^ (row & 7)];
-          uint32_t out[S::kWords];
+          for (int j = 0; j < 4; ++j) in[j] = from[(4 * h + j) ^ (row & 7)];
+          uint32_t out[32];
 #pragma unroll
-          for (int j = 0; j < S::kWords / 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             const uint32_t word[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
             if constexpr (S::kUnits) {
               // 16 units, two 16-byte pieces of row q (its second 64 in the second box) of the swizzled boxes.
@@ -482,7 +473,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 #pragma unroll
               for (int p = 0; p < 2; ++p)
                 *reinterpret_cast<uint4*>(u + 4 * p) = *reinterpret_cast<const uint4*>(
-                    units + (S::kWords * h / 32) * 512 + q * 128 + (((2 * (S::kWords / 8 * h % 4 + j) + p) ^ (q + 4 * (S::kWords * h / 32))) << 4));
+                    units + h * 512 + q * 128 + (((2 * j + p) ^ (q + 4 * h)) << 4));
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 if constexpr (S::kKind == kBf16) {
@@ -507,12 +498,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             wait(&slot_empty[t.i], t.parity ^ 1u);
             __syncwarp();
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          }
-          if (h == 64 / S::kWords - 1) {
+          } else {
             __syncwarp();
             if (lane == 0) dev::mbar_arrive(&a_empty[s.i]);
           }
-          write_tmem(to + t.i * S::kSlotCols + S::kWords * h, out);
+          write_tmem32(to + t.i * S::kSlotCols + 32 * h, out);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");

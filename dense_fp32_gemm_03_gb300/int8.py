@@ -14,7 +14,9 @@ takes part in autograd: forward and backward are calls of their own.
 
 Every call takes a ``stream`` (default: the current one).  It does not wait for
 the stream on which its inputs were made; a ``stream`` that was passed is
-recorded on them, so they may be dropped once the call returned.
+recorded on them, so they may be dropped once the call returned.  Scratch
+belongs to the stream: the first call that needs more of it is made outside
+graph capture, and two graphs captured on one stream do not run at one time.
 """
 from __future__ import annotations
 
@@ -24,7 +26,6 @@ import struct
 import torch
 
 from . import binding
-from .binding import OK, SgemmError
 from .fp4 import _DTYPES, _call, _dense, _empty, _output, _read_on
 
 ORDERS = ("channels", "tokens")
@@ -335,7 +336,8 @@ def int8_checkpoint(x, out=None, stream=None):
     """Keeps x (tokens x channels, any row stride) in 8 bits for :func:`int8_weight_grad`: an :class:`Int8Checkpoint`.
 
     Blocks of 32 channels of a token share a power of two; the error is at most
-    2^-7 of a block's largest value.  ``out`` (of x's shape and type, order
+    2^-7 of a block's largest value (in float32 and bfloat16 of one above
+    2^-120; what is below 2^-127 becomes 0).  ``out`` (of x's shape and type, order
     ``"channels"``) is filled if given.
     """
     ld, rows, cols = _dense(x, "x")

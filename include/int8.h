@@ -22,15 +22,20 @@
  *
  * so that every value is exact in bfloat16, or, kept from 16-bit floats
  * (INT8_F16), in those.  A block that holds a NaN or an infinity gets u = NaN
- * and q = 0.  x is kept with an error of at most u / 2 (u where |x| > 127 u), 2^-7 of a
- * block's largest value.
+ * and q = 0.  x is kept with an error of at most u / 2 (u where |x| > 127 u): 2^-7 of a
+ * block's largest value, where e0 does not bound the exponent (a block below 2^-127 is
+ * kept as zeros; 16-bit floats of INT8_F16 lose nothing there).
  *
  * Memory and ownership are those of sgemm.h: device pointers owned by the
  * caller, calls asynchronous on `stream`, scratch from the per-(device,
  * stream) cache (so calls on one stream must not be made from several host
  * threads at the same time, the first call that needs more scratch is made
  * outside stream capture, and two graphs captured on one stream, which share
- * its scratch, must not run at the same time).  Outputs are write-only unless
+ * its scratch, must not run at the same time).  The stream keeps the most that a call on it took: int8_linear()
+ * up to 2 bytes for each element of x (its columns rounded up to 64), int8_gemm() as much for A;
+ * int8_weight_grad() of INT8_F32 6 bytes for each element of dY, of 16-bit
+ * types 2 if dY's rows are not at multiples of 16 bytes; and where sums are cut into shares, up to 20 MB for them.
+ * sgemm_release_workspaces() frees it.  Outputs are write-only unless
  * said otherwise and must not overlap inputs or one another.
  */
 #ifndef GB300_INT8_H
